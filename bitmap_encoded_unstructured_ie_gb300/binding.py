@@ -7,7 +7,7 @@ no CPU fallback.
 
 Function names follow the C ABI: ``us_encode``, ``us_spmm_w4a4``,
 ``us_spmm_f16``, ``us_spmspv_f16``, ``us_colinfo``, ``us_spmspv_f16_ci``, ``us_quantize_x``,
-``us_workspace_bytes``, ``us_pick_split_k``,
+``us_kv_write``, ``us_kv_read``, ``us_kv_commit``, ``us_attn_kv``, ``us_workspace_bytes``, ``us_pick_split_k``,
 ``us_validate``, ``us_get_last_device_status``.
 """
 from __future__ import annotations
@@ -24,13 +24,14 @@ LIB_PATH = os.path.join(_HERE, "_build", "libus.so")
 
 US_OK, US_ERR_INVALID_ARG, US_ERR_UNSUPPORTED, US_ERR_TOO_LARGE = 0, 1, 2, 3
 US_ERR_WORKSPACE, US_ERR_CUDA, US_ERR_TIMEOUT, US_ERR_CORRUPT = 4, 5, 6, 7
-US_F16, US_I4, US_I2 = 0, 1, 2
+US_F16, US_I4, US_I2, US_I8 = 0, 1, 2, 3          # US_I8: K/V cache only
 US_ORDER_ROW, US_ORDER_COL = 0, 1
 US_OP_ENCODE, US_OP_SPMM_W4A4, US_OP_SPMM_F16, US_OP_SPMSPV_F16 = 0, 1, 2, 3
 US_BITMAP_STATIC = 1
 
 EXPORTED = ("us_encode_sizes", "us_encode", "us_spmm_w4a4", "us_spmm_f16", "us_spmm_f16_noalloc", "us_spmspv_f16",
             "us_colinfo", "us_spmspv_f16_ci", "us_quantize_x",
+            "us_kv_write", "us_kv_read", "us_kv_commit", "us_attn_kv", "us_attn_kv_workspace_bytes",
             "us_encode_ie_sizes", "us_encode_ie", "us_reorder_rows", "us_spmm_w4a4_ie", "us_workspace_bytes_ie",
             "us_pick_split_k_ie",
             "us_workspace_bytes", "us_pick_split_k", "us_validate", "us_get_last_device_status",
@@ -56,6 +57,14 @@ class us_bitmap(ctypes.Structure):
 
 class us_bitmap_ie(ctypes.Structure):
     _fields_ = [("W", us_bitmap), ("RA", ctypes.c_int32), ("CA", ctypes.c_int32), ("perm", ctypes.c_void_p)]
+
+
+class us_kv_cache(ctypes.Structure):
+    _fields_ = [("elem", ctypes.c_int32), ("D", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -91,6 +100,12 @@ def load(path: str = LIB_PATH):
         lib.us_pick_split_k_ie.argtypes = [pie, i32, ctypes.POINTER(ctypes.c_int)]
         lib.us_spmspv_f16_ci.argtypes = [pbm, P, P, i32, ctypes.c_float, P, P, sz, P]
         lib.us_quantize_x.argtypes = [P, i32, i32, P, P, P]
+        pkv = ctypes.POINTER(us_kv_cache)
+        lib.us_kv_write.argtypes = [pkv, P, i64, P, i64, i32, P, P, i32, P]
+        lib.us_kv_read.argtypes = [pkv, i32, P, P, i32, P, i64, P, i64, P]
+        lib.us_kv_commit.argtypes = [pkv, i32, P, P, P, i32, P]
+        lib.us_attn_kv.argtypes = [pkv, P, i64, i32, i32, P, P, P, i32, ctypes.c_float, P, i64, P, sz, P]
+        lib.us_attn_kv_workspace_bytes.argtypes = [pkv, i32, i32, psz]
         lib.us_workspace_bytes.argtypes = [i32, pbm, i32, i32, psz]
         lib.us_pick_split_k.argtypes = [i32, pbm, i32, ctypes.POINTER(ctypes.c_int)]
         lib.us_validate.argtypes = [pbm]
@@ -356,6 +371,104 @@ def us_quantize_x(X: torch.Tensor, N: int, K: int, Xq: torch.Tensor, s_x: torch.
     """fp16 activations (N x K, token-major) -> packed int4 codes (N x K/2 bytes)
     and one fp16 scale per token."""
     _check("us_quantize_x", load().us_quantize_x(_dptr(X), N, K, _dptr(Xq), _dptr(s_x), _stream(stream)))
+
+
+@dataclass
+class KVCache:
+    """A paged, quantised key/value cache over device tensors: codes k and v
+    (uint8, pages x Hkv x slots x row bytes), scales (fp16 or its bit pattern,
+    pages x Hkv x slots x 2: K, then V) and the page table (int32, B x pages)."""
+    elem: int                 # US_I8 or US_I4
+    D: int
+    k: torch.Tensor
+    v: torch.Tensor
+    scale: torch.Tensor
+    page_table: torch.Tensor
+
+    def desc(self) -> us_kv_cache:
+        num_pages, Hkv, page_size, row = self.k.shape
+        B, max_pages = self.page_table.shape
+        assert row * 8 == self.D * (8 if self.elem == US_I8 else 4), "k: rows of D codes"
+        assert self.v.shape == self.k.shape and tuple(self.scale.shape) == (num_pages, Hkv, page_size, 2)
+        assert self.k.element_size() == self.v.element_size() == 1 and self.scale.element_size() == 2
+        assert self.page_table.dtype == torch.int32
+        return us_kv_cache(self.elem, self.D, Hkv, page_size, num_pages, B, max_pages, 0, _dptr(self.k),
+                           _dptr(self.v), _dptr(self.scale), _dptr(self.page_table))
+
+    @property
+    def page_size(self) -> int:
+        return self.k.shape[2]
+
+
+def kv_cache(elem: int, D: int, Hkv: int, page_size: int, num_pages: int, page_table: torch.Tensor) -> KVCache:
+    """An empty cache of num_pages pages on the page table's device."""
+    dev, row = page_table.device, D * (8 if elem == US_I8 else 4) // 8
+    k, v = (torch.zeros(num_pages, Hkv, page_size, row, dtype=torch.uint8, device=dev) for _ in range(2))
+    return KVCache(elem, D, k, v, torch.ones(num_pages, Hkv, page_size, 2, dtype=torch.float16, device=dev), page_table)
+
+
+def _rows(x: torch.Tensor):
+    """Pointer and row distance of T x H x D fp16 rows whose heads are contiguous."""
+    T, H, D = x.shape
+    assert x.is_cuda and x.element_size() == 2 and x.stride(2) == 1 and (H == 1 or x.stride(1) == D), \
+        "rows must be CUDA fp16 with contiguous heads"
+    return x.data_ptr(), (x.stride(0) if T > 1 else H * D)
+
+
+def _i32(x: torch.Tensor, n: int):
+    assert x.dtype == torch.int32 and x.numel() == n, "int32 array of the wrong type or length"
+    return _dptr(x)
+
+
+def us_kv_write(C: KVCache, K: torch.Tensor, V: torch.Tensor, tok_off: torch.Tensor, pos: torch.Tensor, max_n: int,
+                stream=None):
+    """Quantise T x Hkv x D rows of K and V into the cache at positions pos[b] .. ."""
+    d, B = C.desc(), C.page_table.shape[0]
+    assert K.shape == V.shape and K.shape[1:] == (C.k.shape[1], C.D)
+    (kp, ldk), (vp, ldv) = _rows(K), _rows(V)
+    _check("us_kv_write", load().us_kv_write(ctypes.byref(d), kp, ldk, vp, ldv, K.shape[0], _i32(tok_off, B + 1),
+                                             _i32(pos, B), max_n, _stream(stream)))
+
+
+def us_kv_read(C: KVCache, tok_off: torch.Tensor, pos: torch.Tensor, max_n: int, K: torch.Tensor, V: torch.Tensor,
+               stream=None):
+    """Read positions pos[b] .. back as fp16 rows (T x Hkv x D) of K and V."""
+    d, B = C.desc(), C.page_table.shape[0]
+    assert K.shape == V.shape and K.shape[1:] == (C.k.shape[1], C.D)
+    (kp, ldk), (vp, ldv) = _rows(K), _rows(V)
+    _check("us_kv_read", load().us_kv_read(ctypes.byref(d), K.shape[0], _i32(tok_off, B + 1), _i32(pos, B), max_n,
+                                           kp, ldk, vp, ldv, _stream(stream)))
+
+
+def us_kv_commit(C: KVCache, acc_off: torch.Tensor, acc: torch.Tensor, pos: torch.Tensor, max_n: int, stream=None):
+    """Move the accepted drafted tokens' entries, pos[b] + acc[i], to pos[b] + i."""
+    d, B = C.desc(), C.page_table.shape[0]
+    _check("us_kv_commit", load().us_kv_commit(ctypes.byref(d), acc.numel(), _i32(acc_off, B + 1),
+                                               _i32(acc, acc.numel()), _i32(pos, B), max_n, _stream(stream)))
+
+
+def us_attn_kv_workspace_bytes(C: KVCache, Hq: int, max_n: int) -> int:
+    n, d = ctypes.c_size_t(), C.desc()
+    _check("us_attn_kv_workspace_bytes", load().us_attn_kv_workspace_bytes(ctypes.byref(d), Hq, max_n, ctypes.byref(n)))
+    return n.value
+
+
+def workspace_attn_kv(C: KVCache, Hq: int, max_n: int) -> torch.Tensor:
+    """A zero-filled workspace of the size us_attn_kv needs."""
+    return torch.zeros(max(us_attn_kv_workspace_bytes(C, Hq, max_n), 16), dtype=torch.uint8, device=C.k.device)
+
+
+def us_attn_kv(C: KVCache, Q: torch.Tensor, tok_off: torch.Tensor, pos: torch.Tensor, mask: torch.Tensor | None,
+               max_n: int, scale: float, O: torch.Tensor, ws: torch.Tensor, stream=None):
+    """Attention of T x Hq x D query rows over the cache; mask: one 64-bit word
+    per row (a tree of drafted tokens), or None (a chain)."""
+    d, B = C.desc(), C.page_table.shape[0]
+    assert Q.shape == O.shape and Q.shape[2] == C.D
+    assert mask is None or (mask.element_size() == 8 and mask.numel() == Q.shape[0])
+    (qp, ldq), (op, ldo) = _rows(Q), _rows(O)
+    _check("us_attn_kv", load().us_attn_kv(ctypes.byref(d), qp, ldq, Q.shape[1], Q.shape[0], _i32(tok_off, B + 1),
+                                           _i32(pos, B), _dptr(mask), max_n, scale, op, ldo, _dptr(ws), ws.numel(),
+                                           _stream(stream)))
 
 
 def us_validate_host(bitmap, tile_off, values, M, K, TM, TK, elem, order) -> int:

@@ -8,6 +8,7 @@
 
 #include "us_common.cuh"
 #include "us_internal.h"
+#include "us_kv.cuh"
 
 __device__ unsigned g_us_status = 0;
 
@@ -199,6 +200,52 @@ __global__ void wait_selftest_kernel(unsigned* status, uint64_t limit_ns, uint64
     const uint64_t t0 = us::globaltimer_ns();
     const bool done = us::mbar_wait_for(&bar, 0u, status, limit_ns);
     if (elapsed_ns) *elapsed_ns = done ? 0ull : us::globaltimer_ns() - t0;
+}
+
+// -------------------------------------------------------------- K/V cache --
+us_status check_kv_cache(const us_kv_cache* C, UsKvCache& c) {
+    if (!C) return US_ERR_INVALID_ARG;
+    if (C->elem != US_I8 && C->elem != US_I4) return US_ERR_INVALID_ARG;
+    if (C->D <= 0 || C->Hkv <= 0 || C->num_pages <= 0 || C->B <= 0 || C->max_pages <= 0 || C->reserved)
+        return US_ERR_INVALID_ARG;
+    if (C->page_size < 16 || C->page_size > 1024 || (C->page_size & (C->page_size - 1))) return US_ERR_INVALID_ARG;
+    if (C->D != 64 && C->D != 128) return US_ERR_UNSUPPORTED;
+    if (C->B > 1024 || C->Hkv > 1024) return US_ERR_TOO_LARGE;
+    if ((int64_t)C->max_pages * C->page_size >= ((int64_t)1 << 30)) return US_ERR_TOO_LARGE;
+    if (!C->k || !C->v || !C->scale || !C->page_table) return US_ERR_INVALID_ARG;
+    if (!aligned16(C->k) || !aligned16(C->v) || !aligned16(C->scale) || !aligned16(C->page_table))
+        return US_ERR_INVALID_ARG;
+    c.elem = C->elem; c.D = C->D; c.Hkv = C->Hkv;
+    c.page_shift = __builtin_ctz((unsigned)C->page_size);
+    c.num_pages = C->num_pages; c.B = C->B; c.max_pages = C->max_pages;
+    c.row_bytes = C->D * (C->elem == US_I8 ? 8 : 4) / 8;
+    c.k = static_cast<uint8_t*>(C->k);
+    c.v = static_cast<uint8_t*>(C->v);
+    c.scale = C->scale;
+    c.table = C->page_table;
+    c.status = status_ptr();
+    return US_OK;
+}
+
+us_status check_kv_call(const us_kv_cache* C, int T, const int32_t* off, const int32_t* pos, int max_n, UsKvCache& c,
+                        UsKvCall& a) {
+    const us_status s = check_kv_cache(C, c);
+    if (s != US_OK) return s;
+    if (T < 0 || max_n < 1 || !off || !pos || !aligned16(off) || !aligned16(pos)) return US_ERR_INVALID_ARG;
+    if ((int64_t)max_n * c.Hkv >= ((int64_t)1 << 30)) return US_ERR_TOO_LARGE;
+    a.off = off; a.pos = pos; a.T = T; a.max_n = max_n;
+    return US_OK;
+}
+
+// rows of H heads of D fp16 values, ld elements apart
+us_status check_rows(const uint16_t* x, int64_t ld, int H, int D) {
+    return x && aligned16(x) && ld >= (int64_t)H * D && ld % 8 == 0 ? US_OK : US_ERR_INVALID_ARG;
+}
+
+us_status check_attn_shape(const UsKvCache& c, int Hq, int max_n) {
+    if (Hq <= 0 || Hq % c.Hkv || max_n < 1) return US_ERR_INVALID_ARG;
+    if (Hq > 4096 || (int64_t)max_n * Hq >= ((int64_t)1 << 30)) return US_ERR_TOO_LARGE;
+    return US_OK;
 }
 
 }  // namespace
@@ -561,6 +608,76 @@ us_status us_quantize_x(const uint16_t* X, int N, int K, uint8_t* Xq, uint16_t* 
     if (!X || !Xq || !s_x || !aligned16(X) || !aligned16(Xq)) return US_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(s_x) & 1u) != 0) return US_ERR_INVALID_ARG;
     return us::launch_quantize_x(X, N, K, Xq, s_x, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_kv_write(const us_kv_cache* C, const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv, int T,
+                      const int32_t* tok_off, const int32_t* pos, int max_n, void* stream) {
+    UsKvCache c;
+    UsKvCall a;
+    us_status s = check_kv_call(C, T, tok_off, pos, max_n, c, a);
+    if (s != US_OK || T == 0) return s;
+    s = check_rows(K, ldk, c.Hkv, c.D);
+    if (s == US_OK) s = check_rows(V, ldv, c.Hkv, c.D);
+    if (s != US_OK) return s;
+    return us::launch_kv_write(c, a, K, ldk, V, ldv, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_kv_read(const us_kv_cache* C, int T, const int32_t* tok_off, const int32_t* pos, int max_n, uint16_t* K,
+                     int64_t ldk, uint16_t* V, int64_t ldv, void* stream) {
+    UsKvCache c;
+    UsKvCall a;
+    us_status s = check_kv_call(C, T, tok_off, pos, max_n, c, a);
+    if (s != US_OK || T == 0) return s;
+    s = check_rows(K, ldk, c.Hkv, c.D);
+    if (s == US_OK) s = check_rows(V, ldv, c.Hkv, c.D);
+    if (s != US_OK) return s;
+    return us::launch_kv_read(c, a, K, ldk, V, ldv, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_kv_commit(const us_kv_cache* C, int T, const int32_t* acc_off, const int32_t* acc, const int32_t* pos,
+                       int max_n, void* stream) {
+    UsKvCache c;
+    UsKvCall a;
+    us_status s = check_kv_call(C, T, acc_off, pos, max_n, c, a);
+    if (s != US_OK || T == 0) return s;
+    if (max_n > US_KV_MAX_COMMIT) return US_ERR_UNSUPPORTED;
+    if (!acc || !aligned16(acc)) return US_ERR_INVALID_ARG;
+    return us::launch_kv_commit(c, a, acc, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_attn_kv_workspace_bytes(const us_kv_cache* C, int Hq, int max_n, size_t* bytes) {
+    if (!bytes) return US_ERR_INVALID_ARG;
+    UsAttnParams p = {};
+    us_status s = check_kv_cache(C, p.c);
+    if (s != US_OK) return s;
+    s = check_attn_shape(p.c, Hq, max_n);
+    if (s != US_OK) return s;
+    p.Hq = Hq;
+    p.a.max_n = max_n;
+    *bytes = us::attn_ws(p);
+    return US_OK;
+}
+
+us_status us_attn_kv(const us_kv_cache* C, const uint16_t* Q, int64_t ldq, int Hq, int T, const int32_t* tok_off,
+                     const int32_t* pos, const uint64_t* mask, int max_n, float scale, uint16_t* O, int64_t ldo,
+                     void* ws, size_t ws_bytes, void* stream) {
+    UsAttnParams p = {};
+    us_status s = check_kv_call(C, T, tok_off, pos, max_n, p.c, p.a);
+    if (s != US_OK) return s;
+    s = check_attn_shape(p.c, Hq, max_n);
+    if (s != US_OK) return s;
+    if (!(scale - scale == 0.f)) return US_ERR_INVALID_ARG;
+    if (mask && max_n > 64) return US_ERR_UNSUPPORTED;
+    if (mask && !aligned16(mask)) return US_ERR_INVALID_ARG;
+    if (T == 0) return US_OK;
+    s = check_rows(Q, ldq, Hq, p.c.D);
+    if (s == US_OK) s = check_rows(O, ldo, Hq, p.c.D);
+    if (s != US_OK) return s;
+    p.Q = Q; p.O = O; p.ldq = ldq; p.ldo = ldo; p.Hq = Hq; p.scale = scale; p.mask = mask;
+    const size_t need = us::attn_ws(p);
+    if (need && (!ws || ws_bytes < need || !aligned16(ws))) return US_ERR_WORKSPACE;
+    p.ws = ws;
+    return us::launch_attn(p, static_cast<cudaStream_t>(stream));
 }
 
 us_status us_validate(const us_bitmap* W) {

@@ -9,6 +9,11 @@
 #include "../../include/us.h"
 
 struct UsKParams;
+struct UsKvCache;
+struct UsKvCall;
+struct UsAttnParams;
+
+constexpr int US_KV_MAX_COMMIT = 64;   // tokens of one request in us_kv_commit
 
 namespace us {
 
@@ -78,6 +83,16 @@ us_status launch_spmspv_stream(UsKParams p, cudaStream_t st);
 
 // per-token int4 quantisation of fp16 activations (us_quant.cu)
 us_status launch_quantize_x(const uint16_t* X, int N, int K, uint8_t* Xq, uint16_t* s_x, cudaStream_t st);
+
+// quantised K/V cache: write, read back, commit (us_kv.cu)
+us_status launch_kv_write(const UsKvCache& c, const UsKvCall& a, const uint16_t* K, int64_t ldk, const uint16_t* V,
+                          int64_t ldv, cudaStream_t st);
+us_status launch_kv_read(const UsKvCache& c, const UsKvCall& a, uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv,
+                         cudaStream_t st);
+us_status launch_kv_commit(const UsKvCache& c, const UsKvCall& a, const int32_t* acc, cudaStream_t st);
+// attention over the cache (us_attn.cu)
+size_t attn_ws(const UsAttnParams& p);
+us_status launch_attn(const UsAttnParams& p, cudaStream_t st);
 
 // device properties of the current device (cached)
 int num_sms();

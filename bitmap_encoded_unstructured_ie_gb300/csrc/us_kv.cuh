@@ -1,0 +1,82 @@
+// us_kv.cuh -- the paged, quantised key/value cache as the kernels see it.
+//
+// A cache entry is one (position, key head): D codes of K, D codes of V (int8,
+// or int4 two per byte, even element in the low nibble) and a pair of fp16
+// scales.  Position p of request b lies in page table[b][p / page_size], slot
+// p % page_size; the entries of one page and head are contiguous.
+#pragma once
+
+#include "us_common.cuh"
+
+struct UsKvCache {
+    int elem, D, Hkv, page_shift, num_pages, B, max_pages, row_bytes;
+    uint8_t* k;
+    uint8_t* v;
+    uint16_t* scale;                 // (K scale, V scale) per entry
+    const int32_t* table;
+    unsigned* status;
+};
+
+// The tokens of one call: request b owns rows off[b] .. off[b+1]-1 and, unless
+// stated otherwise, positions pos[b] .. of the cache.
+struct UsKvCall {
+    const int32_t* off;
+    const int32_t* pos;
+    int T, max_n;
+};
+
+// Attention over the cache: Q and O token-major rows of Hq heads.
+struct UsAttnParams {
+    UsKvCache c;
+    UsKvCall a;
+    const uint16_t* Q;
+    uint16_t* O;
+    int64_t ldq, ldo;
+    int Hq;
+    float scale;
+    const uint64_t* mask;            // per token, or nullptr: a chain
+    void* ws;
+};
+
+namespace us {
+
+// Rows of request b: first row and count (0 if the offsets are not usable).
+US_DEV int kv_rows(const UsKvCache& c, const UsKvCall& a, int b, int& row0) {
+    const int o0 = a.off[b], o1 = a.off[b + 1];
+    row0 = o0;
+    if (o0 >= 0 && o1 >= o0 && o1 <= a.T && o1 - o0 <= a.max_n) return o1 - o0;
+    set_status(c.status, US_ERR_INVALID_ARG);
+    return 0;
+}
+
+// Page of position p of request b, or -1 (recorded) if there is none.
+US_DEV int kv_page(const UsKvCache& c, int b, int p) {
+    const int i = p >> c.page_shift;
+    if (p < 0 || i >= c.max_pages) {
+        set_status(c.status, US_ERR_INVALID_ARG);
+        return -1;
+    }
+    const int id = c.table[(int64_t)b * c.max_pages + i];
+    if (id >= 0 && id < c.num_pages) return id;
+    set_status(c.status, US_ERR_CORRUPT);
+    return -1;
+}
+
+// Index of the entry of head h at slot p % page_size of page `id`.
+US_DEV int64_t kv_entry(const UsKvCache& c, int id, int h, int p) {
+    return ((((int64_t)id * c.Hkv + h) << c.page_shift)) + (p & ((1 << c.page_shift) - 1));
+}
+
+// base + i for positions: wraps negative instead of overflowing (kv_page refuses it)
+US_DEV int kv_pos(int base, int i) { return (int)((unsigned)base + (unsigned)i); }
+
+// Context length of request b with n tokens behind it, or -1 (recorded) if
+// the page table's row cannot hold them.
+US_DEV int kv_context(const UsKvCache& c, const UsKvCall& a, int b, int n) {
+    const int ctx = a.pos[b];
+    if (ctx >= 0 && ctx <= ((int64_t)c.max_pages << c.page_shift) - n) return ctx;
+    set_status(c.status, US_ERR_INVALID_ARG);
+    return -1;
+}
+
+}  // namespace us

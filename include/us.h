@@ -77,7 +77,7 @@ typedef enum {
  * the earlier element in the lower bits, two's complement in [-2, 1]: the
  * pages name W2A4 in UnionSparse Fig. 11 without its layout, so this is the
  * plain reading).  Runs are padded to 16 bytes: 8 / 32 / 64 elements. */
-typedef enum { US_F16 = 0, US_I4 = 1, US_I2 = 2 } us_elem;
+typedef enum { US_F16 = 0, US_I4 = 1, US_I2 = 2, US_I8 = 3 /* K/V cache only */ } us_elem;
 typedef enum { US_ORDER_ROW = 0, US_ORDER_COL = 1 } us_order;
 typedef enum {
     US_OP_ENCODE = 0,
@@ -293,6 +293,84 @@ us_status us_spmspv_f16_ci(const us_bitmap* W, const uint32_t* colinfo, const ui
  * s_x: N fp16.  1 <= N, K % 32 == 0.  NaN does not take part in the maximum and
  * gives code 0.  One pass over X: its output feeds us_spmm_w4a4 directly. */
 us_status us_quantize_x(const uint16_t* X, int N, int K, uint8_t* Xq, uint16_t* s_x, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Quantised key/value cache, and attention over it.  (No counterpart on the
+ * pages, whose W4A4 products leave the cache to the serving system; the rule
+ * of quantisation is us_quantize_x's, per head.)
+ *
+ * An entry holds one (position, key head): D codes of K, D codes of V, and
+ * their fp16 scales.  elem US_I8: one code a byte; US_I4: two a byte, even
+ * element in the low nibble; two's complement.  Row bytes R = D (US_I8) or
+ * D/2 (US_I4).
+ *   k, v:   [num_pages][Hkv][page_size][R] bytes
+ *   scale:  [num_pages][Hkv][page_size][2] fp16, the K scale, then the V scale
+ *   page_table: int32 [B][max_pages]: position p of request b is slot
+ *           p % page_size of page page_table[b][p / page_size]; entries behind
+ *           a request's last position are not read
+ * D: 64 or 128 (US_ERR_UNSUPPORTED otherwise); page_size: a power of two,
+ * 16..1024; B <= 1024 and max_pages * page_size < 2^30 (US_ERR_TOO_LARGE).
+ *
+ * Every call names its tokens the same way: T rows in all, request b owning
+ * rows tok_off[b] .. tok_off[b+1]-1 (int32 [B+1], at most max_n each, none
+ * allowed) and a first position pos[b] (int32 [B]).  Both arrays are read on
+ * the device, so a captured graph follows their values.  Offsets that do not
+ * ascend, leave 0..T or give a request more than max_n rows record
+ * US_ERR_INVALID_ARG in the device status word and the request is skipped.  So
+ * do positions that the page table's row cannot hold (us_attn_kv skips the
+ * request, the others those positions).  A page number outside
+ * 0..num_pages-1 records US_ERR_CORRUPT and its positions are skipped (not
+ * attended to).
+ * fp16 rows hold whole heads side by side; ld* is the distance of two rows in
+ * elements (a multiple of 8, so that slices of a fused projection serve).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t elem;             /* US_I8 or US_I4 */
+    int32_t D, Hkv, page_size, num_pages, B, max_pages;
+    int32_t reserved;         /* must be 0 */
+    void* k;
+    void* v;
+    uint16_t* scale;
+    const int32_t* page_table;
+} us_kv_cache;
+
+/* Quantise and append: row t = tok_off[b] + i of K and V (Hkv heads of D fp16
+ * values) becomes the entries of position pos[b] + i.  Per row and head
+ *   s = fp16_rn(max|x| / q), 1 if that is 0,   q = 127 (US_I8) or 7 (US_I4)
+ *   code = clamp(rint(x / s), -q-1, q)          (fp32 divisions, ties to even)
+ * Infinities count as +-65504 and NaN as 0: what is stored is finite. */
+us_status us_kv_write(const us_kv_cache* C, const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv, int T,
+                      const int32_t* tok_off, const int32_t* pos, int max_n, void* stream);
+
+/* Read positions pos[b] .. back as fp16 rows: fp16_rn(code * s). */
+us_status us_kv_read(const us_kv_cache* C, int T, const int32_t* tok_off, const int32_t* pos, int max_n, uint16_t* K,
+                     int64_t ldk, uint16_t* V, int64_t ldv, void* stream);
+
+/* After a tree of drafted tokens at positions pos[b] .. was verified: the
+ * entry at pos[b] + acc[acc_off[b] + i] moves to pos[b] + i, for the i-th
+ * accepted token; all of a request's entries are read before any is written,
+ * so a path may overlap itself.  acc: int32, T entries; max_n <= 64
+ * (US_ERR_UNSUPPORTED otherwise). */
+us_status us_kv_commit(const us_kv_cache* C, int T, const int32_t* acc_off, const int32_t* acc, const int32_t* pos,
+                       int max_n, void* stream);
+
+/* Attention of the call's tokens over the cache, whose entries for these
+ * tokens (positions pos[b] + i) have been written.  Token i of request b sees
+ * every position p < pos[b], and of the call's own positions pos[b] + j those
+ * with bit j of mask[t] set (mask NULL: a chain, j <= i).  With query head hq
+ * on key head hq / (Hq / Hkv):
+ *   O[t][hq] = fp16(sum_p w_p v_p / sum_p w_p),  w_p = exp(scale * Q[t][hq].k_p)
+ * and 0 for a row that sees no position.  Scores, weights' sums and outputs
+ * are accumulated in fp32; weights enter the product with V as fp16.
+ * Q, O: T rows of Hq heads.  mask: uint64 per row (a tree of at most 64 tokens
+ * a request: max_n <= 64, else US_ERR_UNSUPPORTED); bits of j >= n are
+ * ignored.  A chain may be of any length (a prompt's chunk).  One token a
+ * request is plain decoding.  Workspace: us_attn_kv_workspace_bytes, zeroed
+ * once.  Repeated calls with the same arguments give the same bits. */
+us_status us_attn_kv(const us_kv_cache* C, const uint16_t* Q, int64_t ldq, int Hq, int T, const int32_t* tok_off,
+                     const int32_t* pos, const uint64_t* mask, int max_n, float scale, uint16_t* O, int64_t ldo,
+                     void* ws, size_t ws_bytes, void* stream);
+us_status us_attn_kv_workspace_bytes(const us_kv_cache* C, int Hq, int max_n, size_t* bytes);
 
 /* Workspace bytes for `op` on W with N tokens and the given split_k
  * (0 = the automatic choice).  For US_OP_ENCODE only W->M, K, TM, TK are read. */
