@@ -373,11 +373,13 @@ def us_quantize_x(X: torch.Tensor, N: int, K: int, Xq: torch.Tensor, s_x: torch.
     _check("us_quantize_x", load().us_quantize_x(_dptr(X), N, K, _dptr(Xq), _dptr(s_x), _stream(stream)))
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class KVCache:
     """A paged, quantised key/value cache over device tensors: codes k and v
     (uint8, pages x Hkv x slots x row bytes), scales (fp16 or its bit pattern,
-    pages x Hkv x slots x 2: K, then V) and the page table (int32, B x pages)."""
+    pages x Hkv x slots x 2: K, then V) and the page table (int32, B x pages).
+    The descriptor is made once, with the object; the tensors' contents may
+    change, the tensors may not."""
     elem: int                 # US_I8 or US_I4
     D: int
     k: torch.Tensor
@@ -385,19 +387,17 @@ class KVCache:
     scale: torch.Tensor
     page_table: torch.Tensor
 
-    def desc(self) -> us_kv_cache:
+    def __post_init__(self):
         num_pages, Hkv, page_size, row = self.k.shape
         B, max_pages = self.page_table.shape
         assert row * 8 == self.D * (8 if self.elem == US_I8 else 4), "k: rows of D codes"
         assert self.v.shape == self.k.shape and tuple(self.scale.shape) == (num_pages, Hkv, page_size, 2)
         assert self.k.element_size() == self.v.element_size() == 1 and self.scale.element_size() == 2
         assert self.page_table.dtype == torch.int32
-        return us_kv_cache(self.elem, self.D, Hkv, page_size, num_pages, B, max_pages, 0, _dptr(self.k),
-                           _dptr(self.v), _dptr(self.scale), _dptr(self.page_table))
-
-    @property
-    def page_size(self) -> int:
-        return self.k.shape[2]
+        d = us_kv_cache(self.elem, self.D, Hkv, page_size, num_pages, B, max_pages, 0, _dptr(self.k), _dptr(self.v),
+                        _dptr(self.scale), _dptr(self.page_table))
+        for name, value in (("B", B), ("Hkv", Hkv), ("page_size", page_size), ("_desc", d), ("_ref", ctypes.byref(d))):
+            object.__setattr__(self, name, value)
 
 
 def kv_cache(elem: int, D: int, Hkv: int, page_size: int, num_pages: int, page_table: torch.Tensor) -> KVCache:
@@ -407,49 +407,56 @@ def kv_cache(elem: int, D: int, Hkv: int, page_size: int, num_pages: int, page_t
     return KVCache(elem, D, k, v, torch.ones(num_pages, Hkv, page_size, 2, dtype=torch.float16, device=dev), page_table)
 
 
-def _rows(x: torch.Tensor):
-    """Pointer and row distance of T x H x D fp16 rows whose heads are contiguous."""
-    T, H, D = x.shape
-    assert x.is_cuda and x.element_size() == 2 and x.stride(2) == 1 and (H == 1 or x.stride(1) == D), \
-        "rows must be CUDA fp16 with contiguous heads"
-    return x.data_ptr(), (x.stride(0) if T > 1 else H * D)
+# The cache's calls are short (a decode step appends and attends in a few
+# microseconds on the GPU), so their marshalling passes plain integers.
+def _rows(x: torch.Tensor, H: int, D: int):
+    """Rows, pointer and row distance of T x H x D fp16 rows whose heads are contiguous."""
+    T, h, d = x.shape
+    ld, sh, sd = x.stride()
+    assert x.is_cuda and x.element_size() == 2 and h == H and d == D and sd == 1 and (sh == D or H == 1), \
+        "rows must be T x H x D CUDA fp16 with contiguous heads"
+    return T, x.data_ptr(), (ld if T > 1 else H * D)
 
 
-def _i32(x: torch.Tensor, n: int):
-    assert x.dtype == torch.int32 and x.numel() == n, "int32 array of the wrong type or length"
-    return _dptr(x)
+def _i32(x: torch.Tensor, n: int) -> int:
+    assert x.is_cuda and x.dtype is torch.int32 and x.numel() == n and x.is_contiguous(), "int32 CUDA array of n entries"
+    return x.data_ptr()
+
+
+def _raw_stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def us_kv_write(C: KVCache, K: torch.Tensor, V: torch.Tensor, tok_off: torch.Tensor, pos: torch.Tensor, max_n: int,
                 stream=None):
     """Quantise T x Hkv x D rows of K and V into the cache at positions pos[b] .. ."""
-    d, B = C.desc(), C.page_table.shape[0]
-    assert K.shape == V.shape and K.shape[1:] == (C.k.shape[1], C.D)
-    (kp, ldk), (vp, ldv) = _rows(K), _rows(V)
-    _check("us_kv_write", load().us_kv_write(ctypes.byref(d), kp, ldk, vp, ldv, K.shape[0], _i32(tok_off, B + 1),
-                                             _i32(pos, B), max_n, _stream(stream)))
+    T, kp, ldk = _rows(K, C.Hkv, C.D)
+    Tv, vp, ldv = _rows(V, C.Hkv, C.D)
+    assert T == Tv
+    _check("us_kv_write", (_lib or load()).us_kv_write(C._ref, kp, ldk, vp, ldv, T, _i32(tok_off, C.B + 1),
+                                                       _i32(pos, C.B), max_n, _raw_stream(stream)))
 
 
 def us_kv_read(C: KVCache, tok_off: torch.Tensor, pos: torch.Tensor, max_n: int, K: torch.Tensor, V: torch.Tensor,
                stream=None):
     """Read positions pos[b] .. back as fp16 rows (T x Hkv x D) of K and V."""
-    d, B = C.desc(), C.page_table.shape[0]
-    assert K.shape == V.shape and K.shape[1:] == (C.k.shape[1], C.D)
-    (kp, ldk), (vp, ldv) = _rows(K), _rows(V)
-    _check("us_kv_read", load().us_kv_read(ctypes.byref(d), K.shape[0], _i32(tok_off, B + 1), _i32(pos, B), max_n,
-                                           kp, ldk, vp, ldv, _stream(stream)))
+    T, kp, ldk = _rows(K, C.Hkv, C.D)
+    Tv, vp, ldv = _rows(V, C.Hkv, C.D)
+    assert T == Tv
+    _check("us_kv_read", (_lib or load()).us_kv_read(C._ref, T, _i32(tok_off, C.B + 1), _i32(pos, C.B), max_n, kp, ldk,
+                                                     vp, ldv, _raw_stream(stream)))
 
 
 def us_kv_commit(C: KVCache, acc_off: torch.Tensor, acc: torch.Tensor, pos: torch.Tensor, max_n: int, stream=None):
     """Move the accepted drafted tokens' entries, pos[b] + acc[i], to pos[b] + i."""
-    d, B = C.desc(), C.page_table.shape[0]
-    _check("us_kv_commit", load().us_kv_commit(ctypes.byref(d), acc.numel(), _i32(acc_off, B + 1),
-                                               _i32(acc, acc.numel()), _i32(pos, B), max_n, _stream(stream)))
+    T = acc.numel()
+    _check("us_kv_commit", (_lib or load()).us_kv_commit(C._ref, T, _i32(acc_off, C.B + 1), _i32(acc, T),
+                                                         _i32(pos, C.B), max_n, _raw_stream(stream)))
 
 
 def us_attn_kv_workspace_bytes(C: KVCache, Hq: int, max_n: int) -> int:
-    n, d = ctypes.c_size_t(), C.desc()
-    _check("us_attn_kv_workspace_bytes", load().us_attn_kv_workspace_bytes(ctypes.byref(d), Hq, max_n, ctypes.byref(n)))
+    n = ctypes.c_size_t()
+    _check("us_attn_kv_workspace_bytes", load().us_attn_kv_workspace_bytes(C._ref, Hq, max_n, ctypes.byref(n)))
     return n.value
 
 
@@ -462,13 +469,16 @@ def us_attn_kv(C: KVCache, Q: torch.Tensor, tok_off: torch.Tensor, pos: torch.Te
                max_n: int, scale: float, O: torch.Tensor, ws: torch.Tensor, stream=None):
     """Attention of T x Hq x D query rows over the cache; mask: one 64-bit word
     per row (a tree of drafted tokens), or None (a chain)."""
-    d, B = C.desc(), C.page_table.shape[0]
-    assert Q.shape == O.shape and Q.shape[2] == C.D
-    assert mask is None or (mask.element_size() == 8 and mask.numel() == Q.shape[0])
-    (qp, ldq), (op, ldo) = _rows(Q), _rows(O)
-    _check("us_attn_kv", load().us_attn_kv(ctypes.byref(d), qp, ldq, Q.shape[1], Q.shape[0], _i32(tok_off, B + 1),
-                                           _i32(pos, B), _dptr(mask), max_n, scale, op, ldo, _dptr(ws), ws.numel(),
-                                           _stream(stream)))
+    Hq = Q.shape[1]
+    T, qp, ldq = _rows(Q, Hq, C.D)
+    To, op, ldo = _rows(O, Hq, C.D)
+    assert T == To and ws.is_cuda and ws.is_contiguous()
+    if mask is not None:
+        assert mask.is_cuda and mask.element_size() == 8 and mask.numel() == T and mask.is_contiguous()
+    _check("us_attn_kv", (_lib or load()).us_attn_kv(C._ref, qp, ldq, Hq, T, _i32(tok_off, C.B + 1), _i32(pos, C.B),
+                                                     None if mask is None else mask.data_ptr(), max_n, scale, op, ldo,
+                                                     ws.data_ptr(), ws.numel() * ws.element_size(),
+                                                     _raw_stream(stream)))
 
 
 def us_validate_host(bitmap, tile_off, values, M, K, TM, TK, elem, order) -> int:

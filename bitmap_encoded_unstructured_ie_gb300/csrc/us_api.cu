@@ -653,6 +653,7 @@ us_status us_attn_kv_workspace_bytes(const us_kv_cache* C, int Hq, int max_n, si
     s = check_attn_shape(p.c, Hq, max_n);
     if (s != US_OK) return s;
     p.Hq = Hq;
+    p.G = Hq / p.c.Hkv;
     p.a.max_n = max_n;
     *bytes = us::attn_ws(p);
     return US_OK;
@@ -673,7 +674,7 @@ us_status us_attn_kv(const us_kv_cache* C, const uint16_t* Q, int64_t ldq, int H
     s = check_rows(Q, ldq, Hq, p.c.D);
     if (s == US_OK) s = check_rows(O, ldo, Hq, p.c.D);
     if (s != US_OK) return s;
-    p.Q = Q; p.O = O; p.ldq = ldq; p.ldo = ldo; p.Hq = Hq; p.scale = scale; p.mask = mask;
+    p.Q = Q; p.O = O; p.ldq = ldq; p.ldo = ldo; p.Hq = Hq; p.G = Hq / p.c.Hkv; p.scale = scale; p.mask = mask;
     const size_t need = us::attn_ws(p);
     if (need && (!ws || ws_bytes < need || !aligned16(ws))) return US_ERR_WORKSPACE;
     p.ws = ws;

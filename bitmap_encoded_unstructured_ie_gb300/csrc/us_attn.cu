@@ -1,109 +1,630 @@
-// us_attn.cu -- attention of new tokens over the quantised K/V cache.
+// us_attn.cu -- attention of few query rows per key head over the quantised
+// K/V cache (single tokens and small trees), on mma.sync.
 //
 // Query row (token i of request b, head hq) sees the positions p < ctx, and of
 // the call's own tokens j = p - ctx those whose bit is set in the token's mask
 // (no mask: j <= i).  o = sum_p w_p v_p / sum_p w_p, w_p = exp(scale q.k_p), 0
-// for a row that sees nothing.
+// for a row that sees nothing.  With k_p = s_kp ck_p and v_p = s_vp cv_p the
+// scales multiply the score and the weight, so the products take the integer
+// codes, which fp16 holds exactly:
+//   S^T = Ck Q^T   (tokens x rows),   O^T = Cv^T P^T   (dimensions x rows).
+// Both products have the cache as the 16-row A operand and the query rows as
+// the 8-column B operand: few rows waste little of an MMA, and each code is
+// converted once for all rows.
 //
-// One CTA per query row; each warp walks every fourth position with a running
-// maximum and sum, its lanes holding D/32 dimensions; the four states are
-// joined at the end.
+// Which lane holds what.  The contraction of S^T may run over the dimensions
+// in any order, and the tokens may enter O^T in any order, so both are chosen
+// such that a lane's codes are neighbours in memory: lane (g, c) = (lane / 4,
+// lane % 4) takes D/4 codes of K of tokens g' and g' + 8, and of V the D/8
+// dimensions from g D/8 of tokens c, c + 4, c + 8, c + 12.
+//
+// Work: the (request, key head, row block) segments are cut into tiles of 64
+// positions, and the tile sequence is spread evenly over the CTAs, whatever
+// the lengths (they are read on the device).  A warp takes 16 positions of each
+// tile: three bulk copies (K, V, scales; a page's entries of one head are
+// contiguous) into the warp's own ring, several tiles ahead and across
+// segments.  A segment shared by several CTAs leaves partial states in the
+// workspace; the CTA that arrives last joins them in the order of the tiles.
 #include "us_internal.h"
 #include "us_kv.cuh"
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kBlock = 16;                        // positions of a warp's step
+constexpr int kTile = kWarps * kBlock;            // positions of a CTA's step
+constexpr float kMaxLag = 4.f;                    // a row's maximum may lag by 2^4 before the state is rescaled
+constexpr float kVHead = 2048.f;                  // weights reach 2^4 2^11 < 65504 as fp16: small ones keep their bits
 
-// D/32 neighbouring codes of a row, from dimension lane * D/32
-template <int ELEM, int DL>
-US_DEV void codes(const uint8_t* row, int lane, float (&x)[DL]) {
+template <int ELEM, int D, int NT>
+struct Shape {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kRow = D * (ELEM == US_I8 ? 8 : 4) / 8;    // bytes of a row of codes
+    static constexpr int kKW = kRow / 16;                           // words a lane holds of a K row
+    static constexpr int kVW = kRow / 32;                           // ... of a V row (its D/8 dimensions)
+    static constexpr int kKS = D / 16;                              // MMA steps over the dimensions
+    static constexpr int kMT = D / 16;                              // 16-dimension blocks of O^T
+    static constexpr int kMinB = NT == 1 ? 4 : NT == 2 ? 3 : 2;     // CTAs an SM
+    static constexpr int kStageBytes = 2 * kBlock * kRow + kBlock * 4;
+    static constexpr int kJoin = kWarps * 32 * 32 * 4;              // O^T of four warps, 32 values a lane at a time
+    static constexpr int kFixed = kJoin + kWarps * kRows * 8 + kRows * 16 + 512;
+    static constexpr int kFit = (224 * 1024 / kMinB - 1024 - kFixed) / (kWarps * kStageBytes);
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kSmem = kFixed + kWarps * kStages * kStageBytes;
+    static_assert(kStages >= 2, "ring");
+    static constexpr int kSlotFloats = 2 * kRows + kRows * D;       // m, l, O^T of one partial state
+};
+
+US_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+US_DEV uint32_t hsub2(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+US_DEV uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b), *reinterpret_cast<__half2*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+US_DEV uint32_t pack_half2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+US_DEV uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Codes of both halves of a word as exact fp16 pairs: 0x6400 | u is 1024 + u,
+// and flipping a code's sign bit makes it u = code + 8 (or + 128).
+// int4: nibbles (0, 4), (1, 5), (2, 6), (3, 7); the odd ones read as 16 u.
+US_DEV void decode_i4(uint32_t x, uint32_t (&q)[4]) {
+    const uint32_t y = x >> 8;
+    q[0] = hsub2(us::lop3<us::kLopAndXor>(x, 0x000F000Fu, 0x64086408u), 0x64086408u);
+    q[1] = hfma2(us::lop3<us::kLopAndXor>(x, 0x00F000F0u, 0x64806480u), 0x2C002C00u, 0xD480D480u);   // x/16 - 72
+    q[2] = hsub2(us::lop3<us::kLopAndXor>(y, 0x000F000Fu, 0x64086408u), 0x64086408u);
+    q[3] = hfma2(us::lop3<us::kLopAndXor>(y, 0x00F000F0u, 0x64806480u), 0x2C002C00u, 0xD480D480u);
+}
+// int8: bytes (0, 2), (1, 3)
+US_DEV void decode_i8(uint32_t x, uint32_t (&q)[2]) {
+    q[0] = hsub2(us::lop3<us::kLopAndXor>(x, 0x00FF00FFu, 0x64806480u), 0x64806480u);
+    q[1] = hsub2(us::lop3<us::kLopAndXor>(x >> 8, 0x00FF00FFu, 0x64806480u), 0x64806480u);
+}
+
+template <int N>
+US_DEV void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+    if constexpr (N >= 4) {
 #pragma unroll
-    for (int i = 0; i < DL; ++i) {
-        const int d = lane * DL + i;
-        x[i] = ELEM == US_I8 ? (float)(int8_t)row[d] : (float)us::sext4((uint32_t)row[d >> 1] >> (4 * (d & 1)));
+        for (int i = 0; i < N / 4; ++i) {
+            // 64 bytes apart: K rows of 128 bytes are read as two halves
+            const uint4 u = *reinterpret_cast<const uint4*>(p + 64 * i);
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+    } else if constexpr (N == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        w[0] = u.x, w[1] = u.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
 }
 
-template <int ELEM, int D>
-__global__ void __launch_bounds__(32 * kWarps)
-attn_row_kernel(const UsAttnParams p) {
-    constexpr int DL = D / 32;
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-    us::pdl_wait();
-    const UsKvCache& c = p.c;
-    const int i = blockIdx.x, hq = blockIdx.y, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int row0;
-    const int n = us::kv_rows(c, p.a, b, row0);
-    if (i >= n) return;
-    const int64_t t = row0 + i;
-    const int ctx = us::kv_context(c, p.a, b, n);
-    if (ctx < 0) return;
-    const int G = p.Hq / c.Hkv, h = hq / G;
-    const uint64_t mask = p.mask ? p.mask[t] : 0;
-    const float sc = p.scale * 1.4426950408889634f;           // exp2 domain
-    float q[DL], o[DL] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int d = 0; d < DL; ++d) q[d] = us::half_bits_to_float(p.Q[t * p.ldq + hq * D + lane * DL + d]) * sc;
-    for (int pos = warp; pos < ctx + n; pos += kWarps) {
-        const int j = pos - ctx;
-        if (j >= 0 && !(p.mask ? (mask >> j) & 1 : j <= i)) continue;
-        const int id = us::kv_page(c, b, pos);
-        if (id < 0) continue;
-        const int64_t e = us::kv_entry(c, id, h, pos);
-        const uint32_t s2 = reinterpret_cast<const uint32_t*>(c.scale)[e];
-        float x[DL], s = 0.f;
-        codes<ELEM, DL>(c.k + e * c.row_bytes, lane, x);
-#pragma unroll
-        for (int d = 0; d < DL; ++d) s += q[d] * x[d];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= us::half_bits_to_float((uint16_t)s2);
-        const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-        const float wv = w * us::half_bits_to_float((uint16_t)(s2 >> 16));
-        codes<ELEM, DL>(c.v + e * c.row_bytes, lane, x);
-#pragma unroll
-        for (int d = 0; d < DL; ++d) o[d] = o[d] * f + wv * x[d];
-        l = l * f + w;
-        m = mn;
-    }
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-    for (int d = 0; d < DL; ++d) so[warp][lane * DL + d] = o[d];
-    __syncthreads();
-    for (int d = threadIdx.x; d < D; d += 32 * kWarps) {
-        float top = -INFINITY, sum = 0.f, y = 0.f;
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - top);
-            sum += sl[w] * f;
-            y += so[w][d] * f;
+// Tiles and row blocks of a request; none where its arguments are not usable.
+struct Request {
+    int row0, n, ctx, tiles, nrb;
+};
+template <int ROWS>
+US_DEV Request load_request(const UsAttnParams& p, int b, unsigned* status) {
+    Request r = {0, 0, 0, 0, 0};
+    UsKvCache c = p.c;
+    c.status = status;
+    r.n = us::kv_rows(c, p.a, b, r.row0);
+    if (r.n > 0) {
+        r.ctx = us::kv_context(c, p.a, b, r.n);
+        if (r.ctx >= 0) {
+            r.tiles = (r.ctx + r.n + kTile - 1) / kTile;
+            r.nrb = (r.n * p.G + ROWS - 1) / ROWS;
         }
-        p.O[t * p.ldo + hq * D + d] = us::float_to_half_bits(sum == 0.f ? 0.f : y / sum);
+    }
+    return r;
+}
+
+// A place in the tile sequence: requests, key heads, row blocks, tiles.
+template <int ROWS>
+struct Cursor {
+    Request r;
+    int b, h, rb, tile;
+    US_DEV void next(const UsAttnParams& p) {
+        if (++tile < r.tiles) return;
+        tile = 0;
+        if (++rb < r.nrb) return;
+        rb = 0;
+        if (++h < p.c.Hkv) return;
+        h = 0;
+        do {
+            ++b;
+            if (b < p.c.B) r = load_request<ROWS>(p, b, nullptr);
+        } while (b < p.c.B && r.tiles == 0);
+    }
+};
+
+template <int ELEM, int D, int NT>
+__global__ void __launch_bounds__(kThreads, (Shape<ELEM, D, NT>::kMinB))
+attn_mma_kernel(const UsAttnParams p) {
+    using Sh = Shape<ELEM, D, NT>;
+    constexpr int kRows = Sh::kRows, kStages = Sh::kStages, kKW = Sh::kKW, kVW = Sh::kVW, kMT = Sh::kMT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* ring = smem;
+    float* join = reinterpret_cast<float*>(ring + kWarps * kStages * Sh::kStageBytes);
+    float* sm_m = join + Sh::kJoin / 4;                    // [kWarps][kRows]
+    float* sm_l = sm_m + kWarps * kRows;
+    uint64_t* sm_mask = reinterpret_cast<uint64_t*>(sm_l + kWarps * kRows);     // [kRows]
+    int* sm_tok = reinterpret_cast<int*>(sm_mask + kRows);                       // [kRows]
+    __shared__ uint64_t full[kWarps][kStages];
+    __shared__ int64_t sh_start[2];                        // found request's first tile; total
+    __shared__ int sh_b;
+    __shared__ int64_t sh_warp[kWarps];
+    __shared__ unsigned sh_last;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
+    const int G = p.G;
+    if (lane < kStages) us::mbar_init(&full[warp][lane], 1);
+    us::fence_mbar_init();
+    us::pdl_wait();
+
+    // ---- this CTA's tiles [t0, t1): a block-wide scan of the requests' tiles
+    const int per = (p.c.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
+    int64_t mine = 0;
+    for (int b = b0; b < min(b0 + per, p.c.B); ++b) {
+        const Request r = load_request<kRows>(p, b, blockIdx.x == 0 ? p.c.status : nullptr);
+        mine += (int64_t)r.tiles * r.nrb * p.c.Hkv;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) sh_warp[warp] = incl;
+    __syncthreads();
+    int64_t total = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sh_warp[w];
+        total += sh_warp[w];
+    }
+    const int64_t ctas = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
+    if ((int64_t)blockIdx.x >= ctas) return;
+    const int64_t t0 = (int64_t)blockIdx.x * total / ctas, t1 = ((int64_t)blockIdx.x + 1) * total / ctas;
+    if (before <= t0 && t0 < before + mine) {
+        for (int b = b0;; ++b) {
+            const Request r = load_request<kRows>(p, b, nullptr);
+            const int64_t k = (int64_t)r.tiles * r.nrb * p.c.Hkv;
+            if (t0 < before + k) {
+                sh_b = b;
+                sh_start[0] = t0 - before;
+                break;
+            }
+            before += k;
+        }
+    }
+    __syncthreads();
+    Cursor<kRows> cur;
+    cur.b = sh_b;
+    cur.r = load_request<kRows>(p, cur.b, nullptr);
+    {
+        const int64_t x = sh_start[0];
+        const int64_t seg = x / cur.r.tiles;
+        cur.tile = (int)(x - seg * cur.r.tiles);
+        cur.h = (int)(seg / cur.r.nrb);
+        cur.rb = (int)(seg - (int64_t)cur.h * cur.r.nrb);
+    }
+    const int count = (int)(t1 - t0);
+
+    // ---- producer: the warp's block of tile `pc` into stage s
+    Cursor<kRows> pc = cur;
+    uint8_t* wring = ring + warp * kStages * Sh::kStageBytes;
+    uint32_t skip = 0;                                     // stages without a block
+    auto issue = [&](int s) {
+        const int pos = pc.tile * kTile + warp * kBlock;
+        int id = -1;
+        if (pos < pc.r.ctx + pc.r.n) id = us::kv_page(p.c, pc.b, pos);
+        skip = id < 0 ? skip | (1u << s) : skip & ~(1u << s);
+        if (id >= 0 && lane < 3) {
+            if (lane == 0) us::mbar_arrive_expect_tx(&full[warp][s], (uint32_t)Sh::kStageBytes);
+            const int64_t e = us::kv_entry(p.c, id, pc.h, pos);
+            const uint8_t* src = lane == 0 ? p.c.k + e * Sh::kRow
+                               : lane == 1 ? p.c.v + e * Sh::kRow
+                                           : reinterpret_cast<const uint8_t*>(p.c.scale) + e * 4;
+            us::bulk_g2s(wring + s * Sh::kStageBytes + lane * kBlock * Sh::kRow, src,
+                         lane == 2 ? (uint32_t)kBlock * 4u : (uint32_t)(kBlock * Sh::kRow), &full[warp][s]);
+        }
+        pc.next(p);
+    };
+    const int ahead = count < kStages ? count : kStages;
+    for (int s = 0; s < ahead; ++s) issue(s);
+
+    // ---- consumer state: maxima, sums and O^T of the warp's positions
+    float m[NT][2], l[NT][2], o[kMT][NT][4], vref = 0.f, vmul = 0.f;
+    uint32_t qf[Sh::kKS][NT][2];
+    const float sc = p.scale * 1.4426950408889634f;        // weights as powers of two
+    uint32_t phase = 0;
+    bool failed = false;
+    const int rt = ((g & 1) << 2) | (g >> 1);              // token of row g (k index 2c -> c, 2c + 1 -> c + 4)
+
+    auto begin_segment = [&]() {
+        const int rows = cur.r.n * G;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int t = 0; t < kMT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][nt][e] = 0.f;
+            const int r = cur.rb * kRows + 8 * nt + g;
+            const int i = r / G;
+            const uint16_t* q = p.Q + (int64_t)(cur.r.row0 + i) * p.ldq + (cur.h * G + r - i * G) * D;
+#pragma unroll
+            for (int w = 0; w < kKW; ++w) {
+                if constexpr (ELEM == US_I4) {
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (r < rows) u = *reinterpret_cast<const uint4*>(q + c4 * (D / 4) + 8 * w);
+                    qf[2 * w][nt][0] = __byte_perm(u.x, u.z, 0x5410), qf[2 * w][nt][1] = __byte_perm(u.x, u.z, 0x7632);
+                    qf[2 * w + 1][nt][0] = __byte_perm(u.y, u.w, 0x5410), qf[2 * w + 1][nt][1] = __byte_perm(u.y, u.w, 0x7632);
+                } else {
+                    uint2 u = make_uint2(0, 0);
+                    if (r < rows) u = *reinterpret_cast<const uint2*>(q + (w >> 2) * 64 + c4 * 16 + 4 * (w & 3));
+                    qf[w][nt][0] = __byte_perm(u.x, u.y, 0x5410), qf[w][nt][1] = __byte_perm(u.x, u.y, 0x7632);
+                }
+            }
+        }
+        vref = vmul = 0.f;
+        if (threadIdx.x < kRows) {
+            const int r = cur.rb * kRows + threadIdx.x, i = r / G;
+            sm_tok[threadIdx.x] = r < rows ? i : -1;
+            sm_mask[threadIdx.x] = r < rows && p.mask ? p.mask[cur.r.row0 + i] : 0;
+        }
+        __syncthreads();
+    };
+
+    begin_segment();
+    int s = 0;
+    for (int it = 0; it < count; ++it) {
+        if (!((skip >> s) & 1u)) {
+            if (!failed && !us::mbar_wait(&full[warp][s], (phase >> s) & 1u, p.c.status)) failed = true;
+            phase ^= 1u << s;
+            const uint8_t* st = wring + s * Sh::kStageBytes;
+            const int pos = cur.tile * kTile + warp * kBlock;
+            // ---- S^T = Ck Q^T
+            float sacc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sacc[nt][e] = 0.f;
+            uint32_t k0[kKW], k1[kKW];
+            lds_words(st + rt * Sh::kRow + c4 * (kKW >= 4 ? 16 : 4 * kKW), k0);
+            lds_words(st + (rt + 8) * Sh::kRow + c4 * (kKW >= 4 ? 16 : 4 * kKW), k1);
+#pragma unroll
+            for (int w = 0; w < kKW; ++w) {
+                if constexpr (ELEM == US_I4) {
+                    uint32_t x[4], y[4];
+                    decode_i4(k0[w], x);
+                    decode_i4(k1[w], y);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        us::mma_m16n8k16_f16(sacc[nt], x[0], y[0], x[1], y[1], qf[2 * w][nt][0], qf[2 * w][nt][1]);
+                        us::mma_m16n8k16_f16(sacc[nt], x[2], y[2], x[3], y[3], qf[2 * w + 1][nt][0], qf[2 * w + 1][nt][1]);
+                    }
+                } else {
+                    uint32_t x[2], y[2];
+                    decode_i8(k0[w], x);
+                    decode_i8(k1[w], y);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        us::mma_m16n8k16_f16(sacc[nt], x[0], y[0], x[1], y[1], qf[w][nt][0], qf[w][nt][1]);
+                }
+            }
+            // ---- scores (row 0: token rt, row 1: token rt + 8), masks
+            const uint32_t* ss = reinterpret_cast<const uint32_t*>(st + 2 * kBlock * Sh::kRow);
+            const uint32_t s0 = ss[rt], s1 = ss[rt + 8];
+            const float ks[2] = {us::half_bits_to_float((uint16_t)s0) * sc, us::half_bits_to_float((uint16_t)s1) * sc};
+            const float vs[2] = {us::half_bits_to_float((uint16_t)(s0 >> 16)), us::half_bits_to_float((uint16_t)(s1 >> 16))};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sacc[nt][e] *= ks[e >> 1];
+            const bool edge = pos + kBlock > cur.r.ctx;
+            if (edge) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int j = pos + rt + 8 * u - cur.r.ctx;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int r = 8 * nt + 2 * c4 + e;
+                            const bool seen = j < 0 || (j < cur.r.n && (p.mask ? (sm_mask[r] >> (j & 63)) & 1 : j <= sm_tok[r]));
+                            if (!seen) sacc[nt][2 * u + e] = -INFINITY;
+                        }
+                }
+            }
+            // ---- running maxima, rescaled only where one has grown by 2^4
+            // (unseen entries may hold any scale: only finite ones count)
+            const float va = fmaxf(fabsf(vs[0]) < INFINITY ? fabsf(vs[0]) : 0.f, fabsf(vs[1]) < INFINITY ? fabsf(vs[1]) : 0.f);
+            bool grow = va >= vref;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) grow |= fmaxf(sacc[nt][e], sacc[nt][e + 2]) > m[nt][e] + kMaxLag;
+            if (__any_sync(0xffffffffu, grow)) {
+                float vm = va;
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
+                float fv = 1.f;
+                if (vm >= vref) {                              // the power of two above it
+                    const float nv = __uint_as_float((__float_as_uint(fmaxf(vm, 1e-30f)) & 0x7F800000u) + 0x00800000u);
+                    fv = vref / nv;
+                    vref = nv;
+                    vmul = kVHead / nv;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(sacc[nt][e], sacc[nt][e + 2]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        mx = fmaxf(mx, m[nt][e]);
+                        const float f = mx == -INFINITY ? 1.f : ex2(m[nt][e] - mx);
+                        m[nt][e] = mx;
+                        l[nt][e] *= f;
+#pragma unroll
+                        for (int t = 0; t < kMT; ++t) {
+                            o[t][nt][e] *= f * fv;
+                            o[t][nt][e + 2] *= f * fv;
+                        }
+                    }
+            }
+            // ---- weights; with V's scale, as fp16, they are the B operand of O^T
+            uint32_t pf[NT][2];
+            const float wv[2] = {vs[0] * vmul, vs[1] * vmul};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float mm = m[nt][e & 1];
+                    w[e] = ex2(sacc[nt][e] - (mm == -INFINITY ? 0.f : mm));
+                    l[nt][e & 1] += w[e];
+                }
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = edge && w[e] == 0.f ? 0.f : w[e] * wv[e >> 1];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) pf[nt][u] = transpose8x8(pack_half2(x[2 * u], x[2 * u + 1]));
+            }
+            // ---- O^T += Cv^T P^T
+            uint32_t v[4][kVW];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                lds_words(st + kBlock * Sh::kRow + (c4 + 4 * i) * Sh::kRow + g * (4 * kVW), v[i]);
+#pragma unroll
+            for (int w = 0; w < kVW; ++w)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const uint32_t x01 = __byte_perm(v[0][w], v[1][w], hh ? 0x7632 : 0x5410);
+                    const uint32_t x23 = __byte_perm(v[2][w], v[3][w], hh ? 0x7632 : 0x5410);
+                    if constexpr (ELEM == US_I4) {
+                        uint32_t a[4], b[4];
+                        decode_i4(x01, a);
+                        decode_i4(x23, b);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            us::mma_m16n8k16_f16(o[4 * w + 2 * hh][nt], a[0], a[1], b[0], b[1], pf[nt][0], pf[nt][1]);
+                            us::mma_m16n8k16_f16(o[4 * w + 2 * hh + 1][nt], a[2], a[3], b[2], b[3], pf[nt][0], pf[nt][1]);
+                        }
+                    } else {
+                        uint32_t a[2], b[2];
+                        decode_i8(x01, a);
+                        decode_i8(x23, b);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            us::mma_m16n8k16_f16(o[2 * w + hh][nt], a[0], a[1], b[0], b[1], pf[nt][0], pf[nt][1]);
+                    }
+                }
+        }
+        __syncwarp();                                      // every lane has read the stage
+        if (it + kStages < count) issue(s);
+        s = s + 1 == kStages ? 0 : s + 1;
+
+        // ---- the end of the segment, or of this CTA's part of it
+        if (cur.tile + 1 == cur.r.tiles || it + 1 == count) {
+            const int rows = min(kRows, cur.r.n * G - cur.rb * kRows);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = l[nt][e];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                    if (g == 0) {
+                        sm_m[warp * kRows + 8 * nt + 2 * c4 + e] = m[nt][e];
+                        sm_l[warp * kRows + 8 * nt + 2 * c4 + e] = x;
+                    }
+                }
+            __syncthreads();
+            // segment [s0, s1) of the tile sequence, this CTA's part, who else has one
+            const int64_t s0 = t0 + it - cur.tile, s1 = s0 + cur.r.tiles;
+            const bool whole = s0 >= t0 && s1 <= t1;
+            const int first = (int)(((s0 + 1) * ctas - 1) / total), last = (int)((s1 * ctas - 1) / total);
+            const int64_t fstart = (int64_t)first * total / ctas;
+            float* slots = p.ws_slots;
+            auto slot_of = [&](int c) {                    // a CTA's second slot: a segment that begins inside it
+                return slots + ((int64_t)2 * c + (c == first && s0 > fstart ? 1 : 0)) * Sh::kSlotFloats;
+            };
+            float* slot = slot_of(blockIdx.x);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * nt + 2 * c4 + e;
+                    float t = sm_m[r];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) t = fmaxf(t, sm_m[w * kRows + r]);
+                    const float f = (m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - t)) * (vref * (1.f / kVHead));
+#pragma unroll
+                    for (int q = 0; q < kMT; ++q) o[q][nt][e] *= f, o[q][nt][e + 2] *= f;
+                }
+            // row sums over the warps
+            auto row_state = [&](int r, float& t, float& sum) {
+                t = sm_m[r];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) t = fmaxf(t, sm_m[w * kRows + r]);
+                sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float mw = sm_m[w * kRows + r];
+                    sum += sm_l[w * kRows + r] * (mw == -INFINITY ? 0.f : ex2(mw - t));
+                }
+            };
+            if (!whole && threadIdx.x < kRows) {
+                float t, sum;
+                row_state(threadIdx.x, t, sum);
+                __stcg(slot + threadIdx.x, t);
+                __stcg(slot + kRows + threadIdx.x, sum);
+            }
+            auto store = [&](int r, int dim, float x, float y) {
+                if (r >= rows) return;
+                const int rr = cur.rb * kRows + r, i = rr / G;
+                uint16_t* out = p.O + (int64_t)(cur.r.row0 + i) * p.ldo + (cur.h * G + rr - i * G) * D + dim;
+                *reinterpret_cast<uint32_t*>(out) = pack_half2(x, y);
+            };
+            constexpr int kPer = 8 / NT;                    // 16-dimension blocks joined at a time
+#pragma unroll
+            for (int ch = 0; ch < (kMT + kPer - 1) / kPer; ++ch) {
+                constexpr int kBlocks = kPer < kMT ? kPer : kMT;
+                if (ch) __syncthreads();
+#pragma unroll
+                for (int q = 0; q < kBlocks; ++q)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            join[((warp * kBlocks + q) * NT + nt) * 128 + e * 32 + lane] = o[ch * kBlocks + q][nt][e];
+                __syncthreads();
+#pragma unroll
+                for (int x = threadIdx.x; x < kBlocks * NT * 64; x += kThreads) {
+                    const int e = (x >> 5) & 1, nt = (x >> 6) % NT, q = (x >> 6) / NT;
+                    float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float* jw = join + ((w * kBlocks + q) * NT + nt) * 128 + e * 32 + lane;
+                        y0 += jw[0];
+                        y1 += jw[64];
+                    }
+                    if (whole) {
+                        const int r = 8 * nt + 2 * c4 + e;
+                        float t, sum;
+                        row_state(r, t, sum);
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        store(r, g * (D / 8) + 2 * (ch * kBlocks + q), y0 * inv, y1 * inv);
+                    } else {
+                        __stcg(reinterpret_cast<float2*>(slot + 2 * kRows) + ch * kBlocks * NT * 64 + x, make_float2(y0, y1));
+                    }
+                }
+            }
+            if (!whole) {
+                __threadfence();
+                __syncthreads();
+                if (threadIdx.x == 0) sh_last = atomicAdd(p.ws_count + first, 1u) == (unsigned)(last - first);
+                __syncthreads();
+                if (sh_last) {
+                    __threadfence();
+                    if (threadIdx.x == 0) p.ws_count[first] = 0;
+                    for (int x = threadIdx.x; x < kMT * NT * 64; x += kThreads) {
+                        const int e = (x >> 5) & 1, nt = (x >> 6) % NT, q = (x >> 6) / NT, r = 8 * nt + 2 * c4 + e;
+                        if (r >= rows) continue;
+                        float t = -INFINITY, sum = 0.f, y0 = 0.f, y1 = 0.f;
+                        for (int c = first; c <= last; ++c) t = fmaxf(t, __ldcg(slot_of(c) + r));
+                        for (int c = first; c <= last; ++c) {
+                            const float* sl = slot_of(c);
+                            const float mc = __ldcg(sl + r), f = mc == -INFINITY ? 0.f : ex2(mc - t);
+                            const float2 y = __ldcg(reinterpret_cast<const float2*>(sl + 2 * kRows) + x);
+                            sum += __ldcg(sl + kRows + r) * f;
+                            y0 += y.x * f;
+                            y1 += y.y * f;
+                        }
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        store(r, g * (D / 8) + 2 * q, y0 * inv, y1 * inv);
+                    }
+                }
+            }
+            if (it + 1 < count) {
+                cur.next(p);
+                begin_segment();                           // its barrier also frees the join buffer
+            }
+        } else {
+            ++cur.tile;
+        }
     }
     us::pdl_launch_dependents();
+}
+
+template <int ELEM, int D, int NT>
+struct Plan {
+    using Sh = Shape<ELEM, D, NT>;
+    static int grid() { return us::num_sms() * Sh::kMinB < 1024 ? us::num_sms() * Sh::kMinB : 1024; }
+    static size_t ws() { return 4096 + (size_t)2 * grid() * Sh::kSlotFloats * 4; }
+    static us_status launch(UsAttnParams p, cudaStream_t st) {
+        p.ws_count = static_cast<unsigned*>(p.ws);
+        p.ws_slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + 4096);
+        auto kern = attn_mma_kernel<ELEM, D, NT>;
+        static bool ready[64] = {};                        // the attribute is set once a device
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return US_ERR_CUDA;
+        if (!ready[dev]) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess)
+                return US_ERR_CUDA;
+            ready[dev] = true;
+        }
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)grid());
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Sh::kSmem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? US_OK : US_ERR_CUDA;
+    }
+};
+
+// f(Plan) for the cache's type and head width and the rows per key head
+template <class F>
+auto with_plan(const UsAttnParams& p, F f) {
+    const int rows = p.a.max_n * p.G;
+#define US_ATTN_PICK(E, D) (rows <= 8 ? f(Plan<E, D, 1>()) : f(Plan<E, D, 2>()))
+    if (p.c.elem == US_I8) return p.c.D == 64 ? US_ATTN_PICK(US_I8, 64) : US_ATTN_PICK(US_I8, 128);
+    return p.c.D == 64 ? US_ATTN_PICK(US_I4, 64) : US_ATTN_PICK(US_I4, 128);
+#undef US_ATTN_PICK
 }
 
 }  // namespace
 
 namespace us {
 
-size_t attn_ws(const UsAttnParams&) { return 0; }
+size_t attn_ws(const UsAttnParams& p) {
+    return with_plan(p, [](auto plan) { return decltype(plan)::ws(); });
+}
 
 us_status launch_attn(const UsAttnParams& p, cudaStream_t st) {
-    auto kern = p.c.elem == US_I8 ? (p.c.D == 64 ? attn_row_kernel<US_I8, 64> : attn_row_kernel<US_I8, 128>)
-                                  : (p.c.D == 64 ? attn_row_kernel<US_I4, 64> : attn_row_kernel<US_I4, 128>);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.a.max_n, (unsigned)p.Hq, (unsigned)p.c.B);
-    cfg.blockDim = dim3(32 * kWarps);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? US_OK : US_ERR_CUDA;
+    return with_plan(p, [&](auto plan) { return decltype(plan)::launch(p, st); });
 }
 
 }  // namespace us

@@ -32,10 +32,12 @@ struct UsAttnParams {
     const uint16_t* Q;
     uint16_t* O;
     int64_t ldq, ldo;
-    int Hq;
+    int Hq, G;                       // G = Hq / Hkv
     float scale;
     const uint64_t* mask;            // per token, or nullptr: a chain
     void* ws;
+    unsigned* ws_count;              // arrival counters, zero between calls
+    float* ws_slots;                 // partial states
 };
 
 namespace us {
