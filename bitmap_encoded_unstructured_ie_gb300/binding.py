@@ -396,7 +396,8 @@ class KVCache:
         assert self.page_table.dtype == torch.int32
         d = us_kv_cache(self.elem, self.D, Hkv, page_size, num_pages, B, max_pages, 0, _dptr(self.k), _dptr(self.v),
                         _dptr(self.scale), _dptr(self.page_table))
-        for name, value in (("B", B), ("Hkv", Hkv), ("page_size", page_size), ("_desc", d), ("_ref", ctypes.byref(d))):
+        for name, value in (("B", B), ("Hkv", Hkv), ("page_size", page_size), ("device", self.k.device.index),
+                            ("_desc", d), ("_ref", ctypes.byref(d))):
             object.__setattr__(self, name, value)
 
 
@@ -423,8 +424,14 @@ def _i32(x: torch.Tensor, n: int) -> int:
     return x.data_ptr()
 
 
-def _raw_stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+# current_stream() builds an object (2.9 us on the GPU machine's host, of a call's 9); the raw handle does not (0.1 us).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, C: KVCache) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream().cuda_stream if _current_raw_stream is None else _current_raw_stream(C.device)
 
 
 def us_kv_write(C: KVCache, K: torch.Tensor, V: torch.Tensor, tok_off: torch.Tensor, pos: torch.Tensor, max_n: int,
@@ -434,7 +441,7 @@ def us_kv_write(C: KVCache, K: torch.Tensor, V: torch.Tensor, tok_off: torch.Ten
     Tv, vp, ldv = _rows(V, C.Hkv, C.D)
     assert T == Tv
     _check("us_kv_write", (_lib or load()).us_kv_write(C._ref, kp, ldk, vp, ldv, T, _i32(tok_off, C.B + 1),
-                                                       _i32(pos, C.B), max_n, _raw_stream(stream)))
+                                                       _i32(pos, C.B), max_n, _raw_stream(stream, C)))
 
 
 def us_kv_read(C: KVCache, tok_off: torch.Tensor, pos: torch.Tensor, max_n: int, K: torch.Tensor, V: torch.Tensor,
@@ -444,14 +451,14 @@ def us_kv_read(C: KVCache, tok_off: torch.Tensor, pos: torch.Tensor, max_n: int,
     Tv, vp, ldv = _rows(V, C.Hkv, C.D)
     assert T == Tv
     _check("us_kv_read", (_lib or load()).us_kv_read(C._ref, T, _i32(tok_off, C.B + 1), _i32(pos, C.B), max_n, kp, ldk,
-                                                     vp, ldv, _raw_stream(stream)))
+                                                     vp, ldv, _raw_stream(stream, C)))
 
 
 def us_kv_commit(C: KVCache, acc_off: torch.Tensor, acc: torch.Tensor, pos: torch.Tensor, max_n: int, stream=None):
     """Move the accepted drafted tokens' entries, pos[b] + acc[i], to pos[b] + i."""
     T = acc.numel()
     _check("us_kv_commit", (_lib or load()).us_kv_commit(C._ref, T, _i32(acc_off, C.B + 1), _i32(acc, T),
-                                                         _i32(pos, C.B), max_n, _raw_stream(stream)))
+                                                         _i32(pos, C.B), max_n, _raw_stream(stream, C)))
 
 
 def us_attn_kv_workspace_bytes(C: KVCache, Hq: int, max_n: int) -> int:
@@ -478,7 +485,7 @@ def us_attn_kv(C: KVCache, Q: torch.Tensor, tok_off: torch.Tensor, pos: torch.Te
     _check("us_attn_kv", (_lib or load()).us_attn_kv(C._ref, qp, ldq, Hq, T, _i32(tok_off, C.B + 1), _i32(pos, C.B),
                                                      None if mask is None else mask.data_ptr(), max_n, scale, op, ldo,
                                                      ws.data_ptr(), ws.numel() * ws.element_size(),
-                                                     _raw_stream(stream)))
+                                                     _raw_stream(stream, C)))
 
 
 def us_validate_host(bitmap, tile_off, values, M, K, TM, TK, elem, order) -> int:

@@ -151,6 +151,90 @@ struct Cursor {
     }
 };
 
+// Where a row's fp16 outputs go: D values at row r of row block rb, head h.
+template <int ROWS>
+US_DEV uint16_t* out_row(const UsAttnParams& p, int row0, int h, int rb, int r, int D) {
+    const int rr = rb * ROWS + r, i = rr / p.G;
+    return p.O + (int64_t)(row0 + i) * p.ldo + (int64_t)(h * p.G + rr - i * p.G) * D;
+}
+
+// A segment shared by CTAs first .. last (second: the first of them left its
+// state in its second slot).
+struct Part {
+    int first, last, row0, h, rb, rows;
+    bool second;
+};
+
+// Joins the partial states of a shared segment: the rows' maxima, then per
+// batch of states their factors (in `buf`), then O^T, eight states' loads at a
+// time.
+template <int ELEM, int D, int NT>
+US_DEV void join_states(const UsAttnParams& p, float* buf, float* top, float* sums, const Part& a) {
+    using Sh = Shape<ELEM, D, NT>;
+    constexpr int kRows = Sh::kRows, kPairs = D * kRows / 2, kMine = kPairs / kThreads, kBatch = 4 * kThreads / kRows;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
+    const int first = a.first, np = a.last - a.first + 1;
+    auto slot_of = [&](int c) {
+        return p.ws_slots + ((int64_t)2 * c + (c == first && a.second ? 1 : 0)) * Sh::kSlotFloats;
+    };
+    const int r = threadIdx.x % kRows, j0 = threadIdx.x / kRows;
+    float t = -INFINITY;
+#pragma unroll 4
+    for (int j = j0; j < np; j += kThreads / kRows) t = fmaxf(t, __ldcg(slot_of(first + j) + r));
+    buf[threadIdx.x] = t;
+    __syncthreads();
+    if (threadIdx.x < kRows) {
+        for (int j = 1; j < kThreads / kRows; ++j) t = fmaxf(t, buf[j * kRows + r]);
+        top[r] = t;
+        sums[r] = 0.f;
+    }
+    float2 y[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) y[k] = make_float2(0.f, 0.f);
+    for (int base = 0; base < np; base += kBatch) {
+        const int nb = min(kBatch, np - base);
+        __syncthreads();
+        for (int x = threadIdx.x; x < nb * kRows; x += kThreads) {
+            const float* sl = slot_of(first + base + x / kRows) + x % kRows;
+            const float mc = __ldcg(sl), lc = __ldcg(sl + kRows);
+            const float f = mc == -INFINITY ? 0.f : ex2(mc - top[x % kRows]);
+            buf[x] = f;
+            buf[kBatch * kRows + x] = lc * f;
+        }
+        __syncthreads();
+        if (threadIdx.x < kRows) {
+            float sum = sums[r];
+            for (int j = 0; j < nb; ++j) sum += buf[kBatch * kRows + j * kRows + r];
+            sums[r] = sum;
+        }
+        for (int j = 0; j < nb; j += 8)
+#pragma unroll
+            for (int k = 0; k < kMine; ++k) {
+                const int x = threadIdx.x + k * kThreads, row = 8 * ((x >> 6) % NT) + 2 * c4 + ((x >> 5) & 1);
+                float2 v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    v[u] = j + u < nb ? __ldcg(reinterpret_cast<const float2*>(slot_of(first + base + j + u) + 2 * kRows) + x)
+                                      : make_float2(0.f, 0.f);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float f = j + u < nb ? buf[(j + u) * kRows + row] : 0.f;
+                    y[k].x += v[u].x * f;
+                    y[k].y += v[u].y * f;
+                }
+            }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        const int x = threadIdx.x + k * kThreads, row = 8 * ((x >> 6) % NT) + 2 * c4 + ((x >> 5) & 1);
+        const float sum = sums[row], inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (row < a.rows)
+            *reinterpret_cast<uint32_t*>(out_row<kRows>(p, a.row0, a.h, a.rb, row, D) + g * (D / 8) + 2 * ((x >> 6) / NT)) =
+                pack_half2(y[k].x * inv, y[k].y * inv);
+    }
+}
+
 template <int ELEM, int D, int NT>
 __global__ void __launch_bounds__(kThreads, (Shape<ELEM, D, NT>::kMinB))
 attn_mma_kernel(const UsAttnParams p) {
@@ -164,10 +248,12 @@ attn_mma_kernel(const UsAttnParams p) {
     uint64_t* sm_mask = reinterpret_cast<uint64_t*>(sm_l + kWarps * kRows);     // [kRows]
     int* sm_tok = reinterpret_cast<int*>(sm_mask + kRows);                       // [kRows]
     __shared__ uint64_t full[kWarps][kStages];
-    __shared__ int64_t sh_start[2];                        // found request's first tile; total
+    __shared__ Request sh_req;                             // the request t0 lies in, and t0's place in it
+    __shared__ int64_t sh_start;
     __shared__ int sh_b;
     __shared__ int64_t sh_warp[kWarps];
     __shared__ unsigned sh_last;
+    __shared__ Part sh_part[2];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
     const int G = p.G;
@@ -178,8 +264,9 @@ attn_mma_kernel(const UsAttnParams p) {
     // ---- this CTA's tiles [t0, t1): a block-wide scan of the requests' tiles
     const int per = (p.c.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
     int64_t mine = 0;
+    Request r = {0, 0, 0, 0, 0};
     for (int b = b0; b < min(b0 + per, p.c.B); ++b) {
-        const Request r = load_request<kRows>(p, b, blockIdx.x == 0 ? p.c.status : nullptr);
+        r = load_request<kRows>(p, b, blockIdx.x == 0 ? p.c.status : nullptr);
         mine += (int64_t)r.tiles * r.nrb * p.c.Hkv;
     }
     int64_t incl = mine;
@@ -201,11 +288,12 @@ attn_mma_kernel(const UsAttnParams p) {
     const int64_t t0 = (int64_t)blockIdx.x * total / ctas, t1 = ((int64_t)blockIdx.x + 1) * total / ctas;
     if (before <= t0 && t0 < before + mine) {
         for (int b = b0;; ++b) {
-            const Request r = load_request<kRows>(p, b, nullptr);
+            if (per > 1) r = load_request<kRows>(p, b, nullptr);
             const int64_t k = (int64_t)r.tiles * r.nrb * p.c.Hkv;
             if (t0 < before + k) {
                 sh_b = b;
-                sh_start[0] = t0 - before;
+                sh_req = r;
+                sh_start = t0 - before;
                 break;
             }
             before += k;
@@ -214,9 +302,9 @@ attn_mma_kernel(const UsAttnParams p) {
     __syncthreads();
     Cursor<kRows> cur;
     cur.b = sh_b;
-    cur.r = load_request<kRows>(p, cur.b, nullptr);
+    cur.r = sh_req;
     {
-        const int64_t x = sh_start[0];
+        const int64_t x = sh_start;
         const int64_t seg = x / cur.r.tiles;
         cur.tile = (int)(x - seg * cur.r.tiles);
         cur.h = (int)(seg / cur.r.nrb);
@@ -253,6 +341,7 @@ attn_mma_kernel(const UsAttnParams p) {
     const float sc = p.scale * 1.4426950408889634f;        // weights as powers of two
     uint32_t phase = 0;
     bool failed = false;
+    int parts = 0;
     const int rt = ((g & 1) << 2) | (g >> 1);              // token of row g (k index 2c -> c, 2c + 1 -> c + 4)
 
     auto begin_segment = [&]() {
@@ -497,12 +586,6 @@ attn_mma_kernel(const UsAttnParams p) {
                 __stcg(slot + threadIdx.x, t);
                 __stcg(slot + kRows + threadIdx.x, sum);
             }
-            auto store = [&](int r, int dim, float x, float y) {
-                if (r >= rows) return;
-                const int rr = cur.rb * kRows + r, i = rr / G;
-                uint16_t* out = p.O + (int64_t)(cur.r.row0 + i) * p.ldo + (cur.h * G + rr - i * G) * D + dim;
-                *reinterpret_cast<uint32_t*>(out) = pack_half2(x, y);
-            };
             constexpr int kPer = 8 / NT;                    // 16-dimension blocks joined at a time
 #pragma unroll
             for (int ch = 0; ch < (kMT + kPer - 1) / kPer; ++ch) {
@@ -531,37 +614,17 @@ attn_mma_kernel(const UsAttnParams p) {
                         float t, sum;
                         row_state(r, t, sum);
                         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                        store(r, g * (D / 8) + 2 * (ch * kBlocks + q), y0 * inv, y1 * inv);
+                        if (r < rows)
+                            *reinterpret_cast<uint32_t*>(out_row<kRows>(p, cur.r.row0, cur.h, cur.rb, r, D) + g * (D / 8) +
+                                                         2 * (ch * kBlocks + q)) = pack_half2(y0 * inv, y1 * inv);
                     } else {
                         __stcg(reinterpret_cast<float2*>(slot + 2 * kRows) + ch * kBlocks * NT * 64 + x, make_float2(y0, y1));
                     }
                 }
             }
-            if (!whole) {
-                __threadfence();
-                __syncthreads();
-                if (threadIdx.x == 0) sh_last = atomicAdd(p.ws_count + first, 1u) == (unsigned)(last - first);
-                __syncthreads();
-                if (sh_last) {
-                    __threadfence();
-                    if (threadIdx.x == 0) p.ws_count[first] = 0;
-                    for (int x = threadIdx.x; x < kMT * NT * 64; x += kThreads) {
-                        const int e = (x >> 5) & 1, nt = (x >> 6) % NT, q = (x >> 6) / NT, r = 8 * nt + 2 * c4 + e;
-                        if (r >= rows) continue;
-                        float t = -INFINITY, sum = 0.f, y0 = 0.f, y1 = 0.f;
-                        for (int c = first; c <= last; ++c) t = fmaxf(t, __ldcg(slot_of(c) + r));
-                        for (int c = first; c <= last; ++c) {
-                            const float* sl = slot_of(c);
-                            const float mc = __ldcg(sl + r), f = mc == -INFINITY ? 0.f : ex2(mc - t);
-                            const float2 y = __ldcg(reinterpret_cast<const float2*>(sl + 2 * kRows) + x);
-                            sum += __ldcg(sl + kRows + r) * f;
-                            y0 += y.x * f;
-                            y1 += y.y * f;
-                        }
-                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                        store(r, g * (D / 8) + 2 * q, y0 * inv, y1 * inv);
-                    }
-                }
+            if (!whole) {                                  // joined after the loop, which needs the registers
+                if (threadIdx.x == 0) sh_part[parts] = Part{first, last, cur.r.row0, cur.h, cur.rb, rows, s0 > fstart};
+                ++parts;
             }
             if (it + 1 < count) {
                 cur.next(p);
@@ -570,6 +633,18 @@ attn_mma_kernel(const UsAttnParams p) {
         } else {
             ++cur.tile;
         }
+    }
+    // ---- shared segments (at most two a CTA): the last CTA to arrive joins them
+    for (int i = 0; i < parts; ++i) {
+        __threadfence();
+        __syncthreads();
+        const Part a = sh_part[i];
+        if (threadIdx.x == 0) sh_last = atomicAdd(p.ws_count + a.first, 1u) == (unsigned)(a.last - a.first);
+        __syncthreads();
+        if (!sh_last) continue;
+        __threadfence();
+        if (threadIdx.x == 0) p.ws_count[a.first] = 0;
+        join_states<ELEM, D, NT>(p, join, sm_m, sm_l, a);
     }
     us::pdl_launch_dependents();
 }
