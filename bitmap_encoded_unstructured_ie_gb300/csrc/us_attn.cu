@@ -18,12 +18,18 @@
 // lane % 4) takes D/4 codes of K of tokens g' and g' + 8, and of V the D/8
 // dimensions from g D/8 of tokens c, c + 4, c + 8, c + 12.
 //
-// Work: the (request, key head, row block) segments are cut into tiles of 64
-// positions, and the tile sequence is spread evenly over the CTAs, whatever
-// the lengths (they are read on the device).  A warp takes 16 positions of each
-// tile: three bulk copies (K, V, scales; a page's entries of one head are
-// contiguous) into the warp's own ring, several tiles ahead and across
-// segments.  A segment shared by several CTAs leaves partial states in the
+// Codes of K need no conversion beyond a mask: with the sign bit flipped, a code
+// is u = code + 8 (or + 128) >= 0, and the fp16 number with the bits of u is
+// u 2^-24 exactly.  The product starts from -8 (-128) 2^-24 sum(q), and the odd
+// nibbles, read in place as 16 u, have their own accumulator.  V's codes are made
+// signed first: a sum over many positions would drift by the offset's rounding.
+//
+// Work: the (request, key head, row block) segments are cut into tiles of 64 or
+// 128 positions, and the tile sequence is spread evenly over the CTAs, whatever
+// the lengths (they are read on the device).  A warp takes 16 or 32 positions of
+// each tile: per 16 positions three bulk copies (K, V, scales; a page's entries
+// of one head are contiguous) into the warp's own ring, several tiles ahead and
+// across segments.  A segment shared by several CTAs leaves partial states in the
 // workspace; the CTA that arrives last joins them in the order of the tiles.
 #include "us_internal.h"
 #include "us_kv.cuh"
@@ -31,8 +37,7 @@
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kBlock = 16;                        // positions of a warp's step
-constexpr int kTile = kWarps * kBlock;            // positions of a CTA's step
+constexpr int kBlock = 16;                        // positions of one MMA's rows: they lie in one page
 constexpr float kMaxLag = 4.f;                    // a row's maximum may lag by 2^4 before the state is rescaled
 constexpr float kVHead = 2048.f;                  // weights reach 2^4 2^11 < 65504 as fp16: small ones keep their bits
 
@@ -45,9 +50,12 @@ struct Shape {
     static constexpr int kKS = D / 16;                              // MMA steps over the dimensions
     static constexpr int kMT = D / 16;                              // 16-dimension blocks of O^T
     static constexpr int kMinB = NT == 1 ? 4 : NT == 2 ? 3 : 2;     // CTAs an SM
-    static constexpr int kStageBytes = 2 * kBlock * kRow + kBlock * 4;
+    static constexpr int kSub = kRow == 128 ? 1 : 2;                // 16-position blocks of a warp's step
+    static constexpr int kStep = kSub * kBlock;
+    static constexpr int kTile = kWarps * kStep;                    // positions of a CTA's step
+    static constexpr int kStageBytes = 2 * kStep * kRow + kStep * 4;
     static constexpr int kJoin = kWarps * 32 * 32 * 4;              // O^T of four warps, 32 values a lane at a time
-    static constexpr int kFixed = kJoin + kWarps * kRows * 8 + kRows * 16 + 512;
+    static constexpr int kFixed = kJoin + kWarps * kRows * 8 + kRows * 20 + 512;
     static constexpr int kFit = (224 * 1024 / kMinB - 1024 - kFixed) / (kWarps * kStageBytes);
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr int kSmem = kFixed + kWarps * kStages * kStageBytes;
@@ -67,6 +75,10 @@ US_DEV uint32_t hsub2(uint32_t a, uint32_t b) {
 US_DEV uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b), *reinterpret_cast<__half2*>(&c));
     return *reinterpret_cast<const uint32_t*>(&r);
+}
+US_DEV float sum_half2(uint32_t a) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    return f.x + f.y;
 }
 US_DEV uint32_t pack_half2(float lo, float hi) {
     uint32_t r;
@@ -88,6 +100,18 @@ US_DEV void decode_i4(uint32_t x, uint32_t (&q)[4]) {
     q[1] = hfma2(us::lop3<us::kLopAndXor>(x, 0x00F000F0u, 0x64806480u), 0x2C002C00u, 0xD480D480u);   // x/16 - 72
     q[2] = hsub2(us::lop3<us::kLopAndXor>(y, 0x000F000Fu, 0x64086408u), 0x64086408u);
     q[3] = hfma2(us::lop3<us::kLopAndXor>(y, 0x00F000F0u, 0x64806480u), 0x2C002C00u, 0xD480D480u);
+}
+// The same without the subtraction: u 2^-24 (the odd nibbles 16 u 2^-24).
+US_DEV void offset_i4(uint32_t x, uint32_t (&q)[4]) {
+    const uint32_t y = x >> 8;
+    q[0] = us::lop3<us::kLopAndXor>(x, 0x000F000Fu, 0x00080008u);
+    q[1] = us::lop3<us::kLopAndXor>(x, 0x00F000F0u, 0x00800080u);
+    q[2] = us::lop3<us::kLopAndXor>(y, 0x000F000Fu, 0x00080008u);
+    q[3] = us::lop3<us::kLopAndXor>(y, 0x00F000F0u, 0x00800080u);
+}
+US_DEV void offset_i8(uint32_t x, uint32_t (&q)[2]) {
+    q[0] = us::lop3<us::kLopAndXor>(x, 0x00FF00FFu, 0x00800080u);
+    q[1] = us::lop3<us::kLopAndXor>(x >> 8, 0x00FF00FFu, 0x00800080u);
 }
 // int8: bytes (0, 2), (1, 3)
 US_DEV void decode_i8(uint32_t x, uint32_t (&q)[2]) {
@@ -116,7 +140,7 @@ US_DEV void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
 struct Request {
     int row0, n, ctx, tiles, nrb;
 };
-template <int ROWS>
+template <int ROWS, int TILE>
 US_DEV Request load_request(const UsAttnParams& p, int b, unsigned* status) {
     Request r = {0, 0, 0, 0, 0};
     UsKvCache c = p.c;
@@ -125,7 +149,7 @@ US_DEV Request load_request(const UsAttnParams& p, int b, unsigned* status) {
     if (r.n > 0) {
         r.ctx = us::kv_context(c, p.a, b, r.n);
         if (r.ctx >= 0) {
-            r.tiles = (r.ctx + r.n + kTile - 1) / kTile;
+            r.tiles = (r.ctx + r.n + TILE - 1) / TILE;
             r.nrb = (r.n * p.G + ROWS - 1) / ROWS;
         }
     }
@@ -133,7 +157,7 @@ US_DEV Request load_request(const UsAttnParams& p, int b, unsigned* status) {
 }
 
 // A place in the tile sequence: requests, key heads, row blocks, tiles.
-template <int ROWS>
+template <int ROWS, int TILE>
 struct Cursor {
     Request r;
     int b, h, rb, tile;
@@ -146,7 +170,7 @@ struct Cursor {
         h = 0;
         do {
             ++b;
-            if (b < p.c.B) r = load_request<ROWS>(p, b, nullptr);
+            if (b < p.c.B) r = load_request<ROWS, TILE>(p, b, nullptr);
         } while (b < p.c.B && r.tiles == 0);
     }
 };
@@ -165,73 +189,86 @@ struct Part {
     bool second;
 };
 
-// Joins the partial states of a shared segment: the rows' maxima, then per
-// batch of states their factors (in `buf`), then O^T, eight states' loads at a
-// time.
+// Joins the partial states of a shared segment: O^T of eight states at a time
+// is on its way while the rows' maxima and the states' factors (kBatch states in
+// `buf`) are found.
 template <int ELEM, int D, int NT>
-US_DEV void join_states(const UsAttnParams& p, float* buf, float* top, float* sums, const Part& a) {
+US_DEV void join_states(const UsAttnParams& p, float* buf, float* sums, const Part& a) {
     using Sh = Shape<ELEM, D, NT>;
-    constexpr int kRows = Sh::kRows, kPairs = D * kRows / 2, kMine = kPairs / kThreads, kBatch = 4 * kThreads / kRows;
+    constexpr int kRows = Sh::kRows, kMine = D * kRows / 4 / kThreads, kPar = kThreads / kRows, kBatch = 8 * kPar;
+    constexpr int kLoads = kMine == 4 ? 4 : 8;             // states in flight
     const int lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
     const int first = a.first, np = a.last - a.first + 1;
-    auto slot_of = [&](int c) {
-        return p.ws_slots + ((int64_t)2 * c + (c == first && a.second ? 1 : 0)) * Sh::kSlotFloats;
+    auto slot_of = [&](int j) {
+        return p.ws_slots + ((int64_t)2 * (first + j) + (j == 0 && a.second ? 1 : 0)) * Sh::kSlotFloats;
     };
+    auto row_of = [&](int k) {
+        const int x = threadIdx.x + k * kThreads;
+        return 8 * ((x >> 6) % NT) + 2 * c4 + ((x >> 5) & 1);
+    };
+    float4 v[kLoads][kMine];
+    auto load = [&](int j) {
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+            for (int k = 0; k < kMine; ++k)
+                v[u][k] = j + u < np && row_of(k) < a.rows
+                              ? __ldcg(reinterpret_cast<const float4*>(slot_of(j + u) + 2 * kRows) + threadIdx.x + k * kThreads)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);
     const int r = threadIdx.x % kRows, j0 = threadIdx.x / kRows;
     float t = -INFINITY;
 #pragma unroll 4
-    for (int j = j0; j < np; j += kThreads / kRows) t = fmaxf(t, __ldcg(slot_of(first + j) + r));
+    for (int j = j0; j < np; j += kPar) t = fmaxf(t, __ldcg(slot_of(j) + r));
     buf[threadIdx.x] = t;
     __syncthreads();
-    if (threadIdx.x < kRows) {
-        for (int j = 1; j < kThreads / kRows; ++j) t = fmaxf(t, buf[j * kRows + r]);
-        top[r] = t;
-        sums[r] = 0.f;
-    }
-    float2 y[kMine];
+    t = buf[r];
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) y[k] = make_float2(0.f, 0.f);
+    for (int j = 1; j < kPar; ++j) t = fmaxf(t, buf[j * kRows + r]);
+    __syncthreads();
+    float sum = 0.f;                                       // of the thread's states of row r
+    float4 y[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int base = 0; base < np; base += kBatch) {
         const int nb = min(kBatch, np - base);
-        __syncthreads();
-        for (int x = threadIdx.x; x < nb * kRows; x += kThreads) {
-            const float* sl = slot_of(first + base + x / kRows) + x % kRows;
-            const float mc = __ldcg(sl), lc = __ldcg(sl + kRows);
-            const float f = mc == -INFINITY ? 0.f : ex2(mc - top[x % kRows]);
-            buf[x] = f;
-            buf[kBatch * kRows + x] = lc * f;
+        if (base) __syncthreads();
+#pragma unroll 4
+        for (int j = j0; j < nb; j += kPar) {
+            const float* sl = slot_of(base + j);
+            const float mc = __ldcg(sl + r), f = mc == -INFINITY ? 0.f : ex2(mc - t);
+            sum += __ldcg(sl + kRows + r) * f;
+            buf[j * kRows + r] = f;
         }
         __syncthreads();
-        if (threadIdx.x < kRows) {
-            float sum = sums[r];
-            for (int j = 0; j < nb; ++j) sum += buf[kBatch * kRows + j * kRows + r];
-            sums[r] = sum;
-        }
-        for (int j = 0; j < nb; j += 8)
+        for (int j = 0; j < nb; j += kLoads) {
 #pragma unroll
-            for (int k = 0; k < kMine; ++k) {
-                const int x = threadIdx.x + k * kThreads, row = 8 * ((x >> 6) % NT) + 2 * c4 + ((x >> 5) & 1);
-                float2 v[8];
+            for (int u = 0; u < kLoads; ++u)
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    v[u] = j + u < nb ? __ldcg(reinterpret_cast<const float2*>(slot_of(first + base + j + u) + 2 * kRows) + x)
-                                      : make_float2(0.f, 0.f);
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const float f = j + u < nb ? buf[(j + u) * kRows + row] : 0.f;
-                    y[k].x += v[u].x * f;
-                    y[k].y += v[u].y * f;
+                for (int k = 0; k < kMine; ++k) {
+                    const float f = j + u < nb ? buf[(j + u) * kRows + row_of(k)] : 0.f;
+                    y[k].x += v[u][k].x * f, y[k].y += v[u][k].y * f;
+                    y[k].z += v[u][k].z * f, y[k].w += v[u][k].w * f;
                 }
-            }
+            load(base + j + kLoads);
+        }
+    }
+    __syncthreads();
+    buf[threadIdx.x] = sum;
+    __syncthreads();
+    if (threadIdx.x < kRows) {
+        for (int j = 1; j < kPar; ++j) sum += buf[j * kRows + r];
+        sums[r] = sum == 0.f ? 0.f : 1.f / sum;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
-        const int x = threadIdx.x + k * kThreads, row = 8 * ((x >> 6) % NT) + 2 * c4 + ((x >> 5) & 1);
-        const float sum = sums[row], inv = sum == 0.f ? 0.f : 1.f / sum;
-        if (row < a.rows)
-            *reinterpret_cast<uint32_t*>(out_row<kRows>(p, a.row0, a.h, a.rb, row, D) + g * (D / 8) + 2 * ((x >> 6) / NT)) =
-                pack_half2(y[k].x * inv, y[k].y * inv);
+        const int x = threadIdx.x + k * kThreads, row = row_of(k);
+        if (row >= a.rows) continue;
+        const float inv = sums[row];
+        uint16_t* out = out_row<kRows>(p, a.row0, a.h, a.rb, row, D) + g * (D / 8) + 4 * ((x >> 6) / NT);
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_half2(y[k].x * inv, y[k].y * inv), pack_half2(y[k].z * inv, y[k].w * inv));
     }
 }
 
@@ -240,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<ELEM, D, NT>::kMinB))
 attn_mma_kernel(const UsAttnParams p) {
     using Sh = Shape<ELEM, D, NT>;
     constexpr int kRows = Sh::kRows, kStages = Sh::kStages, kKW = Sh::kKW, kVW = Sh::kVW, kMT = Sh::kMT;
+    constexpr int kSub = Sh::kSub, kStep = Sh::kStep;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;
     float* join = reinterpret_cast<float*>(ring + kWarps * kStages * Sh::kStageBytes);
@@ -247,6 +285,7 @@ attn_mma_kernel(const UsAttnParams p) {
     float* sm_l = sm_m + kWarps * kRows;
     uint64_t* sm_mask = reinterpret_cast<uint64_t*>(sm_l + kWarps * kRows);     // [kRows]
     int* sm_tok = reinterpret_cast<int*>(sm_mask + kRows);                       // [kRows]
+    float* sm_inv = reinterpret_cast<float*>(sm_tok + kRows);                    // [kRows]
     __shared__ uint64_t full[kWarps][kStages];
     __shared__ Request sh_req;                             // the request t0 lies in, and t0's place in it
     __shared__ int64_t sh_start;
@@ -266,7 +305,7 @@ attn_mma_kernel(const UsAttnParams p) {
     int64_t mine = 0;
     Request r = {0, 0, 0, 0, 0};
     for (int b = b0; b < min(b0 + per, p.c.B); ++b) {
-        r = load_request<kRows>(p, b, blockIdx.x == 0 ? p.c.status : nullptr);
+        r = load_request<kRows, Sh::kTile>(p, b, blockIdx.x == 0 ? p.c.status : nullptr);
         mine += (int64_t)r.tiles * r.nrb * p.c.Hkv;
     }
     int64_t incl = mine;
@@ -288,7 +327,7 @@ attn_mma_kernel(const UsAttnParams p) {
     const int64_t t0 = (int64_t)blockIdx.x * total / ctas, t1 = ((int64_t)blockIdx.x + 1) * total / ctas;
     if (before <= t0 && t0 < before + mine) {
         for (int b = b0;; ++b) {
-            if (per > 1) r = load_request<kRows>(p, b, nullptr);
+            if (per > 1) r = load_request<kRows, Sh::kTile>(p, b, nullptr);
             const int64_t k = (int64_t)r.tiles * r.nrb * p.c.Hkv;
             if (t0 < before + k) {
                 sh_b = b;
@@ -300,7 +339,7 @@ attn_mma_kernel(const UsAttnParams p) {
         }
     }
     __syncthreads();
-    Cursor<kRows> cur;
+    Cursor<kRows, Sh::kTile> cur;
     cur.b = sh_b;
     cur.r = sh_req;
     {
@@ -312,33 +351,52 @@ attn_mma_kernel(const UsAttnParams p) {
     }
     const int count = (int)(t1 - t0);
 
-    // ---- producer: the warp's block of tile `pc` into stage s
-    Cursor<kRows> pc = cur;
+    // ---- producer: the warp's positions of tile `pc` into stage s.  Lanes 3 i
+    // to 3 i + 2 copy K, V and scales of 16-position block i; the page numbers
+    // are loaded one tile ahead.
+    Cursor<kRows, Sh::kTile> pc = cur;
     uint8_t* wring = ring + warp * kStages * Sh::kStageBytes;
-    uint32_t skip = 0;                                     // stages without a block
-    auto issue = [&](int s) {
-        const int pos = pc.tile * kTile + warp * kBlock;
-        int id = -1;
-        if (pos < pc.r.ctx + pc.r.n) id = us::kv_page(p.c, pc.b, pos);
-        skip = id < 0 ? skip | (1u << s) : skip & ~(1u << s);
-        if (id >= 0 && lane < 3) {
-            if (lane == 0) us::mbar_arrive_expect_tx(&full[warp][s], (uint32_t)Sh::kStageBytes);
-            const int64_t e = us::kv_entry(p.c, id, pc.h, pos);
-            const uint8_t* src = lane == 0 ? p.c.k + e * Sh::kRow
-                               : lane == 1 ? p.c.v + e * Sh::kRow
-                                           : reinterpret_cast<const uint8_t*>(p.c.scale) + e * 4;
-            us::bulk_g2s(wring + s * Sh::kStageBytes + lane * kBlock * Sh::kRow, src,
-                         lane == 2 ? (uint32_t)kBlock * 4u : (uint32_t)(kBlock * Sh::kRow), &full[warp][s]);
+    uint32_t have = 0;                                     // kSub bits a stage: which blocks it holds
+    const int my_sub = lane / 3, my_part = lane - 3 * my_sub;
+    constexpr int kNoPage = -0x7fffffff - 1;               // nothing to copy (any other bad number is recorded)
+    int page = kNoPage, page_pos = 0;
+    auto find_page = [&]() {
+        page_pos = pc.tile * Sh::kTile + warp * kStep + my_sub * kBlock;
+        page = my_sub < kSub && page_pos < pc.r.ctx + pc.r.n
+                   ? p.c.table[(int64_t)pc.b * p.c.max_pages + (page_pos >> p.c.page_shift)] : kNoPage;
+    };
+    auto issue = [&](int s, bool more) {
+        const bool ok = page >= 0 && page < p.c.num_pages;
+        if (!ok && page != kNoPage) us::set_status(p.c.status, US_ERR_CORRUPT);
+        const uint32_t votes = __ballot_sync(0xffffffffu, ok && my_part == 0);
+        uint32_t bits = votes & 1u;
+        if constexpr (kSub == 2) bits |= (votes >> 2) & 2u;
+        have = (have & ~(((1u << kSub) - 1u) << (s * kSub))) | (bits << (s * kSub));
+        if (ok) {
+            if (lane == (bits & 1u ? 0 : 3))
+                us::mbar_arrive_expect_tx(&full[warp][s], (uint32_t)(__popc(bits) * (2 * kBlock * Sh::kRow + kBlock * 4)));
+            const int64_t e = us::kv_entry(p.c, page, pc.h, page_pos);
+            const uint8_t* src = my_part == 0 ? p.c.k + e * Sh::kRow
+                               : my_part == 1 ? p.c.v + e * Sh::kRow
+                                              : reinterpret_cast<const uint8_t*>(p.c.scale) + e * 4;
+            const int off = my_part < 2 ? (my_part * kStep + my_sub * kBlock) * Sh::kRow
+                                        : 2 * kStep * Sh::kRow + my_sub * kBlock * 4;
+            us::bulk_g2s(wring + s * Sh::kStageBytes + off, src, my_part == 2 ? (uint32_t)kBlock * 4u : (uint32_t)(kBlock * Sh::kRow),
+                         &full[warp][s]);
         }
-        pc.next(p);
+        if (more) {
+            pc.next(p);
+            find_page();
+        }
     };
     const int ahead = count < kStages ? count : kStages;
-    for (int s = 0; s < ahead; ++s) issue(s);
+    find_page();
+    for (int s = 0; s < ahead; ++s) issue(s, s + 1 < count);
 
     // ---- consumer state: maxima, sums and O^T of the warp's positions
-    float m[NT][2], l[NT][2], o[kMT][NT][4], vref = 0.f, vmul = 0.f;
+    float m[NT][2], l[NT][2], qb[NT][2], o[kMT][NT][4], vref = 0.f, vmul = 0.f;
     uint32_t qf[Sh::kKS][NT][2];
-    const float sc = p.scale * 1.4426950408889634f;        // weights as powers of two
+    const float sc = p.scale * (1.4426950408889634f * 16777216.f);   // weights as powers of two; codes came as u 2^-24
     uint32_t phase = 0;
     bool failed = false;
     int parts = 0;
@@ -357,19 +415,27 @@ attn_mma_kernel(const UsAttnParams p) {
             const int r = cur.rb * kRows + 8 * nt + g;
             const int i = r / G;
             const uint16_t* q = p.Q + (int64_t)(cur.r.row0 + i) * p.ldq + (cur.h * G + r - i * G) * D;
+            float sum = 0.f;                               // of the lane's part of row g
 #pragma unroll
             for (int w = 0; w < kKW; ++w) {
                 if constexpr (ELEM == US_I4) {
                     uint4 u = make_uint4(0, 0, 0, 0);
                     if (r < rows) u = *reinterpret_cast<const uint4*>(q + c4 * (D / 4) + 8 * w);
-                    qf[2 * w][nt][0] = __byte_perm(u.x, u.z, 0x5410), qf[2 * w][nt][1] = __byte_perm(u.x, u.z, 0x7632);
-                    qf[2 * w + 1][nt][0] = __byte_perm(u.y, u.w, 0x5410), qf[2 * w + 1][nt][1] = __byte_perm(u.y, u.w, 0x7632);
+                    qf[2 * w][nt][0] = __byte_perm(u.x, u.z, 0x5410), qf[2 * w][nt][1] = __byte_perm(u.y, u.w, 0x5410);
+                    qf[2 * w + 1][nt][0] = __byte_perm(u.x, u.z, 0x7632), qf[2 * w + 1][nt][1] = __byte_perm(u.y, u.w, 0x7632);
+                    sum += (sum_half2(u.x) + sum_half2(u.y)) + (sum_half2(u.z) + sum_half2(u.w));
                 } else {
                     uint2 u = make_uint2(0, 0);
                     if (r < rows) u = *reinterpret_cast<const uint2*>(q + (w >> 2) * 64 + c4 * 16 + 4 * (w & 3));
                     qf[w][nt][0] = __byte_perm(u.x, u.y, 0x5410), qf[w][nt][1] = __byte_perm(u.x, u.y, 0x7632);
+                    sum += sum_half2(u.x) + sum_half2(u.y);
                 }
             }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)                    // the offset's share of column 2 c + e
+                qb[nt][e] = __shfl_sync(0xffffffffu, sum, (2 * c4 + e) * 4) * ((ELEM == US_I4 ? -8.f : -128.f) / 16777216.f);
         }
         vref = vmul = 0.f;
         if (threadIdx.x < kRows) {
@@ -383,79 +449,98 @@ attn_mma_kernel(const UsAttnParams p) {
     begin_segment();
     int s = 0;
     for (int it = 0; it < count; ++it) {
-        if (!((skip >> s) & 1u)) {
+        const uint32_t blocks = (have >> (s * kSub)) & ((1u << kSub) - 1u);
+        if (blocks) {
             if (!failed && !us::mbar_wait(&full[warp][s], (phase >> s) & 1u, p.c.status)) failed = true;
             phase ^= 1u << s;
             const uint8_t* st = wring + s * Sh::kStageBytes;
-            const int pos = cur.tile * kTile + warp * kBlock;
-            // ---- S^T = Ck Q^T
-            float sacc[NT][4];
+            const int pos = cur.tile * Sh::kTile + warp * kStep;
+            float sx[kSub][NT][4], vs[kSub][2];
+            const bool edge = pos + kStep > cur.r.ctx || blocks != (1u << kSub) - 1u;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int sb = 0; sb < kSub; ++sb) {
+                // ---- S^T = Ck Q^T
+                float (&sa)[NT][4] = sx[sb];
+                float so[NT][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sacc[nt][e] = 0.f;
-            uint32_t k0[kKW], k1[kKW];
-            lds_words(st + rt * Sh::kRow + c4 * (kKW >= 4 ? 16 : 4 * kKW), k0);
-            lds_words(st + (rt + 8) * Sh::kRow + c4 * (kKW >= 4 ? 16 : 4 * kKW), k1);
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int w = 0; w < kKW; ++w) {
-                if constexpr (ELEM == US_I4) {
-                    uint32_t x[4], y[4];
-                    decode_i4(k0[w], x);
-                    decode_i4(k1[w], y);
+                    for (int e = 0; e < 4; ++e) sa[nt][e] = qb[nt][e & 1], so[nt][e] = 0.f;
+                uint32_t k0[kKW], k1[kKW];
+                const uint8_t* kr = st + (sb * kBlock + rt) * Sh::kRow + c4 * (kKW >= 4 ? 16 : 4 * kKW);
+                lds_words(kr, k0);
+                lds_words(kr + 8 * Sh::kRow, k1);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        us::mma_m16n8k16_f16(sacc[nt], x[0], y[0], x[1], y[1], qf[2 * w][nt][0], qf[2 * w][nt][1]);
-                        us::mma_m16n8k16_f16(sacc[nt], x[2], y[2], x[3], y[3], qf[2 * w + 1][nt][0], qf[2 * w + 1][nt][1]);
-                    }
-                } else {
-                    uint32_t x[2], y[2];
-                    decode_i8(k0[w], x);
-                    decode_i8(k1[w], y);
+                for (int w = 0; w < kKW; ++w) {
+                    if constexpr (ELEM == US_I4) {
+                        uint32_t x[4], y[4];
+                        offset_i4(k0[w], x);
+                        offset_i4(k1[w], y);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        us::mma_m16n8k16_f16(sacc[nt], x[0], y[0], x[1], y[1], qf[w][nt][0], qf[w][nt][1]);
-                }
-            }
-            // ---- scores (row 0: token rt, row 1: token rt + 8), masks
-            const uint32_t* ss = reinterpret_cast<const uint32_t*>(st + 2 * kBlock * Sh::kRow);
-            const uint32_t s0 = ss[rt], s1 = ss[rt + 8];
-            const float ks[2] = {us::half_bits_to_float((uint16_t)s0) * sc, us::half_bits_to_float((uint16_t)s1) * sc};
-            const float vs[2] = {us::half_bits_to_float((uint16_t)(s0 >> 16)), us::half_bits_to_float((uint16_t)(s1 >> 16))};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sacc[nt][e] *= ks[e >> 1];
-            const bool edge = pos + kBlock > cur.r.ctx;
-            if (edge) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int j = pos + rt + 8 * u - cur.r.ctx;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int r = 8 * nt + 2 * c4 + e;
-                            const bool seen = j < 0 || (j < cur.r.n && (p.mask ? (sm_mask[r] >> (j & 63)) & 1 : j <= sm_tok[r]));
-                            if (!seen) sacc[nt][2 * u + e] = -INFINITY;
+                        for (int nt = 0; nt < NT; ++nt) {
+                            us::mma_m16n8k16_f16(sa[nt], x[0], y[0], x[2], y[2], qf[2 * w][nt][0], qf[2 * w][nt][1]);
+                            us::mma_m16n8k16_f16(so[nt], x[1], y[1], x[3], y[3], qf[2 * w + 1][nt][0], qf[2 * w + 1][nt][1]);
                         }
+                    } else {
+                        uint32_t x[2], y[2];
+                        offset_i8(k0[w], x);
+                        offset_i8(k1[w], y);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            us::mma_m16n8k16_f16(w & 1 ? so[nt] : sa[nt], x[0], y[0], x[1], y[1], qf[w][nt][0], qf[w][nt][1]);
+                    }
+                }
+                // ---- scores (elements 0, 1: token rt; 2, 3: token rt + 8), masks
+                const uint32_t* ss = reinterpret_cast<const uint32_t*>(st + 2 * kStep * Sh::kRow) + sb * kBlock;
+                const uint32_t s0 = ss[rt], s1 = ss[rt + 8];
+                const float ks[2] = {us::half_bits_to_float((uint16_t)s0) * sc, us::half_bits_to_float((uint16_t)s1) * sc};
+                vs[sb][0] = us::half_bits_to_float((uint16_t)(s0 >> 16));
+                vs[sb][1] = us::half_bits_to_float((uint16_t)(s1 >> 16));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sa[nt][e] = (ELEM == US_I4 ? fmaf(so[nt][e], 0.0625f, sa[nt][e]) : sa[nt][e] + so[nt][e]) * ks[e >> 1];
+                if (edge) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int j = ((blocks >> sb) & 1u) ? pos + sb * kBlock + rt + 8 * u - cur.r.ctx : cur.r.n;
+                        if (j >= cur.r.n) vs[sb][u] = 0.f;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int r = 8 * nt + 2 * c4 + e;
+                                const bool seen = j < 0 || (j < cur.r.n && (p.mask ? (sm_mask[r] >> (j & 63)) & 1 : j <= sm_tok[r]));
+                                if (!seen) sa[nt][2 * u + e] = -INFINITY;
+                            }
+                    }
                 }
             }
             // ---- running maxima, rescaled only where one has grown by 2^4
-            // (unseen entries may hold any scale: only finite ones count)
-            const float va = fmaxf(fabsf(vs[0]) < INFINITY ? fabsf(vs[0]) : 0.f, fabsf(vs[1]) < INFINITY ? fabsf(vs[1]) : 0.f);
-            bool grow = va >= vref;
+            // (entries that no row sees may hold any scale: only finite ones count)
+            float va = 0.f;
+            bool grow = false;
+#pragma unroll
+            for (int sb = 0; sb < kSub; ++sb)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) va = fmaxf(va, fabsf(vs[sb][u]) < INFINITY ? fabsf(vs[sb][u]) : 0.f);
+            grow = va >= vref;
+            float mx[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) grow |= fmaxf(sacc[nt][e], sacc[nt][e + 2]) > m[nt][e] + kMaxLag;
+                for (int e = 0; e < 2; ++e) {
+                    mx[nt][e] = fmaxf(sx[0][nt][e], sx[0][nt][e + 2]);
+                    if constexpr (kSub == 2) mx[nt][e] = fmaxf(mx[nt][e], fmaxf(sx[1][nt][e], sx[1][nt][e + 2]));
+                    grow |= mx[nt][e] > m[nt][e] + kMaxLag;
+                }
             if (__any_sync(0xffffffffu, grow)) {
-                float vm = va;
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
+                for (int d = 4; d < 32; d <<= 1) va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, d));
                 float fv = 1.f;
-                if (vm >= vref) {                              // the power of two above it
-                    const float nv = __uint_as_float((__float_as_uint(fmaxf(vm, 1e-30f)) & 0x7F800000u) + 0x00800000u);
+                if (va >= vref) {                              // the power of two above it
+                    const float nv = __uint_as_float((__float_as_uint(fmaxf(va, 1e-30f)) & 0x7F800000u) + 0x00800000u);
                     fv = vref / nv;
                     vref = nv;
                     vmul = kVHead / nv;
@@ -464,12 +549,12 @@ attn_mma_kernel(const UsAttnParams p) {
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(sacc[nt][e], sacc[nt][e + 2]);
+                        float x = mx[nt][e];
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                        mx = fmaxf(mx, m[nt][e]);
-                        const float f = mx == -INFINITY ? 1.f : ex2(m[nt][e] - mx);
-                        m[nt][e] = mx;
+                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        x = fmaxf(x, m[nt][e]);
+                        const float f = x == -INFINITY ? 1.f : ex2(m[nt][e] - x);
+                        m[nt][e] = x;
                         l[nt][e] *= f;
 #pragma unroll
                         for (int t = 0; t < kMT; ++t) {
@@ -478,56 +563,57 @@ attn_mma_kernel(const UsAttnParams p) {
                         }
                     }
             }
-            // ---- weights; with V's scale, as fp16, they are the B operand of O^T
-            uint32_t pf[NT][2];
-            const float wv[2] = {vs[0] * vmul, vs[1] * vmul};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float w[4];
+            for (int sb = 0; sb < kSub; ++sb) {
+                // ---- weights; with V's scale, as fp16, they are the B operand of O^T
+                uint32_t pf[NT][2];
+                const float wv[2] = {vs[sb][0] * vmul, vs[sb][1] * vmul};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float mm = m[nt][e & 1];
-                    w[e] = ex2(sacc[nt][e] - (mm == -INFINITY ? 0.f : mm));
-                    l[nt][e & 1] += w[e];
-                }
-                float x[4];
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4], x[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = edge && w[e] == 0.f ? 0.f : w[e] * wv[e >> 1];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) pf[nt][u] = transpose8x8(pack_half2(x[2 * u], x[2 * u + 1]));
-            }
-            // ---- O^T += Cv^T P^T
-            uint32_t v[4][kVW];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                lds_words(st + kBlock * Sh::kRow + (c4 + 4 * i) * Sh::kRow + g * (4 * kVW), v[i]);
-#pragma unroll
-            for (int w = 0; w < kVW; ++w)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const uint32_t x01 = __byte_perm(v[0][w], v[1][w], hh ? 0x7632 : 0x5410);
-                    const uint32_t x23 = __byte_perm(v[2][w], v[3][w], hh ? 0x7632 : 0x5410);
-                    if constexpr (ELEM == US_I4) {
-                        uint32_t a[4], b[4];
-                        decode_i4(x01, a);
-                        decode_i4(x23, b);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            us::mma_m16n8k16_f16(o[4 * w + 2 * hh][nt], a[0], a[1], b[0], b[1], pf[nt][0], pf[nt][1]);
-                            us::mma_m16n8k16_f16(o[4 * w + 2 * hh + 1][nt], a[2], a[3], b[2], b[3], pf[nt][0], pf[nt][1]);
-                        }
-                    } else {
-                        uint32_t a[2], b[2];
-                        decode_i8(x01, a);
-                        decode_i8(x23, b);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            us::mma_m16n8k16_f16(o[2 * w + hh][nt], a[0], a[1], b[0], b[1], pf[nt][0], pf[nt][1]);
+                    for (int e = 0; e < 4; ++e) {
+                        const float mm = m[nt][e & 1];
+                        w[e] = ex2(sx[sb][nt][e] - (edge && mm == -INFINITY ? 0.f : mm));
+                        l[nt][e & 1] += w[e];
+                        x[e] = edge && w[e] == 0.f ? 0.f : w[e] * wv[e >> 1];
                     }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) pf[nt][u] = transpose8x8(pack_half2(x[2 * u], x[2 * u + 1]));
                 }
+                // ---- O^T += Cv^T P^T
+                uint32_t v[4][kVW];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    lds_words(st + (kStep + sb * kBlock + c4 + 4 * i) * Sh::kRow + g * (4 * kVW), v[i]);
+#pragma unroll
+                for (int w = 0; w < kVW; ++w)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const uint32_t x01 = __byte_perm(v[0][w], v[1][w], hh ? 0x7632 : 0x5410);
+                        const uint32_t x23 = __byte_perm(v[2][w], v[3][w], hh ? 0x7632 : 0x5410);
+                        if constexpr (ELEM == US_I4) {
+                            uint32_t a[4], b[4];
+                            decode_i4(x01, a);
+                            decode_i4(x23, b);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                us::mma_m16n8k16_f16(o[4 * w + 2 * hh][nt], a[0], a[1], b[0], b[1], pf[nt][0], pf[nt][1]);
+                                us::mma_m16n8k16_f16(o[4 * w + 2 * hh + 1][nt], a[2], a[3], b[2], b[3], pf[nt][0], pf[nt][1]);
+                            }
+                        } else {
+                            uint32_t a[2], b[2];
+                            decode_i8(x01, a);
+                            decode_i8(x23, b);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                us::mma_m16n8k16_f16(o[2 * w + hh][nt], a[0], a[1], b[0], b[1], pf[nt][0], pf[nt][1]);
+                        }
+                    }
+            }
         }
         __syncwarp();                                      // every lane has read the stage
-        if (it + kStages < count) issue(s);
+        if (it + kStages < count) issue(s, it + kStages + 1 < count);
         s = s + 1 == kStages ? 0 : s + 1;
 
         // ---- the end of the segment, or of this CTA's part of it
@@ -568,23 +654,21 @@ attn_mma_kernel(const UsAttnParams p) {
 #pragma unroll
                     for (int q = 0; q < kMT; ++q) o[q][nt][e] *= f, o[q][nt][e + 2] *= f;
                 }
-            // row sums over the warps
-            auto row_state = [&](int r, float& t, float& sum) {
-                t = sm_m[r];
+            if (threadIdx.x < kRows) {                      // row maxima and sums over the warps
+                const int r = threadIdx.x;
+                float t = sm_m[r], sum = 0.f;
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) t = fmaxf(t, sm_m[w * kRows + r]);
-                sum = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float mw = sm_m[w * kRows + r];
                     sum += sm_l[w * kRows + r] * (mw == -INFINITY ? 0.f : ex2(mw - t));
                 }
-            };
-            if (!whole && threadIdx.x < kRows) {
-                float t, sum;
-                row_state(threadIdx.x, t, sum);
-                __stcg(slot + threadIdx.x, t);
-                __stcg(slot + kRows + threadIdx.x, sum);
+                sm_inv[r] = sum == 0.f ? 0.f : 1.f / sum;
+                if (!whole) {
+                    __stcg(slot + r, t);
+                    __stcg(slot + kRows + r, sum);
+                }
             }
             constexpr int kPer = 8 / NT;                    // 16-dimension blocks joined at a time
 #pragma unroll
@@ -599,26 +683,27 @@ attn_mma_kernel(const UsAttnParams p) {
                         for (int e = 0; e < 4; ++e)
                             join[((warp * kBlocks + q) * NT + nt) * 128 + e * 32 + lane] = o[ch * kBlocks + q][nt][e];
                 __syncthreads();
+                // four neighbouring dimensions of a row at a time
 #pragma unroll
-                for (int x = threadIdx.x; x < kBlocks * NT * 64; x += kThreads) {
-                    const int e = (x >> 5) & 1, nt = (x >> 6) % NT, q = (x >> 6) / NT;
-                    float y0 = 0.f, y1 = 0.f;
+                for (int x = threadIdx.x; x < kBlocks * NT * 32; x += kThreads) {
+                    const int e = (x >> 5) & 1, nt = (x >> 6) % NT, q = 2 * ((x >> 6) / NT);
+                    float y[4] = {};
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
                         const float* jw = join + ((w * kBlocks + q) * NT + nt) * 128 + e * 32 + lane;
-                        y0 += jw[0];
-                        y1 += jw[64];
+                        y[0] += jw[0], y[1] += jw[64], y[2] += jw[128 * NT], y[3] += jw[128 * NT + 64];
                     }
+                    const int r = 8 * nt + 2 * c4 + e;
                     if (whole) {
-                        const int r = 8 * nt + 2 * c4 + e;
-                        float t, sum;
-                        row_state(r, t, sum);
-                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                        if (r < rows)
-                            *reinterpret_cast<uint32_t*>(out_row<kRows>(p, cur.r.row0, cur.h, cur.rb, r, D) + g * (D / 8) +
-                                                         2 * (ch * kBlocks + q)) = pack_half2(y0 * inv, y1 * inv);
+                        if (r < rows) {
+                            const float inv = sm_inv[r];
+                            uint16_t* out = out_row<kRows>(p, cur.r.row0, cur.h, cur.rb, r, D) + g * (D / 8) + 2 * (ch * kBlocks + q);
+                            *reinterpret_cast<uint2*>(out) =
+                                make_uint2(pack_half2(y[0] * inv, y[1] * inv), pack_half2(y[2] * inv, y[3] * inv));
+                        }
                     } else {
-                        __stcg(reinterpret_cast<float2*>(slot + 2 * kRows) + ch * kBlocks * NT * 64 + x, make_float2(y0, y1));
+                        __stcg(reinterpret_cast<float4*>(slot + 2 * kRows) + ch * kBlocks * NT * 32 + x,
+                               make_float4(y[0], y[1], y[2], y[3]));
                     }
                 }
             }
@@ -644,7 +729,7 @@ attn_mma_kernel(const UsAttnParams p) {
         if (!sh_last) continue;
         __threadfence();
         if (threadIdx.x == 0) p.ws_count[a.first] = 0;
-        join_states<ELEM, D, NT>(p, join, sm_m, sm_l, a);
+        join_states<ELEM, D, NT>(p, join, sm_inv, a);
     }
     us::pdl_launch_dependents();
 }
