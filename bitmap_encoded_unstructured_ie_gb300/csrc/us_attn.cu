@@ -20,9 +20,9 @@
 //
 // Codes of K need no conversion beyond a mask: with the sign bit flipped, a code
 // is u = code + 8 (or + 128) >= 0, and the fp16 number with the bits of u is
-// u 2^-24 exactly.  The product starts from -8 (-128) 2^-24 sum(q), and the odd
-// nibbles, read in place as 16 u, have their own accumulator.  V's codes are made
-// signed first: a sum over many positions would drift by the offset's rounding.
+// u 2^-24 exactly.  S^T starts from -8 (-128) 2^-24 sum(q), and the odd nibbles,
+// read in place as 16 u, have their own accumulator.  V's codes are made signed
+// first: an output may be far smaller than the offset's rounding in its sum.
 //
 // Work: the (request, key head, row block) segments are cut into tiles of 64 or
 // 128 positions, and the tile sequence is spread evenly over the CTAs, whatever
@@ -31,59 +31,41 @@
 // of one head are contiguous) into the warp's own ring, several tiles ahead and
 // across segments.  A segment shared by several CTAs leaves partial states in the
 // workspace; the CTA that arrives last joins them in the order of the tiles.
+#include "us_attn.cuh"
 #include "us_internal.h"
-#include "us_kv.cuh"
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kBlock = 16;                        // positions of one MMA's rows: they lie in one page
-constexpr float kMaxLag = 4.f;                    // a row's maximum may lag by 2^4 before the state is rescaled
-constexpr float kVHead = 2048.f;                  // weights reach 2^4 2^11 < 65504 as fp16: small ones keep their bits
+using namespace us::attn;
 
-template <int ELEM, int D, int NT>
+constexpr int kBlock = 16;                        // positions of one MMA's rows: they lie in one page
+
+template <int ELEM, int D, int NT, int W>
 struct Shape {
+    static constexpr int kWarps = W, kThreads = 32 * W;
     static constexpr int kRows = 8 * NT;
     static constexpr int kRow = D * (ELEM == US_I8 ? 8 : 4) / 8;    // bytes of a row of codes
     static constexpr int kKW = kRow / 16;                           // words a lane holds of a K row
     static constexpr int kVW = kRow / 32;                           // ... of a V row (its D/8 dimensions)
     static constexpr int kKS = D / 16;                              // MMA steps over the dimensions
     static constexpr int kMT = D / 16;                              // 16-dimension blocks of O^T
-    static constexpr int kMinB = NT == 1 ? 4 : NT == 2 ? 3 : 2;     // CTAs an SM
+    static constexpr int kMinB = W == 8 ? 2 : 3;                  // CTAs an SM
     static constexpr int kSub = kRow == 128 ? 1 : 2;                // 16-position blocks of a warp's step
     static constexpr int kStep = kSub * kBlock;
     static constexpr int kTile = kWarps * kStep;                    // positions of a CTA's step
     static constexpr int kStageBytes = 2 * kStep * kRow + kStep * 4;
     static constexpr int kJoin = kWarps * 32 * 32 * 4;              // O^T of four warps, 32 values a lane at a time
     static constexpr int kFixed = kJoin + kWarps * kRows * 8 + kRows * 20 + 512;
-    static constexpr int kFit = (224 * 1024 / kMinB - 1024 - kFixed) / (kWarps * kStageBytes);
-    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kFit = (224 * 1024 / kMinB - 2048 - kFixed) / (kWarps * kStageBytes);
+    static constexpr int kStages = kFit > 5 ? 5 : kFit;
     static constexpr int kSmem = kFixed + kWarps * kStages * kStageBytes;
     static_assert(kStages >= 2, "ring");
     static constexpr int kSlotFloats = 2 * kRows + kRows * D;       // m, l, O^T of one partial state
 };
 
-US_DEV float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-US_DEV uint32_t hsub2(uint32_t a, uint32_t b) {
-    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+US_DEV uint32_t hmax2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
-}
-US_DEV uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-    const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b), *reinterpret_cast<__half2*>(&c));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-US_DEV float sum_half2(uint32_t a) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    return f.x + f.y;
-}
-US_DEV uint32_t pack_half2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 US_DEV uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
@@ -91,17 +73,8 @@ US_DEV uint32_t transpose8x8(uint32_t x) {
     return r;
 }
 
-// Codes of both halves of a word as exact fp16 pairs: 0x6400 | u is 1024 + u,
-// and flipping a code's sign bit makes it u = code + 8 (or + 128).
-// int4: nibbles (0, 4), (1, 5), (2, 6), (3, 7); the odd ones read as 16 u.
-US_DEV void decode_i4(uint32_t x, uint32_t (&q)[4]) {
-    const uint32_t y = x >> 8;
-    q[0] = hsub2(us::lop3<us::kLopAndXor>(x, 0x000F000Fu, 0x64086408u), 0x64086408u);
-    q[1] = hfma2(us::lop3<us::kLopAndXor>(x, 0x00F000F0u, 0x64806480u), 0x2C002C00u, 0xD480D480u);   // x/16 - 72
-    q[2] = hsub2(us::lop3<us::kLopAndXor>(y, 0x000F000Fu, 0x64086408u), 0x64086408u);
-    q[3] = hfma2(us::lop3<us::kLopAndXor>(y, 0x00F000F0u, 0x64806480u), 0x2C002C00u, 0xD480D480u);
-}
-// The same without the subtraction: u 2^-24 (the odd nibbles 16 u 2^-24).
+// Codes of both halves of a word as fp16 pairs u 2^-24, u = code + 8 (+ 128).
+// int4: nibbles (0, 4), (1, 5), (2, 6), (3, 7); the odd ones as 16 u 2^-24.
 US_DEV void offset_i4(uint32_t x, uint32_t (&q)[4]) {
     const uint32_t y = x >> 8;
     q[0] = us::lop3<us::kLopAndXor>(x, 0x000F000Fu, 0x00080008u);
@@ -109,16 +82,11 @@ US_DEV void offset_i4(uint32_t x, uint32_t (&q)[4]) {
     q[2] = us::lop3<us::kLopAndXor>(y, 0x000F000Fu, 0x00080008u);
     q[3] = us::lop3<us::kLopAndXor>(y, 0x00F000F0u, 0x00800080u);
 }
+// int8: bytes (0, 2), (1, 3).
 US_DEV void offset_i8(uint32_t x, uint32_t (&q)[2]) {
     q[0] = us::lop3<us::kLopAndXor>(x, 0x00FF00FFu, 0x00800080u);
     q[1] = us::lop3<us::kLopAndXor>(x >> 8, 0x00FF00FFu, 0x00800080u);
 }
-// int8: bytes (0, 2), (1, 3)
-US_DEV void decode_i8(uint32_t x, uint32_t (&q)[2]) {
-    q[0] = hsub2(us::lop3<us::kLopAndXor>(x, 0x00FF00FFu, 0x64806480u), 0x64806480u);
-    q[1] = hsub2(us::lop3<us::kLopAndXor>(x >> 8, 0x00FF00FFu, 0x64806480u), 0x64806480u);
-}
-
 template <int N>
 US_DEV void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
     if constexpr (N >= 4) {
@@ -136,72 +104,19 @@ US_DEV void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
     }
 }
 
-// Tiles and row blocks of a request; none where its arguments are not usable.
-struct Request {
-    int row0, n, ctx, tiles, nrb;
-};
-template <int ROWS, int TILE>
-US_DEV Request load_request(const UsAttnParams& p, int b, unsigned* status) {
-    Request r = {0, 0, 0, 0, 0};
-    UsKvCache c = p.c;
-    c.status = status;
-    r.n = us::kv_rows(c, p.a, b, r.row0);
-    if (r.n > 0) {
-        r.ctx = us::kv_context(c, p.a, b, r.n);
-        if (r.ctx >= 0) {
-            r.tiles = (r.ctx + r.n + TILE - 1) / TILE;
-            r.nrb = (r.n * p.G + ROWS - 1) / ROWS;
-        }
-    }
-    return r;
-}
-
-// A place in the tile sequence: requests, key heads, row blocks, tiles.
-template <int ROWS, int TILE>
-struct Cursor {
-    Request r;
-    int b, h, rb, tile;
-    US_DEV void next(const UsAttnParams& p) {
-        if (++tile < r.tiles) return;
-        tile = 0;
-        if (++rb < r.nrb) return;
-        rb = 0;
-        if (++h < p.c.Hkv) return;
-        h = 0;
-        do {
-            ++b;
-            if (b < p.c.B) r = load_request<ROWS, TILE>(p, b, nullptr);
-        } while (b < p.c.B && r.tiles == 0);
-    }
-};
-
-// Where a row's fp16 outputs go: D values at row r of row block rb, head h.
-template <int ROWS>
-US_DEV uint16_t* out_row(const UsAttnParams& p, int row0, int h, int rb, int r, int D) {
-    const int rr = rb * ROWS + r, i = rr / p.G;
-    return p.O + (int64_t)(row0 + i) * p.ldo + (int64_t)(h * p.G + rr - i * p.G) * D;
-}
-
-// A segment shared by CTAs first .. last (second: the first of them left its
-// state in its second slot).
-struct Part {
-    int first, last, row0, h, rb, rows;
-    bool second;
-};
-
 // Joins the partial states of a shared segment: O^T of eight states at a time
 // is on its way while the rows' maxima and the states' factors (kBatch states in
 // `buf`) are found.
-template <int ELEM, int D, int NT>
+template <int ELEM, int D, int NT, int W>
 US_DEV void join_states(const UsAttnParams& p, float* buf, float* sums, const Part& a) {
-    using Sh = Shape<ELEM, D, NT>;
-    constexpr int kRows = Sh::kRows, kMine = D * kRows / 4 / kThreads, kPar = kThreads / kRows, kBatch = 8 * kPar;
-    constexpr int kLoads = kMine == 4 ? 4 : 8;             // states in flight
+    using Sh = Shape<ELEM, D, NT, W>;
+    constexpr int kThreads = Sh::kThreads, kRows = Sh::kRows, kQuads = D * kRows / 4;
+    constexpr int kMine = (kQuads + kThreads - 1) / kThreads, kPar = kThreads / kRows, kBatch = 8 * kPar;
+    constexpr int kLoads = kMine > 2 ? 4 : 8;              // states in flight
+    static_assert(kBatch * kRows * 4 <= Sh::kJoin, "factors");
     const int lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
     const int first = a.first, np = a.last - a.first + 1;
-    auto slot_of = [&](int j) {
-        return p.ws_slots + ((int64_t)2 * (first + j) + (j == 0 && a.second ? 1 : 0)) * Sh::kSlotFloats;
-    };
+    auto slot_of = [&](int j) { return p.ws_slots + a.slot(first + j) * Sh::kSlotFloats; };
     auto row_of = [&](int k) {
         const int x = threadIdx.x + k * kThreads;
         return 8 * ((x >> 6) % NT) + 2 * c4 + ((x >> 5) & 1);
@@ -212,15 +127,17 @@ US_DEV void join_states(const UsAttnParams& p, float* buf, float* sums, const Pa
         for (int u = 0; u < kLoads; ++u)
 #pragma unroll
             for (int k = 0; k < kMine; ++k)
-                v[u][k] = j + u < np && row_of(k) < a.rows
+                v[u][k] = j + u < np && row_of(k) < a.rows && threadIdx.x + k * kThreads < kQuads
                               ? __ldcg(reinterpret_cast<const float4*>(slot_of(j + u) + 2 * kRows) + threadIdx.x + k * kThreads)
                               : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     load(0);
     const int r = threadIdx.x % kRows, j0 = threadIdx.x / kRows;
-    float t = -INFINITY;
+    float m0 = -INFINITY, l0 = 0.f;                        // of the thread's first state
+    if (j0 < np) m0 = __ldcg(slot_of(j0) + r), l0 = __ldcg(slot_of(j0) + kRows + r);
+    float t = m0;
 #pragma unroll 4
-    for (int j = j0; j < np; j += kPar) t = fmaxf(t, __ldcg(slot_of(j) + r));
+    for (int j = j0 + kPar; j < np; j += kPar) t = fmaxf(t, __ldcg(slot_of(j) + r));
     buf[threadIdx.x] = t;
     __syncthreads();
     t = buf[r];
@@ -234,11 +151,12 @@ US_DEV void join_states(const UsAttnParams& p, float* buf, float* sums, const Pa
     for (int base = 0; base < np; base += kBatch) {
         const int nb = min(kBatch, np - base);
         if (base) __syncthreads();
-#pragma unroll 4
         for (int j = j0; j < nb; j += kPar) {
             const float* sl = slot_of(base + j);
-            const float mc = __ldcg(sl + r), f = mc == -INFINITY ? 0.f : ex2(mc - t);
-            sum += __ldcg(sl + kRows + r) * f;
+            const bool kept = base + j == j0;
+            const float mc = kept ? m0 : __ldcg(sl + r), lc = kept ? l0 : __ldcg(sl + kRows + r);
+            const float f = mc == -INFINITY ? 0.f : ex2(mc - t);
+            sum += lc * f;
             buf[j * kRows + r] = f;
         }
         __syncthreads();
@@ -265,19 +183,19 @@ US_DEV void join_states(const UsAttnParams& p, float* buf, float* sums, const Pa
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
         const int x = threadIdx.x + k * kThreads, row = row_of(k);
-        if (row >= a.rows) continue;
+        if (row >= a.rows || x >= kQuads) continue;
         const float inv = sums[row];
         uint16_t* out = out_row<kRows>(p, a.row0, a.h, a.rb, row, D) + g * (D / 8) + 4 * ((x >> 6) / NT);
         *reinterpret_cast<uint2*>(out) = make_uint2(pack_half2(y[k].x * inv, y[k].y * inv), pack_half2(y[k].z * inv, y[k].w * inv));
     }
 }
 
-template <int ELEM, int D, int NT>
-__global__ void __launch_bounds__(kThreads, (Shape<ELEM, D, NT>::kMinB))
+template <int ELEM, int D, int NT, int W>
+__global__ void __launch_bounds__(32 * W, (Shape<ELEM, D, NT, W>::kMinB))
 attn_mma_kernel(const UsAttnParams p) {
-    using Sh = Shape<ELEM, D, NT>;
+    using Sh = Shape<ELEM, D, NT, W>;
     constexpr int kRows = Sh::kRows, kStages = Sh::kStages, kKW = Sh::kKW, kVW = Sh::kVW, kMT = Sh::kMT;
-    constexpr int kSub = Sh::kSub, kStep = Sh::kStep;
+    constexpr int kSub = Sh::kSub, kStep = Sh::kStep, kWarps = Sh::kWarps, kThreads = Sh::kThreads;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;
     float* join = reinterpret_cast<float*>(ring + kWarps * kStages * Sh::kStageBytes);
@@ -287,10 +205,6 @@ attn_mma_kernel(const UsAttnParams p) {
     int* sm_tok = reinterpret_cast<int*>(sm_mask + kRows);                       // [kRows]
     float* sm_inv = reinterpret_cast<float*>(sm_tok + kRows);                    // [kRows]
     __shared__ uint64_t full[kWarps][kStages];
-    __shared__ Request sh_req;                             // the request t0 lies in, and t0's place in it
-    __shared__ int64_t sh_start;
-    __shared__ int sh_b;
-    __shared__ int64_t sh_warp[kWarps];
     __shared__ unsigned sh_last;
     __shared__ Part sh_part[2];
 
@@ -300,55 +214,11 @@ attn_mma_kernel(const UsAttnParams p) {
     us::fence_mbar_init();
     us::pdl_wait();
 
-    // ---- this CTA's tiles [t0, t1): a block-wide scan of the requests' tiles
-    const int per = (p.c.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
-    int64_t mine = 0;
-    Request r = {0, 0, 0, 0, 0};
-    for (int b = b0; b < min(b0 + per, p.c.B); ++b) {
-        r = load_request<kRows, Sh::kTile>(p, b, blockIdx.x == 0 ? p.c.status : nullptr);
-        mine += (int64_t)r.tiles * r.nrb * p.c.Hkv;
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-    }
-    if (lane == 31) sh_warp[warp] = incl;
-    __syncthreads();
-    int64_t total = 0, before = incl - mine;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sh_warp[w];
-        total += sh_warp[w];
-    }
-    const int64_t ctas = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
-    if ((int64_t)blockIdx.x >= ctas) return;
-    const int64_t t0 = (int64_t)blockIdx.x * total / ctas, t1 = ((int64_t)blockIdx.x + 1) * total / ctas;
-    if (before <= t0 && t0 < before + mine) {
-        for (int b = b0;; ++b) {
-            if (per > 1) r = load_request<kRows, Sh::kTile>(p, b, nullptr);
-            const int64_t k = (int64_t)r.tiles * r.nrb * p.c.Hkv;
-            if (t0 < before + k) {
-                sh_b = b;
-                sh_req = r;
-                sh_start = t0 - before;
-                break;
-            }
-            before += k;
-        }
-    }
-    __syncthreads();
+    // ---- this CTA's tiles
+    Work wk;
     Cursor<kRows, Sh::kTile> cur;
-    cur.b = sh_b;
-    cur.r = sh_req;
-    {
-        const int64_t x = sh_start;
-        const int64_t seg = x / cur.r.tiles;
-        cur.tile = (int)(x - seg * cur.r.tiles);
-        cur.h = (int)(seg / cur.r.nrb);
-        cur.rb = (int)(seg - (int64_t)cur.h * cur.r.nrb);
-    }
+    if (!find_work<kRows, Sh::kTile, kThreads>(p, wk, cur)) return;
+    const int64_t t0 = wk.t0, t1 = wk.t1;
     const int count = (int)(t1 - t0);
 
     // ---- producer: the warp's positions of tile `pc` into stage s.  Lanes 3 i
@@ -360,6 +230,17 @@ attn_mma_kernel(const UsAttnParams p) {
     const int my_sub = lane / 3, my_part = lane - 3 * my_sub;
     constexpr int kNoPage = -0x7fffffff - 1;               // nothing to copy (any other bad number is recorded)
     int page = kNoPage, page_pos = 0;
+    auto copy = [&](const Cursor<kRows, Sh::kTile>& at, int id, int pos, int s, int sub, int part, uint32_t bits) {
+        if (part == 0 && sub == (bits & 1u ? 0 : 1))       // the stage's first copy also says what is to come
+            us::mbar_arrive_expect_tx(&full[warp][s], (uint32_t)(__popc(bits) * (2 * kBlock * Sh::kRow + kBlock * 4)));
+        const int64_t e = us::kv_entry(p.c, id, at.h, pos);
+        const uint8_t* src = part == 0 ? p.c.k + e * Sh::kRow
+                           : part == 1 ? p.c.v + e * Sh::kRow
+                                       : reinterpret_cast<const uint8_t*>(p.c.scale) + e * 4;
+        const int off = part < 2 ? (part * kStep + sub * kBlock) * Sh::kRow : 2 * kStep * Sh::kRow + sub * kBlock * 4;
+        us::bulk_g2s(wring + s * Sh::kStageBytes + off, src, part == 2 ? (uint32_t)kBlock * 4u : (uint32_t)(kBlock * Sh::kRow),
+                     &full[warp][s]);
+    };
     auto find_page = [&]() {
         page_pos = pc.tile * Sh::kTile + warp * kStep + my_sub * kBlock;
         page = my_sub < kSub && page_pos < pc.r.ctx + pc.r.n
@@ -372,26 +253,34 @@ attn_mma_kernel(const UsAttnParams p) {
         uint32_t bits = votes & 1u;
         if constexpr (kSub == 2) bits |= (votes >> 2) & 2u;
         have = (have & ~(((1u << kSub) - 1u) << (s * kSub))) | (bits << (s * kSub));
-        if (ok) {
-            if (lane == (bits & 1u ? 0 : 3))
-                us::mbar_arrive_expect_tx(&full[warp][s], (uint32_t)(__popc(bits) * (2 * kBlock * Sh::kRow + kBlock * 4)));
-            const int64_t e = us::kv_entry(p.c, page, pc.h, page_pos);
-            const uint8_t* src = my_part == 0 ? p.c.k + e * Sh::kRow
-                               : my_part == 1 ? p.c.v + e * Sh::kRow
-                                              : reinterpret_cast<const uint8_t*>(p.c.scale) + e * 4;
-            const int off = my_part < 2 ? (my_part * kStep + my_sub * kBlock) * Sh::kRow
-                                        : 2 * kStep * Sh::kRow + my_sub * kBlock * 4;
-            us::bulk_g2s(wring + s * Sh::kStageBytes + off, src, my_part == 2 ? (uint32_t)kBlock * 4u : (uint32_t)(kBlock * Sh::kRow),
-                         &full[warp][s]);
-        }
+        if (ok) copy(pc, page, page_pos, s, my_sub, my_part, bits);
         if (more) {
             pc.next(p);
             find_page();
         }
     };
+    // The first stages at once: lane groups of 3 kSub lanes each take one.
     const int ahead = count < kStages ? count : kStages;
-    find_page();
-    for (int s = 0; s < ahead; ++s) issue(s, s + 1 < count);
+    {
+        static_assert(kStages * 3 * kSub <= 32, "a lane per copy");
+        const int st = lane / (3 * kSub), in = lane - st * 3 * kSub, sub = in / 3, part = in - 3 * sub;
+        Cursor<kRows, Sh::kTile> at = cur;
+        for (int i = 0; i < st && st < ahead; ++i) at.next(p);
+        const int pos = at.tile * Sh::kTile + warp * kStep + sub * kBlock;
+        const bool want = st < ahead && pos < at.r.ctx + at.r.n;
+        const int id = want ? p.c.table[(int64_t)at.b * p.c.max_pages + (pos >> p.c.page_shift)] : -1;
+        const bool ok = id >= 0 && id < p.c.num_pages;
+        if (want && !ok) us::set_status(p.c.status, US_ERR_CORRUPT);
+        const uint32_t votes = __ballot_sync(0xffffffffu, ok && part == 0);
+#pragma unroll
+        for (int i = 0; i < kStages * kSub; ++i) have |= ((votes >> (3 * i)) & 1u) << i;
+        if (ok) {
+            const uint32_t bits = (have >> (st * kSub)) & ((1u << kSub) - 1u);
+            copy(at, id, pos, st, sub, part, bits);
+        }
+        for (int i = 0; i < ahead && i + 1 < count; ++i) pc.next(p);
+        if (ahead < count) find_page();
+    }
 
     // ---- consumer state: maxima, sums and O^T of the warp's positions
     float m[NT][2], l[NT][2], qb[NT][2], o[kMT][NT][4], vref = 0.f, vmul = 0.f;
@@ -456,6 +345,8 @@ attn_mma_kernel(const UsAttnParams p) {
             const uint8_t* st = wring + s * Sh::kStageBytes;
             const int pos = cur.tile * Sh::kTile + warp * kStep;
             float sx[kSub][NT][4], vs[kSub][2];
+            float vtop;
+            uint32_t top2 = 0;                             // (K, V) scale maxima
             const bool edge = pos + kStep > cur.r.ctx || blocks != (1u << kSub) - 1u;
 #pragma unroll
             for (int sb = 0; sb < kSub; ++sb) {
@@ -493,6 +384,7 @@ attn_mma_kernel(const UsAttnParams p) {
                 // ---- scores (elements 0, 1: token rt; 2, 3: token rt + 8), masks
                 const uint32_t* ss = reinterpret_cast<const uint32_t*>(st + 2 * kStep * Sh::kRow) + sb * kBlock;
                 const uint32_t s0 = ss[rt], s1 = ss[rt + 8];
+                top2 = sb ? hmax2(top2, hmax2(s0 & 0x7FFFFFFFu, s1 & 0x7FFFFFFFu)) : hmax2(s0 & 0x7FFFFFFFu, s1 & 0x7FFFFFFFu);
                 const float ks[2] = {us::half_bits_to_float((uint16_t)s0) * sc, us::half_bits_to_float((uint16_t)s1) * sc};
                 vs[sb][0] = us::half_bits_to_float((uint16_t)(s0 >> 16));
                 vs[sb][1] = us::half_bits_to_float((uint16_t)(s1 >> 16));
@@ -505,7 +397,7 @@ attn_mma_kernel(const UsAttnParams p) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int j = ((blocks >> sb) & 1u) ? pos + sb * kBlock + rt + 8 * u - cur.r.ctx : cur.r.n;
-                        if (j >= cur.r.n) vs[sb][u] = 0.f;
+                        if (j >= cur.r.n) vs[sb][u] = 0.f;     // nothing sees it, whatever its scale
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -519,13 +411,18 @@ attn_mma_kernel(const UsAttnParams p) {
             }
             // ---- running maxima, rescaled only where one has grown by 2^4
             // (entries that no row sees may hold any scale: only finite ones count)
-            float va = 0.f;
             bool grow = false;
+            if (edge) {
+                float va = 0.f;
 #pragma unroll
-            for (int sb = 0; sb < kSub; ++sb)
+                for (int sb = 0; sb < kSub; ++sb)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) va = fmaxf(va, fabsf(vs[sb][u]) < INFINITY ? fabsf(vs[sb][u]) : 0.f);
-            grow = va >= vref;
+                    for (int u = 0; u < 2; ++u) va = fmaxf(va, fabsf(vs[sb][u]) < INFINITY ? fabsf(vs[sb][u]) : 0.f);
+                vtop = va;
+            } else {
+                vtop = us::half_bits_to_float((uint16_t)(top2 >> 16));
+            }
+            grow = vtop >= vref;
             float mx[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -537,10 +434,10 @@ attn_mma_kernel(const UsAttnParams p) {
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, d));
+                for (int d = 4; d < 32; d <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, d));
                 float fv = 1.f;
-                if (va >= vref) {                              // the power of two above it
-                    const float nv = __uint_as_float((__float_as_uint(fmaxf(va, 1e-30f)) & 0x7F800000u) + 0x00800000u);
+                if (vtop >= vref) {                              // the power of two above it
+                    const float nv = __uint_as_float((__float_as_uint(fmaxf(vtop, 1e-30f)) & 0x7F800000u) + 0x00800000u);
                     fv = vref / nv;
                     vref = nv;
                     vmul = kVHead / nv;
@@ -576,7 +473,12 @@ attn_mma_kernel(const UsAttnParams p) {
                         const float mm = m[nt][e & 1];
                         w[e] = ex2(sx[sb][nt][e] - (edge && mm == -INFINITY ? 0.f : mm));
                         l[nt][e & 1] += w[e];
-                        x[e] = edge && w[e] == 0.f ? 0.f : w[e] * wv[e >> 1];
+                        x[e] = w[e] * wv[e >> 1];
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (w[e] == 0.f) x[e] = 0.f;       // an unseen entry's scale may be anything
                     }
 #pragma unroll
                     for (int u = 0; u < 2; ++u) pf[nt][u] = transpose8x8(pack_half2(x[2 * u], x[2 * u + 1]));
@@ -612,12 +514,13 @@ attn_mma_kernel(const UsAttnParams p) {
                     }
             }
         }
+        const bool ends = cur.tile + 1 == cur.tiles || it + 1 == count;
         __syncwarp();                                      // every lane has read the stage
         if (it + kStages < count) issue(s, it + kStages + 1 < count);
         s = s + 1 == kStages ? 0 : s + 1;
 
         // ---- the end of the segment, or of this CTA's part of it
-        if (cur.tile + 1 == cur.r.tiles || it + 1 == count) {
+        if (ends) {
             const int rows = min(kRows, cur.r.n * G - cur.rb * kRows);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -633,15 +536,10 @@ attn_mma_kernel(const UsAttnParams p) {
                 }
             __syncthreads();
             // segment [s0, s1) of the tile sequence, this CTA's part, who else has one
-            const int64_t s0 = t0 + it - cur.tile, s1 = s0 + cur.r.tiles;
-            const bool whole = s0 >= t0 && s1 <= t1;
-            const int first = (int)(((s0 + 1) * ctas - 1) / total), last = (int)((s1 * ctas - 1) / total);
-            const int64_t fstart = (int64_t)first * total / ctas;
-            float* slots = p.ws_slots;
-            auto slot_of = [&](int c) {                    // a CTA's second slot: a segment that begins inside it
-                return slots + ((int64_t)2 * c + (c == first && s0 > fstart ? 1 : 0)) * Sh::kSlotFloats;
-            };
-            float* slot = slot_of(blockIdx.x);
+            const int64_t s0 = t0 + it - cur.tile, s1 = s0 + cur.tiles;
+            const Part part = wk.sharers(s0, s1, cur, rows);
+            const bool whole = part.first == part.last;
+            float* slot = p.ws_slots + part.slot(blockIdx.x) * Sh::kSlotFloats;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -708,7 +606,7 @@ attn_mma_kernel(const UsAttnParams p) {
                 }
             }
             if (!whole) {                                  // joined after the loop, which needs the registers
-                if (threadIdx.x == 0) sh_part[parts] = Part{first, last, cur.r.row0, cur.h, cur.rb, rows, s0 > fstart};
+                if (threadIdx.x == 0) sh_part[parts] = part;
                 ++parts;
             }
             if (it + 1 < count) {
@@ -721,28 +619,30 @@ attn_mma_kernel(const UsAttnParams p) {
     }
     // ---- shared segments (at most two a CTA): the last CTA to arrive joins them
     for (int i = 0; i < parts; ++i) {
-        __threadfence();
         __syncthreads();
         const Part a = sh_part[i];
-        if (threadIdx.x == 0) sh_last = atomicAdd(p.ws_count + a.first, 1u) == (unsigned)(a.last - a.first);
+        if (threadIdx.x == 0) {                            // one thread's fences order the whole CTA's accesses
+            __threadfence();
+            sh_last = atomicAdd(p.ws_count + a.first, 1u) == (unsigned)(a.last - a.first);
+            __threadfence();
+        }
         __syncthreads();
         if (!sh_last) continue;
-        __threadfence();
         if (threadIdx.x == 0) p.ws_count[a.first] = 0;
-        join_states<ELEM, D, NT>(p, join, sm_inv, a);
+        join_states<ELEM, D, NT, W>(p, join, sm_inv, a);
     }
     us::pdl_launch_dependents();
 }
 
-template <int ELEM, int D, int NT>
+template <int ELEM, int D, int NT, int W>
 struct Plan {
-    using Sh = Shape<ELEM, D, NT>;
+    using Sh = Shape<ELEM, D, NT, W>;
     static int grid() { return us::num_sms() * Sh::kMinB < 1024 ? us::num_sms() * Sh::kMinB : 1024; }
     static size_t ws() { return 4096 + (size_t)2 * grid() * Sh::kSlotFloats * 4; }
     static us_status launch(UsAttnParams p, cudaStream_t st) {
         p.ws_count = static_cast<unsigned*>(p.ws);
         p.ws_slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + 4096);
-        auto kern = attn_mma_kernel<ELEM, D, NT>;
+        auto kern = attn_mma_kernel<ELEM, D, NT, W>;
         static bool ready[64] = {};                        // the attribute is set once a device
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return US_ERR_CUDA;
@@ -753,7 +653,7 @@ struct Plan {
         }
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)grid());
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(Sh::kThreads);
         cfg.dynamicSmemBytes = Sh::kSmem;
         cfg.stream = st;
         cudaLaunchAttribute attr[1];
@@ -765,11 +665,16 @@ struct Plan {
     }
 };
 
-// f(Plan) for the cache's type and head width and the rows per key head
+// f(Plan) for the cache's type and head width and the rows per key head.  Eight
+// warps a CTA, two CTAs an SM, for up to 8 rows: on one token of two 131000-
+// position requests 83.5 us (four CTAs of four warps: 88.7, one of 16: 82.4), on
+// 48 requests of 4096 to 8192 positions in int4 86.8 (85.4, 94.3), on one of 777
+// 9.5 (9.8, 11.4): fewer CTAs leave fewer partial states to join, more keep
+// working while one starts a segment.
 template <class F>
 auto with_plan(const UsAttnParams& p, F f) {
     const int rows = p.a.max_n * p.G;
-#define US_ATTN_PICK(E, D) (rows <= 8 ? f(Plan<E, D, 1>()) : f(Plan<E, D, 2>()))
+#define US_ATTN_PICK(E, D) (rows <= 8 ? f(Plan<E, D, 1, 8>()) : f(Plan<E, D, 2, 4>()))
     if (p.c.elem == US_I8) return p.c.D == 64 ? US_ATTN_PICK(US_I8, 64) : US_ATTN_PICK(US_I8, 128);
     return p.c.D == 64 ? US_ATTN_PICK(US_I4, 64) : US_ATTN_PICK(US_I4, 128);
 #undef US_ATTN_PICK
@@ -780,10 +685,12 @@ auto with_plan(const UsAttnParams& p, F f) {
 namespace us {
 
 size_t attn_ws(const UsAttnParams& p) {
+    if (attn_tc_serves(p)) return attn_tc_ws(p);
     return with_plan(p, [](auto plan) { return decltype(plan)::ws(); });
 }
 
 us_status launch_attn(const UsAttnParams& p, cudaStream_t st) {
+    if (attn_tc_serves(p)) return launch_attn_tc(p, st);
     return with_plan(p, [&](auto plan) { return decltype(plan)::launch(p, st); });
 }
 

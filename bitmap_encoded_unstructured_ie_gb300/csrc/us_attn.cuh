@@ -1,0 +1,216 @@
+// us_attn.cuh -- what the attention kernels share: the even partition of the
+// (request, key head, row block, tile) sequence over the CTAs, and the codes as
+// fp16 pairs.
+#pragma once
+
+#include "us_kv.cuh"
+
+namespace us {
+namespace attn {
+
+constexpr float kMaxLag = 4.f;                    // a row's maximum may lag by 2^4 before the state is rescaled
+constexpr float kVHead = 2048.f;                  // weights reach 2^4 2^11 < 65504 as fp16: small ones keep their bits
+
+US_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+US_DEV uint32_t hsub2(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+US_DEV uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b), *reinterpret_cast<__half2*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+US_DEV float sum_half2(uint32_t a) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    return f.x + f.y;
+}
+US_DEV uint32_t pack_half2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Both halves of a word of codes as exact fp16 pairs: 0x6400 | u is the fp16
+// number 1024 + u, and flipping a code's sign bit makes it u = code + 8 (+ 128).
+// int4: nibbles (0, 4), (1, 5), (2, 6), (3, 7); int8: bytes (0, 2), (1, 3).
+US_DEV void decode_i4(uint32_t x, uint32_t (&q)[4]) {
+    const uint32_t y = x >> 8;
+    q[0] = hsub2(us::lop3<us::kLopAndXor>(x, 0x000F000Fu, 0x64086408u), 0x64086408u);
+    q[1] = hfma2(us::lop3<us::kLopAndXor>(x, 0x00F000F0u, 0x64806480u), 0x2C002C00u, 0xD480D480u);   // x/16 - 72
+    q[2] = hsub2(us::lop3<us::kLopAndXor>(y, 0x000F000Fu, 0x64086408u), 0x64086408u);
+    q[3] = hfma2(us::lop3<us::kLopAndXor>(y, 0x00F000F0u, 0x64806480u), 0x2C002C00u, 0xD480D480u);
+}
+US_DEV void decode_i8(uint32_t x, uint32_t (&q)[2]) {
+    q[0] = hsub2(us::lop3<us::kLopAndXor>(x, 0x00FF00FFu, 0x64806480u), 0x64806480u);
+    q[1] = hsub2(us::lop3<us::kLopAndXor>(x >> 8, 0x00FF00FFu, 0x64806480u), 0x64806480u);
+}
+
+// a / b, in 32 bits where that does
+US_DEV int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// A request's tokens, context and row blocks; none where its arguments are not
+// usable.
+struct Request {
+    int row0, n, ctx, nrb;
+};
+
+// Tiles that row block rb of ROWS rows reads: a chain's rows see no position
+// behind their own.
+template <int ROWS, int TILE>
+US_DEV int tiles_of(const UsAttnParams& p, const Request& r, int rb) {
+    int end = r.n;
+    if (!p.mask) {
+        const int64_t rows = (int64_t)(rb + 1) * ROWS;
+        if (rows < (int64_t)r.n * p.G) end = (int)((rows - 1) / p.G) + 1;
+    }
+    return (r.ctx + end + TILE - 1) / TILE;
+}
+
+template <int ROWS>
+US_DEV Request load_request(const UsAttnParams& p, int b, unsigned* status) {
+    Request r = {0, 0, 0, 0};
+    const int ctx = p.a.pos[b];                            // with the offsets, not after them
+    r.n = us::kv_rows(p.a, b, r.row0, status);
+    if (r.n > 0) {
+        r.ctx = us::kv_context(p.c, ctx, r.n, status);
+        if (r.ctx >= 0) r.nrb = (r.n * p.G + ROWS - 1) / ROWS;
+    }
+    return r;
+}
+
+// Tiles of one key head of a request.
+template <int ROWS, int TILE>
+US_DEV int64_t head_tiles(const UsAttnParams& p, const Request& r) {
+    if (p.mask) return r.nrb ? (int64_t)r.nrb * tiles_of<ROWS, TILE>(p, r, 0) : 0;
+    int64_t sum = 0;
+    for (int rb = 0; rb < r.nrb; ++rb) sum += tiles_of<ROWS, TILE>(p, r, rb);
+    return sum;
+}
+
+// A place in the tile sequence.
+template <int ROWS, int TILE>
+struct Cursor {
+    Request r;
+    int b, h, rb, tile, tiles;                             // tiles: of this row block
+    US_DEV void next(const UsAttnParams& p) {
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++rb == r.nrb) {
+            rb = 0;
+            if (++h == p.c.Hkv) {
+                h = 0;
+                do {
+                    ++b;
+                    if (b < p.c.B) r = load_request<ROWS>(p, b, nullptr);
+                } while (b < p.c.B && r.nrb == 0);
+                if (b == p.c.B) return;
+            }
+        }
+        tiles = tiles_of<ROWS, TILE>(p, r, rb);
+    }
+};
+
+// A segment (request, key head, row block) shared by CTAs first .. last; second:
+// the first of them leaves its state in its second slot, because its part is not
+// the first thing it does.
+struct Part {
+    int first, last, row0, h, rb, rows;
+    bool second;
+    US_DEV int64_t slot(int cta) const { return (int64_t)2 * cta + (cta == first && second ? 1 : 0); }
+};
+
+// A CTA's share [t0, t1) of the sequence of `total` tiles spread over `ctas` CTAs.
+struct Work {
+    int64_t t0, t1, total, ctas;
+    template <class C>
+    US_DEV Part sharers(int64_t s0, int64_t s1, const C& at, int rows) const {
+        Part a;
+        a.first = (int)quotient((s0 + 1) * ctas - 1, total);
+        a.last = (int)quotient(s1 * ctas - 1, total);
+        a.second = s0 > quotient(a.first * total, ctas);
+        a.row0 = at.r.row0, a.h = at.h, a.rb = at.rb, a.rows = rows;
+        return a;
+    }
+};
+
+// The share of this CTA and where it begins: a block-wide scan of the requests'
+// tiles (all THREADS threads take part).  False if there is none for it.
+template <int ROWS, int TILE, int THREADS>
+US_DEV bool find_work(const UsAttnParams& p, Work& w, Cursor<ROWS, TILE>& at) {
+    __shared__ Request sh_req;
+    __shared__ int64_t sh_x, sh_warp[THREADS / 32];
+    __shared__ int sh_b;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = (p.c.B + THREADS - 1) / THREADS, b0 = threadIdx.x * per;
+    int64_t mine = 0;
+    Request r = {0, 0, 0, 0};
+    for (int b = b0; b < min(b0 + per, p.c.B); ++b) {
+        r = load_request<ROWS>(p, b, blockIdx.x == 0 ? p.c.status : nullptr);
+        mine += head_tiles<ROWS, TILE>(p, r) * p.c.Hkv;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) sh_warp[warp] = incl;
+    __syncthreads();
+    int64_t total = 0, before = incl - mine;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < warp) before += sh_warp[i];
+        total += sh_warp[i];
+    }
+    w.total = total;
+    w.ctas = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
+    if ((int64_t)blockIdx.x >= w.ctas) return false;
+    w.t0 = quotient(blockIdx.x * total, w.ctas), w.t1 = quotient((blockIdx.x + 1) * total, w.ctas);
+    if (before <= w.t0 && w.t0 < before + mine) {
+        for (int b = b0;; ++b) {
+            if (per > 1) r = load_request<ROWS>(p, b, nullptr);
+            const int64_t k = head_tiles<ROWS, TILE>(p, r) * p.c.Hkv;
+            if (w.t0 < before + k) {
+                sh_b = b;
+                sh_req = r;
+                sh_x = w.t0 - before;
+                break;
+            }
+            before += k;
+        }
+    }
+    __syncthreads();
+    at.b = sh_b;
+    at.r = sh_req;
+    const int64_t head = head_tiles<ROWS, TILE>(p, at.r);
+    at.h = (int)quotient(sh_x, head);
+    int64_t x = sh_x - at.h * head;
+    at.rb = 0;
+    at.tiles = tiles_of<ROWS, TILE>(p, at.r, 0);
+    if (p.mask) {
+        at.rb = (int)quotient(x, at.tiles);
+        x -= (int64_t)at.rb * at.tiles;
+    } else {
+        while (x >= at.tiles) {
+            x -= at.tiles;
+            at.tiles = tiles_of<ROWS, TILE>(p, at.r, ++at.rb);
+        }
+    }
+    at.tile = (int)x;
+    return true;
+}
+
+// Where a row's fp16 outputs go: D values at row r of row block rb, head h.
+template <int ROWS>
+US_DEV uint16_t* out_row(const UsAttnParams& p, int row0, int h, int rb, int r, int D) {
+    const int rr = rb * ROWS + r, i = rr / p.G;
+    return p.O + (int64_t)(row0 + i) * p.ldo + (int64_t)(h * p.G + rr - i * p.G) * D;
+}
+
+}  // namespace attn
+}  // namespace us

@@ -1,0 +1,554 @@
+// us_attn_tc.cu -- attention of many query rows per key head over the quantised
+// K/V cache (drafted trees, chunks of a prompt), on the tensor cores (tcgen05).
+//
+// Same function as us_attn.cu.  A segment is (request, key head, block of 128
+// query rows); its positions come in tiles of 128, and the tiles of all segments
+// are spread evenly over the CTAs (one an SM):
+//   S = Q Ck^T    A = Q (shared memory), B = the tile's K codes as fp16
+//   O += P Cv     A = P (TMEM, fp16), B = the tile's V codes as fp16, MN-major
+// with K's scale on the scores and V's scale in the weights P.  The dimensions
+// stand in shared memory in the order in which the codes leave their words
+// (within each eight), the same for Q, K and V; only the outputs are put back.
+//
+// Tiles alternate between two streams, each with its own scores, outputs, row
+// references and softmax warps, so that the tensor cores work on one stream while
+// the other's weights are made; the streams are joined at the segment's end.
+//   warps 0-3, 4-7: softmax of stream 0 / 1, one thread a row; one of them issues
+//               the stream's MMAs: PV of this tile, then QK of the stream's next
+//   warps 8-15: codes -> fp16, 16 positions each; the next tile's codes are in
+//               their registers while this one's are converted
+// 16 warps: a thread may have 128 registers (17 would leave 96).
+// A row's reference R stands for its maximum and for the size of V's scales at
+// once: weights are w = 2^(s - R), the row sum adds w, P holds w s_v as fp16, and R
+// moves only when some w s_v could pass 2^15.  R, sums and outputs of a segment
+// shared by several CTAs are joined by the last of them to arrive.
+#include "us_attn.cuh"
+#include "us_internal.h"
+#include "us_tcgen05.cuh"
+
+namespace {
+
+using namespace us::attn;
+
+constexpr int kRows = 128, kTile = 128;           // query rows of a segment, positions of a tile
+constexpr int kSoftWarps = 8, kConvWarps = 8;
+constexpr int kThreads = 32 * (kSoftWarps + kConvWarps);
+constexpr int kKS = 2, kVS = 3, kSS = 4;          // stages: K, V, scales
+constexpr float kTop = 11.f, kLag = 4.f;          // a row's largest w s_v is 2^11 at first, 2^15 at most
+
+struct Header {
+    uint64_t k_full[kKS], v_full[kVS], s_full[kSS];
+    uint64_t qk_done[2], pv_done[2], v_free[kVS];  // v_free: the same event as pv_done, by stage
+    float ks[kSS][kTile], sv[kSS][kTile];         // scales of the tiles on their way: K's times scale log2(e), V's
+    float svmax[kSS][kConvWarps];
+    uint16_t valid[kSS][kConvWarps];              // which of a warp's 16 positions exist
+    float xr[2][kRows], xl[2][kRows];             // the streams' references and sums
+    uint32_t tmem;
+    unsigned last;
+    Part part[2];
+};
+
+template <int ELEM, int D>
+struct Shape {
+    static constexpr int kRow = D * (ELEM == US_I8 ? 8 : 4) / 8;    // bytes of a row of codes
+    static constexpr int kC = kRow / 16;                            // 16-byte chunks of it
+    static constexpr int kLoads = kC / 2;                           // chunks a lane converts of 16 rows
+    static constexpr int kOut = ELEM == US_I8 ? 2 : 4;              // 16-byte chunks of fp16 a chunk becomes
+    static constexpr int kOperand = 128 * D * 2;                    // Q, K tile or V tile as fp16
+    static constexpr int kGroup = 128 * 128;                        // one 64-dimension half of it
+    static constexpr int kSmem = (1 + kKS + kVS) * kOperand + (int)sizeof(Header) + 1024;
+    static constexpr int kSlotFloats = 2 * kRows + kRows * D;
+};
+
+// Column j of eight -> its dimension of eight: the order in which codes leave a word.
+template <int ELEM>
+US_DEV constexpr int dim_of(int j) {
+    return ELEM == US_I8 ? (j & 4) | ((j & 1) << 1) | ((j >> 1) & 1) : ((j & 1) << 2) | (j >> 1);
+}
+
+// 16 bytes of codes -> kOut chunks of eight fp16 values
+template <int ELEM>
+US_DEV void convert(uint4 u, uint4 (&out)[ELEM == US_I8 ? 2 : 4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (ELEM == US_I8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t a[2], b[2];
+            decode_i8(w[2 * i], a);
+            decode_i8(w[2 * i + 1], b);
+            out[i] = make_uint4(a[0], a[1], b[0], b[1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t a[4];
+            decode_i4(w[i], a);
+            out[i] = make_uint4(a[0], a[1], a[2], a[3]);
+        }
+    }
+}
+
+// Eight fp16 values in the order of dim_of
+template <int ELEM>
+US_DEV uint4 reorder(uint4 u) {
+    if constexpr (ELEM == US_I8)
+        return make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x5410),
+                          __byte_perm(u.z, u.w, 0x7632));
+    else
+        return make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
+                          __byte_perm(u.y, u.w, 0x7632));
+}
+
+// 16-byte chunk `chunk` of row `row` of an operand (64-dimension halves, 128-byte swizzle)
+US_DEV uint8_t* operand_at(uint8_t* base, int row, int chunk) {
+    return base + (chunk >> 3) * (128 * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// Eight outputs in the order of dim_of -> fp16 in the order of the dimensions
+template <int ELEM>
+US_DEV void store8(uint16_t* out, const float* y, float f) {
+    float d[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[dim_of<ELEM>(j)] = y[j] * f;
+    *reinterpret_cast<uint4*>(out) =
+        make_uint4(pack_half2(d[0], d[1]), pack_half2(d[2], d[3]), pack_half2(d[4], d[5]), pack_half2(d[6], d[7]));
+}
+
+// The last CTA of a shared segment joins the partial states: a thread takes a
+// quarter of a row, O stands as float4 of four columns, row after row.
+template <int ELEM, int D>
+US_DEV void join_states(const UsAttnParams& p, const Part& a) {
+    using Sh = Shape<ELEM, D>;
+    if (threadIdx.x >= 4 * kRows) return;
+    constexpr int kN = D / 16;                             // float4 of a quarter row
+    const int row = threadIdx.x & (kRows - 1), quarter = threadIdx.x / kRows;
+    if (row >= a.rows) return;
+    float top = -INFINITY, sum = 0.f, y[4 * kN];
+#pragma unroll
+    for (int i = 0; i < 4 * kN; ++i) y[i] = 0.f;
+#pragma unroll 4
+    for (int c = a.first; c <= a.last; ++c) top = fmaxf(top, __ldcg(p.ws_slots + a.slot(c) * Sh::kSlotFloats + row));
+#pragma unroll 2
+    for (int c = a.first; c <= a.last; ++c) {
+        const float* sl = p.ws_slots + a.slot(c) * Sh::kSlotFloats;
+        const float r = __ldcg(sl + row), f = r == -INFINITY ? 0.f : ex2(r - top);
+        sum += __ldcg(sl + kRows + row) * f;
+        const float4* o = reinterpret_cast<const float4*>(sl + 2 * kRows) + quarter * kN * kRows + row;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const float4 v = __ldcg(o + i * kRows);
+            y[4 * i] += v.x * f, y[4 * i + 1] += v.y * f, y[4 * i + 2] += v.z * f, y[4 * i + 3] += v.w * f;
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint16_t* out = out_row<kRows>(p, a.row0, a.h, a.rb, row, D) + quarter * (D / 4);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) store8<ELEM>(out + 8 * i, y + 8 * i, inv);
+}
+
+template <int ELEM, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tc_kernel(const UsAttnParams p) {
+    using Sh = Shape<ELEM, D>;
+    using Cur = Cursor<kRows, kTile>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* q_sm = smem;
+    uint8_t* k_sm = q_sm + Sh::kOperand;
+    uint8_t* v_sm = k_sm + kKS * Sh::kOperand;
+    Header& H = *reinterpret_cast<Header*>(v_sm + kVS * Sh::kOperand);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kKS; ++i) us::mbar_init(&H.k_full[i], kConvWarps);
+        for (int i = 0; i < kVS; ++i) us::mbar_init(&H.v_full[i], kConvWarps), us::mbar_init(&H.v_free[i], 1);
+        for (int i = 0; i < kSS; ++i) us::mbar_init(&H.s_full[i], kConvWarps);
+        for (int i = 0; i < 2; ++i) us::mbar_init(&H.qk_done[i], 1), us::mbar_init(&H.pv_done[i], 1);
+        us::fence_mbar_init();
+    }
+    if (warp == kSoftWarps) us::tmem_alloc(&H.tmem, 512);
+    us::pdl_wait();
+
+    Work wk;
+    Cur cur;
+    const bool any = find_work<kRows, kTile, kThreads>(p, wk, cur);       // its barrier covers the set-up above
+    us::tc_fence_after();
+    const uint32_t tmem = H.tmem;                          // S0, S1, O0, O1: 128 columns each
+    const int count = any ? (int)(wk.t1 - wk.t0) : 0, G = p.G;
+    bool failed = false;
+    auto wait = [&](uint64_t* bar, int use) {              // for the use-th completion of bar
+        if (!failed && !us::mbar_wait(bar, (uint32_t)use & 1u, p.c.status)) failed = true;
+    };
+
+    // ---- converters: where a warp's 16 positions of a tile are
+    struct Where {
+        int page, pos, h;
+        bool want;
+    };
+    Cur ahead = cur;                                       // two tiles ahead of the conversion
+    int found = 0;                                         // tiles whose page numbers were loaded
+    auto locate = [&]() {
+        Where w = {-1, 0, 0, false};
+        if (found < count) {
+            if (found) ahead.next(p);
+            ++found;
+            w.pos = ahead.tile * kTile + (warp - kSoftWarps) * 16;
+            w.h = ahead.h;
+            w.want = w.pos < ahead.r.ctx + ahead.r.n;
+            if (w.want) w.page = p.c.table[(int64_t)ahead.b * p.c.max_pages + (w.pos >> p.c.page_shift)];
+        }
+        return w;
+    };
+    uint4 kreg[Sh::kLoads], vreg[Sh::kLoads];
+    uint32_t sreg = 0;
+    int npos = 0;                                          // the 16 positions: 16 or none
+    auto row_chunk = [&](int u, int& row, int& chunk) {    // eight lanes on eight rows: no bank conflicts
+        if constexpr (Sh::kC == 2) row = lane & 15, chunk = lane >> 4;
+        else row = 8 * (u / (Sh::kC / 4)) + (lane & 7), chunk = 4 * (u % (Sh::kC / 4)) + (lane >> 3);
+    };
+    auto fetch = [&](const Where& w, const uint8_t* pool, uint4 (&reg)[Sh::kLoads]) {
+        const bool ok = w.want && w.page >= 0 && w.page < p.c.num_pages;
+        if (ok) {
+            const uint8_t* src = pool + us::kv_entry(p.c, w.page, w.h, w.pos) * Sh::kRow;
+#pragma unroll
+            for (int u = 0; u < Sh::kLoads; ++u) {
+                int row, chunk;
+                row_chunk(u, row, chunk);
+                reg[u] = __ldcg(reinterpret_cast<const uint4*>(src + row * Sh::kRow) + chunk);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < Sh::kLoads; ++u) reg[u] = make_uint4(0, 0, 0, 0);
+        }
+        return ok;
+    };
+    auto fetch_k = [&](const Where& w) {
+        const bool ok = fetch(w, p.c.k, kreg);
+        if (w.want && !ok) us::set_status(p.c.status, US_ERR_CORRUPT);
+        npos = ok ? 16 : 0;
+        sreg = ok && lane < 16 ? __ldcg(reinterpret_cast<const uint32_t*>(p.c.scale) + us::kv_entry(p.c, w.page, w.h, w.pos) + lane) : 0u;
+    };
+    auto put = [&](uint8_t* operand, const uint4 (&reg)[Sh::kLoads]) {
+#pragma unroll
+        for (int u = 0; u < Sh::kLoads; ++u) {
+            int row, chunk;
+            row_chunk(u, row, chunk);
+            uint4 out[Sh::kOut];
+            convert<ELEM>(reg[u], out);
+#pragma unroll
+            for (int k = 0; k < Sh::kOut; ++k)
+                *reinterpret_cast<uint4*>(operand_at(operand, (warp - kSoftWarps) * 16 + row, chunk * Sh::kOut + k)) = out[k];
+        }
+    };
+    Where now = {-1, 0, 0, false}, next = now;
+    if (warp >= kSoftWarps) {
+        now = locate();
+        next = locate();
+        fetch_k(now);
+        fetch(now, p.c.v, vreg);
+    }
+
+    int parts = 0;
+    for (int it = 0; it < count;) {
+        // ---- a segment, or this CTA's part of it: tiles it .. end - 1
+        const int end = min(count, it + cur.tiles - cur.tile), tile0 = cur.tile;
+        const int rows = min(kRows, cur.r.n * G - cur.rb * kRows);
+        for (int x = threadIdx.x; x < kRows * (D / 8); x += kThreads) {
+            const int r = x / (D / 8), chunk = x % (D / 8), rr = cur.rb * kRows + r, i = rr / G;
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (r < rows)
+                u = *reinterpret_cast<const uint4*>(p.Q + (int64_t)(cur.r.row0 + i) * p.ldq + (int64_t)(cur.h * G + rr - i * G) * D + 8 * chunk);
+            *reinterpret_cast<uint4*>(operand_at(q_sm, r, chunk)) = reorder<ELEM>(u);
+        }
+        us::fence_proxy_async_smem();
+        __syncthreads();
+
+        if (warp < kSoftWarps) {
+            // ------------------------------------------------------- softmax
+            const int st = warp >> 2, row = threadIdx.x & (kRows - 1);
+            const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+            const uint32_t s_tm = tmem + lanes + st * 128, o_tm = tmem + lanes + 256 + st * 128;
+            const bool live = (warp & 3) * 32 < rows;
+            const int i_tok = (cur.rb * kRows + row) / G;
+            uint64_t mask = 0;
+            if (p.mask && row < rows) mask = p.mask[cur.r.row0 + i_tok] & (~0ull >> (64 - cur.r.n));
+            // positions that this row sees among 32 from `base` behind the context
+            auto seen32 = [&](int base) {
+                if (base <= -32) return 0xFFFFFFFFu;
+                const int lo = base < 0 ? -base : 0;       // context positions among them
+                uint32_t own;
+                if (p.mask) {
+                    own = base < 64 ? (uint32_t)(mask >> (base > 0 ? base : 0)) : 0u;
+                } else {
+                    const int k = (row < rows ? i_tok : -1) + 1 - (base > 0 ? base : 0);
+                    own = k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u;
+                }
+                return (own << lo) | (lo ? 0xFFFFFFFFu >> (32 - lo) : 0u);
+            };
+            float R = -INFINITY, l = 0.f;
+            // the stream's MMAs, by one thread
+            const bool leads = (warp & 3) == 0 && lane == 0;
+            auto qk = [&](int i) {
+                constexpr uint32_t id = us::umma_idesc_f16(kRows, kTile);
+                wait(&H.k_full[i % kKS], i / kKS);
+                us::tc_fence_after();
+                const uint64_t qd = us::umma_smem_desc_sw128(q_sm), kd = us::umma_smem_desc_sw128(k_sm + (i % kKS) * Sh::kOperand);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t at = (uint64_t)(((kk >> 2) * Sh::kGroup + (kk & 3) * 32) >> 4);
+                    us::umma_f16(tmem + st * 128, qd + at, kd + at, id, kk > 0);
+                }
+                us::umma_commit(&H.qk_done[st]);
+            };
+            auto pv = [&](int i) {
+                constexpr uint32_t id = us::umma_idesc_f16(kRows, D) | us::kUmmaBMajorMN;
+                wait(&H.v_full[i % kVS], i / kVS);
+                us::tc_fence_after();
+                const uint64_t vd = us::umma_smem_desc_mn_sw128(v_sm + (i % kVS) * Sh::kOperand, Sh::kGroup);
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    us::umma_f16_ta(tmem + 256 + st * 128, tmem + st * 128 + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), id,
+                                    i - it >= 2 || kk > 0);
+                us::umma_commit(&H.pv_done[st]);
+                us::umma_commit(&H.v_free[i % kVS]);
+            };
+            const int i0 = it + ((it ^ st) & 1);
+            if (leads && i0 < end) qk(i0);
+            __syncwarp();
+            for (int i = i0; i < end; i += 2) {
+                const int ss = i % kSS;
+                wait(&H.s_full[ss], i / kSS);
+                wait(&H.qk_done[st], i / 2);
+                us::tc_fence_after();
+                if (live) {
+                    const float4* ks4 = reinterpret_cast<const float4*>(H.ks[ss]);
+                    const float4* sv4 = reinterpret_cast<const float4*>(H.sv[ss]);
+                    const uint4 ok = *reinterpret_cast<const uint4*>(H.valid[ss]);
+                    const int base = (tile0 + i - it) * kTile - cur.r.ctx;
+                    const bool edge = base + kTile > 0 || (ok.x & ok.y & ok.z & ok.w) != 0xFFFFFFFFu;
+                    const uint32_t okw[4] = {ok.x, ok.y, ok.z, ok.w};
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        us::tmem_ld32(s_tm + 32 * c, v);
+                        const uint32_t seen = edge ? seen32(base + 32 * c) & okw[c] : 0xFFFFFFFFu;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 k = ks4[8 * c + j / 4];
+                            float x[4] = {v[j] * k.x, v[j + 1] * k.y, v[j + 2] * k.z, v[j + 3] * k.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, !edge || (seen >> (j + e)) & 1u ? x[e] : -INFINITY);
+                        }
+                    }
+                    float vm = H.svmax[ss][0];
+#pragma unroll
+                    for (int w = 1; w < kConvWarps; ++w) vm = fmaxf(vm, H.svmax[ss][w]);
+                    // log2 of the power of two above the largest scale
+                    const float lv = (float)((int)(__float_as_uint(fmaxf(vm, 5.9604645e-8f)) >> 23) - 126);
+                    const bool move = mx + lv > R + (kTop + kLag);
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float to = move ? mx + lv - kTop : R;
+                        const float f = move ? ex2(R - to) : 1.f;
+                        R = to;
+                        l *= f;
+                        if (i - it >= 2) {                 // the stream has outputs: PV of its last tile first
+                            wait(&H.pv_done[st], i / 2 - 1);
+                            us::tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                float v[16];
+                                uint32_t u[16];
+                                us::tmem_ld16(o_tm + c, v);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(v[j] * f);
+                                us::tmem_st16(o_tm + c, u);
+                            }
+                            us::tmem_wait_st();
+                        }
+                    }
+                    const float ref = R == -INFINITY ? 0.f : R;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        uint32_t u[16];
+                        us::tmem_ld32(s_tm + 32 * c, v);
+                        const uint32_t seen = edge ? seen32(base + 32 * c) & okw[c] : 0xFFFFFFFFu;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 k = ks4[8 * c + j / 4], s = sv4[8 * c + j / 4];
+                            float w[4] = {ex2(fmaf(v[j], k.x, -ref)), ex2(fmaf(v[j + 1], k.y, -ref)),
+                                          ex2(fmaf(v[j + 2], k.z, -ref)), ex2(fmaf(v[j + 3], k.w, -ref))};
+                            float x[4] = {w[0] * s.x, w[1] * s.y, w[2] * s.z, w[3] * s.w};
+                            if (edge) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (!((seen >> (j + e)) & 1u)) w[e] = x[e] = 0.f;
+                            }
+                            l += (w[0] + w[1]) + (w[2] + w[3]);
+                            u[j / 2] = pack_half2(x[0], x[1]);
+                            u[j / 2 + 1] = pack_half2(x[2], x[3]);
+                        }
+                        us::tmem_st16(s_tm + 16 * c, u);   // over scores that were read
+                    }
+                    us::tmem_wait_st();
+                }
+                us::tc_fence_before();
+                us::named_bar_sync(2 + st, 128);
+                if (leads) {
+                    us::tc_fence_after();
+                    pv(i);
+                    if (i + 2 < end) qk(i + 2);
+                }
+                __syncwarp();
+            }
+            // ---- the segment's end: both streams' sums and outputs
+            const bool has[2] = {end - it >= 2 || !(it & 1), end - it >= 2 || (it & 1)};
+            H.xr[st][row] = R, H.xl[st][row] = l;
+            wait(&H.pv_done[(end - 1) & 1], (end - 1) / 2);
+            if (end - it >= 2) wait(&H.pv_done[end & 1], (end - 2) / 2);
+            us::named_bar_sync(1, 32 * kSoftWarps);
+            us::tc_fence_after();
+            const int64_t s0 = wk.t0 + it - tile0;
+            const Part part = wk.sharers(s0, s0 + cur.tiles, cur, rows);
+            const bool whole = part.first == part.last;
+            if (live) {
+                const float r0 = H.xr[0][row], r1 = H.xr[1][row], top = fmaxf(r0, r1);
+                const float f0 = r0 == -INFINITY ? 0.f : ex2(r0 - top), f1 = r1 == -INFINITY ? 0.f : ex2(r1 - top);
+                const float sum = H.xl[0][row] * f0 + H.xl[1][row] * f1, inv = sum == 0.f ? 0.f : 1.f / sum;
+                float* slot = p.ws_slots + part.slot(blockIdx.x) * Sh::kSlotFloats;
+                if (!whole && st == 0) {
+                    __stcg(slot + row, top);
+                    __stcg(slot + kRows + row, sum);
+                }
+                uint16_t* out = row < rows ? out_row<kRows>(p, cur.r.row0, cur.h, cur.rb, row, D) : nullptr;
+#pragma unroll 1
+                for (int c = st * (D / 2); c < (st + 1) * (D / 2); c += 16) {
+                    float a[16], b[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) a[j] = b[j] = 0.f;
+                    if (has[0]) us::tmem_ld16(tmem + lanes + 256 + c, a);
+                    if (has[1]) us::tmem_ld16(tmem + lanes + 384 + c, b);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) a[j] = (f0 == 0.f ? 0.f : a[j] * f0) + (f1 == 0.f ? 0.f : b[j] * f1);
+                    if (whole) {
+                        if (row < rows) {
+                            store8<ELEM>(out + c, a, inv);
+                            store8<ELEM>(out + c + 8, a + 8, inv);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            __stcg(reinterpret_cast<float4*>(slot + 2 * kRows) + (c + j) / 4 * kRows + row,
+                                   make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]));
+                    }
+                }
+            }
+            us::tc_fence_before();
+            if (!whole) {
+                if (threadIdx.x == 0) H.part[parts] = part;
+            }
+        } else {
+            // ---------------------------------------------------- conversion
+            for (int i = it; i < end; ++i) {
+                const int w = warp - kSoftWarps, ss = i % kSS;
+                const Where w2 = locate();                 // tile i + 2
+                if (i >= kKS) wait(&H.qk_done[i % kKS], i / kKS - 1);
+                put(k_sm + (i % kKS) * Sh::kOperand, kreg);
+                const float sk = us::half_bits_to_float((uint16_t)sreg) * (p.scale * 1.4426950408889634f), sv = us::half_bits_to_float((uint16_t)(sreg >> 16));
+                float vm = fabsf(sv) < INFINITY ? fabsf(sv) : 0.f;     // entries that no row sees may hold anything
+                {
+                    const int left = cur.r.ctx + cur.r.n - ((tile0 + i - it) * kTile + 16 * w);
+                    if (lane >= left) vm = 0.f;
+                }
+#pragma unroll
+                for (int d = 1; d < 16; d <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
+                if (lane < 16) H.ks[ss][16 * w + lane] = sk, H.sv[ss][16 * w + lane] = sv;
+                if (lane == 0) H.svmax[ss][w] = vm, H.valid[ss][w] = npos ? 0xFFFFu : 0u;
+                us::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) us::mbar_arrive(&H.k_full[i % kKS]), us::mbar_arrive(&H.s_full[ss]);
+                fetch_k(next);
+                if (i >= kVS) wait(&H.v_free[i % kVS], i / kVS - 1);
+                put(v_sm + (i % kVS) * Sh::kOperand, vreg);
+                us::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) us::mbar_arrive(&H.v_full[i % kVS]);
+                fetch(next, p.c.v, vreg);
+                next = w2;
+            }
+        }
+        {
+            const int64_t s0 = wk.t0 + it - tile0;
+            if (wk.sharers(s0, s0 + cur.tiles, cur, rows).first != wk.sharers(s0, s0 + cur.tiles, cur, rows).last) ++parts;
+        }
+        __syncthreads();                                   // Q, the streams and their TMEM are free
+        us::tc_fence_after();
+        for (; it < end; ++it)
+            if (it + 1 < count) cur.next(p);
+    }
+
+    // ---- shared segments (at most two a CTA): the last CTA to arrive joins them
+    for (int i = 0; i < parts; ++i) {
+        __syncthreads();
+        const Part a = H.part[i];
+        if (threadIdx.x == 0) {                            // one thread's fences order the whole CTA's accesses
+            __threadfence();
+            H.last = atomicAdd(p.ws_count + a.first, 1u) == (unsigned)(a.last - a.first);
+            __threadfence();
+        }
+        __syncthreads();
+        if (!H.last) continue;
+        if (threadIdx.x == 0) p.ws_count[a.first] = 0;
+        join_states<ELEM, D>(p, a);
+    }
+    us::tc_fence_before();
+    __syncthreads();
+    if (warp == kSoftWarps) us::tmem_dealloc(tmem, 512);
+    us::pdl_launch_dependents();
+}
+
+template <int ELEM, int D>
+us_status launch(UsAttnParams p, cudaStream_t st) {
+    using Sh = Shape<ELEM, D>;
+    static_assert(Sh::kSmem <= 232448, "shared memory");
+    p.ws_count = static_cast<unsigned*>(p.ws);
+    p.ws_slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + 4096);
+    auto kern = attn_tc_kernel<ELEM, D>;
+    static bool ready[64] = {};                            // the attribute is set once a device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return US_ERR_CUDA;
+    if (!ready[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess)
+            return US_ERR_CUDA;
+        ready[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)us::num_sms());
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Sh::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? US_OK : US_ERR_CUDA;
+}
+
+}  // namespace
+
+namespace us {
+
+bool attn_tc_serves(const UsAttnParams& p) { return (int64_t)p.a.max_n * p.G > 16; }
+
+size_t attn_tc_ws(const UsAttnParams& p) {
+    return 4096 + (size_t)2 * num_sms() * (2 * kRows + kRows * p.c.D) * 4;
+}
+
+us_status launch_attn_tc(const UsAttnParams& p, cudaStream_t st) {
+    if (p.c.elem == US_I8) return p.c.D == 64 ? launch<US_I8, 64>(p, st) : launch<US_I8, 128>(p, st);
+    return p.c.D == 64 ? launch<US_I4, 64>(p, st) : launch<US_I4, 128>(p, st);
+}
+
+}  // namespace us

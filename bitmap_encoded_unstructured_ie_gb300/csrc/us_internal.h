@@ -93,6 +93,10 @@ us_status launch_kv_commit(const UsKvCache& c, const UsKvCall& a, const int32_t*
 // attention over the cache (us_attn.cu)
 size_t attn_ws(const UsAttnParams& p);
 us_status launch_attn(const UsAttnParams& p, cudaStream_t st);
+// ... of more than 16 rows per key head, on tcgen05 (us_attn_tc.cu)
+bool attn_tc_serves(const UsAttnParams& p);
+size_t attn_tc_ws(const UsAttnParams& p);
+us_status launch_attn_tc(const UsAttnParams& p, cudaStream_t st);
 
 // device properties of the current device (cached)
 int num_sms();

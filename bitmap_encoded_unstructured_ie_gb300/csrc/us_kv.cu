@@ -60,7 +60,7 @@ kv_write_kernel(const UsKvCache c, const UsKvCall a, const uint16_t* __restrict_
     us::pdl_wait();
     const int b = blockIdx.y;
     int row0;
-    const int n = us::kv_rows(c, a, b, row0);
+    const int n = us::kv_rows(a, b, row0, c.status);
     const int r = blockIdx.x * kRows + threadIdx.x / kLanes, j = threadIdx.x % kLanes;
     const int i = r / c.Hkv, h = r - i * c.Hkv;
     const bool in = i < n;
@@ -111,7 +111,7 @@ kv_read_kernel(const UsKvCache c, const UsKvCall a, uint16_t* __restrict__ K, in
     us::pdl_wait();
     const int b = blockIdx.y;
     int row0;
-    const int n = us::kv_rows(c, a, b, row0);
+    const int n = us::kv_rows(a, b, row0, c.status);
     const int r = blockIdx.x * kRows + threadIdx.x / kLanes, j = threadIdx.x % kLanes;
     const int i = r / c.Hkv, h = r - i * c.Hkv;
     if (i < n) {
@@ -136,7 +136,7 @@ kv_commit_kernel(const UsKvCache c, const UsKvCall a, const int32_t* __restrict_
     us::pdl_wait();
     const int h = blockIdx.x, b = blockIdx.y;
     int row0;
-    const int n = us::kv_rows(c, a, b, row0), chunks = c.row_bytes / 16;
+    const int n = us::kv_rows(a, b, row0, c.status), chunks = c.row_bytes / 16;
     uint32_t* held_s = reinterpret_cast<uint32_t*>(held + (size_t)a.max_n * 2 * c.row_bytes);
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const int p0 = a.pos[b], d = acc[row0 + i];

@@ -43,11 +43,11 @@ struct UsAttnParams {
 namespace us {
 
 // Rows of request b: first row and count (0 if the offsets are not usable).
-US_DEV int kv_rows(const UsKvCache& c, const UsKvCall& a, int b, int& row0) {
+US_DEV int kv_rows(const UsKvCall& a, int b, int& row0, unsigned* status) {
     const int o0 = a.off[b], o1 = a.off[b + 1];
     row0 = o0;
     if (o0 >= 0 && o1 >= o0 && o1 <= a.T && o1 - o0 <= a.max_n) return o1 - o0;
-    set_status(c.status, US_ERR_INVALID_ARG);
+    set_status(status, US_ERR_INVALID_ARG);
     return 0;
 }
 
@@ -72,12 +72,10 @@ US_DEV int64_t kv_entry(const UsKvCache& c, int id, int h, int p) {
 // base + i for positions: wraps negative instead of overflowing (kv_page refuses it)
 US_DEV int kv_pos(int base, int i) { return (int)((unsigned)base + (unsigned)i); }
 
-// Context length of request b with n tokens behind it, or -1 (recorded) if
-// the page table's row cannot hold them.
-US_DEV int kv_context(const UsKvCache& c, const UsKvCall& a, int b, int n) {
-    const int ctx = a.pos[b];
+// ctx if the page table's row can hold n positions behind it, else -1 (recorded).
+US_DEV int kv_context(const UsKvCache& c, int ctx, int n, unsigned* status) {
     if (ctx >= 0 && ctx <= ((int64_t)c.max_pages << c.page_shift) - n) return ctx;
-    set_status(c.status, US_ERR_INVALID_ARG);
+    set_status(status, US_ERR_INVALID_ARG);
     return -1;
 }
 
