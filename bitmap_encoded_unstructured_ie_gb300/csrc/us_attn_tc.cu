@@ -45,8 +45,17 @@ struct Header {
     float xr[2][kRows], xl[2][kRows];             // the streams' references and sums
     uint32_t tmem;
     unsigned last;
+    int parts;
     Part part[2];
 };
+
+struct Yes {
+    constexpr bool operator()() const { return true; }
+};
+struct No {
+    constexpr bool operator()() const { return false; }
+};
+constexpr int kNoPage = -0x7fffffff - 1;          // nothing to read (any other bad number is recorded)
 
 template <int ELEM, int D>
 struct Shape {
@@ -180,98 +189,31 @@ attn_tc_kernel(const UsAttnParams p) {
         if (!failed && !us::mbar_wait(bar, (uint32_t)use & 1u, p.c.status)) failed = true;
     };
 
-    // ---- converters: where a warp's 16 positions of a tile are
-    struct Where {
-        int page, pos, h;
-        bool want;
-    };
-    Cur ahead = cur;                                       // two tiles ahead of the conversion
-    int found = 0;                                         // tiles whose page numbers were loaded
-    auto locate = [&]() {
-        Where w = {-1, 0, 0, false};
-        if (found < count) {
-            if (found) ahead.next(p);
-            ++found;
-            w.pos = ahead.tile * kTile + (warp - kSoftWarps) * 16;
-            w.h = ahead.h;
-            w.want = w.pos < ahead.r.ctx + ahead.r.n;
-            if (w.want) w.page = p.c.table[(int64_t)ahead.b * p.c.max_pages + (w.pos >> p.c.page_shift)];
-        }
-        return w;
-    };
-    uint4 kreg[Sh::kLoads], vreg[Sh::kLoads];
-    uint32_t sreg = 0;
-    int npos = 0;                                          // the 16 positions: 16 or none
-    auto row_chunk = [&](int u, int& row, int& chunk) {    // eight lanes on eight rows: no bank conflicts
-        if constexpr (Sh::kC == 2) row = lane & 15, chunk = lane >> 4;
-        else row = 8 * (u / (Sh::kC / 4)) + (lane & 7), chunk = 4 * (u % (Sh::kC / 4)) + (lane >> 3);
-    };
-    auto fetch = [&](const Where& w, const uint8_t* pool, uint4 (&reg)[Sh::kLoads]) {
-        const bool ok = w.want && w.page >= 0 && w.page < p.c.num_pages;
-        if (ok) {
-            const uint8_t* src = pool + us::kv_entry(p.c, w.page, w.h, w.pos) * Sh::kRow;
+    if (warp < kSoftWarps) {
+        // ----------------------------------------------------------- softmax
+        const int st = warp >> 2, row = threadIdx.x & (kRows - 1);
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+        const uint32_t s_tm = tmem + lanes + st * 128, o_tm = tmem + lanes + 256 + st * 128;
+        const bool leads = (warp & 3) == 0 && lane == 0;   // issues the stream's MMAs
+        int parts = 0;
+        for (int it = 0; it < count;) {
+            // ---- a segment, or this CTA's part of it: tiles it .. end - 1
+            const int end = min(count, it + cur.tiles - cur.tile), tile0 = cur.tile;
+            const int rows = min(kRows, cur.r.n * G - cur.rb * kRows);
 #pragma unroll
-            for (int u = 0; u < Sh::kLoads; ++u) {
-                int row, chunk;
-                row_chunk(u, row, chunk);
-                reg[u] = __ldcg(reinterpret_cast<const uint4*>(src + row * Sh::kRow) + chunk);
+            for (int x = threadIdx.x; x < kRows * (D / 8); x += 32 * kSoftWarps) {
+                const int r = x / (D / 8), chunk = x % (D / 8), rr = cur.rb * kRows + r, i = rr / G;
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (r < rows)
+                    u = *reinterpret_cast<const uint4*>(p.Q + (int64_t)(cur.r.row0 + i) * p.ldq + (int64_t)(cur.h * G + rr - i * G) * D + 8 * chunk);
+                *reinterpret_cast<uint4*>(operand_at(q_sm, r, chunk)) = reorder<ELEM>(u);
             }
-        } else {
-#pragma unroll
-            for (int u = 0; u < Sh::kLoads; ++u) reg[u] = make_uint4(0, 0, 0, 0);
-        }
-        return ok;
-    };
-    auto fetch_k = [&](const Where& w) {
-        const bool ok = fetch(w, p.c.k, kreg);
-        if (w.want && !ok) us::set_status(p.c.status, US_ERR_CORRUPT);
-        npos = ok ? 16 : 0;
-        sreg = ok && lane < 16 ? __ldcg(reinterpret_cast<const uint32_t*>(p.c.scale) + us::kv_entry(p.c, w.page, w.h, w.pos) + lane) : 0u;
-    };
-    auto put = [&](uint8_t* operand, const uint4 (&reg)[Sh::kLoads]) {
-#pragma unroll
-        for (int u = 0; u < Sh::kLoads; ++u) {
-            int row, chunk;
-            row_chunk(u, row, chunk);
-            uint4 out[Sh::kOut];
-            convert<ELEM>(reg[u], out);
-#pragma unroll
-            for (int k = 0; k < Sh::kOut; ++k)
-                *reinterpret_cast<uint4*>(operand_at(operand, (warp - kSoftWarps) * 16 + row, chunk * Sh::kOut + k)) = out[k];
-        }
-    };
-    Where now = {-1, 0, 0, false}, next = now;
-    if (warp >= kSoftWarps) {
-        now = locate();
-        next = locate();
-        fetch_k(now);
-        fetch(now, p.c.v, vreg);
-    }
-
-    int parts = 0;
-    for (int it = 0; it < count;) {
-        // ---- a segment, or this CTA's part of it: tiles it .. end - 1
-        const int end = min(count, it + cur.tiles - cur.tile), tile0 = cur.tile;
-        const int rows = min(kRows, cur.r.n * G - cur.rb * kRows);
-        for (int x = threadIdx.x; x < kRows * (D / 8); x += kThreads) {
-            const int r = x / (D / 8), chunk = x % (D / 8), rr = cur.rb * kRows + r, i = rr / G;
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (r < rows)
-                u = *reinterpret_cast<const uint4*>(p.Q + (int64_t)(cur.r.row0 + i) * p.ldq + (int64_t)(cur.h * G + rr - i * G) * D + 8 * chunk);
-            *reinterpret_cast<uint4*>(operand_at(q_sm, r, chunk)) = reorder<ELEM>(u);
-        }
-        us::fence_proxy_async_smem();
-        __syncthreads();
-
-        if (warp < kSoftWarps) {
-            // ------------------------------------------------------- softmax
-            const int st = warp >> 2, row = threadIdx.x & (kRows - 1);
-            const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
-            const uint32_t s_tm = tmem + lanes + st * 128, o_tm = tmem + lanes + 256 + st * 128;
             const bool live = (warp & 3) * 32 < rows;
             const int i_tok = (cur.rb * kRows + row) / G;
             uint64_t mask = 0;
             if (p.mask && row < rows) mask = p.mask[cur.r.row0 + i_tok] & (~0ull >> (64 - cur.r.n));
+            us::fence_proxy_async_smem();
+            us::named_bar_sync(1, 32 * kSoftWarps);
             // positions that this row sees among 32 from `base` behind the context
             auto seen32 = [&](int base) {
                 if (base <= -32) return 0xFFFFFFFFu;
@@ -285,9 +227,6 @@ attn_tc_kernel(const UsAttnParams p) {
                 }
                 return (own << lo) | (lo ? 0xFFFFFFFFu >> (32 - lo) : 0u);
             };
-            float R = -INFINITY, l = 0.f;
-            // the stream's MMAs, by one thread
-            const bool leads = (warp & 3) == 0 && lane == 0;
             auto qk = [&](int i) {
                 constexpr uint32_t id = us::umma_idesc_f16(kRows, kTile);
                 wait(&H.k_full[i % kKS], i / kKS);
@@ -312,6 +251,8 @@ attn_tc_kernel(const UsAttnParams p) {
                 us::umma_commit(&H.pv_done[st]);
                 us::umma_commit(&H.v_free[i % kVS]);
             };
+            float R = -INFINITY;
+            uint64_t l2 = 0;                               // two partial sums
             const int i0 = it + ((it ^ st) & 1);
             if (leads && i0 < end) qk(i0);
             __syncwarp();
@@ -325,22 +266,73 @@ attn_tc_kernel(const UsAttnParams p) {
                     const float4* sv4 = reinterpret_cast<const float4*>(H.sv[ss]);
                     const uint4 ok = *reinterpret_cast<const uint4*>(H.valid[ss]);
                     const int base = (tile0 + i - it) * kTile - cur.r.ctx;
-                    const bool edge = base + kTile > 0 || (ok.x & ok.y & ok.z & ok.w) != 0xFFFFFFFFu;
                     const uint32_t okw[4] = {ok.x, ok.y, ok.z, ok.w};
-                    float mx = -INFINITY;
+                    // the largest score
+                    auto largest = [&](auto edge) {
+                        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        us::tmem_ld32(s_tm + 32 * c, v);
-                        const uint32_t seen = edge ? seen32(base + 32 * c) & okw[c] : 0xFFFFFFFFu;
+                        for (int c = 0; c < 4; ++c) {
+                            float v[32];
+                            us::tmem_ld32(s_tm + 32 * c, v);
+                            const uint32_t seen = edge() ? seen32(base + 32 * c) & okw[c] : 0u;
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 k = ks4[8 * c + j / 4];
-                            float x[4] = {v[j] * k.x, v[j + 1] * k.y, v[j + 2] * k.z, v[j + 3] * k.w};
+                            for (int j = 0; j < 32; j += 4) {
+                                const float4 k = ks4[8 * c + j / 4];
+                                float x[4];
+                                unpair(mul2(pair(v[j], v[j + 1]), pair(k.x, k.y)), x[0], x[1]);
+                                unpair(mul2(pair(v[j + 2], v[j + 3]), pair(k.z, k.w)), x[2], x[3]);
+                                if constexpr (edge()) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, !edge || (seen >> (j + e)) & 1u ? x[e] : -INFINITY);
+                                    for (int e = 0; e < 4; ++e)
+                                        if (!((seen >> (j + e)) & 1u)) x[e] = -INFINITY;
+                                }
+                                mx[0] = max3(mx[0], x[0], x[1]);
+                                mx[1] = max3(mx[1], x[2], x[3]);
+                            }
                         }
-                    }
+                        return fmaxf(mx[0], mx[1]);
+                    };
+                    // the weights, with V's scales as fp16 over the scores that were read
+                    auto weights = [&](auto edge) {
+                        const float ref = R == -INFINITY ? 0.f : R;
+                        const uint64_t neg = pair(-ref, -ref);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            float v[32];
+                            uint32_t u[16];
+                            us::tmem_ld32(s_tm + 32 * c, v);
+                            const uint32_t seen = edge() ? seen32(base + 32 * c) & okw[c] : 0u;
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                const float4 k = ks4[8 * c + j / 4], s = sv4[8 * c + j / 4];
+                                float w[4], x[4];
+                                unpair(fma2(pair(v[j], v[j + 1]), pair(k.x, k.y), neg), w[0], w[1]);
+                                unpair(fma2(pair(v[j + 2], v[j + 3]), pair(k.z, k.w), neg), w[2], w[3]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) w[e] = ex2(w[e]);
+                                if constexpr (edge()) {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (!((seen >> (j + e)) & 1u)) w[e] = 0.f;
+                                }
+                                const uint64_t w01 = pair(w[0], w[1]), w23 = pair(w[2], w[3]);
+                                l2 = add2(l2, add2(w01, w23));
+                                unpair(mul2(w01, pair(s.x, s.y)), x[0], x[1]);
+                                unpair(mul2(w23, pair(s.z, s.w)), x[2], x[3]);
+                                if constexpr (edge()) {    // an unseen entry's scale may be anything
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (!((seen >> (j + e)) & 1u)) x[e] = 0.f;
+                                }
+                                u[j / 2] = pack_half2(x[0], x[1]);
+                                u[j / 2 + 1] = pack_half2(x[2], x[3]);
+                            }
+                            us::tmem_st16(s_tm + 16 * c, u);
+                        }
+                        us::tmem_wait_st();
+                    };
+                    const bool edge = base + kTile > 0 || (ok.x & ok.y & ok.z & ok.w) != 0xFFFFFFFFu;
+                    const float mx = edge ? largest(Yes()) : largest(No());
                     float vm = H.svmax[ss][0];
 #pragma unroll
                     for (int w = 1; w < kConvWarps; ++w) vm = fmaxf(vm, H.svmax[ss][w]);
@@ -351,7 +343,7 @@ attn_tc_kernel(const UsAttnParams p) {
                         const float to = move ? mx + lv - kTop : R;
                         const float f = move ? ex2(R - to) : 1.f;
                         R = to;
-                        l *= f;
+                        l2 = mul2(l2, pair(f, f));
                         if (i - it >= 2) {                 // the stream has outputs: PV of its last tile first
                             wait(&H.pv_done[st], i / 2 - 1);
                             us::tc_fence_after();
@@ -367,31 +359,8 @@ attn_tc_kernel(const UsAttnParams p) {
                             us::tmem_wait_st();
                         }
                     }
-                    const float ref = R == -INFINITY ? 0.f : R;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        uint32_t u[16];
-                        us::tmem_ld32(s_tm + 32 * c, v);
-                        const uint32_t seen = edge ? seen32(base + 32 * c) & okw[c] : 0xFFFFFFFFu;
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 k = ks4[8 * c + j / 4], s = sv4[8 * c + j / 4];
-                            float w[4] = {ex2(fmaf(v[j], k.x, -ref)), ex2(fmaf(v[j + 1], k.y, -ref)),
-                                          ex2(fmaf(v[j + 2], k.z, -ref)), ex2(fmaf(v[j + 3], k.w, -ref))};
-                            float x[4] = {w[0] * s.x, w[1] * s.y, w[2] * s.z, w[3] * s.w};
-                            if (edge) {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (!((seen >> (j + e)) & 1u)) w[e] = x[e] = 0.f;
-                            }
-                            l += (w[0] + w[1]) + (w[2] + w[3]);
-                            u[j / 2] = pack_half2(x[0], x[1]);
-                            u[j / 2 + 1] = pack_half2(x[2], x[3]);
-                        }
-                        us::tmem_st16(s_tm + 16 * c, u);   // over scores that were read
-                    }
-                    us::tmem_wait_st();
+                    if (edge) weights(Yes());
+                    else weights(No());
                 }
                 us::tc_fence_before();
                 us::named_bar_sync(2 + st, 128);
@@ -404,7 +373,9 @@ attn_tc_kernel(const UsAttnParams p) {
             }
             // ---- the segment's end: both streams' sums and outputs
             const bool has[2] = {end - it >= 2 || !(it & 1), end - it >= 2 || (it & 1)};
-            H.xr[st][row] = R, H.xl[st][row] = l;
+            float la, lb;
+            unpair(l2, la, lb);
+            H.xr[st][row] = R, H.xl[st][row] = la + lb;
             wait(&H.pv_done[(end - 1) & 1], (end - 1) / 2);
             if (end - it >= 2) wait(&H.pv_done[end & 1], (end - 2) / 2);
             us::named_bar_sync(1, 32 * kSoftWarps);
@@ -444,49 +415,105 @@ attn_tc_kernel(const UsAttnParams p) {
                     }
                 }
             }
-            us::tc_fence_before();
             if (!whole) {
                 if (threadIdx.x == 0) H.part[parts] = part;
+                ++parts;
             }
-        } else {
-            // ---------------------------------------------------- conversion
-            for (int i = it; i < end; ++i) {
-                const int w = warp - kSoftWarps, ss = i % kSS;
-                const Where w2 = locate();                 // tile i + 2
-                if (i >= kKS) wait(&H.qk_done[i % kKS], i / kKS - 1);
-                put(k_sm + (i % kKS) * Sh::kOperand, kreg);
-                const float sk = us::half_bits_to_float((uint16_t)sreg) * (p.scale * 1.4426950408889634f), sv = us::half_bits_to_float((uint16_t)(sreg >> 16));
-                float vm = fabsf(sv) < INFINITY ? fabsf(sv) : 0.f;     // entries that no row sees may hold anything
-                {
-                    const int left = cur.r.ctx + cur.r.n - ((tile0 + i - it) * kTile + 16 * w);
-                    if (lane >= left) vm = 0.f;
-                }
+            us::tc_fence_before();
+            us::named_bar_sync(1, 32 * kSoftWarps);        // Q, the streams' TMEM and sums are free
+            us::tc_fence_after();
+            it = end;
+            if (it < count) cur.next_segment(p);
+        }
+        if (threadIdx.x == 0) H.parts = parts;
+    } else {
+        // -------------------------------------------------------- conversion
+        // Tile after tile, across segments.  The 16 positions of this warp: their
+        // page number is loaded two tiles ahead, their codes one tile ahead.
+        const int cw = warp - kSoftWarps;
+        struct Where {
+            int page, pos, h, left;                        // left: positions up to the last of the request
+        };
+        int found = 0;
+        auto locate = [&]() {
+            Where w = {kNoPage, 0, 0, 0};
+            if (found < count) {
+                if (found) cur.next(p);
+                ++found;
+                w.pos = cur.tile * kTile + cw * 16;
+                w.h = cur.h;
+                w.left = cur.r.ctx + cur.r.n - w.pos;
+                if (w.left > 0) w.page = p.c.table[(int64_t)cur.b * p.c.max_pages + (w.pos >> p.c.page_shift)];
+            }
+            return w;
+        };
+        uint4 kreg[Sh::kLoads], vreg[Sh::kLoads];
+        uint32_t sreg = 0;
+        auto row_chunk = [&](int u, int& r, int& chunk) {  // eight lanes on eight rows: no bank conflicts
+            if constexpr (Sh::kC == 2) r = lane & 15, chunk = lane >> 4;
+            else r = 8 * (u / (Sh::kC / 4)) + (lane & 7), chunk = 4 * (u % (Sh::kC / 4)) + (lane >> 3);
+        };
+        auto exists = [&](const Where& w) { return w.page >= 0 && w.page < p.c.num_pages; };
+        auto fetch = [&](const Where& w, const uint8_t* pool, uint4 (&reg)[Sh::kLoads]) {
+            const bool ok = exists(w);
+            const uint8_t* src = pool + us::kv_entry(p.c, w.page, w.h, w.pos) * Sh::kRow;
 #pragma unroll
-                for (int d = 1; d < 16; d <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
-                if (lane < 16) H.ks[ss][16 * w + lane] = sk, H.sv[ss][16 * w + lane] = sv;
-                if (lane == 0) H.svmax[ss][w] = vm, H.valid[ss][w] = npos ? 0xFFFFu : 0u;
-                us::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) us::mbar_arrive(&H.k_full[i % kKS]), us::mbar_arrive(&H.s_full[ss]);
-                fetch_k(next);
-                if (i >= kVS) wait(&H.v_free[i % kVS], i / kVS - 1);
-                put(v_sm + (i % kVS) * Sh::kOperand, vreg);
-                us::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) us::mbar_arrive(&H.v_full[i % kVS]);
-                fetch(next, p.c.v, vreg);
-                next = w2;
+            for (int u = 0; u < Sh::kLoads; ++u) {
+                int r, chunk;
+                row_chunk(u, r, chunk);
+                reg[u] = ok ? __ldcg(reinterpret_cast<const uint4*>(src + r * Sh::kRow) + chunk) : make_uint4(0, 0, 0, 0);
             }
+        };
+        auto fetch_k = [&](const Where& w) {
+            fetch(w, p.c.k, kreg);
+            if (w.page != kNoPage && !exists(w)) us::set_status(p.c.status, US_ERR_CORRUPT);
+            sreg = exists(w) && lane < 16
+                       ? __ldcg(reinterpret_cast<const uint32_t*>(p.c.scale) + us::kv_entry(p.c, w.page, w.h, w.pos) + lane) : 0u;
+        };
+        auto put = [&](uint8_t* operand, const uint4 (&reg)[Sh::kLoads]) {
+#pragma unroll
+            for (int u = 0; u < Sh::kLoads; ++u) {
+                int r, chunk;
+                row_chunk(u, r, chunk);
+                uint4 out[Sh::kOut];
+                convert<ELEM>(reg[u], out);
+#pragma unroll
+                for (int k = 0; k < Sh::kOut; ++k)
+                    *reinterpret_cast<uint4*>(operand_at(operand, cw * 16 + r, chunk * Sh::kOut + k)) = out[k];
+            }
+        };
+        Where now = locate(), next = locate();
+        fetch_k(now);
+        fetch(now, p.c.v, vreg);
+        for (int i = 0; i < count; ++i) {
+            const int ss = i % kSS;
+            const Where after = locate();
+            if (i >= kKS) wait(&H.qk_done[i % kKS], i / kKS - 1);
+            put(k_sm + (i % kKS) * Sh::kOperand, kreg);
+            const float sk = us::half_bits_to_float((uint16_t)sreg) * (p.scale * 1.4426950408889634f);
+            const float sv = us::half_bits_to_float((uint16_t)(sreg >> 16));
+            // entries that no row sees may hold anything: only the request's finite scales count
+            float vm = lane < now.left && fabsf(sv) < INFINITY ? fabsf(sv) : 0.f;
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
+            if (lane < 16) H.ks[ss][16 * cw + lane] = sk, H.sv[ss][16 * cw + lane] = sv;
+            if (lane == 0) H.svmax[ss][cw] = vm, H.valid[ss][cw] = exists(now) ? 0xFFFFu : 0u;
+            us::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) us::mbar_arrive(&H.k_full[i % kKS]), us::mbar_arrive(&H.s_full[ss]);
+            fetch_k(next);
+            if (i >= kVS) wait(&H.v_free[i % kVS], i / kVS - 1);
+            put(v_sm + (i % kVS) * Sh::kOperand, vreg);
+            us::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) us::mbar_arrive(&H.v_full[i % kVS]);
+            fetch(next, p.c.v, vreg);
+            now = next;
+            next = after;
         }
-        {
-            const int64_t s0 = wk.t0 + it - tile0;
-            if (wk.sharers(s0, s0 + cur.tiles, cur, rows).first != wk.sharers(s0, s0 + cur.tiles, cur, rows).last) ++parts;
-        }
-        __syncthreads();                                   // Q, the streams and their TMEM are free
-        us::tc_fence_after();
-        for (; it < end; ++it)
-            if (it + 1 < count) cur.next(p);
     }
+    __syncthreads();
+    const int parts = any ? H.parts : 0;
 
     // ---- shared segments (at most two a CTA): the last CTA to arrive joins them
     for (int i = 0; i < parts; ++i) {
