@@ -6,22 +6,29 @@
 // are spread evenly over the CTAs (one an SM):
 //   S = Q Ck^T    A = Q (shared memory), B = the tile's K codes as fp16
 //   O += P Cv     A = P (TMEM, fp16), B = the tile's V codes as fp16, MN-major
-// with K's scale on the scores and V's scale in the weights P.  The dimensions
-// stand in shared memory in the order in which the codes leave their words
-// (within each eight), the same for Q, K and V; only the outputs are put back.
+// K enters as its codes, its scale on the scores in fp32.  V enters as fp16(code *
+// scale), the values that us_kv_read returns: one more rounding of 2^-11 of a value,
+// against a register's worth of shared memory traffic per score for a scale in the
+// weights.  The dimensions stand in shared memory in the order in which the codes
+// leave their words (within each eight), the same for Q, K and V; only the outputs
+// are put back.
 //
 // Tiles alternate between two streams, each with its own scores, outputs, row
 // references and softmax warps, so that the tensor cores work on one stream while
 // the other's weights are made; the streams are joined at the segment's end.
-//   warps 0-3, 4-7: softmax of stream 0 / 1, one thread a row; one of them issues
-//               the stream's MMAs: PV of this tile, then QK of the stream's next
+//   warps 0-3, 4-7: softmax of stream 0 / 1, 32 rows each, 16 at a time, in the
+//               fragment order of 16-lane TMEM loads: a lane has a quarter of the
+//               columns, so it reads a quarter of the scales (what bounds these warps
+//               is the load / store pipe: every register that comes from TMEM or
+//               shared memory takes a cycle of it a warp).  One of them issues the
+//               stream's MMAs: PV of this tile, then QK of the stream's next
 //   warps 8-15: codes -> fp16, 16 positions each; the next tile's codes are in
 //               their registers while this one's are converted
 // 16 warps: a thread may have 128 registers (17 would leave 96).
-// A row's reference R stands for its maximum and for the size of V's scales at
-// once: weights are w = 2^(s - R), the row sum adds w, P holds w s_v as fp16, and R
-// moves only when some w s_v could pass 2^15.  R, sums and outputs of a segment
-// shared by several CTAs are joined by the last of them to arrive.
+// Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set,
+// and moves only when a weight could pass 2^15 (fp16 keeps 2^-14 of them exactly as
+// it does the largest).  R, sums and outputs of a segment shared by several CTAs are
+// joined by the last of them to arrive.
 #include "us_attn.cuh"
 #include "us_internal.h"
 #include "us_tcgen05.cuh"
@@ -34,13 +41,12 @@ constexpr int kRows = 128, kTile = 128;           // query rows of a segment, po
 constexpr int kSoftWarps = 8, kConvWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + kConvWarps);
 constexpr int kKS = 2, kVS = 3, kSS = 4;          // stages: K, V, scales
-constexpr float kTop = 11.f, kLag = 4.f;          // a row's largest w s_v is 2^11 at first, 2^15 at most
+constexpr float kTop = 11.f, kLag = 4.f;          // a row's largest weight is 2^11 at first, 2^15 at most
 
 struct Header {
     uint64_t k_full[kKS], v_full[kVS], s_full[kSS];
     uint64_t qk_done[2], pv_done[2], v_free[kVS];  // v_free: the same event as pv_done, by stage
-    float ks[kSS][kTile], sv[kSS][kTile];         // scales of the tiles on their way: K's times scale log2(e), V's
-    float svmax[kSS][kConvWarps];
+    float ks[kSS][kTile];                         // K's scales times scale log2(e) of the tiles on their way
     uint16_t valid[kSS][kConvWarps];              // which of a warp's 16 positions exist
     float xr[2][kRows], xl[2][kRows];             // the streams' references and sums
     uint32_t tmem;
@@ -49,12 +55,6 @@ struct Header {
     Part part[2];
 };
 
-struct Yes {
-    constexpr bool operator()() const { return true; }
-};
-struct No {
-    constexpr bool operator()() const { return false; }
-};
 constexpr int kNoPage = -0x7fffffff - 1;          // nothing to read (any other bad number is recorded)
 
 template <int ELEM, int D>
@@ -191,8 +191,9 @@ attn_tc_kernel(const UsAttnParams p) {
 
     if (warp < kSoftWarps) {
         // ----------------------------------------------------------- softmax
-        const int st = warp >> 2, row = threadIdx.x & (kRows - 1);
-        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+        const int st = warp >> 2, g = lane >> 2, c2 = 2 * (lane & 3);
+        const int row = threadIdx.x & (kRows - 1), wrow = (warp & 3) * 32;
+        const uint32_t lanes = (uint32_t)wrow << 16;
         const uint32_t s_tm = tmem + lanes + st * 128, o_tm = tmem + lanes + 256 + st * 128;
         const bool leads = (warp & 3) == 0 && lane == 0;   // issues the stream's MMAs
         int parts = 0;
@@ -208,21 +209,28 @@ attn_tc_kernel(const UsAttnParams p) {
                     u = *reinterpret_cast<const uint4*>(p.Q + (int64_t)(cur.r.row0 + i) * p.ldq + (int64_t)(cur.h * G + rr - i * G) * D + 8 * chunk);
                 *reinterpret_cast<uint4*>(operand_at(q_sm, r, chunk)) = reorder<ELEM>(u);
             }
-            const bool live = (warp & 3) * 32 < rows;
-            const int i_tok = (cur.rb * kRows + row) / G;
-            uint64_t mask = 0;
-            if (p.mask && row < rows) mask = p.mask[cur.r.row0 + i_tok] & (~0ull >> (64 - cur.r.n));
+            // the lane's four rows: wrow + 16 h + 8 u + g
+            uint64_t mask[2][2];
+            int own_n[2][2];                               // a chain's row: tokens of the call that it sees
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int r = wrow + 16 * h + 8 * u + g, i = (cur.rb * kRows + r) / G;
+                    mask[h][u] = p.mask && r < rows ? p.mask[cur.r.row0 + i] & (~0ull >> (64 - cur.r.n)) : 0ull;
+                    own_n[h][u] = r < rows ? i + 1 : 0;
+                }
             us::fence_proxy_async_smem();
             us::named_bar_sync(1, 32 * kSoftWarps);
-            // positions that this row sees among 32 from `base` behind the context
-            auto seen32 = [&](int base) {
+            // positions that a row sees among 32 from `base` behind the context
+            auto seen32 = [&](int base, uint64_t tree, int chain) {
                 if (base <= -32) return 0xFFFFFFFFu;
                 const int lo = base < 0 ? -base : 0;       // context positions among them
                 uint32_t own;
                 if (p.mask) {
-                    own = base < 64 ? (uint32_t)(mask >> (base > 0 ? base : 0)) : 0u;
+                    own = base < 64 ? (uint32_t)(tree >> (base > 0 ? base : 0)) : 0u;
                 } else {
-                    const int k = (row < rows ? i_tok : -1) + 1 - (base > 0 ? base : 0);
+                    const int k = chain - (base > 0 ? base : 0);
                     own = k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u;
                 }
                 return (own << lo) | (lo ? 0xFFFFFFFFu >> (32 - lo) : 0u);
@@ -251,8 +259,8 @@ attn_tc_kernel(const UsAttnParams p) {
                 us::umma_commit(&H.pv_done[st]);
                 us::umma_commit(&H.v_free[i % kVS]);
             };
-            float R = -INFINITY;
-            uint64_t l2 = 0;                               // two partial sums
+            float R[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+            uint64_t l2[2][2] = {};                        // two partial sums each
             const int i0 = it + ((it ^ st) & 1);
             if (leads && i0 < end) qk(i0);
             __syncwarp();
@@ -261,107 +269,91 @@ attn_tc_kernel(const UsAttnParams p) {
                 wait(&H.s_full[ss], i / kSS);
                 wait(&H.qk_done[st], i / 2);
                 us::tc_fence_after();
-                if (live) {
-                    const float4* ks4 = reinterpret_cast<const float4*>(H.ks[ss]);
-                    const float4* sv4 = reinterpret_cast<const float4*>(H.sv[ss]);
-                    const uint4 ok = *reinterpret_cast<const uint4*>(H.valid[ss]);
-                    const int base = (tile0 + i - it) * kTile - cur.r.ctx;
-                    const uint32_t okw[4] = {ok.x, ok.y, ok.z, ok.w};
-                    // the largest score
-                    auto largest = [&](auto edge) {
-                        float mx[2] = {-INFINITY, -INFINITY};
+                const float2* ks2 = reinterpret_cast<const float2*>(H.ks[ss]) + (lane & 3);
+                const uint4 ok = *reinterpret_cast<const uint4*>(H.valid[ss]);
+                const int base = (tile0 + i - it) * kTile - cur.r.ctx;
+                const bool edge = base + kTile > 0 || (ok.x & ok.y & ok.z & ok.w) != 0xFFFFFFFFu;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            float v[32];
-                            us::tmem_ld32(s_tm + 32 * c, v);
-                            const uint32_t seen = edge() ? seen32(base + 32 * c) & okw[c] : 0u;
+                for (int h = 0; h < 2; ++h) {
+                    if (wrow + 16 * h >= rows) continue;
+                    const uint32_t half = (uint32_t)(16 * h) << 16;
+                    float v[64];
+                    us::tmem_ld_frag128(s_tm + half, v);
+                    // scores and their maxima
+                    float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 k = ks4[8 * c + j / 4];
-                                float x[4];
-                                unpair(mul2(pair(v[j], v[j + 1]), pair(k.x, k.y)), x[0], x[1]);
-                                unpair(mul2(pair(v[j + 2], v[j + 3]), pair(k.z, k.w)), x[2], x[3]);
-                                if constexpr (edge()) {
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 sk = ks2[4 * k];
+                        const uint64_t s = pair(sk.x, sk.y);
+                        unpair(mul2(pair(v[4 * k], v[4 * k + 1]), s), v[4 * k], v[4 * k + 1]);
+                        unpair(mul2(pair(v[4 * k + 2], v[4 * k + 3]), s), v[4 * k + 2], v[4 * k + 3]);
+                    }
+                    if (edge) {
+                        const uint32_t okw[4] = {ok.x, ok.y, ok.z, ok.w};
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (!((seen >> (j + e)) & 1u)) x[e] = -INFINITY;
-                                }
-                                mx[0] = max3(mx[0], x[0], x[1]);
-                                mx[1] = max3(mx[1], x[2], x[3]);
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t seen = (seen32(base + 32 * c, mask[h][u], own_n[h][u]) & okw[c]) >> c2;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        if (!((seen >> (8 * k + e)) & 1u)) v[4 * (4 * c + k) + 2 * u + e] = -INFINITY;
                             }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        mx[0] = max3(mx[0], v[4 * k], v[4 * k + 1]);
+                        mx[1] = max3(mx[1], v[4 * k + 2], v[4 * k + 3]);
+                    }
+                    if (__any_sync(0xffffffffu, mx[0] > R[h][0] + (kTop + kLag) || mx[1] > R[h][1] + (kTop + kLag))) {
+                        float f[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            float x = mx[u];
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                            const float to = x > R[h][u] + (kTop + kLag) ? x - kTop : R[h][u];
+                            f[u] = to == R[h][u] ? 1.f : ex2(R[h][u] - to);
+                            R[h][u] = to;
+                            l2[h][u] = mul2(l2[h][u], pair(f[u], f[u]));
                         }
-                        return fmaxf(mx[0], mx[1]);
-                    };
-                    // the weights, with V's scales as fp16 over the scores that were read
-                    auto weights = [&](auto edge) {
-                        const float ref = R == -INFINITY ? 0.f : R;
-                        const uint64_t neg = pair(-ref, -ref);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            float v[32];
-                            uint32_t u[16];
-                            us::tmem_ld32(s_tm + 32 * c, v);
-                            const uint32_t seen = edge() ? seen32(base + 32 * c) & okw[c] : 0u;
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 k = ks4[8 * c + j / 4], s = sv4[8 * c + j / 4];
-                                float w[4], x[4];
-                                unpair(fma2(pair(v[j], v[j + 1]), pair(k.x, k.y), neg), w[0], w[1]);
-                                unpair(fma2(pair(v[j + 2], v[j + 3]), pair(k.z, k.w), neg), w[2], w[3]);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) w[e] = ex2(w[e]);
-                                if constexpr (edge()) {
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (!((seen >> (j + e)) & 1u)) w[e] = 0.f;
-                                }
-                                const uint64_t w01 = pair(w[0], w[1]), w23 = pair(w[2], w[3]);
-                                l2 = add2(l2, add2(w01, w23));
-                                unpair(mul2(w01, pair(s.x, s.y)), x[0], x[1]);
-                                unpair(mul2(w23, pair(s.z, s.w)), x[2], x[3]);
-                                if constexpr (edge()) {    // an unseen entry's scale may be anything
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (!((seen >> (j + e)) & 1u)) x[e] = 0.f;
-                                }
-                                u[j / 2] = pack_half2(x[0], x[1]);
-                                u[j / 2 + 1] = pack_half2(x[2], x[3]);
-                            }
-                            us::tmem_st16(s_tm + 16 * c, u);
-                        }
-                        us::tmem_wait_st();
-                    };
-                    const bool edge = base + kTile > 0 || (ok.x & ok.y & ok.z & ok.w) != 0xFFFFFFFFu;
-                    const float mx = edge ? largest(Yes()) : largest(No());
-                    float vm = H.svmax[ss][0];
-#pragma unroll
-                    for (int w = 1; w < kConvWarps; ++w) vm = fmaxf(vm, H.svmax[ss][w]);
-                    // log2 of the power of two above the largest scale
-                    const float lv = (float)((int)(__float_as_uint(fmaxf(vm, 5.9604645e-8f)) >> 23) - 126);
-                    const bool move = mx + lv > R + (kTop + kLag);
-                    if (__any_sync(0xffffffffu, move)) {
-                        const float to = move ? mx + lv - kTop : R;
-                        const float f = move ? ex2(R - to) : 1.f;
-                        R = to;
-                        l2 = mul2(l2, pair(f, f));
                         if (i - it >= 2) {                 // the stream has outputs: PV of its last tile first
                             wait(&H.pv_done[st], i / 2 - 1);
                             us::tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                float v[16];
-                                uint32_t u[16];
-                                us::tmem_ld16(o_tm + c, v);
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t w[16];
+                                us::tmem_ld_frag32(o_tm + half + c, w);
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(v[j] * f);
-                                us::tmem_st16(o_tm + c, u);
+                                for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * f[(j >> 1) & 1]);
+                                us::tmem_st_frag32(o_tm + half + c, w);
                             }
                             us::tmem_wait_st();
                         }
                     }
-                    if (edge) weights(Yes());
-                    else weights(No());
+                    // weights, as fp16 over the scores
+                    uint32_t w[32];
+                    uint64_t neg[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float ref = R[h][u] == -INFINITY ? 0.f : R[h][u];
+                        neg[u] = pair(-ref, -ref);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            float a, b;
+                            unpair(add2(pair(v[4 * k + 2 * u], v[4 * k + 2 * u + 1]), neg[u]), a, b);
+                            a = ex2(a), b = ex2(b);
+                            l2[h][u] = add2(l2[h][u], pair(a, b));
+                            w[2 * k + u] = pack_half2(a, b);
+                        }
+                    us::tmem_st_pairs64(s_tm + half, w);
                 }
+                us::tmem_wait_st();
                 us::tc_fence_before();
                 us::named_bar_sync(2 + st, 128);
                 if (leads) {
@@ -373,9 +365,17 @@ attn_tc_kernel(const UsAttnParams p) {
             }
             // ---- the segment's end: both streams' sums and outputs
             const bool has[2] = {end - it >= 2 || !(it & 1), end - it >= 2 || (it & 1)};
-            float la, lb;
-            unpair(l2, la, lb);
-            H.xr[st][row] = R, H.xl[st][row] = la + lb;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float a, b;
+                    unpair(l2[h][u], a, b);
+                    a += b;
+                    a += __shfl_xor_sync(0xffffffffu, a, 1);
+                    a += __shfl_xor_sync(0xffffffffu, a, 2);
+                    if (c2 == 0) H.xr[st][wrow + 16 * h + 8 * u + g] = R[h][u], H.xl[st][wrow + 16 * h + 8 * u + g] = a;
+                }
             wait(&H.pv_done[(end - 1) & 1], (end - 1) / 2);
             if (end - it >= 2) wait(&H.pv_done[end & 1], (end - 2) / 2);
             us::named_bar_sync(1, 32 * kSoftWarps);
@@ -383,7 +383,7 @@ attn_tc_kernel(const UsAttnParams p) {
             const int64_t s0 = wk.t0 + it - tile0;
             const Part part = wk.sharers(s0, s0 + cur.tiles, cur, rows);
             const bool whole = part.first == part.last;
-            if (live) {
+            if (wrow < rows) {
                 const float r0 = H.xr[0][row], r1 = H.xr[1][row], top = fmaxf(r0, r1);
                 const float f0 = r0 == -INFINITY ? 0.f : ex2(r0 - top), f1 = r1 == -INFINITY ? 0.f : ex2(r1 - top);
                 const float sum = H.xl[0][row] * f0 + H.xl[1][row] * f1, inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -470,13 +470,19 @@ attn_tc_kernel(const UsAttnParams p) {
             sreg = exists(w) && lane < 16
                        ? __ldcg(reinterpret_cast<const uint32_t*>(p.c.scale) + us::kv_entry(p.c, w.page, w.h, w.pos) + lane) : 0u;
         };
-        auto put = [&](uint8_t* operand, const uint4 (&reg)[Sh::kLoads]) {
+        auto put = [&](uint8_t* operand, const uint4 (&reg)[Sh::kLoads], const uint32_t* scale) {
 #pragma unroll
             for (int u = 0; u < Sh::kLoads; ++u) {
                 int r, chunk;
                 row_chunk(u, r, chunk);
                 uint4 out[Sh::kOut];
                 convert<ELEM>(reg[u], out);
+                if (scale) {
+                    const uint32_t s = scale[Sh::kC == 2 ? 0 : u / (Sh::kC / 4)];
+#pragma unroll
+                    for (int k = 0; k < Sh::kOut; ++k)
+                        out[k] = make_uint4(hmul2(out[k].x, s), hmul2(out[k].y, s), hmul2(out[k].z, s), hmul2(out[k].w, s));
+                }
 #pragma unroll
                 for (int k = 0; k < Sh::kOut; ++k)
                     *reinterpret_cast<uint4*>(operand_at(operand, cw * 16 + r, chunk * Sh::kOut + k)) = out[k];
@@ -489,21 +495,26 @@ attn_tc_kernel(const UsAttnParams p) {
             const int ss = i % kSS;
             const Where after = locate();
             if (i >= kKS) wait(&H.qk_done[i % kKS], i / kKS - 1);
-            put(k_sm + (i % kKS) * Sh::kOperand, kreg);
-            const float sk = us::half_bits_to_float((uint16_t)sreg) * (p.scale * 1.4426950408889634f);
-            const float sv = us::half_bits_to_float((uint16_t)(sreg >> 16));
-            // entries that no row sees may hold anything: only the request's finite scales count
-            float vm = lane < now.left && fabsf(sv) < INFINITY ? fabsf(sv) : 0.f;
+            put(k_sm + (i % kKS) * Sh::kOperand, kreg, nullptr);
+            // Entries that no row sees may hold any scale: behind the request's last
+            // position V's counts as 0, and one that is not finite is left to those
+            // who see its entry, through K's.
+            float sk = us::half_bits_to_float((uint16_t)sreg) * (p.scale * 1.4426950408889634f);
+            uint32_t sv = sreg >> 16;
+            if ((sv & 0x7C00u) == 0x7C00u) sv = 0, sk = __uint_as_float(0x7FC00000u);
+            if (lane >= now.left) sv = 0;
+            sv |= sv << 16;
+            uint32_t vscale[2];                            // of the lane's rows
 #pragma unroll
-            for (int d = 1; d < 16; d <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
-            if (lane < 16) H.ks[ss][16 * cw + lane] = sk, H.sv[ss][16 * cw + lane] = sv;
-            if (lane == 0) H.svmax[ss][cw] = vm, H.valid[ss][cw] = exists(now) ? 0xFFFFu : 0u;
+            for (int u = 0; u < 2; ++u) vscale[u] = __shfl_sync(0xffffffffu, sv, Sh::kC == 2 ? lane & 15 : 8 * u + (lane & 7));
+            if (lane < 16) H.ks[ss][16 * cw + lane] = sk;
+            if (lane == 0) H.valid[ss][cw] = exists(now) ? 0xFFFFu : 0u;
             us::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) us::mbar_arrive(&H.k_full[i % kKS]), us::mbar_arrive(&H.s_full[ss]);
             fetch_k(next);
             if (i >= kVS) wait(&H.v_free[i % kVS], i / kVS - 1);
-            put(v_sm + (i % kVS) * Sh::kOperand, vreg);
+            put(v_sm + (i % kVS) * Sh::kOperand, vreg, vscale);
             us::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) us::mbar_arrive(&H.v_full[i % kVS]);
