@@ -25,9 +25,11 @@
 //               shared memory takes a cycle of it a warp)
 //   warp 8: one thread issues the MMAs: PV of a tile, then QK of the stream's next
 //               (it is held up at the rate of their execution, 64 cycles each)
-//   warps 9-15: codes -> fp16, in items of 16 positions of K or of V; the codes of
-//               a warp's next two items are on their way to its registers
-// 16 warps: a thread may have 128 registers (17 would leave 96).
+//   warps 9-15: codes -> fp16, in items of 16 positions of K or of V; a warp's next
+//               items are on their way to its own ring, each lane's to its own place
+// 16 warps: a thread may have 128 registers (17 would leave 96).  The roles' loops
+// are kept short (one copy of each body): four warps of a scheduler run three
+// different programs, and fetching them was a sixth of its time.
 // Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set,
 // and moves only when a weight could pass 2^15 (fp16 keeps 2^-14 of them exactly as
 // it does the largest).  R, sums and outputs of a segment shared by several CTAs are
@@ -45,6 +47,7 @@ constexpr int kSoftWarps = 8, kMmaWarp = 8, kConvWarps = 7;
 constexpr int kThreads = 32 * (kSoftWarps + 1 + kConvWarps);
 constexpr int kItems = 16;                        // of a tile: 8 of K, then 8 of V
 constexpr int kKS = 2, kSS = 4;                   // stages: K, scales (V: Shape::kVS)
+constexpr int kTries = 20000;                     // of a wait, before the call gives up
 constexpr float kTop = 11.f, kLag = 4.f;          // a row's largest weight is 2^11 at first, 2^15 at most
 
 struct Header {
@@ -74,9 +77,25 @@ struct Shape {
     static constexpr int kGroup = 128 * 128;                        // one 64-dimension half of it
     static constexpr int kRows = kM * NQ;                           // query rows of a segment
     static constexpr int kVS = NQ == 2 ? 2 : 3;
-    static constexpr int kSmem = (NQ + kKS + kVS) * kOperand + (int)sizeof(Header) + 1024;
+    static constexpr int kRaw = 16 * kRow + 64;                     // codes and scales of an item
+    static constexpr int kFit = (232448 - 1024 - 512 - (NQ + kKS + kVS) * kOperand - (int)sizeof(Header)) / (kConvWarps * kRaw);
+    static constexpr int kRS = kFit > 4 ? 4 : kFit;                 // items of a warp's ring
+    static_assert(kRS >= 2, "ring");
+    static constexpr int kSmem = (NQ + kKS + kVS) * kOperand + (int)sizeof(Header) + kConvWarps * kRS * kRaw + 1024;
     static constexpr int kSlotFloats = 2 * kRows + kRows * D;
 };
+
+US_DEV void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+US_DEV void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+US_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+US_DEV void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Column j of eight -> its dimension of eight: the order in which codes leave a word.
 template <int ELEM>
@@ -174,7 +193,8 @@ attn_tc_kernel(const UsAttnParams p) {
     uint8_t* q_sm = smem;
     uint8_t* k_sm = q_sm + NQ * Sh::kOperand;
     uint8_t* v_sm = k_sm + kKS * Sh::kOperand;
-    Header& H = *reinterpret_cast<Header*>(v_sm + kVS * Sh::kOperand);
+    uint8_t* raw_sm = v_sm + kVS * Sh::kOperand;
+    Header& H = *reinterpret_cast<Header*>(raw_sm + kConvWarps * Sh::kRS * Sh::kRaw);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -198,7 +218,13 @@ attn_tc_kernel(const UsAttnParams p) {
     const int count = any ? (int)(wk.t1 - wk.t0) : 0, G = p.G;
     bool failed = false;
     auto wait = [&](uint64_t* bar, int use) {              // for the use-th completion of bar
-        if (!failed && !us::mbar_wait(bar, (uint32_t)use & 1u, p.c.status)) failed = true;
+        if (us::mbar_try_wait(bar, (uint32_t)use & 1u) || failed) return;
+        for (int n = 0; !us::mbar_try_wait_sleep(bar, (uint32_t)use & 1u, 100000u); ++n)
+            if (n == kTries) {
+                us::set_status(p.c.status, US_ERR_TIMEOUT);
+                failed = true;
+                return;
+            }
     };
 
     if (warp < kSoftWarps) {
@@ -236,8 +262,10 @@ attn_tc_kernel(const UsAttnParams p) {
                 }
                 return (own << lo) | (lo ? 0xFFFFFFFFu >> (32 - lo) : 0u);
             };
-            float R[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
-            uint64_t l2[2][2] = {};                        // two partial sums each
+            // references and sums (two partial ones each) of rows g, g + 8 of the half at
+            // hand, and of the other half: they change places after every half
+            float R[2] = {-INFINITY, -INFINITY}, Ro[2] = {-INFINITY, -INFINITY};
+            uint64_t l2[2] = {}, l2o[2] = {};
             constexpr int kStep = NQ == 2 ? 1 : 2;         // a stream's tiles: every one, or every other
             const int i0 = NQ == 2 ? it : it + ((it ^ st) & 1);
             for (int i = i0; i < end; i += kStep) {
@@ -249,89 +277,122 @@ attn_tc_kernel(const UsAttnParams p) {
                 const uint4 ok = *reinterpret_cast<const uint4*>(H.valid[ss]);
                 const int base = (tile0 + i - it) * kTile - cur.r.ctx;
                 const bool edge = base + kTile > 0 || (ok.x & ok.y & ok.z & ok.w) != 0xFFFFFFFFu;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (wrow + 16 * h >= rows) continue;
-                    const uint32_t half = (uint32_t)(16 * h) << 16;
-                    float v[64];
-                    us::tmem_ld_frag128(s_tm + half, v);
-                    // scores and their maxima
-                    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 sk = ks2[4 * k];
-                        const uint64_t s = pair(sk.x, sk.y);
-                        unpair(mul2(pair(v[4 * k], v[4 * k + 1]), s), v[4 * k], v[4 * k + 1]);
-                        unpair(mul2(pair(v[4 * k + 2], v[4 * k + 3]), s), v[4 * k + 2], v[4 * k + 3]);
-                    }
-                    if (edge) {
-                        const uint32_t okw[4] = {ok.x, ok.y, ok.z, ok.w};
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int r = wrow + 16 * h + 8 * u + g, tok = (cur.rb * kRows + r) / G;
-                            const uint64_t mask = p.mask && r < rows ? p.mask[cur.r.row0 + tok] & (~0ull >> (64 - cur.r.n)) : 0ull;
-                            const int own = r < rows ? tok + 1 : 0;        // a chain's row sees so many of the call
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint32_t seen = (seen32(base + 32 * c, mask, own) & okw[c]) >> c2;
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e)
-                                        if (!((seen >> (8 * k + e)) & 1u)) v[4 * (4 * c + k) + 2 * u + e] = -INFINITY;
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        mx[0] = max3(mx[0], v[4 * k], v[4 * k + 1]);
-                        mx[1] = max3(mx[1], v[4 * k + 2], v[4 * k + 3]);
-                    }
-                    if (__any_sync(0xffffffffu, mx[0] > R[h][0] + (kTop + kLag) || mx[1] > R[h][1] + (kTop + kLag))) {
-                        float f[2];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            float x = mx[u];
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                            const float to = x > R[h][u] + (kTop + kLag) ? x - kTop : R[h][u];
-                            f[u] = to == R[h][u] ? 1.f : ex2(R[h][u] - to);
-                            R[h][u] = to;
-                            l2[h][u] = mul2(l2[h][u], pair(f[u], f[u]));
-                        }
-                        if (i - it >= kStep) {             // the stream has outputs: PV of its last tile first
-                            wait(&H.pv_done[st], i / kStep - 1);
-                            us::tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t w[16];
-                                us::tmem_ld_frag32(o_tm + half + c, w);
+                for (int h = 0; h < 2; ++h) {
+                    if (wrow + 16 * h < rows) {
+                        const uint32_t half = (uint32_t)(16 * h) << 16;
+                        // A tile's scores mostly stay below R + 15: their weights are made at once,
+                        // while the maxima are found, and made again if one does not (or where
+                        // some are unseen).
+                        uint32_t w[32];
+                        uint64_t sum[2] = {0, 0};
+                        float over[2];                         // the rows' largest s - R
+                        auto weights = [&](const float (&v)[64], const uint64_t (&neg)[2], bool scaled) {
+                            over[0] = over[1] = -INFINITY;
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * f[(j >> 1) & 1]);
-                                us::tmem_st_frag32(o_tm + half + c, w);
+                            for (int k = 0; k < 16; ++k) {
+                                const float2 sk = ks2[4 * k];
+                                const uint64_t s = pair(sk.x, sk.y);
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    float a, b;
+                                    const uint64_t x = pair(v[4 * k + 2 * u], v[4 * k + 2 * u + 1]);
+                                    unpair(scaled ? add2(x, neg[u]) : fma2(x, s, neg[u]), a, b);
+                                    over[u] = max3(over[u], a, b);
+                                    a = ex2(a), b = ex2(b);
+                                    sum[u] = add2(sum[u], pair(a, b));
+                                    w[2 * k + u] = pack_half2(a, b);
+                                }
                             }
-                            us::tmem_wait_st();
+                        };
+                        float v[64];
+                        us::tmem_ld_frag128(s_tm + half, v);
+                        bool again = edge;
+                        if (!edge) {
+                            // (a row without a reference yet has -R = +inf: its weights are not used)
+                            const uint64_t neg[2] = {pair(-R[0], -R[0]), pair(-R[1], -R[1])};
+                            weights(v, neg, false);
+                            again = __any_sync(0xffffffffu, !(over[0] <= kTop + kLag) || !(over[1] <= kTop + kLag));
                         }
+                        if (again) {
+                            if (!edge) us::tmem_ld_frag128(s_tm + half, v);
+                            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float2 sk = ks2[4 * k];
+                                const uint64_t s = pair(sk.x, sk.y);
+                                unpair(mul2(pair(v[4 * k], v[4 * k + 1]), s), v[4 * k], v[4 * k + 1]);
+                                unpair(mul2(pair(v[4 * k + 2], v[4 * k + 3]), s), v[4 * k + 2], v[4 * k + 3]);
+                            }
+                            if (edge) {
+                                const uint32_t okw[4] = {ok.x, ok.y, ok.z, ok.w};
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const int r = wrow + 16 * h + 8 * u + g, tok = (cur.rb * kRows + r) / G;
+                                    const uint64_t mask = p.mask && r < rows ? p.mask[cur.r.row0 + tok] & (~0ull >> (64 - cur.r.n)) : 0ull;
+                                    const int own = r < rows ? tok + 1 : 0;    // a chain's row sees so many of the call
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c) {
+                                        const uint32_t seen = (seen32(base + 32 * c, mask, own) & okw[c]) >> c2;
+#pragma unroll
+                                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                            for (int e = 0; e < 2; ++e)
+                                                if (!((seen >> (8 * k + e)) & 1u)) v[4 * (4 * c + k) + 2 * u + e] = -INFINITY;
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                mx[0] = max3(mx[0], v[4 * k], v[4 * k + 1]);
+                                mx[1] = max3(mx[1], v[4 * k + 2], v[4 * k + 3]);
+                            }
+                            float f[2];
+                            bool moved = false;
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                float x = mx[u];
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                                const float to = x > R[u] + (kTop + kLag) ? x - kTop : R[u];
+                                f[u] = to == R[u] ? 1.f : ex2(R[u] - to);
+                                moved |= to != R[u];
+                                R[u] = to;
+                                l2[u] = mul2(l2[u], pair(f[u], f[u]));
+                            }
+                            if (i - it >= kStep && __any_sync(0xffffffffu, moved)) {
+                                wait(&H.pv_done[st], i / kStep - 1);           // the stream's outputs of its last tile first
+                                us::tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 32) {
+                                    uint32_t y[16];
+                                    us::tmem_ld_frag32(o_tm + half + c, y);
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f[(j >> 1) & 1]);
+                                    us::tmem_st_frag32(o_tm + half + c, y);
+                                }
+                                us::tmem_wait_st();
+                            }
+                            uint64_t neg[2];
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const float ref = R[u] == -INFINITY ? 0.f : R[u];
+                                neg[u] = pair(-ref, -ref);
+                                sum[u] = 0;
+                            }
+                            weights(v, neg, true);
+                        }
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) l2[u] = add2(l2[u], sum[u]);
+                        us::tmem_st_pairs64(s_tm + half, w);
                     }
-                    // weights, as fp16 over the scores
-                    uint32_t w[32];
-                    uint64_t neg[2];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const float ref = R[h][u] == -INFINITY ? 0.f : R[h][u];
-                        neg[u] = pair(-ref, -ref);
+                        const float r = R[u];
+                        const uint64_t t = l2[u];
+                        R[u] = Ro[u], Ro[u] = r;
+                        l2[u] = l2o[u], l2o[u] = t;
                     }
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            float a, b;
-                            unpair(add2(pair(v[4 * k + 2 * u], v[4 * k + 2 * u + 1]), neg[u]), a, b);
-                            a = ex2(a), b = ex2(b);
-                            l2[h][u] = add2(l2[h][u], pair(a, b));
-                            w[2 * k + u] = pack_half2(a, b);
-                        }
-                    us::tmem_st_pairs64(s_tm + half, w);
                 }
                 us::tmem_wait_st();
                 us::tc_fence_before();
@@ -345,11 +406,11 @@ attn_tc_kernel(const UsAttnParams p) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     float a, b;
-                    unpair(l2[h][u], a, b);
+                    unpair(h ? l2o[u] : l2[u], a, b);
                     a += b;
                     a += __shfl_xor_sync(0xffffffffu, a, 1);
                     a += __shfl_xor_sync(0xffffffffu, a, 2);
-                    if (c2 == 0) H.xr[st][srow + 16 * h + 8 * u + g] = R[h][u], H.xl[st][srow + 16 * h + 8 * u + g] = a;
+                    if (c2 == 0) H.xr[st][srow + 16 * h + 8 * u + g] = h ? Ro[u] : R[u], H.xl[st][srow + 16 * h + 8 * u + g] = a;
                 }
             // the streams whose outputs the warp reads, and whether they had a tile
             bool has[2];
@@ -474,68 +535,64 @@ attn_tc_kernel(const UsAttnParams p) {
     } else {
         // -------------------------------------------------------- conversion
         // Items in their order, tile after tile across segments: item x of the CTA is
-        // block x % 16 of tile x / 16, every seventh is this warp's.  Three are under
-        // way: the page number of one, the codes of one, the conversion of one.
-        struct Where {
-            int item, page, pos, h, left;                  // left: positions up to the last of the request
-        };
-        int next_item = warp - kSoftWarps - 1, tile = 0;   // the cursor's tile
+        // block x % 16 of tile x / 16, every seventh is this warp's.  While one is
+        // converted, the next kRS - 1 are copied and the page number of the one behind
+        // them is loaded.
+        constexpr int kRS = Sh::kRS;
+        const int items = kItems * count;
+        // the lane's chunks: u-th is 8 rows, or 64 bytes, behind the one before (eight
+        // lanes on eight rows: no bank conflicts when they are put)
+        const int lrow = Sh::kC == 2 ? lane & 15 : lane & 7, lchunk = Sh::kC == 2 ? lane >> 4 : lane >> 3;
+        const uint32_t get_at = (uint32_t)(lrow * Sh::kRow + lchunk * 16);
+        auto get_u = [](int u) { return Sh::kC == 8 ? (u >> 1) * 8 * Sh::kRow + (u & 1) * 64 : u * 8 * Sh::kRow; };
+        // where they go (operand_at, with what depends on the lane alone): row, 64
+        // dimensions, swizzled chunk
+        const uint32_t put_base = (uint32_t)(lrow * 128 + (lchunk * Sh::kOut >> 3) * Sh::kGroup);
+        const uint32_t put_chunk = (uint32_t)(((lchunk * Sh::kOut & 7) ^ (lrow & 7)) << 4);
+        auto put_u = [](int u) { return Sh::kC == 8 ? (u >> 1) * 1024 + (u & 1) * Sh::kGroup : u * 1024; };
+        uint8_t* raw = raw_sm + (warp - kMmaWarp - 1) * kRS * Sh::kRaw;
+
+        // the item whose page number is on its way
+        int nx_item = warp - kMmaWarp - 1, nx_tile = 0, nx_page = kNoPage, nx_pos = 0;
         auto locate = [&]() {
-            Where w = {next_item, kNoPage, 0, 0, 0};
-            next_item += kConvWarps;
-            const int i = w.item / kItems;
-            if (i < count) {
-                if (i > tile) cur.next(p), ++tile;
-                w.pos = cur.tile * kTile + (w.item & 7) * 16;
-                w.h = cur.h;
-                w.left = cur.r.ctx + cur.r.n - w.pos;
-                if (w.left > 0) w.page = p.c.table[(int64_t)cur.b * p.c.max_pages + (w.pos >> p.c.page_shift)];
-            }
-            return w;
+            if (nx_item >= items) return;
+            if ((nx_item >> 4) > nx_tile) cur.next(p), ++nx_tile;
+            nx_pos = cur.tile * kTile + (nx_item & 7) * 16;
+            nx_page = nx_pos < cur.r.ctx + cur.r.n
+                          ? p.c.table[(int64_t)cur.b * p.c.max_pages + (nx_pos >> p.c.page_shift)] : kNoPage;
         };
-        struct Codes {
-            uint4 c[Sh::kLoads];
-            uint32_t scale;                                // (K, V) scales of position `lane`
-        };
-        auto row_chunk = [&](int u, int& r, int& chunk) {  // eight lanes on eight rows: no bank conflicts
-            if constexpr (Sh::kC == 2) r = lane & 15, chunk = lane >> 4;
-            else r = 8 * (u / (Sh::kC / 4)) + (lane & 7), chunk = 4 * (u % (Sh::kC / 4)) + (lane >> 3);
-        };
-        // where a lane's first chunk of an item goes (operand_at, with what depends on
-        // the lane alone): its row, its 64 dimensions, and the swizzled chunk
-        uint32_t put_base, put_chunk;
-        {
-            int r, chunk;
-            row_chunk(0, r, chunk);
-            put_base = (uint32_t)(r * 128 + (chunk * Sh::kOut >> 3) * Sh::kGroup);
-            put_chunk = (uint32_t)(((chunk * Sh::kOut & 7) ^ (r & 7)) << 4);
-        }
-        auto exists = [&](const Where& w) { return w.page >= 0 && w.page < p.c.num_pages; };
-        auto fetch = [&](const Where& w, Codes& f) {
-            const bool ok = exists(w);
-            if (w.page != kNoPage && !ok) us::set_status(p.c.status, US_ERR_CORRUPT);
-            const int64_t e = us::kv_entry(p.c, w.page, w.h, w.pos);
-            const uint8_t* src = (w.item & 8 ? p.c.v : p.c.k) + e * Sh::kRow;
+        // copies it to ring place `slot`; says whether it has an entry, and how many of
+        // its positions are the request's
+        auto fetch = [&](int slot) {
+            int left = 0;
+            if (nx_item < items) {
+                const bool ok = nx_page >= 0 && nx_page < p.c.num_pages;
+                if (ok) {
+                    const int64_t e = us::kv_entry(p.c, nx_page, cur.h, nx_pos);
+                    const uint8_t* src = (nx_item & 8 ? p.c.v : p.c.k) + e * Sh::kRow + get_at;
+                    const uint32_t to = us::smem_addr(raw + slot * Sh::kRaw) + lane * 16;
 #pragma unroll
-            for (int u = 0; u < Sh::kLoads; ++u) {
-                int r, chunk;
-                row_chunk(u, r, chunk);
-                f.c[u] = ok ? __ldcg(reinterpret_cast<const uint4*>(src + r * Sh::kRow) + chunk) : make_uint4(0, 0, 0, 0);
+                    for (int u = 0; u < Sh::kLoads; ++u) cp_async16(to + u * 512, src + get_u(u));
+                    if (lane < 16)
+                        cp_async4(us::smem_addr(raw + slot * Sh::kRaw) + 16 * Sh::kRow + lane * 4, p.c.scale + 2 * (e + lane));
+                    left = min(16, cur.r.ctx + cur.r.n - nx_pos);
+                } else if (nx_page != kNoPage) {
+                    us::set_status(p.c.status, US_ERR_CORRUPT);
+                }
+                nx_item += kConvWarps;
+                locate();
             }
-            f.scale = ok && lane < 16 ? __ldcg(reinterpret_cast<const uint32_t*>(p.c.scale) + e + lane) : 0u;
+            cp_async_commit();
+            return left;
         };
-        // one item: its place in the ring, the conversion, the sign that it is there
-        auto convert_item = [&](const Where& w, const Codes& f) {
-            const int i = w.item / kItems, block = w.item & 7, ss = i % kSS;
-            const bool is_v = (w.item & 8) != 0;
-            // Entries that no row sees may hold any scale: behind the request's last
-            // position V's counts as 0, and one that is not finite is left to those
-            // who see its entry, through K's.
-            float sk = us::half_bits_to_float((uint16_t)f.scale) * (p.scale * 1.4426950408889634f);
-            uint32_t sv = f.scale >> 16;
-            if ((sv & 0x7C00u) == 0x7C00u) sv = 0, sk = __uint_as_float(0x7FC00000u);
-            if (lane >= w.left) sv = 0;
-            sv |= sv << 16;
+        locate();
+        uint32_t lefts = 0;                                // of the items under way, 8 bits each
+#pragma unroll
+        for (int s = 0; s < kRS; ++s) lefts |= (uint32_t)fetch(s) << (8 * s);
+        int slot = 0;
+        for (int item = warp - kMmaWarp - 1; item < items; item += kConvWarps) {
+            const int i = item >> 4, block = item & 7, left = (int)(lefts & 0xFFu);
+            const bool is_v = (item & 8) != 0;
             uint8_t* operand;
             if (is_v) {
                 if (i >= kVS) wait(&H.v_free[i % kVS], i / kVS - 1);
@@ -543,43 +600,47 @@ attn_tc_kernel(const UsAttnParams p) {
             } else {
                 if (i >= kKS) wait(&H.k_free[i % kKS], i / kKS - 1);
                 operand = k_sm + (i % kKS) * Sh::kOperand;
-                if (lane < 16) H.ks[ss][16 * block + lane] = sk;
-                if (lane == 0) H.valid[ss][block] = exists(w) ? 0xFFFFu : 0u;
             }
-            uint8_t* at = operand + block * 16 * 128 + put_base;
+            cp_async_wait<kRS - 1>();                      // a lane reads what it copied
+            const uint8_t* r = raw + slot * Sh::kRaw;
+            const uint32_t scale = left && lane < 16 ? reinterpret_cast<const uint32_t*>(r + 16 * Sh::kRow)[lane] : 0u;
+            // Entries that no row sees may hold any scale: behind the request's last
+            // position V's counts as 0, and one that is not finite is left to those
+            // who see its entry, through K's.
+            uint32_t sv = scale >> 16;
+            const bool bad = (sv & 0x7C00u) == 0x7C00u;
+            if (bad || lane >= left) sv = 0;
+            sv |= sv << 16;
+            if (!is_v) {
+                const float sk = us::half_bits_to_float((uint16_t)scale) * (p.scale * 1.4426950408889634f);
+                if (lane < 16) H.ks[i % kSS][16 * block + lane] = bad ? __uint_as_float(0x7FC00000u) : sk;
+                if (lane == 0) H.valid[i % kSS][block] = left ? 0xFFFFu : 0u;
+            }
+            uint8_t* to = operand + block * 16 * 128 + put_base;
 #pragma unroll
             for (int u = 0; u < Sh::kLoads; ++u) {
-                uint4 out[Sh::kOut];
-                convert<ELEM>(f.c[u], out);
+                uint4 c = make_uint4(0, 0, 0, 0), out[Sh::kOut];
+                if (left) c = *reinterpret_cast<const uint4*>(r + u * 512 + lane * 16);
+                convert<ELEM>(c, out);
                 if (is_v) {
                     const uint32_t s = __shfl_sync(0xffffffffu, sv, Sh::kC == 2 ? lane & 15 : 8 * (u / (Sh::kC / 4)) + (lane & 7));
 #pragma unroll
                     for (int k = 0; k < Sh::kOut; ++k)
                         out[k] = make_uint4(hmul2(out[k].x, s), hmul2(out[k].y, s), hmul2(out[k].z, s), hmul2(out[k].w, s));
                 }
-                // eight rows further, or the other 64 dimensions
-                uint8_t* to = at + (Sh::kC == 8 ? (u >> 1) * 1024 + (u & 1) * Sh::kGroup : u * 1024);
 #pragma unroll
-                for (int k = 0; k < Sh::kOut; ++k) *reinterpret_cast<uint4*>(to + (put_chunk ^ (k << 4))) = out[k];
+                for (int k = 0; k < Sh::kOut; ++k) *reinterpret_cast<uint4*>(to + put_u(u) + (put_chunk ^ (k << 4))) = out[k];
             }
             us::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 us::mbar_arrive(is_v ? &H.v_full[i % kVS] : &H.k_full[i % kKS]);
-                if (!is_v) us::mbar_arrive(&H.s_full[ss]);
+                if (!is_v) us::mbar_arrive(&H.s_full[i % kSS]);
             }
-        };
-        Codes fa, fb;
-        Where wa = locate(), wb = locate();
-        fetch(wa, fa);
-        fetch(wb, fb);
-        Where wc = locate(), wd = locate();                // two behind them, page numbers on their way
-        for (; wa.item < kItems * count; wa = wc, wb = wd, wc = locate(), wd = locate()) {
-            convert_item(wa, fa);
-            fetch(wc, fa);
-            if (wb.item < kItems * count) convert_item(wb, fb);
-            fetch(wd, fb);
+            lefts = lefts >> 8 | (uint32_t)fetch(slot) << (8 * (kRS - 1));
+            slot = slot + 1 == kRS ? 0 : slot + 1;
         }
+        cp_async_wait<0>();
     }
     __syncthreads();
     const int parts = any ? H.parts : 0;
