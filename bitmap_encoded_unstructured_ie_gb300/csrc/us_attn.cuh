@@ -94,12 +94,9 @@ struct Request {
 // behind their own.
 template <int ROWS, int TILE>
 US_DEV int tiles_of(const UsAttnParams& p, const Request& r, int rb) {
-    int end = r.n;
-    if (!p.mask) {
-        const int64_t rows = (int64_t)(rb + 1) * ROWS;
-        if (rows < (int64_t)r.n * p.G) end = (int)((rows - 1) / p.G) + 1;
-    }
-    return (r.ctx + end + TILE - 1) / TILE;
+    unsigned end = (unsigned)r.n;
+    if (!p.mask && rb + 1 < r.nrb) end = (unsigned)((rb + 1) * ROWS - 1) / (unsigned)p.G + 1u;   // n G < 2^30
+    return (int)(((unsigned)r.ctx + end + TILE - 1u) / TILE);
 }
 
 template <int ROWS>
@@ -109,7 +106,7 @@ US_DEV Request load_request(const UsAttnParams& p, int b, unsigned* status) {
     r.n = us::kv_rows(p.a, b, r.row0, status);
     if (r.n > 0) {
         r.ctx = us::kv_context(p.c, ctx, r.n, status);
-        if (r.ctx >= 0) r.nrb = (r.n * p.G + ROWS - 1) / ROWS;
+        if (r.ctx >= 0) r.nrb = (int)((unsigned)(r.n * p.G + ROWS - 1) / ROWS);
     }
     return r;
 }

@@ -33,7 +33,7 @@
 // Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set,
 // and moves only when a weight could pass 2^15 (fp16 keeps 2^-14 of them exactly as
 // it does the largest).  R, sums and outputs of a segment shared by several CTAs are
-// joined by the last of them to arrive.
+// joined by a second kernel.
 #include "us_attn.cuh"
 #include "us_internal.h"
 #include "us_tcgen05.cuh"
@@ -58,9 +58,6 @@ struct Header {
     alignas(16) uint16_t valid[kSS][8];                       // which of 16 positions exist
     float xr[2][kM], xl[2][kM];                   // the streams' references and sums
     uint32_t tmem;
-    unsigned last;
-    int parts;
-    Part part[2];
     Work work;
 };
 
@@ -151,37 +148,6 @@ US_DEV void store8(uint16_t* out, const float* y, float f) {
         make_uint4(pack_half2(d[0], d[1]), pack_half2(d[2], d[3]), pack_half2(d[4], d[5]), pack_half2(d[6], d[7]));
 }
 
-// The last CTA of a shared segment joins the partial states: 4 / NQ threads take a
-// row's columns, O stands as float4 of four columns, row after row.
-template <int ELEM, int D, int NQ>
-US_DEV void join_states(const UsAttnParams& p, const Part& a) {
-    using Sh = Shape<ELEM, D, NQ>;
-    constexpr int kRows = Sh::kRows, kCols = D * NQ / 4, kN = kCols / 4;
-    static_assert(kThreads == 4 * kM, "threads of a row");
-    const int row = threadIdx.x & (kRows - 1), part = threadIdx.x / kRows;
-    if (row >= a.rows) return;
-    float top = -INFINITY, sum = 0.f, y[kCols];
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) y[i] = 0.f;
-#pragma unroll 4
-    for (int c = a.first; c <= a.last; ++c) top = fmaxf(top, __ldcg(p.ws_slots + a.slot(c) * Sh::kSlotFloats + row));
-    for (int c = a.first; c <= a.last; ++c) {
-        const float* sl = p.ws_slots + a.slot(c) * Sh::kSlotFloats;
-        const float r = __ldcg(sl + row), f = r == -INFINITY ? 0.f : ex2(r - top);
-        sum += __ldcg(sl + kRows + row) * f;
-        const float4* o = reinterpret_cast<const float4*>(sl + 2 * kRows) + part * kN * kRows + row;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const float4 v = __ldcg(o + i * kRows);
-            y[4 * i] += v.x * f, y[4 * i + 1] += v.y * f, y[4 * i + 2] += v.z * f, y[4 * i + 3] += v.w * f;
-        }
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t* out = out_row<kRows>(p, a.row0, a.h, a.rb, row, D) + part * kCols;
-#pragma unroll
-    for (int i = 0; i < kCols / 8; ++i) store8<ELEM>(out + 8 * i, y + 8 * i, inv);
-}
-
 template <int ELEM, int D, int NQ>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const UsAttnParams p) {
@@ -233,7 +199,7 @@ attn_tc_kernel(const UsAttnParams p) {
         const int wrow = (warp & 3) * 32 + (NQ == 2 ? kM * st : 0);           // the warp's first row of the segment
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
         const uint32_t s_tm = tmem + lanes + st * 128, o_tm = tmem + lanes + 256 + st * 128;
-        int parts = 0;
+        if (threadIdx.x == 0) p.ws_parts[blockIdx.x].rows = 0;     // until a shared segment begins here
         for (int it = 0; it < count;) {
             // ---- a segment, or this CTA's part of it: tiles it .. end - 1
             const int end = min(count, it + cur.tiles - cur.tile), tile0 = cur.tile;
@@ -307,15 +273,16 @@ attn_tc_kernel(const UsAttnParams p) {
                         };
                         float v[64];
                         us::tmem_ld_frag128(s_tm + half, v);
-                        bool again = edge;
-                        if (!edge) {
-                            // (a row without a reference yet has -R = +inf: its weights are not used)
+                        const bool direct = !edge && i != i0;              // (a segment's first tile has no reference yet)
+                        bool again = !direct;
+                        if (direct) {
+                            // (a row without a reference has -R = +inf: its weights are not used)
                             const uint64_t neg[2] = {pair(-R[0], -R[0]), pair(-R[1], -R[1])};
                             weights(v, neg, false);
                             again = __any_sync(0xffffffffu, !(over[0] <= kTop + kLag) || !(over[1] <= kTop + kLag));
                         }
                         if (again) {
-                            if (!edge) us::tmem_ld_frag128(s_tm + half, v);
+                            if (direct) us::tmem_ld_frag128(s_tm + half, v);
                             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
@@ -463,17 +430,13 @@ attn_tc_kernel(const UsAttnParams p) {
                     }
                 }
             }
-            if (!whole) {
-                if (threadIdx.x == 0) H.part[parts] = part;
-                ++parts;
-            }
+            if (!whole && part.first == (int)blockIdx.x && threadIdx.x == 0) p.ws_parts[blockIdx.x] = part;
             us::tc_fence_before();
             us::named_bar_sync(1, 32 * kSoftWarps);        // Q, the streams' TMEM and sums are free
             us::tc_fence_after();
             it = end;
             if (it < count) cur.next_segment(p);
         }
-        if (threadIdx.x == 0) H.parts = parts;
     } else if (warp == kMmaWarp) {
         // --------------------------------------------------------------- MMA
         if (lane == 0) {
@@ -554,41 +517,65 @@ attn_tc_kernel(const UsAttnParams p) {
 
         // the item whose page number is on its way
         int nx_item = warp - kMmaWarp - 1, nx_tile = 0, nx_page = kNoPage, nx_pos = 0;
-        auto locate = [&]() {
+        auto locate = [&]() {                              // (at most one tile further)
             if (nx_item >= items) return;
             if ((nx_item >> 4) > nx_tile) cur.next(p), ++nx_tile;
             nx_pos = cur.tile * kTile + (nx_item & 7) * 16;
             nx_page = nx_pos < cur.r.ctx + cur.r.n
                           ? p.c.table[(int64_t)cur.b * p.c.max_pages + (nx_pos >> p.c.page_shift)] : kNoPage;
         };
-        // copies it to ring place `slot`; says whether it has an entry, and how many of
-        // its positions are the request's
-        auto fetch = [&](int slot) {
+        // copies it (key head h, `after` positions of the request from its first on) to
+        // ring place `slot`; says how many of its positions are the request's, 0 if it
+        // has no entries
+        auto copy_item = [&](int slot, int h, int after) {
             int left = 0;
-            if (nx_item < items) {
-                const bool ok = nx_page >= 0 && nx_page < p.c.num_pages;
-                if (ok) {
-                    const int64_t e = us::kv_entry(p.c, nx_page, cur.h, nx_pos);
+            if (nx_item < items && nx_page != kNoPage) {
+                if (nx_page >= 0 && nx_page < p.c.num_pages) {
+                    const int64_t e = us::kv_entry(p.c, nx_page, h, nx_pos);
                     const uint8_t* src = (nx_item & 8 ? p.c.v : p.c.k) + e * Sh::kRow + get_at;
                     const uint32_t to = us::smem_addr(raw + slot * Sh::kRaw) + lane * 16;
 #pragma unroll
                     for (int u = 0; u < Sh::kLoads; ++u) cp_async16(to + u * 512, src + get_u(u));
                     if (lane < 16)
                         cp_async4(us::smem_addr(raw + slot * Sh::kRaw) + 16 * Sh::kRow + lane * 4, p.c.scale + 2 * (e + lane));
-                    left = min(16, cur.r.ctx + cur.r.n - nx_pos);
-                } else if (nx_page != kNoPage) {
+                    left = min(16, after);
+                } else {
                     us::set_status(p.c.status, US_ERR_CORRUPT);
                 }
-                nx_item += kConvWarps;
-                locate();
             }
             cp_async_commit();
             return left;
         };
-        locate();
+        auto fetch = [&](int slot) {
+            const int left = copy_item(slot, cur.h, cur.r.ctx + cur.r.n - nx_pos);
+            if (nx_item < items) {
+                nx_item += kConvWarps;
+                locate();
+            }
+            return left;
+        };
+        // the first kRS items: their page numbers at once, a lane each
         uint32_t lefts = 0;                                // of the items under way, 8 bits each
+        {
+            Cur at = cur;
+            const int mine = nx_item + kConvWarps * lane, tile = mine >> 4;
+            const bool want = lane < kRS && mine < items;
+            if (want)
+                for (int t = 0; t < tile; ++t) at.next(p);
+            const int pos = at.tile * kTile + (mine & 7) * 16, left = want ? at.r.ctx + at.r.n - pos : 0;
+            const int page = left > 0 ? p.c.table[(int64_t)at.b * p.c.max_pages + (pos >> p.c.page_shift)] : kNoPage;
 #pragma unroll
-        for (int s = 0; s < kRS; ++s) lefts |= (uint32_t)fetch(s) << (8 * s);
+            for (int s = 0; s < kRS; ++s) {
+                nx_page = __shfl_sync(0xffffffffu, page, s);
+                nx_pos = __shfl_sync(0xffffffffu, pos, s);
+                const int h = __shfl_sync(0xffffffffu, at.h, s), l = __shfl_sync(0xffffffffu, left, s);
+                lefts |= (uint32_t)copy_item(s, h, l) << (8 * s);
+                if (nx_item < items) nx_item += kConvWarps;
+            }
+            const int last = nx_item < items ? nx_item >> 4 : 0;
+            for (; nx_tile < last; ++nx_tile) cur.next(p);
+            locate();
+        }
         int slot = 0;
         for (int item = warp - kMmaWarp - 1; item < items; item += kConvWarps) {
             const int i = item >> 4, block = item & 7, left = (int)(lefts & 0xFFu);
@@ -642,35 +629,76 @@ attn_tc_kernel(const UsAttnParams p) {
         }
         cp_async_wait<0>();
     }
-    __syncthreads();
-    const int parts = any ? H.parts : 0;
-
-    // ---- shared segments (at most two a CTA): the last CTA to arrive joins them
-    for (int i = 0; i < parts; ++i) {
-        __syncthreads();
-        const Part a = H.part[i];
-        if (threadIdx.x == 0) {                            // one thread's fences order the whole CTA's accesses
-            __threadfence();
-            H.last = atomicAdd(p.ws_count + a.first, 1u) == (unsigned)(a.last - a.first);
-            __threadfence();
-        }
-        __syncthreads();
-        if (!H.last) continue;
-        if (threadIdx.x == 0) p.ws_count[a.first] = 0;
-        join_states<ELEM, D, NQ>(p, a);
-    }
     us::tc_fence_before();
     __syncthreads();
     if (warp == kSoftWarps) us::tmem_dealloc(tmem, 512);
     us::pdl_launch_dependents();
 }
 
+// Joins the partial states of shared segments: CTA (x, c) the rows from 32 x of the
+// segment whose first sharer was CTA c, if there is one.  A thread takes 16 columns
+// of a row, four states' loads on their way at once.  A launch of its own: joined by
+// one of the sharers, a segment's states (131 KB each at 256 rows of 128) came at
+// the 76 GB/s that one SM draws from L2.
+constexpr int kJoinRows = 32;
+template <int ELEM, int D, int NQ>
+__global__ void __launch_bounds__(kJoinRows * D / 16)
+attn_tc_join_kernel(const UsAttnParams p) {
+    using Sh = Shape<ELEM, D, NQ>;
+    constexpr int kRows = Sh::kRows;
+    us::pdl_wait();
+    const Part a = p.ws_parts[blockIdx.y];
+    const int row = blockIdx.x * kJoinRows + (threadIdx.x & 31), col = threadIdx.x / 32 * 16;
+    if (row < a.rows) {
+        const int np = a.last - a.first + 1;
+        auto slot = [&](int c) { return p.ws_slots + a.slot(a.first + c) * Sh::kSlotFloats; };
+        float top = -INFINITY, sum = 0.f, y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = 0.f;
+#pragma unroll 8
+        for (int c = 0; c < np; ++c) top = fmaxf(top, __ldcg(slot(c) + row));
+        for (int c = 0; c < np; c += 4) {
+            float4 v[4][4];
+            float r[4], l[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float* sl = slot(c + u < np ? c + u : c);
+                const float4* o = reinterpret_cast<const float4*>(sl + 2 * kRows) + col / 4 * kRows + row;
+                r[u] = c + u < np ? __ldcg(sl + row) : -INFINITY;
+                l[u] = __ldcg(sl + kRows + row);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[u][i] = __ldcg(o + i * kRows);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (r[u] == -INFINITY) continue;
+                const float f = ex2(r[u] - top);
+                sum += l[u] * f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[4 * i] += v[u][i].x * f, y[4 * i + 1] += v[u][i].y * f;
+                    y[4 * i + 2] += v[u][i].z * f, y[4 * i + 3] += v[u][i].w * f;
+                }
+            }
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint16_t* out = out_row<kRows>(p, a.row0, a.h, a.rb, row, D) + col;
+        store8<ELEM>(out, y, inv);
+        store8<ELEM>(out + 8, y + 8, inv);
+    }
+    us::pdl_launch_dependents();
+}
+
+int grid() { return us::num_sms() < 512 ? us::num_sms() : 512; }
+constexpr int kPartBytes = 4096 + 512 * 32;       // counters, parts
+static_assert(sizeof(Part) <= 32, "parts");
+
 template <int ELEM, int D, int NQ>
 us_status launch(UsAttnParams p, cudaStream_t st) {
     using Sh = Shape<ELEM, D, NQ>;
     static_assert(Sh::kSmem <= 232448, "shared memory");
-    p.ws_count = static_cast<unsigned*>(p.ws);
-    p.ws_slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + 4096);
+    p.ws_parts = reinterpret_cast<Part*>(static_cast<uint8_t*>(p.ws) + 4096);      // behind the other kernel's counters
+    p.ws_slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kPartBytes);
     auto kern = attn_tc_kernel<ELEM, D, NQ>;
     static bool ready[64] = {};                            // the attribute is set once a device
     int dev = 0;
@@ -681,7 +709,7 @@ us_status launch(UsAttnParams p, cudaStream_t st) {
         ready[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)us::num_sms());
+    cfg.gridDim = dim3((unsigned)grid());
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Sh::kSmem;
     cfg.stream = st;
@@ -690,7 +718,11 @@ us_status launch(UsAttnParams p, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? US_OK : US_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return US_ERR_CUDA;
+    cfg.gridDim = dim3(Sh::kRows / kJoinRows, (unsigned)grid());
+    cfg.blockDim = dim3(kJoinRows * D / 16);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<ELEM, D, NQ>, p) == cudaSuccess ? US_OK : US_ERR_CUDA;
 }
 
 }  // namespace
@@ -701,7 +733,7 @@ bool attn_tc_serves(const UsAttnParams& p) { return (int64_t)p.a.max_n * p.G > 1
 
 size_t attn_tc_ws(const UsAttnParams& p) {
     const size_t rows = (int64_t)p.a.max_n * p.G > kM ? 2 * kM : kM;
-    return 4096 + (size_t)2 * num_sms() * (2 * rows + rows * p.c.D) * 4;
+    return kPartBytes + (size_t)2 * grid() * (2 * rows + rows * p.c.D) * 4;
 }
 
 us_status launch_attn_tc(const UsAttnParams& p, cudaStream_t st) {

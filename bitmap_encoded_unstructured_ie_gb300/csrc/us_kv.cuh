@@ -25,6 +25,12 @@ struct UsKvCall {
     int T, max_n;
 };
 
+namespace us {
+namespace attn {
+struct Part;
+}
+}  // namespace us
+
 // Attention over the cache: Q and O token-major rows of Hq heads.
 struct UsAttnParams {
     UsKvCache c;
@@ -38,6 +44,7 @@ struct UsAttnParams {
     void* ws;
     unsigned* ws_count;              // arrival counters, zero between calls
     float* ws_slots;                 // partial states
+    us::attn::Part* ws_parts;        // shared segments
 };
 
 namespace us {
