@@ -340,7 +340,7 @@ attn_mma_kernel(const UsAttnParams p) {
     for (int it = 0; it < count; ++it) {
         const uint32_t blocks = (have >> (s * kSub)) & ((1u << kSub) - 1u);
         if (blocks) {
-            if (!failed && !us::mbar_wait(&full[warp][s], (phase >> s) & 1u, p.c.status)) failed = true;
+            if (!failed && !wait_bar(&full[warp][s], (phase >> s) & 1u, p.c.status)) failed = true;
             phase ^= 1u << s;
             const uint8_t* st = wring + s * Sh::kStageBytes;
             const int pos = cur.tile * Sh::kTile + warp * kStep;

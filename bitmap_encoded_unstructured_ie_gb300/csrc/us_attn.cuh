@@ -11,6 +11,22 @@ namespace attn {
 constexpr float kMaxLag = 4.f;                    // a row's maximum may lag by 2^4 before the state is rescaled
 constexpr float kVHead = 2048.f;                  // weights reach 2^4 2^11 < 65504 as fp16: small ones keep their bits
 
+// Waits for phase `parity` of `bar`, at most kWaitLimitNs (then US_ERR_TIMEOUT is
+// recorded).  A try, a sleep of some 20 ns, a try: try_wait alone comes back at once
+// and its loop took most of the issue slots; with a time hint it woke warps late.
+US_DEV bool wait_bar(uint64_t* bar, uint32_t parity, unsigned* status) {
+    if (us::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = us::globaltimer_ns();
+    do {
+        if (us::globaltimer_ns() - t0 > us::kWaitLimitNs) {
+            us::set_status(status, US_ERR_TIMEOUT);
+            return false;
+        }
+        __nanosleep(20);
+    } while (!us::mbar_try_wait(bar, parity));
+    return true;
+}
+
 US_DEV float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -47,7 +47,6 @@ constexpr int kSoftWarps = 8, kMmaWarp = 8, kConvWarps = 7;
 constexpr int kThreads = 32 * (kSoftWarps + 1 + kConvWarps);
 constexpr int kItems = 16;                        // of a tile: 8 of K, then 8 of V
 constexpr int kKS = 2, kSS = 4;                   // stages: K, scales (V: Shape::kVS)
-constexpr int kTries = 20000;                     // of a wait, before the call gives up
 constexpr float kTop = 11.f, kLag = 4.f;          // a row's largest weight is 2^11 at first, 2^15 at most
 
 struct Header {
@@ -155,7 +154,7 @@ attn_tc_kernel(const UsAttnParams p) {
     constexpr int kRows = Sh::kRows, kVS = Sh::kVS;
     using Cur = Cursor<kRows, kTile>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = smem_raw + ((0u - us::smem_addr(smem_raw)) & 1023u);     // (still known to be shared memory)
     uint8_t* q_sm = smem;
     uint8_t* k_sm = q_sm + NQ * Sh::kOperand;
     uint8_t* v_sm = k_sm + kKS * Sh::kOperand;
@@ -184,13 +183,7 @@ attn_tc_kernel(const UsAttnParams p) {
     const int count = any ? (int)(wk.t1 - wk.t0) : 0, G = p.G;
     bool failed = false;
     auto wait = [&](uint64_t* bar, int use) {              // for the use-th completion of bar
-        if (us::mbar_try_wait(bar, (uint32_t)use & 1u) || failed) return;
-        for (int n = 0; !us::mbar_try_wait_sleep(bar, (uint32_t)use & 1u, 100000u); ++n)
-            if (n == kTries) {
-                us::set_status(p.c.status, US_ERR_TIMEOUT);
-                failed = true;
-                return;
-            }
+        if (!failed && !wait_bar(bar, (uint32_t)use & 1u, p.c.status)) failed = true;
     };
 
     if (warp < kSoftWarps) {
@@ -204,13 +197,24 @@ attn_tc_kernel(const UsAttnParams p) {
             // ---- a segment, or this CTA's part of it: tiles it .. end - 1
             const int end = min(count, it + cur.tiles - cur.tile), tile0 = cur.tile;
             const int rows = min(kRows, cur.r.n * G - cur.rb * kRows);
+            // Q: a thread takes one 16-byte chunk of every kQR-th row, up to 16 loads at once
+            constexpr int kQR = 32 * kSoftWarps / (D / 8), kAtOnce = kRows / kQR < 16 ? kRows / kQR : 16;
+            const int q_row = threadIdx.x / (D / 8), q_chunk = threadIdx.x % (D / 8);
+#pragma unroll 1
+            for (int r0 = q_row; r0 < kRows; r0 += kAtOnce * kQR) {
+                uint4 u[kAtOnce];
 #pragma unroll
-            for (int x = threadIdx.x; x < kRows * (D / 8); x += 32 * kSoftWarps) {
-                const int r = x / (D / 8), chunk = x % (D / 8), rr = cur.rb * kRows + r, i = rr / G;
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (r < rows)
-                    u = *reinterpret_cast<const uint4*>(p.Q + (int64_t)(cur.r.row0 + i) * p.ldq + (int64_t)(cur.h * G + rr - i * G) * D + 8 * chunk);
-                *reinterpret_cast<uint4*>(operand_at(q_sm + (r / kM) * Sh::kOperand, r % kM, chunk)) = reorder<ELEM>(u);
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const int r = r0 + k * kQR, rr = cur.rb * kRows + r, i = (int)((unsigned)rr / (unsigned)G);
+                    u[k] = make_uint4(0, 0, 0, 0);
+                    if (r < rows)
+                        u[k] = __ldg(reinterpret_cast<const uint4*>(p.Q + (int64_t)(cur.r.row0 + i) * p.ldq + (int64_t)(cur.h * G + rr - i * G) * D) + q_chunk);
+                }
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const int r = r0 + k * kQR;
+                    *reinterpret_cast<uint4*>(operand_at(q_sm + (r / kM) * Sh::kOperand, r % kM, q_chunk)) = reorder<ELEM>(u[k]);
+                }
             }
             us::fence_proxy_async_smem();
             __syncwarp();
