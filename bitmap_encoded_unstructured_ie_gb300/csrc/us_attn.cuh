@@ -17,14 +17,16 @@ constexpr float kVHead = 2048.f;                  // weights reach 2^4 2^11 < 65
 US_DEV bool wait_bar(uint64_t* bar, uint32_t parity, unsigned* status) {
     if (us::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = us::globaltimer_ns();
-    do {
-        if (us::globaltimer_ns() - t0 > us::kWaitLimitNs) {
-            us::set_status(status, US_ERR_TIMEOUT);
-            return false;
+    for (;;) {
+#pragma unroll 1
+        for (int n = 0; n < 64; ++n) {
+            __nanosleep(20);
+            if (us::mbar_try_wait(bar, parity)) return true;
         }
-        __nanosleep(20);
-    } while (!us::mbar_try_wait(bar, parity));
-    return true;
+        if (us::globaltimer_ns() - t0 > us::kWaitLimitNs) break;
+    }
+    us::set_status(status, US_ERR_TIMEOUT);
+    return false;
 }
 
 US_DEV float ex2(float x) {

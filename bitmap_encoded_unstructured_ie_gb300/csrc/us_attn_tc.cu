@@ -18,12 +18,12 @@
 // With more than 128 rows (NQ = 2) a stream is a half of the rows and takes every
 // tile: each tile's codes are converted once for 256 rows.  Else (NQ = 1) the tiles
 // alternate between the streams, which are joined at the segment's end.
-//   warps 0-3, 4-7: softmax of stream 0 / 1, 32 rows each, 16 at a time, in the
-//               fragment order of 16-lane TMEM loads: a lane has a quarter of the
-//               columns, so it reads a quarter of the scales (what bounds these warps
-//               is the load / store pipe: every register that comes from TMEM or
-//               shared memory takes a cycle of it a warp)
-//   warp 8: one thread issues the MMAs: PV of a tile, then QK of the stream's next
+//   warps 0-3, 4-7: softmax of stream 0 / 1, 32 rows each, 64 positions at a time
+//               (the scores of the other 64 are made meanwhile), in the fragment
+//               order of 16-lane TMEM loads: a lane has a quarter of the columns, so
+//               it reads a quarter of the scales (every register that comes from
+//               TMEM or shared memory takes a cycle of the load / store pipe a warp)
+//   warp 8: one thread issues the MMAs: PV of a half tile, then QK of the next tile's
 //               (it is held up at the rate of their execution, 64 cycles each)
 //   warps 9-15: codes -> fp16, in items of 16 positions of K or of V; a warp's next
 //               items are on their way to its own ring, each lane's to its own place
@@ -51,7 +51,7 @@ constexpr float kTop = 11.f, kLag = 4.f;          // a row's largest weight is 2
 
 struct Header {
     uint64_t k_full[kKS], k_free[kKS], v_full[3], v_free[3], s_full[kSS];
-    uint64_t qk_done[2], p_full[2], pv_done[2];   // by stream
+    uint64_t qk_done[2][2], p_full[2][2], pv_done[2][2];       // by stream and half tile
     uint64_t q_full;
     alignas(16) float ks[kSS][kTile];                         // K's scales times scale log2(e) of the tiles on their way
     alignas(16) uint16_t valid[kSS][8];                       // which of 16 positions exist
@@ -61,6 +61,12 @@ struct Header {
 };
 
 static_assert(offsetof(Header, ks) % 16 == 0 && offsetof(Header, valid) % 16 == 0, "read 8 and 16 bytes at a time");
+struct Yes {
+    constexpr bool operator()() const { return true; }
+};
+struct No {
+    constexpr bool operator()() const { return false; }
+};
 constexpr int kNoPage = -0x7fffffff - 1;          // nothing to read (any other bad number is recorded)
 
 template <int ELEM, int D, int NQ>
@@ -166,8 +172,10 @@ attn_tc_kernel(const UsAttnParams p) {
         for (int i = 0; i < kKS; ++i) us::mbar_init(&H.k_full[i], 8), us::mbar_init(&H.k_free[i], 1);
         for (int i = 0; i < kVS; ++i) us::mbar_init(&H.v_full[i], 8), us::mbar_init(&H.v_free[i], 1);
         for (int i = 0; i < kSS; ++i) us::mbar_init(&H.s_full[i], 8);
-        for (int i = 0; i < 2; ++i)
-            us::mbar_init(&H.qk_done[i], 1), us::mbar_init(&H.p_full[i], 4), us::mbar_init(&H.pv_done[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            for (int a = 0; a < 2; ++a)
+                us::mbar_init(&H.qk_done[i][a], 1), us::mbar_init(&H.p_full[i][a], 4), us::mbar_init(&H.pv_done[i][a], 1);
+        }
         us::mbar_init(&H.q_full, kSoftWarps);
         us::fence_mbar_init();
     }
@@ -232,167 +240,168 @@ attn_tc_kernel(const UsAttnParams p) {
                 }
                 return (own << lo) | (lo ? 0xFFFFFFFFu >> (32 - lo) : 0u);
             };
-            // references and sums (two partial ones each) of rows g, g + 8 of the half at
-            // hand, and of the other half: they change places after every half
-            float R[2] = {-INFINITY, -INFINITY}, Ro[2] = {-INFINITY, -INFINITY};
-            uint64_t l2[2] = {}, l2o[2] = {};
+            // references and sums (two partial ones each) of the lane's rows wrow + 8 q + g
+            float R[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint64_t l2[4] = {};
             constexpr int kStep = NQ == 2 ? 1 : 2;         // a stream's tiles: every one, or every other
             const int i0 = NQ == 2 ? it : it + ((it ^ st) & 1);
             for (int i = i0; i < end; i += kStep) {
                 const int ss = i % kSS;
                 wait(&H.s_full[ss], i / kSS);
-                wait(&H.qk_done[st], i / kStep);
-                us::tc_fence_after();
-                const float2* ks2 = reinterpret_cast<const float2*>(H.ks[ss]) + (lane & 3);
-                const uint4 ok = *reinterpret_cast<const uint4*>(H.valid[ss]);
-                const int base = (tile0 + i - it) * kTile - cur.r.ctx;
-                const bool edge = base + kTile > 0 || (ok.x & ok.y & ok.z & ok.w) != 0xFFFFFFFFu;
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if (wrow + 16 * h < rows) {
-                        const uint32_t half = (uint32_t)(16 * h) << 16;
-                        // A tile's scores mostly stay below R + 15: their weights are made at once,
-                        // while the maxima are found, and made again if one does not (or where
-                        // some are unseen).
-                        uint32_t w[32];
-                        uint64_t sum[2] = {0, 0};
-                        float over[2];                         // the rows' largest s - R
-                        auto weights = [&](const float (&v)[64], const uint64_t (&neg)[2], bool scaled) {
-                            over[0] = over[1] = -INFINITY;
+                for (int a = 0; a < 2; ++a) {              // the tile's halves of 64 positions
+                    wait(&H.qk_done[st][a], i / kStep);
+                    us::tc_fence_after();
+                    const uint2 ok = *reinterpret_cast<const uint2*>(&H.valid[ss][4 * a]);
+                    const int base = (tile0 + i - it) * kTile + 64 * a - cur.r.ctx;
+                    const bool edge = base + 64 > 0 || (ok.x & ok.y) != 0xFFFFFFFFu;
+                    if (wrow < rows) {
+                        const float2* ks2 = reinterpret_cast<const float2*>(H.ks[ss]) + 32 * a + (lane & 3);
+                        // Scores mostly stay below R + 15: their weights are made at once, while
+                        // the maxima are found, and made again if one does not (or where some
+                        // are unseen).
+                        uint32_t w[32];                    // the weights as fp16 pairs
+                        uint64_t sum[4];
+                        float over[4];                     // the rows' largest s - R
+                        auto weights = [&](const float (&v)[64], const uint64_t (&neg)[4], auto scaled) {
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float2 sk = ks2[4 * k];
-                                const uint64_t s = pair(sk.x, sk.y);
+                            for (int q = 0; q < 4; ++q) over[q] = -INFINITY, sum[q] = 0;
 #pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    float a, b;
-                                    const uint64_t x = pair(v[4 * k + 2 * u], v[4 * k + 2 * u + 1]);
-                                    unpair(scaled ? add2(x, neg[u]) : fma2(x, s, neg[u]), a, b);
-                                    over[u] = max3(over[u], a, b);
-                                    a = ex2(a), b = ex2(b);
-                                    sum[u] = add2(sum[u], pair(a, b));
-                                    w[2 * k + u] = pack_half2(a, b);
+                            for (int k = 0; k < 8; ++k) {
+                                uint64_t s = 0;
+                                if constexpr (!scaled()) {
+                                    const float2 sk = ks2[4 * k];
+                                    s = pair(sk.x, sk.y);
+                                }
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const int at = 32 * (q >> 1) + 4 * k + 2 * (q & 1);
+                                    float x, y;
+                                    if constexpr (scaled()) unpair(add2(pair(v[at], v[at + 1]), neg[q]), x, y);
+                                    else unpair(fma2(pair(v[at], v[at + 1]), s, neg[q]), x, y);
+                                    over[q] = max3(over[q], x, y);
+                                    x = ex2(x), y = ex2(y);
+                                    sum[q] = add2(sum[q], pair(x, y));
+                                    w[16 * (q >> 1) + 2 * k + (q & 1)] = pack_half2(x, y);
                                 }
                             }
                         };
                         float v[64];
-                        us::tmem_ld_frag128(s_tm + half, v);
-                        const bool direct = !edge && i != i0;              // (a segment's first tile has no reference yet)
-                        bool again = !direct;
-                        if (direct) {
-                            // (a row without a reference has -R = +inf: its weights are not used)
-                            const uint64_t neg[2] = {pair(-R[0], -R[0]), pair(-R[1], -R[1])};
-                            weights(v, neg, false);
-                            again = __any_sync(0xffffffffu, !(over[0] <= kTop + kLag) || !(over[1] <= kTop + kLag));
+                        us::tmem_ld_frag64(s_tm + 64 * a, v);
+                        uint64_t neg[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) neg[q] = pair(-R[q], -R[q]);
+                        // (a segment's first tile has no reference yet: -R = +inf, weights that are not used)
+                        bool again = edge || (i == i0 && a == 0);
+                        if (!again) {
+                            weights(v, neg, No());
+                            bool far = false;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) far |= !(over[q] <= kTop + kLag);
+                            again = __any_sync(0xffffffffu, far);
+                            if (again) us::tmem_ld_frag64(s_tm + 64 * a, v);
                         }
                         if (again) {
-                            if (direct) us::tmem_ld_frag128(s_tm + half, v);
-                            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) {
+                            for (int k = 0; k < 8; ++k) {
                                 const float2 sk = ks2[4 * k];
-                                const uint64_t s = pair(sk.x, sk.y);
-                                unpair(mul2(pair(v[4 * k], v[4 * k + 1]), s), v[4 * k], v[4 * k + 1]);
-                                unpair(mul2(pair(v[4 * k + 2], v[4 * k + 3]), s), v[4 * k + 2], v[4 * k + 3]);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const int at = 32 * (q >> 1) + 4 * k + 2 * (q & 1);
+                                    v[at] *= sk.x, v[at + 1] *= sk.y;
+                                }
                             }
                             if (edge) {
-                                const uint32_t okw[4] = {ok.x, ok.y, ok.z, ok.w};
 #pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const int r = wrow + 16 * h + 8 * u + g, tok = (cur.rb * kRows + r) / G;
+                                for (int q = 0; q < 4; ++q) {
+                                    const int r = wrow + 8 * q + g, tok = (int)((unsigned)(cur.rb * kRows + r) / (unsigned)G);
                                     const uint64_t mask = p.mask && r < rows ? p.mask[cur.r.row0 + tok] & (~0ull >> (64 - cur.r.n)) : 0ull;
                                     const int own = r < rows ? tok + 1 : 0;    // a chain's row sees so many of the call
 #pragma unroll
-                                    for (int c = 0; c < 4; ++c) {
-                                        const uint32_t seen = (seen32(base + 32 * c, mask, own) & okw[c]) >> c2;
+                                    for (int c = 0; c < 2; ++c) {
+                                        const uint32_t seen = (seen32(base + 32 * c, mask, own) & (c ? ok.y : ok.x)) >> c2;
 #pragma unroll
                                         for (int k = 0; k < 4; ++k)
 #pragma unroll
                                             for (int e = 0; e < 2; ++e)
-                                                if (!((seen >> (8 * k + e)) & 1u)) v[4 * (4 * c + k) + 2 * u + e] = -INFINITY;
+                                                if (!((seen >> (8 * k + e)) & 1u)) v[32 * (q >> 1) + 4 * (4 * c + k) + 2 * (q & 1) + e] = -INFINITY;
                                     }
                                 }
                             }
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                mx[0] = max3(mx[0], v[4 * k], v[4 * k + 1]);
-                                mx[1] = max3(mx[1], v[4 * k + 2], v[4 * k + 3]);
-                            }
-                            float f[2];
+                            float f[4];
                             bool moved = false;
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                float x = mx[u];
+                            for (int q = 0; q < 4; ++q) {
+                                float x = -INFINITY;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    const int at = 32 * (q >> 1) + 4 * k + 2 * (q & 1);
+                                    x = max3(x, v[at], v[at + 1]);
+                                }
                                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                                const float to = x > R[u] + (kTop + kLag) ? x - kTop : R[u];
-                                f[u] = to == R[u] ? 1.f : ex2(R[u] - to);
-                                moved |= to != R[u];
-                                R[u] = to;
-                                l2[u] = mul2(l2[u], pair(f[u], f[u]));
+                                const float to = x > R[q] + (kTop + kLag) ? x - kTop : R[q];
+                                f[q] = to == R[q] ? 1.f : ex2(R[q] - to);
+                                moved |= to != R[q];
+                                R[q] = to;
+                                l2[q] = mul2(l2[q], pair(f[q], f[q]));
+                                const float ref = to == -INFINITY ? 0.f : to;
+                                neg[q] = pair(-ref, -ref);
                             }
-                            if (i - it >= kStep && __any_sync(0xffffffffu, moved)) {
-                                wait(&H.pv_done[st], i / kStep - 1);           // the stream's outputs of its last tile first
+                            if ((i != i0 || a) && __any_sync(0xffffffffu, moved)) {
+                                wait(&H.pv_done[st][a ^ 1], i / kStep + a - 1);    // the stream's outputs so far first
                                 us::tc_fence_after();
 #pragma unroll 1
-                                for (int c = 0; c < D; c += 32) {
+                                for (int c = 0; c < 2 * D; c += 32) {
+                                    const uint32_t at = o_tm + (uint32_t)(c & (D - 1)) + (c < D ? 0u : 16u << 16);
                                     uint32_t y[16];
-                                    us::tmem_ld_frag32(o_tm + half + c, y);
+                                    us::tmem_ld_frag32(at, y);
+                                    const float fa = c < D ? f[0] : f[2], fb = c < D ? f[1] : f[3];
 #pragma unroll
-                                    for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f[(j >> 1) & 1]);
-                                    us::tmem_st_frag32(o_tm + half + c, y);
+                                    for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * ((j >> 1) & 1 ? fb : fa));
+                                    us::tmem_st_frag32(at, y);
                                 }
                                 us::tmem_wait_st();
                             }
-                            uint64_t neg[2];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const float ref = R[u] == -INFINITY ? 0.f : R[u];
-                                neg[u] = pair(-ref, -ref);
-                                sum[u] = 0;
-                            }
-                            weights(v, neg, true);
+                            weights(v, neg, Yes());
                         }
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) l2[u] = add2(l2[u], sum[u]);
-                        us::tmem_st_pairs64(s_tm + half, w);
+                        for (int q = 0; q < 4; ++q) l2[q] = add2(l2[q], sum[q]);
+                        us::tmem_st_pairs32(s_tm + 64 * a, w);     // over scores that were read
+                        us::tmem_st_pairs32(s_tm + 64 * a + (16u << 16), w + 16);
+                        us::tmem_wait_st();
                     }
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float r = R[u];
-                        const uint64_t t = l2[u];
-                        R[u] = Ro[u], Ro[u] = r;
-                        l2[u] = l2o[u], l2o[u] = t;
-                    }
+                    us::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) us::mbar_arrive(&H.p_full[st][a]);
                 }
-                us::tmem_wait_st();
-                us::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) us::mbar_arrive(&H.p_full[st]);
             }
             // ---- the segment's end: the streams' sums and outputs
             const int srow = (warp & 3) * 32;              // the warp's first row of its stream
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float a, b;
-                    unpair(h ? l2o[u] : l2[u], a, b);
-                    a += b;
-                    a += __shfl_xor_sync(0xffffffffu, a, 1);
-                    a += __shfl_xor_sync(0xffffffffu, a, 2);
-                    if (c2 == 0) H.xr[st][srow + 16 * h + 8 * u + g] = h ? Ro[u] : R[u], H.xl[st][srow + 16 * h + 8 * u + g] = a;
-                }
+            for (int q = 0; q < 4; ++q) {
+                float a, b;
+                unpair(l2[q], a, b);
+                a += b;
+                a += __shfl_xor_sync(0xffffffffu, a, 1);
+                a += __shfl_xor_sync(0xffffffffu, a, 2);
+                if (c2 == 0) H.xr[st][srow + 8 * q + g] = R[q], H.xl[st][srow + 8 * q + g] = a;
+            }
             // the streams whose outputs the warp reads, and whether they had a tile
             bool has[2];
+            // PV of the last tile of stream x (the tile before it is done: a parity tells
+            // only neighbouring phases apart)
+            auto finish = [&](int x, int tile) { wait(&H.pv_done[x][1], tile / kStep); };
             if constexpr (NQ == 2) {
                 has[0] = true, has[1] = false;
-                wait(&H.pv_done[st], end - 1);
+                finish(st, end - 1);
                 __syncwarp();
             } else {
                 has[0] = end - it >= 2 || !(it & 1), has[1] = end - it >= 2 || (it & 1);
-                wait(&H.pv_done[(end - 1) & 1], (end - 1) / 2);
-                if (end - it >= 2) wait(&H.pv_done[end & 1], (end - 2) / 2);
+                // the warp's own stream first: all but the last tile of the other come before it
+                const int own = ((end - 1) & 1) == st ? end - 1 : end - 2, other = 2 * end - 3 - own;
+                if (has[st]) finish(st, own);
+                if (has[st ^ 1]) finish(st ^ 1, other);
                 us::named_bar_sync(1, 32 * kSoftWarps);
             }
             us::tc_fence_after();
@@ -443,56 +452,59 @@ attn_tc_kernel(const UsAttnParams p) {
         }
     } else if (warp == kMmaWarp) {
         // --------------------------------------------------------------- MMA
-        if (lane == 0) {
+        if (us::elect_one()) {
             int segment = 0;
             for (int it = 0; it < count; ++segment) {
                 const int end = min(count, it + cur.tiles - cur.tile);
-                // scores of tile i for stream st, and whether they are the last that read its K
-                auto qk = [&](int i, int st, bool last) {
-                    constexpr uint32_t id = us::umma_idesc_f16(kM, kTile);
-                    wait(&H.k_full[i % kKS], i / kKS);
+                // scores of half a of tile i for stream st; last: nothing after them reads the tile's K
+                auto qk = [&](int i, int st, int a, bool last) {
+                    constexpr uint32_t id = us::umma_idesc_f16(kM, 64);
+                    if (a == 0) wait(&H.k_full[i % kKS], i / kKS);
                     us::tc_fence_after();
                     const uint64_t qd = us::umma_smem_desc_sw128(q_sm + (NQ == 2 ? st * Sh::kOperand : 0));
-                    const uint64_t kd = us::umma_smem_desc_sw128(k_sm + (i % kKS) * Sh::kOperand);
+                    const uint64_t kd = us::umma_smem_desc_sw128(k_sm + (i % kKS) * Sh::kOperand) + (uint64_t)(a * 64 * 128 >> 4);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t at = (uint64_t)(((kk >> 2) * Sh::kGroup + (kk & 3) * 32) >> 4);
-                        us::umma_f16(tmem + st * 128, qd + at, kd + at, id, kk > 0);
+                        us::umma_f16(tmem + st * 128 + a * 64, qd + at, kd + at, id, kk > 0);
                     }
-                    us::umma_commit(&H.qk_done[st]);
+                    us::umma_commit(&H.qk_done[st][a]);
                     if (last) us::umma_commit(&H.k_free[i % kKS]);
                 };
-                // outputs of tile i for stream st; its weights are the stream's use-th
-                auto pv = [&](int i, int st, int use, bool first, bool last) {
+                // outputs of half a of tile i for stream st, whose use-th tile it is
+                auto pv = [&](int i, int st, int a, int use, bool first, bool last) {
                     constexpr uint32_t id = us::umma_idesc_f16(kM, D) | us::kUmmaBMajorMN;
-                    wait(&H.v_full[i % kVS], i / kVS);
-                    wait(&H.p_full[st], use);
+                    if (a == 0) wait(&H.v_full[i % kVS], i / kVS);
+                    wait(&H.p_full[st][a], use);
                     us::tc_fence_after();
-                    const uint64_t vd = us::umma_smem_desc_mn_sw128(v_sm + (i % kVS) * Sh::kOperand, Sh::kGroup);
+                    const uint64_t vd = us::umma_smem_desc_mn_sw128(v_sm + (i % kVS) * Sh::kOperand, Sh::kGroup) + (uint64_t)(a * 64 * 128 >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        us::umma_f16_ta(tmem + 256 + st * 128, tmem + st * 128 + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), id,
+                    for (int kk = 0; kk < 4; ++kk)
+                        us::umma_f16_ta(tmem + 256 + st * 128, tmem + st * 128 + a * 64 + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), id,
                                         !first || kk > 0);
-                    us::umma_commit(&H.pv_done[st]);
+                    us::umma_commit(&H.pv_done[st][a]);
                     if (last) us::umma_commit(&H.v_free[i % kVS]);
                 };
                 wait(&H.q_full, segment);
                 if constexpr (NQ == 2) {
-                    qk(it, 0, false);
-                    qk(it, 1, true);
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x) qk(it, x & 1, x >> 1, x == 3);
                     for (int i = it; i < end; ++i)
-#pragma unroll
-                        for (int st = 0; st < 2; ++st) {
-                            pv(i, st, i, i == it, st == 1);
-                            if (i + 1 < end) qk(i + 1, st, st == 1);
+#pragma unroll 1
+                        for (int x = 0; x < 4; ++x) {
+                            const int st = x & 1, a = x >> 1;
+                            pv(i, st, a, i, i == it && a == 0, x == 3);
+                            if (i + 1 < end) qk(i + 1, st, a, x == 3);
                         }
                 } else {
-                    qk(it, it & 1, true);
-                    if (it + 1 < end) qk(it + 1, (it + 1) & 1, true);
-                    for (int i = it; i < end; ++i) {
-                        pv(i, i & 1, i / 2, i - it < 2, true);
-                        if (i + 2 < end) qk(i + 2, i & 1, true);
-                    }
+#pragma unroll 1
+                    for (int x = 0; x < 4 && it + (x >> 1) < end; ++x) qk(it + (x >> 1), (it + (x >> 1)) & 1, x & 1, x & 1);
+                    for (int i = it; i < end; ++i)
+#pragma unroll 1
+                        for (int a = 0; a < 2; ++a) {
+                            pv(i, i & 1, a, i / 2, i - it < 2 && a == 0, a == 1);
+                            if (i + 2 < end) qk(i + 2, i & 1, a, a == 1);
+                        }
                 }
                 it = end;
                 if (it < count) cur.next_segment(p);
@@ -584,16 +596,12 @@ attn_tc_kernel(const UsAttnParams p) {
         for (int item = warp - kMmaWarp - 1; item < items; item += kConvWarps) {
             const int i = item >> 4, block = item & 7, left = (int)(lefts & 0xFFu);
             const bool is_v = (item & 8) != 0;
-            uint8_t* operand;
-            if (is_v) {
-                if (i >= kVS) wait(&H.v_free[i % kVS], i / kVS - 1);
-                operand = v_sm + (i % kVS) * Sh::kOperand;
-            } else {
-                if (i >= kKS) wait(&H.k_free[i % kKS], i / kKS - 1);
-                operand = k_sm + (i % kKS) * Sh::kOperand;
-            }
             cp_async_wait<kRS - 1>();                      // a lane reads what it copied
             const uint8_t* r = raw + slot * Sh::kRaw;
+            uint4 c[Sh::kLoads];
+#pragma unroll
+            for (int u = 0; u < Sh::kLoads; ++u)
+                c[u] = left ? *reinterpret_cast<const uint4*>(r + u * 512 + lane * 16) : make_uint4(0, 0, 0, 0);
             const uint32_t scale = left && lane < 16 ? reinterpret_cast<const uint32_t*>(r + 16 * Sh::kRow)[lane] : 0u;
             // Entries that no row sees may hold any scale: behind the request's last
             // position V's counts as 0, and one that is not finite is left to those
@@ -602,7 +610,18 @@ attn_tc_kernel(const UsAttnParams p) {
             const bool bad = (sv & 0x7C00u) == 0x7C00u;
             if (bad || lane >= left) sv = 0;
             sv |= sv << 16;
-            if (!is_v) {
+            uint32_t vscale[2];                            // of the lane's rows
+#pragma unroll
+            for (int u = 0; u < 2; ++u) vscale[u] = __shfl_sync(0xffffffffu, sv, Sh::kC == 2 ? lane & 15 : 8 * u + (lane & 7));
+            lefts = lefts >> 8 | (uint32_t)fetch(slot) << (8 * (kRS - 1));       // its place is free
+            slot = slot + 1 == kRS ? 0 : slot + 1;
+            uint8_t* operand;
+            if (is_v) {
+                if (i >= kVS) wait(&H.v_free[i % kVS], i / kVS - 1);
+                operand = v_sm + (i % kVS) * Sh::kOperand;
+            } else {
+                if (i >= kKS) wait(&H.k_free[i % kKS], i / kKS - 1);
+                operand = k_sm + (i % kKS) * Sh::kOperand;
                 const float sk = us::half_bits_to_float((uint16_t)scale) * (p.scale * 1.4426950408889634f);
                 if (lane < 16) H.ks[i % kSS][16 * block + lane] = bad ? __uint_as_float(0x7FC00000u) : sk;
                 if (lane == 0) H.valid[i % kSS][block] = left ? 0xFFFFu : 0u;
@@ -610,11 +629,10 @@ attn_tc_kernel(const UsAttnParams p) {
             uint8_t* to = operand + block * 16 * 128 + put_base;
 #pragma unroll
             for (int u = 0; u < Sh::kLoads; ++u) {
-                uint4 c = make_uint4(0, 0, 0, 0), out[Sh::kOut];
-                if (left) c = *reinterpret_cast<const uint4*>(r + u * 512 + lane * 16);
-                convert<ELEM>(c, out);
+                uint4 out[Sh::kOut];
+                convert<ELEM>(c[u], out);
                 if (is_v) {
-                    const uint32_t s = __shfl_sync(0xffffffffu, sv, Sh::kC == 2 ? lane & 15 : 8 * (u / (Sh::kC / 4)) + (lane & 7));
+                    const uint32_t s = vscale[Sh::kC == 2 ? 0 : u / (Sh::kC / 4)];
 #pragma unroll
                     for (int k = 0; k < Sh::kOut; ++k)
                         out[k] = make_uint4(hmul2(out[k].x, s), hmul2(out[k].y, s), hmul2(out[k].z, s), hmul2(out[k].w, s));
@@ -628,8 +646,6 @@ attn_tc_kernel(const UsAttnParams p) {
                 us::mbar_arrive(is_v ? &H.v_full[i % kVS] : &H.k_full[i % kKS]);
                 if (!is_v) us::mbar_arrive(&H.s_full[i % kSS]);
             }
-            lefts = lefts >> 8 | (uint32_t)fetch(slot) << (8 * (kRS - 1));
-            slot = slot + 1 == kRS ? 0 : slot + 1;
         }
         cp_async_wait<0>();
     }
