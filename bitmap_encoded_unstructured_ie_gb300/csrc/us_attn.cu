@@ -50,7 +50,7 @@ struct Shape {
     static constexpr int kKS = D / 16;                              // MMA steps over the dimensions
     static constexpr int kMT = D / 16;                              // 16-dimension blocks of O^T
     static constexpr int kMinB = W == 8 ? 2 : 3;                  // CTAs an SM
-    static constexpr int kSub = kRow == 128 ? 1 : 2;                // 16-position blocks of a warp's step
+    static constexpr int kSub = kRow == 128 || NT == 4 ? 1 : 2;     // 16-position blocks of a warp's step
     static constexpr int kStep = kSub * kBlock;
     static constexpr int kTile = kWarps * kStep;                    // positions of a CTA's step
     static constexpr int kStageBytes = 2 * kStep * kRow + kStep * 4;
@@ -675,6 +675,7 @@ template <class F>
 auto with_plan(const UsAttnParams& p, F f) {
     const int rows = p.a.max_n * p.G;
 #define US_ATTN_PICK(E, D) (rows <= 8 ? f(Plan<E, D, 1, 8>()) : f(Plan<E, D, 2, 4>()))
+    if (p.c.D == 64 && rows > 16) return p.c.elem == US_I8 ? f(Plan<US_I8, 64, 4, 4>()) : f(Plan<US_I4, 64, 4, 4>());
     if (p.c.elem == US_I8) return p.c.D == 64 ? US_ATTN_PICK(US_I8, 64) : US_ATTN_PICK(US_I8, 128);
     return p.c.D == 64 ? US_ATTN_PICK(US_I4, 64) : US_ATTN_PICK(US_I4, 128);
 #undef US_ATTN_PICK

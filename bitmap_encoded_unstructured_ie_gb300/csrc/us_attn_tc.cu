@@ -749,7 +749,10 @@ us_status launch(UsAttnParams p, cudaStream_t st) {
 
 namespace us {
 
-bool attn_tc_serves(const UsAttnParams& p) { return (int64_t)p.a.max_n * p.G > 16; }
+// From 17 rows per key head of 128 dimensions, 33 of 64: below, the mma.sync kernel
+// is faster (16 requests of 4000 positions, int4: 32 rows of 64 dimensions 38 us
+// there, 52 here; 32 rows of 128 59 and 61, of one request 27 and 23).
+bool attn_tc_serves(const UsAttnParams& p) { return (int64_t)p.a.max_n * p.G > (p.c.D == 64 ? 32 : 16); }
 
 size_t attn_tc_ws(const UsAttnParams& p) {
     const size_t rows = (int64_t)p.a.max_n * p.G > kM ? 2 * kM : kM;
