@@ -27,9 +27,8 @@
 // Work: the (request, key head, row block) segments are cut into tiles of 64 or
 // 128 positions, and the tile sequence is spread evenly over the CTAs, whatever
 // the lengths (they are read on the device).  A warp takes 16 or 32 positions of
-// each tile: per 16 positions three bulk copies (K, V, scales; a page's entries
-// of one head are contiguous) into the warp's own ring, several tiles ahead and
-// across segments.  A segment shared by several CTAs leaves partial states in the
+// each tile, copied into the warp's own ring several tiles ahead and across
+// segments (a page's entries of one head are contiguous).  A segment shared by several CTAs leaves partial states in the
 // workspace; the CTA that arrives last joins them in the order of the tiles.
 #include "us_attn.cuh"
 #include "us_internal.h"
@@ -204,14 +203,11 @@ attn_mma_kernel(const UsAttnParams p) {
     uint64_t* sm_mask = reinterpret_cast<uint64_t*>(sm_l + kWarps * kRows);     // [kRows]
     int* sm_tok = reinterpret_cast<int*>(sm_mask + kRows);                       // [kRows]
     float* sm_inv = reinterpret_cast<float*>(sm_tok + kRows);                    // [kRows]
-    __shared__ uint64_t full[kWarps][kStages];
     __shared__ unsigned sh_last;
     __shared__ Part sh_part[2];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
     const int G = p.G;
-    if (lane < kStages) us::mbar_init(&full[warp][lane], 1);
-    us::fence_mbar_init();
     us::pdl_wait();
 
     // ---- this CTA's tiles
@@ -221,49 +217,52 @@ attn_mma_kernel(const UsAttnParams p) {
     const int64_t t0 = wk.t0, t1 = wk.t1;
     const int count = (int)(t1 - t0);
 
-    // ---- producer: the warp's positions of tile `pc` into stage s.  Lanes 3 i
-    // to 3 i + 2 copy K, V and scales of 16-position block i; the page numbers
-    // are loaded one tile ahead.
+    // ---- producer: the warp's positions of tile `pc` into stage s, 16 bytes a lane
+    // at a time; the page numbers are loaded one tile ahead.
     Cursor<kRows, Sh::kTile> pc = cur;
     uint8_t* wring = ring + warp * kStages * Sh::kStageBytes;
     uint32_t have = 0;                                     // kSub bits a stage: which blocks it holds
-    const int my_sub = lane / 3, my_part = lane - 3 * my_sub;
     constexpr int kNoPage = -0x7fffffff - 1;               // nothing to copy (any other bad number is recorded)
-    int page = kNoPage, page_pos = 0;
-    auto copy = [&](const Cursor<kRows, Sh::kTile>& at, int id, int pos, int s, int sub, int part, uint32_t bits) {
-        if (part == 0 && sub == (bits & 1u ? 0 : 1))       // the stage's first copy also says what is to come
-            us::mbar_arrive_expect_tx(&full[warp][s], (uint32_t)(__popc(bits) * (2 * kBlock * Sh::kRow + kBlock * 4)));
-        const int64_t e = us::kv_entry(p.c, id, at.h, pos);
-        const uint8_t* src = part == 0 ? p.c.k + e * Sh::kRow
-                           : part == 1 ? p.c.v + e * Sh::kRow
-                                       : reinterpret_cast<const uint8_t*>(p.c.scale) + e * 4;
-        const int off = part < 2 ? (part * kStep + sub * kBlock) * Sh::kRow : 2 * kStep * Sh::kRow + sub * kBlock * 4;
-        us::bulk_g2s(wring + s * Sh::kStageBytes + off, src, part == 2 ? (uint32_t)kBlock * 4u : (uint32_t)(kBlock * Sh::kRow),
-                     &full[warp][s]);
+    int page[kSub];
+    auto copy = [&](int s, int sub, int64_t e) {           // the 16-position block at entry e
+        const uint32_t st = us::smem_addr(wring + s * Sh::kStageBytes) + lane * 16;
+        const uint8_t *k = p.c.k + e * Sh::kRow + lane * 16, *v = p.c.v + e * Sh::kRow + lane * 16;
+#pragma unroll
+        for (int u = 0; u < kBlock * Sh::kRow / 512; ++u) {
+            cp_async16(st + sub * kBlock * Sh::kRow + u * 512, k + u * 512);
+            cp_async16(st + (kStep + sub * kBlock) * Sh::kRow + u * 512, v + u * 512);
+        }
+        if (lane < kBlock / 4)
+            cp_async16(st + 2 * kStep * Sh::kRow + sub * kBlock * 4, reinterpret_cast<const uint8_t*>(p.c.scale) + e * 4 + lane * 16);
     };
-    auto find_page = [&]() {
-        page_pos = pc.tile * Sh::kTile + warp * kStep + my_sub * kBlock;
-        page = my_sub < kSub && page_pos < pc.r.ctx + pc.r.n
-                   ? p.c.table[(int64_t)pc.b * p.c.max_pages + (page_pos >> p.c.page_shift)] : kNoPage;
-    };
-    auto issue = [&](int s, bool more) {
-        const bool ok = page >= 0 && page < p.c.num_pages;
-        if (!ok && page != kNoPage) us::set_status(p.c.status, US_ERR_CORRUPT);
-        const uint32_t votes = __ballot_sync(0xffffffffu, ok && my_part == 0);
-        uint32_t bits = votes & 1u;
-        if constexpr (kSub == 2) bits |= (votes >> 2) & 2u;
-        have = (have & ~(((1u << kSub) - 1u) << (s * kSub))) | (bits << (s * kSub));
-        if (ok) copy(pc, page, page_pos, s, my_sub, my_part, bits);
-        if (more) {
-            pc.next(p);
-            find_page();
+    auto find_pages = [&]() {
+#pragma unroll
+        for (int sb = 0; sb < kSub; ++sb) {
+            const int pos = pc.tile * Sh::kTile + warp * kStep + sb * kBlock;
+            page[sb] = kNoPage;
+            if (pos < pc.r.ctx + pc.r.n) page[sb] = p.c.table[(int64_t)pc.b * p.c.max_pages + (pos >> p.c.page_shift)];
         }
     };
-    // The first stages at once: lane groups of 3 kSub lanes each take one.
+    auto issue = [&](int s, bool more) {
+        have &= ~(((1u << kSub) - 1u) << (s * kSub));
+#pragma unroll
+        for (int sb = 0; sb < kSub; ++sb) {
+            if (page[sb] >= 0 && page[sb] < p.c.num_pages) {
+                copy(s, sb, us::kv_entry(p.c, page[sb], pc.h, pc.tile * Sh::kTile + warp * kStep + sb * kBlock));
+                have |= 1u << (s * kSub + sb);
+            } else if (page[sb] != kNoPage) {
+                us::set_status(p.c.status, US_ERR_CORRUPT);
+            }
+        }
+        if (more) {
+            pc.next(p);
+            find_pages();
+        }
+    };
+    // The first stages: their page numbers at once, a lane a block.
     const int ahead = count < kStages ? count : kStages;
     {
-        static_assert(kStages * 3 * kSub <= 32, "a lane per copy");
-        const int st = lane / (3 * kSub), in = lane - st * 3 * kSub, sub = in / 3, part = in - 3 * sub;
+        const int st = lane / kSub, sub = lane - st * kSub;
         Cursor<kRows, Sh::kTile> at = cur;
         for (int i = 0; i < st && st < ahead; ++i) at.next(p);
         const int pos = at.tile * Sh::kTile + warp * kStep + sub * kBlock;
@@ -271,23 +270,24 @@ attn_mma_kernel(const UsAttnParams p) {
         const int id = want ? p.c.table[(int64_t)at.b * p.c.max_pages + (pos >> p.c.page_shift)] : -1;
         const bool ok = id >= 0 && id < p.c.num_pages;
         if (want && !ok) us::set_status(p.c.status, US_ERR_CORRUPT);
-        const uint32_t votes = __ballot_sync(0xffffffffu, ok && part == 0);
+        const int64_t e = ok ? us::kv_entry(p.c, id, at.h, pos) : -1;
 #pragma unroll
-        for (int i = 0; i < kStages * kSub; ++i) have |= ((votes >> (3 * i)) & 1u) << i;
-        if (ok) {
-            const uint32_t bits = (have >> (st * kSub)) & ((1u << kSub) - 1u);
-            copy(at, id, pos, st, sub, part, bits);
+        for (int i = 0; i < kStages * kSub; ++i) {
+            const int64_t ei = __shfl_sync(0xffffffffu, e, i);
+            if (ei >= 0) {
+                copy(i / kSub, i % kSub, ei);
+                have |= 1u << i;
+            }
+            if (i % kSub == kSub - 1) cp_async_commit();
         }
         for (int i = 0; i < ahead && i + 1 < count; ++i) pc.next(p);
-        if (ahead < count) find_page();
+        if (ahead < count) find_pages();
     }
 
     // ---- consumer state: maxima, sums and O^T of the warp's positions
     float m[NT][2], l[NT][2], qb[NT][2], o[kMT][NT][4], vref = 0.f, vmul = 0.f;
     uint32_t qf[Sh::kKS][NT][2];
     const float sc = p.scale * (1.4426950408889634f * 16777216.f);   // weights as powers of two; codes came as u 2^-24
-    uint32_t phase = 0;
-    bool failed = false;
     int parts = 0;
     const int rt = ((g & 1) << 2) | (g >> 1);              // token of row g (k index 2c -> c, 2c + 1 -> c + 4)
 
@@ -338,10 +338,10 @@ attn_mma_kernel(const UsAttnParams p) {
     begin_segment();
     int s = 0;
     for (int it = 0; it < count; ++it) {
+        cp_async_wait<kStages - 1>();
+        __syncwarp();                                      // every lane's part of the stage is there
         const uint32_t blocks = (have >> (s * kSub)) & ((1u << kSub) - 1u);
         if (blocks) {
-            if (!failed && !wait_bar(&full[warp][s], (phase >> s) & 1u, p.c.status)) failed = true;
-            phase ^= 1u << s;
             const uint8_t* st = wring + s * Sh::kStageBytes;
             const int pos = cur.tile * Sh::kTile + warp * kStep;
             float sx[kSub][NT][4], vs[kSub][2];
@@ -517,6 +517,7 @@ attn_mma_kernel(const UsAttnParams p) {
         const bool ends = cur.tile + 1 == cur.tiles || it + 1 == count;
         __syncwarp();                                      // every lane has read the stage
         if (it + kStages < count) issue(s, it + kStages + 1 < count);
+        cp_async_commit();
         s = s + 1 == kStages ? 0 : s + 1;
 
         // ---- the end of the segment, or of this CTA's part of it

@@ -87,18 +87,6 @@ struct Shape {
     static constexpr int kSlotFloats = 2 * kRows + kRows * D;
 };
 
-US_DEV void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-US_DEV void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-US_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-US_DEV void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Column j of eight -> its dimension of eight: the order in which codes leave a word.
 template <int ELEM>
 US_DEV constexpr int dim_of(int j) {
