@@ -6,10 +6,10 @@
 // are spread evenly over the CTAs (one an SM):
 //   S = Q Ck^T    A = Q (shared memory), B = the tile's K codes as fp16
 //   O += P Cv     A = P (TMEM, fp16), B = the tile's V codes as fp16, MN-major
-// K enters as its codes, its scale on the scores in fp32.  V enters as fp16(code *
-// scale), the values that us_kv_read returns: one more rounding of 2^-11 of a value,
-// against a register's worth of shared memory traffic per score for a scale in the
-// weights.  The dimensions stand in shared memory in the order in which the codes
+// K enters as its codes, its scale on the scores in fp32.  V enters as code * 2^e,
+// exactly; the rest of its scale 2^e m (1 <= m < 2) multiplies the weight in fp32, so
+// that a weight's rounding to fp16 is the only one (V as fp16(code * scale) needs no
+// multiplication there, but a second rounding of 2^-11).  The dimensions stand in shared memory in the order in which the codes
 // leave their words (within each eight), the same for Q, K and V; only the outputs
 // are put back.
 //
@@ -27,11 +27,12 @@
 //               (it is held up at the rate of their execution, 64 cycles each)
 //   warps 9-15: codes -> fp16, in items of 16 positions of K or of V; a warp's next
 //               items are on their way to its own ring, each lane's to its own place
-// 16 warps: a thread may have 128 registers (17 would leave 96).  The roles' loops
+// 16 warps: 128 registers a thread, of which the softmax takes 160 and leaves 96 to
+// the others (at 128 it spilled: chunk of 512 tokens 202 us, 195 so).  The roles' loops
 // are kept short (one copy of each body): four warps of a scheduler run three
 // different programs, and fetching them was a sixth of its time.
 // Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set,
-// and moves only when a weight could pass 2^15 (fp16 keeps 2^-14 of them exactly as
+// and moves only when a weight could pass 2^14.9 (fp16 keeps 2^-14 of them exactly as
 // it does the largest).  R, sums and outputs of a segment shared by several CTAs are
 // joined by a second kernel.
 #include "us_attn.cuh"
@@ -47,25 +48,22 @@ constexpr int kSoftWarps = 8, kMmaWarp = 8, kConvWarps = 7;
 constexpr int kThreads = 32 * (kSoftWarps + 1 + kConvWarps);
 constexpr int kItems = 16;                        // of a tile: 8 of K, then 8 of V
 constexpr int kKS = 2, kSS = 4;                   // stages: K, scales (V: Shape::kVS)
-constexpr float kTop = 11.f, kLag = 4.f;          // a row's largest weight is 2^11 at first, 2^15 at most
+constexpr float kTop = 11.f, kMost = 30573.f;     // a row's largest weight is 2^11 at first, 2^14.9 at most (times m: fp16)
 
 struct Header {
     uint64_t k_full[kKS], k_free[kKS], v_full[3], v_free[3], s_full[kSS];
     uint64_t qk_done[2][2], p_full[2][2], pv_done[2][2];       // by stream and half tile
     uint64_t q_full;
-    alignas(16) float ks[kSS][kTile];                         // K's scales times scale log2(e) of the tiles on their way
+    // by pairs of positions of the tiles on their way: K's scales times scale log2(e), V's m
+    float4 scales[kSS][kTile / 2];
     alignas(16) uint16_t valid[kSS][8];                       // which of 16 positions exist
-    float xr[2][kM], xl[2][kM];                   // the streams' references and sums
     uint32_t tmem;
     Work work;
 };
 
-static_assert(offsetof(Header, ks) % 16 == 0 && offsetof(Header, valid) % 16 == 0, "read 8 and 16 bytes at a time");
-struct Yes {
-    constexpr bool operator()() const { return true; }
-};
-struct No {
-    constexpr bool operator()() const { return false; }
+static_assert(offsetof(Header, scales) % 16 == 0 && offsetof(Header, valid) % 16 == 0, "read 8 and 16 bytes at a time");
+struct Ends {                                     // of a stream's rows at a segment's end, where Q was
+    float ref[kM], sum[kM];
 };
 constexpr int kNoPage = -0x7fffffff - 1;          // nothing to read (any other bad number is recorded)
 
@@ -182,6 +180,9 @@ attn_tc_kernel(const UsAttnParams p) {
         if (!failed && !wait_bar(bar, (uint32_t)use & 1u, p.c.status)) failed = true;
     };
 
+    // 256 threads of each: together the 128 registers a thread of the launch
+    if (warp < kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp < kSoftWarps) {
         // ----------------------------------------------------------- softmax
         const int st = warp >> 2, g = lane >> 2, c2 = 2 * (lane & 3);
@@ -238,120 +239,126 @@ attn_tc_kernel(const UsAttnParams p) {
                 wait(&H.s_full[ss], i / kSS);
 #pragma unroll 1
                 for (int a = 0; a < 2; ++a) {              // the tile's halves of 64 positions
-                    wait(&H.qk_done[st][a], i / kStep);
-                    us::tc_fence_after();
                     const uint2 ok = *reinterpret_cast<const uint2*>(&H.valid[ss][4 * a]);
                     const int base = (tile0 + i - it) * kTile + 64 * a - cur.r.ctx;
                     const bool edge = base + 64 > 0 || (ok.x & ok.y) != 0xFFFFFFFFu;
+                    wait(&H.qk_done[st][a], i / kStep);
+                    us::tc_fence_after();
                     if (wrow < rows) {
-                        const float2* ks2 = reinterpret_cast<const float2*>(H.ks[ss]) + 32 * a + (lane & 3);
-                        // Scores mostly stay below R + 15: their weights are made at once, while
-                        // the maxima are found, and made again if one does not (or where some
-                        // are unseen).
+                        const float4* sc2 = H.scales[ss] + 32 * a + (lane & 3);
+                        // Scores mostly stay below R + 14.9: their weights are made at once, and
+                        // again if a lane's sum of eight of them passes 2^14.9 (rows of equal
+                        // scores reach 2^14), or where some are unseen.
                         uint32_t w[32];                    // the weights as fp16 pairs
-                        uint64_t sum[4];
-                        float over[4];                     // the rows' largest s - R
-                        auto weights = [&](const float (&v)[64], const uint64_t (&neg)[4], auto scaled) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) over[q] = -INFINITY, sum[q] = 0;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                uint64_t s = 0;
-                                if constexpr (!scaled()) {
-                                    const float2 sk = ks2[4 * k];
-                                    s = pair(sk.x, sk.y);
-                                }
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int at = 32 * (q >> 1) + 4 * k + 2 * (q & 1);
-                                    float x, y;
-                                    if constexpr (scaled()) unpair(add2(pair(v[at], v[at + 1]), neg[q]), x, y);
-                                    else unpair(fma2(pair(v[at], v[at + 1]), s, neg[q]), x, y);
-                                    over[q] = max3(over[q], x, y);
-                                    x = ex2(x), y = ex2(y);
-                                    sum[q] = add2(sum[q], pair(x, y));
-                                    w[16 * (q >> 1) + 2 * k + (q & 1)] = pack_half2(x, y);
-                                }
-                            }
-                        };
-                        float v[64];
-                        us::tmem_ld_frag64(s_tm + 64 * a, v);
-                        uint64_t neg[4];
+                        uint64_t sum[4], neg[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) neg[q] = pair(-R[q], -R[q]);
-                        // (a segment's first tile has no reference yet: -R = +inf, weights that are not used)
-                        bool again = edge || (i == i0 && a == 0);
-                        if (!again) {
-                            weights(v, neg, No());
-                            bool far = false;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) far |= !(over[q] <= kTop + kLag);
-                            again = __any_sync(0xffffffffu, far);
-                            if (again) us::tmem_ld_frag64(s_tm + 64 * a, v);
-                        }
-                        if (again) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float2 sk = ks2[4 * k];
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int at = 32 * (q >> 1) + 4 * k + 2 * (q & 1);
-                                    v[at] *= sk.x, v[at + 1] *= sk.y;
-                                }
-                            }
-                            if (edge) {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int r = wrow + 8 * q + g, tok = (int)((unsigned)(cur.rb * kRows + r) / (unsigned)G);
-                                    const uint64_t mask = p.mask && r < rows ? p.mask[cur.r.row0 + tok] & (~0ull >> (64 - cur.r.n)) : 0ull;
-                                    const int own = r < rows ? tok + 1 : 0;    // a chain's row sees so many of the call
-#pragma unroll
-                                    for (int c = 0; c < 2; ++c) {
-                                        const uint32_t seen = (seen32(base + 32 * c, mask, own) & (c ? ok.y : ok.x)) >> c2;
-#pragma unroll
-                                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                                            for (int e = 0; e < 2; ++e)
-                                                if (!((seen >> (8 * k + e)) & 1u)) v[32 * (q >> 1) + 4 * (4 * c + k) + 2 * (q & 1) + e] = -INFINITY;
-                                    }
-                                }
-                            }
-                            float f[4];
-                            bool moved = false;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                float x = -INFINITY;
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    const int at = 32 * (q >> 1) + 4 * k + 2 * (q & 1);
-                                    x = max3(x, v[at], v[at + 1]);
-                                }
-                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                                const float to = x > R[q] + (kTop + kLag) ? x - kTop : R[q];
-                                f[q] = to == R[q] ? 1.f : ex2(R[q] - to);
-                                moved |= to != R[q];
-                                R[q] = to;
-                                l2[q] = mul2(l2[q], pair(f[q], f[q]));
-                                const float ref = to == -INFINITY ? 0.f : to;
-                                neg[q] = pair(-ref, -ref);
-                            }
-                            if ((i != i0 || a) && __any_sync(0xffffffffu, moved)) {
-                                wait(&H.pv_done[st][a ^ 1], i / kStep + a - 1);    // the stream's outputs so far first
-                                us::tc_fence_after();
+                        // (a segment's first tile has no reference yet)
+                        for (bool fit = edge || (i == i0 && a == 0);; fit = true) {
+                            if (fit) {
+                                // scaled and masked scores, back in their place, and what they move
+                                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                                for (int c = 0; c < 2 * D; c += 32) {
-                                    const uint32_t at = o_tm + (uint32_t)(c & (D - 1)) + (c < D ? 0u : 16u << 16);
-                                    uint32_t y[16];
-                                    us::tmem_ld_frag32(at, y);
-                                    const float fa = c < D ? f[0] : f[2], fb = c < D ? f[1] : f[3];
+                                for (int c = 0; c < 2; ++c) {
+                                    float v[32];
+                                    us::tmem_ld_frag32(s_tm + 64 * a + 32 * c, v);
 #pragma unroll
-                                    for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * ((j >> 1) & 1 ? fb : fa));
-                                    us::tmem_st_frag32(at, y);
+                                    for (int k = 0; k < 4; ++k) {
+                                        const float4 sc = sc2[16 * c + 4 * k];
+#pragma unroll
+                                        for (int q = 0; q < 4; ++q) {
+                                            const int at = 16 * (q >> 1) + 4 * k + 2 * (q & 1);
+                                            v[at] *= sc.x, v[at + 1] *= sc.y;
+                                        }
+                                    }
+                                    if (edge) {
+#pragma unroll
+                                        for (int q = 0; q < 4; ++q) {
+                                            const int r = wrow + 8 * q + g, tok = (int)((unsigned)(cur.rb * kRows + r) / (unsigned)G);
+                                            const uint64_t mask = p.mask && r < rows ? p.mask[cur.r.row0 + tok] & (~0ull >> (64 - cur.r.n)) : 0ull;
+                                            const int own = r < rows ? tok + 1 : 0;    // a chain's row sees so many of the call
+                                            const uint32_t seen = (seen32(base + 32 * c, mask, own) & (c ? ok.y : ok.x)) >> c2;
+#pragma unroll
+                                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                                for (int e = 0; e < 2; ++e)
+                                                    if (!((seen >> (8 * k + e)) & 1u)) v[16 * (q >> 1) + 4 * k + 2 * (q & 1) + e] = -INFINITY;
+                                        }
+                                    }
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                                        for (int k = 0; k < 4; ++k) {
+                                            const int at = 16 * (q >> 1) + 4 * k + 2 * (q & 1);
+                                            top[q] = max3(top[q], v[at], v[at + 1]);
+                                        }
+                                    us::tmem_st_frag32(s_tm + 64 * a + 32 * c, v);
                                 }
                                 us::tmem_wait_st();
+                                float f[4];
+                                bool moved = false;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    float x = top[q];
+                                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                                    const float to = x > R[q] + kTop ? x - kTop : R[q];
+                                    f[q] = to == R[q] ? 1.f : ex2(R[q] - to);
+                                    moved |= to != R[q];
+                                    R[q] = to;
+                                    l2[q] = mul2(l2[q], pair(f[q], f[q]));
+                                    const float ref = to == -INFINITY ? 0.f : to;
+                                    neg[q] = pair(-ref, -ref);
+                                }
+                                if ((i != i0 || a) && __any_sync(0xffffffffu, moved)) {
+                                    wait(&H.pv_done[st][a ^ 1], i / kStep + a - 1);    // the stream's outputs so far first
+                                    us::tc_fence_after();
+#pragma unroll 1
+                                    for (int c = 0; c < D; c += 32) {
+                                        float y[32];
+                                        us::tmem_ld_frag32(o_tm + c, y);
+#pragma unroll
+                                        for (int j = 0; j < 32; ++j) y[j] *= f[2 * (j >> 4) + ((j >> 1) & 1)];
+                                        us::tmem_st_frag32(o_tm + c, y);
+                                    }
+                                    us::tmem_wait_st();
+                                }
                             }
-                            weights(v, neg, Yes());
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) sum[q] = 0;
+                            auto weigh = [&](const float (&v)[32], int c, int k) {     // 8 positions
+                                const float4 sc = sc2[16 * c + 4 * k];
+                                const uint64_t s = fit ? pair(1.f, 1.f) : pair(sc.x, sc.y), m = pair(sc.z, sc.w);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const int at = 16 * (q >> 1) + 4 * k + 2 * (q & 1);
+                                    float x, y;
+                                    unpair(fma2(pair(v[at], v[at + 1]), s, neg[q]), x, y);
+                                    const uint64_t e = pair(ex2(x), ex2(y));
+                                    sum[q] = add2(sum[q], e);
+                                    unpair(mul2(e, m), x, y);
+                                    w[16 * (q >> 1) + 8 * c + 2 * k + (q & 1)] = pack_half2(x, y);
+                                }
+                            };
+                            // 32 positions at a time, the second ones loaded when half of the first are done
+                            uint32_t r[32];
+                            float v[32];
+                            us::tmem_ld_frag32(s_tm + 64 * a, v);
+                            weigh(v, 0, 0), weigh(v, 0, 1);
+                            us::tmem_ld_frag32_begin(s_tm + 64 * a + 32, r);
+                            weigh(v, 0, 2), weigh(v, 0, 3);
+                            us::tmem_ld_frag32_end(r, v);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) weigh(v, 1, k);
+                            if (fit) break;
+                            bool far = false;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                float x, y;
+                                unpair(sum[q], x, y);
+                                far |= !(fmaxf(x, y) <= kMost) || x != x || y != y;
+                            }
+                            if (!__any_sync(0xffffffffu, far)) break;
                         }
 #pragma unroll
                         for (int q = 0; q < 4; ++q) l2[q] = add2(l2[q], sum[q]);
@@ -366,6 +373,26 @@ attn_tc_kernel(const UsAttnParams p) {
             }
             // ---- the segment's end: the streams' sums and outputs
             const int srow = (warp & 3) * 32;              // the warp's first row of its stream
+            // the streams whose outputs the warp reads, and whether they had a tile
+            bool has[2];
+            // PV of the last tile of stream x (the tile before it is done: a parity tells
+            // only neighbouring phases apart); nothing reads its Q any more
+            auto finish = [&](int x, int tile) { wait(&H.pv_done[x][1], tile / kStep); };
+            if constexpr (NQ == 2) {
+                has[0] = true, has[1] = false;
+                finish(st, end - 1);
+            } else {
+                has[0] = end - it >= 2 || !(it & 1), has[1] = end - it >= 2 || (it & 1);
+                // the warp's own stream first: all but the last tile of the other come before it
+                const int own = ((end - 1) & 1) == st ? end - 1 : end - 2, other = 2 * end - 3 - own;
+                if (has[st]) finish(st, own);
+                if (has[st ^ 1]) finish(st ^ 1, other);
+            }
+            // (NQ = 2: a stream's Q is its own; else both streams are done)
+            auto ends = [&](int x) -> Ends& {
+                return *reinterpret_cast<Ends*>(NQ == 2 ? q_sm + x * Sh::kOperand : q_sm + x * sizeof(Ends));
+            };
+            __syncwarp();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float a, b;
@@ -373,34 +400,19 @@ attn_tc_kernel(const UsAttnParams p) {
                 a += b;
                 a += __shfl_xor_sync(0xffffffffu, a, 1);
                 a += __shfl_xor_sync(0xffffffffu, a, 2);
-                if (c2 == 0) H.xr[st][srow + 8 * q + g] = R[q], H.xl[st][srow + 8 * q + g] = a;
+                if (c2 == 0) ends(st).ref[srow + 8 * q + g] = R[q], ends(st).sum[srow + 8 * q + g] = a;
             }
-            // the streams whose outputs the warp reads, and whether they had a tile
-            bool has[2];
-            // PV of the last tile of stream x (the tile before it is done: a parity tells
-            // only neighbouring phases apart)
-            auto finish = [&](int x, int tile) { wait(&H.pv_done[x][1], tile / kStep); };
-            if constexpr (NQ == 2) {
-                has[0] = true, has[1] = false;
-                finish(st, end - 1);
-                __syncwarp();
-            } else {
-                has[0] = end - it >= 2 || !(it & 1), has[1] = end - it >= 2 || (it & 1);
-                // the warp's own stream first: all but the last tile of the other come before it
-                const int own = ((end - 1) & 1) == st ? end - 1 : end - 2, other = 2 * end - 3 - own;
-                if (has[st]) finish(st, own);
-                if (has[st ^ 1]) finish(st ^ 1, other);
-                us::named_bar_sync(1, 32 * kSoftWarps);
-            }
+            if constexpr (NQ == 2) __syncwarp();
+            else us::named_bar_sync(1, 32 * kSoftWarps);
             us::tc_fence_after();
             const int64_t s0 = H.work.t0 + it - tile0;
             const Part part = H.work.sharers(s0, s0 + cur.tiles, cur, rows);
             const bool whole = part.first == part.last;
             if (wrow < rows) {
                 const int row = wrow + lane, sr = srow + lane, s1 = NQ == 2 ? st : 0;
-                const float r0 = H.xr[s1][sr], r1 = NQ == 2 ? -INFINITY : H.xr[1][sr], top = fmaxf(r0, r1);
+                const float r0 = ends(s1).ref[sr], r1 = NQ == 2 ? -INFINITY : ends(1).ref[sr], top = fmaxf(r0, r1);
                 const float f0 = r0 == -INFINITY ? 0.f : ex2(r0 - top), f1 = r1 == -INFINITY ? 0.f : ex2(r1 - top);
-                const float sum = H.xl[s1][sr] * f0 + (NQ == 2 ? 0.f : H.xl[1][sr] * f1), inv = sum == 0.f ? 0.f : 1.f / sum;
+                const float sum = ends(s1).sum[sr] * f0 + (NQ == 2 ? 0.f : ends(1).sum[sr] * f1), inv = sum == 0.f ? 0.f : 1.f / sum;
                 float* slot = p.ws_slots + part.slot(blockIdx.x) * Sh::kSlotFloats;
                 if (!whole && (NQ == 2 || st == 0)) {
                     __stcg(slot + row, top);
@@ -597,10 +609,12 @@ attn_tc_kernel(const UsAttnParams p) {
             uint32_t sv = scale >> 16;
             const bool bad = (sv & 0x7C00u) == 0x7C00u;
             if (bad || lane >= left) sv = 0;
-            sv |= sv << 16;
+            const uint32_t vbits = __float_as_uint(us::half_bits_to_float((uint16_t)sv));      // (a subnormal scale too)
+            const float vp = __uint_as_float(vbits & 0x7F800000u), vm = __uint_as_float((vbits & 0x807FFFFFu) | 0x3F800000u);
+            const uint32_t vp2 = pack_half2(vp, vp);
             uint32_t vscale[2];                            // of the lane's rows
 #pragma unroll
-            for (int u = 0; u < 2; ++u) vscale[u] = __shfl_sync(0xffffffffu, sv, Sh::kC == 2 ? lane & 15 : 8 * u + (lane & 7));
+            for (int u = 0; u < 2; ++u) vscale[u] = __shfl_sync(0xffffffffu, vp2, Sh::kC == 2 ? lane & 15 : 8 * u + (lane & 7));
             lefts = lefts >> 8 | (uint32_t)fetch(slot) << (8 * (kRS - 1));       // its place is free
             slot = slot + 1 == kRS ? 0 : slot + 1;
             uint8_t* operand;
@@ -611,7 +625,11 @@ attn_tc_kernel(const UsAttnParams p) {
                 if (i >= kKS) wait(&H.k_free[i % kKS], i / kKS - 1);
                 operand = k_sm + (i % kKS) * Sh::kOperand;
                 const float sk = us::half_bits_to_float((uint16_t)scale) * (p.scale * 1.4426950408889634f);
-                if (lane < 16) H.ks[i % kSS][16 * block + lane] = bad ? __uint_as_float(0x7FC00000u) : sk;
+                if (lane < 16) {
+                    float* at = reinterpret_cast<float*>(H.scales[i % kSS]) + 32 * block + 4 * (lane >> 1) + (lane & 1);
+                    at[0] = bad ? __uint_as_float(0x7FC00000u) : sk;
+                    at[2] = vm;
+                }
                 if (lane == 0) H.valid[i % kSS][block] = left ? 0xFFFFu : 0u;
             }
             uint8_t* to = operand + block * 16 * 128 + put_base;
