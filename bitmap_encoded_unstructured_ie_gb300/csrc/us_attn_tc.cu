@@ -216,15 +216,22 @@ attn_tc_kernel(const UsAttnParams p) {
             us::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) us::mbar_arrive(&H.q_full);
+            // what the lane's rows see of the call's own positions: their masks, or in a chain how many
+            uint64_t own_seen[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = wrow + 8 * q + g, tok = (int)((unsigned)(cur.rb * kRows + r) / (unsigned)G);
+                own_seen[q] = r >= rows ? 0 : p.mask ? __ldg(p.mask + cur.r.row0 + tok) & (~0ull >> (64 - cur.r.n)) : (uint64_t)(tok + 1);
+            }
             // positions that a row sees among 32 from `base` behind the context
-            auto seen32 = [&](int base, uint64_t tree, int chain) {
+            auto seen32 = [&](int base, uint64_t row) {
                 if (base <= -32) return 0xFFFFFFFFu;
                 const int lo = base < 0 ? -base : 0;       // context positions among them
                 uint32_t own;
                 if (p.mask) {
-                    own = base < 64 ? (uint32_t)(tree >> (base > 0 ? base : 0)) : 0u;
+                    own = base < 64 ? (uint32_t)(row >> (base > 0 ? base : 0)) : 0u;
                 } else {
-                    const int k = chain - (base > 0 ? base : 0);
+                    const int k = (int)row - (base > 0 ? base : 0);
                     own = k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u;
                 }
                 return (own << lo) | (lo ? 0xFFFFFFFFu >> (32 - lo) : 0u);
@@ -274,10 +281,7 @@ attn_tc_kernel(const UsAttnParams p) {
                                     if (edge) {
 #pragma unroll
                                         for (int q = 0; q < 4; ++q) {
-                                            const int r = wrow + 8 * q + g, tok = (int)((unsigned)(cur.rb * kRows + r) / (unsigned)G);
-                                            const uint64_t mask = p.mask && r < rows ? p.mask[cur.r.row0 + tok] & (~0ull >> (64 - cur.r.n)) : 0ull;
-                                            const int own = r < rows ? tok + 1 : 0;    // a chain's row sees so many of the call
-                                            const uint32_t seen = (seen32(base + 32 * c, mask, own) & (c ? ok.y : ok.x)) >> c2;
+                                            const uint32_t seen = (seen32(base + 32 * c, own_seen[q]) & (c ? ok.y : ok.x)) >> c2;
 #pragma unroll
                                             for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -421,23 +425,31 @@ attn_tc_kernel(const UsAttnParams p) {
                 uint16_t* out = row < rows ? out_row<kRows>(p, cur.r.row0, cur.h, cur.rb, row, D) : nullptr;
                 // NQ = 1: each stream's warps put out half of the columns
                 const int c0 = NQ == 2 ? 0 : st * (D / 2), c1 = NQ == 2 ? D : c0 + D / 2;
+                constexpr int kCols = NQ == 2 ? 32 : 16;
 #pragma unroll 1
-                for (int c = c0; c < c1; c += 16) {
-                    float a[16], b[16];
+                for (int c = c0; c < c1; c += kCols) {
+                    float a[kCols];
+                    if constexpr (NQ == 2) {
+                        us::tmem_ld32(tmem + lanes + 256 + st * 128 + c, a);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) a[j] = b[j] = 0.f;
-                    if (has[0]) us::tmem_ld16(tmem + lanes + 256 + s1 * 128 + c, a);
-                    if (NQ == 1 && has[1]) us::tmem_ld16(tmem + lanes + 384 + c, b);
+                        for (int j = 0; j < kCols; ++j) a[j] = f0 == 0.f ? 0.f : a[j] * f0;
+                    } else {
+                        float b[kCols];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) a[j] = (f0 == 0.f ? 0.f : a[j] * f0) + (f1 == 0.f ? 0.f : b[j] * f1);
+                        for (int j = 0; j < kCols; ++j) a[j] = b[j] = 0.f;
+                        if (has[0]) us::tmem_ld16(tmem + lanes + 256 + c, a);
+                        if (has[1]) us::tmem_ld16(tmem + lanes + 384 + c, b);
+#pragma unroll
+                        for (int j = 0; j < kCols; ++j) a[j] = (f0 == 0.f ? 0.f : a[j] * f0) + (f1 == 0.f ? 0.f : b[j] * f1);
+                    }
                     if (whole) {
                         if (row < rows) {
-                            store8<ELEM>(out + c, a, inv);
-                            store8<ELEM>(out + c + 8, a + 8, inv);
+#pragma unroll
+                            for (int j = 0; j < kCols; j += 8) store8<ELEM>(out + c + j, a + j, inv);
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4)
+                        for (int j = 0; j < kCols; j += 4)
                             __stcg(reinterpret_cast<float4*>(slot + 2 * kRows) + (c + j) / 4 * kRows + row,
                                    make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]));
                     }
