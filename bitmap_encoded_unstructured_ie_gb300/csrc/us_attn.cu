@@ -205,6 +205,7 @@ attn_mma_kernel(const UsAttnParams p) {
     float* sm_inv = reinterpret_cast<float*>(sm_tok + kRows);                    // [kRows]
     __shared__ unsigned sh_last;
     __shared__ Part sh_part[2];
+    __shared__ Work sh_work;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
     const int G = p.G;
@@ -213,9 +214,9 @@ attn_mma_kernel(const UsAttnParams p) {
     // ---- this CTA's tiles
     Work wk;
     Cursor<kRows, Sh::kTile> cur;
-    if (!find_work<kRows, Sh::kTile, kThreads>(p, wk, cur)) return;
-    const int64_t t0 = wk.t0, t1 = wk.t1;
-    const int count = (int)(t1 - t0);
+    if (!find_work<kRows, Sh::kTile>(p, wk, cur)) return;
+    const int count = (int)(wk.t1 - wk.t0);
+    if (threadIdx.x == 0) sh_work = wk;                    // read at a segment's end: no registers for it meanwhile
 
     // ---- producer: the warp's positions of tile `pc` into stage s, 16 bytes a lane
     // at a time; the page numbers are loaded one tile ahead.
@@ -537,8 +538,8 @@ attn_mma_kernel(const UsAttnParams p) {
                 }
             __syncthreads();
             // segment [s0, s1) of the tile sequence, this CTA's part, who else has one
-            const int64_t s0 = t0 + it - cur.tile, s1 = s0 + cur.tiles;
-            const Part part = wk.sharers(s0, s1, cur, rows);
+            const int64_t s0 = sh_work.t0 + it - cur.tile, s1 = s0 + cur.tiles;
+            const Part part = sh_work.sharers(s0, s1, cur, rows);
             const bool whole = part.first == part.last;
             float* slot = p.ws_slots + part.slot(blockIdx.x) * Sh::kSlotFloats;
 #pragma unroll

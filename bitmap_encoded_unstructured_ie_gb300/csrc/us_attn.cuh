@@ -129,24 +129,37 @@ US_DEV int tiles_of(const UsAttnParams& p, const Request& r, int rb) {
     return (int)(((unsigned)r.ctx + end + TILE - 1u) / TILE);
 }
 
+// The request whose tokens are rows o0 .. o1 - 1, with `ctx` positions before them.
 template <int ROWS>
-US_DEV Request load_request(const UsAttnParams& p, int b, unsigned* status) {
-    Request r = {0, 0, 0, 0};
-    const int ctx = p.a.pos[b];                            // with the offsets, not after them
-    r.n = us::kv_rows(p.a, b, r.row0, status);
+US_DEV Request make_request(const UsAttnParams& p, int o0, int o1, int ctx, unsigned* status) {
+    Request r = {o0, us::kv_row_count(p.a, o0, o1, status), 0, 0};
     if (r.n > 0) {
         r.ctx = us::kv_context(p.c, ctx, r.n, status);
         if (r.ctx >= 0) r.nrb = (int)((unsigned)(r.n * p.G + ROWS - 1) / ROWS);
     }
     return r;
 }
+template <int ROWS>
+US_DEV Request load_request(const UsAttnParams& p, int b, unsigned* status) {
+    return make_request<ROWS>(p, p.a.off[b], p.a.off[b + 1], p.a.pos[b], status);
+}
 
-// Tiles of one key head of a request.
+// Tiles of one key head of a request.  A chain's row blocks are walked without
+// dividing: the tokens of (rb + 1) ROWS rows from those of rb ROWS.
 template <int ROWS, int TILE>
 US_DEV int64_t head_tiles(const UsAttnParams& p, const Request& r) {
-    if (p.mask) return r.nrb ? (int64_t)r.nrb * tiles_of<ROWS, TILE>(p, r, 0) : 0;
-    int64_t sum = 0;
-    for (int rb = 0; rb < r.nrb; ++rb) sum += tiles_of<ROWS, TILE>(p, r, rb);
+    if (r.nrb == 0) return 0;
+    const unsigned last = ((unsigned)r.ctx + (unsigned)r.n + TILE - 1u) / TILE;
+    if (p.mask) return (int64_t)r.nrb * last;
+    int64_t sum = last;
+    if (r.nrb > 1) {
+        const unsigned G = (unsigned)p.G, q = ROWS / G, m = ROWS % G;
+        for (unsigned rb = 1, end = 0, over = 0; rb < (unsigned)r.nrb; ++rb) {
+            end += q, over += m;
+            if (over >= G) over -= G, ++end;
+            sum += ((unsigned)r.ctx + end + (over ? 1u : 0u) + TILE - 1u) / TILE;
+        }
+    }
     return sum;
 }
 
@@ -187,34 +200,52 @@ struct Part {
     US_DEV int64_t slot(int cta) const { return (int64_t)2 * cta + (cta == first && second ? 1 : 0); }
 };
 
-// A CTA's share [t0, t1) of the sequence of `total` tiles spread over `ctas` CTAs.
+// A CTA's share [t0, t1) of the sequence of tiles: `per` tiles a CTA, one more for
+// the first `extra` of them.
 struct Work {
-    int64_t t0, t1, total, ctas;
+    int64_t t0, t1, per;
+    int extra;
+    US_DEV int64_t begin(int cta) const { return cta * per + min(cta, extra); }
+    US_DEV int owner(int64_t t) const {
+        const int64_t rest = t - extra * (per + 1);
+        return rest < 0 ? (int)quotient(t, per + 1) : extra + (int)quotient(rest, per);
+    }
     template <class C>
     US_DEV Part sharers(int64_t s0, int64_t s1, const C& at, int rows) const {
         Part a;
-        a.first = (int)quotient((s0 + 1) * ctas - 1, total);
-        a.last = (int)quotient(s1 * ctas - 1, total);
-        a.second = s0 > quotient(a.first * total, ctas);
+        a.first = owner(s0);
+        a.last = owner(s1 - 1);
+        a.second = s0 > begin(a.first);
         a.row0 = at.r.row0, a.h = at.h, a.rb = at.rb, a.rows = rows;
         return a;
     }
 };
 
-// The share of this CTA and where it begins: a block-wide scan of the requests'
-// tiles (all THREADS threads take part).  False if there is none for it.
-template <int ROWS, int TILE, int THREADS>
+// The share of this CTA and where it begins; false if there is none for it.  Each
+// warp finds it for itself, without a barrier: a lane adds up the tiles of B / 32
+// requests, a scan over the lanes finds the one with the share's first tile (4500
+// cycles by a scan over the block with 64-bit divisions, at 16 row blocks of a chain
+// 15000).
+template <int ROWS, int TILE>
 US_DEV bool find_work(const UsAttnParams& p, Work& w, Cursor<ROWS, TILE>& at) {
-    __shared__ Request sh_req;
-    __shared__ int64_t sh_x, sh_warp[THREADS / 32];
-    __shared__ int sh_b;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = (p.c.B + THREADS - 1) / THREADS, b0 = threadIdx.x * per;
-    int64_t mine = 0;
+    const int lane = threadIdx.x & 31;
+    unsigned* status = blockIdx.x == 0 && threadIdx.x < 32 ? p.c.status : nullptr;
+    const int each = (p.c.B + 31) / 32, b0 = lane * each, b1 = min(b0 + each, p.c.B);
+    int64_t mine = 0, head = 0;
     Request r = {0, 0, 0, 0};
-    for (int b = b0; b < min(b0 + per, p.c.B); ++b) {
-        r = load_request<ROWS>(p, b, blockIdx.x == 0 ? p.c.status : nullptr);
-        mine += head_tiles<ROWS, TILE>(p, r) * p.c.Hkv;
+    for (int b = b0; b < b1; b += 4) {                     // four requests' loads at once
+        int off[5], pos[4];
+#pragma unroll
+        for (int u = 0; u < 5; ++u) off[u] = b + u <= b1 ? p.a.off[b + u] : 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) pos[u] = b + u < b1 ? p.a.pos[b + u] : 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (b + u >= b1) break;
+            r = make_request<ROWS>(p, off[u], off[u + 1], pos[u], status);
+            head = head_tiles<ROWS, TILE>(p, r);
+            mine += head * p.c.Hkv;
+        }
     }
     int64_t incl = mine;
 #pragma unroll
@@ -222,42 +253,37 @@ US_DEV bool find_work(const UsAttnParams& p, Work& w, Cursor<ROWS, TILE>& at) {
         const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += o;
     }
-    if (lane == 31) sh_warp[warp] = incl;
-    __syncthreads();
-    int64_t total = 0, before = incl - mine;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-        if (i < warp) before += sh_warp[i];
-        total += sh_warp[i];
-    }
-    w.total = total;
-    w.ctas = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
-    if ((int64_t)blockIdx.x >= w.ctas) return false;
-    w.t0 = quotient(blockIdx.x * total, w.ctas), w.t1 = quotient((blockIdx.x + 1) * total, w.ctas);
-    if (before <= w.t0 && w.t0 < before + mine) {
-        for (int b = b0;; ++b) {
-            if (per > 1) r = load_request<ROWS>(p, b, nullptr);
-            const int64_t k = head_tiles<ROWS, TILE>(p, r) * p.c.Hkv;
-            if (w.t0 < before + k) {
-                sh_b = b;
-                sh_req = r;
-                sh_x = w.t0 - before;
-                break;
-            }
-            before += k;
+    const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
+    const int ctas = total < (int64_t)gridDim.x ? (int)total : (int)gridDim.x;
+    if ((int)blockIdx.x >= ctas) return false;
+    w.per = quotient(total, ctas);
+    w.extra = (int)(total - w.per * ctas);
+    w.t0 = w.begin((int)blockIdx.x), w.t1 = w.begin((int)blockIdx.x + 1);
+    int64_t x = w.t0 - (incl - mine);
+    const bool here = x >= 0 && x < mine;
+    int b = b0;
+    if (here && each > 1) {
+        for (;; ++b) {
+            r = load_request<ROWS>(p, b, nullptr);
+            head = head_tiles<ROWS, TILE>(p, r);
+            if (x < head * p.c.Hkv) break;
+            x -= head * p.c.Hkv;
         }
     }
-    __syncthreads();
-    at.b = sh_b;
-    at.r = sh_req;
-    const int64_t head = head_tiles<ROWS, TILE>(p, at.r);
-    at.h = (int)quotient(sh_x, head);
-    int64_t x = sh_x - at.h * head;
+    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    at.b = __shfl_sync(0xffffffffu, b, src);
+    at.r.row0 = __shfl_sync(0xffffffffu, r.row0, src);
+    at.r.n = __shfl_sync(0xffffffffu, r.n, src);
+    at.r.ctx = __shfl_sync(0xffffffffu, r.ctx, src);
+    at.r.nrb = __shfl_sync(0xffffffffu, r.nrb, src);
+    x = __shfl_sync(0xffffffffu, x, src);
+    head = __shfl_sync(0xffffffffu, head, src);
+    at.h = 0;
+    if (x >= head) at.h = (int)quotient(x, head), x -= at.h * head;
     at.rb = 0;
     at.tiles = tiles_of<ROWS, TILE>(p, at.r, 0);
     if (p.mask) {
-        at.rb = (int)quotient(x, at.tiles);
-        x -= (int64_t)at.rb * at.tiles;
+        if (x >= at.tiles) at.rb = (int)quotient(x, at.tiles), x -= (int64_t)at.rb * at.tiles;
     } else {
         while (x >= at.tiles) {
             x -= at.tiles;

@@ -166,11 +166,12 @@ attn_tc_kernel(const UsAttnParams p) {
         us::fence_mbar_init();
     }
     if (warp == kSoftWarps) us::tmem_alloc(&H.tmem, 512);
+    __syncthreads();
     us::pdl_wait();
 
     Work wk;
     Cur cur;
-    const bool any = find_work<kRows, kTile, kThreads>(p, wk, cur);       // its barrier covers the set-up above
+    const bool any = find_work<kRows, kTile>(p, wk, cur);
     if (threadIdx.x == 0) H.work = wk;                     // the softmax warps need it at a segment's end
     us::tc_fence_after();
     const uint32_t tmem = H.tmem;                          // S0, S1, O0, O1: 128 columns each
@@ -197,15 +198,19 @@ attn_tc_kernel(const UsAttnParams p) {
             // Q: a thread takes one 16-byte chunk of every kQR-th row, up to 16 loads at once
             constexpr int kQR = 32 * kSoftWarps / (D / 8), kAtOnce = kRows / kQR < 16 ? kRows / kQR : 16;
             const int q_row = threadIdx.x / (D / 8), q_chunk = threadIdx.x % (D / 8);
+            // (row q_row + k kQR: token q_tok, query head q_head of the key head's)
+            const int q_dtok = (int)((unsigned)kQR / (unsigned)G), q_dhead = kQR - q_dtok * G, q_first = cur.rb * kRows + q_row;
+            int q_tok = (int)((unsigned)q_first / (unsigned)G), q_head = q_first - q_tok * G;
 #pragma unroll 1
             for (int r0 = q_row; r0 < kRows; r0 += kAtOnce * kQR) {
                 uint4 u[kAtOnce];
 #pragma unroll
                 for (int k = 0; k < kAtOnce; ++k) {
-                    const int r = r0 + k * kQR, rr = cur.rb * kRows + r, i = (int)((unsigned)rr / (unsigned)G);
                     u[k] = make_uint4(0, 0, 0, 0);
-                    if (r < rows)
-                        u[k] = __ldg(reinterpret_cast<const uint4*>(p.Q + (int64_t)(cur.r.row0 + i) * p.ldq + (int64_t)(cur.h * G + rr - i * G) * D) + q_chunk);
+                    if (r0 + k * kQR < rows)
+                        u[k] = __ldg(reinterpret_cast<const uint4*>(p.Q + (int64_t)(cur.r.row0 + q_tok) * p.ldq + (int64_t)(cur.h * G + q_head) * D) + q_chunk);
+                    q_tok += q_dtok, q_head += q_dhead;
+                    if (q_head >= G) q_head -= G, ++q_tok;
                 }
 #pragma unroll
                 for (int k = 0; k < kAtOnce; ++k) {

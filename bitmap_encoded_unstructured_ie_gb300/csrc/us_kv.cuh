@@ -50,12 +50,14 @@ struct UsAttnParams {
 namespace us {
 
 // Rows of request b: first row and count (0 if the offsets are not usable).
-US_DEV int kv_rows(const UsKvCall& a, int b, int& row0, unsigned* status) {
-    const int o0 = a.off[b], o1 = a.off[b + 1];
-    row0 = o0;
+US_DEV int kv_row_count(const UsKvCall& a, int o0, int o1, unsigned* status) {
     if (o0 >= 0 && o1 >= o0 && o1 <= a.T && o1 - o0 <= a.max_n) return o1 - o0;
     set_status(status, US_ERR_INVALID_ARG);
     return 0;
+}
+US_DEV int kv_rows(const UsKvCall& a, int b, int& row0, unsigned* status) {
+    row0 = a.off[b];
+    return kv_row_count(a, row0, a.off[b + 1], status);
 }
 
 // Page of position p of request b, or -1 (recorded) if there is none.
