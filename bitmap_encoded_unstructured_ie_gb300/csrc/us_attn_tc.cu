@@ -678,56 +678,57 @@ attn_tc_kernel(const UsAttnParams p) {
     us::pdl_launch_dependents();
 }
 
-// Joins the partial states of shared segments: CTA (x, c) the rows from 32 x of the
-// segment whose first sharer was CTA c, if there is one.  A thread takes 16 columns
-// of a row, four states' loads on their way at once.  A launch of its own: joined by
-// one of the sharers, a segment's states (131 KB each at 256 rows of 128) came at
-// the 76 GB/s that one SM draws from L2.
-constexpr int kJoinRows = 32;
+// Joins the partial states of shared segments: CTA (x, c) 16 rows from 16 x of the
+// segment whose first sharer was CTA c, if there is one.  A thread takes 8 columns
+// of a row; its loads of two states are on their way at once, and six CTAs an SM (40
+// registers) leave few waves of the 16 x 152 (eight states at once, two CTAs an SM:
+// 10 us more for a chunk of 512 tokens).  A launch of its own: joined by one of the
+// sharers, a segment's states (131 KB each at 256 rows of 128) came at the 76 GB/s
+// that one SM draws from L2.
+constexpr int kJoinRows = 16, kAtOnce = 2;        // rows of a CTA, states a thread loads at once
 template <int ELEM, int D, int NQ>
-__global__ void __launch_bounds__(kJoinRows * D / 16)
+__global__ void __launch_bounds__(kJoinRows * D / 8, 768 / D)
 attn_tc_join_kernel(const UsAttnParams p) {
     using Sh = Shape<ELEM, D, NQ>;
     constexpr int kRows = Sh::kRows;
     us::pdl_wait();
     const Part a = p.ws_parts[blockIdx.y];
-    const int row = blockIdx.x * kJoinRows + (threadIdx.x & 31), col = threadIdx.x / 32 * 16;
+    const int row = blockIdx.x * kJoinRows + threadIdx.x % kJoinRows, col = threadIdx.x / kJoinRows * 8;
     if (row < a.rows) {
-        const int np = a.last - a.first + 1;
-        auto slot = [&](int c) { return p.ws_slots + a.slot(a.first + c) * Sh::kSlotFloats; };
-        float top = -INFINITY, sum = 0.f, y[16];
+        float top = -INFINITY, sum = 0.f, y[8] = {};
+        for (int c = a.first; c <= a.last; c += kAtOnce) {
+            float4 v[kAtOnce][2];
+            float r[kAtOnce], l[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = 0.f;
-#pragma unroll 8
-        for (int c = 0; c < np; ++c) top = fmaxf(top, __ldcg(slot(c) + row));
-        for (int c = 0; c < np; c += 4) {
-            float4 v[4][4];
-            float r[4], l[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float* sl = slot(c + u < np ? c + u : c);
+            for (int u = 0; u < kAtOnce; ++u) {
+                const float* sl = p.ws_slots + a.slot(min(c + u, a.last)) * Sh::kSlotFloats;
                 const float4* o = reinterpret_cast<const float4*>(sl + 2 * kRows) + col / 4 * kRows + row;
-                r[u] = c + u < np ? __ldcg(sl + row) : -INFINITY;
+                r[u] = __ldcg(sl + row);
                 l[u] = __ldcg(sl + kRows + row);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[u][i] = __ldcg(o + i * kRows);
+                v[u][0] = __ldcg(o), v[u][1] = __ldcg(o + kRows);
             }
+            float m = top;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (r[u] == -INFINITY) continue;
-                const float f = ex2(r[u] - top);
+            for (int u = 0; u < kAtOnce; ++u) m = fmaxf(m, r[u]);
+            if (m == -INFINITY) continue;
+            const float f0 = ex2(top - m);
+            sum *= f0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] *= f0;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                if (c + u > a.last || r[u] == -INFINITY) continue;
+                const float f = ex2(r[u] - m);
                 sum += l[u] * f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     y[4 * i] += v[u][i].x * f, y[4 * i + 1] += v[u][i].y * f;
                     y[4 * i + 2] += v[u][i].z * f, y[4 * i + 3] += v[u][i].w * f;
                 }
             }
+            top = m;
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint16_t* out = out_row<kRows>(p, a.row0, a.h, a.rb, row, D) + col;
-        store8<ELEM>(out, y, inv);
-        store8<ELEM>(out + 8, y + 8, inv);
+        store8<ELEM>(out_row<kRows>(p, a.row0, a.h, a.rb, row, D) + col, y, sum == 0.f ? 0.f : 1.f / sum);
     }
     us::pdl_launch_dependents();
 }
@@ -763,7 +764,7 @@ us_status launch(UsAttnParams p, cudaStream_t st) {
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return US_ERR_CUDA;
     cfg.gridDim = dim3(Sh::kRows / kJoinRows, (unsigned)grid());
-    cfg.blockDim = dim3(kJoinRows * D / 16);
+    cfg.blockDim = dim3(kJoinRows * D / 8);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<ELEM, D, NQ>, p) == cudaSuccess ? US_OK : US_ERR_CUDA;
 }
