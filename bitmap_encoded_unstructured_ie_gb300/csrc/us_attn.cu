@@ -48,8 +48,16 @@ struct Shape {
     static constexpr int kVW = kRow / 32;                           // ... of a V row (its D/8 dimensions)
     static constexpr int kKS = D / 16;                              // MMA steps over the dimensions
     static constexpr int kMT = D / 16;                              // 16-dimension blocks of O^T
-    static constexpr int kMinB = W == 8 ? 2 : 3;                  // CTAs an SM
-    static constexpr int kSub = kRow == 128 || NT == 4 ? 1 : 2;     // 16-position blocks of a warp's step
+    // CTAs an SM.  Rows of 128 dimensions, and 17 to 32 rows of 64, need more than the
+    // 168 registers that three CTAs of four warps leave (16 trees of 4 tokens, 4 query
+    // heads to a key head, behind 4095 positions, int4: 34 us with two CTAs, 43 with
+    // three; 12 trees of 13 to 25, 64 dimensions, int8: 66 and 72); 9 to 16 rows of 64
+    // do not (trees of up to 12: 47 and 41).
+    static constexpr int kMinB = W == 8 || NT == 4 || D == 128 ? 2 : 3;
+    // 16-position blocks of a warp's step: with two there are twice as many MMAs that do
+    // not wait for each other (4 tokens of two requests of 131000 positions, int8: 90 us
+    // against 103), where the registers hold their codes.
+    static constexpr int kSub = kRow == 128 && NT == 1 ? 1 : 2;
     static constexpr int kStep = kSub * kBlock;
     static constexpr int kTile = kWarps * kStep;                    // positions of a CTA's step
     static constexpr int kStageBytes = 2 * kStep * kRow + kStep * 4;
