@@ -98,23 +98,27 @@ US_DEV void store_codes(uint8_t* dst, uint2 w) {
     else *reinterpret_cast<uint32_t*>(dst) = w.x;
 }
 
-// The tokens of one CTA of write and read, [i0, i1) of request b: their first
-// row, and their entries' page and slot (head 0), -1 where there is none.
+// The tokens of one CTA of write and read, [i0, i1) of request b, and their first
+// row.
 struct Tokens {
-    int i0, i1, row0;
+    int i0, i1, row0, pos;
 };
-US_DEV Tokens find_tokens(const UsKvCache& c, const UsKvCall& a, int tokens, int64_t* place) {
+US_DEV Tokens find_tokens(const UsKvCache& c, const UsKvCall& a, int tokens) {
     Tokens t;
-    const int b = blockIdx.y, pos = a.pos[b];
+    const int b = blockIdx.y;
+    t.pos = a.pos[b];
     const int n = us::kv_rows(a, b, t.row0, c.status);
     t.i0 = blockIdx.x * tokens, t.i1 = min(n, t.i0 + tokens);
+    return t;
+}
+// Their entries' page and slot (head 0), -1 where there is none; ends with a barrier.
+US_DEV void find_places(const UsKvCache& c, const Tokens& t, int64_t* place) {
     const int i = t.i0 + (int)threadIdx.x;
     if (i < t.i1) {
-        const int p = us::kv_pos(pos, i), id = us::kv_page(c, b, p);
+        const int p = us::kv_pos(t.pos, i), id = us::kv_page(c, blockIdx.y, p);
         place[threadIdx.x] = id < 0 ? -1 : us::kv_entry(c, id, 0, p);
     }
     __syncthreads();
-    return t;
 }
 
 // D/8 lanes per (token, head), 16 bytes of K and of V each; heads run fastest, so
@@ -127,8 +131,9 @@ kv_write_kernel(const UsKvCache c, const UsKvCall a, int tokens, const uint16_t*
     constexpr int kLanes = D / 8, kRows = kThreads / kLanes, kBytes = D * (ELEM == US_I8 ? 8 : 4) / 8;
     __shared__ int64_t place[kTokens];
     us::pdl_wait();
-    const Tokens tk = find_tokens(c, a, tokens, place);
+    const Tokens tk = find_tokens(c, a, tokens);
     const int j = threadIdx.x % kLanes, rows = (tk.i1 - tk.i0) * c.Hkv;
+    bool first = true;
     for (int r0 = threadIdx.x / kLanes; r0 - (int)threadIdx.x / kLanes < rows; r0 += kAtOnce * kRows) {
         uint4 k[kAtOnce], v[kAtOnce];
         int tok[kAtOnce], h[kAtOnce];
@@ -143,6 +148,7 @@ kv_write_kernel(const UsKvCache c, const UsKvCall a, int tokens, const uint16_t*
                 v[u] = __ldcs(reinterpret_cast<const uint4*>(V + t * ldv + h[u] * D + 8 * j));
             }
         }
+        if (first) find_places(c, tk, place), first = false;   // while the rows are on their way
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
             if (u && r0 - (int)threadIdx.x / kLanes + u * kRows >= rows) break;
@@ -189,7 +195,8 @@ kv_read_kernel(const UsKvCache c, const UsKvCall a, int tokens, uint16_t* __rest
     constexpr int kLanes = D / 8, kRows = kThreads / kLanes, kBytes = D * (ELEM == US_I8 ? 8 : 4) / 8;
     __shared__ int64_t place[kTokens];
     us::pdl_wait();
-    const Tokens tk = find_tokens(c, a, tokens, place);
+    const Tokens tk = find_tokens(c, a, tokens);
+    find_places(c, tk, place);
     const int j = threadIdx.x % kLanes, rows = (tk.i1 - tk.i0) * c.Hkv;
     for (int r0 = threadIdx.x / kLanes; r0 < rows; r0 += kAtOnce * kRows) {
         uint2 k[kAtOnce], v[kAtOnce];
