@@ -229,7 +229,8 @@ kv_read_kernel(const UsKvCache c, const UsKvCall a, int tokens, uint16_t* __rest
 }
 
 // One CTA per (head, request): the listed entries of K, of V and the scales are
-// read into shared memory, then written, so that a path may overlap itself.
+// read into shared memory, then written, so that a path may overlap itself.  As many
+// threads as there are 16-byte pieces of K, so that more CTAs wait side by side.
 __global__ void __launch_bounds__(kThreads)
 kv_commit_kernel(const UsKvCache c, const UsKvCall a, const int32_t* __restrict__ acc) {
     extern __shared__ __align__(16) uint8_t held[];
@@ -239,7 +240,7 @@ kv_commit_kernel(const UsKvCache c, const UsKvCall a, const int32_t* __restrict_
     int row0;
     const int n = us::kv_rows(a, b, row0, c.status), chunks = c.row_bytes / 16;
     uint32_t* held_s = reinterpret_cast<uint32_t*>(held + (size_t)a.max_n * 2 * c.row_bytes);
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const int p0 = a.pos[b], d = acc[row0 + i];
         const int sp = d >= 0 ? us::kv_pos(p0, d) : -1, dp = us::kv_pos(p0, i);
         const int si = us::kv_page(c, b, sp), di = us::kv_page(c, b, dp);
@@ -251,7 +252,7 @@ kv_commit_kernel(const UsKvCache c, const UsKvCall a, const int32_t* __restrict_
     uint4* hv = reinterpret_cast<uint4*>(held);
     const uint4* k4 = reinterpret_cast<const uint4*>(c.k);
     const uint4* v4 = reinterpret_cast<const uint4*>(c.v);
-    for (int x = threadIdx.x; x < n * chunks; x += kThreads) {
+    for (int x = threadIdx.x; x < n * chunks; x += blockDim.x) {
         const int i = x / chunks, j = x - i * chunks;
         if (from[i] < 0) continue;
         hv[2 * x] = k4[from[i] * chunks + j];
@@ -259,7 +260,7 @@ kv_commit_kernel(const UsKvCache c, const UsKvCall a, const int32_t* __restrict_
         if (j == 0) held_s[i] = reinterpret_cast<const uint32_t*>(c.scale)[from[i]];
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < n * chunks; x += kThreads) {
+    for (int x = threadIdx.x; x < n * chunks; x += blockDim.x) {
         const int i = x / chunks, j = x - i * chunks;
         if (from[i] < 0) continue;
         reinterpret_cast<uint4*>(c.k)[to[i] * chunks + j] = hv[2 * x];
@@ -270,10 +271,10 @@ kv_commit_kernel(const UsKvCache c, const UsKvCall a, const int32_t* __restrict_
 }
 
 template <class Kern, class... Args>
-us_status launch(Kern kern, dim3 grid, size_t smem, cudaStream_t st, Args... args) {
+us_status launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -305,19 +306,20 @@ us_status launch_kv_write(const UsKvCache& c, const UsKvCall& a, const uint16_t*
                           int64_t ldv, cudaStream_t st) {
     auto kern = c.elem == US_I8 ? (c.D == 64 ? kv_write_kernel<US_I8, 64> : kv_write_kernel<US_I8, 128>)
                                 : (c.D == 64 ? kv_write_kernel<US_I4, 64> : kv_write_kernel<US_I4, 128>);
-    return launch(kern, row_grid(c, a), 0, st, c, a, cta_tokens(c, a), K, ldk, V, ldv);
+    return launch(kern, row_grid(c, a), kThreads, 0, st, c, a, cta_tokens(c, a), K, ldk, V, ldv);
 }
 
 us_status launch_kv_read(const UsKvCache& c, const UsKvCall& a, uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv,
                          cudaStream_t st) {
     auto kern = c.elem == US_I8 ? (c.D == 64 ? kv_read_kernel<US_I8, 64> : kv_read_kernel<US_I8, 128>)
                                 : (c.D == 64 ? kv_read_kernel<US_I4, 64> : kv_read_kernel<US_I4, 128>);
-    return launch(kern, row_grid(c, a), 0, st, c, a, cta_tokens(c, a), K, ldk, V, ldv);
+    return launch(kern, row_grid(c, a), kThreads, 0, st, c, a, cta_tokens(c, a), K, ldk, V, ldv);
 }
 
 us_status launch_kv_commit(const UsKvCache& c, const UsKvCall& a, const int32_t* acc, cudaStream_t st) {
     const size_t smem = (size_t)a.max_n * (2 * c.row_bytes + 4);
-    return launch(kv_commit_kernel, dim3((unsigned)c.Hkv, (unsigned)c.B), smem, st, c, a, acc);
+    const int pieces = (a.max_n * (c.row_bytes / 16) + 31) / 32 * 32, threads = pieces < 64 ? 64 : pieces > kThreads ? kThreads : pieces;
+    return launch(kv_commit_kernel, dim3((unsigned)c.Hkv, (unsigned)c.B), threads, smem, st, c, a, acc);
 }
 
 }  // namespace us
