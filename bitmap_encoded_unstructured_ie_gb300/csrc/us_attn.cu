@@ -24,12 +24,19 @@
 // read in place as 16 u, have their own accumulator.  V's codes are made signed
 // first: an output may be far smaller than the offset's rounding in its sum.
 //
-// Work: the (request, key head, row block) segments are cut into tiles of 64 or
-// 128 positions, and the tile sequence is spread evenly over the CTAs, whatever
-// the lengths (they are read on the device).  A warp takes 16 or 32 positions of
-// each tile, copied into the warp's own ring several tiles ahead and across
-// segments (a page's entries of one head are contiguous).  A segment shared by several CTAs leaves partial states in the
-// workspace; the CTA that arrives last joins them in the order of the tiles.
+// Work: the (request, key head, row block) segments are cut into tiles of 64 to 256
+// positions, and the tile sequence is spread evenly over the CTAs, whatever the
+// lengths (they are read on the device).  A warp takes 16 or 32 positions of each
+// tile, copied into the warp's own ring several tiles ahead and across segments (a
+// page's entries of one head are contiguous).  A segment shared by several CTAs leaves
+// partial states in the workspace; the CTA that arrives last joins them in the order
+// of the tiles.
+//
+// What bounds it: at one token of a long context HBM (two requests of 131000
+// positions, int8: 5.3 TB/s of a cache that streams once), with more requests the
+// instructions of the codes' conversion (48 requests of 4096 to 8192, int4: ALU pipe
+// 47 % and issue slots 54 % busy, 3.8 TB/s), with one short request latency (9.5 us
+// for 777 positions: starting, finding the work, three trips to memory, the join).
 #include "us_attn.cuh"
 #include "us_internal.h"
 
@@ -676,11 +683,9 @@ struct Plan {
 };
 
 // f(Plan) for the cache's type and head width and the rows per key head.  Eight
-// warps a CTA, two CTAs an SM, for up to 8 rows: on one token of two 131000-
-// position requests 83.5 us (four CTAs of four warps: 88.7, one of 16: 82.4), on
-// 48 requests of 4096 to 8192 positions in int4 86.8 (85.4, 94.3), on one of 777
-// 9.5 (9.8, 11.4): fewer CTAs leave fewer partial states to join, more keep
-// working while one starts a segment.
+// warps a CTA, two CTAs an SM, for up to 8 rows: on 48 requests of 4096 to 8192
+// positions in int4 82 us (92 with two CTAs of four warps and twice the positions a
+// step), on one token of two requests of 131000 78 (78), on one of 777 9.5 (9.3).
 template <class F>
 auto with_plan(const UsAttnParams& p, F f) {
     const int rows = p.a.max_n * p.G;

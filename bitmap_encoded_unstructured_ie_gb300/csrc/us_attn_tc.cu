@@ -678,46 +678,68 @@ attn_tc_kernel(const UsAttnParams p) {
     us::pdl_launch_dependents();
 }
 
-// Joins the partial states of shared segments: CTA (x, c) 16 rows from 16 x of the
-// segment whose first sharer was CTA c, if there is one.  A thread takes 8 columns
-// of a row; its loads of two states are on their way at once, and six CTAs an SM (40
-// registers) leave few waves of the 16 x 152 (eight states at once, two CTAs an SM:
-// 10 us more for a chunk of 512 tokens).  A launch of its own: joined by one of the
-// sharers, a segment's states (131 KB each at 256 rows of 128) came at the 76 GB/s
-// that one SM draws from L2.
-constexpr int kJoinRows = 16, kAtOnce = 2;        // rows of a CTA, states a thread loads at once
-template <int ELEM, int D, int NQ>
-__global__ void __launch_bounds__(kJoinRows * D / 8, 768 / D)
-attn_tc_join_kernel(const UsAttnParams p) {
+// Joins the partial states of shared segments, 16 rows of one at a time: CTAs take
+// such pieces in turn from the list of shared segments, which each makes for itself
+// (part c: the segment whose first sharer was CTA c, if there is one).  A thread takes
+// 8 columns of a row; its loads of AT states are on their way at once.  A launch of
+// its own: joined by one of the sharers, a segment's states (131 KB each at 256 rows
+// of 128) came at the 76 GB/s that one SM draws from L2.
+// Few segments have many sharers each: eight states at once (a tree of 32 to 64
+// tokens of one request behind 4000 positions: 18 us with the attention, 31 with two
+// at once).  Many have about two: two at once, and three times as many CTAs (chunk of
+// 512: 177 us, 183 with eight).
+constexpr int kJoinRows = 16, kMaxCtas = 512;
+constexpr int join_ctas(int at, int D) { return (at == 8 ? 256 : 768) / D; }       // an SM
+template <int ELEM, int D, int NQ, int AT>
+__global__ void __launch_bounds__(kJoinRows * D / 8, join_ctas(AT, D))
+attn_tc_join_kernel(const UsAttnParams p, int ctas) {
     using Sh = Shape<ELEM, D, NQ>;
-    constexpr int kRows = Sh::kRows;
+    constexpr int kRows = Sh::kRows, kPieces = kRows / kJoinRows;
+    __shared__ uint16_t list[kMaxCtas];
+    __shared__ int listed;
     us::pdl_wait();
-    const Part a = p.ws_parts[blockIdx.y];
-    const int row = blockIdx.x * kJoinRows + threadIdx.x % kJoinRows, col = threadIdx.x / kJoinRows * 8;
-    if (row < a.rows) {
+    if (threadIdx.x < 32) {
+        int n = 0;
+        for (int c0 = 0; c0 < ctas; c0 += 32) {
+            const int c = c0 + (int)threadIdx.x;
+            const bool shared = c < ctas && p.ws_parts[c].rows > 0;
+            const unsigned who = __ballot_sync(0xffffffffu, shared);
+            if (shared) list[n + __popc(who & ((1u << threadIdx.x) - 1u))] = (uint16_t)c;
+            n += __popc(who);
+        }
+        if (threadIdx.x == 0) listed = n;
+    }
+    __syncthreads();
+    for (int x = blockIdx.x; x < listed * kPieces; x += gridDim.x) {
+        const Part a = p.ws_parts[list[x / kPieces]];
+        const int row = x % kPieces * kJoinRows + threadIdx.x % kJoinRows, col = threadIdx.x / kJoinRows * 8;
+        if (row >= a.rows) continue;
         float top = -INFINITY, sum = 0.f, y[8] = {};
-        for (int c = a.first; c <= a.last; c += kAtOnce) {
-            float4 v[kAtOnce][2];
-            float r[kAtOnce], l[kAtOnce];
+        for (int c = a.first; c <= a.last; c += AT) {
+            float4 v[AT][2];
+            float r[AT], l[AT];
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const float* sl = p.ws_slots + a.slot(min(c + u, a.last)) * Sh::kSlotFloats;
+            for (int u = 0; u < AT; ++u) {
+                const float* sl = p.ws_slots + a.slot(c + u) * Sh::kSlotFloats;
                 const float4* o = reinterpret_cast<const float4*>(sl + 2 * kRows) + col / 4 * kRows + row;
-                r[u] = __ldcg(sl + row);
-                l[u] = __ldcg(sl + kRows + row);
-                v[u][0] = __ldcg(o), v[u][1] = __ldcg(o + kRows);
+                r[u] = -INFINITY;
+                if (c + u <= a.last) {
+                    r[u] = __ldcg(sl + row);
+                    l[u] = __ldcg(sl + kRows + row);
+                    v[u][0] = __ldcg(o), v[u][1] = __ldcg(o + kRows);
+                }
             }
             float m = top;
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) m = fmaxf(m, r[u]);
+            for (int u = 0; u < AT; ++u) m = fmaxf(m, r[u]);
             if (m == -INFINITY) continue;
             const float f0 = ex2(top - m);
             sum *= f0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] *= f0;
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                if (c + u > a.last || r[u] == -INFINITY) continue;
+            for (int u = 0; u < AT; ++u) {
+                if (r[u] == -INFINITY) continue;
                 const float f = ex2(r[u] - m);
                 sum += l[u] * f;
 #pragma unroll
@@ -733,8 +755,8 @@ attn_tc_join_kernel(const UsAttnParams p) {
     us::pdl_launch_dependents();
 }
 
-int grid() { return us::num_sms() < 512 ? us::num_sms() : 512; }
-constexpr int kPartBytes = 4096 + 512 * 32;       // counters, parts
+int grid() { return us::num_sms() < kMaxCtas ? us::num_sms() : kMaxCtas; }
+constexpr int kPartBytes = 4096 + kMaxCtas * 32;       // counters, parts
 static_assert(sizeof(Part) <= 32, "parts");
 
 template <int ELEM, int D, int NQ>
@@ -763,20 +785,24 @@ us_status launch(UsAttnParams p, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return US_ERR_CUDA;
-    cfg.gridDim = dim3(Sh::kRows / kJoinRows, (unsigned)grid());
+    const int64_t segments = (((int64_t)p.a.max_n * p.G + Sh::kRows - 1) / Sh::kRows) * p.c.Hkv * p.c.B;      // at most
+    const bool few = 4 * segments <= grid();
+    cfg.gridDim = dim3((unsigned)(join_ctas(few ? 8 : 2, D) * us::num_sms()));
     cfg.blockDim = dim3(kJoinRows * D / 8);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<ELEM, D, NQ>, p) == cudaSuccess ? US_OK : US_ERR_CUDA;
+    auto join = few ? attn_tc_join_kernel<ELEM, D, NQ, 8> : attn_tc_join_kernel<ELEM, D, NQ, 2>;
+    return cudaLaunchKernelEx(&cfg, join, p, grid()) == cudaSuccess ? US_OK : US_ERR_CUDA;
 }
 
 }  // namespace
 
 namespace us {
 
-// From 17 rows per key head of 128 dimensions, 33 of 64: below, the mma.sync kernel
-// is faster (16 requests of 4000 positions, int4: 32 rows of 64 dimensions 38 us
-// there, 52 here; 32 rows of 128 59 and 61, of one request 27 and 23).
-bool attn_tc_serves(const UsAttnParams& p) { return (int64_t)p.a.max_n * p.G > (p.c.D == 64 ? 32 : 16); }
+// From 33 rows per key head: below, the mma.sync kernel holds a segment's rows at
+// once and is faster, above it reads the cache again for the next 32 (16 for 128
+// dimensions).  16 requests of 4000 positions, int4: 32 rows of 128 dimensions 48 us
+// there, 55 here, 36 rows 64 and 58; of 64 dimensions 32 and 51, then 50 and 51.
+bool attn_tc_serves(const UsAttnParams& p) { return (int64_t)p.a.max_n * p.G > 32; }
 
 size_t attn_tc_ws(const UsAttnParams& p) {
     const size_t rows = (int64_t)p.a.max_n * p.G > kM ? 2 * kM : kM;
