@@ -33,9 +33,10 @@
 // are kept short (one copy of each body): four warps of a scheduler run three
 // different programs, and fetching them was a sixth of its time.
 // Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set,
-// and moves only when a weight could pass 2^14.9 (fp16 keeps 2^-14 of them exactly as
-// it does the largest).  R, sums and outputs of a segment shared by several CTAs are
-// joined by a second kernel.
+// and moves when eight weights of a lane sum to more than 2^14.9, which no fp16 weight
+// times m < 2 may reach, or a masked tile has a larger maximum (at 2^11 and above,
+// fp16 keeps all of its bits down to 2^-25 of a weight).  R, sums and outputs of a
+// segment shared by several CTAs are joined by a second kernel.
 //
 // What bounds it.  A tile of 256 rows takes about 5200 cycles: the tensor pipe is busy
 // for 33 % (48 MMAs of 64 cycles; a score MMA of 64 positions reads 6 KB of shared
@@ -59,7 +60,7 @@ constexpr int kSoftWarps = 8, kMmaWarp = 8, kConvWarps = 7;
 constexpr int kThreads = 32 * (kSoftWarps + 1 + kConvWarps);
 constexpr int kItems = 16;                        // of a tile: 8 of K, then 8 of V
 constexpr int kKS = 2, kSS = 4;                   // stages: K, scales (V: Shape::kVS)
-constexpr float kTop = 11.f, kMost = 30573.f;     // a row's largest weight is 2^11 at first, 2^14.9 at most (times m: fp16)
+constexpr float kTop = 11.f, kMost = 30573.f;     // log2 of a row's largest weight when R is set; 2^14.9
 
 struct Header {
     uint64_t k_full[kKS], k_free[kKS], v_full[3], v_free[3], s_full[kSS];
