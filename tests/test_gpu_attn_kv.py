@@ -283,3 +283,24 @@ def test_bad_lengths_and_pages_are_recorded(us):
     s.ref.table[0, 1:-1], s.ref.table[0, -1] = s.ref.table[0, 2:], -1
     s.ctx[0] = 24
     s.check(got, grids, only={0})
+
+
+@pytest.mark.parametrize("elem,D,G,n", [(kv.I4, 64, 1, 64), (kv.I8, 128, 4, 40), (kv.I8, 128, 4, 6), (kv.I4, 64, 3, 9)])
+def test_states_of_many_ctas(us, elem, D, G, n):
+    """One request whose tiles go to a CTA each: two dozen or more partial states a row."""
+    s = Setup(us, elem, D, 1, G, 64, [2900], [n], 25)
+    words, grids = s.tree()
+    s.check(s.run(words), grids)
+
+
+@pytest.mark.parametrize("D,G,n", [(128, 4, 1), (128, 4, 6), (64, 4, 8), (64, 4, 16), (128, 4, 40)])
+def test_scores_that_rise_along_the_context(us, D, G, n):
+    """Keys that grow tile after tile: the largest score moves all the way, and with it what came before."""
+    s = Setup(us, kv.I8, D, 2, G, 32, [900, 50], [n, n], 26)
+    for b, (c, k) in enumerate(zip(s.ctx, s.n)):
+        for p in range(c + k):
+            g, slot = s.ref.at(b, p)
+            s.ref.scale[g, :, slot, 0] *= np.float16(0.25 + p / 50)
+    s.C = us.KVCache(kv.I8, D, s.C.k, s.C.v, dev(s.ref.scale), s.C.page_table)
+    words, grids = s.tree()
+    s.check(s.run(words), grids)
