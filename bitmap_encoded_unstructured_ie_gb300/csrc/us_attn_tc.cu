@@ -734,7 +734,8 @@ attn_tc_join_kernel(const UsAttnParams p, int ctas) {
             for (int u = 0; u < AT; ++u) {
                 const float* sl = p.ws_slots + a.slot(c + u) * Sh::kSlotFloats;
                 const float4* o = reinterpret_cast<const float4*>(sl + 2 * kRows) + col / 4 * kRows + row;
-                r[u] = -INFINITY;
+                r[u] = -INFINITY, l[u] = 0.f;
+                v[u][0] = v[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (c + u <= a.last) {
                     r[u] = __ldcg(sl + row);
                     l[u] = __ldcg(sl + kRows + row);
@@ -744,15 +745,14 @@ attn_tc_join_kernel(const UsAttnParams p, int ctas) {
             float m = top;
 #pragma unroll
             for (int u = 0; u < AT; ++u) m = fmaxf(m, r[u]);
-            if (m == -INFINITY) continue;
-            const float f0 = ex2(top - m);
+            // (a state without a reference has weights 0, or NaN, which stays)
+            const float at = m == -INFINITY ? 0.f : m, f0 = ex2(top - at);
             sum *= f0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] *= f0;
 #pragma unroll
             for (int u = 0; u < AT; ++u) {
-                if (r[u] == -INFINITY) continue;
-                const float f = ex2(r[u] - m);
+                const float f = ex2(r[u] - at);
                 sum += l[u] * f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {

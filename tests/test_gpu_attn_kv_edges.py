@@ -1,0 +1,40 @@
+"""Attention over the quantised cache where its numerics are at their edges:
+queries that are not finite.  Tolerances are those of the attention's own tests.
+"""
+import numpy as np
+import pytest
+
+from oracle import kv
+from tests.test_gpu_attn_kv import Setup
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def us():
+    from bitmap_encoded_unstructured_ie_gb300 import binding
+    binding.load()
+    return binding
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("ctx", [40, 2900])
+@pytest.mark.parametrize("elem,D,G,n", [(kv.I8, 128, 4, 1), (kv.I4, 128, 4, 4), (kv.I8, 64, 4, 8), (kv.I8, 128, 4, 10),
+                                        (kv.I4, 64, 4, 40)])
+def test_queries_that_are_not_numbers(us, elem, D, G, n, ctx, value):
+    """exp of a NaN score, and infinite scores' differences, are NaN: so are that row's outputs, and no
+    other's, whether a segment is one CTA's or many CTAs'."""
+    s = Setup(us, elem, D, 1, G, 64, [ctx], [n], 31)
+    words, grids = s.tree()
+    clean, at = s.run(words), (n // 2, 1)
+    codes = np.array([kv.unpack(s.ref.k[s.ref.at(0, p)[0], 0, s.ref.at(0, p)[1]], elem)[5] for p in range(ctx)])
+    assert (codes > 0).any() and (codes < 0).any()              # one score is +inf, whichever sign the query has
+    s.Q[at][5] = value
+    got = s.run(words)
+    assert np.isnan(got[at]).all()
+    got[at], s.Q[at][5] = clean[at], 0
+    keep = clean[at].copy()
+    want, mag, big = kv.attend(s.ref, 0, s.Q, ctx, grids[0], s.scale)
+    tol = 2.0 ** -11 * np.abs(want) + 2.0 ** -24 + mag * (2 * 2.0 ** -11 + 2 * (D + 8) * 2.0 ** -24 * big[..., None])
+    tol[at] = np.inf
+    assert np.array_equal(keep, got[at]) and (np.abs(got - want) <= tol).all()
