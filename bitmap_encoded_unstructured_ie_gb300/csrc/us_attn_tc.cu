@@ -641,6 +641,9 @@ attn_tc_kernel(const UsAttnParams p) {
             const uint32_t vbits = __float_as_uint(us::half_bits_to_float((uint16_t)sv));      // (a subnormal scale too)
             const float vp = __uint_as_float(vbits & 0x7F800000u), vm = __uint_as_float((vbits & 0x807FFFFFu) | 0x3F800000u);
             const uint32_t vp2 = pack_half2(vp, vp);
+            // -128 at 2^9 and -8 at 2^13 are beyond fp16: us_kv_write stores no such entry, but
+            // 0 times an infinity would be every row's NaN.  Largest codes saturate instead.
+            const bool large = __any_sync(0xffffffffu, vp >= (ELEM == US_I8 ? 512.f : 8192.f));
             uint32_t vscale[2];                            // of the lane's rows
 #pragma unroll
             for (int u = 0; u < 2; ++u) vscale[u] = __shfl_sync(0xffffffffu, vp2, Sh::kC == 2 ? lane & 15 : 8 * u + (lane & 7));
@@ -671,6 +674,12 @@ attn_tc_kernel(const UsAttnParams p) {
 #pragma unroll
                     for (int k = 0; k < Sh::kOut; ++k)
                         out[k] = make_uint4(hmul2(out[k].x, s), hmul2(out[k].y, s), hmul2(out[k].z, s), hmul2(out[k].w, s));
+                    if (large) {
+#pragma unroll
+                        for (int k = 0; k < Sh::kOut; ++k)
+                            out[k] = make_uint4(us::saturate_half2(out[k].x), us::saturate_half2(out[k].y),
+                                                us::saturate_half2(out[k].z), us::saturate_half2(out[k].w));
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < Sh::kOut; ++k) *reinterpret_cast<uint4*>(to + put_u(u) + (put_chunk ^ (k << 4))) = out[k];

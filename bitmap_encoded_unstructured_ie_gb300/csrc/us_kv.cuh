@@ -81,6 +81,14 @@ US_DEV int64_t kv_entry(const UsKvCache& c, int id, int h, int p) {
 // base + i for positions: wraps negative instead of overflowing (kv_page refuses it)
 US_DEV int kv_pos(int base, int i) { return (int)((unsigned)base + (unsigned)i); }
 
+// fp16 pairs at most 65504 in magnitude; NaN stays.
+US_DEV uint32_t saturate_half2(uint32_t x) {
+    const uint32_t hi = 0x7BFF7BFFu, lo = 0xFBFFFBFFu;
+    const __half2 r = __hmin2_nan(__hmax2_nan(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&lo)),
+                                  *reinterpret_cast<const __half2*>(&hi));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // ctx if the page table's row can hold n positions behind it, else -1 (recorded).
 US_DEV int kv_context(const UsKvCache& c, int ctx, int n, unsigned* status) {
     if (ctx >= 0 && ctx <= ((int64_t)c.max_pages << c.page_shift) - n) return ctx;

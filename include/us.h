@@ -363,7 +363,9 @@ us_status us_kv_commit(const us_kv_cache* C, int T, const int32_t* acc_off, cons
  * and 0 for a row that sees no position.  Scores, weights' sums and outputs
  * are accumulated in fp32; a weight enters the product with V's codes as fp16,
  * rounded once, V's scale in it.  us_kv_write's scales are finite; what an entry
- * with another scale does stays with the rows that see it.
+ * with another scale does stays with the rows that see it.  Values beyond fp16
+ * (|code| 2^floor(log2 s) > 65504, which us_kv_write does not store) may count as
+ * 65504 times the scale's remaining factor, below 2.
  * Q, O: T rows of Hq heads.  mask: uint64 per row (a tree of at most 64 tokens
  * a request: max_n <= 64, else US_ERR_UNSUPPORTED); bits of j >= n are
  * ignored.  A chain may be of any length (a prompt's chunk).  One token a

@@ -1,11 +1,12 @@
 """Attention over the quantised cache where its numerics are at their edges:
-queries that are not finite.  Tolerances are those of the attention's own tests.
+queries that are not finite, values beyond fp16.  Tolerances are those of the attention's own tests.
 """
 import numpy as np
 import pytest
 
 from oracle import kv
 from tests.test_gpu_attn_kv import Setup
+from tests.test_gpu_kv_cache import dev
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,19 @@ def test_queries_that_are_not_numbers(us, elem, D, G, n, ctx, value):
     tol = 2.0 ** -11 * np.abs(want) + 2.0 ** -24 + mag * (2 * 2.0 ** -11 + 2 * (D + 8) * 2.0 ** -24 * big[..., None])
     tol[at] = np.inf
     assert np.array_equal(keep, got[at]) and (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("elem,scale,code", [(kv.I8, 512.0, -128), (kv.I8, 1024.0, 127), (kv.I4, 8192.0, -8), (kv.I4, 16384.0, 7)])
+@pytest.mark.parametrize("D,G,n", [(128, 4, 10), (64, 8, 64), (128, 8, 32)])
+def test_unseen_entries_of_large_values(us, elem, scale, code, D, G, n):
+    """A drafted entry whose values are beyond fp16's leaves the rows that do not see it as they are."""
+    s = Setup(us, elem, D, 1, G, 16, [90], [n], 33)
+    words, grids = s.tree()
+    words[:] &= ~np.int64(1 << (n - 1)) if n < 64 else np.int64(2 ** 63 - 1)
+    for g in grids[0]:
+        g[n - 1] = 0
+    page, slot = s.ref.at(0, 90 + n - 1)
+    s.ref.v[page, :, slot] = kv.pack(np.full((1, D), code), elem)
+    s.ref.scale[page, :, slot, 1] = scale
+    s.C = us.KVCache(elem, D, s.C.k, dev(s.ref.v), dev(s.ref.scale), s.C.page_table)
+    s.check(s.run(words), grids)
