@@ -45,6 +45,9 @@ namespace {
 using namespace us::attn;
 
 constexpr int kBlock = 16;                        // positions of one MMA's rows: they lie in one page
+// log2 of a row's largest weight with V's scale in it: when its reference is set, and what
+// it may grow to after that (2^15 < 65504; small weights keep fp16's bits down to 2^-25 of it)
+constexpr float kTop = 11.f, kMost = 15.f;
 
 template <int ELEM, int D, int NT, int W>
 struct Shape {
@@ -77,10 +80,6 @@ struct Shape {
     static constexpr int kSlotFloats = 2 * kRows + kRows * D;       // m, l, O^T of one partial state
 };
 
-US_DEV uint32_t hmax2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
 US_DEV uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -300,8 +299,10 @@ attn_mma_kernel(const UsAttnParams p) {
         if (ahead < count) find_pages();
     }
 
-    // ---- consumer state: maxima, sums and O^T of the warp's positions
-    float m[NT][2], l[NT][2], qb[NT][2], o[kMT][NT][4], vref = 0.f, vmul = 0.f;
+    // ---- consumer state: references, sums and O^T of the warp's positions.  Weights are
+    // 2^(s - m); a row's m is 11 less than its largest s + log2(V's scale), so that an
+    // entry which a row does not see, or hardly weighs, takes no bits from its weights.
+    float m[NT][2], l[NT][2], qb[NT][2], o[kMT][NT][4];
     uint32_t qf[Sh::kKS][NT][2];
     const float sc = p.scale * (1.4426950408889634f * 16777216.f);   // weights as powers of two; codes came as u 2^-24
     int parts = 0;
@@ -342,7 +343,6 @@ attn_mma_kernel(const UsAttnParams p) {
             for (int e = 0; e < 2; ++e)                    // the offset's share of column 2 c + e
                 qb[nt][e] = __shfl_sync(0xffffffffu, sum, (2 * c4 + e) * 4) * ((ELEM == US_I4 ? -8.f : -128.f) / 16777216.f);
         }
-        vref = vmul = 0.f;
         if (threadIdx.x < kRows) {
             const int r = cur.rb * kRows + threadIdx.x, i = r / G;
             sm_tok[threadIdx.x] = r < rows ? i : -1;
@@ -360,9 +360,7 @@ attn_mma_kernel(const UsAttnParams p) {
         if (blocks) {
             const uint8_t* st = wring + s * Sh::kStageBytes;
             const int pos = cur.tile * Sh::kTile + warp * kStep;
-            float sx[kSub][NT][4], vs[kSub][2];
-            float vtop;
-            uint32_t top2 = 0;                             // (K, V) scale maxima
+            float sx[kSub][NT][4], vs[kSub][2], lv[kSub][2];
             const bool edge = pos + kStep > cur.r.ctx || blocks != (1u << kSub) - 1u;
 #pragma unroll
             for (int sb = 0; sb < kSub; ++sb) {
@@ -400,10 +398,11 @@ attn_mma_kernel(const UsAttnParams p) {
                 // ---- scores (elements 0, 1: token rt; 2, 3: token rt + 8), masks
                 const uint32_t* ss = reinterpret_cast<const uint32_t*>(st + 2 * kStep * Sh::kRow) + sb * kBlock;
                 const uint32_t s0 = ss[rt], s1 = ss[rt + 8];
-                top2 = sb ? hmax2(top2, hmax2(s0 & 0x7FFFFFFFu, s1 & 0x7FFFFFFFu)) : hmax2(s0 & 0x7FFFFFFFu, s1 & 0x7FFFFFFFu);
                 const float ks[2] = {us::half_bits_to_float((uint16_t)s0) * sc, us::half_bits_to_float((uint16_t)s1) * sc};
                 vs[sb][0] = us::half_bits_to_float((uint16_t)(s0 >> 16));
                 vs[sb][1] = us::half_bits_to_float((uint16_t)(s1 >> 16));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) lv[sb][u] = fmaxf(lg2(fabsf(vs[sb][u])), -24.f);   // fp16's smallest, also for 0 and NaN
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -413,7 +412,6 @@ attn_mma_kernel(const UsAttnParams p) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int j = ((blocks >> sb) & 1u) ? pos + sb * kBlock + rt + 8 * u - cur.r.ctx : cur.r.n;
-                        if (j >= cur.r.n) vs[sb][u] = 0.f;     // nothing sees it, whatever its scale
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -426,38 +424,18 @@ attn_mma_kernel(const UsAttnParams p) {
                 }
             }
             // ---- running maxima, rescaled only where one has grown by 2^4
-            // (entries that no row sees may hold any scale: only finite ones count)
+            // (an unseen entry's scale may be anything: -inf and NaN move no maximum)
             bool grow = false;
-            if (edge) {
-                float va = 0.f;
-#pragma unroll
-                for (int sb = 0; sb < kSub; ++sb)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) va = fmaxf(va, fabsf(vs[sb][u]) < INFINITY ? fabsf(vs[sb][u]) : 0.f);
-                vtop = va;
-            } else {
-                vtop = us::half_bits_to_float((uint16_t)(top2 >> 16));
-            }
-            grow = vtop >= vref;
             float mx[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    mx[nt][e] = fmaxf(sx[0][nt][e], sx[0][nt][e + 2]);
-                    if constexpr (kSub == 2) mx[nt][e] = fmaxf(mx[nt][e], fmaxf(sx[1][nt][e], sx[1][nt][e + 2]));
-                    grow |= mx[nt][e] > m[nt][e] + kMaxLag;
+                    mx[nt][e] = fmaxf(sx[0][nt][e] + lv[0][0], sx[0][nt][e + 2] + lv[0][1]);
+                    if constexpr (kSub == 2) mx[nt][e] = max3(mx[nt][e], sx[1][nt][e] + lv[1][0], sx[1][nt][e + 2] + lv[1][1]);
+                    grow |= mx[nt][e] > m[nt][e] + kMost;
                 }
             if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, d));
-                float fv = 1.f;
-                if (vtop >= vref) {                              // the power of two above it
-                    const float nv = __uint_as_float((__float_as_uint(fmaxf(vtop, 1e-30f)) & 0x7F800000u) + 0x00800000u);
-                    fv = vref / nv;
-                    vref = nv;
-                    vmul = kVHead / nv;
-                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -465,14 +443,14 @@ attn_mma_kernel(const UsAttnParams p) {
                         float x = mx[nt][e];
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        x = fmaxf(x, m[nt][e]);
+                        x = fmaxf(x - kTop, m[nt][e]);
                         const float f = x == -INFINITY ? 1.f : ex2(m[nt][e] - x);
                         m[nt][e] = x;
                         l[nt][e] *= f;
 #pragma unroll
                         for (int t = 0; t < kMT; ++t) {
-                            o[t][nt][e] *= f * fv;
-                            o[t][nt][e + 2] *= f * fv;
+                            o[t][nt][e] *= f;
+                            o[t][nt][e + 2] *= f;
                         }
                     }
             }
@@ -480,21 +458,20 @@ attn_mma_kernel(const UsAttnParams p) {
             for (int sb = 0; sb < kSub; ++sb) {
                 // ---- weights; with V's scale, as fp16, they are the B operand of O^T
                 uint32_t pf[NT][2];
-                const float wv[2] = {vs[sb][0] * vmul, vs[sb][1] * vmul};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float w[4], x[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float mm = m[nt][e & 1];
-                        w[e] = ex2(sx[sb][nt][e] - (edge && mm == -INFINITY ? 0.f : mm));
+                        w[e] = ex2(sx[sb][nt][e] - (mm == -INFINITY ? 0.f : mm));
                         l[nt][e & 1] += w[e];
-                        x[e] = w[e] * wv[e >> 1];
+                        x[e] = w[e] * vs[sb][e >> 1];
                     }
                     if (edge) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (w[e] == 0.f) x[e] = 0.f;       // an unseen entry's scale may be anything
+                            if (sx[sb][nt][e] == -INFINITY) x[e] = 0.f;
                     }
 #pragma unroll
                     for (int u = 0; u < 2; ++u) pf[nt][u] = transpose8x8(pack_half2(x[2 * u], x[2 * u + 1]));
@@ -565,7 +542,7 @@ attn_mma_kernel(const UsAttnParams p) {
                     float t = sm_m[r];
 #pragma unroll
                     for (int w = 1; w < kWarps; ++w) t = fmaxf(t, sm_m[w * kRows + r]);
-                    const float f = (m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - t)) * (vref * (1.f / kVHead));
+                    const float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - t);
 #pragma unroll
                     for (int q = 0; q < kMT; ++q) o[q][nt][e] *= f, o[q][nt][e + 2] *= f;
                 }

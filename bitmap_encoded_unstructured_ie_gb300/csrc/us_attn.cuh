@@ -8,9 +8,6 @@
 namespace us {
 namespace attn {
 
-constexpr float kMaxLag = 4.f;                    // a row's maximum may lag by 2^4 before the state is rescaled
-constexpr float kVHead = 2048.f;                  // weights reach 2^4 2^11 < 65504 as fp16: small ones keep their bits
-
 // Waits for phase `parity` of `bar`, at most kWaitLimitNs (then US_ERR_TIMEOUT is
 // recorded).  A try, a sleep of some 20 ns, a try: try_wait alone comes back at once
 // and its loop took most of the issue slots; with a time hint it woke warps late.
@@ -44,6 +41,11 @@ US_DEV void cp_async_wait() {
 US_DEV float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+US_DEV float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 // two fp32 operations in one instruction

@@ -42,7 +42,7 @@ def test_queries_that_are_not_numbers(us, elem, D, G, n, ctx, value):
 
 
 @pytest.mark.parametrize("elem,scale,code", [(kv.I8, 512.0, -128), (kv.I8, 1024.0, 127), (kv.I4, 8192.0, -8), (kv.I4, 16384.0, 7)])
-@pytest.mark.parametrize("D,G,n", [(128, 4, 10), (64, 8, 64), (128, 8, 32)])
+@pytest.mark.parametrize("D,G,n", [(128, 4, 4), (64, 4, 8), (64, 1, 6), (128, 4, 10), (64, 8, 64), (128, 8, 32)])
 def test_unseen_entries_of_large_values(us, elem, scale, code, D, G, n):
     """A drafted entry whose values are beyond fp16's leaves the rows that do not see it as they are."""
     s = Setup(us, elem, D, 1, G, 16, [90], [n], 33)
