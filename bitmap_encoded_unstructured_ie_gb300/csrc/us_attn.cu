@@ -18,11 +18,10 @@
 // lane % 4) takes D/4 codes of K of tokens g' and g' + 8, and of V the D/8
 // dimensions from g D/8 of tokens c, c + 4, c + 8, c + 12.
 //
-// Codes of K need no conversion beyond a mask: with the sign bit flipped, a code
-// is u = code + 8 (or + 128) >= 0, and the fp16 number with the bits of u is
-// u 2^-24 exactly.  S^T starts from -8 (-128) 2^-24 sum(q), and the odd nibbles,
-// read in place as 16 u, have their own accumulator.  V's codes are made signed
-// first: an output may be far smaller than the offset's rounding in its sum.
+// Codes of both become signed fp16 numbers before the product.  K's could enter with
+// their offset of 8 (128), taken back from the sum, for one operation a pair less; but
+// then rounding goes by 128 sum |q| however small the products are (keys of few large
+// channels, one rounding a step: scores of 220 off by 4.7).  So with V's in an output.
 //
 // Work: the (request, key head, row block) segments are cut into tiles of 64 to 256
 // positions, and the tile sequence is spread evenly over the CTAs, whatever the
@@ -86,20 +85,6 @@ US_DEV uint32_t transpose8x8(uint32_t x) {
     return r;
 }
 
-// Codes of both halves of a word as fp16 pairs u 2^-24, u = code + 8 (+ 128).
-// int4: nibbles (0, 4), (1, 5), (2, 6), (3, 7); the odd ones as 16 u 2^-24.
-US_DEV void offset_i4(uint32_t x, uint32_t (&q)[4]) {
-    const uint32_t y = x >> 8;
-    q[0] = us::lop3<us::kLopAndXor>(x, 0x000F000Fu, 0x00080008u);
-    q[1] = us::lop3<us::kLopAndXor>(x, 0x00F000F0u, 0x00800080u);
-    q[2] = us::lop3<us::kLopAndXor>(y, 0x000F000Fu, 0x00080008u);
-    q[3] = us::lop3<us::kLopAndXor>(y, 0x00F000F0u, 0x00800080u);
-}
-// int8: bytes (0, 2), (1, 3).
-US_DEV void offset_i8(uint32_t x, uint32_t (&q)[2]) {
-    q[0] = us::lop3<us::kLopAndXor>(x, 0x00FF00FFu, 0x00800080u);
-    q[1] = us::lop3<us::kLopAndXor>(x >> 8, 0x00FF00FFu, 0x00800080u);
-}
 template <int N>
 US_DEV void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
     if constexpr (N >= 4) {
@@ -302,9 +287,9 @@ attn_mma_kernel(const UsAttnParams p) {
     // ---- consumer state: references, sums and O^T of the warp's positions.  Weights are
     // 2^(s - m); a row's m is 11 less than its largest s + log2(V's scale), so that an
     // entry which a row does not see, or hardly weighs, takes no bits from its weights.
-    float m[NT][2], l[NT][2], qb[NT][2], o[kMT][NT][4];
+    float m[NT][2], l[NT][2], o[kMT][NT][4];
     uint32_t qf[Sh::kKS][NT][2];
-    const float sc = p.scale * (1.4426950408889634f * 16777216.f);   // weights as powers of two; codes came as u 2^-24
+    const float sc = p.scale * 1.4426950408889634f;        // weights as powers of two
     int parts = 0;
     const int rt = ((g & 1) << 2) | (g >> 1);              // token of row g (k index 2c -> c, 2c + 1 -> c + 4)
 
@@ -321,7 +306,6 @@ attn_mma_kernel(const UsAttnParams p) {
             const int r = cur.rb * kRows + 8 * nt + g;
             const int i = r / G;
             const uint16_t* q = p.Q + (int64_t)(cur.r.row0 + i) * p.ldq + (cur.h * G + r - i * G) * D;
-            float sum = 0.f;                               // of the lane's part of row g
 #pragma unroll
             for (int w = 0; w < kKW; ++w) {
                 if constexpr (ELEM == US_I4) {
@@ -329,19 +313,12 @@ attn_mma_kernel(const UsAttnParams p) {
                     if (r < rows) u = *reinterpret_cast<const uint4*>(q + c4 * (D / 4) + 8 * w);
                     qf[2 * w][nt][0] = __byte_perm(u.x, u.z, 0x5410), qf[2 * w][nt][1] = __byte_perm(u.y, u.w, 0x5410);
                     qf[2 * w + 1][nt][0] = __byte_perm(u.x, u.z, 0x7632), qf[2 * w + 1][nt][1] = __byte_perm(u.y, u.w, 0x7632);
-                    sum += (sum_half2(u.x) + sum_half2(u.y)) + (sum_half2(u.z) + sum_half2(u.w));
                 } else {
                     uint2 u = make_uint2(0, 0);
                     if (r < rows) u = *reinterpret_cast<const uint2*>(q + (w >> 2) * 64 + c4 * 16 + 4 * (w & 3));
                     qf[w][nt][0] = __byte_perm(u.x, u.y, 0x5410), qf[w][nt][1] = __byte_perm(u.x, u.y, 0x7632);
-                    sum += sum_half2(u.x) + sum_half2(u.y);
                 }
             }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)                    // the offset's share of column 2 c + e
-                qb[nt][e] = __shfl_sync(0xffffffffu, sum, (2 * c4 + e) * 4) * ((ELEM == US_I4 ? -8.f : -128.f) / 16777216.f);
         }
         if (threadIdx.x < kRows) {
             const int r = cur.rb * kRows + threadIdx.x, i = r / G;
@@ -370,7 +347,7 @@ attn_mma_kernel(const UsAttnParams p) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sa[nt][e] = qb[nt][e & 1], so[nt][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) sa[nt][e] = so[nt][e] = 0.f;
                 uint32_t k0[kKW], k1[kKW];
                 const uint8_t* kr = st + (sb * kBlock + rt) * Sh::kRow + c4 * (kKW >= 4 ? 16 : 4 * kKW);
                 lds_words(kr, k0);
@@ -379,8 +356,8 @@ attn_mma_kernel(const UsAttnParams p) {
                 for (int w = 0; w < kKW; ++w) {
                     if constexpr (ELEM == US_I4) {
                         uint32_t x[4], y[4];
-                        offset_i4(k0[w], x);
-                        offset_i4(k1[w], y);
+                        decode_i4(k0[w], x);
+                        decode_i4(k1[w], y);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             us::mma_m16n8k16_f16(sa[nt], x[0], y[0], x[2], y[2], qf[2 * w][nt][0], qf[2 * w][nt][1]);
@@ -388,8 +365,8 @@ attn_mma_kernel(const UsAttnParams p) {
                         }
                     } else {
                         uint32_t x[2], y[2];
-                        offset_i8(k0[w], x);
-                        offset_i8(k1[w], y);
+                        decode_i8(k0[w], x);
+                        decode_i8(k1[w], y);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             us::mma_m16n8k16_f16(w & 1 ? so[nt] : sa[nt], x[0], y[0], x[1], y[1], qf[w][nt][0], qf[w][nt][1]);
@@ -407,7 +384,7 @@ attn_mma_kernel(const UsAttnParams p) {
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        sa[nt][e] = (ELEM == US_I4 ? fmaf(so[nt][e], 0.0625f, sa[nt][e]) : sa[nt][e] + so[nt][e]) * ks[e >> 1];
+                        sa[nt][e] = (sa[nt][e] + so[nt][e]) * ks[e >> 1];
                 if (edge) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {

@@ -87,10 +87,6 @@ US_DEV uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b), *reinterpret_cast<__half2*>(&c));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
-US_DEV float sum_half2(uint32_t a) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    return f.x + f.y;
-}
 US_DEV uint32_t pack_half2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

@@ -1,5 +1,6 @@
 """Attention over the quantised cache where its numerics are at their edges:
-queries that are not finite, values beyond fp16.  Tolerances are those of the attention's own tests.
+queries that are not finite, values beyond fp16, keys of few large channels.
+Tolerances are those of the attention's own tests.
 """
 import numpy as np
 import pytest
@@ -54,4 +55,27 @@ def test_unseen_entries_of_large_values(us, elem, scale, code, D, G, n):
     s.ref.v[page, :, slot] = kv.pack(np.full((1, D), code), elem)
     s.ref.scale[page, :, slot, 1] = scale
     s.C = us.KVCache(elem, D, s.C.k, dev(s.ref.v), dev(s.ref.scale), s.C.page_table)
+    s.check(s.run(words), grids)
+
+
+@pytest.mark.parametrize("elem", [kv.I8, kv.I4])
+@pytest.mark.parametrize("D,G,n", [(128, 4, 1), (64, 4, 1), (128, 4, 4), (64, 8, 4), (128, 4, 16), (128, 8, 32)])
+def test_keys_of_few_large_channels(us, elem, D, G, n):
+    """Four channels set the keys' scales and the other codes are 0 or 1; queries are large where all codes
+    are 0.  Scores are small sums of the products that are left: nothing else may enter their rounding."""
+    s = Setup(us, elem, D, 1, G, 16, [60], [n], 32)
+    rng, r, q = s.rng, s.ref, kv.QMAX[elem]
+    large = rng.choice(np.arange(0, D, 2), 4, replace=False)
+    free = np.setdiff1d(np.arange(0, D, 2), large)
+    codes = np.zeros((*r.k.shape[:3], D), np.int64)
+    codes[..., large] = rng.choice([-q, q], codes[..., large].shape)
+    np.put_along_axis(codes, rng.choice(free, (*codes.shape[:3], 1)), 1, -1)
+    r.k[:] = kv.pack(codes, elem)
+    fin = np.isfinite(r.scale[..., 0].astype(np.float32))
+    r.scale[..., 0][fin] = 5 / s.scale                          # scores of about 200
+    s.Q[:] = 40 + 2 * rng.standard_normal(s.Q.shape)
+    s.Q[..., 1::2] = 12000 + 1000 * rng.standard_normal(s.Q[..., 1::2].shape)
+    s.Q[..., large] = 0
+    s.C = us.KVCache(elem, D, dev(r.k), s.C.v, dev(r.scale), s.C.page_table)
+    words, grids = s.tree()
     s.check(s.run(words), grids)
