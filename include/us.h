@@ -338,11 +338,14 @@ typedef struct {
  * values) becomes the entries of position pos[b] + i.  Per row and head
  *   s = fp16_rn(max|x| / q), 1 if that is 0,   q = 127 (US_I8) or 7 (US_I4)
  *   code = clamp(rint(x / s), -q-1, q)          (fp32 divisions, ties to even)
- * Infinities count as +-65504 and NaN as 0: what is stored is finite. */
+ * Infinities count as +-65504 and NaN as 0: what is stored is finite.  (Where max|x|
+ * is 65504, q s is 65532 (US_I8) or 65520 (US_I4): beyond fp16, so results that
+ * stand for more than 65504 are given as 65504.) */
 us_status us_kv_write(const us_kv_cache* C, const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv, int T,
                       const int32_t* tok_off, const int32_t* pos, int max_n, void* stream);
 
-/* Read positions pos[b] .. back as fp16 rows: fp16_rn(code * s). */
+/* Read positions pos[b] .. back as fp16 rows: fp16_rn(code * s), at most 65504 in
+ * magnitude (NaN stays). */
 us_status us_kv_read(const us_kv_cache* C, int T, const int32_t* tok_off, const int32_t* pos, int max_n, uint16_t* K,
                      int64_t ldk, uint16_t* V, int64_t ldv, void* stream);
 
