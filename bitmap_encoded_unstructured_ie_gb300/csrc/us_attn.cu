@@ -184,7 +184,7 @@ US_DEV void join_states(const UsAttnParams& p, float* buf, float* sums, const Pa
         if (row >= a.rows || x >= kQuads) continue;
         const float inv = sums[row];
         uint16_t* out = out_row<kRows>(p, a.row0, a.h, a.rb, row, D) + g * (D / 8) + 4 * ((x >> 6) / NT);
-        *reinterpret_cast<uint2*>(out) = make_uint2(pack_half2(y[k].x * inv, y[k].y * inv), pack_half2(y[k].z * inv, y[k].w * inv));
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_out(y[k].x * inv, y[k].y * inv), pack_out(y[k].z * inv, y[k].w * inv));
     }
 }
 
@@ -568,7 +568,7 @@ attn_mma_kernel(const UsAttnParams p) {
                             const float inv = sm_inv[r];
                             uint16_t* out = out_row<kRows>(p, cur.r.row0, cur.h, cur.rb, r, D) + g * (D / 8) + 2 * (ch * kBlocks + q);
                             *reinterpret_cast<uint2*>(out) =
-                                make_uint2(pack_half2(y[0] * inv, y[1] * inv), pack_half2(y[2] * inv, y[3] * inv));
+                                make_uint2(pack_out(y[0] * inv, y[1] * inv), pack_out(y[2] * inv, y[3] * inv));
                         }
                     } else {
                         __stcg(reinterpret_cast<float4*>(slot + 2 * kRows) + ch * kBlocks * NT * 32 + x,

@@ -92,6 +92,8 @@ US_DEV uint32_t pack_half2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// Outputs, at most 65504 in magnitude (entries of the largest values stand for up to 65532).
+US_DEV uint32_t pack_out(float lo, float hi) { return us::saturate_half2(pack_half2(lo, hi)); }
 // Both halves of a word of codes as exact fp16 pairs: 0x6400 | u is the fp16
 // number 1024 + u, and flipping a code's sign bit makes it u = code + 8 (+ 128).
 // int4: nibbles (0, 4), (1, 5), (2, 6), (3, 7); int8: bytes (0, 2), (1, 3).

@@ -148,7 +148,7 @@ US_DEV void store8(uint16_t* out, const float* y, float f) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) d[dim_of<ELEM>(j)] = y[j] * f;
     *reinterpret_cast<uint4*>(out) =
-        make_uint4(pack_half2(d[0], d[1]), pack_half2(d[2], d[3]), pack_half2(d[4], d[5]), pack_half2(d[6], d[7]));
+        make_uint4(pack_out(d[0], d[1]), pack_out(d[2], d[3]), pack_out(d[4], d[5]), pack_out(d[6], d[7]));
 }
 
 template <int ELEM, int D, int NQ>

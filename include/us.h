@@ -363,9 +363,9 @@ us_status us_kv_commit(const us_kv_cache* C, int T, const int32_t* acc_off, cons
  * with bit j of mask[t] set (mask NULL: a chain, j <= i).  With query head hq
  * on key head hq / (Hq / Hkv):
  *   O[t][hq] = fp16(sum_p w_p v_p / sum_p w_p),  w_p = exp(scale * Q[t][hq].k_p)
- * and 0 for a row that sees no position.  Scores, weights' sums and outputs
- * are accumulated in fp32; a weight enters the product with V's codes as fp16,
- * rounded once, V's scale in it.  us_kv_write's scales are finite; what an entry
+ * at most 65504 in magnitude, and 0 for a row that sees no position.  Scores,
+ * weights' sums and outputs are accumulated in fp32; a weight enters the product
+ * with V's codes as fp16, rounded once, V's scale in it.  us_kv_write's scales are finite; what an entry
  * with another scale does stays with the rows that see it.  Values beyond fp16
  * (|code| 2^floor(log2 s) > 65504, which us_kv_write does not store) may count as
  * 65504 times the scale's remaining factor, below 2.

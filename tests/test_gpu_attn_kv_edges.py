@@ -79,3 +79,20 @@ def test_keys_of_few_large_channels(us, elem, D, G, n):
     s.C = us.KVCache(elem, D, dev(r.k), s.C.v, dev(r.scale), s.C.page_table)
     words, grids = s.tree()
     s.check(s.run(words), grids)
+
+
+@pytest.mark.parametrize("elem", [kv.I8, kv.I4])
+@pytest.mark.parametrize("D,G,n", [(128, 4, 1), (128, 4, 4), (64, 4, 8), (128, 4, 10), (64, 8, 64)])
+def test_largest_values_stay_finite(us, elem, D, G, n):
+    """V of +-65504 throughout: its entries stand for a little more, the outputs do not."""
+    s = Setup(us, elem, D, 1, G, 16, [300], [n], 34)
+    x = s.rng.choice([-65504.0, 65504.0], D)
+    c, sc = kv.quantise(x, elem)
+    fin = np.isfinite(s.ref.scale[..., 1].astype(np.float32))
+    s.ref.v[:] = kv.pack(c, elem)
+    s.ref.scale[..., 1][fin] = sc
+    s.C = us.KVCache(elem, D, s.C.k, dev(s.ref.v), dev(s.ref.scale), s.C.page_table)
+    got = s.run(s.tree()[0])
+    # sums of equal values: within the weights' rounding of +-65532 (65520), and at most 65504
+    assert (np.sign(got) == np.sign(x)).all() and (np.abs(got) <= 65504).all()
+    assert (np.abs(got) >= 65504 * (1 - 3 * 2.0 ** -11)).all()
