@@ -373,10 +373,15 @@ def us_quantize_x(X: torch.Tensor, N: int, K: int, Xq: torch.Tensor, s_x: torch.
     _check("us_quantize_x", load().us_quantize_x(_dptr(X), N, K, _dptr(Xq), _dptr(s_x), _stream(stream)))
 
 
+_HALVES = frozenset((torch.float16, torch.int16, torch.uint16))     # fp16, or its bit pattern
+_BYTES = frozenset((torch.uint8, torch.int8))
+_WORDS = frozenset((torch.int64, torch.uint64))
+
+
 @dataclass(frozen=True, eq=False)
 class KVCache:
     """A paged, quantised key/value cache over device tensors: codes k and v
-    (uint8, pages x Hkv x slots x row bytes), scales (fp16 or its bit pattern,
+    (bytes, pages x Hkv x slots x row bytes), scales (fp16 or its bit pattern,
     pages x Hkv x slots x 2: K, then V) and the page table (int32, B x pages).
     The descriptor is made once, with the object; the tensors' contents may
     change, the tensors may not."""
@@ -392,7 +397,8 @@ class KVCache:
         B, max_pages = self.page_table.shape
         assert row * 8 == self.D * (8 if self.elem == US_I8 else 4), "k: rows of D codes"
         assert self.v.shape == self.k.shape and tuple(self.scale.shape) == (num_pages, Hkv, page_size, 2)
-        assert self.k.element_size() == self.v.element_size() == 1 and self.scale.element_size() == 2
+        assert self.k.dtype in _BYTES and self.v.dtype in _BYTES, "k, v: bytes"
+        assert self.scale.dtype in _HALVES, "scale: fp16 or its bit pattern"
         assert self.page_table.dtype == torch.int32
         d = us_kv_cache(self.elem, self.D, Hkv, page_size, num_pages, B, max_pages, 0, _dptr(self.k), _dptr(self.v),
                         _dptr(self.scale), _dptr(self.page_table))
@@ -414,7 +420,7 @@ def _rows(x: torch.Tensor, H: int, D: int):
     """Rows, pointer and row distance of T x H x D fp16 rows whose heads are contiguous."""
     T, h, d = x.shape
     ld, sh, sd = x.stride()
-    assert x.is_cuda and x.element_size() == 2 and h == H and d == D and sd == 1 and (sh == D or H == 1), \
+    assert x.is_cuda and x.dtype in _HALVES and h == H and d == D and sd == 1 and (sh == D or H == 1), \
         "rows must be T x H x D CUDA fp16 with contiguous heads"
     return T, x.data_ptr(), (ld if T > 1 else H * D)
 
@@ -481,7 +487,8 @@ def us_attn_kv(C: KVCache, Q: torch.Tensor, tok_off: torch.Tensor, pos: torch.Te
     To, op, ldo = _rows(O, Hq, C.D)
     assert T == To and ws.is_cuda and ws.is_contiguous()
     if mask is not None:
-        assert mask.is_cuda and mask.element_size() == 8 and mask.numel() == T and mask.is_contiguous()
+        assert mask.is_cuda and mask.dtype in _WORDS and mask.numel() == T and mask.is_contiguous(), \
+            "mask must be T CUDA 64-bit words"
     _check("us_attn_kv", (_lib or load()).us_attn_kv(C._ref, qp, ldq, Hq, T, _i32(tok_off, C.B + 1), _i32(pos, C.B),
                                                      None if mask is None else mask.data_ptr(), max_n, scale, op, ldo,
                                                      ws.data_ptr(), ws.numel() * ws.element_size(),
