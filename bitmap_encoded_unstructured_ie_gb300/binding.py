@@ -373,6 +373,7 @@ def us_quantize_x(X: torch.Tensor, N: int, K: int, Xq: torch.Tensor, s_x: torch.
     _check("us_quantize_x", load().us_quantize_x(_dptr(X), N, K, _dptr(Xq), _dptr(s_x), _stream(stream)))
 
 
+_F16, _I32 = torch.float16, torch.int32
 _HALVES = frozenset((torch.float16, torch.int16, torch.uint16))     # fp16, or its bit pattern
 _BYTES = frozenset((torch.uint8, torch.int8))
 _WORDS = frozenset((torch.int64, torch.uint64))
@@ -400,9 +401,11 @@ class KVCache:
         assert self.k.dtype in _BYTES and self.v.dtype in _BYTES, "k, v: bytes"
         assert self.scale.dtype in _HALVES, "scale: fp16 or its bit pattern"
         assert self.page_table.dtype == torch.int32
+        device = self.k.get_device()
+        assert all(t.get_device() == device for t in (self.v, self.scale, self.page_table)), "tensors of one device"
         d = us_kv_cache(self.elem, self.D, Hkv, page_size, num_pages, B, max_pages, 0, _dptr(self.k), _dptr(self.v),
                         _dptr(self.scale), _dptr(self.page_table))
-        for name, value in (("B", B), ("Hkv", Hkv), ("page_size", page_size), ("device", self.k.device.index),
+        for name, value in (("B", B), ("Hkv", Hkv), ("page_size", page_size), ("device", device),
                             ("_desc", d), ("_ref", ctypes.byref(d))):
             object.__setattr__(self, name, value)
 
@@ -416,26 +419,33 @@ def kv_cache(elem: int, D: int, Hkv: int, page_size: int, num_pages: int, page_t
 
 # The cache's calls are short (a decode step appends and attends in a few
 # microseconds on the GPU), so their marshalling passes plain integers.
-def _rows(x: torch.Tensor, H: int, D: int):
+def _rows(x: torch.Tensor, H: int, C: KVCache):
     """Rows, pointer and row distance of T x H x D fp16 rows whose heads are contiguous."""
     T, h, d = x.shape
     ld, sh, sd = x.stride()
-    assert x.is_cuda and x.dtype in _HALVES and h == H and d == D and sd == 1 and (sh == D or H == 1), \
+    t = x.dtype
+    assert (t is _F16 or t in _HALVES) and h == H and d == C.D and sd == 1 and (sh == d or H == 1), \
         "rows must be T x H x D CUDA fp16 with contiguous heads"
-    return T, x.data_ptr(), (ld if T > 1 else H * D)
+    assert x.get_device() == C.device, "rows must be on the cache's device"
+    return T, x.data_ptr(), (ld if T > 1 else H * d)
 
 
-def _i32(x: torch.Tensor, n: int) -> int:
-    assert x.is_cuda and x.dtype is torch.int32 and x.numel() == n and x.is_contiguous(), "int32 CUDA array of n entries"
+def _i32(x: torch.Tensor, n: int, C: KVCache) -> int:
+    assert x.dtype is _I32 and x.numel() == n and x.is_contiguous(), "int32 CUDA array of n entries"
+    assert x.get_device() == C.device, "arrays must be on the cache's device"
     return x.data_ptr()
 
 
 # current_stream() builds an object (2.9 us on the GPU machine's host, of a call's 9); the raw handle does not (0.1 us).
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _raw_stream(stream, C: KVCache) -> int:
+    # (the library launches on the current device)
+    assert _current_device() == C.device, "the cache's device must be the current one"
     if stream is not None:
+        assert stream.device_index == C.device, "the stream must be of the cache's device"
         return stream.cuda_stream
     return torch.cuda.current_stream().cuda_stream if _current_raw_stream is None else _current_raw_stream(C.device)
 
@@ -443,28 +453,28 @@ def _raw_stream(stream, C: KVCache) -> int:
 def us_kv_write(C: KVCache, K: torch.Tensor, V: torch.Tensor, tok_off: torch.Tensor, pos: torch.Tensor, max_n: int,
                 stream=None):
     """Quantise T x Hkv x D rows of K and V into the cache at positions pos[b] .. ."""
-    T, kp, ldk = _rows(K, C.Hkv, C.D)
-    Tv, vp, ldv = _rows(V, C.Hkv, C.D)
+    T, kp, ldk = _rows(K, C.Hkv, C)
+    Tv, vp, ldv = _rows(V, C.Hkv, C)
     assert T == Tv
-    _check("us_kv_write", (_lib or load()).us_kv_write(C._ref, kp, ldk, vp, ldv, T, _i32(tok_off, C.B + 1),
-                                                       _i32(pos, C.B), max_n, _raw_stream(stream, C)))
+    _check("us_kv_write", (_lib or load()).us_kv_write(C._ref, kp, ldk, vp, ldv, T, _i32(tok_off, C.B + 1, C),
+                                                       _i32(pos, C.B, C), max_n, _raw_stream(stream, C)))
 
 
 def us_kv_read(C: KVCache, tok_off: torch.Tensor, pos: torch.Tensor, max_n: int, K: torch.Tensor, V: torch.Tensor,
                stream=None):
     """Read positions pos[b] .. back as fp16 rows (T x Hkv x D) of K and V."""
-    T, kp, ldk = _rows(K, C.Hkv, C.D)
-    Tv, vp, ldv = _rows(V, C.Hkv, C.D)
+    T, kp, ldk = _rows(K, C.Hkv, C)
+    Tv, vp, ldv = _rows(V, C.Hkv, C)
     assert T == Tv
-    _check("us_kv_read", (_lib or load()).us_kv_read(C._ref, T, _i32(tok_off, C.B + 1), _i32(pos, C.B), max_n, kp, ldk,
+    _check("us_kv_read", (_lib or load()).us_kv_read(C._ref, T, _i32(tok_off, C.B + 1, C), _i32(pos, C.B, C), max_n, kp, ldk,
                                                      vp, ldv, _raw_stream(stream, C)))
 
 
 def us_kv_commit(C: KVCache, acc_off: torch.Tensor, acc: torch.Tensor, pos: torch.Tensor, max_n: int, stream=None):
     """Move the accepted drafted tokens' entries, pos[b] + acc[i], to pos[b] + i."""
     T = acc.numel()
-    _check("us_kv_commit", (_lib or load()).us_kv_commit(C._ref, T, _i32(acc_off, C.B + 1), _i32(acc, T),
-                                                         _i32(pos, C.B), max_n, _raw_stream(stream, C)))
+    _check("us_kv_commit", (_lib or load()).us_kv_commit(C._ref, T, _i32(acc_off, C.B + 1, C), _i32(acc, T, C),
+                                                         _i32(pos, C.B, C), max_n, _raw_stream(stream, C)))
 
 
 def us_attn_kv_workspace_bytes(C: KVCache, Hq: int, max_n: int) -> int:
@@ -483,13 +493,13 @@ def us_attn_kv(C: KVCache, Q: torch.Tensor, tok_off: torch.Tensor, pos: torch.Te
     """Attention of T x Hq x D query rows over the cache; mask: one 64-bit word
     per row (a tree of drafted tokens), or None (a chain)."""
     Hq = Q.shape[1]
-    T, qp, ldq = _rows(Q, Hq, C.D)
-    To, op, ldo = _rows(O, Hq, C.D)
-    assert T == To and ws.is_cuda and ws.is_contiguous()
+    T, qp, ldq = _rows(Q, Hq, C)
+    To, op, ldo = _rows(O, Hq, C)
+    assert T == To and ws.is_contiguous() and ws.get_device() == C.device, "ws must be contiguous, on the cache's device"
     if mask is not None:
-        assert mask.is_cuda and mask.dtype in _WORDS and mask.numel() == T and mask.is_contiguous(), \
-            "mask must be T CUDA 64-bit words"
-    _check("us_attn_kv", (_lib or load()).us_attn_kv(C._ref, qp, ldq, Hq, T, _i32(tok_off, C.B + 1), _i32(pos, C.B),
+        assert mask.dtype in _WORDS and mask.numel() == T and mask.is_contiguous(), "mask must be T CUDA 64-bit words"
+        assert mask.get_device() == C.device, "mask must be on the cache's device"
+    _check("us_attn_kv", (_lib or load()).us_attn_kv(C._ref, qp, ldq, Hq, T, _i32(tok_off, C.B + 1, C), _i32(pos, C.B, C),
                                                      None if mask is None else mask.data_ptr(), max_n, scale, op, ldo,
                                                      ws.data_ptr(), ws.numel() * ws.element_size(),
                                                      _raw_stream(stream, C)))
