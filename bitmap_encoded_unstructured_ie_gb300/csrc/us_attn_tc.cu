@@ -220,7 +220,7 @@ attn_tc_kernel(const UsAttnParams p) {
                 for (int k = 0; k < kAtOnce; ++k) {
                     u[k] = make_uint4(0, 0, 0, 0);
                     if (r0 + k * kQR < rows)
-                        u[k] = __ldg(reinterpret_cast<const uint4*>(p.Q + (int64_t)(cur.r.row0 + q_tok) * p.ldq + (int64_t)(cur.h * G + q_head) * D) + q_chunk);
+                        u[k] = reinterpret_cast<const uint4*>(p.Q + (int64_t)(cur.r.row0 + q_tok) * p.ldq + (int64_t)(cur.h * G + q_head) * D)[q_chunk];
                     q_tok += q_dtok, q_head += q_dhead;
                     if (q_head >= G) q_head -= G, ++q_tok;
                 }
@@ -238,7 +238,7 @@ attn_tc_kernel(const UsAttnParams p) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int r = wrow + 8 * q + g, tok = (int)((unsigned)(cur.rb * kRows + r) / (unsigned)G);
-                own_seen[q] = r >= rows ? 0 : p.mask ? __ldg(p.mask + cur.r.row0 + tok) & (~0ull >> (64 - cur.r.n)) : (uint64_t)(tok + 1);
+                own_seen[q] = r >= rows ? 0 : p.mask ? p.mask[cur.r.row0 + tok] & (~0ull >> (64 - cur.r.n)) : (uint64_t)(tok + 1);
             }
             // positions that a row sees among 32 from `base` behind the context
             auto seen32 = [&](int base, uint64_t row) {

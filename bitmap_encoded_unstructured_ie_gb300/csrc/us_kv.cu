@@ -242,7 +242,7 @@ kv_read_kernel(const UsKvCache c, const UsKvCall a, int tokens, uint16_t* __rest
 // read into shared memory, then written, so that a path may overlap itself.  As many
 // threads as there are 16-byte pieces of K, so that more CTAs wait side by side.
 __global__ void __launch_bounds__(kThreads)
-kv_commit_kernel(const UsKvCache c, const UsKvCall a, const int32_t* __restrict__ acc) {
+kv_commit_kernel(const UsKvCache c, const UsKvCall a, const int32_t* acc) {
     extern __shared__ __align__(16) uint8_t held[];
     __shared__ int64_t from[US_KV_MAX_COMMIT], to[US_KV_MAX_COMMIT];
     us::pdl_wait();
