@@ -36,6 +36,8 @@
 // instructions of the codes' conversion (48 requests of 4096 to 8192, int4: ALU pipe
 // 47 % and issue slots 54 % busy, 3.8 TB/s), with one short request latency (9.5 us
 // for 777 positions: starting, finding the work, three trips to memory, the join).
+#include <atomic>
+
 #include "us_attn.cuh"
 #include "us_internal.h"
 
@@ -614,13 +616,13 @@ struct Plan {
         p.ws_count = static_cast<unsigned*>(p.ws);
         p.ws_slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + 4096);
         auto kern = attn_mma_kernel<ELEM, D, NT, W>;
-        static bool ready[64] = {};                        // the attribute is set once a device
+        static std::atomic<bool> ready[64];            // the attribute is set once a device, by whichever thread
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return US_ERR_CUDA;
-        if (!ready[dev]) {
+        if (!ready[dev].load(std::memory_order_acquire)) {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess)
                 return US_ERR_CUDA;
-            ready[dev] = true;
+            ready[dev].store(true, std::memory_order_release);
         }
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)grid());

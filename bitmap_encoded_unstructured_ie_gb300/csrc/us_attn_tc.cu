@@ -47,6 +47,8 @@
 // four trees of 64 tokens of 32 heads on 8, behind 4095, int4: 39 us, of which 13 are
 // tiles, 5 pass until the first scores, 4 are a CTA's partial state, and the rest is
 // the join and two launches.
+#include <atomic>
+
 #include "us_attn.cuh"
 #include "us_internal.h"
 #include "us_tcgen05.cuh"
@@ -787,13 +789,13 @@ us_status launch(UsAttnParams p, cudaStream_t st) {
     p.ws_parts = reinterpret_cast<Part*>(static_cast<uint8_t*>(p.ws) + 4096);      // behind the other kernel's counters
     p.ws_slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kPartBytes);
     auto kern = attn_tc_kernel<ELEM, D, NQ>;
-    static bool ready[64] = {};                            // the attribute is set once a device
+    static std::atomic<bool> ready[64];                // the attribute is set once a device, by whichever thread
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return US_ERR_CUDA;
-    if (!ready[dev]) {
+    if (!ready[dev].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess)
             return US_ERR_CUDA;
-        ready[dev] = true;
+        ready[dev].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid());

@@ -2,12 +2,15 @@
 queries that are not finite, values beyond fp16, keys of few large channels.
 Tolerances are those of the attention's own tests.
 """
+import threading
+
 import numpy as np
 import pytest
+import torch
 
 from oracle import kv
 from tests.test_gpu_attn_kv import Setup
-from tests.test_gpu_kv_cache import dev
+from tests.test_gpu_kv_cache import dev, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +99,33 @@ def test_largest_values_stay_finite(us, elem, D, G, n):
     # sums of equal values: within the weights' rounding of +-65532 (65520), and at most 65504
     assert (np.sign(got) == np.sign(x)).all() and (np.abs(got) <= 65504).all()
     assert (np.abs(got) >= 65504 * (1 - 3 * 2.0 ** -11)).all()
+
+
+@pytest.mark.parametrize("G,n", [(4, 2), (4, 33)])
+def test_calls_of_several_threads(us, G, n):
+    """Host threads with a stream and a workspace each."""
+    s = Setup(us, kv.I8, 64, 1, G, 16, [700], [n], 37)
+    words, grids = s.tree()
+    want = s.run(words)
+    q, m, off, pos = dev(s.Q), dev(words), dev(offsets(s.n)), dev(np.array(s.ctx, np.int32))
+    outs = [torch.zeros(n, s.Hq, 64, dtype=torch.float16, device="cuda") for _ in range(4)]
+    sets = [(torch.cuda.Stream(), us.workspace_attn_kv(s.C, s.Hq, n), o) for o in outs]
+    torch.cuda.synchronize()
+    start, failed = threading.Barrier(len(sets)), []
+
+    def work(stream, ws, o):
+        try:
+            start.wait(timeout=60)
+            for _ in range(20):
+                us.us_attn_kv(s.C, q, off, pos, m, n, s.scale, o, ws, stream=stream)
+        except BaseException as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=x) for x in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed and us.us_get_last_device_status() == us.US_OK
+    assert all(np.array_equal(o.cpu().numpy().astype(np.float64), want) for o in outs)
