@@ -540,6 +540,13 @@ attn_tc_kernel(const UsAttnParams p) {
                 it = end;
                 if (it < count) cur.next_segment(p);
             }
+            // Arrivals that no other warp waits for: they land while the CTA still has its shared memory
+            for (int i = max(0, count - kKS); i < count; ++i) wait(&H.k_free[i % kKS], i / kKS);
+            for (int i = max(0, count - kVS); i < count; ++i) wait(&H.v_free[i % kVS], i / kVS);
+            for (int x = 0; x < 2; ++x) {
+                const int used = NQ == 2 ? count : (count + 1 - x) / 2;     // tiles of stream x
+                if (used) wait(&H.pv_done[x][0], used - 1);
+            }
         }
         __syncwarp();
     } else {
