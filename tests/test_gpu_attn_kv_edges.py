@@ -1,5 +1,6 @@
 """Attention over the quantised cache where its numerics are at their edges:
-queries that are not finite, values beyond fp16, keys of few large channels.
+queries that are not finite, values beyond fp16, keys of few large channels; and
+where its work is cut: row blocks inside a token, requests of many lengths.
 Tolerances are those of the attention's own tests.
 """
 import threading
@@ -129,3 +130,23 @@ def test_calls_of_several_threads(us, G, n):
     torch.cuda.synchronize()
     assert not failed and us.us_get_last_device_status() == us.US_OK
     assert all(np.array_equal(o.cpu().numpy().astype(np.float64), want) for o in outs)
+
+
+@pytest.mark.parametrize("elem", [kv.I8, kv.I4])
+@pytest.mark.parametrize("D,Hkv,G,ctx,n", [
+    (128, 1, 5, [0, 37], [110, 9]), (64, 1, 7, [128, 1], [90, 40]), (128, 1, 3, [127], [190]), (64, 2, 5, [0], [60]),
+    (128, 1, 5, [70, 3], [5, 6]), (64, 1, 3, [16, 250], [10, 7]), (128, 1, 8, [100], [100]), (64, 1, 7, [0], [37])])
+def test_chains_of_several_row_blocks(us, elem, D, Hkv, G, ctx, n):
+    """Query heads that do not divide a block's rows: blocks begin inside a token, on both kernels."""
+    s = Setup(us, elem, D, Hkv, G, 32, ctx, n, 35)
+    words, grids = s.chain()
+    s.check(s.run(words), grids)
+
+
+@pytest.mark.parametrize("elem", [kv.I8, kv.I4])
+@pytest.mark.parametrize("D,G,tree", [(128, 4, False), (64, 8, True), (128, 7, True)])
+def test_long_requests_beside_single_tokens(us, elem, D, G, tree):
+    n = [1, 50, 1, 0, 1, 64, 2] if tree else [1, 1, 150, 0, 1, 3, 1]
+    s = Setup(us, elem, D, 2 if G == 4 else 1, G, 16, [300, 20, 0, 9, 128, 65, 700], n, 36)
+    words, grids = s.tree() if tree else s.chain()
+    s.check(s.run(words, pad=8), grids)
