@@ -224,7 +224,6 @@ attn_mma_kernel(const UsAttnParams p) {
     Cursor<kRows, Sh::kTile> pc = cur;
     uint8_t* wring = ring + warp * kStages * Sh::kStageBytes;
     uint32_t have = 0;                                     // kSub bits a stage: which blocks it holds
-    constexpr int kNoPage = -0x7fffffff - 1;               // nothing to copy (any other bad number is recorded)
     int page[kSub];
     auto copy = [&](int s, int sub, int64_t e) {           // the 16-position block at entry e
         const uint32_t st = us::smem_addr(wring + s * Sh::kStageBytes) + lane * 16;
@@ -241,7 +240,7 @@ attn_mma_kernel(const UsAttnParams p) {
 #pragma unroll
         for (int sb = 0; sb < kSub; ++sb) {
             const int pos = pc.tile * Sh::kTile + warp * kStep + sb * kBlock;
-            page[sb] = kNoPage;
+            page[sb] = -1;
             if (pos < pc.r.ctx + pc.r.n) page[sb] = p.c.table[(int64_t)pc.b * p.c.max_pages + (pos >> p.c.page_shift)];
         }
     };
@@ -249,10 +248,11 @@ attn_mma_kernel(const UsAttnParams p) {
         have &= ~(((1u << kSub) - 1u) << (s * kSub));
 #pragma unroll
         for (int sb = 0; sb < kSub; ++sb) {
+            const int pos = pc.tile * Sh::kTile + warp * kStep + sb * kBlock;
             if (page[sb] >= 0 && page[sb] < p.c.num_pages) {
-                copy(s, sb, us::kv_entry(p.c, page[sb], pc.h, pc.tile * Sh::kTile + warp * kStep + sb * kBlock));
+                copy(s, sb, us::kv_entry(p.c, page[sb], pc.h, pos));
                 have |= 1u << (s * kSub + sb);
-            } else if (page[sb] != kNoPage) {
+            } else if (pos < pc.r.ctx + pc.r.n) {
                 us::set_status(p.c.status, US_ERR_CORRUPT);
             }
         }

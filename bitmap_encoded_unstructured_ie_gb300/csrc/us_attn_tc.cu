@@ -79,7 +79,6 @@ static_assert(offsetof(Header, scales) % 16 == 0 && offsetof(Header, valid) % 16
 struct Ends {                                     // of a stream's rows at a segment's end, where Q was
     float ref[kM], sum[kM];
 };
-constexpr int kNoPage = -0x7fffffff - 1;          // nothing to read (any other bad number is recorded)
 
 template <int ELEM, int D, int NQ>
 struct Shape {
@@ -570,20 +569,19 @@ attn_tc_kernel(const UsAttnParams p) {
         uint8_t* raw = raw_sm + (warp - kMmaWarp - 1) * kRS * Sh::kRaw;
 
         // the item whose page number is on its way
-        int nx_item = warp - kMmaWarp - 1, nx_tile = 0, nx_page = kNoPage, nx_pos = 0;
+        int nx_item = warp - kMmaWarp - 1, nx_tile = 0, nx_page = -1, nx_pos = 0;
         auto locate = [&]() {                              // (at most one tile further)
             if (nx_item >= items) return;
             if ((nx_item >> 4) > nx_tile) cur.next(p), ++nx_tile;
             nx_pos = cur.tile * kTile + (nx_item & 7) * 16;
-            nx_page = nx_pos < cur.r.ctx + cur.r.n
-                          ? p.c.table[(int64_t)cur.b * p.c.max_pages + (nx_pos >> p.c.page_shift)] : kNoPage;
+            if (nx_pos < cur.r.ctx + cur.r.n) nx_page = p.c.table[(int64_t)cur.b * p.c.max_pages + (nx_pos >> p.c.page_shift)];
         };
         // copies it (key head h, `after` positions of the request from its first on) to
         // ring place `slot`; says how many of its positions are the request's, 0 if it
         // has no entries
         auto copy_item = [&](int slot, int h, int after) {
             int left = 0;
-            if (nx_item < items && nx_page != kNoPage) {
+            if (nx_item < items && after > 0) {
                 if (nx_page >= 0 && nx_page < p.c.num_pages) {
                     const int64_t e = us::kv_entry(p.c, nx_page, h, nx_pos);
                     const uint8_t* src = (nx_item & 8 ? p.c.v : p.c.k) + e * Sh::kRow + get_at;
@@ -617,7 +615,7 @@ attn_tc_kernel(const UsAttnParams p) {
             if (want)
                 for (int t = 0; t < tile; ++t) at.next(p);
             const int pos = at.tile * kTile + (mine & 7) * 16, left = want ? at.r.ctx + at.r.n - pos : 0;
-            const int page = left > 0 ? p.c.table[(int64_t)at.b * p.c.max_pages + (pos >> p.c.page_shift)] : kNoPage;
+            const int page = left > 0 ? p.c.table[(int64_t)at.b * p.c.max_pages + (pos >> p.c.page_shift)] : -1;
 #pragma unroll
             for (int s = 0; s < kRS; ++s) {
                 nx_page = __shfl_sync(0xffffffffu, page, s);

@@ -150,3 +150,22 @@ def test_long_requests_beside_single_tokens(us, elem, D, G, tree):
     s = Setup(us, elem, D, 2 if G == 4 else 1, G, 16, [300, 20, 0, 9, 128, 65, 700], n, 36)
     words, grids = s.tree() if tree else s.chain()
     s.check(s.run(words, pad=8), grids)
+
+
+@pytest.mark.parametrize("number", [-2 ** 31, -1, 2 ** 31 - 1])
+@pytest.mark.parametrize("B,ctx,n,G,bad", [(1024, 511, 1, 4, 3), (2, 90, 16, 4, 1)])
+def test_any_bad_page_number_is_recorded(us, B, ctx, n, G, bad, number):
+    """Whichever tile of its share a CTA meets it in; the request's other positions are attended to."""
+    s = Setup(us, kv.I4, 64, 1, G, 16, [ctx] * B, [n] * B, 38)
+    words, grids = s.chain()
+    s.C.page_table[bad, 0] = number
+    o = torch.zeros(s.T, s.Hq, 64, dtype=torch.float16, device="cuda")
+    us.us_attn_kv(s.C, dev(s.Q), dev(offsets(s.n)), dev(np.array(s.ctx, np.int32)), None, n, s.scale, o,
+                  us.workspace_attn_kv(s.C, s.Hq, n))
+    assert us.us_get_last_device_status() == us.US_ERR_CORRUPT
+    got = o.cpu().numpy().astype(np.float64)
+    s.check(got, grids, only={0, 1, B - 1} - {bad})
+    s.ref.table = s.ref.table.copy()
+    s.ref.table[bad, :-1], s.ref.table[bad, -1] = s.ref.table[bad, 1:], -1
+    s.ctx[bad] = ctx - 16                                       # positions 0..15 are not attended to
+    s.check(got, grids, only={bad})
