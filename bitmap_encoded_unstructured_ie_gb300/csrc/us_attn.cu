@@ -34,7 +34,7 @@
 // What bounds it: at one token of a long context HBM (two requests of 131000
 // positions, int8: 5.3 TB/s of a cache that streams once), with more requests the
 // instructions of the codes' conversion (48 requests of 4096 to 8192, int4: ALU pipe
-// 47 % and issue slots 54 % busy, 3.8 TB/s), with one short request latency (9.5 us
+// 45 % and issue slots 56 % busy, 3.8 TB/s), with one short request latency (9 us
 // for 777 positions: starting, finding the work, three trips to memory, the join).
 #include <atomic>
 
@@ -61,9 +61,9 @@ struct Shape {
     static constexpr int kMT = D / 16;                              // 16-dimension blocks of O^T
     // CTAs an SM.  Rows of 128 dimensions, and 17 to 32 rows of 64, need more than the
     // 168 registers that three CTAs of four warps leave (16 trees of 4 tokens, 4 query
-    // heads to a key head, behind 4095 positions, int4: 34 us with two CTAs, 43 with
-    // three; 12 trees of 13 to 25, 64 dimensions, int8: 66 and 72); 9 to 16 rows of 64
-    // do not (trees of up to 12: 47 and 41).
+    // heads to a key head, behind 4095 positions, int4: 33 us with two CTAs, 35 with
+    // three of one block a step; 12 trees of 13 to 25, 64 dimensions, int8: 62 and 96);
+    // 9 to 16 rows of 64 do not (trees of up to 12: 46 and 41).
     static constexpr int kMinB = W == 8 || NT == 4 || D == 128 ? 2 : 3;
     // 16-position blocks of a warp's step: with two there are twice as many MMAs that do
     // not wait for each other (4 tokens of two requests of 131000 positions, int8: 90 us
@@ -640,8 +640,8 @@ struct Plan {
 
 // f(Plan) for the cache's type and head width and the rows per key head.  Eight
 // warps a CTA, two CTAs an SM, for up to 8 rows: on 48 requests of 4096 to 8192
-// positions in int4 82 us (92 with two CTAs of four warps and twice the positions a
-// step), on one token of two requests of 131000 78 (78), on one of 777 9.5 (9.3).
+// positions in int4 83 us (97 with two CTAs of four warps and twice the positions a
+// step), on one token of two requests of 131000 77 (78), on one of 777 9.0 (9.1).
 template <class F>
 auto with_plan(const UsAttnParams& p, F f) {
     const int rows = p.a.max_n * p.G;

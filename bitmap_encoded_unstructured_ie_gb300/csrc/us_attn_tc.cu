@@ -43,8 +43,8 @@
 // memory for its 32 cycles of work), issue slots for 56 %, the exponentials' unit for
 // 35 %.  Softmax, MMAs and conversion wait for each other in turn; what would shorten
 // the turn (more stages, scores of a whole tile) has no shared memory or TMEM left.
-// 512 tokens of 64 query heads on 8, behind 8192 positions, int8: 177 us, 790 TFLOP/s;
-// four trees of 64 tokens of 32 heads on 8, behind 4095, int4: 39 us, of which 13 are
+// 512 tokens of 64 query heads on 8, behind 8192 positions, int8: 178 us, 800 TFLOP/s;
+// four trees of 64 tokens of 32 heads on 8, behind 4095, int4: 40 us, of which 13 are
 // tiles, 5 pass until the first scores, 4 are a CTA's partial state, and the rest is
 // the join and two launches.
 #include <atomic>
@@ -712,10 +712,10 @@ attn_tc_kernel(const UsAttnParams p) {
 // 8 columns of a row; its loads of AT states are on their way at once.  A launch of
 // its own: joined by one of the sharers, a segment's states (131 KB each at 256 rows
 // of 128) came at the 76 GB/s that one SM draws from L2.
-// Few segments have many sharers each: eight states at once (a tree of 32 to 64
-// tokens of one request behind 4000 positions: 18 us with the attention, 31 with two
-// at once).  Many have about two: two at once, and three times as many CTAs (chunk of
-// 512: 177 us, 183 with eight).
+// Few segments have many sharers each: eight states at once (a tree of 32
+// tokens of one request behind 4000 positions: 20 us with the attention, 29 with two
+// at once; of 64 tokens 23 and 27).  Many have about two: two at once, and three times
+// as many CTAs (chunk of 512: 177 us, 180 with eight).
 constexpr int kJoinRows = 16, kMaxCtas = 512;
 constexpr int join_ctas(int at, int D) { return (at == 8 ? 256 : 768) / D; }       // an SM
 template <int ELEM, int D, int NQ, int AT>
@@ -826,10 +826,13 @@ us_status launch(UsAttnParams p, cudaStream_t st) {
 
 namespace us {
 
-// From 33 rows per key head: below, the mma.sync kernel holds a segment's rows at
-// once and is faster, above it reads the cache again for the next 32 (16 for 128
-// dimensions).  16 requests of 4000 positions, int4: 32 rows of 128 dimensions 48 us
-// there, 55 here, 36 rows 64 and 58; of 64 dimensions 32 and 51, then 50 and 51.
+// From 33 rows per key head.  Below, the mma.sync kernel is faster, although it reads
+// the cache once for every 16 rows of 128 dimensions; it has 32 of 64 at once (32 rows,
+// 16 requests of 4000 positions / two of 131000, us there and here; int4, 128: 50, 59 /
+// 146, 173; int8, 128: 54, 62 / 159, 184; int4, 64: 32, 52 / 86, 152; int8, 64: 35, 53 /
+// 89, 157).  Above, 128 dimensions need a third pass (36 rows; int4: 66, 61 / 205, 181;
+// int8: 72, 64 / 224, 193).  64 need a second, and there the two are near each other
+// (int4: 50, 53 / 147, 159; int8: 53, 54 / 151, 161): one rule for both widths.
 bool attn_tc_serves(const UsAttnParams& p) { return (int64_t)p.a.max_n * p.G > 32; }
 
 size_t attn_tc_ws(const UsAttnParams& p) {

@@ -9,8 +9,10 @@
 // request's reads before its writes.
 //
 // Bytes bound the long calls: four prompts of up to 4096 tokens written and read back
-// (152 MB) in 32 us, 253 MB of a prefix read in 43.5 (5.8 TB/s, 87 % of a plain copy).
-// Short calls are latency: offsets, page table, rows, one after the other, 2.4 us each.
+// (152 MB) in 32 us, of which the write takes 21; 253 MB of a prefix read in 42.3 (6.0
+// TB/s, 90 % of a plain copy).  Short calls are latency: offsets, page table, rows, one
+// after the other, 2.5 to 3 us each in a replayed graph (launched one by one, the host's
+// 5 to 6 us a call bound them).
 #include "us_internal.h"
 #include "us_kv.cuh"
 
