@@ -7,13 +7,17 @@ no CPU fallback.
 
 Function names follow the C ABI: ``us_encode``, ``us_spmm_w4a4``,
 ``us_spmm_f16``, ``us_spmspv_f16``, ``us_colinfo``, ``us_spmspv_f16_ci``, ``us_quantize_x``,
-``us_kv_write``, ``us_kv_read``, ``us_kv_commit``, ``us_attn_kv``, ``us_workspace_bytes``, ``us_pick_split_k``,
+``us_kv_write``, ``us_kv_read``, ``us_kv_commit``, ``us_attn_kv``, ``us_kv_reserve``, ``us_kv_slots``,
+``us_norm_rope``, ``us_kv_append``, ``us_lat_write``, ``us_lat_read``, ``us_lat_commit``, ``us_attn_lat``,
+``us_attn_rows``, ``us_workspace_bytes``, ``us_pick_split_k``,
 ``us_validate``, ``us_get_last_device_status``.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 import threading
 from dataclasses import dataclass
 
@@ -28,11 +32,14 @@ US_F16, US_I4, US_I2, US_I8 = 0, 1, 2, 3          # US_I8: K/V cache only
 US_ORDER_ROW, US_ORDER_COL = 0, 1
 US_OP_ENCODE, US_OP_SPMM_W4A4, US_OP_SPMM_F16, US_OP_SPMSPV_F16 = 0, 1, 2, 3
 US_BITMAP_STATIC = 1
+US_ROPE_HALVES, US_ROPE_PAIRS = 0, 1
 
 EXPORTED = ("us_encode_sizes", "us_encode", "us_spmm_w4a4", "us_spmm_f16", "us_spmm_f16_noalloc", "us_spmspv_f16",
             "us_colinfo", "us_spmspv_f16_ci", "us_quantize_x",
             "us_kv_write", "us_kv_read", "us_kv_commit", "us_attn_kv", "us_attn_kv_workspace_bytes",
-            "us_encode_ie_sizes", "us_encode_ie", "us_reorder_rows", "us_spmm_w4a4_ie", "us_workspace_bytes_ie",
+            "us_kv_reserve", "us_kv_slots", "us_norm_rope", "us_kv_append", "us_lat_write", "us_lat_read", "us_lat_commit",
+           "us_attn_lat", "us_attn_lat_workspace_bytes", "us_attn_rows", "us_attn_rows_workspace_bytes",
+           "us_encode_ie_sizes", "us_encode_ie", "us_reorder_rows", "us_spmm_w4a4_ie", "us_workspace_bytes_ie",
             "us_pick_split_k_ie",
             "us_workspace_bytes", "us_pick_split_k", "us_validate", "us_get_last_device_status",
             "us_selftest_wait_timeout", "us_status_string", "us_version")
@@ -66,6 +73,42 @@ class us_kv_cache(ctypes.Structure):
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("page_table", ctypes.c_void_p)]
 
+
+class us_kv_pool(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p)]
+
+
+class us_rope(ctypes.Structure):
+    _fields_ = [("style", ctypes.c_int32), ("R", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turns", ctypes.c_void_p)]
+
+
+class us_heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld", ctypes.c_int64), ("hs", ctypes.c_int64), ("y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("hsy", ctypes.c_int64), ("w", ctypes.c_void_p), ("H", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class us_lat_cache(ctypes.Structure):
+    _fields_ = [("Dc", ctypes.c_int32), ("Dr", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("rows", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
+
+
+class us_attn_kv_rows(ctypes.Structure):
+    _fields_ = [("Dn", ctypes.c_int32), ("Dr", ctypes.c_int32), ("Dv", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("K", ctypes.c_void_p), ("ldk", ctypes.c_int64), ("hsk", ctypes.c_int64), ("KR", ctypes.c_void_p),
+                ("ldkr", ctypes.c_int64), ("V", ctypes.c_void_p), ("ldv", ctypes.c_int64), ("hsv", ctypes.c_int64),
+                ("S", ctypes.c_int64)]
+
+
+# The same as bytes, which the calls pass: a Structure takes three times as long to fill.
+_pack_heads = struct.Struct("@PqqPqqPii").pack
+_pack_rows = struct.Struct("@iiiiPqqPqPqqq").pack
+assert struct.calcsize("@PqqPqqPii") == ctypes.sizeof(us_heads)
+assert struct.calcsize("@iiiiPqqPqPqqq") == ctypes.sizeof(us_attn_kv_rows)
 
 _lock = threading.Lock()
 _lib = None
@@ -106,6 +149,19 @@ def load(path: str = LIB_PATH):
         lib.us_kv_commit.argtypes = [pkv, i32, P, P, P, i32, P]
         lib.us_attn_kv.argtypes = [pkv, P, i64, i32, i32, P, P, P, i32, ctypes.c_float, P, i64, P, sz, P]
         lib.us_attn_kv_workspace_bytes.argtypes = [pkv, i32, i32, psz]
+        f32, ppl = ctypes.c_float, ctypes.POINTER(us_kv_pool)
+        prp, plt = ctypes.POINTER(us_rope), ctypes.POINTER(us_lat_cache)
+        lib.us_kv_reserve.argtypes = [ppl, P, P]
+        lib.us_kv_slots.argtypes = [ppl, i32, P, P, i32, P, P]
+        lib.us_norm_rope.argtypes = [prp, i32, P, P, i32, i32, P, P, P, i32, P]
+        lib.us_kv_append.argtypes = [pkv, prp, P, P, P, i64, i32, P, P, P, i32, P]
+        lib.us_lat_write.argtypes = [plt, prp, P, i64, P, i32, P, P, P, i32, P]
+        lib.us_lat_read.argtypes = [plt, i32, P, P, i32, P, i64, P]
+        lib.us_lat_commit.argtypes = [plt, i32, P, P, P, i32, P]
+        lib.us_attn_lat.argtypes = [plt, P, i64, i32, i32, P, P, P, i32, f32, P, i64, P, sz, P]
+        lib.us_attn_lat_workspace_bytes.argtypes = [plt, i32, i32, psz]
+        lib.us_attn_rows.argtypes = [P, P, i64, i32, i32, P, P, i32, f32, P, i64, P, sz, P]
+        lib.us_attn_rows_workspace_bytes.argtypes = [P, i32, i32, psz]
         lib.us_workspace_bytes.argtypes = [i32, pbm, i32, i32, psz]
         lib.us_pick_split_k.argtypes = [i32, pbm, i32, ctypes.POINTER(ctypes.c_int)]
         lib.us_validate.argtypes = [pbm]
@@ -503,6 +559,274 @@ def us_attn_kv(C: KVCache, Q: torch.Tensor, tok_off: torch.Tensor, pos: torch.Te
                                                      None if mask is None else mask.data_ptr(), max_n, scale, op, ldo,
                                                      ws.data_ptr(), ws.numel() * ws.element_size(),
                                                      _raw_stream(stream, C)))
+
+
+# ---- page tables from request lengths
+@dataclass(frozen=True, eq=False)
+class KVPool:
+    """The pages that requests hold and those that are free, all int32 on the device:
+    the page table (B x max_pages, as in KVCache; the same tensor may serve caches),
+    how many pages each request holds (B), the stack of free pages (num_pages) and how
+    many of it are free (1).  us_kv_reserve changes their contents."""
+    page_size: int
+    page_table: torch.Tensor
+    held: torch.Tensor
+    free_pages: torch.Tensor
+    free_count: torch.Tensor
+
+    def __post_init__(self):
+        B, max_pages = self.page_table.shape
+        parts = (self.page_table, self.held, self.free_pages, self.free_count)
+        assert all(t.dtype is _I32 for t in parts), "a pool's tensors are int32"
+        assert self.held.numel() == B and self.free_count.numel() == 1
+        device = self.page_table.get_device()
+        assert all(t.get_device() == device for t in parts), "tensors of one device"
+        d = us_kv_pool(B, self.page_size, self.free_pages.numel(), max_pages, *(_dptr(t) for t in parts))
+        for name, value in (("B", B), ("num_pages", self.free_pages.numel()), ("device", device), ("_desc", d),
+                            ("_ref", ctypes.byref(d))):
+            object.__setattr__(self, name, value)
+
+
+def kv_pool(page_size: int, num_pages: int, B: int, max_pages: int, device="cuda") -> KVPool:
+    """A pool of which all pages are free (page 0 is taken first)."""
+    return KVPool(page_size, torch.full((B, max_pages), -1, dtype=_I32, device=device),
+                  torch.zeros(B, dtype=_I32, device=device),
+                  torch.arange(num_pages - 1, -1, -1, dtype=_I32, device=device),
+                  torch.full((1,), num_pages, dtype=_I32, device=device))
+
+
+def us_kv_reserve(P: KVPool, length: torch.Tensor, stream=None):
+    """Request b comes to hold the pages of length[b] positions: gives back, then takes."""
+    _check("us_kv_reserve", (_lib or load()).us_kv_reserve(P._ref, _i32(length, P.B, P), _raw_stream(stream, P)))
+
+
+def us_kv_slots(P: KVPool, tok_off: torch.Tensor, pos: torch.Tensor, max_n: int, slots: torch.Tensor, stream=None):
+    """slots[t]: the row of a pool of pages where token t's entry lies (int64; -1: nowhere)."""
+    assert slots.dtype is torch.int64 and slots.is_contiguous() and slots.get_device() == P.device, \
+        "slots must be contiguous int64 on the pool's device"
+    _check("us_kv_slots", (_lib or load()).us_kv_slots(P._ref, slots.numel(), _i32(tok_off, P.B + 1, P), _i32(pos, P.B, P),
+                                                       max_n, slots.data_ptr(), _raw_stream(stream, P)))
+
+
+# ---- norm and rotation of queries and keys
+def rope_freq(freq: torch.Tensor) -> torch.Tensor:
+    """Frequencies in radians a position -> the 64-bit fractions of a turn that Rope takes
+    (int64, the bits of uint64), on the same device."""
+    turns = [int(math.ldexp(math.fmod(f / (2 * math.pi), 1.0) % 1.0, 64)) & (1 << 64) - 1 for f in freq.double().reshape(-1).tolist()]
+    return torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=freq.device)
+
+
+@dataclass(frozen=True, eq=False)
+class Rope:
+    """A rotation by position and the eps of the norm before it.  turns: R/2 frequencies
+    (rope_freq) on the device; an empty tensor: no rotation."""
+    style: int                # US_ROPE_HALVES or US_ROPE_PAIRS
+    turns: torch.Tensor
+    eps: float = 1e-6
+
+    def __post_init__(self):
+        assert self.turns.dtype in _WORDS, "turns: 64-bit words (rope_freq)"
+        d = us_rope(self.style, 2 * self.turns.numel(), self.eps, 0, _dptr(self.turns))
+        for name, value in (("R", 2 * self.turns.numel()), ("device", self.turns.get_device()), ("_desc", d),
+                            ("_ref", ctypes.byref(d))):
+            object.__setattr__(self, name, value)
+
+
+def _apart(x: torch.Tensor, D: int, device: int):
+    """Rows, heads, pointer and distances of T x H x D fp16 heads."""
+    T, H, d = x.shape
+    ld, hs, sd = x.stride()
+    assert x.dtype in _HALVES and d == D and sd == 1, "heads must be T x H x D CUDA fp16 with contiguous values"
+    assert x.get_device() == device, "tensors must be on one device"
+    if H == 1:
+        hs = D
+    return T, H, x.data_ptr(), (ld if T > 1 else H * hs), hs
+
+
+def _heads(x, w, y, D: int, device: int, T: int):
+    """us_heads as bytes; None for no heads."""
+    if x is None:
+        return None
+    Tx, H, xp, ld, hs = _apart(x, D, device)
+    assert Tx == T, "as many rows of queries as of keys"
+    yp = ldy = hsy = 0
+    if y is not None:
+        Ty, Hy, yp, ldy, hsy = _apart(y, D, device)
+        assert Ty == T and Hy == H, "results have the shape of their inputs"
+    return _pack_heads(xp, ld, hs, yp, ldy, hsy, _weight(w, D, device), H, 0)
+
+
+def _weight(w, D: int, device: int) -> int:
+    if w is None:
+        return 0
+    assert w.dtype in _HALVES and w.numel() == D and w.is_contiguous(), "weights: D contiguous CUDA fp16 values"
+    assert w.get_device() == device, "tensors must be on one device"
+    return w.data_ptr()
+
+
+def us_norm_rope(rope: Rope, Q, wq, Qo, K, wk, Ko, tok_off: torch.Tensor, pos: torch.Tensor, depth, max_n: int, stream=None):
+    """Norm (weights wq, wk of D values, or None) and rotation of T x H x D query and key
+    heads (either may be None) into Qo and Ko, which may be Q and K themselves."""
+    T, _, D = (Q if Q is not None else K).shape
+    dev = rope.device
+    _check("us_norm_rope", (_lib or load()).us_norm_rope(
+        rope._ref, D, _heads(Q, wq, Qo, D, dev, T), _heads(K, wk, Ko, D, dev, T), pos.numel(), T,
+        _i32(tok_off, pos.numel() + 1, rope), _i32(pos, pos.numel(), rope), None if depth is None else _i32(depth, T, rope), max_n,
+        _raw_stream(stream, rope)))
+
+
+def us_kv_append(C: KVCache, rope: Rope, Q, wq, Qo, K: torch.Tensor, wk, V: torch.Tensor, tok_off: torch.Tensor,
+                 pos: torch.Tensor, depth, max_n: int, Ko=None, stream=None):
+    """us_norm_rope of Q (or None) and K, then us_kv_write of the keys it gives and of V, in one pass."""
+    T, vp, ldv = _rows(V, C.Hkv, C)
+    assert K.shape[1] == C.Hkv and rope.device == C.device
+    dev, D = C.device, C.D
+    _check("us_kv_append", (_lib or load()).us_kv_append(
+        C._ref, rope._ref, _heads(Q, wq, Qo, D, dev, T), _heads(K, wk, Ko, D, dev, T), vp, ldv, T, _i32(tok_off, C.B + 1, C),
+        _i32(pos, C.B, C), None if depth is None else _i32(depth, T, C), max_n, _raw_stream(stream, C)))
+
+
+# ---- the cache of latent rows, and attention over it
+@dataclass(frozen=True, eq=False)
+class LatCache:
+    """A paged cache of latent rows over device tensors: rows (fp16, pages x slots x
+    (Dc + Dr)) and the page table (int32, B x pages).  The tensors' contents may change,
+    the tensors may not."""
+    Dc: int
+    Dr: int
+    rows: torch.Tensor
+    page_table: torch.Tensor
+
+    def __post_init__(self):
+        num_pages, page_size, W = self.rows.shape
+        B, max_pages = self.page_table.shape
+        assert W == self.Dc + self.Dr, "rows of Dc + Dr values"
+        assert self.rows.dtype in _HALVES, "rows: fp16 or its bit pattern"
+        assert self.page_table.dtype is _I32
+        device = self.rows.get_device()
+        assert self.page_table.get_device() == device, "tensors of one device"
+        d = us_lat_cache(self.Dc, self.Dr, page_size, num_pages, B, max_pages, _dptr(self.rows), _dptr(self.page_table))
+        for name, value in (("B", B), ("W", W), ("page_size", page_size), ("device", device), ("_desc", d),
+                            ("_ref", ctypes.byref(d))):
+            object.__setattr__(self, name, value)
+
+
+def lat_cache(Dc: int, Dr: int, page_size: int, num_pages: int, page_table: torch.Tensor) -> LatCache:
+    """An empty cache of num_pages pages on the page table's device."""
+    return LatCache(Dc, Dr, torch.zeros(num_pages, page_size, Dc + Dr, dtype=_F16, device=page_table.device), page_table)
+
+
+def _row2(X: torch.Tensor, W: int, device: int):
+    """Rows, pointer and row distance of T x W fp16 rows."""
+    T, w = X.shape
+    assert X.dtype in _HALVES and w == W and X.stride(1) == 1, "rows must be T x W CUDA fp16 with contiguous values"
+    assert X.get_device() == device, "tensors must be on one device"
+    return T, X.data_ptr(), (X.stride(0) if T > 1 else W)
+
+
+def us_lat_write(C: LatCache, rope: Rope, X: torch.Tensor, w, tok_off: torch.Tensor, pos: torch.Tensor, depth, max_n: int,
+                 stream=None):
+    """Append rows X (T x (Dc + Dr)): latent values normed (weights w of Dc values, or None), the key rotated."""
+    T, xp, ldx = _row2(X, C.W, C.device)
+    assert rope.device == C.device, "tensors must be on one device"
+    _check("us_lat_write", (_lib or load()).us_lat_write(
+        C._ref, rope._ref, xp, ldx, _weight(w, C.Dc, C.device) or None, T, _i32(tok_off, C.B + 1, C), _i32(pos, C.B, C),
+        None if depth is None else _i32(depth, T, C), max_n, _raw_stream(stream, C)))
+
+
+def us_lat_read(C: LatCache, tok_off: torch.Tensor, pos: torch.Tensor, max_n: int, X: torch.Tensor, stream=None):
+    """Read positions pos[b] .. back as rows (T x (Dc + Dr))."""
+    T, xp, ldx = _row2(X, C.W, C.device)
+    _check("us_lat_read", (_lib or load()).us_lat_read(C._ref, T, _i32(tok_off, C.B + 1, C), _i32(pos, C.B, C), max_n, xp, ldx,
+                                                       _raw_stream(stream, C)))
+
+
+def us_lat_commit(C: LatCache, acc_off: torch.Tensor, acc: torch.Tensor, pos: torch.Tensor, max_n: int, stream=None):
+    """Move the accepted drafted tokens' rows, pos[b] + acc[i], to pos[b] + i."""
+    T = acc.numel()
+    _check("us_lat_commit", (_lib or load()).us_lat_commit(C._ref, T, _i32(acc_off, C.B + 1, C), _i32(acc, T, C),
+                                                           _i32(pos, C.B, C), max_n, _raw_stream(stream, C)))
+
+
+def us_attn_lat_workspace_bytes(C: LatCache, Hq: int, max_n: int) -> int:
+    n = ctypes.c_size_t()
+    _check("us_attn_lat_workspace_bytes", load().us_attn_lat_workspace_bytes(C._ref, Hq, max_n, ctypes.byref(n)))
+    return n.value
+
+
+def workspace_attn_lat(C: LatCache, Hq: int, max_n: int) -> torch.Tensor:
+    """A zero-filled workspace of the size us_attn_lat needs."""
+    return torch.zeros(max(us_attn_lat_workspace_bytes(C, Hq, max_n), 16), dtype=torch.uint8, device=C.rows.device)
+
+
+def _packed(x: torch.Tensor, H: int, D: int, device: int):
+    """Rows, pointer and row distance of T x H x D fp16 rows whose heads are side by side."""
+    T, h, d = x.shape
+    ld, sh, sd = x.stride()
+    assert x.dtype in _HALVES and h == H and d == D and sd == 1 and (sh == d or H == 1), \
+        "rows must be T x H x D CUDA fp16 with contiguous heads"
+    assert x.get_device() == device, "tensors must be on one device"
+    return T, x.data_ptr(), (ld if T > 1 else H * D)
+
+
+def _space(ws: torch.Tensor, device: int) -> int:
+    assert ws.is_contiguous() and ws.get_device() == device, "ws must be contiguous, on the call's device"
+    return ws.numel() * ws.element_size()
+
+
+def us_attn_lat(C: LatCache, Q: torch.Tensor, tok_off: torch.Tensor, pos: torch.Tensor, mask, max_n: int, scale: float,
+                O: torch.Tensor, ws: torch.Tensor, stream=None):
+    """Attention of T x Hq x (Dc + Dr) query rows over the latent rows, to T x Hq x Dc; mask as in us_attn_kv."""
+    Hq, dev = Q.shape[1], C.device
+    T, qp, ldq = _packed(Q, Hq, C.W, dev)
+    To, op, ldo = _packed(O, Hq, C.Dc, dev)
+    assert T == To
+    if mask is not None:
+        assert mask.dtype in _WORDS and mask.numel() == T and mask.is_contiguous(), "mask must be T CUDA 64-bit words"
+        assert mask.get_device() == dev, "mask must be on the cache's device"
+    _check("us_attn_lat", (_lib or load()).us_attn_lat(C._ref, qp, ldq, Hq, T, _i32(tok_off, C.B + 1, C), _i32(pos, C.B, C),
+                                                       None if mask is None else mask.data_ptr(), max_n, scale, op, ldo,
+                                                       ws.data_ptr(), _space(ws, dev), _raw_stream(stream, C)))
+
+
+def us_attn_rows_workspace_bytes(Dn: int, Dr: int, Dv: int, H: int, B: int, max_n: int) -> int:
+    n = ctypes.c_size_t()
+    a = _pack_rows(Dn, Dr, Dv, H, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    _check("us_attn_rows_workspace_bytes", load().us_attn_rows_workspace_bytes(a, B, max_n, ctypes.byref(n)))
+    return n.value
+
+
+def workspace_attn_rows(Dn: int, Dr: int, Dv: int, H: int, B: int, max_n: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of the size us_attn_rows needs."""
+    return torch.zeros(max(us_attn_rows_workspace_bytes(Dn, Dr, Dv, H, B, max_n), 16), dtype=torch.uint8, device=device)
+
+
+class _On:
+    """A device, where a call has no object that names it."""
+    __slots__ = ("device",)
+
+    def __init__(self, device):
+        self.device = device
+
+
+def us_attn_rows(Q: torch.Tensor, K: torch.Tensor, KR: torch.Tensor, V: torch.Tensor, tok_off: torch.Tensor,
+                 kv_off: torch.Tensor, max_n: int, scale: float, O: torch.Tensor, ws: torch.Tensor, stream=None):
+    """Causal attention of T x H x (Dn + Dr) query rows, the last of their requests' key
+    rows, over S x H x Dn keys K, the S x Dr key part KR that all heads share and
+    S x H x Dv values V, to T x H x Dv."""
+    on = _On(Q.get_device())
+    dev, H, S = on.device, Q.shape[1], K.shape[0]
+    Dn, Dr, Dv = K.shape[2], KR.shape[1], V.shape[2]
+    T, qp, ldq = _packed(Q, H, Dn + Dr, dev)
+    To, op, ldo = _packed(O, H, Dv, dev)
+    Sk, Hk, kp, ldk, hsk = _apart(K, Dn, dev)
+    Sv, Hv, vp, ldv, hsv = _apart(V, Dv, dev)
+    Sr, rp, ldkr = _row2(KR, Dr, dev)
+    assert T == To and Sv == S and Sr == S and Hk == H and Hv == H, "K, KR and V have the same rows, K and V Q's heads"
+    B = tok_off.numel() - 1
+    a = _pack_rows(Dn, Dr, Dv, H, kp, ldk, hsk, rp, ldkr, vp, ldv, hsv, S)
+    _check("us_attn_rows", (_lib or load()).us_attn_rows(a, qp, ldq, B, T, _i32(tok_off, B + 1, on), _i32(kv_off, B + 1, on), max_n,
+                                                         scale, op, ldo, ws.data_ptr(), _space(ws, dev), _raw_stream(stream, on)))
 
 
 def us_validate_host(bitmap, tile_off, values, M, K, TM, TK, elem, order) -> int:

@@ -8,6 +8,7 @@
 
 #include "us_common.cuh"
 #include "us_internal.h"
+#include "us_attn_lat.cuh"
 #include "us_kv.cuh"
 
 __device__ unsigned g_us_status = 0;
@@ -240,6 +241,82 @@ us_status check_kv_call(const us_kv_cache* C, int T, const int32_t* off, const i
 // rows of H heads of D fp16 values, ld elements apart
 us_status check_rows(const uint16_t* x, int64_t ld, int H, int D) {
     return x && aligned16(x) && ld >= (int64_t)H * D && ld % 8 == 0 ? US_OK : US_ERR_INVALID_ARG;
+}
+
+// what the caches share: pages, table, requests
+us_status check_pages(int B, int page_size, int num_pages, int max_pages, const int32_t* table, UsKvCache& c) {
+    if (B <= 0 || num_pages <= 0 || max_pages <= 0) return US_ERR_INVALID_ARG;
+    if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1))) return US_ERR_INVALID_ARG;
+    if (B > 1024 || (int64_t)max_pages * page_size >= ((int64_t)1 << 30)) return US_ERR_TOO_LARGE;
+    if (!table || !aligned16(table)) return US_ERR_INVALID_ARG;
+    c = UsKvCache{};
+    c.page_shift = __builtin_ctz((unsigned)page_size);
+    c.num_pages = num_pages; c.B = B; c.max_pages = max_pages;
+    c.table = table;
+    c.status = status_ptr();
+    return US_OK;
+}
+
+// how a call names its tokens
+us_status check_tokens(int T, const int32_t* off, const int32_t* pos, const int32_t* depth, int max_n, UsKvCall& a) {
+    if (T < 0 || max_n < 1 || !off || !pos || !aligned16(off) || !aligned16(pos)) return US_ERR_INVALID_ARG;
+    if (depth && !aligned16(depth)) return US_ERR_INVALID_ARG;
+    if (max_n >= 1 << 30) return US_ERR_TOO_LARGE;
+    a.off = off; a.pos = pos; a.T = T; a.max_n = max_n;
+    return US_OK;
+}
+
+us_status check_pool(const us_kv_pool* P, UsKvCache& c) {
+    if (!P) return US_ERR_INVALID_ARG;
+    const us_status s = check_pages(P->B, P->page_size, P->num_pages, P->max_pages, P->page_table, c);
+    if (s != US_OK) return s;
+    return P->num_pages > 1 << 30 ? US_ERR_TOO_LARGE : US_OK;
+}
+
+us_status check_rope(const us_rope* r, int D) {
+    if (!r || r->reserved || (r->style != US_ROPE_HALVES && r->style != US_ROPE_PAIRS)) return US_ERR_INVALID_ARG;
+    if (r->R < 0 || r->R > D || r->R % 16) return US_ERR_INVALID_ARG;
+    if (!(r->eps >= 0.f) || !(r->eps - r->eps == 0.f)) return US_ERR_INVALID_ARG;
+    if (r->R && (!r->turns || !aligned16(r->turns))) return US_ERR_INVALID_ARG;
+    return US_OK;
+}
+
+bool heads_apart(int64_t ld, int64_t hs, int H, int D) {
+    return ld >= 0 && hs >= 0 && ld % 8 == 0 && hs % 8 == 0 && (H == 1 || hs >= D) && ld >= (H - 1) * hs + D;
+}
+// out: y is needed
+us_status check_heads(const us_heads* g, int D, bool out) {
+    if (g->reserved || g->H < 1) return US_ERR_INVALID_ARG;
+    if (g->H > 4096) return US_ERR_TOO_LARGE;
+    if (!g->x || !aligned16(g->x) || (out && !g->y) || !aligned16(g->y) || !aligned16(g->w)) return US_ERR_INVALID_ARG;
+    if (!heads_apart(g->ld, g->hs, g->H, D) || (g->y && !heads_apart(g->ldy, g->hsy, g->H, D))) return US_ERR_INVALID_ARG;
+    return US_OK;
+}
+
+us_status check_lat(const us_lat_cache* C, UsLatCache& L) {
+    if (!C || C->Dc <= 0 || C->Dr <= 0) return US_ERR_INVALID_ARG;
+    const us_status s = check_pages(C->B, C->page_size, C->num_pages, C->max_pages, C->page_table, L.c);
+    if (s != US_OK) return s;
+    if ((C->Dc != 256 && C->Dc != 512) || C->Dr != us::kLatDr) return US_ERR_UNSUPPORTED;
+    if (!C->rows || !aligned16(C->rows)) return US_ERR_INVALID_ARG;
+    if ((int64_t)C->num_pages * C->page_size >= (int64_t)1 << 31) return US_ERR_TOO_LARGE;
+    L.Dc = C->Dc; L.W = C->Dc + C->Dr; L.rows = C->rows;
+    return US_OK;
+}
+
+us_status check_attn_lat(const us_lat_cache* C, int Hq, int max_n, UsLatCache& L) {
+    const us_status s = check_lat(C, L);
+    if (s != US_OK) return s;
+    if (Hq <= 0 || max_n < 1) return US_ERR_INVALID_ARG;
+    if (Hq > 1024 || (int64_t)max_n * Hq >= ((int64_t)1 << 30)) return US_ERR_TOO_LARGE;
+    return US_OK;
+}
+
+us_status check_attn_rows(const us_attn_kv_rows* A, int B, int max_n) {
+    if (!A || A->Dn <= 0 || A->Dr <= 0 || A->Dv <= 0 || A->H <= 0 || B <= 0 || max_n < 1) return US_ERR_INVALID_ARG;
+    if (A->Dr != 64 || A->Dn != A->Dv || (A->Dn != 64 && A->Dn != 128)) return US_ERR_UNSUPPORTED;
+    if (B > 1024 || A->H > 1024 || (int64_t)max_n * A->H >= ((int64_t)1 << 30)) return US_ERR_TOO_LARGE;
+    return US_OK;
 }
 
 us_status check_attn_shape(const UsKvCache& c, int Hq, int max_n) {
@@ -679,6 +756,169 @@ us_status us_attn_kv(const us_kv_cache* C, const uint16_t* Q, int64_t ldq, int H
     if (need && (!ws || ws_bytes < need || !aligned16(ws))) return US_ERR_WORKSPACE;
     p.ws = ws;
     return us::launch_attn(p, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_kv_reserve(const us_kv_pool* P, const int32_t* len, void* stream) {
+    UsKvCache c;
+    const us_status s = check_pool(P, c);
+    if (s != US_OK) return s;
+    if (!P->held || !P->free_pages || !P->free_count || !len) return US_ERR_INVALID_ARG;
+    if (!aligned16(P->held) || !aligned16(P->free_pages) || !aligned16(P->free_count) || !aligned16(len)) return US_ERR_INVALID_ARG;
+    return us::launch_reserve(*P, len, c.status, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_kv_slots(const us_kv_pool* P, int T, const int32_t* tok_off, const int32_t* pos, int max_n, int64_t* slots,
+                      void* stream) {
+    UsKvCache c;
+    UsKvCall a;
+    us_status s = check_pool(P, c);
+    if (s == US_OK) s = check_tokens(T, tok_off, pos, nullptr, max_n, a);
+    if (s != US_OK || T == 0) return s;
+    if (!slots || !aligned16(slots)) return US_ERR_INVALID_ARG;
+    return us::launch_slots(c, a, slots, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_norm_rope(const us_rope* rope, int D, const us_heads* q, const us_heads* k, int B, int T,
+                       const int32_t* tok_off, const int32_t* pos, const int32_t* depth, int max_n, void* stream) {
+    if (D < 8 || D > 256 || D % 8 || B <= 0 || (!q && !k)) return US_ERR_INVALID_ARG;
+    if (B > 1024) return US_ERR_TOO_LARGE;
+    UsKvCache c = {};
+    UsKvCall a;
+    us_status s = check_rope(rope, D);
+    if (s == US_OK) s = check_tokens(T, tok_off, pos, depth, max_n, a);
+    if (s != US_OK || T == 0) return s;
+    if (q) s = check_heads(q, D, true);
+    if (s == US_OK && k) s = check_heads(k, D, true);
+    if (s != US_OK) return s;
+    c.B = B;
+    c.status = status_ptr();
+    return us::launch_norm_rope(*rope, D, q ? *q : us_heads{}, k ? *k : us_heads{}, c, a, depth, nullptr, 0,
+                                static_cast<cudaStream_t>(stream));
+}
+
+us_status us_kv_append(const us_kv_cache* C, const us_rope* rope, const us_heads* q, const us_heads* k, const uint16_t* V,
+                       int64_t ldv, int T, const int32_t* tok_off, const int32_t* pos, const int32_t* depth, int max_n,
+                       void* stream) {
+    UsKvCache c;
+    UsKvCall a;
+    us_status s = check_kv_call(C, T, tok_off, pos, max_n, c, a);
+    if (s == US_OK) s = check_rope(rope, c.D);
+    if (s == US_OK) s = check_tokens(T, tok_off, pos, depth, max_n, a);
+    if (s != US_OK) return s;
+    if (!k || k->H != c.Hkv) return US_ERR_INVALID_ARG;
+    if (T == 0) return US_OK;
+    if (q) s = check_heads(q, c.D, true);
+    if (s == US_OK) s = check_heads(k, c.D, false);
+    if (s == US_OK) s = check_rows(V, ldv, c.Hkv, c.D);
+    if (s != US_OK) return s;
+    return us::launch_norm_rope(*rope, c.D, q ? *q : us_heads{}, *k, c, a, depth, V, ldv, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_lat_write(const us_lat_cache* C, const us_rope* rope, const uint16_t* X, int64_t ldx, const uint16_t* w,
+                       int T, const int32_t* tok_off, const int32_t* pos, const int32_t* depth, int max_n, void* stream) {
+    UsLatCache L;
+    UsKvCall a;
+    us_status s = check_lat(C, L);
+    if (s == US_OK) s = check_rope(rope, C->Dr);
+    if (s == US_OK && rope->R && rope->R != C->Dr) s = US_ERR_INVALID_ARG;
+    if (s == US_OK) s = check_tokens(T, tok_off, pos, depth, max_n, a);
+    if (s != US_OK || T == 0) return s;
+    s = check_rows(X, ldx, 1, L.W);
+    if (s != US_OK) return s;
+    if (!aligned16(w)) return US_ERR_INVALID_ARG;
+    return us::launch_lat_write(L, a, *rope, X, ldx, w, depth, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_lat_read(const us_lat_cache* C, int T, const int32_t* tok_off, const int32_t* pos, int max_n, uint16_t* X,
+                      int64_t ldx, void* stream) {
+    UsLatCache L;
+    UsKvCall a;
+    us_status s = check_lat(C, L);
+    if (s == US_OK) s = check_tokens(T, tok_off, pos, nullptr, max_n, a);
+    if (s != US_OK || T == 0) return s;
+    s = check_rows(X, ldx, 1, L.W);
+    if (s != US_OK) return s;
+    return us::launch_lat_read(L, a, X, ldx, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_lat_commit(const us_lat_cache* C, int T, const int32_t* acc_off, const int32_t* acc, const int32_t* pos,
+                        int max_n, void* stream) {
+    UsLatCache L;
+    UsKvCall a;
+    us_status s = check_lat(C, L);
+    if (s == US_OK) s = check_tokens(T, acc_off, pos, nullptr, max_n, a);
+    if (s != US_OK || T == 0) return s;
+    if (max_n > US_KV_MAX_COMMIT) return US_ERR_UNSUPPORTED;
+    if (!acc || !aligned16(acc)) return US_ERR_INVALID_ARG;
+    return us::launch_lat_commit(L, a, acc, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_attn_lat_workspace_bytes(const us_lat_cache* C, int Hq, int max_n, size_t* bytes) {
+    if (!bytes) return US_ERR_INVALID_ARG;
+    UsAttnLatParams p = {};
+    const us_status s = check_attn_lat(C, Hq, max_n, p.L);
+    if (s != US_OK) return s;
+    p.Hq = Hq;
+    p.a.max_n = max_n;
+    *bytes = us::attn_lat_ws(p);
+    return US_OK;
+}
+
+us_status us_attn_lat(const us_lat_cache* C, const uint16_t* Q, int64_t ldq, int Hq, int T, const int32_t* tok_off,
+                      const int32_t* pos, const uint64_t* mask, int max_n, float scale, uint16_t* O, int64_t ldo,
+                      void* ws, size_t ws_bytes, void* stream) {
+    UsAttnLatParams p = {};
+    us_status s = check_attn_lat(C, Hq, max_n, p.L);
+    if (s == US_OK) s = check_tokens(T, tok_off, pos, nullptr, max_n, p.a);
+    if (s != US_OK) return s;
+    if (!(scale - scale == 0.f)) return US_ERR_INVALID_ARG;
+    if (mask && max_n > 64) return US_ERR_UNSUPPORTED;
+    if (mask && !aligned16(mask)) return US_ERR_INVALID_ARG;
+    if (T == 0) return US_OK;
+    s = check_rows(Q, ldq, Hq, p.L.W);
+    if (s == US_OK) s = check_rows(O, ldo, Hq, p.L.Dc);
+    if (s != US_OK) return s;
+    p.Q = Q; p.O = O; p.ldq = ldq; p.ldo = ldo; p.Hq = Hq; p.scale = scale; p.mask = mask;
+    const size_t need = us::attn_lat_ws(p);
+    if (need && (!ws || ws_bytes < need || !aligned16(ws))) return US_ERR_WORKSPACE;
+    p.ws = ws;
+    return us::launch_attn_lat(p, static_cast<cudaStream_t>(stream));
+}
+
+us_status us_attn_rows_workspace_bytes(const us_attn_kv_rows* A, int B, int max_n, size_t* bytes) {
+    if (!bytes) return US_ERR_INVALID_ARG;
+    const us_status s = check_attn_rows(A, B, max_n);
+    if (s != US_OK) return s;
+    UsAttnRowsParams p = {};
+    p.k = *A; p.B = B; p.max_n = max_n;
+    *bytes = us::attn_rows_ws(p);
+    return US_OK;
+}
+
+us_status us_attn_rows(const us_attn_kv_rows* A, const uint16_t* Q, int64_t ldq, int B, int T, const int32_t* tok_off,
+                       const int32_t* kv_off, int max_n, float scale, uint16_t* O, int64_t ldo, void* ws,
+                       size_t ws_bytes, void* stream) {
+    us_status s = check_attn_rows(A, B, max_n);
+    if (s != US_OK) return s;
+    if (T < 0 || !tok_off || !kv_off || !aligned16(tok_off) || !aligned16(kv_off)) return US_ERR_INVALID_ARG;
+    if (!(scale - scale == 0.f)) return US_ERR_INVALID_ARG;
+    if (T == 0) return US_OK;
+    s = check_rows(Q, ldq, A->H, A->Dn + A->Dr);
+    if (s == US_OK) s = check_rows(O, ldo, A->H, A->Dv);
+    if (s == US_OK) s = check_rows(A->KR, A->ldkr, 1, A->Dr);
+    if (s != US_OK) return s;
+    if (!A->K || !A->V || !aligned16(A->K) || !aligned16(A->V) || A->S < 1) return US_ERR_INVALID_ARG;
+    if (!heads_apart(A->ldk, A->hsk, A->H, A->Dn) || !heads_apart(A->ldv, A->hsv, A->H, A->Dv)) return US_ERR_INVALID_ARG;
+    if (A->S >= (int64_t)1 << 31) return US_ERR_TOO_LARGE;
+    UsAttnRowsParams p = {};
+    p.k = *A;
+    p.Q = Q; p.O = O; p.ldq = ldq; p.ldo = ldo; p.B = B; p.T = T; p.max_n = max_n;
+    p.off = tok_off; p.kv_off = kv_off; p.scale = scale;
+    p.status = status_ptr();
+    const size_t need = us::attn_rows_ws(p);
+    if (need && (!ws || ws_bytes < need || !aligned16(ws))) return US_ERR_WORKSPACE;
+    p.ws = ws;
+    return us::launch_attn_rows(p, static_cast<cudaStream_t>(stream));
 }
 
 us_status us_validate(const us_bitmap* W) {

@@ -12,6 +12,9 @@ struct UsKParams;
 struct UsKvCache;
 struct UsKvCall;
 struct UsAttnParams;
+struct UsLatCache;
+struct UsAttnLatParams;
+struct UsAttnRowsParams;
 
 constexpr int US_KV_MAX_COMMIT = 64;   // tokens of one request in us_kv_commit
 
@@ -97,6 +100,23 @@ us_status launch_attn(const UsAttnParams& p, cudaStream_t st);
 bool attn_tc_serves(const UsAttnParams& p);
 size_t attn_tc_ws(const UsAttnParams& p);
 us_status launch_attn_tc(const UsAttnParams& p, cudaStream_t st);
+
+// page tables and slots from request lengths (us_pages.cu)
+us_status launch_reserve(const us_kv_pool& P, const int32_t* len, unsigned* status, cudaStream_t st);
+us_status launch_slots(const UsKvCache& c, const UsKvCall& a, int64_t* slots, cudaStream_t st);
+// norm and rotation of heads; with V, keys and values go to the cache c (us_rope.cu)
+us_status launch_norm_rope(const us_rope& rope, int D, const us_heads& q, const us_heads& k, const UsKvCache& c, const UsKvCall& a,
+                           const int32_t* depth, const uint16_t* V, int64_t ldv, cudaStream_t st);
+// cache of latent rows: write, read back, commit (us_lat.cu)
+us_status launch_lat_write(const UsLatCache& L, const UsKvCall& a, const us_rope& rope, const uint16_t* X, int64_t ldx,
+                           const uint16_t* w, const int32_t* depth, cudaStream_t st);
+us_status launch_lat_read(const UsLatCache& L, const UsKvCall& a, uint16_t* X, int64_t ldx, cudaStream_t st);
+us_status launch_lat_commit(const UsLatCache& L, const UsKvCall& a, const int32_t* acc, cudaStream_t st);
+// attention over latent rows, and over rows expanded from them (us_attn_lat.cu)
+size_t attn_lat_ws(const UsAttnLatParams& p);
+us_status launch_attn_lat(const UsAttnLatParams& p, cudaStream_t st);
+size_t attn_rows_ws(const UsAttnRowsParams& p);
+us_status launch_attn_rows(const UsAttnRowsParams& p, cudaStream_t st);
 
 // device properties of the current device (cached)
 int num_sms();

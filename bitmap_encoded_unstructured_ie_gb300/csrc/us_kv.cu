@@ -14,7 +14,8 @@
 // after the other, 2.5 to 3 us each in a replayed graph (launched one by one, the host's
 // 5 to 6 us a call bound them).
 #include "us_internal.h"
-#include "us_kv.cuh"
+#include "us_kv_quant.cuh"
+#include "us_launch.cuh"
 
 namespace {
 
@@ -22,88 +23,8 @@ constexpr int kThreads = 256;
 constexpr int kTokens = 64;                       // of a CTA of write and read, at most
 constexpr int kAtOnce = 4;                        // (token, head) rows of a thread on their way at once
 
-// x as eight fp32 values, infinities at the largest fp16 value, NaN as 0
-US_DEV void unpack8(uint4 w, float (&x)[8]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float f = us::half_bits_to_float((uint16_t)(u[i >> 1] >> (16 * (i & 1))));
-        x[i] = f == f ? fminf(fmaxf(f, -65504.f), 65504.f) : 0.f;
-    }
-}
-
-// Eight codes (as fp32 whole numbers plus 1.5 2^23, whose low bits they are) -> bytes or nibbles.
-template <int ELEM>
-US_DEV uint2 pack_codes(const float (&v)[8]) {
-    uint32_t b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(v[i]);
-    if constexpr (ELEM == US_I8) {
-        return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
-                          __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
-    } else {
-        uint32_t w = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w |= (b[i] & 0xFu) << (4 * i);
-        return make_uint2(w, 0u);
-    }
-}
-
-// Quantises one row held eight values a lane by D/8 neighbouring lanes (all
-// 32 lanes of the warp take part); returns the scale.
-//
-// rint(x / s) without a division: q = x (1/s), corrected once by its exact
-// remainder.  x and s have 11 bits, so x / s is either exactly a half-way point
-// k + 1/2, which has few bits and is what the correction then arrives at, or at
-// least 2^-20 of itself away from one, where an error of 2^-22 does not matter.
-// Rows with infinities, NaN or a subnormal scale (whose codes may need the clamp)
-// take the plain way.
-template <int ELEM, int D>
-US_DEV uint16_t quantise_row(uint4 in, uint2& codes) {
-    constexpr float q = ELEM == US_I8 ? 127.f : 7.f, kRound = 12582912.f;
-    const uint32_t u[4] = {in.x, in.y, in.z, in.w};
-    auto h2 = [](uint32_t x) { return *reinterpret_cast<const __half2*>(&x); };
-    __half2 m2 = h2(u[0] & 0x7FFF7FFFu);
-#pragma unroll
-    for (int i = 1; i < 4; ++i) m2 = __hmax2_nan(m2, h2(u[i] & 0x7FFF7FFFu));
-#pragma unroll
-    for (int d = D / 16; d > 0; d >>= 1) m2 = __hmax2_nan(m2, __shfl_xor_sync(0xffffffffu, m2, d));
-    const __half m = __hmax_nan(__low2half(m2), __high2half(m2));
-    float amax = __half2float(m);
-    uint16_t s16 = us::float_to_half_bits(amax / q);
-    float v[8];
-    if (__any_sync(0xffffffffu, !(amax <= 65504.f) || (s16 < 0x0400u && s16 != 0u))) {
-        unpack8(in, v);
-        amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-#pragma unroll
-        for (int d = D / 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-        s16 = us::float_to_half_bits(amax / q);
-        if (s16 == 0) s16 = 0x3C00u;                          // 1.0
-        const float s = us::half_bits_to_float(s16);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(rintf(v[i] / s), -q - 1.f), q) + kRound;
-    } else {
-        if (s16 == 0) s16 = 0x3C00u;
-        const float s = us::half_bits_to_float(s16), inv = 1.f / s;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 x = __half22float2(h2(u[i]));
-            const float a = x.x * inv, b = x.y * inv;
-            v[2 * i] = fmaf(fmaf(-a, s, x.x), inv, a) + kRound;
-            v[2 * i + 1] = fmaf(fmaf(-b, s, x.y), inv, b) + kRound;
-        }
-    }
-    codes = pack_codes<ELEM>(v);
-    return s16;
-}
-
-template <int ELEM>
-US_DEV void store_codes(uint8_t* dst, uint2 w) {
-    if constexpr (ELEM == US_I8) *reinterpret_cast<uint2*>(dst) = w;
-    else *reinterpret_cast<uint32_t*>(dst) = w.x;
-}
+using us::quantise_row;
+using us::store_codes;
 
 // The tokens of one CTA of write and read, [i0, i1) of request b, and their first
 // row.
@@ -282,21 +203,6 @@ kv_commit_kernel(const UsKvCache c, const UsKvCall a, const int32_t* acc) {
     us::pdl_launch_dependents();
 }
 
-template <class Kern, class... Args>
-us_status launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? US_OK : US_ERR_CUDA;
-}
-
 // Tokens of a CTA: four (token, head) rows a thread, or one where that leaves
 // SMs without a CTA.
 int cta_tokens(const UsKvCache& c, const UsKvCall& a) {
@@ -318,20 +224,20 @@ us_status launch_kv_write(const UsKvCache& c, const UsKvCall& a, const uint16_t*
                           int64_t ldv, cudaStream_t st) {
     auto kern = c.elem == US_I8 ? (c.D == 64 ? kv_write_kernel<US_I8, 64> : kv_write_kernel<US_I8, 128>)
                                 : (c.D == 64 ? kv_write_kernel<US_I4, 64> : kv_write_kernel<US_I4, 128>);
-    return launch(kern, row_grid(c, a), kThreads, 0, st, c, a, cta_tokens(c, a), K, ldk, V, ldv);
+    return launch_pdl(kern, row_grid(c, a), kThreads, 0, st, c, a, cta_tokens(c, a), K, ldk, V, ldv);
 }
 
 us_status launch_kv_read(const UsKvCache& c, const UsKvCall& a, uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv,
                          cudaStream_t st) {
     auto kern = c.elem == US_I8 ? (c.D == 64 ? kv_read_kernel<US_I8, 64> : kv_read_kernel<US_I8, 128>)
                                 : (c.D == 64 ? kv_read_kernel<US_I4, 64> : kv_read_kernel<US_I4, 128>);
-    return launch(kern, row_grid(c, a), kThreads, 0, st, c, a, cta_tokens(c, a), K, ldk, V, ldv);
+    return launch_pdl(kern, row_grid(c, a), kThreads, 0, st, c, a, cta_tokens(c, a), K, ldk, V, ldv);
 }
 
 us_status launch_kv_commit(const UsKvCache& c, const UsKvCall& a, const int32_t* acc, cudaStream_t st) {
     const size_t smem = (size_t)a.max_n * (2 * c.row_bytes + 4);
     const int pieces = (a.max_n * (c.row_bytes / 16) + 31) / 32 * 32, threads = pieces < 64 ? 64 : pieces > kThreads ? kThreads : pieces;
-    return launch(kv_commit_kernel, dim3((unsigned)c.Hkv, (unsigned)c.B), threads, smem, st, c, a, acc);
+    return launch_pdl(kv_commit_kernel, dim3((unsigned)c.Hkv, (unsigned)c.B), threads, smem, st, c, a, acc);
 }
 
 }  // namespace us

@@ -381,6 +381,178 @@ us_status us_attn_kv(const us_kv_cache* C, const uint16_t* Q, int64_t ldq, int H
                      void* ws, size_t ws_bytes, void* stream);
 us_status us_attn_kv_workspace_bytes(const us_kv_cache* C, int Hq, int max_n, size_t* bytes);
 
+/* ---------------------------------------------------------------------------
+ * Page tables built on the GPU.  (No counterpart on the pages.)
+ *
+ * A pool names the pages that requests hold and those that are free:
+ *   page_table: int32 [B][max_pages], as in us_kv_cache; one table may serve
+ *               several caches of the same page_size and num_pages
+ *   held:       int32 [B], pages that request b holds: entries 0 .. held[b]-1 of
+ *               its row; the others are -1
+ *   free_pages: int32 [num_pages], a stack of which the first *free_count are free
+ *   free_count: int32 [1]
+ * All of them live on the device and are changed by the GPU alone, so a captured
+ * graph follows them.  An empty pool: held 0, page_table -1, free_pages any
+ * permutation of 0..num_pages-1, *free_count = num_pages.  B, page_size and
+ * max_pages as in us_kv_cache.  Calls on one pool follow one another (one stream,
+ * or events between them).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t B, page_size, num_pages, max_pages;
+    int32_t* page_table;
+    int32_t* held;
+    int32_t* free_pages;
+    int32_t* free_count;
+} us_kv_pool;
+
+/* Request b comes to hold ceil(len[b] / page_size) pages (len: int32 [B]; 0: it
+ * gives all of them back).  First the pages that are given back are pushed, those of
+ * request 0 first and each request's in the order of its positions, their entries
+ * becoming -1; then new pages are popped, for request 0 first.  From the first
+ * request on that the free pages do not suffice for, requests that want more get
+ * none and keep what they hold: US_ERR_WORKSPACE is recorded in the device status
+ * word (and held tells which).  A length below 0 or beyond the table's row records
+ * US_ERR_INVALID_ARG and leaves the request as it is.  A count outside 0..num_pages,
+ * a held outside 0..max_pages, or more pages given back than the stack has room for
+ * records US_ERR_CORRUPT and changes nothing. */
+us_status us_kv_reserve(const us_kv_pool* P, const int32_t* len, void* stream);
+
+/* slots[t] = page * page_size + slot of each of the call's tokens (named as in
+ * us_kv_write), the row of a pool of pages where its entry lies; -1, with what
+ * us_kv_write records, where it has none.  slots: int64, T entries; those of no
+ * request are left as they are.  held, free_pages and free_count are not read and
+ * may be NULL. */
+us_status us_kv_slots(const us_kv_pool* P, int T, const int32_t* tok_off, const int32_t* pos, int max_n, int64_t* slots,
+                      void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Norm and position rotation of queries and keys.  (No counterpart on the pages.)
+ *
+ * A row x of D values (one token's head) becomes
+ *   y = x / sqrt(mean(x^2) + eps) * w      (w NULL: y = x)
+ * and the first R of its values are turned in pairs (a, b) = (j, j + R/2) in
+ * US_ROPE_HALVES, (2j, 2j + 1) in US_ROPE_PAIRS, by the angle A_j of its position p:
+ *   (y_a, y_b) -> (y_a cos A_j - y_b sin A_j, y_b cos A_j + y_a sin A_j)
+ * all in fp32, rounded to fp16 once at the end.  A_j = 2 pi p turns[j] / 2^64, with
+ * turns[j] uint64, a frequency in turns a position: p turns[j] modulo 2^64 is the
+ * angle's fraction of a turn, exact at any position.  R: a multiple of 16, at most D
+ * (0: no rotation, turns may be NULL).
+ * Token i of request b stands at position pos[b] + i, or pos[b] + depth[t] where
+ * `depth` (int32 [T]) is given: a tree's drafts stand at their depth.
+ * ------------------------------------------------------------------------- */
+typedef enum { US_ROPE_HALVES = 0, US_ROPE_PAIRS = 1 } us_rope_style;
+typedef struct {
+    int32_t style;            /* us_rope_style */
+    int32_t R;
+    float eps;                /* >= 0 */
+    int32_t reserved;         /* must be 0 */
+    const uint64_t* turns;    /* device, R/2 entries */
+} us_rope;
+
+/* T rows of H heads of fp16: head h of row t at x + t ld + h hs elements, its result
+ * at y + t ldy + h hsy; y may be x with the same distances.  Distances are multiples
+ * of 8.  w: D fp16 values, or NULL. */
+typedef struct {
+    const uint16_t* x;
+    int64_t ld, hs;
+    uint16_t* y;
+    int64_t ldy, hsy;
+    const uint16_t* w;
+    int32_t H;
+    int32_t reserved;         /* must be 0 */
+} us_heads;
+
+/* Norm and rotation of the call's tokens' query heads q and key heads k (either may
+ * be NULL) of D values, D a multiple of 8 up to 256.  B requests (at most 1024). */
+us_status us_norm_rope(const us_rope* rope, int D, const us_heads* q, const us_heads* k, int B, int T,
+                       const int32_t* tok_off, const int32_t* pos, const int32_t* depth, int max_n, void* stream);
+
+/* us_norm_rope of q (or NULL) and k, then us_kv_write of the k rows it gives and of
+ * V, in one pass: the same bits.  D and the heads of k are the cache's; k->y may be
+ * NULL (the rotated keys go to the cache only).  Entries go to positions pos[b] + i,
+ * whatever depth says. */
+us_status us_kv_append(const us_kv_cache* C, const us_rope* rope, const us_heads* q, const us_heads* k, const uint16_t* V,
+                       int64_t ldv, int T, const int32_t* tok_off, const int32_t* pos, const int32_t* depth, int max_n,
+                       void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Latent attention: a cache of one fp16 row a token, Dc latent values from which
+ * every head's key and value derive and Dr values of a rotated key that all heads
+ * share.  (No counterpart on the pages.)
+ *   rows: [num_pages][page_size][Dc + Dr] fp16
+ *   page_table as in us_kv_cache, and its limits on page_size, B and max_pages.
+ * Dc: 256 or 512, Dr: 64 (US_ERR_UNSUPPORTED otherwise).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t Dc, Dr, page_size, num_pages, B, max_pages;
+    uint16_t* rows;
+    const int32_t* page_table;
+} us_lat_cache;
+
+/* Append: row t of X (Dc latent values, then Dr of the key, fp16, ldx elements apart)
+ * becomes the entry of position pos[b] + i: the latent values normed as in
+ * us_norm_rope (w: Dc fp16 or NULL), the key rotated (rope->R = Dr, or 0).  What is
+ * stored is finite: beyond fp16 +-65504, NaN 0. */
+us_status us_lat_write(const us_lat_cache* C, const us_rope* rope, const uint16_t* X, int64_t ldx, const uint16_t* w,
+                       int T, const int32_t* tok_off, const int32_t* pos, const int32_t* depth, int max_n, void* stream);
+
+/* The entries of positions pos[b] .. as rows of Dc + Dr values. */
+us_status us_lat_read(const us_lat_cache* C, int T, const int32_t* tok_off, const int32_t* pos, int max_n, uint16_t* X,
+                      int64_t ldx, void* stream);
+
+/* us_kv_commit for latent rows. */
+us_status us_lat_commit(const us_lat_cache* C, int T, const int32_t* acc_off, const int32_t* acc, const int32_t* pos,
+                        int max_n, void* stream);
+
+/* Attention in the latent space (queries taken through the keys' expansion before,
+ * outputs to be taken through the values' after), over the entries of the call's
+ * tokens and of what came before them, seen as in us_attn_kv:
+ *   O[t][h] = fp16(sum_p w_p c_p / sum_p w_p),  w_p = exp(scale * Q[t][h].row_p)
+ * with row_p the entry's Dc + Dr values and c_p its first Dc; at most 65504 in
+ * magnitude, 0 for a row that sees no position.  Scores, sums and outputs are
+ * accumulated in fp32; a weight enters its product as fp16, rounded once.  Entries of
+ * positions that are read are finite (us_lat_write stores no others); what lies
+ * behind a request's last position is not looked at.
+ * Q: T rows of Hq heads of Dc + Dr values, O: of Dc.  mask, max_n, errors and the
+ * workspace (zeroed once) as in us_attn_kv; Hq <= 1024.  Repeated calls give the same
+ * bits. */
+us_status us_attn_lat(const us_lat_cache* C, const uint16_t* Q, int64_t ldq, int Hq, int T, const int32_t* tok_off,
+                      const int32_t* pos, const uint64_t* mask, int max_n, float scale, uint16_t* O, int64_t ldo,
+                      void* ws, size_t ws_bytes, void* stream);
+us_status us_attn_lat_workspace_bytes(const us_lat_cache* C, int Hq, int max_n, size_t* bytes);
+
+/* Attention over expanded rows (a prompt's tokens: keys and values of each head made
+ * from latent rows by a product).  Request b owns query rows tok_off[b] ..
+ * tok_off[b+1]-1 and the key rows kv_off[b] .. kv_off[b+1]-1 (int32 [B+1]) of K, KR
+ * and V; its n queries are the last n of its key rows' tokens, and query i sees key
+ * rows up to its own:
+ *   O[t][h] = fp16(sum_p w_p V[p][h] / sum_p w_p)
+ *   w_p = exp(scale * (Q[t][h][:Dn] . K[p][h] + Q[t][h][Dn:] . KR[p]))
+ * at most 65504 in magnitude; accumulation and weights as in us_attn_lat.
+ * Key rows that a query does not see have no part in its output, whatever they hold
+ * as long as it is finite; rows outside kv_off[b] .. are not looked at.
+ * Q: T rows of H heads of Dn + Dr values side by side, O: of Dv; K: S rows of Dn
+ * values a head, ldk elements apart, a head hsk behind the last; V the same, of Dv;
+ * KR: S rows of Dr.  Distances are multiples of 8.  (Dn, Dr, Dv): (128, 64, 128) or
+ * (64, 64, 64) (US_ERR_UNSUPPORTED otherwise); B and H at most 1024; S < 2^31.
+ * Offsets that do not ascend, leave 0..T or 0..S, give a request more than max_n
+ * queries or more queries than key rows record US_ERR_INVALID_ARG and the request is
+ * skipped.  Workspace: zeroed once.  Repeated calls give the same bits. */
+typedef struct {
+    int32_t Dn, Dr, Dv, H;
+    const uint16_t* K;
+    int64_t ldk, hsk;
+    const uint16_t* KR;
+    int64_t ldkr;
+    const uint16_t* V;
+    int64_t ldv, hsv;
+    int64_t S;
+} us_attn_kv_rows;
+us_status us_attn_rows(const us_attn_kv_rows* A, const uint16_t* Q, int64_t ldq, int B, int T, const int32_t* tok_off,
+                       const int32_t* kv_off, int max_n, float scale, uint16_t* O, int64_t ldo, void* ws,
+                       size_t ws_bytes, void* stream);
+us_status us_attn_rows_workspace_bytes(const us_attn_kv_rows* A, int B, int max_n, size_t* bytes);
+
 /* Workspace bytes for `op` on W with N tokens and the given split_k
  * (0 = the automatic choice).  For US_OP_ENCODE only W->M, K, TM, TK are read. */
 us_status us_workspace_bytes(us_op op, const us_bitmap* W, int N, int split_k, size_t* bytes);
