@@ -856,10 +856,10 @@ us_status us_lat_commit(const us_lat_cache* C, int T, const int32_t* acc_off, co
 us_status us_attn_lat_workspace_bytes(const us_lat_cache* C, int Hq, int max_n, size_t* bytes) {
     if (!bytes) return US_ERR_INVALID_ARG;
     UsAttnLatParams p = {};
-    const us_status s = check_attn_lat(C, Hq, max_n, p.L);
+    UsLatCache L;
+    const us_status s = check_attn_lat(C, Hq, max_n, L);
     if (s != US_OK) return s;
-    p.Hq = Hq;
-    p.a.max_n = max_n;
+    p.Dc = L.Dc;
     *bytes = us::attn_lat_ws(p);
     return US_OK;
 }
@@ -868,19 +868,23 @@ us_status us_attn_lat(const us_lat_cache* C, const uint16_t* Q, int64_t ldq, int
                       const int32_t* pos, const uint64_t* mask, int max_n, float scale, uint16_t* O, int64_t ldo,
                       void* ws, size_t ws_bytes, void* stream) {
     UsAttnLatParams p = {};
-    us_status s = check_attn_lat(C, Hq, max_n, p.L);
+    UsLatCache L;
+    us_status s = check_attn_lat(C, Hq, max_n, L);
     if (s == US_OK) s = check_tokens(T, tok_off, pos, nullptr, max_n, p.a);
     if (s != US_OK) return s;
     if (!(scale - scale == 0.f)) return US_ERR_INVALID_ARG;
     if (mask && max_n > 64) return US_ERR_UNSUPPORTED;
     if (mask && !aligned16(mask)) return US_ERR_INVALID_ARG;
     if (T == 0) return US_OK;
-    s = check_rows(Q, ldq, Hq, p.L.W);
-    if (s == US_OK) s = check_rows(O, ldo, Hq, p.L.Dc);
+    s = check_rows(Q, ldq, Hq, L.W);
+    if (s == US_OK) s = check_rows(O, ldo, Hq, L.Dc);
     if (s != US_OK) return s;
-    p.Q = Q; p.O = O; p.ldq = ldq; p.ldo = ldo; p.Hq = Hq; p.scale = scale; p.mask = mask;
+    p.c = L.c;
+    p.c.Hkv = 1;
+    p.Q = Q; p.O = O; p.ldq = ldq; p.ldo = ldo; p.Hq = p.G = Hq; p.scale = scale; p.mask = mask;
+    p.rows = L.rows; p.Dc = L.Dc; p.W = L.W;
     const size_t need = us::attn_lat_ws(p);
-    if (need && (!ws || ws_bytes < need || !aligned16(ws))) return US_ERR_WORKSPACE;
+    if (!ws || ws_bytes < need || !aligned16(ws)) return US_ERR_WORKSPACE;
     p.ws = ws;
     return us::launch_attn_lat(p, static_cast<cudaStream_t>(stream));
 }

@@ -120,18 +120,21 @@ struct Request {
     int row0, n, ctx, nrb;
 };
 
+// Positions before the tokens of request b, rows o0 .. o1 - 1.
+US_DEV int context_at(const UsAttnParams& p, int b, int, int) { return p.a.pos[b]; }
+
 // Tiles that row block rb of ROWS rows reads: a chain's rows see no position
 // behind their own.
-template <int ROWS, int TILE>
-US_DEV int tiles_of(const UsAttnParams& p, const Request& r, int rb) {
+template <int ROWS, int TILE, class P>
+US_DEV int tiles_of(const P& p, const Request& r, int rb) {
     unsigned end = (unsigned)r.n;
     if (!p.mask && rb + 1 < r.nrb) end = (unsigned)((rb + 1) * ROWS - 1) / (unsigned)p.G + 1u;   // n G < 2^30
     return (int)(((unsigned)r.ctx + end + TILE - 1u) / TILE);
 }
 
 // The request whose tokens are rows o0 .. o1 - 1, with `ctx` positions before them.
-template <int ROWS>
-US_DEV Request make_request(const UsAttnParams& p, int o0, int o1, int ctx, unsigned* status) {
+template <int ROWS, class P>
+US_DEV Request make_request(const P& p, int o0, int o1, int ctx, unsigned* status) {
     Request r = {o0, us::kv_row_count(p.a, o0, o1, status), 0, 0};
     if (r.n > 0) {
         r.ctx = us::kv_context(p.c, ctx, r.n, status);
@@ -139,15 +142,16 @@ US_DEV Request make_request(const UsAttnParams& p, int o0, int o1, int ctx, unsi
     }
     return r;
 }
-template <int ROWS>
-US_DEV Request load_request(const UsAttnParams& p, int b, unsigned* status) {
-    return make_request<ROWS>(p, p.a.off[b], p.a.off[b + 1], p.a.pos[b], status);
+template <int ROWS, class P>
+US_DEV Request load_request(const P& p, int b, unsigned* status) {
+    const int o0 = p.a.off[b], o1 = p.a.off[b + 1];
+    return make_request<ROWS>(p, o0, o1, context_at(p, b, o0, o1), status);
 }
 
 // Tiles of one key head of a request.  A chain's row blocks are walked without
 // dividing: the tokens of (rb + 1) ROWS rows from those of rb ROWS.
-template <int ROWS, int TILE>
-US_DEV int64_t head_tiles(const UsAttnParams& p, const Request& r) {
+template <int ROWS, int TILE, class P>
+US_DEV int64_t head_tiles(const P& p, const Request& r) {
     if (r.nrb == 0) return 0;
     const unsigned last = ((unsigned)r.ctx + (unsigned)r.n + TILE - 1u) / TILE;
     if (p.mask) return (int64_t)r.nrb * last;
@@ -168,7 +172,8 @@ template <int ROWS, int TILE>
 struct Cursor {
     Request r;
     int b, h, rb, tile, tiles;                             // tiles: of this row block
-    US_DEV void next(const UsAttnParams& p) {
+    template <class P>
+    US_DEV void next(const P& p) {
         if (++tile < tiles) return;
         tile = 0;
         if (++rb == r.nrb) {
@@ -185,7 +190,8 @@ struct Cursor {
         tiles = tiles_of<ROWS, TILE>(p, r, rb);
     }
     // to the row block behind this one
-    US_DEV void next_segment(const UsAttnParams& p) {
+    template <class P>
+    US_DEV void next_segment(const P& p) {
         tile = tiles - 1;
         next(p);
     }
@@ -226,8 +232,8 @@ struct Work {
 // requests, a scan over the lanes finds the one with the share's first tile (4500
 // cycles by a scan over the block with 64-bit divisions, at 16 row blocks of a chain
 // 15000).
-template <int ROWS, int TILE>
-US_DEV bool find_work(const UsAttnParams& p, Work& w, Cursor<ROWS, TILE>& at) {
+template <int ROWS, int TILE, class P>
+US_DEV bool find_work(const P& p, Work& w, Cursor<ROWS, TILE>& at) {
     const int lane = threadIdx.x & 31;
     unsigned* status = blockIdx.x == 0 && threadIdx.x < 32 ? p.c.status : nullptr;
     const int each = (p.c.B + 31) / 32, b0 = lane * each, b1 = min(b0 + each, p.c.B);
@@ -238,7 +244,7 @@ US_DEV bool find_work(const UsAttnParams& p, Work& w, Cursor<ROWS, TILE>& at) {
 #pragma unroll
         for (int u = 0; u < 5; ++u) off[u] = b + u <= b1 ? p.a.off[b + u] : 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) pos[u] = b + u < b1 ? p.a.pos[b + u] : 0;
+        for (int u = 0; u < 4; ++u) pos[u] = b + u < b1 ? context_at(p, b + u, off[u], off[u + 1]) : 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             if (b + u >= b1) break;
@@ -295,8 +301,8 @@ US_DEV bool find_work(const UsAttnParams& p, Work& w, Cursor<ROWS, TILE>& at) {
 }
 
 // Where a row's fp16 outputs go: D values at row r of row block rb, head h.
-template <int ROWS>
-US_DEV uint16_t* out_row(const UsAttnParams& p, int row0, int h, int rb, int r, int D) {
+template <int ROWS, class P>
+US_DEV uint16_t* out_row(const P& p, int row0, int h, int rb, int r, int D) {
     const int rr = rb * ROWS + r, i = rr / p.G;
     return p.O + (int64_t)(row0 + i) * p.ldo + (int64_t)(h * p.G + rr - i * p.G) * D;
 }

@@ -1,117 +1,579 @@
-// us_attn_lat.cu -- attention over latent rows and over expanded rows: one CTA a query
-// row and head, its warps taking the positions in turn, with a running maximum and sum
-// each, joined at the end.
+// us_attn_lat.cu -- attention over the paged cache of latent rows, on the tensor cores
+// (tcgen05).
+//
+// All heads of a token share one key row of W = Dc + 64 values, whose first Dc are the
+// value row too: the n Hq query rows of a request are the rows of one product,
+//   S = Q X^T     A = Q (shared memory), B = 64 positions' rows X, K-major
+//   O += P X_c    A = P (shared memory, fp16), B = the same X in shared memory,
+//                 its first Dc columns, MN-major
+// so a position's row is read once and used twice, for 64 query rows.
+//
+// A segment is (request, block of 64 query rows); its positions come in tiles of 64,
+// and the tiles of all segments are spread evenly over the CTAs (one an SM).  64 rows
+// a block, not 128: O's 512 columns of 128 rows would take all of TMEM.  A product of
+// 64 rows takes 16 lanes of each warp's 32 in TMEM; O's columns 256 .. 511 lie in the
+// other 16 lanes, so O takes 256 columns and two tiles' scores 128 more.
+//   warps 0-3: softmax of 16 rows each, the segment's Q and its outputs
+//   warp 4: finds pages and issues the tiles' copies (TMA, 128-byte swizzle)
+//   warp 5: one thread issues the MMAs, whichever of the next tile's scores (its rows
+//           have landed) and the last one's outputs (its weights are there) can go
+// Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set, and
+// moves when a score passes R + 14 (fp16 holds 2^14 and keeps all bits of weights down
+// to 2^-25 of the largest).  R, sums and outputs of a segment shared by several CTAs
+// are joined by a second kernel.
+#include <atomic>
+
 #include "us_attn_lat.cuh"
 #include "us_internal.h"
 #include "us_launch.cuh"
+#include "us_tcgen05.cuh"
 
 namespace {
 
-constexpr int kWarps = 4;
+using namespace us::attn;
 
-US_DEV float2 two(const uint16_t* p) { return __half22float2(*reinterpret_cast<const __half2*>(p)); }
+constexpr int kM = 64, kTile = 64;                // query rows of a segment, positions of a tile
+constexpr int kSoftWarps = 4, kLoadWarp = 4, kMmaWarp = 5, kThreads = 192;
+constexpr float kTop = 11.f, kRoom = 14.f;        // log2 of a row's largest weight when R is set, and at most
+constexpr int kBlock = 64 * 128;                  // bytes of 64 rows of 64 values
+constexpr int kMaxStages = 4;
 
-// KW, VW: values of a key and of a value; key(p, j), value(p, j): two values from the
-// 2j-th on; seen(p)
-template <int KW, int VW, class Key, class Value, class Seen>
-US_DEV void attend(const uint16_t* q, uint16_t* out, int positions, float scale, Key key, Value value, Seen seen) {
-    __shared__ float part[kWarps][VW + 2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float m = -INFINITY, l = 0.f, o[VW / 32] = {};
-    for (int p = warp; p < positions; p += kWarps) {
-        if (!seen(p)) continue;
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < KW / 64; ++j) {
-            const float2 a = two(q + 2 * (lane + 32 * j)), b = key(p, lane + 32 * j);
-            s = fmaf(a.x, b.x, fmaf(a.y, b.y, s));
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= scale;
-        const float t = fmaxf(m, s), f = m == -INFINITY ? 0.f : expf(m - t), w = expf(s - t);
-        l = l * f + w;
-        m = t;
-#pragma unroll
-        for (int j = 0; j < VW / 64; ++j) {
-            const float2 v = value(p, lane + 32 * j);
-            o[2 * j] = o[2 * j] * f + w * v.x;
-            o[2 * j + 1] = o[2 * j + 1] * f + w * v.y;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < VW / 64; ++j)
-        part[warp][2 * (lane + 32 * j)] = o[2 * j], part[warp][2 * (lane + 32 * j) + 1] = o[2 * j + 1];
-    if (lane == 0) part[warp][VW] = m, part[warp][VW + 1] = l;
-    __syncthreads();
-    float top = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part[w][VW]);
-    for (int w = 0; w < kWarps; ++w) sum += part[w][VW] == -INFINITY ? 0.f : part[w][VW + 1] * expf(part[w][VW] - top);
-    for (int d = threadIdx.x; d < VW; d += 32 * kWarps) {
-        float y = 0.f;
-        for (int w = 0; w < kWarps; ++w)
-            if (part[w][VW] != -INFINITY) y += part[w][d] * expf(part[w][VW] - top);
-        y = sum == 0.f ? 0.f : y / sum;
-        out[d] = us::float_to_half_bits(y != y ? y : fminf(fmaxf(y, -65504.f), 65504.f));
-    }
+struct Header {
+    uint64_t full[kMaxStages], free[kMaxStages], s_full[2], p_full, pv_done, q_full;
+    uint64_t valid[kMaxStages];                   // which of the tile's positions exist
+    uint32_t tmem;
+};
+
+template <int DC>
+struct Shape {
+    static constexpr int kW = DC + us::kLatDr, kC = kW / 64;        // blocks of 64 values of a row
+    static constexpr int kOperand = kC * kBlock;                    // Q, or a tile's rows
+    static constexpr int kStages = DC == 512 ? 2 : 4;
+    static constexpr int kHalves = DC / 256;                        // products of 256 columns of O
+    static constexpr int kSmem = (1 + kStages) * kOperand + kBlock + (int)sizeof(Header) + 1024;
+    static constexpr int kSlotFloats = 2 * kM + kM * DC;            // of a partial state
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+US_DEV void tma_load_rows(void* dst, const CUtensorMap* map, int row, int block, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(us::smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(block), "r"(us::smem_addr(bar))
+        : "memory");
+}
+
+// 16 lanes x 64 columns in fragment order: lane (g, c) gets rows g (v[4k], v[4k + 1])
+// and g + 8 (v[4k + 2], v[4k + 3]) of columns 8k + 2c, 8k + 2c + 1
+US_DEV void tmem_ld_frag64(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+    us::tmem_ld_frag32_end(r, v);
+}
+US_DEV void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+        "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]),
+        "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]),
+        "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]),
+        "r"(taddr)
+        : "memory");
 }
 
 template <int DC>
-__global__ void __launch_bounds__(32 * kWarps) attn_lat_kernel(const UsAttnLatParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map) {
+    using Sh = Shape<DC>;
+    constexpr int kStages = Sh::kStages;
+    using Cur = Cursor<kM, kTile>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((0u - us::smem_addr(smem_raw)) & 1023u);
+    uint8_t* q_sm = smem;
+    uint8_t* x_sm = q_sm + Sh::kOperand;
+    uint8_t* p_sm = x_sm + kStages * Sh::kOperand;
+    Header& H = *reinterpret_cast<Header*>(p_sm + kBlock);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) us::mbar_init(&H.full[i], 1), us::mbar_init(&H.free[i], 1);
+        for (int i = 0; i < 2; ++i) us::mbar_init(&H.s_full[i], 1);
+        us::mbar_init(&H.p_full, kSoftWarps), us::mbar_init(&H.pv_done, 1), us::mbar_init(&H.q_full, kSoftWarps);
+        us::fence_mbar_init();
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
+    }
+    if (warp == kMmaWarp) us::tmem_alloc(&H.tmem, 512);
+    us::tc_fence_before();
+    __syncthreads();
+    us::tc_fence_after();
     us::pdl_wait();
-    const int b = blockIdx.y, i = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
-    int row0;
-    const int n = us::kv_rows(p.a, b, row0, p.L.c.status);
-    const int ctx = n ? us::kv_context(p.L.c, p.a.pos[b], n, p.L.c.status) : -1;
-    if (i < n && ctx >= 0) {
-        const uint64_t own = p.mask ? p.mask[row0 + i] : 0;
-        auto row = [&](int pos) { return us::lat_row(p.L, b, pos); };
-        attend<DC + us::kLatDr, DC>(
-            p.Q + (int64_t)(row0 + i) * p.ldq + (int64_t)h * p.L.W, p.O + (int64_t)(row0 + i) * p.ldo + (int64_t)h * DC, ctx + n,
-            p.scale, [&](int pos, int j) { return two(p.L.rows + row(pos) + 2 * j); },
-            [&](int pos, int j) { return two(p.L.rows + row(pos) + 2 * j); },
-            [&](int pos) {
-                if (pos >= ctx && !(p.mask ? own >> (pos - ctx) & 1 : pos - ctx <= i)) return false;
-                return row(pos) >= 0;
-            });
+
+    Work wk;
+    Cur cur;
+    const bool any = find_work<kM, kTile>(p, wk, cur);
+    const uint32_t tmem = H.tmem;                          // O: 256 columns; scores: 2 x 64
+    const int count = any ? (int)(wk.t1 - wk.t0) : 0, G = p.G;
+    bool failed = false;
+    auto wait = [&](uint64_t* bar, int use) {              // for the use-th completion of bar
+        if (!failed && !wait_bar(bar, (uint32_t)use & 1u, p.c.status)) failed = true;
+    };
+
+    if (warp < kSoftWarps) {
+        // ----------------------------------------------------------- softmax
+        const int g = lane >> 2, c2 = 2 * (lane & 3), wrow = 16 * warp;
+        const uint32_t lanes = (uint32_t)warp * 32u << 16;
+        const float scale = p.scale * 1.4426950408889634f;
+        if (threadIdx.x == 0) p.ws_parts[blockIdx.x].rows = 0;     // until a shared segment begins here
+        // A segment's Q on its way to shared memory: two threads a row
+        auto request_q = [&](const Cur& at) {
+            const int r = threadIdx.x >> 1, rr = at.rb * kM + r;
+            if (rr < at.r.n * G) {
+                const int i = (int)((unsigned)rr / (unsigned)G), h = rr - i * G;
+                const uint16_t* src = p.Q + (int64_t)(at.r.row0 + i) * p.ldq + (int64_t)h * Sh::kW;
+                const uint32_t to = us::smem_addr(q_sm) + r * 128;
+#pragma unroll 9
+                for (int k = threadIdx.x & 1; k < Sh::kW / 8; k += 2)
+                    cp_async16(to + (k >> 3) * kBlock + (((k & 7) ^ (r & 7)) << 4), src + 8 * k);
+            }
+            cp_async_commit();
+        };
+        if (count) request_q(cur);
+        for (int it = 0; it < count;) {
+            // ---- a segment, or this CTA's part of it: tiles it .. end - 1
+            const int end = min(count, it + cur.tiles - cur.tile), tile0 = cur.tile;
+            const int rows = min(kM, cur.r.n * G - cur.rb * kM);
+            cp_async_wait<0>();
+            us::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) us::mbar_arrive(&H.q_full);
+            Cur next = cur;
+            if (end < count) next.next_segment(p);
+            // what the lane's rows see of the call's own positions: their masks, or in a chain how many
+            uint64_t own_seen[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int r = wrow + 8 * q + g, tok = (int)((unsigned)(cur.rb * kM + r) / (unsigned)G);
+                own_seen[q] = r >= rows ? 0 : p.mask ? p.mask[cur.r.row0 + tok] & (~0ull >> (64 - cur.r.n)) : (uint64_t)(tok + 1);
+            }
+            // positions that a row sees among 64 from `base` behind the context
+            auto seen64 = [&](int base, uint64_t row) {
+                if (base <= -64) return ~0ull;
+                const int lo = base < 0 ? -base : 0;       // context positions among them
+                uint64_t own;
+                if (p.mask) {
+                    own = base < 64 ? row >> (base > 0 ? base : 0) : 0ull;
+                } else {
+                    const int k = (int)row - (base > 0 ? base : 0);
+                    own = k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1ull;
+                }
+                return (own << lo) | (lo ? ~0ull >> (64 - lo) : 0ull);
+            };
+            float R[2] = {-INFINITY, -INFINITY};           // of the lane's rows wrow + 8 q + g
+            uint64_t l2[2] = {};                           // their sums, two partial ones each
+            for (int i = it; i < end; ++i) {
+                const int st = i % kStages;
+                wait(&H.full[st], i / kStages);            // (the scores came from it: for its positions)
+                wait(&H.s_full[i & 1], i >> 1);
+                us::tc_fence_after();
+                if (i == end - 1 && end < count) request_q(next);  // nothing reads this segment's Q any more
+                const uint64_t ok = H.valid[st];
+                const int base = (tile0 + i - it) * kTile - cur.r.ctx;
+                if (wrow < rows) {
+                    float v[32];
+                    tmem_ld_frag64(tmem + lanes + 256 + 64 * (i & 1), v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] *= scale;
+                    if (base + 64 > 0 || ok != ~0ull) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint64_t seen = (seen64(base, own_seen[q]) & ok) >> c2;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (!((seen >> (8 * k + e)) & 1ull)) v[4 * k + 2 * q + e] = -INFINITY;
+                        }
+                    }
+                    uint64_t neg[2];
+                    float f[2];
+                    bool moved = false;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) top = max3(top, v[4 * k + 2 * q], v[4 * k + 2 * q + 1]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        const float to = top > R[q] + kRoom ? top - kTop : R[q];
+                        f[q] = to == R[q] ? 1.f : ex2(R[q] - to);
+                        moved |= to != R[q];
+                        R[q] = to;
+                        l2[q] = mul2(l2[q], pair(f[q], f[q]));
+                        const float ref = to == -INFINITY ? 0.f : to;
+                        neg[q] = pair(-ref, -ref);
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            float x, y;
+                            unpair(add2(pair(v[4 * k + 2 * q], v[4 * k + 2 * q + 1]), neg[q]), x, y);
+                            const uint64_t e = pair(ex2(x), ex2(y));
+                            l2[q] = add2(l2[q], e);
+                            unpair(e, x, y);
+                            w[2 * k + q] = pack_half2(x, y);
+                        }
+                    if (i > it) {                          // the tile before: its weights are read, the outputs so far there
+                        wait(&H.pv_done, i - 1);
+                        us::tc_fence_after();
+                        if (__any_sync(0xffffffffu, moved)) {
+                            // lane: row lane & 15, of which row g = lane & 7 of the quads' first or second ones
+                            const float f0 = __shfl_sync(0xffffffffu, f[0], 4 * (lane & 7)), f1 = __shfl_sync(0xffffffffu, f[1], 4 * (lane & 7));
+                            const float fr = lane & 8 ? f1 : f0;
+#pragma unroll 1
+                            for (int c = 0; c < 256; c += 32) {
+                                float y[32];
+                                us::tmem_ld32(tmem + lanes + c, y);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) y[j] *= fr;
+                                tmem_st32(tmem + lanes + c, y);
+                            }
+                            us::tmem_wait_st();
+                        }
+                    }
+                    uint8_t* to = p_sm + (wrow + g) * 128 + 2 * c2;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        *reinterpret_cast<uint32_t*>(to + ((k ^ g) << 4)) = w[2 * k];
+                        *reinterpret_cast<uint32_t*>(to + 1024 + ((k ^ g) << 4)) = w[2 * k + 1];
+                    }
+                }
+                if (ok != ~0ull) {                         // what lies where no position is counts as 0
+                    uint8_t* x = x_sm + st * Sh::kOperand;
+                    for (int r = 0; r < kTile; ++r)
+                        if (!((ok >> r) & 1ull))
+                            for (int k = threadIdx.x; k < DC / 8; k += 32 * kSoftWarps)
+                                *reinterpret_cast<uint4*>(x + (k >> 3) * kBlock + r * 128 + ((k & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                }
+                us::fence_proxy_async_smem();
+                us::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) us::mbar_arrive(&H.p_full);
+            }
+            // ---- the segment's end
+            wait(&H.pv_done, end - 1);
+            us::tc_fence_after();
+            const int64_t s0 = wk.t0 + it - tile0;
+            const Part part = wk.sharers(s0, s0 + cur.tiles, cur, rows);
+            const bool whole = part.first == part.last;
+            if (wrow < rows) {
+                float l[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float a, b;
+                    unpair(l2[q], a, b);
+                    a += b;
+                    a += __shfl_xor_sync(0xffffffffu, a, 1);
+                    l[q] = a + __shfl_xor_sync(0xffffffffu, a, 2);
+                }
+                const int src = 4 * (lane & 7), row = wrow + (lane & 15);
+                const float l0 = __shfl_sync(0xffffffffu, l[0], src), l1 = __shfl_sync(0xffffffffu, l[1], src);
+                const float r0 = __shfl_sync(0xffffffffu, R[0], src), r1 = __shfl_sync(0xffffffffu, R[1], src);
+                const float sum = lane & 8 ? l1 : l0, ref = lane & 8 ? r1 : r0, inv = sum == 0.f ? 0.f : 1.f / sum;
+                float* slot = p.ws_slots + part.slot(blockIdx.x) * Sh::kSlotFloats;
+                if (!whole && lane < 16) {
+                    __stcg(slot + row, ref);
+                    __stcg(slot + kM + row, sum);
+                }
+                const bool mine = row < rows && (Sh::kHalves == 2 || lane < 16);
+                const int col0 = lane & 16 ? 256 : 0;
+                uint16_t* out = mine ? out_row<kM>(p, cur.r.row0, 0, cur.rb, row, DC) + col0 : nullptr;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 32) {
+                    float a[32];
+                    us::tmem_ld32(tmem + lanes + c, a);
+                    if (mine && whole) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            *reinterpret_cast<uint4*>(out + c + j) =
+                                make_uint4(pack_out(a[j] * inv, a[j + 1] * inv), pack_out(a[j + 2] * inv, a[j + 3] * inv),
+                                           pack_out(a[j + 4] * inv, a[j + 5] * inv), pack_out(a[j + 6] * inv, a[j + 7] * inv));
+                    } else if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            __stcg(reinterpret_cast<float4*>(slot + 2 * kM) + (col0 + c + j) / 4 * kM + row,
+                                   make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!whole && part.first == (int)blockIdx.x && threadIdx.x == 0) p.ws_parts[blockIdx.x] = part;
+            it = end;
+            cur = next;
+        }
+    } else if (warp == kLoadWarp) {
+        // ------------------------------------------------------------- copies
+        // Pieces of a page each (page_size positions, 64 at most): one copy for 64, else
+        // one for each 64 values of its rows.
+        const int piece = min(kTile, 1 << p.c.page_shift), pieces = kTile / piece, shift = __ffs(piece) - 1;
+        for (int it = 0; it < count;) {
+            const int end = min(count, it + cur.tiles - cur.tile), last = cur.r.ctx + cur.r.n;
+            const int32_t* table = p.c.table + (int64_t)cur.b * p.c.max_pages;
+            // page of this lane's piece among 32, and the 32 behind them on their way
+            auto page_of = [&](int at) {                   // of the piece-th piece of the segment's part
+                const int pos = cur.tile * kTile + ((at + lane) << shift);
+                return pos < last ? table[pos >> p.c.page_shift] : -1;
+            };
+            int ids = page_of(0), ahead = page_of(32), at = 0;
+            for (int i = it; i < end; ++i, at += pieces) {
+                if (at && (at & 31) == 0) ids = ahead, ahead = page_of(at + 32);
+                const int st = i % kStages, pos0 = (cur.tile + i - it) * kTile;
+                if (i >= kStages) wait(&H.free[st], i / kStages - 1);
+                uint8_t* x = x_sm + st * Sh::kOperand;
+                uint64_t ok = 0;
+                int bytes = 0;
+                for (int k = 0; k < pieces; ++k) {
+                    const int id = __shfl_sync(0xffffffffu, ids, (at + k) & 31), pos = pos0 + (k << shift), here = min(piece, last - pos);
+                    if (here <= 0) break;
+                    if (id < 0 || id >= p.c.num_pages) {
+                        us::set_status(p.c.status, US_ERR_CORRUPT);
+                        continue;
+                    }
+                    ok |= (here == 64 ? ~0ull : (1ull << here) - 1ull) << (k << shift);
+                    bytes += piece * Sh::kW * 2;
+                }
+                if (lane == 0) {
+                    H.valid[st] = ok;
+                    if (bytes) us::mbar_arrive_expect_tx(&H.full[st], (uint32_t)bytes);
+                    else us::mbar_arrive(&H.full[st]);
+                }
+                __syncwarp();
+                for (int k = 0; k < pieces; ++k) {
+                    const int id = __shfl_sync(0xffffffffu, ids, (at + k) & 31);
+                    if (!((ok >> (k << shift)) & 1ull)) continue;
+                    const int row = (id << p.c.page_shift) + ((pos0 + (k << shift)) & ((1 << p.c.page_shift) - 1));
+                    if (pieces == 1) {
+                        if (lane == 0) tma_load_rows(x, &map, row, 0, &H.full[st]);
+                    } else if (lane < Sh::kC) {
+                        tma_load_rows(x + lane * kBlock + (k << shift) * 128, &map, row, lane, &H.full[st]);
+                    }
+                }
+                __syncwarp();
+            }
+            it = end;
+            if (it < count) cur.next_segment(p);
+        }
+        // nothing of its own is left in flight when the CTA ends
+        for (int i = max(0, count - kStages); i < count; ++i) wait(&H.full[i % kStages], i / kStages);
+    } else {
+        // --------------------------------------------------------------- MMA
+        if (us::elect_one()) {
+            int segment = 0;
+            for (int it = 0; it < count && !failed; ++segment) {
+                const int end = min(count, it + cur.tiles - cur.tile);
+                wait(&H.q_full, segment);
+                us::tc_fence_after();
+                const uint64_t qd = us::umma_smem_desc_sw128(q_sm), pd = us::umma_smem_desc_sw128(p_sm);
+                int s = it, o = it;                        // the next tile's scores, the next one's outputs
+                uint64_t since = 0;
+                unsigned idle = 0;
+                while (o < end && !failed) {
+                    const int st = s % kStages;
+                    if (s < end && s - o < 2 && us::mbar_test(&H.full[st], (uint32_t)(s / kStages) & 1u)) {
+                        constexpr uint32_t id = us::umma_idesc_f16(kM, kTile);
+                        us::tc_fence_after();
+                        const uint64_t xd = us::umma_smem_desc_sw128(x_sm + st * Sh::kOperand);
+#pragma unroll
+                        for (int kk = 0; kk < Sh::kW / 16; ++kk) {
+                            const uint64_t at = (uint64_t)(((kk >> 2) * kBlock + (kk & 3) * 32) >> 4);
+                            us::umma_f16(tmem + 256 + 64 * (s & 1), qd + at, xd + at, id, kk > 0);
+                        }
+                        us::umma_commit(&H.s_full[s & 1]);
+                        ++s, idle = 0;
+                    } else if (o < s && us::mbar_test(&H.p_full, (uint32_t)o & 1u)) {
+                        constexpr uint32_t id = us::umma_idesc_f16(kM, 256) | us::kUmmaBMajorMN;
+                        us::tc_fence_after();
+                        const int os = o % kStages;
+#pragma unroll
+                        for (int h = 0; h < Sh::kHalves; ++h) {
+                            const uint64_t xd = us::umma_smem_desc_mn_sw128(x_sm + os * Sh::kOperand + 4 * h * kBlock, kBlock);
+#pragma unroll
+                            for (int kk = 0; kk < kTile / 16; ++kk)
+                                us::umma_f16(tmem + ((uint32_t)(16 * h) << 16), pd + (uint64_t)(kk * 32 >> 4),
+                                             xd + (uint64_t)(kk * 2048 >> 4), id, o > it || kk > 0);
+                        }
+                        us::umma_commit(&H.free[os]);
+                        us::umma_commit(&H.pv_done);
+                        ++o, idle = 0;
+                    } else if ((++idle & 1023u) == 0) {    // bounded, as every wait
+                        const uint64_t now = us::globaltimer_ns();
+                        if (idle == 1024u) since = now;
+                        else if (now - since > us::kWaitLimitNs) us::set_status(p.c.status, US_ERR_TIMEOUT), failed = true;
+                    }
+                }
+                it = end;
+                if (it < count) cur.next_segment(p);
+            }
+            // Arrivals that no other warp waits for: they land while the CTA still has its shared memory
+            if (count) {
+                for (int i = max(0, count - kStages); i < count; ++i) wait(&H.free[i % kStages], i / kStages);
+                wait(&H.pv_done, count - 1);
+            }
+        }
+        __syncwarp();
+    }
+    us::tc_fence_before();
+    __syncthreads();
+    us::tc_fence_after();
+    if (warp == kMmaWarp) us::tmem_dealloc(tmem, 512);
+    us::pdl_launch_dependents();
+}
+
+// Joins the partial states of shared segments: pieces of 16 rows and 16 columns, whose
+// states eight groups of 64 threads take in turn and add up through shared memory.
+constexpr int kMaxCtas = 512, kJoinThreads = 512, kGroups = kJoinThreads / 64, kAtOnce = 4;
+template <int DC>
+__global__ void __launch_bounds__(kJoinThreads)
+attn_lat_join_kernel(const UsAttnLatParams p, int ctas) {
+    using Sh = Shape<DC>;
+    __shared__ uint16_t list[kMaxCtas];
+    __shared__ uint16_t upto[kMaxCtas];           // pieces of the listed segments up to this one, itself among them, in rows of 16
+    __shared__ int listed;
+    __shared__ float held[6][kJoinThreads];
+    us::pdl_wait();
+    if (threadIdx.x < 32) {
+        int n = 0, sum = 0;
+        for (int c0 = 0; c0 < ctas; c0 += 32) {
+            const int c = c0 + (int)threadIdx.x;
+            const int rows = c < ctas ? p.ws_parts[c].rows : 0;
+            const unsigned who = __ballot_sync(0xffffffffu, rows > 0);
+            const int incl = us::warp_incl_scan((rows + 15) / 16);
+            if (rows > 0) {
+                const int at = n + __popc(who & ((1u << threadIdx.x) - 1u));
+                list[at] = (uint16_t)c, upto[at] = (uint16_t)(sum + incl);
+            }
+            n += __popc(who), sum += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (threadIdx.x == 0) listed = n;
+    }
+    __syncthreads();
+    const int group = threadIdx.x / 64, t = threadIdx.x & 63;
+    constexpr int kCols = DC / 16;
+    const int pieces = listed ? (int)upto[listed - 1] * kCols : 0;
+    for (int x = blockIdx.x; x < pieces; x += gridDim.x) {
+        const int block = x / kCols;
+        int s = 0;
+        while (upto[s] <= block) ++s;
+        const Part a = p.ws_parts[list[s]];
+        const int row = (block - (s ? upto[s - 1] : 0)) * 16 + (t & 15), col = (x % kCols) * 16 + (t >> 4) * 4;
+        float top = -INFINITY, sum = 0.f, y[4] = {};
+        for (int c = a.first + group; c <= a.last; c += kGroups * kAtOnce) {
+            float4 v[kAtOnce];
+            float r[kAtOnce], l[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int cta = c + u * kGroups;
+                r[u] = -INFINITY, l[u] = 0.f, v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (cta <= a.last && row < a.rows) {
+                    const float* sl = p.ws_slots + a.slot(cta) * Sh::kSlotFloats;
+                    r[u] = __ldcg(sl + row), l[u] = __ldcg(sl + kM + row);
+                    v[u] = __ldcg(reinterpret_cast<const float4*>(sl + 2 * kM) + col / 4 * kM + row);
+                }
+            }
+            float m = top;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) m = fmaxf(m, r[u]);
+            // (a state without a reference has weights 0, or NaN, which stays)
+            const float at = m == -INFINITY ? 0.f : m, f0 = ex2(top - at);
+            sum *= f0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] *= f0;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const float f = ex2(r[u] - at);
+                sum += l[u] * f;
+                y[0] += v[u].x * f, y[1] += v[u].y * f, y[2] += v[u].z * f, y[3] += v[u].w * f;
+            }
+            top = m;
+        }
+        held[0][threadIdx.x] = top, held[1][threadIdx.x] = sum;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) held[2 + i][threadIdx.x] = y[i];
+        __syncthreads();
+        if (group == 0 && row < a.rows) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kGroups; ++u) m = fmaxf(m, held[0][64 * u + t]);
+            const float at = m == -INFINITY ? 0.f : m;
+            sum = 0.f, y[0] = y[1] = y[2] = y[3] = 0.f;
+#pragma unroll
+            for (int u = 0; u < kGroups; ++u) {
+                const float f = ex2(held[0][64 * u + t] - at);
+                sum += held[1][64 * u + t] * f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] += held[2 + i][64 * u + t] * f;
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            *reinterpret_cast<uint2*>(out_row<kM>(p, a.row0, 0, a.rb, row, DC) + col) =
+                make_uint2(pack_out(y[0] * inv, y[1] * inv), pack_out(y[2] * inv, y[3] * inv));
+        }
+        __syncthreads();
     }
     us::pdl_launch_dependents();
 }
 
-template <int DN, int DV>
-__global__ void __launch_bounds__(32 * kWarps) attn_rows_kernel(const UsAttnRowsParams p) {
-    us::pdl_wait();
-    const int b = blockIdx.y, i = blockIdx.x / p.k.H, h = blockIdx.x % p.k.H;
-    const int row0 = p.off[b], n = p.off[b + 1] - row0, k0 = p.kv_off[b], kn = p.kv_off[b + 1] - k0;
-    const bool ok = row0 >= 0 && n >= 0 && row0 + n <= p.T && n <= p.max_n && k0 >= 0 && kn >= n && k0 + (int64_t)kn <= p.k.S;
-    if (!ok) us::set_status(p.status, US_ERR_INVALID_ARG);
-    if (ok && i < n) {
-        attend<DN + 64, DV>(
-            p.Q + (int64_t)(row0 + i) * p.ldq + (int64_t)h * (DN + 64), p.O + (int64_t)(row0 + i) * p.ldo + (int64_t)h * DV,
-            kn - n + i + 1, p.scale,
-            [&](int pos, int j) {
-                return 2 * j < DN ? two(p.k.K + (k0 + pos) * p.k.ldk + h * p.k.hsk + 2 * j)
-                                  : two(p.k.KR + (k0 + pos) * p.k.ldkr + 2 * j - DN);
-            },
-            [&](int pos, int j) { return two(p.k.V + (k0 + pos) * p.k.ldv + h * p.k.hsv + 2 * j); },
-            [](int) { return true; });
+int grid() { return us::num_sms() < kMaxCtas ? us::num_sms() : kMaxCtas; }
+constexpr int kPartBytes = kMaxCtas * 32;
+static_assert(sizeof(Part) <= 32, "parts");
+
+template <int DC>
+us_status launch(UsAttnLatParams p, cudaStream_t st) {
+    using Sh = Shape<DC>;
+    auto enc = us::tensor_map_encoder();
+    if (!enc) return US_ERR_CUDA;
+    p.ws_parts = static_cast<Part*>(p.ws);
+    p.ws_slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kPartBytes);
+    // the cache as (64 values, rows, blocks of 64 values)
+    CUtensorMap map;
+    const int page = 1 << p.c.page_shift;
+    const cuuint64_t dim[3] = {64, (cuuint64_t)p.c.num_pages * page, (cuuint64_t)Sh::kC}, stride[2] = {(cuuint64_t)Sh::kW * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(page < kTile ? page : kTile), (cuuint32_t)(page < kTile ? 1 : Sh::kC)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(p.rows), dim, stride, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return US_ERR_CUDA;
+    auto kern = attn_lat_kernel<DC>;
+    static std::atomic<bool> ready[64];                // the attribute is set once a device, by whichever thread
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return US_ERR_CUDA;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess)
+            return US_ERR_CUDA;
+        ready[dev].store(true, std::memory_order_release);
     }
-    us::pdl_launch_dependents();
+    us_status s = us::launch_pdl(kern, dim3((unsigned)grid()), kThreads, Sh::kSmem, st, p, map);
+    if (s != US_OK) return s;
+    return us::launch_pdl(attn_lat_join_kernel<DC>, dim3((unsigned)(4 * us::num_sms())), kJoinThreads, 0, st, p, grid());
 }
 
 }  // namespace
 
 namespace us {
 
-size_t attn_lat_ws(const UsAttnLatParams&) { return 0; }
-us_status launch_attn_lat(const UsAttnLatParams& p, cudaStream_t st) {
-    return launch_pdl(p.L.Dc == 512 ? attn_lat_kernel<512> : attn_lat_kernel<256>,
-                      dim3((unsigned)(p.a.max_n * p.Hq), (unsigned)p.L.c.B), 32 * kWarps, 0, st, p);
+size_t attn_lat_ws(const UsAttnLatParams& p) {
+    return kPartBytes + (size_t)2 * grid() * (2 * kM + kM * p.Dc) * 4;
 }
-size_t attn_rows_ws(const UsAttnRowsParams&) { return 0; }
-us_status launch_attn_rows(const UsAttnRowsParams& p, cudaStream_t st) {
-    return launch_pdl(p.k.Dn == 128 ? attn_rows_kernel<128, 128> : attn_rows_kernel<64, 64>,
-                      dim3((unsigned)(p.max_n * p.k.H), (unsigned)p.B), 32 * kWarps, 0, st, p);
-}
+
+us_status launch_attn_lat(const UsAttnLatParams& p, cudaStream_t st) { return p.Dc == 512 ? launch<512>(p, st) : launch<256>(p, st); }
 
 }  // namespace us

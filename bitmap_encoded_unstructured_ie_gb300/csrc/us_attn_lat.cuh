@@ -1,18 +1,14 @@
-// us_attn_lat.cuh -- parameters of the attention over latent rows and over expanded rows.
+// us_attn_lat.cuh -- parameters of the attention over latent rows and over expanded
+// rows, and the join of the states that several CTAs hold of one segment.
 #pragma once
 
+#include "us_attn.cuh"
 #include "us_lat.cuh"
 
-struct UsAttnLatParams {
-    UsLatCache L;
-    UsKvCall a;
-    const uint16_t* Q;
-    uint16_t* O;
-    int64_t ldq, ldo;
-    int Hq;
-    float scale;
-    const uint64_t* mask;            // per token, or nullptr: a chain
-    void* ws;
+// Of the base: c has the pages and one key head, G = Hq.
+struct UsAttnLatParams : UsAttnParams {
+    const uint16_t* rows;
+    int Dc, W;
 };
 
 struct UsAttnRowsParams {
