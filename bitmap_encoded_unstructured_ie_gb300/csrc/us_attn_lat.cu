@@ -39,7 +39,7 @@ constexpr int kBlock = 64 * 128;                  // bytes of 64 rows of 64 valu
 constexpr int kMaxStages = 4;
 
 struct Header {
-    uint64_t full[kMaxStages], free[kMaxStages], s_full[2], p_full, pv_done, q_full;
+    uint64_t full[kMaxStages][3], free[kMaxStages][3], s_full[2], p_full, pv_done, q_full;
     uint64_t valid[kMaxStages];                   // which of the tile's positions exist
     uint32_t tmem;
 };
@@ -50,10 +50,28 @@ struct Shape {
     static constexpr int kOperand = kC * kBlock;                    // Q, or a tile's rows
     static constexpr int kStages = DC == 512 ? 2 : 4;
     static constexpr int kHalves = DC / 256;                        // products of 256 columns of O
+    // A tile's parts land and are freed by themselves: those of each half's columns,
+    // and the key's 64 values (part kHalves), which the scores alone read.
+    static constexpr int kParts = kHalves + 1;
     static constexpr int kSmem = (1 + kStages) * kOperand + kBlock + (int)sizeof(Header) + 1024;
     static constexpr int kSlotFloats = 2 * kM + kM * DC;            // of a partial state
     static_assert(kSmem <= 232448, "shared memory");
 };
+
+// Waits for phase `parity` of `bar`, at most kWaitLimitNs (then US_ERR_TIMEOUT is
+// recorded).  Without a pause between tries: six warps leave the issue slots to it.
+US_DEV bool spin(uint64_t* bar, uint32_t parity, unsigned* status) {
+    if (us::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = us::globaltimer_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int n = 0; n < 1024; ++n)
+            if (us::mbar_try_wait(bar, parity)) return true;
+        if (us::globaltimer_ns() - t0 > us::kWaitLimitNs) break;
+    }
+    us::set_status(status, US_ERR_TIMEOUT);
+    return false;
+}
 
 US_DEV void tma_load_rows(void* dst, const CUtensorMap* map, int row, int block, uint64_t* bar) {
     asm volatile(
@@ -104,7 +122,8 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) us::mbar_init(&H.full[i], 1), us::mbar_init(&H.free[i], 1);
+        for (int i = 0; i < kStages; ++i)
+            for (int j = 0; j < Sh::kParts; ++j) us::mbar_init(&H.full[i][j], 1), us::mbar_init(&H.free[i][j], 1);
         for (int i = 0; i < 2; ++i) us::mbar_init(&H.s_full[i], 1);
         us::mbar_init(&H.p_full, kSoftWarps), us::mbar_init(&H.pv_done, 1), us::mbar_init(&H.q_full, kSoftWarps);
         us::fence_mbar_init();
@@ -123,7 +142,7 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
     const int count = any ? (int)(wk.t1 - wk.t0) : 0, G = p.G;
     bool failed = false;
     auto wait = [&](uint64_t* bar, int use) {              // for the use-th completion of bar
-        if (!failed && !wait_bar(bar, (uint32_t)use & 1u, p.c.status)) failed = true;
+        if (!failed && !spin(bar, (uint32_t)use & 1u, p.c.status)) failed = true;
     };
 
     if (warp < kSoftWarps) {
@@ -145,15 +164,18 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
             }
             cp_async_commit();
         };
+        auto hand_over_q = [&]() {
+            cp_async_wait<0>();
+            us::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) us::mbar_arrive(&H.q_full);
+        };
         if (count) request_q(cur);
         for (int it = 0; it < count;) {
             // ---- a segment, or this CTA's part of it: tiles it .. end - 1
             const int end = min(count, it + cur.tiles - cur.tile), tile0 = cur.tile;
             const int rows = min(kM, cur.r.n * G - cur.rb * kM);
-            cp_async_wait<0>();
-            us::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) us::mbar_arrive(&H.q_full);
+            if (it == 0) hand_over_q();
             Cur next = cur;
             if (end < count) next.next_segment(p);
             // what the lane's rows see of the call's own positions: their masks, or in a chain how many
@@ -180,7 +202,7 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
             uint64_t l2[2] = {};                           // their sums, two partial ones each
             for (int i = it; i < end; ++i) {
                 const int st = i % kStages;
-                wait(&H.full[st], i / kStages);            // (the scores came from it: for its positions)
+                wait(&H.full[st][0], i / kStages);         // (the scores came from it: for its positions)
                 wait(&H.s_full[i & 1], i >> 1);
                 us::tc_fence_after();
                 if (i == end - 1 && end < count) request_q(next);  // nothing reads this segment's Q any more
@@ -257,6 +279,8 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
                         *reinterpret_cast<uint32_t*>(to + 1024 + ((k ^ g) << 4)) = w[2 * k + 1];
                     }
                 }
+                // (a warp without rows must not arrive for this tile while the last one's phase is open)
+                if (wrow >= rows && i > it) wait(&H.pv_done, i - 1);
                 if (ok != ~0ull) {                         // what lies where no position is counts as 0
                     uint8_t* x = x_sm + st * Sh::kOperand;
                     for (int r = 0; r < kTile; ++r)
@@ -269,7 +293,8 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
                 __syncwarp();
                 if (lane == 0) us::mbar_arrive(&H.p_full);
             }
-            // ---- the segment's end
+            // ---- the segment's end; the next one's first scores are made meanwhile
+            if (end < count) hand_over_q();
             wait(&H.pv_done, end - 1);
             us::tc_fence_after();
             const int64_t s0 = wk.t0 + it - tile0;
@@ -322,58 +347,64 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
         }
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------- copies
-        // Pieces of a page each (page_size positions, 64 at most): one copy for 64, else
-        // one for each 64 values of its rows.
+        // Pieces of a page each (page_size positions, 64 at most), a copy for each 64
+        // values of their rows, a lane each.
         const int piece = min(kTile, 1 << p.c.page_shift), pieces = kTile / piece, shift = __ffs(piece) - 1;
+        // page of this lane's piece among the 32 from piece `first` of a segment's part on
+        auto page_of = [&](const Cur& c, int first) {
+            const int pos = c.tile * kTile + ((first + lane) << shift);
+            return pos < c.r.ctx + c.r.n ? p.c.table[(int64_t)c.b * p.c.max_pages + (pos >> p.c.page_shift)] : -1;
+        };
+        int ids = count ? page_of(cur, 0) : -1;
         for (int it = 0; it < count;) {
             const int end = min(count, it + cur.tiles - cur.tile), last = cur.r.ctx + cur.r.n;
-            const int32_t* table = p.c.table + (int64_t)cur.b * p.c.max_pages;
-            // page of this lane's piece among 32, and the 32 behind them on their way
-            auto page_of = [&](int at) {                   // of the piece-th piece of the segment's part
-                const int pos = cur.tile * kTile + ((at + lane) << shift);
-                return pos < last ? table[pos >> p.c.page_shift] : -1;
-            };
-            int ids = page_of(0), ahead = page_of(32), at = 0;
+            Cur next = cur;
+            if (end < count) next.next_segment(p);
+            // the pages behind these, and the next segment's first ones, on their way
+            int ahead = page_of(cur, 32), at = 0;
+            const int after = end < count ? page_of(next, 0) : -1;
             for (int i = it; i < end; ++i, at += pieces) {
-                if (at && (at & 31) == 0) ids = ahead, ahead = page_of(at + 32);
+                if (at && (at & 31) == 0) ids = ahead, ahead = page_of(cur, at + 32);
                 const int st = i % kStages, pos0 = (cur.tile + i - it) * kTile;
-                if (i >= kStages) wait(&H.free[st], i / kStages - 1);
-                uint8_t* x = x_sm + st * Sh::kOperand;
                 uint64_t ok = 0;
-                int bytes = 0;
+                int bytes = 0;                             // of 64 values
                 for (int k = 0; k < pieces; ++k) {
-                    const int id = __shfl_sync(0xffffffffu, ids, (at + k) & 31), pos = pos0 + (k << shift), here = min(piece, last - pos);
+                    const int id = __shfl_sync(0xffffffffu, ids, (at + k) & 31), here = min(piece, last - pos0 - (k << shift));
                     if (here <= 0) break;
                     if (id < 0 || id >= p.c.num_pages) {
                         us::set_status(p.c.status, US_ERR_CORRUPT);
                         continue;
                     }
                     ok |= (here == 64 ? ~0ull : (1ull << here) - 1ull) << (k << shift);
-                    bytes += piece * Sh::kW * 2;
+                    bytes += piece * 128;
                 }
-                if (lane == 0) {
-                    H.valid[st] = ok;
-                    if (bytes) us::mbar_arrive_expect_tx(&H.full[st], (uint32_t)bytes);
-                    else us::mbar_arrive(&H.full[st]);
-                }
-                __syncwarp();
-                for (int k = 0; k < pieces; ++k) {
-                    const int id = __shfl_sync(0xffffffffu, ids, (at + k) & 31);
-                    if (!((ok >> (k << shift)) & 1ull)) continue;
-                    const int row = (id << p.c.page_shift) + ((pos0 + (k << shift)) & ((1 << p.c.page_shift) - 1));
-                    if (pieces == 1) {
-                        if (lane == 0) tma_load_rows(x, &map, row, 0, &H.full[st]);
-                    } else if (lane < Sh::kC) {
-                        tma_load_rows(x + lane * kBlock + (k << shift) * 128, &map, row, lane, &H.full[st]);
+                uint8_t* x = x_sm + st * Sh::kOperand;
+#pragma unroll
+                for (int j = 0; j < Sh::kParts; ++j) {
+                    const int part = j ? j - 1 : Sh::kHalves, blocks = j ? 4 : 1;      // the key's part first
+                    if (i >= kStages) wait(&H.free[st][part], i / kStages - 1);
+                    if (lane == 0) {
+                        if (j == 1) H.valid[st] = ok;      // (part 0 was freed by those who read it)
+                        if (bytes) us::mbar_arrive_expect_tx(&H.full[st][part], (uint32_t)(blocks * bytes));
+                        else us::mbar_arrive(&H.full[st][part]);
                     }
+                    __syncwarp();
+                    for (int k = 0; k < pieces; ++k) {
+                        const int id = __shfl_sync(0xffffffffu, ids, (at + k) & 31), block = 4 * part + lane;
+                        if (((ok >> (k << shift)) & 1ull) && lane < blocks)
+                            tma_load_rows(x + block * kBlock + (k << shift) * 128, &map,
+                                          (id << p.c.page_shift) + ((pos0 + (k << shift)) & ((1 << p.c.page_shift) - 1)), block,
+                                          &H.full[st][part]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             it = end;
-            if (it < count) cur.next_segment(p);
+            cur = next, ids = after;
         }
         // nothing of its own is left in flight when the CTA ends
-        for (int i = max(0, count - kStages); i < count; ++i) wait(&H.full[i % kStages], i / kStages);
+        for (int i = max(0, count - kStages); i < count; ++i)
+            for (int j = 0; j < Sh::kParts; ++j) wait(&H.full[i % kStages][j], i / kStages);
     } else {
         // --------------------------------------------------------------- MMA
         if (us::elect_one()) {
@@ -383,22 +414,36 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
                 wait(&H.q_full, segment);
                 us::tc_fence_after();
                 const uint64_t qd = us::umma_smem_desc_sw128(q_sm), pd = us::umma_smem_desc_sw128(p_sm);
-                int s = it, o = it;                        // the next tile's scores, the next one's outputs
+                int s = it, sp = 0, o = it;                // the next tile's scores (from part sp on), the next one's outputs
                 uint64_t since = 0;
                 unsigned idle = 0;
                 while (o < end && !failed) {
-                    const int st = s % kStages;
-                    if (s < end && s - o < 2 && us::mbar_test(&H.full[st], (uint32_t)(s / kStages) & 1u)) {
+                    const int st = s % kStages, part = sp ? sp - 1 : Sh::kHalves;
+                    if (s < end && s - o < 2 && us::mbar_test(&H.full[st][part], (uint32_t)(s / kStages) & 1u)) {
                         constexpr uint32_t id = us::umma_idesc_f16(kM, kTile);
                         us::tc_fence_after();
-                        const uint64_t xd = us::umma_smem_desc_sw128(x_sm + st * Sh::kOperand);
+                        const uint64_t from = (uint64_t)(4 * part * kBlock >> 4);
+                        const uint64_t q = qd + from, xd = us::umma_smem_desc_sw128(x_sm + st * Sh::kOperand) + from;
+                        const uint32_t to = tmem + 256 + 64 * (s & 1);
+                        auto block = [&](int k, bool first) {
 #pragma unroll
-                        for (int kk = 0; kk < Sh::kW / 16; ++kk) {
-                            const uint64_t at = (uint64_t)(((kk >> 2) * kBlock + (kk & 3) * 32) >> 4);
-                            us::umma_f16(tmem + 256 + 64 * (s & 1), qd + at, xd + at, id, kk > 0);
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const uint64_t at = (uint64_t)((k * kBlock + kk * 32) >> 4);
+                                us::umma_f16(to, q + at, xd + at, id, !first || kk > 0);
+                            }
+                        };
+                        if (sp == 0) {
+                            block(0, true);
+                            us::umma_commit(&H.free[st][Sh::kHalves]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) block(k, false);
                         }
-                        us::umma_commit(&H.s_full[s & 1]);
-                        ++s, idle = 0;
+                        if (++sp == Sh::kParts) {
+                            us::umma_commit(&H.s_full[s & 1]);
+                            ++s, sp = 0;
+                        }
+                        idle = 0;
                     } else if (o < s && us::mbar_test(&H.p_full, (uint32_t)o & 1u)) {
                         constexpr uint32_t id = us::umma_idesc_f16(kM, 256) | us::kUmmaBMajorMN;
                         us::tc_fence_after();
@@ -410,8 +455,8 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
                             for (int kk = 0; kk < kTile / 16; ++kk)
                                 us::umma_f16(tmem + ((uint32_t)(16 * h) << 16), pd + (uint64_t)(kk * 32 >> 4),
                                              xd + (uint64_t)(kk * 2048 >> 4), id, o > it || kk > 0);
+                            us::umma_commit(&H.free[os][h]);
                         }
-                        us::umma_commit(&H.free[os]);
                         us::umma_commit(&H.pv_done);
                         ++o, idle = 0;
                     } else if ((++idle & 1023u) == 0) {    // bounded, as every wait
@@ -425,7 +470,8 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
             }
             // Arrivals that no other warp waits for: they land while the CTA still has its shared memory
             if (count) {
-                for (int i = max(0, count - kStages); i < count; ++i) wait(&H.free[i % kStages], i / kStages);
+                for (int i = max(0, count - kStages); i < count; ++i)
+                    for (int j = 0; j < Sh::kParts; ++j) wait(&H.free[i % kStages][j], i / kStages);
                 wait(&H.pv_done, count - 1);
             }
         }
@@ -438,56 +484,54 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
     us::pdl_launch_dependents();
 }
 
-// Joins the partial states of shared segments: pieces of 16 rows and 16 columns, whose
-// states eight groups of 64 threads take in turn and add up through shared memory.
-constexpr int kMaxCtas = 512, kJoinThreads = 512, kGroups = kJoinThreads / 64, kAtOnce = 4;
-template <int DC>
+// Joins the partial states of shared segments.  A thread adds up kVec times four
+// columns of a row, kAtOnce states at once; its group of threads takes every
+// GROUPS-th state of the segment, and the groups' sums are added in shared memory.
+// Few segments have many sharers each and are given 8 groups; many have about two, and
+// one group does.  blockIdx.x: a shared segment and 16 of its rows (of `blocks` such),
+// blockIdx.y: which columns; segments by the CTA that shares one first, or, where they
+// are few, counted.
+constexpr int kMaxCtas = 512, kJoinThreads = 256;
+template <int DC, int GROUPS>
 __global__ void __launch_bounds__(kJoinThreads)
-attn_lat_join_kernel(const UsAttnLatParams p, int ctas) {
+attn_lat_join_kernel(const UsAttnLatParams p, int blocks, int ctas) {
     using Sh = Shape<DC>;
-    __shared__ uint16_t list[kMaxCtas];
-    __shared__ uint16_t upto[kMaxCtas];           // pieces of the listed segments up to this one, itself among them, in rows of 16
-    __shared__ int listed;
-    __shared__ float held[6][kJoinThreads];
+    constexpr int kVec = GROUPS == 1 ? 4 : 1, kAtOnce = GROUPS == 1 ? 2 : 4, kLanes = kJoinThreads / GROUPS;
+    __shared__ float held[GROUPS == 1 ? 1 : 6][kJoinThreads];
     us::pdl_wait();
-    if (threadIdx.x < 32) {
-        int n = 0, sum = 0;
-        for (int c0 = 0; c0 < ctas; c0 += 32) {
-            const int c = c0 + (int)threadIdx.x;
-            const int rows = c < ctas ? p.ws_parts[c].rows : 0;
-            const unsigned who = __ballot_sync(0xffffffffu, rows > 0);
-            const int incl = us::warp_incl_scan((rows + 15) / 16);
-            if (rows > 0) {
-                const int at = n + __popc(who & ((1u << threadIdx.x) - 1u));
-                list[at] = (uint16_t)c, upto[at] = (uint16_t)(sum + incl);
-            }
-            n += __popc(who), sum += __shfl_sync(0xffffffffu, incl, 31);
+    int which = (int)blockIdx.x / blocks;
+    if constexpr (GROUPS > 1) {
+        const int lane = threadIdx.x & 31;
+        int at = -1;
+        for (int c0 = 0; c0 < ctas && at < 0; c0 += 32) {
+            const unsigned who = __ballot_sync(0xffffffffu, c0 + lane < ctas && p.ws_parts[c0 + lane].rows > 0);
+            if (which < __popc(who)) at = c0 + __fns(who, 0, which + 1);
+            else which -= __popc(who);
         }
-        if (threadIdx.x == 0) listed = n;
+        which = at;
+        if (at < 0) {
+            us::pdl_launch_dependents();
+            return;
+        }
     }
-    __syncthreads();
-    const int group = threadIdx.x / 64, t = threadIdx.x & 63;
-    constexpr int kCols = DC / 16;
-    const int pieces = listed ? (int)upto[listed - 1] * kCols : 0;
-    for (int x = blockIdx.x; x < pieces; x += gridDim.x) {
-        const int block = x / kCols;
-        int s = 0;
-        while (upto[s] <= block) ++s;
-        const Part a = p.ws_parts[list[s]];
-        const int row = (block - (s ? upto[s - 1] : 0)) * 16 + (t & 15), col = (x % kCols) * 16 + (t >> 4) * 4;
-        float top = -INFINITY, sum = 0.f, y[4] = {};
-        for (int c = a.first + group; c <= a.last; c += kGroups * kAtOnce) {
-            float4 v[kAtOnce];
+    const Part a = p.ws_parts[which];
+    const int group = threadIdx.x / kLanes, t = threadIdx.x % kLanes;
+    const int row = (int)blockIdx.x % blocks * 16 + (t & 15), col = ((int)blockIdx.y * (kLanes / 16 * kVec) + (t >> 4)) * 4;
+    if (row - (t & 15) < a.rows) {                         // (uniform; 0 rows: no shared segment)
+        float top = -INFINITY, sum = 0.f, y[kVec][4] = {};
+        for (int c = a.first + group; c <= a.last; c += GROUPS * kAtOnce) {
+            float4 v[kAtOnce][kVec];
             float r[kAtOnce], l[kAtOnce];
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
-                const int cta = c + u * kGroups;
-                r[u] = -INFINITY, l[u] = 0.f, v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (cta <= a.last && row < a.rows) {
-                    const float* sl = p.ws_slots + a.slot(cta) * Sh::kSlotFloats;
-                    r[u] = __ldcg(sl + row), l[u] = __ldcg(sl + kM + row);
-                    v[u] = __ldcg(reinterpret_cast<const float4*>(sl + 2 * kM) + col / 4 * kM + row);
-                }
+                const int cta = c + u * GROUPS;
+                const bool there = cta <= a.last && row < a.rows;
+                const float* sl = p.ws_slots + a.slot(there ? cta : a.first) * Sh::kSlotFloats;
+                r[u] = there ? __ldcg(sl + row) : -INFINITY, l[u] = there ? __ldcg(sl + kM + row) : 0.f;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k)
+                    v[u][k] = there ? __ldcg(reinterpret_cast<const float4*>(sl + 2 * kM) + (col / 4 + k * (kLanes / 16)) * kM + row)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float m = top;
 #pragma unroll
@@ -496,37 +540,45 @@ attn_lat_join_kernel(const UsAttnLatParams p, int ctas) {
             const float at = m == -INFINITY ? 0.f : m, f0 = ex2(top - at);
             sum *= f0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] *= f0;
+            for (int k = 0; k < kVec; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[k][i] *= f0;
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
                 const float f = ex2(r[u] - at);
                 sum += l[u] * f;
-                y[0] += v[u].x * f, y[1] += v[u].y * f, y[2] += v[u].z * f, y[3] += v[u].w * f;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k)
+                    y[k][0] += v[u][k].x * f, y[k][1] += v[u][k].y * f, y[k][2] += v[u][k].z * f, y[k][3] += v[u][k].w * f;
             }
             top = m;
         }
-        held[0][threadIdx.x] = top, held[1][threadIdx.x] = sum;
+        if constexpr (GROUPS > 1) {
+            held[0][threadIdx.x] = top, held[1][threadIdx.x] = sum;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) held[2 + i][threadIdx.x] = y[i];
-        __syncthreads();
-        if (group == 0 && row < a.rows) {
+            for (int i = 0; i < 4; ++i) held[2 + i][threadIdx.x] = y[0][i];
+            __syncthreads();
             float m = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < kGroups; ++u) m = fmaxf(m, held[0][64 * u + t]);
+            for (int u = 0; u < GROUPS; ++u) m = fmaxf(m, held[0][kLanes * u + t]);
             const float at = m == -INFINITY ? 0.f : m;
-            sum = 0.f, y[0] = y[1] = y[2] = y[3] = 0.f;
+            sum = 0.f, y[0][0] = y[0][1] = y[0][2] = y[0][3] = 0.f;
 #pragma unroll
-            for (int u = 0; u < kGroups; ++u) {
-                const float f = ex2(held[0][64 * u + t] - at);
-                sum += held[1][64 * u + t] * f;
+            for (int u = 0; u < GROUPS; ++u) {
+                const float f = ex2(held[0][kLanes * u + t] - at);
+                sum += held[1][kLanes * u + t] * f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] += held[2 + i][64 * u + t] * f;
+                for (int i = 0; i < 4; ++i) y[0][i] += held[2 + i][kLanes * u + t] * f;
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            *reinterpret_cast<uint2*>(out_row<kM>(p, a.row0, 0, a.rb, row, DC) + col) =
-                make_uint2(pack_out(y[0] * inv, y[1] * inv), pack_out(y[2] * inv, y[3] * inv));
         }
-        __syncthreads();
+        if (group == 0 && row < a.rows) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            uint16_t* out = out_row<kM>(p, a.row0, 0, a.rb, row, DC) + col;
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                *reinterpret_cast<uint2*>(out + k * (kLanes / 4)) =
+                    make_uint2(pack_out(y[k][0] * inv, y[k][1] * inv), pack_out(y[k][2] * inv, y[k][3] * inv));
+        }
     }
     us::pdl_launch_dependents();
 }
@@ -546,7 +598,7 @@ us_status launch(UsAttnLatParams p, cudaStream_t st) {
     CUtensorMap map;
     const int page = 1 << p.c.page_shift;
     const cuuint64_t dim[3] = {64, (cuuint64_t)p.c.num_pages * page, (cuuint64_t)Sh::kC}, stride[2] = {(cuuint64_t)Sh::kW * 2, 128};
-    const cuuint32_t box[3] = {64, (cuuint32_t)(page < kTile ? page : kTile), (cuuint32_t)(page < kTile ? 1 : Sh::kC)};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(page < kTile ? page : kTile), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(p.rows), dim, stride, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -563,7 +615,11 @@ us_status launch(UsAttnLatParams p, cudaStream_t st) {
     }
     us_status s = us::launch_pdl(kern, dim3((unsigned)grid()), kThreads, Sh::kSmem, st, p, map);
     if (s != US_OK) return s;
-    return us::launch_pdl(attn_lat_join_kernel<DC>, dim3((unsigned)(4 * us::num_sms())), kJoinThreads, 0, st, p, grid());
+    const int64_t rows = (int64_t)p.a.max_n * p.G, segments = (rows + kM - 1) / kM * p.c.B;       // at most
+    const int blocks = rows < kM ? ((int)rows + 15) / 16 : kM / 16, ctas = grid();
+    return 8 * segments <= ctas
+               ? us::launch_pdl(attn_lat_join_kernel<DC, 8>, dim3((unsigned)(segments * blocks), DC / 8), kJoinThreads, 0, st, p, blocks, ctas)
+               : us::launch_pdl(attn_lat_join_kernel<DC, 1>, dim3((unsigned)(ctas * blocks), DC / 256), kJoinThreads, 0, st, p, blocks, ctas);
 }
 
 }  // namespace
