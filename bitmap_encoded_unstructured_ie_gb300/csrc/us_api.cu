@@ -894,7 +894,7 @@ us_status us_attn_rows_workspace_bytes(const us_attn_kv_rows* A, int B, int max_
     const us_status s = check_attn_rows(A, B, max_n);
     if (s != US_OK) return s;
     UsAttnRowsParams p = {};
-    p.k = *A; p.B = B; p.max_n = max_n;
+    p.k = *A;
     *bytes = us::attn_rows_ws(p);
     return US_OK;
 }
@@ -913,14 +913,16 @@ us_status us_attn_rows(const us_attn_kv_rows* A, const uint16_t* Q, int64_t ldq,
     if (s != US_OK) return s;
     if (!A->K || !A->V || !aligned16(A->K) || !aligned16(A->V) || A->S < 1) return US_ERR_INVALID_ARG;
     if (!heads_apart(A->ldk, A->hsk, A->H, A->Dn) || !heads_apart(A->ldv, A->hsv, A->H, A->Dv)) return US_ERR_INVALID_ARG;
-    if (A->S >= (int64_t)1 << 31) return US_ERR_TOO_LARGE;
+    if (A->S > (int64_t)1 << 30) return US_ERR_TOO_LARGE;
     UsAttnRowsParams p = {};
     p.k = *A;
-    p.Q = Q; p.O = O; p.ldq = ldq; p.ldo = ldo; p.B = B; p.T = T; p.max_n = max_n;
-    p.off = tok_off; p.kv_off = kv_off; p.scale = scale;
-    p.status = status_ptr();
+    p.c.Hkv = A->H; p.c.B = B; p.c.page_shift = 10; p.c.max_pages = 1 << 20;       // 2^30 positions
+    p.c.status = status_ptr();
+    p.a.off = tok_off; p.a.T = T; p.a.max_n = max_n;
+    p.Q = Q; p.O = O; p.ldq = ldq; p.ldo = ldo; p.Hq = A->H; p.G = 1; p.scale = scale;
+    p.kv_off = kv_off;
     const size_t need = us::attn_rows_ws(p);
-    if (need && (!ws || ws_bytes < need || !aligned16(ws))) return US_ERR_WORKSPACE;
+    if (!ws || ws_bytes < need || !aligned16(ws)) return US_ERR_WORKSPACE;
     p.ws = ws;
     return us::launch_attn_rows(p, static_cast<cudaStream_t>(stream));
 }

@@ -120,9 +120,6 @@ struct Request {
     int row0, n, ctx, nrb;
 };
 
-// Positions before the tokens of request b, rows o0 .. o1 - 1.
-US_DEV int context_at(const UsAttnParams& p, int b, int, int) { return p.a.pos[b]; }
-
 // Tiles that row block rb of ROWS rows reads: a chain's rows see no position
 // behind their own.
 template <int ROWS, int TILE, class P>
@@ -145,7 +142,7 @@ US_DEV Request make_request(const P& p, int o0, int o1, int ctx, unsigned* statu
 template <int ROWS, class P>
 US_DEV Request load_request(const P& p, int b, unsigned* status) {
     const int o0 = p.a.off[b], o1 = p.a.off[b + 1];
-    return make_request<ROWS>(p, o0, o1, context_at(p, b, o0, o1), status);
+    return make_request<ROWS>(p, o0, o1, p.context(b, o0, o1), status);
 }
 
 // Tiles of one key head of a request.  A chain's row blocks are walked without
@@ -244,7 +241,7 @@ US_DEV bool find_work(const P& p, Work& w, Cursor<ROWS, TILE>& at) {
 #pragma unroll
         for (int u = 0; u < 5; ++u) off[u] = b + u <= b1 ? p.a.off[b + u] : 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) pos[u] = b + u < b1 ? context_at(p, b + u, off[u], off[u + 1]) : 0;
+        for (int u = 0; u < 4; ++u) pos[u] = b + u < b1 ? p.context(b + u, off[u], off[u + 1]) : 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             if (b + u >= b1) break;

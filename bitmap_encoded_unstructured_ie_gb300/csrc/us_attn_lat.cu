@@ -54,24 +54,9 @@ struct Shape {
     // and the key's 64 values (part kHalves), which the scores alone read.
     static constexpr int kParts = kHalves + 1;
     static constexpr int kSmem = (1 + kStages) * kOperand + kBlock + (int)sizeof(Header) + 1024;
-    static constexpr int kSlotFloats = 2 * kM + kM * DC;            // of a partial state
+    static constexpr int kSlotFloats = us::attn::slot_floats(kM, DC);
     static_assert(kSmem <= 232448, "shared memory");
 };
-
-// Waits for phase `parity` of `bar`, at most kWaitLimitNs (then US_ERR_TIMEOUT is
-// recorded).  Without a pause between tries: six warps leave the issue slots to it.
-US_DEV bool spin(uint64_t* bar, uint32_t parity, unsigned* status) {
-    if (us::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = us::globaltimer_ns();
-    for (;;) {
-#pragma unroll 1
-        for (int n = 0; n < 1024; ++n)
-            if (us::mbar_try_wait(bar, parity)) return true;
-        if (us::globaltimer_ns() - t0 > us::kWaitLimitNs) break;
-    }
-    us::set_status(status, US_ERR_TIMEOUT);
-    return false;
-}
 
 US_DEV void tma_load_rows(void* dst, const CUtensorMap* map, int row, int block, uint64_t* bar) {
     asm volatile(
@@ -484,109 +469,6 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
     us::pdl_launch_dependents();
 }
 
-// Joins the partial states of shared segments.  A thread adds up kVec times four
-// columns of a row, kAtOnce states at once; its group of threads takes every
-// GROUPS-th state of the segment, and the groups' sums are added in shared memory.
-// Few segments have many sharers each and are given 8 groups; many have about two, and
-// one group does.  blockIdx.x: a shared segment and 16 of its rows (of `blocks` such),
-// blockIdx.y: which columns; segments by the CTA that shares one first, or, where they
-// are few, counted.
-constexpr int kMaxCtas = 512, kJoinThreads = 256;
-template <int DC, int GROUPS>
-__global__ void __launch_bounds__(kJoinThreads)
-attn_lat_join_kernel(const UsAttnLatParams p, int blocks, int ctas) {
-    using Sh = Shape<DC>;
-    constexpr int kVec = GROUPS == 1 ? 4 : 1, kAtOnce = GROUPS == 1 ? 2 : 4, kLanes = kJoinThreads / GROUPS;
-    __shared__ float held[GROUPS == 1 ? 1 : 6][kJoinThreads];
-    us::pdl_wait();
-    int which = (int)blockIdx.x / blocks;
-    if constexpr (GROUPS > 1) {
-        const int lane = threadIdx.x & 31;
-        int at = -1;
-        for (int c0 = 0; c0 < ctas && at < 0; c0 += 32) {
-            const unsigned who = __ballot_sync(0xffffffffu, c0 + lane < ctas && p.ws_parts[c0 + lane].rows > 0);
-            if (which < __popc(who)) at = c0 + __fns(who, 0, which + 1);
-            else which -= __popc(who);
-        }
-        which = at;
-        if (at < 0) {
-            us::pdl_launch_dependents();
-            return;
-        }
-    }
-    const Part a = p.ws_parts[which];
-    const int group = threadIdx.x / kLanes, t = threadIdx.x % kLanes;
-    const int row = (int)blockIdx.x % blocks * 16 + (t & 15), col = ((int)blockIdx.y * (kLanes / 16 * kVec) + (t >> 4)) * 4;
-    if (row - (t & 15) < a.rows) {                         // (uniform; 0 rows: no shared segment)
-        float top = -INFINITY, sum = 0.f, y[kVec][4] = {};
-        for (int c = a.first + group; c <= a.last; c += GROUPS * kAtOnce) {
-            float4 v[kAtOnce][kVec];
-            float r[kAtOnce], l[kAtOnce];
-#pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const int cta = c + u * GROUPS;
-                const bool there = cta <= a.last && row < a.rows;
-                const float* sl = p.ws_slots + a.slot(there ? cta : a.first) * Sh::kSlotFloats;
-                r[u] = there ? __ldcg(sl + row) : -INFINITY, l[u] = there ? __ldcg(sl + kM + row) : 0.f;
-#pragma unroll
-                for (int k = 0; k < kVec; ++k)
-                    v[u][k] = there ? __ldcg(reinterpret_cast<const float4*>(sl + 2 * kM) + (col / 4 + k * (kLanes / 16)) * kM + row)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            float m = top;
-#pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) m = fmaxf(m, r[u]);
-            // (a state without a reference has weights 0, or NaN, which stays)
-            const float at = m == -INFINITY ? 0.f : m, f0 = ex2(top - at);
-            sum *= f0;
-#pragma unroll
-            for (int k = 0; k < kVec; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[k][i] *= f0;
-#pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const float f = ex2(r[u] - at);
-                sum += l[u] * f;
-#pragma unroll
-                for (int k = 0; k < kVec; ++k)
-                    y[k][0] += v[u][k].x * f, y[k][1] += v[u][k].y * f, y[k][2] += v[u][k].z * f, y[k][3] += v[u][k].w * f;
-            }
-            top = m;
-        }
-        if constexpr (GROUPS > 1) {
-            held[0][threadIdx.x] = top, held[1][threadIdx.x] = sum;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) held[2 + i][threadIdx.x] = y[0][i];
-            __syncthreads();
-            float m = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < GROUPS; ++u) m = fmaxf(m, held[0][kLanes * u + t]);
-            const float at = m == -INFINITY ? 0.f : m;
-            sum = 0.f, y[0][0] = y[0][1] = y[0][2] = y[0][3] = 0.f;
-#pragma unroll
-            for (int u = 0; u < GROUPS; ++u) {
-                const float f = ex2(held[0][kLanes * u + t] - at);
-                sum += held[1][kLanes * u + t] * f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[0][i] += held[2 + i][kLanes * u + t] * f;
-            }
-        }
-        if (group == 0 && row < a.rows) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            uint16_t* out = out_row<kM>(p, a.row0, 0, a.rb, row, DC) + col;
-#pragma unroll
-            for (int k = 0; k < kVec; ++k)
-                *reinterpret_cast<uint2*>(out + k * (kLanes / 4)) =
-                    make_uint2(pack_out(y[k][0] * inv, y[k][1] * inv), pack_out(y[k][2] * inv, y[k][3] * inv));
-        }
-    }
-    us::pdl_launch_dependents();
-}
-
-int grid() { return us::num_sms() < kMaxCtas ? us::num_sms() : kMaxCtas; }
-constexpr int kPartBytes = kMaxCtas * 32;
-static_assert(sizeof(Part) <= 32, "parts");
-
 template <int DC>
 us_status launch(UsAttnLatParams p, cudaStream_t st) {
     using Sh = Shape<DC>;
@@ -613,13 +495,9 @@ us_status launch(UsAttnLatParams p, cudaStream_t st) {
             return US_ERR_CUDA;
         ready[dev].store(true, std::memory_order_release);
     }
-    us_status s = us::launch_pdl(kern, dim3((unsigned)grid()), kThreads, Sh::kSmem, st, p, map);
+    us_status s = us::launch_pdl(kern, dim3((unsigned)us::attn::join_ctas()), kThreads, Sh::kSmem, st, p, map);
     if (s != US_OK) return s;
-    const int64_t rows = (int64_t)p.a.max_n * p.G, segments = (rows + kM - 1) / kM * p.c.B;       // at most
-    const int blocks = rows < kM ? ((int)rows + 15) / 16 : kM / 16, ctas = grid();
-    return 8 * segments <= ctas
-               ? us::launch_pdl(attn_lat_join_kernel<DC, 8>, dim3((unsigned)(segments * blocks), DC / 8), kJoinThreads, 0, st, p, blocks, ctas)
-               : us::launch_pdl(attn_lat_join_kernel<DC, 1>, dim3((unsigned)(ctas * blocks), DC / 256), kJoinThreads, 0, st, p, blocks, ctas);
+    return us::attn::launch_join<kM, DC>(p, st);
 }
 
 }  // namespace
@@ -627,7 +505,7 @@ us_status launch(UsAttnLatParams p, cudaStream_t st) {
 namespace us {
 
 size_t attn_lat_ws(const UsAttnLatParams& p) {
-    return kPartBytes + (size_t)2 * grid() * (2 * kM + kM * p.Dc) * 4;
+    return us::attn::join_ws(kM, p.Dc);
 }
 
 us_status launch_attn_lat(const UsAttnLatParams& p, cudaStream_t st) { return p.Dc == 512 ? launch<512>(p, st) : launch<256>(p, st); }

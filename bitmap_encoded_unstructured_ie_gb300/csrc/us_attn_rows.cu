@@ -1,90 +1,418 @@
-// us_attn_rows.cu -- attention over expanded rows: one CTA a query
-// row and head, its warps taking the positions in turn, with a running maximum and sum
-// each, joined at the end.
+// us_attn_rows.cu -- causal attention over expanded rows (a prompt's tokens, their keys
+// and values made from latent rows for each head), on the tensor cores (tcgen05).
+//
+//   S = Q K^T     A = Q (shared memory), B = 128 positions' keys: Dn of the head's own
+//                 and 64 that all heads share
+//   O += P V      A = P (TMEM, fp16, where S was), B = the positions' values, MN-major
+//
+// A segment is (request, head, block of 256 query rows); its positions come in tiles of
+// 128, and the tiles of all segments are spread evenly over the CTAs (one an SM).  Two
+// streams of 128 rows, each with its own scores, outputs and softmax warps: the tensor
+// cores work on one while the other's weights are made.  A stream takes the tiles that
+// its last row sees.
+//   warps 0-3, 4-7: softmax of stream 0 / 1, a thread a row
+//   warp 8: one thread issues the MMAs
+//   warp 9: one thread issues the copies (TMA, 128-byte swizzle): Q, then tile after
+//           tile in blocks of 128 rows of 64 values, into a ring of such blocks that are
+//           filled and freed one by one
+// Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set, and
+// moves when a score passes R + 14 (fp16 holds 2^14 and keeps all bits of weights down
+// to 2^-25 of the largest).  R, sums and outputs of a segment shared by several CTAs
+// are joined by a second kernel.
+#include <atomic>
+
 #include "us_attn_lat.cuh"
 #include "us_internal.h"
 #include "us_launch.cuh"
+#include "us_tcgen05.cuh"
 
 namespace {
 
-constexpr int kWarps = 4;
+using namespace us::attn;
 
-US_DEV float2 two(const uint16_t* p) { return __half22float2(*reinterpret_cast<const __half2*>(p)); }
+constexpr int kM = 128, kRows = 256, kTile = 128; // query rows of a stream, of a segment; positions of a tile
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kThreads = 320;
+constexpr float kTop = 11.f, kRoom = 14.f;        // log2 of a row's largest weight when R is set, and at most
+constexpr int kBlock = 128 * 128;                 // bytes of 128 rows of 64 values
+constexpr int kMaxSlots = 10;
 
-// KW, VW: values of a key and of a value; key(p, j), value(p, j): two values from the
-// 2j-th on; seen(p)
-template <int KW, int VW, class Key, class Value, class Seen>
-US_DEV void attend(const uint16_t* q, uint16_t* out, int positions, float scale, Key key, Value value, Seen seen) {
-    __shared__ float part[kWarps][VW + 2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float m = -INFINITY, l = 0.f, o[VW / 32] = {};
-    for (int p = warp; p < positions; p += kWarps) {
-        if (!seen(p)) continue;
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < KW / 64; ++j) {
-            const float2 a = two(q + 2 * (lane + 32 * j)), b = key(p, lane + 32 * j);
-            s = fmaf(a.x, b.x, fmaf(a.y, b.y, s));
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= scale;
-        const float t = fmaxf(m, s), f = m == -INFINITY ? 0.f : expf(m - t), w = expf(s - t);
-        l = l * f + w;
-        m = t;
-#pragma unroll
-        for (int j = 0; j < VW / 64; ++j) {
-            const float2 v = value(p, lane + 32 * j);
-            o[2 * j] = o[2 * j] * f + w * v.x;
-            o[2 * j + 1] = o[2 * j + 1] * f + w * v.y;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < VW / 64; ++j)
-        part[warp][2 * (lane + 32 * j)] = o[2 * j], part[warp][2 * (lane + 32 * j) + 1] = o[2 * j + 1];
-    if (lane == 0) part[warp][VW] = m, part[warp][VW + 1] = l;
-    __syncthreads();
-    float top = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part[w][VW]);
-    for (int w = 0; w < kWarps; ++w) sum += part[w][VW] == -INFINITY ? 0.f : part[w][VW + 1] * expf(part[w][VW] - top);
-    for (int d = threadIdx.x; d < VW; d += 32 * kWarps) {
-        float y = 0.f;
-        for (int w = 0; w < kWarps; ++w)
-            if (part[w][VW] != -INFINITY) y += part[w][d] * expf(part[w][VW] - top);
-        y = sum == 0.f ? 0.f : y / sum;
-        out[d] = us::float_to_half_bits(y != y ? y : fminf(fmaxf(y, -65504.f), 65504.f));
-    }
+struct Header {
+    uint64_t full[kMaxSlots], free[kMaxSlots];
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], pv_done[2];       // by stream
+    uint32_t tmem;
+};
+
+template <int D>                                  // Dn = Dv
+struct Shape {
+    static constexpr int kK = D / 64 + 1, kV = D / 64, kT = kK + kV;       // blocks of a tile's keys, values, both
+    static constexpr int kSlots = D == 128 ? 8 : 10;
+    static constexpr int kSmem = (2 * kK + kSlots) * kBlock + (int)sizeof(Header) + 1024;
+    static constexpr int kSlotFloats = slot_floats(kRows, D);
+    static_assert(kSmem <= 232448 && kSlots <= kMaxSlots, "shared memory");
+};
+
+struct Maps {
+    CUtensorMap q, k, r, v;
+};
+
+US_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(us::smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(us::smem_addr(bar))
+        : "memory");
 }
 
-template <int DN, int DV>
-__global__ void __launch_bounds__(32 * kWarps) attn_rows_kernel(const UsAttnRowsParams p) {
-    us::pdl_wait();
-    const int b = blockIdx.y, i = blockIdx.x / p.k.H, h = blockIdx.x % p.k.H;
-    const int row0 = p.off[b], n = p.off[b + 1] - row0, k0 = p.kv_off[b], kn = p.kv_off[b + 1] - k0;
-    const bool ok = row0 >= 0 && n >= 0 && row0 + n <= p.T && n <= p.max_n && k0 >= 0 && kn >= n && k0 + (int64_t)kn <= p.k.S;
-    if (!ok) us::set_status(p.status, US_ERR_INVALID_ARG);
-    if (ok && i < n) {
-        attend<DN + 64, DV>(
-            p.Q + (int64_t)(row0 + i) * p.ldq + (int64_t)h * (DN + 64), p.O + (int64_t)(row0 + i) * p.ldo + (int64_t)h * DV,
-            kn - n + i + 1, p.scale,
-            [&](int pos, int j) {
-                return 2 * j < DN ? two(p.k.K + (k0 + pos) * p.k.ldk + h * p.k.hsk + 2 * j)
-                                  : two(p.k.KR + (k0 + pos) * p.k.ldkr + 2 * j - DN);
-            },
-            [&](int pos, int j) { return two(p.k.V + (k0 + pos) * p.k.ldv + h * p.k.hsv + 2 * j); },
-            [](int) { return true; });
+US_DEV void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+        "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+        "r"(taddr)
+        : "memory");
+}
+
+// Tiles of the segment that stream st's rows see (none: it has no rows).
+US_DEV int stream_tiles(const Request& r, int rb, int st) {
+    const int first = rb * kRows + st * kM, end = min(r.n, first + kM);
+    return first >= r.n ? 0 : (r.ctx + end + kTile - 1) / kTile;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
+    using Sh = Shape<D>;
+    constexpr int kK = Sh::kK, kV = Sh::kV, kT = Sh::kT, kSlots = Sh::kSlots;
+    using Cur = Cursor<kRows, kTile>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((0u - us::smem_addr(smem_raw)) & 1023u);
+    uint8_t* q_sm = smem;
+    uint8_t* ring = q_sm + 2 * kK * kBlock;
+    Header& H = *reinterpret_cast<Header*>(ring + kSlots * kBlock);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) us::mbar_init(&H.full[i], 1), us::mbar_init(&H.free[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            us::mbar_init(&H.q_full[i], 1), us::mbar_init(&H.q_free[i], 1), us::mbar_init(&H.s_full[i], 1);
+            us::mbar_init(&H.p_full[i], 4), us::mbar_init(&H.pv_done[i], 1);
+        }
+        us::fence_mbar_init();
     }
+    if (warp == kLoadWarp && lane < 4)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.q + lane)) : "memory");
+    if (warp == kMmaWarp) us::tmem_alloc(&H.tmem, 512);
+    us::tc_fence_before();
+    __syncthreads();
+    us::tc_fence_after();
+    us::pdl_wait();
+
+    Work wk;
+    Cur cur;
+    const bool any = find_work<kRows, kTile>(p, wk, cur);
+    const uint32_t tmem = H.tmem;                          // S0, S1, O0, O1: 128 columns each
+    const int count = any ? (int)(wk.t1 - wk.t0) : 0;
+    bool failed = false;
+    auto wait = [&](uint64_t* bar, int use) {              // for the use-th completion of bar
+        if (!failed && !spin(bar, (uint32_t)use & 1u, p.c.status)) failed = true;
+    };
+
+    if (warp < kSoftWarps) {
+        // ----------------------------------------------------------- softmax
+        const int st = warp >> 2, row = (warp & 3) * 32 + lane;               // of the stream
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+        const uint32_t s_tm = tmem + lanes + st * 128, o_tm = tmem + lanes + 256 + st * 128;
+        // (a scale of 0 would make NaN of masked scores; this one makes 1 of every weight, too)
+        const float scale = p.scale == 0.f ? 1e-37f : p.scale * 1.4426950408889634f;
+        if (threadIdx.x == 0) p.ws_parts[blockIdx.x].rows = 0;     // until a shared segment begins here
+        int used = 0;                                      // tiles of this stream so far
+        for (int it = 0; it < count;) {
+            // ---- a segment, or this CTA's part of it: tiles it .. end - 1, of which the stream's `mine`
+            const int end = min(count, it + cur.tiles - cur.tile), tile0 = cur.tile;
+            const int rows = min(kRows, cur.r.n - cur.rb * kRows), tok = min(cur.r.n - 1, cur.rb * kRows + st * kM + row);
+            const int mine = min(end - it, max(0, stream_tiles(cur.r, cur.rb, st) - tile0));
+            const int other = st ? min(end - it, max(0, stream_tiles(cur.r, cur.rb, 0) - tile0)) : 0;
+            float R = -INFINITY;
+            uint64_t l2 = 0;
+            for (int j = 0; j < mine; ++j, ++used) {
+                const int pos0 = (tile0 + j) * kTile;
+                wait(&H.s_full[st], used);
+                us::tc_fence_after();
+                // the largest score: the scores are read twice, 32 at a time (128 at once spilled)
+                const int seen = cur.r.ctx + tok + 1 - pos0;               // positions that the row sees
+                const bool edge = __any_sync(0xffffffffu, seen < kTile);
+                const float none = scale < 0.f ? INFINITY : -INFINITY;
+                auto scores = [&](int c, float (&v)[32]) {
+                    us::tmem_ld32(s_tm + 32 * c, v);
+                    if (edge) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k >= seen) v[k] = none;
+                    }
+                };
+                float top = none;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    scores(c, v);
+                    if (scale < 0.f) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) top = fminf(top, v[k]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) top = max3(top, v[k], v[k + 1]);
+                    }
+                }
+                top *= scale;
+                const float to = top > R + kRoom ? top - kTop : R;
+                const float f = to == R ? 1.f : ex2(R - to);
+                const bool moved = to != R;
+                R = to;
+                l2 = mul2(l2, pair(f, f));
+                const float ref = to == -INFINITY ? 0.f : to;
+                const uint64_t s2 = pair(scale, scale), neg = pair(-ref, -ref);
+                if (j && __any_sync(0xffffffffu, moved)) { // the outputs so far first (its PV is done: its scores came after)
+                    wait(&H.pv_done[st], used - 1);
+                    us::tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float y[32];
+                        uint32_t o[32];
+                        us::tmem_ld32(o_tm + c, y);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(y[k] * f);
+                        tmem_st32(o_tm + c, o);
+                    }
+                    us::tmem_wait_st();
+                }
+                uint64_t sums[4] = {};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float v[32];
+                        scores(2 * half + c, v);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float x, y;
+                            unpair(fma2(pair(v[2 * k], v[2 * k + 1]), s2, neg), x, y);
+                            x = ex2(x), y = ex2(y);
+                            sums[k & 3] = add2(sums[k & 3], pair(x, y));
+                            w[16 * c + k] = pack_half2(x, y);
+                        }
+                    }
+                    tmem_st32(s_tm + 32 * half, w);            // over scores that were read
+                }
+                l2 = add2(l2, add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
+                us::tmem_wait_st();
+                // Values where no position is count as 0; the first stream that reads the tile sees to it.
+                const int there = cur.r.ctx + cur.r.n - pos0;
+                if (there < kTile && j >= other) {
+                    const int x0 = (it + j) * kT + kK;
+                    for (int c = 0; c < kV; ++c) {
+                        wait(&H.full[(x0 + c) % kSlots], (x0 + c) / kSlots);
+                        uint8_t* b = ring + (x0 + c) % kSlots * kBlock;
+                        for (int i = (threadIdx.x & 127) + there * 8; i < 128 * 8; i += 128)
+                            *reinterpret_cast<uint4*>(b + i * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    us::fence_proxy_async_smem();
+                }
+                us::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) us::mbar_arrive(&H.p_full[st]);
+            }
+            // ---- the segment's end
+            if (mine) wait(&H.pv_done[st], used - 1);
+            us::tc_fence_after();
+            const int64_t s0 = wk.t0 + it - tile0;
+            const Part part = wk.sharers(s0, s0 + cur.tiles, cur, rows);
+            const bool whole = part.first == part.last;
+            const int srow = st * kM + row;                // of the segment
+            if (st * kM + (row & ~31) < rows) {
+                float a, b;
+                unpair(l2, a, b);
+                const float sum = a + b, inv = sum == 0.f ? 0.f : 1.f / sum;
+                float* slot = p.ws_slots + part.slot(blockIdx.x) * Sh::kSlotFloats;
+                if (!whole) {
+                    __stcg(slot + srow, R);
+                    __stcg(slot + kRows + srow, sum);
+                }
+                uint16_t* out = srow < rows ? out_row<kRows>(p, cur.r.row0, cur.h, cur.rb, srow, D) : nullptr;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float y[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) y[k] = 0.f;
+                    if (mine) us::tmem_ld32(o_tm + c, y);
+                    if (!whole) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            __stcg(reinterpret_cast<float4*>(slot + 2 * kRows) + (c + k) / 4 * kRows + srow,
+                                   make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]));
+                    } else if (srow < rows) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8)
+                            *reinterpret_cast<uint4*>(out + c + k) =
+                                make_uint4(pack_out(y[k] * inv, y[k + 1] * inv), pack_out(y[k + 2] * inv, y[k + 3] * inv),
+                                           pack_out(y[k + 4] * inv, y[k + 5] * inv), pack_out(y[k + 6] * inv, y[k + 7] * inv));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!whole && part.first == (int)blockIdx.x && threadIdx.x == 0) p.ws_parts[blockIdx.x] = part;
+            it = end;
+            if (it < count) cur.next_segment(p);
+        }
+    } else if (warp == kLoadWarp) {
+        // ------------------------------------------------------------- copies
+        if (us::elect_one()) {
+            int segment[2] = {0, 0};                       // segments of each stream so far
+            for (int it = 0; it < count;) {
+                const int end = min(count, it + cur.tiles - cur.tile), k0 = p.kv_off[cur.b];
+                for (int st = 0; st < 2; ++st) {
+                    if (stream_tiles(cur.r, cur.rb, st) <= cur.tile) continue;
+                    if (segment[st]) wait(&H.q_free[st], segment[st] - 1);
+                    ++segment[st];
+                    us::mbar_arrive_expect_tx(&H.q_full[st], kK * kBlock);
+                    for (int c = 0; c < kK; ++c)
+                        tma_load_3d(q_sm + (st * kK + c) * kBlock, &maps.q, 64 * c, cur.h, cur.r.row0 + cur.rb * kRows + st * kM, &H.q_full[st]);
+                }
+                for (int i = it; i < end; ++i)
+#pragma unroll 1
+                    for (int c = 0; c < kT; ++c) {
+                        const int x = i * kT + c, slot = x % kSlots, row = k0 + (cur.tile + i - it) * kTile;
+                        if (x >= kSlots) wait(&H.free[slot], x / kSlots - 1);
+                        us::mbar_arrive_expect_tx(&H.full[slot], kBlock);
+                        uint8_t* to = ring + slot * kBlock;
+                        if (c < kK - 1) tma_load_3d(to, &maps.k, 64 * c, cur.h, row, &H.full[slot]);
+                        else if (c == kK - 1) tma_load_3d(to, &maps.r, 0, 0, row, &H.full[slot]);
+                        else tma_load_3d(to, &maps.v, 64 * (c - kK), cur.h, row, &H.full[slot]);
+                    }
+                it = end;
+                if (it < count) cur.next_segment(p);
+            }
+            // nothing of its own is left in flight when the CTA ends
+            for (int x = max(0, count * kT - kSlots); x < count * kT; ++x) wait(&H.full[x % kSlots], x / kSlots);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // --------------------------------------------------------------- MMA
+        if (us::elect_one()) {
+            int segment[2] = {0, 0}, used[2] = {0, 0};     // segments and tiles of each stream so far
+            for (int it = 0; it < count && !failed;) {
+                const int end = min(count, it + cur.tiles - cur.tile), n = end - it;
+                int mine[2];
+                for (int st = 0; st < 2; ++st) mine[st] = min(n, max(0, stream_tiles(cur.r, cur.rb, st) - cur.tile));
+                auto last_of = [&](int j) { return mine[1] > j ? 1 : 0; };         // the stream that reads tile j last
+                auto qk = [&](int st, int j) {
+                    constexpr uint32_t id = us::umma_idesc_f16(kM, kTile);
+                    if (j == 0) wait(&H.q_full[st], segment[st]++);
+                    const uint64_t qd = us::umma_smem_desc_sw128(q_sm + st * kK * kBlock);
+#pragma unroll 1
+                    for (int c = 0; c < kK; ++c) {
+                        const int x = (it + j) * kT + c, slot = x % kSlots;
+                        wait(&H.full[slot], x / kSlots);
+                        us::tc_fence_after();
+                        const uint64_t kd = us::umma_smem_desc_sw128(ring + slot * kBlock);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            us::umma_f16(tmem + st * 128, qd + (uint64_t)((c * kBlock + kk * 32) >> 4), kd + (uint64_t)(kk * 32 >> 4), id,
+                                         c > 0 || kk > 0);
+                        if (st == last_of(j)) us::umma_commit(&H.free[slot]);
+                    }
+                    us::umma_commit(&H.s_full[st]);
+                    if (j == mine[st] - 1) us::umma_commit(&H.q_free[st]);
+                };
+                auto pv = [&](int st, int j) {
+                    constexpr uint32_t id = us::umma_idesc_f16(kM, 64) | us::kUmmaBMajorMN;
+                    wait(&H.p_full[st], used[st]++);
+                    us::tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < kV; ++c) {
+                        const int x = (it + j) * kT + kK + c, slot = x % kSlots;
+                        wait(&H.full[slot], x / kSlots);
+                        us::tc_fence_after();
+                        const uint64_t vd = us::umma_smem_desc_mn_sw128(ring + slot * kBlock, kBlock);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            us::umma_f16_ta(tmem + 256 + st * 128 + 64 * c, tmem + st * 128 + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), id,
+                                            j > 0 || kk > 0);
+                        if (st == last_of(j)) us::umma_commit(&H.free[slot]);
+                    }
+                    us::umma_commit(&H.pv_done[st]);
+                };
+                // (one copy of each body)
+#pragma unroll 1
+                for (int x = -2; x < 2 * n && !failed; ++x) {
+                    const int st = x & 1, j = x >> 1;
+                    if (j >= 0 && j < mine[st]) pv(st, j);
+                    if (j + 1 < mine[st]) qk(st, j + 1);
+                }
+                it = end;
+                if (it < count) cur.next_segment(p);
+            }
+            // Arrivals that no other warp waits for: they land while the CTA still has its shared memory
+            for (int x = max(0, count * kT - kSlots); x < count * kT; ++x) wait(&H.free[x % kSlots], x / kSlots);
+            for (int st = 0; st < 2; ++st) {
+                if (used[st]) wait(&H.pv_done[st], used[st] - 1);
+                if (segment[st]) wait(&H.q_free[st], segment[st] - 1);
+            }
+        }
+        __syncwarp();
+    }
+    us::tc_fence_before();
+    __syncthreads();
+    us::tc_fence_after();
+    if (warp == kMmaWarp) us::tmem_dealloc(tmem, 512);
     us::pdl_launch_dependents();
+}
+
+// (64 values, heads, rows) of rows `ld` and heads `hs` elements apart, 128 rows of a head a copy
+bool encode_map(CUtensorMap* map, const uint16_t* x, int width, int heads, int64_t hs, int64_t rows, int64_t ld) {
+    auto enc = us::tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dim[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t stride[2] = {(cuuint64_t)hs * 2, (cuuint64_t)ld * 2};
+    const cuuint32_t box[3] = {64, 1, 128}, estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(x), dim, stride, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+us_status launch(UsAttnRowsParams p, cudaStream_t st) {
+    using Sh = Shape<D>;
+    p.ws_parts = static_cast<Part*>(p.ws);
+    p.ws_slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kPartBytes);
+    Maps maps;
+    const us_attn_kv_rows& k = p.k;
+    if (!encode_map(&maps.q, p.Q, D + us::kLatDr, k.H, D + us::kLatDr, p.a.T, p.ldq) ||
+        !encode_map(&maps.k, k.K, D, k.H, k.H > 1 ? k.hsk : D, k.S, k.ldk) ||
+        !encode_map(&maps.r, k.KR, us::kLatDr, 1, us::kLatDr, k.S, k.ldkr) ||
+        !encode_map(&maps.v, k.V, D, k.H, k.H > 1 ? k.hsv : D, k.S, k.ldv))
+        return US_ERR_CUDA;
+    auto kern = attn_rows_kernel<D>;
+    static std::atomic<bool> ready[64];                // the attribute is set once a device, by whichever thread
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return US_ERR_CUDA;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess)
+            return US_ERR_CUDA;
+        ready[dev].store(true, std::memory_order_release);
+    }
+    const us_status s = us::launch_pdl(kern, dim3((unsigned)join_ctas()), kThreads, Sh::kSmem, st, p, maps);
+    return s != US_OK ? s : launch_join<kRows, D>(p, st);
 }
 
 }  // namespace
 
 namespace us {
 
-size_t attn_rows_ws(const UsAttnRowsParams&) { return 0; }
-us_status launch_attn_rows(const UsAttnRowsParams& p, cudaStream_t st) {
-    return launch_pdl(p.k.Dn == 128 ? attn_rows_kernel<128, 128> : attn_rows_kernel<64, 64>,
-                      dim3((unsigned)(p.max_n * p.k.H), (unsigned)p.B), 32 * kWarps, 0, st, p);
-}
+size_t attn_rows_ws(const UsAttnRowsParams& p) { return attn::join_ws(kRows, p.k.Dv); }
+
+us_status launch_attn_rows(const UsAttnRowsParams& p, cudaStream_t st) { return p.k.Dv == 128 ? launch<128>(p, st) : launch<64>(p, st); }
 
 }  // namespace us

@@ -45,6 +45,9 @@ struct UsAttnParams {
     unsigned* ws_count;              // arrival counters, zero between calls
     float* ws_slots;                 // partial states
     us::attn::Part* ws_parts;        // shared segments
+
+    // positions before the tokens of request b, rows o0 .. o1 - 1
+    US_DEV int context(int b, int, int) const { return a.pos[b]; }
 };
 
 namespace us {

@@ -534,7 +534,7 @@ us_status us_attn_lat_workspace_bytes(const us_lat_cache* C, int Hq, int max_n, 
  * Q: T rows of H heads of Dn + Dr values side by side, O: of Dv; K: S rows of Dn
  * values a head, ldk elements apart, a head hsk behind the last; V the same, of Dv;
  * KR: S rows of Dr.  Distances are multiples of 8.  (Dn, Dr, Dv): (128, 64, 128) or
- * (64, 64, 64) (US_ERR_UNSUPPORTED otherwise); B and H at most 1024; S < 2^31.
+ * (64, 64, 64) (US_ERR_UNSUPPORTED otherwise); B and H at most 1024; S at most 2^30.
  * Offsets that do not ascend, leave 0..T or 0..S, give a request more than max_n
  * queries or more queries than key rows record US_ERR_INVALID_ARG and the request is
  * skipped.  Workspace: zeroed once.  Repeated calls give the same bits. */
