@@ -266,12 +266,15 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
                 }
                 // (a warp without rows must not arrive for this tile while the last one's phase is open)
                 if (wrow >= rows && i > it) wait(&H.pv_done, i - 1);
-                if (ok != ~0ull) {                         // what lies where no position is counts as 0
+                // what lies where no position is counts as 0, and what some rows do not see is made finite
+                if (ok != ~0ull || (base + kTile > 0 && cur.r.n > 1)) {
                     uint8_t* x = x_sm + st * Sh::kOperand;
-                    for (int r = 0; r < kTile; ++r)
-                        if (!((ok >> r) & 1ull))
-                            for (int k = threadIdx.x; k < DC / 8; k += 32 * kSoftWarps)
-                                *reinterpret_cast<uint4*>(x + (k >> 3) * kBlock + r * 128 + ((k & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    for (int k = threadIdx.x; k < kTile * DC / 8; k += 32 * kSoftWarps) {
+                        const int r = (k >> 3) & (kTile - 1);
+                        uint4* at = reinterpret_cast<uint4*>(x + (k >> 9) * kBlock + r * 128 + ((k & 7) << 4));
+                        if (!((ok >> r) & 1ull)) *at = make_uint4(0, 0, 0, 0);
+                        else if (base + r >= 0) scrub(at);
+                    }
                 }
                 us::fence_proxy_async_smem();
                 us::tc_fence_before();

@@ -45,6 +45,16 @@ US_DEV bool spin(uint64_t* bar, uint32_t parity, unsigned* status) {
     return false;
 }
 
+// fp16 pairs with infinities and NaN as 0.  A value that a row does not see has weight
+// 0 in it, and 0 times what is not finite would be NaN; in a row that does see it, its
+// key has made NaN of the weight.
+US_DEV uint32_t finite_pairs(uint32_t x) { return x & ~__vcmpeq2(x & 0x7C007C00u, 0x7C007C00u); }
+US_DEV void scrub(uint4* at) {
+    const uint4 x = *at;
+    const uint4 y = make_uint4(finite_pairs(x.x), finite_pairs(x.y), finite_pairs(x.z), finite_pairs(x.w));
+    if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) *at = y;
+}
+
 // A partial state of ROWS rows of D columns in the workspace: the rows' references, their
 // sums, then the outputs in fours of columns, rows side by side.
 constexpr int slot_floats(int rows, int d) { return 2 * rows + rows * d; }

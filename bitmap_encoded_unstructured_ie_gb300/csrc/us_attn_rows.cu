@@ -20,6 +20,7 @@
 // to 2^-25 of the largest).  R, sums and outputs of a segment shared by several CTAs
 // are joined by a second kernel.
 #include <atomic>
+#include <type_traits>
 
 #include "us_attn_lat.cuh"
 #include "us_internal.h"
@@ -208,15 +209,18 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                 }
                 l2 = add2(l2, add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
                 us::tmem_wait_st();
-                // Values where no position is count as 0; the first stream that reads the tile sees to it.
+                // Values where no position is count as 0, and what some rows do not see is made
+                // finite; the first stream that reads the tile sees to it.
                 const int there = cur.r.ctx + cur.r.n - pos0;
-                if (there < kTile && j >= other) {
+                if ((there < kTile || (pos0 + kTile > cur.r.ctx && cur.r.n > 1)) && j >= other) {
                     const int x0 = (it + j) * kT + kK;
                     for (int c = 0; c < kV; ++c) {
                         wait(&H.full[(x0 + c) % kSlots], (x0 + c) / kSlots);
-                        uint8_t* b = ring + (x0 + c) % kSlots * kBlock;
-                        for (int i = (threadIdx.x & 127) + there * 8; i < 128 * 8; i += 128)
-                            *reinterpret_cast<uint4*>(b + i * 16) = make_uint4(0, 0, 0, 0);
+                        uint4* b = reinterpret_cast<uint4*>(ring + (x0 + c) % kSlots * kBlock);
+                        for (int i = threadIdx.x & 127; i < 128 * 8; i += 128) {
+                            if (i >= there * 8) b[i] = make_uint4(0, 0, 0, 0);
+                            else if (pos0 + i / 8 >= cur.r.ctx) scrub(b + i);
+                        }
                     }
                     us::fence_proxy_async_smem();
                 }
@@ -304,52 +308,73 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
             int segment[2] = {0, 0}, used[2] = {0, 0};     // segments and tiles of each stream so far
             for (int it = 0; it < count && !failed;) {
                 const int end = min(count, it + cur.tiles - cur.tile), n = end - it;
-                int mine[2];
-                for (int st = 0; st < 2; ++st) mine[st] = min(n, max(0, stream_tiles(cur.r, cur.rb, st) - cur.tile));
-                auto last_of = [&](int j) { return mine[1] > j ? 1 : 0; };         // the stream that reads tile j last
-                auto qk = [&](int st, int j) {
+                const int mine0 = min(n, max(0, stream_tiles(cur.r, cur.rb, 0) - cur.tile));
+                const int mine1 = min(n, max(0, stream_tiles(cur.r, cur.rb, 1) - cur.tile));
+                // scores of tile j for stream ST, which has `mine` of them; awaited: the tile has landed
+                // for the other stream; last: nothing after them reads the tile's keys
+                auto qk = [&](auto ST, int j, int mine, bool awaited, bool last) {
+                    constexpr int st = decltype(ST)::value;
                     constexpr uint32_t id = us::umma_idesc_f16(kM, kTile);
                     if (j == 0) wait(&H.q_full[st], segment[st]++);
                     const uint64_t qd = us::umma_smem_desc_sw128(q_sm + st * kK * kBlock);
-#pragma unroll 1
+                    const int x = (it + j) * kT, use = x / kSlots, slot0 = x - use * kSlots;
+#pragma unroll
                     for (int c = 0; c < kK; ++c) {
-                        const int x = (it + j) * kT + c, slot = x % kSlots;
-                        wait(&H.full[slot], x / kSlots);
+                        const bool wraps = slot0 + c >= kSlots;
+                        const int slot = wraps ? slot0 + c - kSlots : slot0 + c;
+                        if (!awaited) wait(&H.full[slot], use + wraps);
                         us::tc_fence_after();
                         const uint64_t kd = us::umma_smem_desc_sw128(ring + slot * kBlock);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             us::umma_f16(tmem + st * 128, qd + (uint64_t)((c * kBlock + kk * 32) >> 4), kd + (uint64_t)(kk * 32 >> 4), id,
                                          c > 0 || kk > 0);
-                        if (st == last_of(j)) us::umma_commit(&H.free[slot]);
+                        if (last) us::umma_commit(&H.free[slot]);
                     }
                     us::umma_commit(&H.s_full[st]);
-                    if (j == mine[st] - 1) us::umma_commit(&H.q_free[st]);
+                    if (j == mine - 1) us::umma_commit(&H.q_free[st]);
                 };
-                auto pv = [&](int st, int j) {
-                    constexpr uint32_t id = us::umma_idesc_f16(kM, 64) | us::kUmmaBMajorMN;
+                auto pv = [&](auto ST, int j, bool awaited, bool last) {
+                    constexpr int st = decltype(ST)::value;
+                    const int x = (it + j) * kT + kK, use = x / kSlots, slot0 = x - use * kSlots;
+                    const bool wraps = kV == 2 && slot0 + 1 == kSlots;
+                    const int slot1 = wraps ? 0 : slot0 + 1;
+                    if (!awaited) {
+                        wait(&H.full[slot0], use);
+                        if (kV == 2) wait(&H.full[slot1], use + wraps);
+                    }
                     wait(&H.p_full[st], used[st]++);
                     us::tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < kV; ++c) {
-                        const int x = (it + j) * kT + kK + c, slot = x % kSlots;
-                        wait(&H.full[slot], x / kSlots);
-                        us::tc_fence_after();
-                        const uint64_t vd = us::umma_smem_desc_mn_sw128(ring + slot * kBlock, kBlock);
+                    const uint32_t o = tmem + 256 + st * 128, w = tmem + st * 128;
+                    const uint64_t vd = us::umma_smem_desc_mn_sw128(ring + slot0 * kBlock, kBlock);
+                    if (kV == 2 && !wraps) {               // both blocks of columns side by side in the ring
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            us::umma_f16_ta(tmem + 256 + st * 128 + 64 * c, tmem + st * 128 + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), id,
+                            us::umma_f16_ta(o, w + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), us::umma_idesc_f16(kM, 128) | us::kUmmaBMajorMN,
                                             j > 0 || kk > 0);
-                        if (st == last_of(j)) us::umma_commit(&H.free[slot]);
+                    } else {
+                        const uint64_t vd1 = us::umma_smem_desc_mn_sw128(ring, kBlock);
+#pragma unroll
+                        for (int c = 0; c < kV; ++c)
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                us::umma_f16_ta(o + 64 * c, w + 8 * kk, (c ? vd1 : vd) + (uint64_t)(kk * 2048 >> 4),
+                                                us::umma_idesc_f16(kM, 64) | us::kUmmaBMajorMN, j > 0 || kk > 0);
+                    }
+                    if (last) {
+                        us::umma_commit(&H.free[slot0]);
+                        if (kV == 2) us::umma_commit(&H.free[slot1]);
                     }
                     us::umma_commit(&H.pv_done[st]);
                 };
-                // (one copy of each body)
+                constexpr std::integral_constant<int, 0> S0{};
+                constexpr std::integral_constant<int, 1> S1{};
 #pragma unroll 1
-                for (int x = -2; x < 2 * n && !failed; ++x) {
-                    const int st = x & 1, j = x >> 1;
-                    if (j >= 0 && j < mine[st]) pv(st, j);
-                    if (j + 1 < mine[st]) qk(st, j + 1);
+                for (int j = -1; j < n && !failed; ++j) {
+                    if (j >= 0 && j < mine0) pv(S0, j, false, j >= mine1);
+                    if (j + 1 < mine0) qk(S0, j + 1, mine0, false, j + 1 >= mine1);
+                    if (j >= 0 && j < mine1) pv(S1, j, j < mine0, true);
+                    if (j + 1 < mine1) qk(S1, j + 1, mine1, j + 1 < mine0, true);
                 }
                 it = end;
                 if (it < count) cur.next_segment(p);

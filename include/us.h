@@ -511,8 +511,9 @@ us_status us_lat_commit(const us_lat_cache* C, int T, const int32_t* acc_off, co
  * with row_p the entry's Dc + Dr values and c_p its first Dc; at most 65504 in
  * magnitude, 0 for a row that sees no position.  Scores, sums and outputs are
  * accumulated in fp32; a weight enters its product as fp16, rounded once.  Entries of
- * positions that are read are finite (us_lat_write stores no others); what lies
- * behind a request's last position is not looked at.
+ * the call's tokens that a row does not see, and what lies behind a request's last
+ * position, may hold anything; those that every row sees (us_lat_write stores finite
+ * ones) make NaN of the rows if they are not finite.
  * Q: T rows of Hq heads of Dc + Dr values, O: of Dc.  mask, max_n, errors and the
  * workspace (zeroed once) as in us_attn_kv; Hq <= 1024.  Repeated calls give the same
  * bits. */
@@ -529,8 +530,8 @@ us_status us_attn_lat_workspace_bytes(const us_lat_cache* C, int Hq, int max_n, 
  *   O[t][h] = fp16(sum_p w_p V[p][h] / sum_p w_p)
  *   w_p = exp(scale * (Q[t][h][:Dn] . K[p][h] + Q[t][h][Dn:] . KR[p]))
  * at most 65504 in magnitude; accumulation and weights as in us_attn_lat.
- * Key rows that a query does not see have no part in its output, whatever they hold
- * as long as it is finite; rows outside kv_off[b] .. are not looked at.
+ * Key rows that a query does not see have no part in its output, whatever they hold;
+ * rows outside kv_off[b] .. are not looked at.
  * Q: T rows of H heads of Dn + Dr values side by side, O: of Dv; K: S rows of Dn
  * values a head, ldk elements apart, a head hsk behind the last; V the same, of Dv;
  * KR: S rows of Dr.  Distances are multiples of 8.  (Dn, Dr, Dv): (128, 64, 128) or
