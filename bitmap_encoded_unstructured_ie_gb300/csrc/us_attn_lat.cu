@@ -18,8 +18,8 @@
 //   warp 5: one thread issues the MMAs, whichever of the next tile's scores (its rows
 //           have landed) and the last one's outputs (its weights are there) can go
 // Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set, and
-// moves when a score passes R + 14 (fp16 holds 2^14 and keeps all bits of weights down
-// to 2^-25 of the largest).  R, sums and outputs of a segment shared by several CTAs
+// moves when a score passes R + 15.9 (fp16 holds 2^15.9 and keeps all bits of weights
+// down to 2^-25 of the largest).  R, sums and outputs of a segment shared by several CTAs
 // are joined by a second kernel.
 #include <atomic>
 
@@ -34,7 +34,7 @@ using namespace us::attn;
 
 constexpr int kM = 64, kTile = 64;                // query rows of a segment, positions of a tile
 constexpr int kSoftWarps = 4, kLoadWarp = 4, kMmaWarp = 5, kThreads = 192;
-constexpr float kTop = 11.f, kRoom = 14.f;        // log2 of a row's largest weight when R is set, and at most
+constexpr float kTop = 11.f, kRoom = 15.9f;        // log2 of a row's largest weight when R is set, and at most
 constexpr int kBlock = 64 * 128;                  // bytes of 64 rows of 64 values
 constexpr int kMaxStages = 4;
 
@@ -266,14 +266,26 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
                 }
                 // (a warp without rows must not arrive for this tile while the last one's phase is open)
                 if (wrow >= rows && i > it) wait(&H.pv_done, i - 1);
-                // what lies where no position is counts as 0, and what some rows do not see is made finite
-                if (ok != ~0ull || (base + kTile > 0 && cur.r.n > 1)) {
+                // What lies where no position is counts as 0, and what some rows do not see is made
+                // finite (drafts, or in a chain what is behind the segment's first token).
+                const int all_see = (p.mask ? (cur.r.n > 1 ? 0 : 1) : cur.rb * kM / G + 1) - base;
+                if (ok != ~0ull || all_see < kTile) {
                     uint8_t* x = x_sm + st * Sh::kOperand;
-                    for (int k = threadIdx.x; k < kTile * DC / 8; k += 32 * kSoftWarps) {
-                        const int r = (k >> 3) & (kTile - 1);
-                        uint4* at = reinterpret_cast<uint4*>(x + (k >> 9) * kBlock + r * 128 + ((k & 7) << 4));
-                        if (!((ok >> r) & 1ull)) *at = make_uint4(0, 0, 0, 0);
-                        else if (base + r >= 0) scrub(at);
+#pragma unroll 1
+                    for (int k0 = threadIdx.x; k0 < kTile * DC / 8; k0 += 8 * 32 * kSoftWarps) {
+                        uint4 y[8];
+                        auto at = [&](int i) {
+                            const int k = k0 + i * 32 * kSoftWarps;
+                            return reinterpret_cast<uint4*>(x + (k >> 9) * kBlock + ((k >> 3) & (kTile - 1)) * 128 + ((k & 7) << 4));
+                        };
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = *at(i);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = ((k0 + i * 32 * kSoftWarps) >> 3) & (kTile - 1);
+                            if (!((ok >> r) & 1ull)) *at(i) = make_uint4(0, 0, 0, 0);
+                            else if (r >= all_see && !all_finite(y[i])) *at(i) = finite(y[i]);
+                        }
                     }
                 }
                 us::fence_proxy_async_smem();
@@ -498,9 +510,9 @@ us_status launch(UsAttnLatParams p, cudaStream_t st) {
             return US_ERR_CUDA;
         ready[dev].store(true, std::memory_order_release);
     }
-    us_status s = us::launch_pdl(kern, dim3((unsigned)us::attn::join_ctas()), kThreads, Sh::kSmem, st, p, map);
+    us_status s = us::launch_pdl(kern, dim3((unsigned)us::attn::attn_ctas()), kThreads, Sh::kSmem, st, p, map);
     if (s != US_OK) return s;
-    return us::attn::launch_join<kM, DC>(p, st);
+    return us::attn::launch_join<kM, DC>(p, us::attn::attn_ctas(), st);
 }
 
 }  // namespace
@@ -508,7 +520,7 @@ us_status launch(UsAttnLatParams p, cudaStream_t st) {
 namespace us {
 
 size_t attn_lat_ws(const UsAttnLatParams& p) {
-    return us::attn::join_ws(kM, p.Dc);
+    return us::attn::join_ws(attn::attn_ctas(), kM, p.Dc);
 }
 
 us_status launch_attn_lat(const UsAttnLatParams& p, cudaStream_t st) { return p.Dc == 512 ? launch<512>(p, st) : launch<256>(p, st); }

@@ -48,11 +48,10 @@ US_DEV bool spin(uint64_t* bar, uint32_t parity, unsigned* status) {
 // fp16 pairs with infinities and NaN as 0.  A value that a row does not see has weight
 // 0 in it, and 0 times what is not finite would be NaN; in a row that does see it, its
 // key has made NaN of the weight.
-US_DEV uint32_t finite_pairs(uint32_t x) { return x & ~__vcmpeq2(x & 0x7C007C00u, 0x7C007C00u); }
-US_DEV void scrub(uint4* at) {
-    const uint4 x = *at;
-    const uint4 y = make_uint4(finite_pairs(x.x), finite_pairs(x.y), finite_pairs(x.z), finite_pairs(x.w));
-    if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) *at = y;
+US_DEV uint32_t not_finite(uint32_t x) { return __vcmpeq2(x & 0x7C007C00u, 0x7C007C00u); }
+US_DEV bool all_finite(uint4 x) { return (not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w)) == 0; }
+US_DEV uint4 finite(uint4 x) {
+    return make_uint4(x.x & ~not_finite(x.x), x.y & ~not_finite(x.y), x.z & ~not_finite(x.z), x.w & ~not_finite(x.w));
 }
 
 // A partial state of ROWS rows of D columns in the workspace: the rows' references, their
@@ -92,7 +91,13 @@ join_kernel(const P p, int blocks, int ctas) {
             return;
         }
     }
-    const Part a = p.ws_parts[which];
+    Part a = p.ws_parts[which];
+    // (a workspace that two calls share at once may hold anything: nothing outside it and O is touched)
+    if (a.rows > 0 && (a.first < 0 || a.last >= ctas || a.rows > ROWS || a.h < 0 || a.h >= p.c.Hkv || a.row0 < 0 || a.rb < 0 ||
+                       (int64_t)a.row0 + ((int64_t)a.rb * ROWS + a.rows - 1) / p.G >= p.a.T)) {
+        us::set_status(p.c.status, US_ERR_CORRUPT);
+        a.rows = 0;
+    }
     const int group = threadIdx.x / kLanes, t = threadIdx.x % kLanes;
     const int row = (int)blockIdx.x % blocks * 16 + (t & 15), col = ((int)blockIdx.y * (kLanes / 16 * kVec) + (t >> 4)) * 4;
     if (row - (t & 15) < a.rows) {                         // (uniform; 0 rows: no shared segment)
@@ -161,13 +166,13 @@ join_kernel(const P p, int blocks, int ctas) {
     us::pdl_launch_dependents();
 }
 
-inline int join_ctas() { return us::num_sms() < kMaxCtas ? us::num_sms() : kMaxCtas; }
-inline size_t join_ws(int rows, int d) { return kPartBytes + (size_t)2 * join_ctas() * slot_floats(rows, d) * 4; }
+inline int attn_ctas() { return us::num_sms() < kMaxCtas ? us::num_sms() : kMaxCtas; }
+inline size_t join_ws(int ctas, int rows, int d) { return kPartBytes + (size_t)2 * ctas * slot_floats(rows, d) * 4; }
 
 template <int ROWS, int D, class P>
-us_status launch_join(const P& p, cudaStream_t st) {
+us_status launch_join(const P& p, int ctas, cudaStream_t st) {
     const int64_t rows = (int64_t)p.a.max_n * p.G, segments = (rows + ROWS - 1) / ROWS * p.c.Hkv * p.c.B;      // at most
-    const int blocks = rows < ROWS ? ((int)rows + 15) / 16 : ROWS / 16, ctas = join_ctas();
+    const int blocks = rows < ROWS ? ((int)rows + 15) / 16 : ROWS / 16;
     if (8 * segments <= ctas)
         return us::launch_pdl(join_kernel<ROWS, D, 8, P>, dim3((unsigned)(segments * blocks), D / 8), kJoinThreads, 0, st, p, blocks, ctas);
     return us::launch_pdl(join_kernel<ROWS, D, 1, P>, dim3((unsigned)(ctas * blocks), D < 256 ? 1 : D / 256), kJoinThreads, 0, st, p, blocks, ctas);

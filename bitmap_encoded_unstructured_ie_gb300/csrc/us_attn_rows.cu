@@ -13,12 +13,12 @@
 //   warps 0-3, 4-7: softmax of stream 0 / 1, a thread a row
 //   warp 8: one thread issues the MMAs
 //   warp 9: one thread issues the copies (TMA, 128-byte swizzle): Q, then tile after
-//           tile in blocks of 128 rows of 64 values, into a ring of such blocks that are
-//           filled and freed one by one
+//           tile, its keys and its values as an item each, in blocks of 128 rows of 64
+//           values, into a ring of such blocks
 // Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set, and
-// moves when a score passes R + 14 (fp16 holds 2^14 and keeps all bits of weights down
-// to 2^-25 of the largest).  R, sums and outputs of a segment shared by several CTAs
-// are joined by a second kernel.
+// moves when a score passes R + 15.9 (fp16 holds 2^15.9 and keeps all bits of weights
+// down to 2^-25 of the largest).  R, sums and outputs of a segment shared by several
+// CTAs are joined by a second kernel.
 #include <atomic>
 #include <type_traits>
 
@@ -33,12 +33,12 @@ using namespace us::attn;
 
 constexpr int kM = 128, kRows = 256, kTile = 128; // query rows of a stream, of a segment; positions of a tile
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kThreads = 320;
-constexpr float kTop = 11.f, kRoom = 14.f;        // log2 of a row's largest weight when R is set, and at most
+constexpr float kTop = 11.f, kRoom = 15.9f;        // log2 of a row's largest weight when R is set, and at most
 constexpr int kBlock = 128 * 128;                 // bytes of 128 rows of 64 values
-constexpr int kMaxSlots = 10;
+constexpr int kItems = 4;                         // keys, and values, of tiles that have a barrier each
 
 struct Header {
-    uint64_t full[kMaxSlots], free[kMaxSlots];
+    uint64_t k_full[kItems], v_full[kItems], k_free[kItems], v_free[kItems];
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2], pv_done[2];       // by stream
     uint32_t tmem;
 };
@@ -46,10 +46,11 @@ struct Header {
 template <int D>                                  // Dn = Dv
 struct Shape {
     static constexpr int kK = D / 64 + 1, kV = D / 64, kT = kK + kV;       // blocks of a tile's keys, values, both
-    static constexpr int kSlots = D == 128 ? 8 : 10;
+    static constexpr int kSlots = D == 128 ? 8 : 9;                        // blocks of the ring
+    static_assert((kSlots + kT - 1) / kT + 1 <= kItems, "tiles that have blocks in the ring");
     static constexpr int kSmem = (2 * kK + kSlots) * kBlock + (int)sizeof(Header) + 1024;
     static constexpr int kSlotFloats = slot_floats(kRows, D);
-    static_assert(kSmem <= 232448 && kSlots <= kMaxSlots, "shared memory");
+    static_assert(kSmem <= 232448, "shared memory");
 };
 
 struct Maps {
@@ -64,17 +65,25 @@ US_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, 
         : "memory");
 }
 
-US_DEV void tmem_st32(uint32_t taddr, const uint32_t* r) {
+US_DEV void tmem_ld32_begin(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-        "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
-        "r"(taddr)
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
         : "memory");
 }
-
+US_DEV void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
+        "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+        : "memory");
+}
 // Tiles of the segment that stream st's rows see (none: it has no rows).
 US_DEV int stream_tiles(const Request& r, int rb, int st) {
     const int first = rb * kRows + st * kM, end = min(r.n, first + kM);
@@ -95,7 +104,8 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) us::mbar_init(&H.full[i], 1), us::mbar_init(&H.free[i], 1);
+        for (int i = 0; i < kItems; ++i)
+            us::mbar_init(&H.k_full[i], 1), us::mbar_init(&H.v_full[i], 1), us::mbar_init(&H.k_free[i], 1), us::mbar_init(&H.v_free[i], 1);
         for (int i = 0; i < 2; ++i) {
             us::mbar_init(&H.q_full[i], 1), us::mbar_init(&H.q_free[i], 1), us::mbar_init(&H.s_full[i], 1);
             us::mbar_init(&H.p_full[i], 4), us::mbar_init(&H.pv_done[i], 1);
@@ -127,6 +137,8 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
         const uint32_t s_tm = tmem + lanes + st * 128, o_tm = tmem + lanes + 256 + st * 128;
         // (a scale of 0 would make NaN of masked scores; this one makes 1 of every weight, too)
         const float scale = p.scale == 0.f ? 1e-37f : p.scale * 1.4426950408889634f;
+        const float none = scale < 0.f ? INFINITY : -INFINITY;         // an unseen score: -inf when scaled
+        const uint64_t s2 = pair(scale, scale);
         if (threadIdx.x == 0) p.ws_parts[blockIdx.x].rows = 0;     // until a shared segment begins here
         int used = 0;                                      // tiles of this stream so far
         for (int it = 0; it < count;) {
@@ -141,85 +153,104 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                 const int pos0 = (tile0 + j) * kTile;
                 wait(&H.s_full[st], used);
                 us::tc_fence_after();
-                // the largest score: the scores are read twice, 32 at a time (128 at once spilled)
-                const int seen = cur.r.ctx + tok + 1 - pos0;               // positions that the row sees
+                // The scores are read twice, 32 at a time, the next ones on their way while these are
+                // used; the loops are kept short, so that the code of all roles stays near.
+                const int seen = cur.r.ctx + tok + 1 - pos0;       // positions that the row sees
                 const bool edge = __any_sync(0xffffffffu, seen < kTile);
-                const float none = scale < 0.f ? INFINITY : -INFINITY;
-                auto scores = [&](int c, float (&v)[32]) {
-                    us::tmem_ld32(s_tm + 32 * c, v);
+                uint32_t r0[32], r1[32];
+                auto finish = [&](int c, uint32_t (&r)[32], float (&v)[32]) {
+                    us::tmem_ld_frag32_end(r, v);
                     if (edge) {
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            if (32 * c + k >= seen) v[k] = none;
+                            if (c + k >= seen) v[k] = none;
                     }
                 };
-                float top = none;
+                float top = -INFINITY;
+                auto largest = [&](const float (&v)[32]) {
+                    float t[2] = {top, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    scores(c, v);
-                    if (scale < 0.f) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) top = fminf(top, v[k]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) top = max3(top, v[k], v[k + 1]);
+                    for (int k = 0; k < 16; ++k) {
+                        float x, y;
+                        unpair(mul2(pair(v[2 * k], v[2 * k + 1]), s2), x, y);
+                        t[k & 1] = max3(t[k & 1], x, y);
                     }
+                    top = fmaxf(t[0], t[1]);
+                };
+                tmem_ld32_begin(s_tm, r0);
+#pragma unroll 1
+                for (int c = 0; c < kTile; c += 64) {
+                    float v[32];
+                    finish(c, r0, v);
+                    tmem_ld32_begin(s_tm + c + 32, r1);
+                    largest(v);
+                    finish(c + 32, r1, v);
+                    tmem_ld32_begin(s_tm + (c ? 0 : 64), r0);      // (at the end: the first ones again)
+                    largest(v);
                 }
-                top *= scale;
                 const float to = top > R + kRoom ? top - kTop : R;
                 const float f = to == R ? 1.f : ex2(R - to);
                 const bool moved = to != R;
                 R = to;
                 l2 = mul2(l2, pair(f, f));
                 const float ref = to == -INFINITY ? 0.f : to;
-                const uint64_t s2 = pair(scale, scale), neg = pair(-ref, -ref);
-                if (j && __any_sync(0xffffffffu, moved)) { // the outputs so far first (its PV is done: its scores came after)
+                const uint64_t neg = pair(-ref, -ref);
+                if (j && __any_sync(0xffffffffu, moved)) { // the outputs so far first (their product is done: these scores came after)
                     wait(&H.pv_done[st], used - 1);
                     us::tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float y[32];
-                        uint32_t o[32];
-                        us::tmem_ld32(o_tm + c, y);
+                    for (int c = 0; c < D; c += 16) {
+                        float y[16];
+                        uint32_t o[16];
+                        us::tmem_ld16(o_tm + c, y);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(y[k] * f);
-                        tmem_st32(o_tm + c, o);
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(y[k] * f);
+                        tmem_st16(o_tm + c, o);
                     }
-                    us::tmem_wait_st();
                 }
-                uint64_t sums[4] = {};
+                uint64_t sums[2] = {};
+                auto weigh = [&](int c, const float (&v)[32]) {
+                    uint32_t w[16];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float v[32];
-                        scores(2 * half + c, v);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            float x, y;
-                            unpair(fma2(pair(v[2 * k], v[2 * k + 1]), s2, neg), x, y);
-                            x = ex2(x), y = ex2(y);
-                            sums[k & 3] = add2(sums[k & 3], pair(x, y));
-                            w[16 * c + k] = pack_half2(x, y);
-                        }
+                    for (int k = 0; k < 16; ++k) {
+                        float x, y;
+                        unpair(fma2(pair(v[2 * k], v[2 * k + 1]), s2, neg), x, y);
+                        x = ex2(x), y = ex2(y);
+                        sums[k & 1] = add2(sums[k & 1], pair(x, y));
+                        w[k] = pack_half2(x, y);
                     }
-                    tmem_st32(s_tm + 32 * half, w);            // over scores that were read
+                    tmem_st16(s_tm + c / 2, w);            // over scores that were read
+                };
+#pragma unroll 1
+                for (int c = 0; c < kTile; c += 64) {
+                    float v[32];
+                    finish(c, r0, v);
+                    tmem_ld32_begin(s_tm + c + 32, r1);
+                    weigh(c, v);
+                    finish(c + 32, r1, v);
+                    if (c == 0) tmem_ld32_begin(s_tm + 64, r0);
+                    weigh(c + 32, v);
                 }
-                l2 = add2(l2, add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
+                l2 = add2(l2, add2(sums[0], sums[1]));
                 us::tmem_wait_st();
-                // Values where no position is count as 0, and what some rows do not see is made
-                // finite; the first stream that reads the tile sees to it.
-                const int there = cur.r.ctx + cur.r.n - pos0;
-                if ((there < kTile || (pos0 + kTile > cur.r.ctx && cur.r.n > 1)) && j >= other) {
-                    const int x0 = (it + j) * kT + kK;
+                // Values where no position is count as 0, and what some rows do not see (positions
+                // behind the segment's first one) is made finite; the first stream that reads the
+                // tile sees to it.
+                const int there = cur.r.ctx + cur.r.n - pos0, all_see = cur.r.ctx + cur.rb * kRows + 1 - pos0;
+                if ((there < kTile || all_see < kTile) && j >= other) {
+                    const int x = it + j;
+                    wait(&H.v_full[x % kItems], x / kItems);
+#pragma unroll 1
                     for (int c = 0; c < kV; ++c) {
-                        wait(&H.full[(x0 + c) % kSlots], (x0 + c) / kSlots);
-                        uint4* b = reinterpret_cast<uint4*>(ring + (x0 + c) % kSlots * kBlock);
-                        for (int i = threadIdx.x & 127; i < 128 * 8; i += 128) {
-                            if (i >= there * 8) b[i] = make_uint4(0, 0, 0, 0);
-                            else if (pos0 + i / 8 >= cur.r.ctx) scrub(b + i);
+                        uint4* b = reinterpret_cast<uint4*>(ring + (x * kT + kK + c) % kSlots * kBlock) + (threadIdx.x & 127);
+                        uint4 y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = b[128 * i];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int at = (threadIdx.x & 127) / 8 + 16 * i;           // the position
+                            if (at >= there) b[128 * i] = make_uint4(0, 0, 0, 0);
+                            else if (at >= all_see && !all_finite(y[i])) b[128 * i] = finite(y[i]);
                         }
                     }
                     us::fence_proxy_async_smem();
@@ -284,22 +315,35 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                     for (int c = 0; c < kK; ++c)
                         tma_load_3d(q_sm + (st * kK + c) * kBlock, &maps.q, 64 * c, cur.h, cur.r.row0 + cur.rb * kRows + st * kM, &H.q_full[st]);
                 }
-                for (int i = it; i < end; ++i)
+                for (int i = it; i < end; ++i) {
+                    const int row = k0 + (cur.tile + i - it) * kTile, item = i % kItems;
+                    // block c of the tile, when the one whose place it takes is free
+                    auto place = [&](int c) {
+                        const int x = i * kT + c, old = x - kSlots, t = old / kT;
+                        if (old >= 0) wait(old - t * kT < kK ? &H.k_free[t % kItems] : &H.v_free[t % kItems], t / kItems);
+                        return ring + x % kSlots * kBlock;
+                    };
+                    uint64_t* bar = &H.k_full[item];
 #pragma unroll 1
-                    for (int c = 0; c < kT; ++c) {
-                        const int x = i * kT + c, slot = x % kSlots, row = k0 + (cur.tile + i - it) * kTile;
-                        if (x >= kSlots) wait(&H.free[slot], x / kSlots - 1);
-                        us::mbar_arrive_expect_tx(&H.full[slot], kBlock);
-                        uint8_t* to = ring + slot * kBlock;
-                        if (c < kK - 1) tma_load_3d(to, &maps.k, 64 * c, cur.h, row, &H.full[slot]);
-                        else if (c == kK - 1) tma_load_3d(to, &maps.r, 0, 0, row, &H.full[slot]);
-                        else tma_load_3d(to, &maps.v, 64 * (c - kK), cur.h, row, &H.full[slot]);
+                    for (int c = 0; c < kK; ++c) {
+                        uint8_t* to = place(c);
+                        if (c == 0) us::mbar_arrive_expect_tx(bar, kK * kBlock);
+                        if (c < kK - 1) tma_load_3d(to, &maps.k, 64 * c, cur.h, row, bar);
+                        else tma_load_3d(to, &maps.r, 0, 0, row, bar);
                     }
+                    bar = &H.v_full[item];
+#pragma unroll 1
+                    for (int c = 0; c < kV; ++c) {
+                        uint8_t* to = place(kK + c);
+                        if (c == 0) us::mbar_arrive_expect_tx(bar, kV * kBlock);
+                        tma_load_3d(to, &maps.v, 64 * c, cur.h, row, bar);
+                    }
+                }
                 it = end;
                 if (it < count) cur.next_segment(p);
             }
             // nothing of its own is left in flight when the CTA ends
-            for (int x = max(0, count * kT - kSlots); x < count * kT; ++x) wait(&H.full[x % kSlots], x / kSlots);
+            for (int i = max(0, count - kItems); i < count; ++i) wait(&H.k_full[i % kItems], i / kItems), wait(&H.v_full[i % kItems], i / kItems);
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -310,77 +354,68 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                 const int end = min(count, it + cur.tiles - cur.tile), n = end - it;
                 const int mine0 = min(n, max(0, stream_tiles(cur.r, cur.rb, 0) - cur.tile));
                 const int mine1 = min(n, max(0, stream_tiles(cur.r, cur.rb, 1) - cur.tile));
-                // scores of tile j for stream ST, which has `mine` of them; awaited: the tile has landed
-                // for the other stream; last: nothing after them reads the tile's keys
-                auto qk = [&](auto ST, int j, int mine, bool awaited, bool last) {
+                // Scores of tile j for stream ST, which has `mine` of them; first: nothing has waited for the
+                // tile yet; last: nothing after them reads its keys.  (A wait for what is there takes some
+                // 150 cycles beside the softmax: there are no more of them than have to be.)
+                auto qk = [&](auto ST, int j, int mine, bool first, bool last) {
                     constexpr int st = decltype(ST)::value;
                     constexpr uint32_t id = us::umma_idesc_f16(kM, kTile);
+                    const int x = it + j, item = x % kItems;
                     if (j == 0) wait(&H.q_full[st], segment[st]++);
+                    if (first) wait(&H.k_full[item], x / kItems);
+                    us::tc_fence_after();
                     const uint64_t qd = us::umma_smem_desc_sw128(q_sm + st * kK * kBlock);
-                    const int x = (it + j) * kT, use = x / kSlots, slot0 = x - use * kSlots;
 #pragma unroll
                     for (int c = 0; c < kK; ++c) {
-                        const bool wraps = slot0 + c >= kSlots;
-                        const int slot = wraps ? slot0 + c - kSlots : slot0 + c;
-                        if (!awaited) wait(&H.full[slot], use + wraps);
-                        us::tc_fence_after();
-                        const uint64_t kd = us::umma_smem_desc_sw128(ring + slot * kBlock);
+                        const uint64_t kd = us::umma_smem_desc_sw128(ring + (x * kT + c) % kSlots * kBlock);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             us::umma_f16(tmem + st * 128, qd + (uint64_t)((c * kBlock + kk * 32) >> 4), kd + (uint64_t)(kk * 32 >> 4), id,
                                          c > 0 || kk > 0);
-                        if (last) us::umma_commit(&H.free[slot]);
                     }
                     us::umma_commit(&H.s_full[st]);
+                    if (last) us::umma_commit(&H.k_free[item]);
                     if (j == mine - 1) us::umma_commit(&H.q_free[st]);
                 };
-                auto pv = [&](auto ST, int j, bool awaited, bool last) {
+                auto pv = [&](auto ST, int j, bool first, bool last) {
                     constexpr int st = decltype(ST)::value;
-                    const int x = (it + j) * kT + kK, use = x / kSlots, slot0 = x - use * kSlots;
-                    const bool wraps = kV == 2 && slot0 + 1 == kSlots;
-                    const int slot1 = wraps ? 0 : slot0 + 1;
-                    if (!awaited) {
-                        wait(&H.full[slot0], use);
-                        if (kV == 2) wait(&H.full[slot1], use + wraps);
-                    }
+                    const int x = it + j, item = x % kItems;
+                    if (first) wait(&H.v_full[item], x / kItems);
                     wait(&H.p_full[st], used[st]++);
                     us::tc_fence_after();
                     const uint32_t o = tmem + 256 + st * 128, w = tmem + st * 128;
-                    const uint64_t vd = us::umma_smem_desc_mn_sw128(ring + slot0 * kBlock, kBlock);
-                    if (kV == 2 && !wraps) {               // both blocks of columns side by side in the ring
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            us::umma_f16_ta(o, w + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), us::umma_idesc_f16(kM, 128) | us::kUmmaBMajorMN,
-                                            j > 0 || kk > 0);
-                    } else {
-                        const uint64_t vd1 = us::umma_smem_desc_mn_sw128(ring, kBlock);
+                    const int v0 = (x * kT + kK) % kSlots;
+                    const uint64_t rd = us::umma_smem_desc_mn_sw128(ring, kBlock), vd = rd + (uint64_t)(v0 * (kBlock >> 4));
+                    if (kV == 1 || v0 + 1 == kSlots) {     // one block of columns, or two that the ring's end parts
 #pragma unroll
                         for (int c = 0; c < kV; ++c)
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
-                                us::umma_f16_ta(o + 64 * c, w + 8 * kk, (c ? vd1 : vd) + (uint64_t)(kk * 2048 >> 4),
+                                us::umma_f16_ta(o + 64 * c, w + 8 * kk, (c ? rd : vd) + (uint64_t)(kk * 2048 >> 4),
                                                 us::umma_idesc_f16(kM, 64) | us::kUmmaBMajorMN, j > 0 || kk > 0);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            us::umma_f16_ta(o, w + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), us::umma_idesc_f16(kM, 64 * kV) | us::kUmmaBMajorMN,
+                                            j > 0 || kk > 0);
                     }
-                    if (last) {
-                        us::umma_commit(&H.free[slot0]);
-                        if (kV == 2) us::umma_commit(&H.free[slot1]);
-                    }
+                    if (last) us::umma_commit(&H.v_free[item]);
                     us::umma_commit(&H.pv_done[st]);
                 };
                 constexpr std::integral_constant<int, 0> S0{};
                 constexpr std::integral_constant<int, 1> S1{};
 #pragma unroll 1
                 for (int j = -1; j < n && !failed; ++j) {
-                    if (j >= 0 && j < mine0) pv(S0, j, false, j >= mine1);
-                    if (j + 1 < mine0) qk(S0, j + 1, mine0, false, j + 1 >= mine1);
-                    if (j >= 0 && j < mine1) pv(S1, j, j < mine0, true);
-                    if (j + 1 < mine1) qk(S1, j + 1, mine1, j + 1 < mine0, true);
+                    if (j >= 0 && j < mine0) pv(S0, j, true, j >= mine1);
+                    if (j + 1 < mine0) qk(S0, j + 1, mine0, true, j + 1 >= mine1);
+                    if (j >= 0 && j < mine1) pv(S1, j, j >= mine0, true);
+                    if (j + 1 < mine1) qk(S1, j + 1, mine1, j + 1 >= mine0, true);
                 }
                 it = end;
                 if (it < count) cur.next_segment(p);
             }
             // Arrivals that no other warp waits for: they land while the CTA still has its shared memory
-            for (int x = max(0, count * kT - kSlots); x < count * kT; ++x) wait(&H.free[x % kSlots], x / kSlots);
+            for (int i = max(0, count - kItems); i < count; ++i) wait(&H.k_free[i % kItems], i / kItems), wait(&H.v_free[i % kItems], i / kItems);
             for (int st = 0; st < 2; ++st) {
                 if (used[st]) wait(&H.pv_done[st], used[st] - 1);
                 if (segment[st]) wait(&H.q_free[st], segment[st] - 1);
@@ -428,15 +463,15 @@ us_status launch(UsAttnRowsParams p, cudaStream_t st) {
             return US_ERR_CUDA;
         ready[dev].store(true, std::memory_order_release);
     }
-    const us_status s = us::launch_pdl(kern, dim3((unsigned)join_ctas()), kThreads, Sh::kSmem, st, p, maps);
-    return s != US_OK ? s : launch_join<kRows, D>(p, st);
+    const us_status s = us::launch_pdl(kern, dim3((unsigned)attn_ctas()), kThreads, Sh::kSmem, st, p, maps);
+    return s != US_OK ? s : launch_join<kRows, D>(p, attn_ctas(), st);
 }
 
 }  // namespace
 
 namespace us {
 
-size_t attn_rows_ws(const UsAttnRowsParams& p) { return attn::join_ws(kRows, p.k.Dv); }
+size_t attn_rows_ws(const UsAttnRowsParams& p) { return attn::join_ws(attn::attn_ctas(), kRows, p.k.Dv); }
 
 us_status launch_attn_rows(const UsAttnRowsParams& p, cudaStream_t st) { return p.k.Dv == 128 ? launch<128>(p, st) : launch<64>(p, st); }
 

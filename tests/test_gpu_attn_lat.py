@@ -278,15 +278,15 @@ def test_another_stream_and_two_graphs(us):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             call()
-        out.append((g, o, want, side))
+        out.append((g, o, want, side, call))                   # (the call's tensors live as long as the graph)
     for _ in range(3):
-        for g, o, want, side in out:
+        for g, o, want, side, _ in out:
             o.zero_()
         torch.cuda.synchronize()
-        for g, o, want, side in out:
+        for g, o, want, side, _ in out:
             with torch.cuda.stream(side):
                 g.replay()
         torch.cuda.synchronize()
-        for g, o, want, side in out:
+        for g, o, want, side, _ in out:
             assert np.array_equal(o.cpu().numpy(), want)
     assert us.us_get_last_device_status() == us.US_OK
