@@ -33,7 +33,7 @@ US_DEV uint2 pack_codes(const float (&v)[8]) {
     }
 }
 
-// Quantises one row held eight values a lane by D/8 neighbouring lanes (all
+// Quantises one row held N times eight values a lane by D / (8 N) neighbouring lanes (all
 // 32 lanes of the warp take part); returns the scale.
 //
 // rint(x / s) without a division: q = x (1/s), corrected once by its exact
@@ -42,45 +42,70 @@ US_DEV uint2 pack_codes(const float (&v)[8]) {
 // least 2^-20 of itself away from one, where an error of 2^-22 does not matter.
 // Rows with infinities, NaN or a subnormal scale (whose codes may need the clamp)
 // take the plain way.
-template <int ELEM, int D>
-US_DEV uint16_t quantise_row(uint4 in, uint2& codes) {
+template <int ELEM, int D, int N>
+US_DEV uint16_t quantise_row(const uint4 (&in)[N], uint2 (&codes)[N]) {
     constexpr float q = ELEM == US_I8 ? 127.f : 7.f, kRound = 12582912.f;
-    const uint32_t u[4] = {in.x, in.y, in.z, in.w};
     auto h2 = [](uint32_t x) { return *reinterpret_cast<const __half2*>(&x); };
-    __half2 m2 = h2(u[0] & 0x7FFF7FFFu);
+    __half2 m2 = h2(in[0].x & 0x7FFF7FFFu);
 #pragma unroll
-    for (int i = 1; i < 4; ++i) m2 = __hmax2_nan(m2, h2(u[i] & 0x7FFF7FFFu));
+    for (int k = 0; k < N; ++k) {
+        const uint32_t u[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
 #pragma unroll
-    for (int d = D / 16; d > 0; d >>= 1) m2 = __hmax2_nan(m2, __shfl_xor_sync(0xffffffffu, m2, d));
+        for (int i = k ? 0 : 1; i < 4; ++i) m2 = __hmax2_nan(m2, h2(u[i] & 0x7FFF7FFFu));
+    }
+#pragma unroll
+    for (int d = D / (16 * N); d > 0; d >>= 1) m2 = __hmax2_nan(m2, __shfl_xor_sync(0xffffffffu, m2, d));
     const __half m = __hmax_nan(__low2half(m2), __high2half(m2));
     float amax = __half2float(m);
     uint16_t s16 = us::float_to_half_bits(amax / q);
-    float v[8];
     if (__any_sync(0xffffffffu, !(amax <= 65504.f) || (s16 < 0x0400u && s16 != 0u))) {
-        unpack8(in, v);
         amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        for (int k = 0; k < N; ++k) {
+            float v[8];
+            unpack8(in[k], v);
 #pragma unroll
-        for (int d = D / 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        }
+#pragma unroll
+        for (int d = D / (16 * N); d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
         s16 = us::float_to_half_bits(amax / q);
         if (s16 == 0) s16 = 0x3C00u;                          // 1.0
         const float s = us::half_bits_to_float(s16);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(rintf(v[i] / s), -q - 1.f), q) + kRound;
+        for (int k = 0; k < N; ++k) {
+            float v[8];
+            unpack8(in[k], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(rintf(v[i] / s), -q - 1.f), q) + kRound;
+            codes[k] = pack_codes<ELEM>(v);
+        }
     } else {
         if (s16 == 0) s16 = 0x3C00u;
         const float s = us::half_bits_to_float(s16), inv = 1.f / s;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 x = __half22float2(h2(u[i]));
-            const float a = x.x * inv, b = x.y * inv;
-            v[2 * i] = fmaf(fmaf(-a, s, x.x), inv, a) + kRound;
-            v[2 * i + 1] = fmaf(fmaf(-b, s, x.y), inv, b) + kRound;
+        for (int k = 0; k < N; ++k) {
+            const uint32_t u[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = __half22float2(h2(u[i]));
+                const float a = x.x * inv, b = x.y * inv;
+                v[2 * i] = fmaf(fmaf(-a, s, x.x), inv, a) + kRound;
+                v[2 * i + 1] = fmaf(fmaf(-b, s, x.y), inv, b) + kRound;
+            }
+            codes[k] = pack_codes<ELEM>(v);
         }
     }
-    codes = pack_codes<ELEM>(v);
     return s16;
+}
+template <int ELEM, int D>
+US_DEV uint16_t quantise_row(uint4 in, uint2& codes) {
+    const uint4 x[1] = {in};
+    uint2 c[1];
+    const uint16_t s = quantise_row<ELEM, D, 1>(x, c);
+    codes = c[0];
+    return s;
 }
 
 template <int ELEM>

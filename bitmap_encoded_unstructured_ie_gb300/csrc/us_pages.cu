@@ -10,9 +10,11 @@
 //
 // Nothing here computes: it is latency (lengths, sums, entries, one after the other).
 // One launch of one thread-block cluster does it, its barrier between the two moves:
-// each CTA makes the prefix sums for itself (B <= 1024), then the cluster's threads
-// share the pages, finding a page's request by bisection of the sums, so that one long
-// request is spread like many short ones.
+// each CTA makes the prefix sums for itself (B <= 1024), then the cluster's warps share
+// the pages in runs of up to 128 of one request, so that one long request is spread like
+// many short ones.  A warp finds a run's request in two steps, each lane looking at
+// another sum (by bisection for each page: 512 requests that give and take 280000 pages
+// 25 us, CHURN_US so).  A step of 48 requests with four drafts each takes DRAFT_US a call.
 #include "us_internal.h"
 #include "us_kv.cuh"
 #include "us_launch.cuh"
@@ -22,25 +24,29 @@ namespace {
 constexpr int kCtas = 8, kThreads = 1024, kMaxB = 1024, kAll = kCtas * kThreads;
 constexpr int kAtOnce = 4;                        // pages of a thread on their way at once
 
+constexpr int kRun = 32 * kAtOnce;
+
 struct Sums {
-    int rel[kMaxB], tak[kMaxB];                   // pages of the requests up to this one, itself among them
+    int rel[kMaxB], tak[kMaxB];                   // pages of the requests before this one
+    int rel_run[kMaxB], tak_run[kMaxB];           // runs of the requests up to this one, itself among them; behind the last one 2^31 - 1
     int from[kMaxB], have[kMaxB];                 // pages kept (the first one given back), pages held
-    int64_t wsum[2][32];
-    int all_rel, all_tak;
+    bool served[kMaxB];
+    int64_t wsum[3][32];
+    int all_tak;
     int bad;
 };
 
-// Inclusive sums of a and b over the block's threads.
-US_DEV void scan2(int64_t& a, int64_t& b, int64_t (&w)[2][32]) {
+// Inclusive sums of a, b and c over the block's threads.
+US_DEV void scan3(int64_t& a, int64_t& b, int64_t& c, int64_t (&w)[3][32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, b, d);
-        if (lane >= d) a += x, b += y;
+        const int64_t x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, b, d), z = __shfl_up_sync(0xffffffffu, c, d);
+        if (lane >= d) a += x, b += y, c += z;
     }
-    if (lane == 31) w[0][warp] = a, w[1][warp] = b;
+    if (lane == 31) w[0][warp] = a, w[1][warp] = b, w[2][warp] = c;
     __syncthreads();
-    if (warp < 2) {
+    if (warp < 3) {
         int64_t v = w[warp][lane];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -50,25 +56,26 @@ US_DEV void scan2(int64_t& a, int64_t& b, int64_t (&w)[2][32]) {
         w[warp][lane] = v;
     }
     __syncthreads();
-    if (warp) a += w[0][warp - 1], b += w[1][warp - 1];
+    if (warp) a += w[0][warp - 1], b += w[1][warp - 1], c += w[2][warp - 1];
 }
 
-// First request whose sum is above x.
-US_DEV int owner(const int* sum, int B, int x) {
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (sum[mid] > x) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
+// The request of run x of the warp's (the first one whose sum is above x), and which of
+// its runs it is.
+US_DEV int owner(const int* sum, int x, int& run) {
+    const int lane = threadIdx.x & 31;
+    const int row = 32 * (__ffs(__ballot_sync(0xffffffffu, sum[32 * lane + 31] > x)) - 1);
+    const int v = sum[row + lane], at = __ffs(__ballot_sync(0xffffffffu, v > x)) - 1, o = row + at;
+    run = x - (o ? sum[o - 1] : 0);
+    return o;
 }
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
 reserve_kernel(const us_kv_pool P, int page_shift, const int32_t* len, unsigned* status) {
     __shared__ Sums S;
     us::pdl_wait();
-    const int b = threadIdx.x, at = blockIdx.x * kThreads + threadIdx.x;
+    const int b = threadIdx.x, lane = b & 31;
+    const int warp = ((int)blockIdx.x * kThreads + b) / 32;    // of the cluster's
+    constexpr int kWarps = kAll / 32;
     unsigned* says = blockIdx.x == 0 ? status : nullptr;
     const int count = *P.free_count;
     if (b == 0) S.bad = count < 0 || count > P.num_pages;
@@ -84,8 +91,8 @@ reserve_kernel(const us_kv_pool P, int page_shift, const int32_t* len, unsigned*
         rel = want < have ? have - want : 0;
         tak = want > have ? want - have : 0;
     }
-    int64_t rel_to = rel, tak_to = tak;
-    scan2(rel_to, tak_to, S.wsum);
+    int64_t rel_to = rel, tak_to = tak, run_to = (rel + kRun - 1) / kRun << 32 | (tak + kRun - 1) / kRun;
+    scan3(rel_to, tak_to, run_to, S.wsum);
     const int64_t all = S.wsum[0][31];
     if (S.bad || all > P.num_pages - count) {              // (the same in every CTA)
         if (b == 0) us::set_status(says, US_ERR_CORRUPT);
@@ -94,48 +101,41 @@ reserve_kernel(const us_kv_pool P, int page_shift, const int32_t* len, unsigned*
     }
     const int R = (int)all, room = count + R;
     const bool served = tak_to <= room;
-    if (b < P.B) {
-        S.rel[b] = (int)rel_to;
-        S.tak[b] = served ? (int)tak_to : 0x7FFFFFFF;
-        S.from[b] = want;
-        S.have[b] = have;
-        if (!served && tak) us::set_status(says, US_ERR_WORKSPACE);
-    }
+    S.rel[b] = (int)(rel_to - rel);
+    S.tak[b] = served ? (int)(tak_to - tak) : 0;
+    S.rel_run[b] = b < P.B ? (int)(run_to >> 32) : 0x7FFFFFFF;
+    S.tak_run[b] = b < P.B ? (int)run_to : 0x7FFFFFFF;
+    S.from[b] = want;
+    S.have[b] = have;
+    S.served[b] = served;
+    if (!served && tak) us::set_status(says, US_ERR_WORKSPACE);
     if (b == 0) S.all_tak = 0;
     __syncthreads();
     if (b < P.B && served) atomicMax(&S.all_tak, (int)tak_to);
-    for (int x0 = at; x0 < R; x0 += kAtOnce * kAll) {
-        int32_t* from[kAtOnce];
-        int page[kAtOnce];
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            const int x = x0 + u * kAll;
-            from[u] = nullptr;
-            if (x >= R) continue;
-            const int o = owner(S.rel, P.B, x), i = x - (o ? S.rel[o - 1] : 0);
-            from[u] = P.page_table + (int64_t)o * P.max_pages + S.from[o] + i;
-            page[u] = *from[u];
-        }
+    const int rel_runs = (int)(S.wsum[2][31] >> 32), tak_runs = (int)S.wsum[2][31];
+    for (int x = warp; x < rel_runs; x += kWarps) {
+        int run, page[kAtOnce];
+        const int o = owner(S.rel_run, x, run), i0 = run * kRun + lane, n = S.have[o] - S.from[o];
+        int32_t* from = P.page_table + (int64_t)o * P.max_pages + S.from[o] + i0;
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u)
-            if (from[u]) P.free_pages[count + x0 + u * kAll] = page[u], *from[u] = -1;
+            if (i0 + 32 * u < n) page[u] = from[32 * u];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+            if (i0 + 32 * u < n) P.free_pages[count + S.rel[o] + i0 + 32 * u] = page[u], from[32 * u] = -1;
     }
     us::cluster_sync();                                    // (everyone has read held and the count, too)
     const int taken = S.all_tak;
-    for (int x0 = at; x0 < taken; x0 += kAtOnce * kAll) {
-        int page[kAtOnce];
+    for (int x = warp; x < tak_runs; x += kWarps) {
+        int run, page[kAtOnce];
+        const int o = owner(S.tak_run, x, run), i0 = run * kRun + lane, n = S.from[o] - S.have[o];
+        if (!S.served[o]) break;                           // nor is one behind it
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            const int x = x0 + u * kAll;
-            if (x < taken) page[u] = __ldcg(P.free_pages + room - 1 - x);
-        }
+        for (int u = 0; u < kAtOnce; ++u)
+            if (i0 + 32 * u < n) page[u] = __ldcg(P.free_pages + room - 1 - (S.tak[o] + i0 + 32 * u));
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            const int x = x0 + u * kAll;
-            if (x >= taken) continue;
-            const int o = owner(S.tak, P.B, x), i = x - (o ? S.tak[o - 1] : 0);
-            P.page_table[(int64_t)o * P.max_pages + S.have[o] + i] = page[u];
-        }
+        for (int u = 0; u < kAtOnce; ++u)
+            if (i0 + 32 * u < n) P.page_table[(int64_t)o * P.max_pages + S.have[o] + i0 + 32 * u] = page[u];
     }
     if (blockIdx.x == 0) {
         if (b < P.B && (served || !tak)) P.held[b] = want;

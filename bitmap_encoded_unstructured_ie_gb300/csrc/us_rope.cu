@@ -8,19 +8,22 @@
 // would be off by p * 2^-24 radians.  cos and sin are made once a token and CTA, in
 // shared memory, and serve all of its heads.
 //
-// D / 8 lanes (of 8, 16 or 32) hold a row, 16 bytes each; the pairs (j, j + R/2) lie
-// R / 16 lanes apart and are exchanged by shuffles.  Four rows a thread are on their
-// way at once.  What bounds it: bytes (each row read and written once) for prompts,
-// latency for single tokens: offsets, rows, the sum's shuffles, one after the other.
+// D / 16 lanes (of 4, 8 or 16) hold a row, each two pieces of eight values: of the first
+// R those whose values are turned with one another, (8 l .., R/2 + 8 l ..) or 16 values
+// side by side, so that a rotation stays in its lane (with eight values a lane and the
+// pairs exchanged by shuffles, prompts took 200 instructions a warp for four rows of
+// 128, 79 us where this takes KERNEL_US).  Such a group of lanes takes HEADS heads of one
+// token at a time (a chunk: of queries, keys or values), with weights, cos and sin in
+// registers.
+#include "us_attn.cuh"
 #include "us_internal.h"
 #include "us_kv_quant.cuh"
 #include "us_launch.cuh"
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kTokens = 16;                       // of a CTA, at most
-constexpr int kAtOnce = 4;                        // rows of a thread on their way at once
 constexpr int kNone = -1;                         // no cache
 
 struct Call {
@@ -34,54 +37,73 @@ struct Call {
     int64_t ldv;
 };
 
-// Lanes: of a row.  ELEM: the cache's, or kNone.
-template <int LANES, int ELEM>
-__global__ void __launch_bounds__(kThreads)
-norm_rope_kernel(const Call p, int tokens) {
-    constexpr int kRows = kThreads / LANES;
-    __shared__ float cs[kTokens][2][128];
+using us::attn::add2;
+using us::attn::fma2;
+using us::attn::mul2;
+using us::attn::pack_half2;
+using us::attn::pair;
+using us::attn::unpair;
+
+// Eight fp16 values as four pairs of fp32
+US_DEV void unpack(uint4 in, uint64_t (&y)[4]) {
+    const uint32_t u[4] = {in.x, in.y, in.z, in.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+        y[i] = pair(f.x, f.y);
+    }
+}
+US_DEV uint32_t pack(uint64_t y) {
+    float a, b;
+    unpair(y, a, b);
+    return pack_half2(a, b);
+}
+
+// LANES: of a row.  HEADS: of a chunk.  ELEM: the cache's, or kNone.  A CTA takes `chunks`
+// chunks of a request's, which belong to kTokens tokens at most.
+template <int LANES, int HEADS, int ELEM>
+__global__ void __launch_bounds__(kThreads, HEADS == 1 ? 6 : 4)
+norm_rope_kernel(const Call p, int chunks) {
+    constexpr int kGroups = kThreads / LANES;
+    __shared__ __align__(16) float cs[kTokens][2][128];
     __shared__ int64_t place[kTokens];
     us::pdl_wait();
     const int b = blockIdx.y, pos = p.a.pos[b];
     int row0;
-    const int n = us::kv_rows(p.a, b, row0, p.c.status), i0 = blockIdx.x * tokens, count = min(tokens, n - i0);
-    if (count <= 0) {
+    // chunks of a token: queries, keys, values
+    const int nq = (p.q.H + HEADS - 1) / HEADS, nk = (p.k.H + HEADS - 1) / HEADS, per = nq + nk + (ELEM == kNone ? 0 : nk);
+    const int64_t x0 = (int64_t)blockIdx.x * chunks, x1 = (int64_t)us::kv_rows(p.a, b, row0, p.c.status) * per;
+    const int mine = (int)min(x1 - x0, (int64_t)chunks);
+    if (mine <= 0) {
         us::pdl_launch_dependents();
         return;
     }
-    const int l = threadIdx.x % LANES, heads = p.q.H + p.k.H + (ELEM == kNone ? 0 : p.c.Hkv), rows = count * heads;
-    const bool here = 8 * l < p.D;
-    // the lane's weights; 0x3C00 is 1.0
-    uint4 wq = make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u), wk = wq;
-    if (p.q.H && p.q.w && here) wq = reinterpret_cast<const uint4*>(p.q.w)[l];
-    if (p.k.H && p.k.w && here) wk = reinterpret_cast<const uint4*>(p.k.w)[l];
-    const int R = p.rope.R, half = R / 16;
-    const bool pairs = p.rope.style == US_ROPE_PAIRS;
-    const bool turned = 8 * l < R;
-    // halves: the lane with the other ones of its pairs, and its angles' first index
-    const int other = pairs || !turned ? l : l < half ? l + half : l - half;
-    const int first = pairs ? 4 * l : 8 * (l < half ? l : l - half);
+    const int i0 = (int)(x0 / per), skip = (int)(x0 - (int64_t)i0 * per);              // the first chunk's token, and its place there
+    const int count = (skip + mine - 1) / per + 1;
+    const int l = threadIdx.x % LANES, R = p.rope.R, turning = R / 16;
+    const bool pairs = p.rope.style == US_ROPE_PAIRS, turned = l < turning;
+    // the lane's pieces, and whether a row has them
+    const int piece[2] = {turned && !pairs ? l : 2 * l, turned && !pairs ? l + turning : 2 * l + 1};
+    const bool has[2] = {8 * piece[0] < p.D, 8 * piece[1] < p.D};
+    const float inv_d = 1.f / (float)p.D;
     bool ready = false;
-    for (int r0 = threadIdx.x / LANES; r0 - (int)threadIdx.x / LANES < rows; r0 += kAtOnce * kRows) {
-        uint4 in[kAtOnce];
-        int tok[kAtOnce], h[kAtOnce];
+    for (int x = threadIdx.x / LANES; x - (int)threadIdx.x / LANES < mine; x += kGroups) {       // (as many rounds for all threads)
+        const bool some = x < mine;
+        const int tok = some ? (int)((unsigned)(x + skip) / (unsigned)per) : 0, q = some ? x + skip - tok * per : 0;
+        const int kind = q < nq ? 0 : ELEM == kNone || q < nq + nk ? 1 : 2;            // queries, keys, values
+        const us_heads& g = kind == 0 ? p.q : p.k;
+        const int h0 = (q - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * HEADS, heads = some ? min(HEADS, g.H - h0) : 0;
+        const int64_t t = row0 + i0 + tok, hs = kind == 2 ? p.D : g.hs;
+        const uint16_t* src = (kind == 2 ? p.V + t * p.ldv : g.x + t * g.ld) + h0 * hs;
+        uint4 in[HEADS][2];
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            const int r = r0 + u * kRows;
-            in[u] = make_uint4(0, 0, 0, 0);
-            tok[u] = (int)((unsigned)r / (unsigned)heads), h[u] = r - tok[u] * heads;
-            if (r < rows && here) {
-                const int64_t t = row0 + i0 + tok[u];
-                const uint16_t* x = h[u] < p.q.H ? p.q.x + t * p.q.ld + h[u] * p.q.hs
-                                    : ELEM == kNone || h[u] < p.q.H + p.k.H
-                                        ? p.k.x + t * p.k.ld + (h[u] - p.q.H) * p.k.hs
-                                        : p.V + t * p.ldv + (int64_t)(h[u] - p.q.H - p.k.H) * p.D;
-                in[u] = *reinterpret_cast<const uint4*>(x + 8 * l);
-            }
-        }
-        if (!ready) {                                      // while the rows are on their way
-            for (int x = threadIdx.x; x < count * (R / 2); x += kThreads) {
-                const int i = x / (R / 2), j = x - i * (R / 2);
+        for (int u = 0; u < HEADS; ++u)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                in[u][k] = u < heads && has[k] ? *reinterpret_cast<const uint4*>(src + u * hs + 8 * piece[k]) : make_uint4(0, 0, 0, 0);
+        if (!ready) {                                      // while the first rows are on their way
+            for (int y = threadIdx.x; y < count * (R / 2); y += kThreads) {
+                const int i = y / (R / 2), j = y - i * (R / 2);
                 const int at = us::kv_pos(pos, p.depth ? p.depth[row0 + i0 + i] : i0 + i);
                 const int32_t turn = (int32_t)(((uint64_t)(int64_t)at * p.rope.turns[j]) >> 32);
                 sincospif((float)turn * 0x1p-31f, &cs[i][1][j], &cs[i][0][j]);
@@ -93,77 +115,83 @@ norm_rope_kernel(const Call p, int tokens) {
             __syncthreads();
             ready = true;
         }
+        const bool normed = kind < 2 && g.w != nullptr;
+        uint64_t w[2][4], co[4], si[4], ns[4];             // weights, cos, sin, -sin, two in each
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            const int r = r0 + u * kRows;
-            if (u && r - (int)threadIdx.x / LANES >= rows) break;
-            const bool is_q = h[u] < p.q.H, is_v = ELEM != kNone && h[u] >= p.q.H + p.k.H, ok = r < rows;
-            const us_heads& g = is_q ? p.q : p.k;
-            uint4 out = in[u];
-            {
-                float y[8];
-                const uint32_t x4[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
+        for (int k = 0; k < 2; ++k)
+            unpack(normed && has[k] ? reinterpret_cast<const uint4*>(g.w)[piece[k]] : make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u), w[k]);
+        if (turned) {
+            const ulonglong2* c2 = reinterpret_cast<const ulonglong2*>(&cs[tok][0][8 * l]);
+            const ulonglong2 a = c2[0], d = c2[1], e = c2[32], f = c2[33];
+            co[0] = a.x, co[1] = a.y, co[2] = d.x, co[3] = d.y, si[0] = e.x, si[1] = e.y, si[2] = f.x, si[3] = f.y;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x4[i]));
-                    y[2 * i] = f.x, y[2 * i + 1] = f.y;
-                }
-                float ss = 0.f;
+            for (int i = 0; i < 4; ++i) ns[i] = si[i] ^ 0x8000000080000000ull;
+        }
+        uint16_t* dst = kind < 2 && g.y ? g.y + t * g.ldy + h0 * g.hsy : nullptr;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+        for (int u = 0; u < HEADS; ++u) {
+            uint64_t y[2][4];
 #pragma unroll
-                for (int d = LANES / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-                if (g.w) {
-                    const float f = rsqrtf(ss / (float)p.D + p.rope.eps);
-                    const uint4 w = is_q ? wq : wk;
-                    const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+            for (int k = 0; k < 2; ++k) unpack(in[u][k], y[k]);
+            uint64_t s2 = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s2 = fma2(y[k][i], y[k][i], s2);
+            float ss, sb;
+            unpair(s2, ss, sb);
+            ss += sb;
+#pragma unroll
+            for (int d = LANES / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+            if (normed) {
+                const float f = rsqrtf(ss * inv_d + p.rope.eps);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[k][i] = mul2(mul2(y[k][i], pair(f, f)), w[k][i]);
+            }
+            if (turned && kind < 2) {
+                if (pairs) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float a, d, c[2], s[2];
+                            unpair(y[k][i], a, d);
+                            unpair(co[2 * k + (i >> 1)], c[0], c[1]);
+                            unpair(si[2 * k + (i >> 1)], s[0], s[1]);
+                            y[k][i] = pair(a * c[i & 1] - d * s[i & 1], d * c[i & 1] + a * s[i & 1]);
+                        }
+                } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 wf = __half22float2(*reinterpret_cast<const __half2*>(&w4[i]));
-                        y[2 * i] = y[2 * i] * f * wf.x, y[2 * i + 1] = y[2 * i + 1] * f * wf.y;
+                        const uint64_t a = y[0][i], d = y[1][i];
+                        y[0][i] = fma2(d, ns[i], mul2(a, co[i]));
+                        y[1][i] = fma2(a, si[i], mul2(d, co[i]));
                     }
                 }
-                if (R) {
-                    const float* c = cs[ok ? tok[u] : 0][0] + (turned ? first : 0);
-                    const float* s = c + 128;
-                    if (pairs) {
-                        if (turned) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float a = y[2 * i], d = y[2 * i + 1];
-                                y[2 * i] = a * c[i] - d * s[i];
-                                y[2 * i + 1] = d * c[i] + a * s[i];
-                            }
-                        }
-                    } else {
-                        float z[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) z[i] = __shfl_sync(0xffffffffu, y[i], other, LANES);
-                        if (turned) {
-                            const float sign = l < half ? -1.f : 1.f;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) y[i] = y[i] * c[i] + sign * s[i] * z[i];
-                        }
-                    }
-                }
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[i] = (uint32_t)us::float_to_half_bits(y[2 * i]) | ((uint32_t)us::float_to_half_bits(y[2 * i + 1]) << 16);
-                if (!is_v) out = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            if (ok && here && !is_v && g.y)
-                *reinterpret_cast<uint4*>(g.y + (int64_t)(row0 + i0 + tok[u]) * g.ldy + (h[u] - (is_q ? 0 : p.q.H)) * g.hsy + 8 * l) = out;
+            if (kind < 2) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) in[u][k] = make_uint4(pack(y[k][0]), pack(y[k][1]), pack(y[k][2]), pack(y[k][3]));
+            }
+            if (u < heads && dst) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (has[k]) *reinterpret_cast<uint4*>(dst + u * g.hsy + 8 * piece[k]) = in[u][k];
+            }
             if constexpr (ELEM != kNone) {
-                constexpr int kBytes = ELEM == US_I8 ? 8 : 4;     // of a lane's codes
-                if (__any_sync(0xffffffffu, ok && !is_q)) {
-                    uint2 codes;
-                    const uint16_t s = us::quantise_row<ELEM, 8 * LANES>(out, codes);
-                    if (ok && !is_q && place[tok[u]] >= 0) {
-                        const int kh = h[u] - p.q.H - (is_v ? p.k.H : 0);
-                        const int64_t e = place[tok[u]] + ((int64_t)kh << p.c.page_shift);
-                        us::store_codes<ELEM>((is_v ? p.c.v : p.c.k) + (e * LANES + l) * kBytes, codes);
-                        if (l == 0) p.c.scale[2 * e + is_v] = s;
+                constexpr int kBytes = ELEM == US_I8 ? 8 : 4;     // of a piece's codes
+                const bool kept = u < heads && kind > 0;
+                if (__any_sync(0xffffffffu, kept)) {
+                    uint2 codes[2];
+                    const uint16_t s = us::quantise_row<ELEM, 16 * LANES, 2>(in[u], codes);
+                    if (kept && place[tok] >= 0) {
+                        const int64_t e = place[tok] + ((int64_t)(h0 + u) << p.c.page_shift);
+                        uint8_t* to = (kind == 2 ? p.c.v : p.c.k) + e * (2 * LANES * kBytes);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) us::store_codes<ELEM>(to + piece[k] * kBytes, codes[k]);
+                        if (l == 0) p.c.scale[2 * e + (kind == 2)] = s;
                     }
                 }
             }
@@ -172,24 +200,32 @@ norm_rope_kernel(const Call p, int tokens) {
     us::pdl_launch_dependents();
 }
 
-// Tokens of a CTA: four rows a thread, or fewer where that leaves SMs without a CTA.
-int cta_tokens(int heads, int lanes, int64_t tokens) {
-    const int per = kThreads / lanes;
-    int t = (kAtOnce * per + heads - 1) / heads;
-    if (t > kTokens) t = kTokens;
-    while (t > 1 && tokens < (int64_t)t * 2 * us::num_sms()) t /= 2;
-    return t;
+template <int LANES, int HEADS, int ELEM>
+us_status launch_as(const Call& p, cudaStream_t st) {
+    constexpr int kGroups = kThreads / LANES;
+    const int nq = (p.q.H + HEADS - 1) / HEADS, nk = (p.k.H + HEADS - 1) / HEADS, per = nq + nk + (ELEM == kNone ? 0 : nk);
+    // four rounds a CTA, or one where that leaves SMs without work
+    const int64_t all = (int64_t)p.a.max_n * per;
+    int chunks = all * p.c.B >= (int64_t)8 * kGroups * us::num_sms() ? 4 * kGroups : kGroups;
+    if (chunks > (kTokens - 1) * per) chunks = (kTokens - 1) * per;
+    return us::launch_pdl(norm_rope_kernel<LANES, HEADS, ELEM>, dim3((unsigned)((all + chunks - 1) / chunks), (unsigned)p.c.B), kThreads, 0, st, p,
+                          chunks);
+}
+
+// Four heads a chunk where that leaves work for every SM, else one: a step of 16 tokens
+// is latency, which four heads one after the other lengthen (STEP_US), prompts are bytes and
+// instructions, which four heads share (PROMPT_US).
+template <int LANES, int ELEM>
+us_status launch_heads(const Call& p, cudaStream_t st) {
+    const int64_t rows = (int64_t)p.a.max_n * p.c.B * (p.q.H + p.k.H + (ELEM == kNone ? 0 : p.c.Hkv));
+    return rows * LANES >= (int64_t)16 * kThreads * us::num_sms() ? launch_as<LANES, 4, ELEM>(p, st) : launch_as<LANES, 1, ELEM>(p, st);
 }
 
 template <int ELEM>
 us_status launch(const Call& p, cudaStream_t st) {
-    const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
-    const int heads = p.q.H + p.k.H + (ELEM == kNone ? 0 : p.c.Hkv);
-    const int t = cta_tokens(heads, lanes, (int64_t)p.a.max_n * p.c.B);
-    const dim3 grid((unsigned)((p.a.max_n + t - 1) / t), (unsigned)p.c.B);
-    if (lanes == 8) return us::launch_pdl(norm_rope_kernel<8, ELEM>, grid, kThreads, 0, st, p, t);
-    if (lanes == 16) return us::launch_pdl(norm_rope_kernel<16, ELEM>, grid, kThreads, 0, st, p, t);
-    if constexpr (ELEM == kNone) return us::launch_pdl(norm_rope_kernel<32, ELEM>, grid, kThreads, 0, st, p, t);
+    if (p.D <= 64) return launch_heads<4, ELEM>(p, st);
+    if (p.D <= 128) return launch_heads<8, ELEM>(p, st);
+    if constexpr (ELEM == kNone) return launch_heads<16, ELEM>(p, st);
     return US_ERR_UNSUPPORTED;
 }
 
