@@ -14,8 +14,10 @@
 // 64 rows takes 16 lanes of each warp's 32 in TMEM; O's columns 256 .. 511 lie in the
 // other 16 lanes, so O takes 256 columns and two tiles' scores 128 more.
 //   warps 0-3: softmax of 16 rows each, the segment's Q and its outputs
-//   warp 4: finds pages and issues the tiles' copies (TMA, 128-byte swizzle)
-//   warp 5: one thread issues the MMAs, whichever of the next tile's scores (its rows
+//   warps 4-7: find pages and copy the tiles' rows, 16 bytes a lane, each to its place of
+//           the 128-byte swizzle.  (By tensor copies a tile came at 33 bytes a cycle, 10 at a
+//           kernel's start, and the issuing thread was held up meanwhile.)
+//   warp 8: one thread issues the MMAs, whichever of the next tile's scores (its rows
 //           have landed) and the last one's outputs (its weights are there) can go
 // Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set, and
 // moves when a score passes R + 15.9 (fp16 holds 2^15.9 and keeps all bits of weights
@@ -33,7 +35,7 @@ namespace {
 using namespace us::attn;
 
 constexpr int kM = 64, kTile = 64;                // query rows of a segment, positions of a tile
-constexpr int kSoftWarps = 4, kLoadWarp = 4, kMmaWarp = 5, kThreads = 192;
+constexpr int kSoftWarps = 4, kLoadWarps = 4, kMmaWarp = kSoftWarps + kLoadWarps, kThreads = 32 * (kMmaWarp + 1);
 constexpr float kTop = 11.f, kRoom = 15.9f;        // log2 of a row's largest weight when R is set, and at most
 constexpr int kBlock = 64 * 128;                  // bytes of 64 rows of 64 values
 constexpr int kMaxStages = 4;
@@ -58,12 +60,10 @@ struct Shape {
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-US_DEV void tma_load_rows(void* dst, const CUtensorMap* map, int row, int block, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(us::smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(block), "r"(us::smem_addr(bar))
-        : "memory");
+// This thread's copies so far arrive at `bar` when they have landed (one of the arrivals
+// that it was set up for).
+US_DEV void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(us::smem_addr(bar)) : "memory");
 }
 
 // 16 lanes x 64 columns in fragment order: lane (g, c) gets rows g (v[4k], v[4k + 1])
@@ -94,7 +94,7 @@ US_DEV void tmem_st32(uint32_t taddr, const float (&v)[32]) {
 
 template <int DC>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map) {
+attn_lat_kernel(const UsAttnLatParams p) {
     using Sh = Shape<DC>;
     constexpr int kStages = Sh::kStages;
     using Cur = Cursor<kM, kTile>;
@@ -108,11 +108,11 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i)
-            for (int j = 0; j < Sh::kParts; ++j) us::mbar_init(&H.full[i][j], 1), us::mbar_init(&H.free[i][j], 1);
+            for (int j = 0; j < Sh::kParts; ++j)               // (part 0: `valid`, too)
+                us::mbar_init(&H.full[i][j], 32 * kLoadWarps + (j == 0)), us::mbar_init(&H.free[i][j], 1);
         for (int i = 0; i < 2; ++i) us::mbar_init(&H.s_full[i], 1);
         us::mbar_init(&H.p_full, kSoftWarps), us::mbar_init(&H.pv_done, 1), us::mbar_init(&H.q_full, kSoftWarps);
         us::fence_mbar_init();
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
     }
     if (warp == kMmaWarp) us::tmem_alloc(&H.tmem, 512);
     us::tc_fence_before();
@@ -345,12 +345,14 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
             it = end;
             cur = next;
         }
-    } else if (warp == kLoadWarp) {
+    } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------- copies
-        // Pieces of a page each (page_size positions, 64 at most), a copy for each 64
-        // values of their rows, a lane each.
+        // Eight lanes have 128 bytes of a row; the warp's rows are 16 k + 4 w + lane / 8, k < 4.
+        const int w = warp - kSoftWarps, row0 = 4 * w + (lane >> 3), chunk = lane & 7;
+        const uint32_t to0 = us::smem_addr(x_sm) + row0 * 128 + ((chunk ^ (row0 & 7)) << 4);
+        // The page of each piece of page_size positions (64 at most), a lane each: of the 32 from piece
+        // `first` of a segment's part on
         const int piece = min(kTile, 1 << p.c.page_shift), pieces = kTile / piece, shift = __ffs(piece) - 1;
-        // page of this lane's piece among the 32 from piece `first` of a segment's part on
         auto page_of = [&](const Cur& c, int first) {
             const int pos = c.tile * kTile + ((first + lane) << shift);
             return pos < c.r.ctx + c.r.n ? p.c.table[(int64_t)c.b * p.c.max_pages + (pos >> p.c.page_shift)] : -1;
@@ -367,44 +369,39 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
                 if (at && (at & 31) == 0) ids = ahead, ahead = page_of(cur, at + 32);
                 const int st = i % kStages, pos0 = (cur.tile + i - it) * kTile;
                 uint64_t ok = 0;
-                int bytes = 0;                             // of 64 values
-                for (int k = 0; k < pieces; ++k) {
-                    const int id = __shfl_sync(0xffffffffu, ids, (at + k) & 31), here = min(piece, last - pos0 - (k << shift));
-                    if (here <= 0) break;
-                    if (id < 0 || id >= p.c.num_pages) {
-                        us::set_status(p.c.status, US_ERR_CORRUPT);
-                        continue;
-                    }
-                    ok |= (here == 64 ? ~0ull : (1ull << here) - 1ull) << (k << shift);
-                    bytes += piece * 128;
+                const uint16_t* src[4];                    // of the lane's rows
+                bool has[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int id = __shfl_sync(0xffffffffu, ids, (at + ((16 * k) >> shift)) & 31), pos = pos0 + 16 * k + row0;
+                    const int here = min(16, last - pos0 - 16 * k);        // of the sixteen rows
+                    const bool good = id >= 0 && id < p.c.num_pages;
+                    if (here > 0 && !good) us::set_status(p.c.status, US_ERR_CORRUPT);
+                    if (here > 0 && good) ok |= ((1ull << here) - 1ull) << (16 * k);
+                    has[k] = (ok >> (16 * k + row0)) & 1ull;
+                    src[k] = p.rows + (((int64_t)id << p.c.page_shift) + (pos & ((1 << p.c.page_shift) - 1))) * Sh::kW + 8 * chunk;
                 }
-                uint8_t* x = x_sm + st * Sh::kOperand;
+                const uint32_t to = to0 + st * Sh::kOperand;
 #pragma unroll
                 for (int j = 0; j < Sh::kParts; ++j) {
-                    const int part = j ? j - 1 : Sh::kHalves, blocks = j ? 4 : 1;      // the key's part first
+                    const int part = j ? j - 1 : Sh::kHalves;              // the key's part first
                     if (i >= kStages) wait(&H.free[st][part], i / kStages - 1);
-                    if (lane == 0) {
-                        if (j == 1) H.valid[st] = ok;      // (part 0 was freed by those who read it)
-                        if (bytes) us::mbar_arrive_expect_tx(&H.full[st][part], (uint32_t)(blocks * bytes));
-                        else us::mbar_arrive(&H.full[st][part]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int c = 0; c < (j ? 4 : 1); ++c)
+                            if (has[k]) cp_async16(to + (4 * part + c) * kBlock + k * 2048, src[k] + (4 * part + c) * 64);
+                    cp_async_arrive(&H.full[st][part]);
+                    if (j == 1 && w == 0 && lane == 0) {   // (part 0 was freed by those who read it)
+                        H.valid[st] = ok;
+                        us::mbar_arrive(&H.full[st][0]);
                     }
-                    __syncwarp();
-                    for (int k = 0; k < pieces; ++k) {
-                        const int id = __shfl_sync(0xffffffffu, ids, (at + k) & 31), block = 4 * part + lane;
-                        if (((ok >> (k << shift)) & 1ull) && lane < blocks)
-                            tma_load_rows(x + block * kBlock + (k << shift) * 128, &map,
-                                          (id << p.c.page_shift) + ((pos0 + (k << shift)) & ((1 << p.c.page_shift) - 1)), block,
-                                          &H.full[st][part]);
-                    }
-                    __syncwarp();
                 }
             }
             it = end;
             cur = next, ids = after;
         }
-        // nothing of its own is left in flight when the CTA ends
-        for (int i = max(0, count - kStages); i < count; ++i)
-            for (int j = 0; j < Sh::kParts; ++j) wait(&H.full[i % kStages][j], i / kStages);
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // --------------------------------------------------------------- MMA
         if (us::elect_one()) {
@@ -421,6 +418,7 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
                     const int st = s % kStages, part = sp ? sp - 1 : Sh::kHalves;
                     if (s < end && s - o < 2 && us::mbar_test(&H.full[st][part], (uint32_t)(s / kStages) & 1u)) {
                         constexpr uint32_t id = us::umma_idesc_f16(kM, kTile);
+                        us::fence_proxy_async_smem();      // (the rows were written by plain copies)
                         us::tc_fence_after();
                         const uint64_t from = (uint64_t)(4 * part * kBlock >> 4);
                         const uint64_t q = qd + from, xd = us::umma_smem_desc_sw128(x_sm + st * Sh::kOperand) + from;
@@ -487,20 +485,8 @@ attn_lat_kernel(const UsAttnLatParams p, const __grid_constant__ CUtensorMap map
 template <int DC>
 us_status launch(UsAttnLatParams p, cudaStream_t st) {
     using Sh = Shape<DC>;
-    auto enc = us::tensor_map_encoder();
-    if (!enc) return US_ERR_CUDA;
     p.ws_parts = static_cast<Part*>(p.ws);
     p.ws_slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kPartBytes);
-    // the cache as (64 values, rows, blocks of 64 values)
-    CUtensorMap map;
-    const int page = 1 << p.c.page_shift;
-    const cuuint64_t dim[3] = {64, (cuuint64_t)p.c.num_pages * page, (cuuint64_t)Sh::kC}, stride[2] = {(cuuint64_t)Sh::kW * 2, 128};
-    const cuuint32_t box[3] = {64, (cuuint32_t)(page < kTile ? page : kTile), 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(p.rows), dim, stride, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return US_ERR_CUDA;
     auto kern = attn_lat_kernel<DC>;
     static std::atomic<bool> ready[64];                // the attribute is set once a device, by whichever thread
     int dev = 0;
@@ -510,7 +496,7 @@ us_status launch(UsAttnLatParams p, cudaStream_t st) {
             return US_ERR_CUDA;
         ready[dev].store(true, std::memory_order_release);
     }
-    us_status s = us::launch_pdl(kern, dim3((unsigned)us::attn::attn_ctas()), kThreads, Sh::kSmem, st, p, map);
+    us_status s = us::launch_pdl(kern, dim3((unsigned)us::attn::attn_ctas()), kThreads, Sh::kSmem, st, p);
     if (s != US_OK) return s;
     return us::attn::launch_join<kM, DC>(p, us::attn::attn_ctas(), st);
 }
