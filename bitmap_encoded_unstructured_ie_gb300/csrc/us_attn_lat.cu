@@ -119,6 +119,7 @@ attn_lat_kernel(const UsAttnLatParams p) {
     __syncthreads();
     us::tc_fence_after();
     us::pdl_wait();
+    us::pdl_launch_dependents();                           // (the join's CTAs come now, and wait for this kernel's end)
 
     Work wk;
     Cur cur;
@@ -270,21 +271,19 @@ attn_lat_kernel(const UsAttnLatParams p) {
                 // finite (drafts, or in a chain what is behind the segment's first token).
                 const int all_see = (p.mask ? (cur.r.n > 1 ? 0 : 1) : cur.rb * kM / G + 1) - base;
                 if (ok != ~0ull || all_see < kTile) {
-                    uint8_t* x = x_sm + st * Sh::kOperand;
+                    // a thread's 16 bytes of every 16th row of a block
+                    uint8_t* x = x_sm + st * Sh::kOperand + threadIdx.x * 16;
+                    const int r0 = threadIdx.x >> 3;
 #pragma unroll 1
-                    for (int k0 = threadIdx.x; k0 < kTile * DC / 8; k0 += 8 * 32 * kSoftWarps) {
-                        uint4 y[8];
-                        auto at = [&](int i) {
-                            const int k = k0 + i * 32 * kSoftWarps;
-                            return reinterpret_cast<uint4*>(x + (k >> 9) * kBlock + ((k >> 3) & (kTile - 1)) * 128 + ((k & 7) << 4));
-                        };
+                    for (int g = 0; g < 4; ++g) {
+                        const int r = r0 + 16 * g;
+                        const bool there = (ok >> r) & 1ull;
+                        if (there && r < all_see) continue;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = *at(i);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = ((k0 + i * 32 * kSoftWarps) >> 3) & (kTile - 1);
-                            if (!((ok >> r) & 1ull)) *at(i) = make_uint4(0, 0, 0, 0);
-                            else if (r >= all_see && !all_finite(y[i])) *at(i) = finite(y[i]);
+                        for (int c = 0; c < DC / 64; ++c) {
+                            uint4* at = reinterpret_cast<uint4*>(x + c * kBlock + g * 2048);
+                            if (!there) *at = make_uint4(0, 0, 0, 0);
+                            else if (const uint4 y = *at; !all_finite(y)) *at = finite(y);
                         }
                     }
                 }
@@ -323,18 +322,22 @@ attn_lat_kernel(const UsAttnLatParams p) {
                 const int col0 = lane & 16 ? 256 : 0;
                 uint16_t* out = mine ? out_row<kM>(p, cur.r.row0, 0, cur.rb, row, DC) + col0 : nullptr;
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 32) {
-                    float a[32];
-                    us::tmem_ld32(tmem + lanes + c, a);
+                for (int c = 0; c < 256; c += 64) {
+                    uint32_t r0[32], r1[32];
+                    float a[64];
+                    tmem_ld32_begin(tmem + lanes + c, r0);
+                    tmem_ld32_begin(tmem + lanes + c + 32, r1);
+                    us::tmem_ld_frag32_end(r0, *reinterpret_cast<float (*)[32]>(a));
+                    us::tmem_ld_frag32_end(r1, *reinterpret_cast<float (*)[32]>(a + 32));
                     if (mine && whole) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
+                        for (int j = 0; j < 64; j += 8)
                             *reinterpret_cast<uint4*>(out + c + j) =
                                 make_uint4(pack_out(a[j] * inv, a[j + 1] * inv), pack_out(a[j + 2] * inv, a[j + 3] * inv),
                                            pack_out(a[j + 4] * inv, a[j + 5] * inv), pack_out(a[j + 6] * inv, a[j + 7] * inv));
                     } else if (mine) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
+                        for (int j = 0; j < 64; j += 4)
                             __stcg(reinterpret_cast<float4*>(slot + 2 * kM) + (col0 + c + j) / 4 * kM + row,
                                    make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]));
                     }
@@ -361,10 +364,7 @@ attn_lat_kernel(const UsAttnLatParams p) {
         for (int it = 0; it < count;) {
             const int end = min(count, it + cur.tiles - cur.tile), last = cur.r.ctx + cur.r.n;
             Cur next = cur;
-            if (end < count) next.next_segment(p);
-            // the pages behind these, and the next segment's first ones, on their way
-            int ahead = page_of(cur, 32), at = 0;
-            const int after = end < count ? page_of(next, 0) : -1;
+            int ahead = page_of(cur, 32), after = -1, at = 0;              // the pages behind these, on their way
             for (int i = it; i < end; ++i, at += pieces) {
                 if (at && (at & 31) == 0) ids = ahead, ahead = page_of(cur, at + 32);
                 const int st = i % kStages, pos0 = (cur.tile + i - it) * kTile;
@@ -396,6 +396,10 @@ attn_lat_kernel(const UsAttnLatParams p) {
                         H.valid[st] = ok;
                         us::mbar_arrive(&H.full[st][0]);
                     }
+                }
+                if (i == it && end < count) {              // the next segment's first pages, too
+                    next.next_segment(p);
+                    after = page_of(next, 0);
                 }
             }
             it = end;
@@ -479,7 +483,6 @@ attn_lat_kernel(const UsAttnLatParams p) {
     __syncthreads();
     us::tc_fence_after();
     if (warp == kMmaWarp) us::tmem_dealloc(tmem, 512);
-    us::pdl_launch_dependents();
 }
 
 template <int DC>

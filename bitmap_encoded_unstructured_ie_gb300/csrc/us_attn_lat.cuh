@@ -54,6 +54,20 @@ US_DEV uint4 finite(uint4 x) {
     return make_uint4(x.x & ~not_finite(x.x), x.y & ~not_finite(x.y), x.z & ~not_finite(x.z), x.w & ~not_finite(x.w));
 }
 
+// us::tmem_ld32 in two parts: its values are there after us::tmem_ld_frag32_end
+US_DEV void tmem_ld32_begin(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
 // A partial state of ROWS rows of D columns in the workspace: the rows' references, their
 // sums, then the outputs in fours of columns, rows side by side.
 constexpr int slot_floats(int rows, int d) { return 2 * rows + rows * d; }
@@ -73,6 +87,7 @@ join_kernel(const P p, int blocks, int ctas) {
     constexpr int kVec = GROUPS > 1 ? 1 : D >= 256 ? 4 : D / 64, kAtOnce = GROUPS > 1 ? 4 : 8 / kVec, kLanes = kJoinThreads / GROUPS;
     __shared__ float held[GROUPS == 1 ? 1 : 6][kJoinThreads];
     us::pdl_wait();
+    us::pdl_launch_dependents();
     int which = (int)blockIdx.x / blocks;
     if constexpr (GROUPS > 1) {
         const int lane = threadIdx.x & 31;
@@ -86,10 +101,7 @@ join_kernel(const P p, int blocks, int ctas) {
                 }
         }
         which = at;
-        if (at < 0) {
-            us::pdl_launch_dependents();
-            return;
-        }
+        if (at < 0) return;
     }
     Part a = p.ws_parts[which];
     // (a workspace that two calls share at once may hold anything: nothing outside it and O is touched)
@@ -163,7 +175,6 @@ join_kernel(const P p, int blocks, int ctas) {
                     make_uint2(pack_out(y[k][0] * inv, y[k][1] * inv), pack_out(y[k][2] * inv, y[k][3] * inv));
         }
     }
-    us::pdl_launch_dependents();
 }
 
 inline int attn_ctas() { return us::num_sms() < kMaxCtas ? us::num_sms() : kMaxCtas; }

@@ -39,7 +39,7 @@ constexpr int kItems = 4;                         // keys, and values, of tiles 
 
 struct Header {
     uint64_t k_full[kItems], v_full[kItems], k_free[kItems], v_free[kItems];
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], pv_done[2];       // by stream
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], pv_done[2];    // by stream (weights: and half of the positions)
     uint32_t tmem;
 };
 
@@ -65,18 +65,6 @@ US_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, 
         : "memory");
 }
 
-US_DEV void tmem_ld32_begin(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
 US_DEV void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
@@ -108,7 +96,7 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
             us::mbar_init(&H.k_full[i], 1), us::mbar_init(&H.v_full[i], 1), us::mbar_init(&H.k_free[i], 1), us::mbar_init(&H.v_free[i], 1);
         for (int i = 0; i < 2; ++i) {
             us::mbar_init(&H.q_full[i], 1), us::mbar_init(&H.q_free[i], 1), us::mbar_init(&H.s_full[i], 1);
-            us::mbar_init(&H.p_full[i], 4), us::mbar_init(&H.pv_done[i], 1);
+            us::mbar_init(&H.p_full[i][0], 4), us::mbar_init(&H.p_full[i][1], 4), us::mbar_init(&H.pv_done[i], 1);
         }
         us::fence_mbar_init();
     }
@@ -119,6 +107,7 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
     __syncthreads();
     us::tc_fence_after();
     us::pdl_wait();
+    us::pdl_launch_dependents();                           // (the join's CTAs come now, and wait for this kernel's end)
 
     Work wk;
     Cur cur;
@@ -208,31 +197,6 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                         tmem_st16(o_tm + c, o);
                     }
                 }
-                uint64_t sums[2] = {};
-                auto weigh = [&](int c, const float (&v)[32]) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float x, y;
-                        unpair(fma2(pair(v[2 * k], v[2 * k + 1]), s2, neg), x, y);
-                        x = ex2(x), y = ex2(y);
-                        sums[k & 1] = add2(sums[k & 1], pair(x, y));
-                        w[k] = pack_half2(x, y);
-                    }
-                    tmem_st16(s_tm + c / 2, w);            // over scores that were read
-                };
-#pragma unroll 1
-                for (int c = 0; c < kTile; c += 64) {
-                    float v[32];
-                    finish(c, r0, v);
-                    tmem_ld32_begin(s_tm + c + 32, r1);
-                    weigh(c, v);
-                    finish(c + 32, r1, v);
-                    if (c == 0) tmem_ld32_begin(s_tm + 64, r0);
-                    weigh(c + 32, v);
-                }
-                l2 = add2(l2, add2(sums[0], sums[1]));
-                us::tmem_wait_st();
                 // Values where no position is count as 0, and what some rows do not see (positions
                 // behind the segment's first one) is made finite; the first stream that reads the
                 // tile sees to it.
@@ -255,9 +219,35 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                     }
                     us::fence_proxy_async_smem();
                 }
-                us::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) us::mbar_arrive(&H.p_full[st]);
+                uint64_t sums[2] = {};
+                auto weigh = [&](int c, const float (&v)[32]) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float x, y;
+                        unpair(fma2(pair(v[2 * k], v[2 * k + 1]), s2, neg), x, y);
+                        x = ex2(x), y = ex2(y);
+                        sums[k & 1] = add2(sums[k & 1], pair(x, y));
+                        w[k] = pack_half2(x, y);
+                    }
+                    tmem_st16(s_tm + c / 2, w);            // over scores that were read
+                };
+#pragma unroll 1
+                for (int c = 0; c < kTile; c += 64) {
+                    float v[32];
+                    finish(c, r0, v);
+                    tmem_ld32_begin(s_tm + c + 32, r1);
+                    weigh(c, v);
+                    finish(c + 32, r1, v);
+                    if (c == 0) tmem_ld32_begin(s_tm + 64, r0);
+                    weigh(c + 32, v);
+                    // (the product of the first half begins while the second is made)
+                    us::tmem_wait_st();
+                    us::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) us::mbar_arrive(&H.p_full[st][c >> 6]);
+                }
+                l2 = add2(l2, add2(sums[0], sums[1]));
             }
             // ---- the segment's end
             if (mine) wait(&H.pv_done[st], used - 1);
@@ -307,14 +297,15 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
             int segment[2] = {0, 0};                       // segments of each stream so far
             for (int it = 0; it < count;) {
                 const int end = min(count, it + cur.tiles - cur.tile), k0 = p.kv_off[cur.b];
-                for (int st = 0; st < 2; ++st) {
-                    if (stream_tiles(cur.r, cur.rb, st) <= cur.tile) continue;
+                auto queries = [&](int st) {
+                    if (stream_tiles(cur.r, cur.rb, st) <= cur.tile) return;
                     if (segment[st]) wait(&H.q_free[st], segment[st] - 1);
                     ++segment[st];
                     us::mbar_arrive_expect_tx(&H.q_full[st], kK * kBlock);
                     for (int c = 0; c < kK; ++c)
                         tma_load_3d(q_sm + (st * kK + c) * kBlock, &maps.q, 64 * c, cur.h, cur.r.row0 + cur.rb * kRows + st * kM, &H.q_full[st]);
-                }
+                };
+                queries(0), queries(1);                                // (in the order in which they are needed)
                 for (int i = it; i < end; ++i) {
                     const int row = k0 + (cur.tile + i - it) * kTile, item = i % kItems;
                     // block c of the tile, when the one whose place it takes is free
@@ -381,24 +372,28 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                     constexpr int st = decltype(ST)::value;
                     const int x = it + j, item = x % kItems;
                     if (first) wait(&H.v_full[item], x / kItems);
-                    wait(&H.p_full[st], used[st]++);
-                    us::tc_fence_after();
                     const uint32_t o = tmem + 256 + st * 128, w = tmem + st * 128;
                     const int v0 = (x * kT + kK) % kSlots;
                     const uint64_t rd = us::umma_smem_desc_mn_sw128(ring, kBlock), vd = rd + (uint64_t)(v0 * (kBlock >> 4));
-                    if (kV == 1 || v0 + 1 == kSlots) {     // one block of columns, or two that the ring's end parts
 #pragma unroll
-                        for (int c = 0; c < kV; ++c)
+                    for (int half = 0; half < 2; ++half) {
+                        wait(&H.p_full[st][half], used[st]);
+                        us::tc_fence_after();
+                        if (kV == 1 || v0 + 1 == kSlots) { // one block of columns, or two that the ring's end parts
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                us::umma_f16_ta(o + 64 * c, w + 8 * kk, (c ? rd : vd) + (uint64_t)(kk * 2048 >> 4),
-                                                us::umma_idesc_f16(kM, 64) | us::kUmmaBMajorMN, j > 0 || kk > 0);
-                    } else {
+                            for (int c = 0; c < kV; ++c)
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            us::umma_f16_ta(o, w + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), us::umma_idesc_f16(kM, 64 * kV) | us::kUmmaBMajorMN,
-                                            j > 0 || kk > 0);
+                                for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                                    us::umma_f16_ta(o + 64 * c, w + 8 * kk, (c ? rd : vd) + (uint64_t)(kk * 2048 >> 4),
+                                                    us::umma_idesc_f16(kM, 64) | us::kUmmaBMajorMN, j > 0 || kk > 0);
+                        } else {
+#pragma unroll
+                            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                                us::umma_f16_ta(o, w + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), us::umma_idesc_f16(kM, 64 * kV) | us::kUmmaBMajorMN,
+                                                j > 0 || kk > 0);
+                        }
                     }
+                    ++used[st];
                     if (last) us::umma_commit(&H.v_free[item]);
                     us::umma_commit(&H.pv_done[st]);
                 };
@@ -427,7 +422,6 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
     __syncthreads();
     us::tc_fence_after();
     if (warp == kMmaWarp) us::tmem_dealloc(tmem, 512);
-    us::pdl_launch_dependents();
 }
 
 // (64 values, heads, rows) of rows `ld` and heads `hs` elements apart, 128 rows of a head a copy
