@@ -229,9 +229,8 @@ struct Work {
 // requests, a scan over the lanes finds the one with the share's first tile (4500
 // cycles by a scan over the block with 64-bit divisions, at 16 row blocks of a chain
 // 15000).
-// (cta of `most`: of CTAs, or of clusters that share their work)
 template <int ROWS, int TILE, class P>
-US_DEV bool find_work(const P& p, Work& w, Cursor<ROWS, TILE>& at, int cta, int most) {
+US_DEV bool find_work(const P& p, Work& w, Cursor<ROWS, TILE>& at) {
     const int lane = threadIdx.x & 31;
     unsigned* status = blockIdx.x == 0 && threadIdx.x < 32 ? p.c.status : nullptr;
     const int each = (p.c.B + 31) / 32, b0 = lane * each, b1 = min(b0 + each, p.c.B);
@@ -258,11 +257,11 @@ US_DEV bool find_work(const P& p, Work& w, Cursor<ROWS, TILE>& at, int cta, int 
         if (lane >= d) incl += o;
     }
     const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
-    const int ctas = total < (int64_t)most ? (int)total : most;
-    if (cta >= ctas) return false;
+    const int ctas = total < (int64_t)gridDim.x ? (int)total : (int)gridDim.x;
+    if ((int)blockIdx.x >= ctas) return false;
     w.per = quotient(total, ctas);
     w.extra = (int)(total - w.per * ctas);
-    w.t0 = w.begin(cta), w.t1 = w.begin(cta + 1);
+    w.t0 = w.begin(blockIdx.x), w.t1 = w.begin(blockIdx.x + 1);
     int64_t x = w.t0 - (incl - mine);
     const bool here = x >= 0 && x < mine;
     int b = b0;
@@ -296,11 +295,6 @@ US_DEV bool find_work(const P& p, Work& w, Cursor<ROWS, TILE>& at, int cta, int 
     }
     at.tile = (int)x;
     return true;
-}
-
-template <int ROWS, int TILE, class P>
-US_DEV bool find_work(const P& p, Work& w, Cursor<ROWS, TILE>& at) {
-    return find_work(p, w, at, (int)blockIdx.x, (int)gridDim.x);
 }
 
 // Where a row's fp16 outputs go: D values at row r of row block rb, head h.

@@ -137,18 +137,29 @@ attn_lat_kernel(const UsAttnLatParams p) {
         const uint32_t lanes = (uint32_t)warp * 32u << 16;
         const float scale = p.scale * 1.4426950408889634f;
         if (threadIdx.x == 0) p.ws_parts[blockIdx.x].rows = 0;     // until a shared segment begins here
-        // A segment's Q on its way to shared memory: two threads a row
+        // A segment's Q on its way to shared memory: eight threads have 128 bytes of a row, rows
+        // 16 k + threadIdx.x / 8; before that, when the segment before it begins, to L2
+        auto q_row = [&](const Cur& at, int r) {
+            const int rr = at.rb * kM + r, i = (int)((unsigned)rr / (unsigned)G), h = rr - i * G;
+            return rr < at.r.n * G ? p.Q + (int64_t)(at.r.row0 + i) * p.ldq + (int64_t)h * Sh::kW : nullptr;
+        };
         auto request_q = [&](const Cur& at) {
-            const int r = threadIdx.x >> 1, rr = at.rb * kM + r;
-            if (rr < at.r.n * G) {
-                const int i = (int)((unsigned)rr / (unsigned)G), h = rr - i * G;
-                const uint16_t* src = p.Q + (int64_t)(at.r.row0 + i) * p.ldq + (int64_t)h * Sh::kW;
-                const uint32_t to = us::smem_addr(q_sm) + r * 128;
-#pragma unroll 9
-                for (int k = threadIdx.x & 1; k < Sh::kW / 8; k += 2)
-                    cp_async16(to + (k >> 3) * kBlock + (((k & 7) ^ (r & 7)) << 4), src + 8 * k);
+            const int r0 = threadIdx.x >> 3, chunk = threadIdx.x & 7;
+            const uint32_t to = us::smem_addr(q_sm) + r0 * 128 + ((chunk ^ (r0 & 7)) << 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint16_t* src = q_row(at, 16 * k + r0);
+                if (!src) break;
+#pragma unroll
+                for (int c = 0; c < Sh::kC; ++c) cp_async16(to + c * kBlock + k * 2048, src + 64 * c + 8 * chunk);
             }
             cp_async_commit();
+        };
+        auto foresee_q = [&](const Cur& at) {
+            const uint16_t* src = q_row(at, threadIdx.x >> 1);
+            if (!src) return;
+#pragma unroll
+            for (int c = threadIdx.x & 1; c < Sh::kC; c += 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64 * c));
         };
         auto hand_over_q = [&]() {
             cp_async_wait<0>();
@@ -163,7 +174,10 @@ attn_lat_kernel(const UsAttnLatParams p) {
             const int rows = min(kM, cur.r.n * G - cur.rb * kM);
             if (it == 0) hand_over_q();
             Cur next = cur;
-            if (end < count) next.next_segment(p);
+            if (end < count) {
+                next.next_segment(p);
+                foresee_q(next);
+            }
             // what the lane's rows see of the call's own positions: their masks, or in a chain how many
             uint64_t own_seen[2];
 #pragma unroll
@@ -320,28 +334,53 @@ attn_lat_kernel(const UsAttnLatParams p) {
                 }
                 const bool mine = row < rows && (Sh::kHalves == 2 || lane < 16);
                 const int col0 = lane & 16 ? 256 : 0;
-                uint16_t* out = mine ? out_row<kM>(p, cur.r.row0, 0, cur.rb, row, DC) + col0 : nullptr;
-#pragma unroll 1
-                for (int c = 0; c < 256; c += 64) {
-                    uint32_t r0[32], r1[32];
-                    float a[64];
-                    tmem_ld32_begin(tmem + lanes + c, r0);
-                    tmem_ld32_begin(tmem + lanes + c + 32, r1);
-                    us::tmem_ld_frag32_end(r0, *reinterpret_cast<float (*)[32]>(a));
-                    us::tmem_ld_frag32_end(r1, *reinterpret_cast<float (*)[32]>(a + 32));
-                    if (mine && whole) {
+                if (whole) {
+                    // Through the weights' place (the warp's 16 rows of 128 bytes, which no product
+                    // reads any more), so that 64 bytes of a row are written at once: 32 columns of
+                    // each half, which the row's two lanes hold.
+                    const int at = lane & 15, chunk = lane & 7, half = chunk >> 2;
+                    uint8_t* st = p_sm + wrow * 128;
+                    uint16_t* to[4];                       // of the rows that the lane writes
 #pragma unroll
-                        for (int j = 0; j < 64; j += 8)
-                            *reinterpret_cast<uint4*>(out + c + j) =
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = wrow + 4 * k + (lane >> 3);
+                        to[k] = r < rows && half < Sh::kHalves ? out_row<kM>(p, cur.r.row0, 0, cur.rb, r, DC) + 256 * half + 8 * (chunk & 3) : nullptr;
+                    }
+#pragma unroll 2
+                    for (int c = 0; c < 256; c += 32) {
+                        float a[32];
+                        us::tmem_ld32(tmem + lanes + c, a);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            *reinterpret_cast<uint4*>(st + at * 128 + ((((lane >> 4) * 4 + j / 8) ^ (at & 7)) << 4)) =
                                 make_uint4(pack_out(a[j] * inv, a[j + 1] * inv), pack_out(a[j + 2] * inv, a[j + 3] * inv),
                                            pack_out(a[j + 4] * inv, a[j + 5] * inv), pack_out(a[j + 6] * inv, a[j + 7] * inv));
-                    } else if (mine) {
+                        __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 64; j += 4)
-                            __stcg(reinterpret_cast<float4*>(slot + 2 * kM) + (col0 + c + j) / 4 * kM + row,
-                                   make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]));
+                        for (int k = 0; k < 4; ++k) {
+                            const int r = 4 * k + (lane >> 3);
+                            const uint4 y = *reinterpret_cast<const uint4*>(st + r * 128 + ((chunk ^ (r & 7)) << 4));
+                            if (to[k]) *reinterpret_cast<uint4*>(to[k] + c) = y;
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < 256; c += 64) {
+                        uint32_t r0[32], r1[32];
+                        float a[64];
+                        tmem_ld32_begin(tmem + lanes + c, r0);
+                        tmem_ld32_begin(tmem + lanes + c + 32, r1);
+                        us::tmem_ld_frag32_end(r0, *reinterpret_cast<float (*)[32]>(a));
+                        us::tmem_ld_frag32_end(r1, *reinterpret_cast<float (*)[32]>(a + 32));
+                        if (mine) {
+#pragma unroll
+                            for (int j = 0; j < 64; j += 4)
+                                __stcg(reinterpret_cast<float4*>(slot + 2 * kM) + (col0 + c + j) / 4 * kM + row,
+                                       make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]));
+                        }
+                        __syncwarp();
+                    }
                 }
             }
             if (!whole && part.first == (int)blockIdx.x && threadIdx.x == 0) p.ws_parts[blockIdx.x] = part;
