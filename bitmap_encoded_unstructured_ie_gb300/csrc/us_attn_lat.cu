@@ -41,7 +41,7 @@ constexpr int kBlock = 64 * 128;                  // bytes of 64 rows of 64 valu
 constexpr int kMaxStages = 4;
 
 struct Header {
-    uint64_t full[kMaxStages][3], free[kMaxStages][3], s_full[2], p_full, pv_done, q_full;
+    uint64_t full[kMaxStages][3], free[kMaxStages][3], s_full[2], p_full, pv_done, q_full, q_free;
     uint64_t valid[kMaxStages];                   // which of the tile's positions exist
     uint32_t tmem;
 };
@@ -64,6 +64,11 @@ struct Shape {
 // that it was set up for).
 US_DEV void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(us::smem_addr(bar)) : "memory");
+}
+
+// 16 bytes of global memory, or of zeros, to shared memory
+US_DEV void cp_async16_if(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 // 16 lanes x 64 columns in fragment order: lane (g, c) gets rows g (v[4k], v[4k + 1])
@@ -111,7 +116,7 @@ attn_lat_kernel(const UsAttnLatParams p) {
             for (int j = 0; j < Sh::kParts; ++j)               // (part 0: `valid`, too)
                 us::mbar_init(&H.full[i][j], 32 * kLoadWarps + (j == 0)), us::mbar_init(&H.free[i][j], 1);
         for (int i = 0; i < 2; ++i) us::mbar_init(&H.s_full[i], 1);
-        us::mbar_init(&H.p_full, kSoftWarps), us::mbar_init(&H.pv_done, 1), us::mbar_init(&H.q_full, kSoftWarps);
+        us::mbar_init(&H.p_full, kSoftWarps), us::mbar_init(&H.pv_done, 1), us::mbar_init(&H.q_full, 32 * kLoadWarps), us::mbar_init(&H.q_free, 1);
         us::fence_mbar_init();
     }
     if (warp == kMmaWarp) us::tmem_alloc(&H.tmem, 512);
@@ -131,60 +136,48 @@ attn_lat_kernel(const UsAttnLatParams p) {
         if (!failed && !spin(bar, (uint32_t)use & 1u, p.c.status)) failed = true;
     };
 
+    // A segment's Q on its way to shared memory, by 128 threads: eight have 128 bytes of a row, rows
+    // 16 k + t / 8.  The first segment's by the softmax warps, the others' by the copying ones.
+    auto q_row = [&](const Cur& at, int r) {
+        const int rr = at.rb * kM + r, i = (int)((unsigned)rr / (unsigned)G), h = rr - i * G;
+        return rr < at.r.n * G ? p.Q + (int64_t)(at.r.row0 + i) * p.ldq + (int64_t)h * Sh::kW : nullptr;
+    };
+    auto request_q = [&](const Cur& at, int t) {
+        const int r0 = t >> 3, chunk = t & 7;
+        const uint32_t to = us::smem_addr(q_sm) + r0 * 128 + ((chunk ^ (r0 & 7)) << 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint16_t* src = q_row(at, 16 * k + r0);
+            if (!src) break;
+#pragma unroll
+            for (int c = 0; c < Sh::kC; ++c) cp_async16(to + c * kBlock + k * 2048, src + 64 * c + 8 * chunk);
+        }
+        cp_async_arrive(&H.q_full);
+    };
+
     if (warp < kSoftWarps) {
         // ----------------------------------------------------------- softmax
         const int g = lane >> 2, c2 = 2 * (lane & 3), wrow = 16 * warp;
         const uint32_t lanes = (uint32_t)warp * 32u << 16;
         const float scale = p.scale * 1.4426950408889634f;
         if (threadIdx.x == 0) p.ws_parts[blockIdx.x].rows = 0;     // until a shared segment begins here
-        // A segment's Q on its way to shared memory: eight threads have 128 bytes of a row, rows
-        // 16 k + threadIdx.x / 8; before that, when the segment before it begins, to L2
-        auto q_row = [&](const Cur& at, int r) {
-            const int rr = at.rb * kM + r, i = (int)((unsigned)rr / (unsigned)G), h = rr - i * G;
-            return rr < at.r.n * G ? p.Q + (int64_t)(at.r.row0 + i) * p.ldq + (int64_t)h * Sh::kW : nullptr;
-        };
-        auto request_q = [&](const Cur& at) {
-            const int r0 = threadIdx.x >> 3, chunk = threadIdx.x & 7;
-            const uint32_t to = us::smem_addr(q_sm) + r0 * 128 + ((chunk ^ (r0 & 7)) << 4);
+        // what the lane's rows see of the call's own positions: their masks, or in a chain how many
+        auto seen_of = [&](const Cur& at, uint64_t (&seen)[2]) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint16_t* src = q_row(at, 16 * k + r0);
-                if (!src) break;
-#pragma unroll
-                for (int c = 0; c < Sh::kC; ++c) cp_async16(to + c * kBlock + k * 2048, src + 64 * c + 8 * chunk);
+            for (int q = 0; q < 2; ++q) {
+                const int rr = at.rb * kM + wrow + 8 * q + g, tok = (int)((unsigned)rr / (unsigned)G);
+                seen[q] = rr >= at.r.n * G ? 0 : p.mask ? p.mask[at.r.row0 + tok] & (~0ull >> (64 - at.r.n)) : (uint64_t)(tok + 1);
             }
-            cp_async_commit();
         };
-        auto foresee_q = [&](const Cur& at) {
-            const uint16_t* src = q_row(at, threadIdx.x >> 1);
-            if (!src) return;
-#pragma unroll
-            for (int c = threadIdx.x & 1; c < Sh::kC; c += 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64 * c));
-        };
-        auto hand_over_q = [&]() {
-            cp_async_wait<0>();
-            us::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) us::mbar_arrive(&H.q_full);
-        };
-        if (count) request_q(cur);
+        uint64_t own_seen[2] = {};
+        if (count) {
+            request_q(cur, threadIdx.x);
+            seen_of(cur, own_seen);
+        }
         for (int it = 0; it < count;) {
             // ---- a segment, or this CTA's part of it: tiles it .. end - 1
             const int end = min(count, it + cur.tiles - cur.tile), tile0 = cur.tile;
             const int rows = min(kM, cur.r.n * G - cur.rb * kM);
-            if (it == 0) hand_over_q();
-            Cur next = cur;
-            if (end < count) {
-                next.next_segment(p);
-                foresee_q(next);
-            }
-            // what the lane's rows see of the call's own positions: their masks, or in a chain how many
-            uint64_t own_seen[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int r = wrow + 8 * q + g, tok = (int)((unsigned)(cur.rb * kM + r) / (unsigned)G);
-                own_seen[q] = r >= rows ? 0 : p.mask ? p.mask[cur.r.row0 + tok] & (~0ull >> (64 - cur.r.n)) : (uint64_t)(tok + 1);
-            }
             // positions that a row sees among 64 from `base` behind the context
             auto seen64 = [&](int base, uint64_t row) {
                 if (base <= -64) return ~0ull;
@@ -205,7 +198,6 @@ attn_lat_kernel(const UsAttnLatParams p) {
                 wait(&H.full[st][0], i / kStages);         // (the scores came from it: for its positions)
                 wait(&H.s_full[i & 1], i >> 1);
                 us::tc_fence_after();
-                if (i == end - 1 && end < count) request_q(next);  // nothing reads this segment's Q any more
                 const uint64_t ok = H.valid[st];
                 const int base = (tile0 + i - it) * kTile - cur.r.ctx;
                 if (wrow < rows) {
@@ -281,24 +273,20 @@ attn_lat_kernel(const UsAttnLatParams p) {
                 }
                 // (a warp without rows must not arrive for this tile while the last one's phase is open)
                 if (wrow >= rows && i > it) wait(&H.pv_done, i - 1);
-                // What lies where no position is counts as 0, and what some rows do not see is made
-                // finite (drafts, or in a chain what is behind the segment's first token).
-                const int all_see = (p.mask ? (cur.r.n > 1 ? 0 : 1) : cur.rb * kM / G + 1) - base;
-                if (ok != ~0ull || all_see < kTile) {
-                    // a thread's 16 bytes of every 16th row of a block
-                    uint8_t* x = x_sm + st * Sh::kOperand + threadIdx.x * 16;
-                    const int r0 = threadIdx.x >> 3;
+                // What some rows do not see is made finite (drafts, or in a chain what is behind the
+                // segment's first token); what is not there was copied as zeros.
+                const int behind = cur.r.n - base, all_see = max(0, (p.mask ? (cur.r.n > 1 ? 0 : 1) : cur.rb * kM / G + 1) - base);
+                if (all_see < min(kTile, behind)) {
+                    // eight threads have 128 bytes of a row, each row's blocks at once
+                    uint8_t* x = x_sm + st * Sh::kOperand + (threadIdx.x & 7) * 16;
 #pragma unroll 1
-                    for (int g = 0; g < 4; ++g) {
-                        const int r = r0 + 16 * g;
-                        const bool there = (ok >> r) & 1ull;
-                        if (there && r < all_see) continue;
+                    for (int r = all_see + (threadIdx.x >> 3); r < min(kTile, behind); r += 16) {
+                        uint4 y[DC / 64];
 #pragma unroll
-                        for (int c = 0; c < DC / 64; ++c) {
-                            uint4* at = reinterpret_cast<uint4*>(x + c * kBlock + g * 2048);
-                            if (!there) *at = make_uint4(0, 0, 0, 0);
-                            else if (const uint4 y = *at; !all_finite(y)) *at = finite(y);
-                        }
+                        for (int c = 0; c < DC / 64; ++c) y[c] = *reinterpret_cast<const uint4*>(x + c * kBlock + r * 128);
+#pragma unroll
+                        for (int c = 0; c < DC / 64; ++c)
+                            if (!all_finite(y[c])) *reinterpret_cast<uint4*>(x + c * kBlock + r * 128) = finite(y[c]);
                     }
                 }
                 us::fence_proxy_async_smem();
@@ -306,87 +294,98 @@ attn_lat_kernel(const UsAttnLatParams p) {
                 __syncwarp();
                 if (lane == 0) us::mbar_arrive(&H.p_full);
             }
-            // ---- the segment's end; the next one's first scores are made meanwhile
-            if (end < count) hand_over_q();
+            // ---- the segment's end: what is to be known for it while the last product runs
+            const bool whole = tile0 == 0 && end - it == cur.tiles;
+            Part part = {};
+            if (!whole) part = wk.sharers(wk.t0 + it - tile0, wk.t0 + it - tile0 + cur.tiles, cur, rows);
+            float l[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float a, b;
+                unpair(l2[q], a, b);
+                a += b;
+                a += __shfl_xor_sync(0xffffffffu, a, 1);
+                l[q] = a + __shfl_xor_sync(0xffffffffu, a, 2);
+            }
+            const int src = 4 * (lane & 7), row = wrow + (lane & 15);
+            const float l0 = __shfl_sync(0xffffffffu, l[0], src), l1 = __shfl_sync(0xffffffffu, l[1], src);
+            const float ref0 = __shfl_sync(0xffffffffu, R[0], src), ref1 = __shfl_sync(0xffffffffu, R[1], src);
+            const float sum = lane & 8 ? l1 : l0, ref = lane & 8 ? ref1 : ref0, inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int chunk = lane & 7, half = chunk >> 2;
+            uint16_t* to[4];                               // of the rows that the lane writes
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = wrow + 4 * k + (lane >> 3);
+                to[k] = whole && r < rows && half < Sh::kHalves ? out_row<kM>(p, cur.r.row0, 0, cur.rb, r, DC) + 256 * half + 8 * (chunk & 3) : nullptr;
+            }
+            float* slot = p.ws_slots + part.slot(blockIdx.x) * Sh::kSlotFloats;
+            if (!whole && wrow < rows && lane < 16) {
+                __stcg(slot + row, ref);
+                __stcg(slot + kM + row, sum);
+            }
+            if (!whole && part.first == (int)blockIdx.x && threadIdx.x == 0) p.ws_parts[blockIdx.x] = part;
+            if (end < count) {
+                cur.next_segment(p);
+                seen_of(cur, own_seen);
+            }
             wait(&H.pv_done, end - 1);
             us::tc_fence_after();
-            const int64_t s0 = wk.t0 + it - tile0;
-            const Part part = wk.sharers(s0, s0 + cur.tiles, cur, rows);
-            const bool whole = part.first == part.last;
             if (wrow < rows) {
-                float l[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float a, b;
-                    unpair(l2[q], a, b);
-                    a += b;
-                    a += __shfl_xor_sync(0xffffffffu, a, 1);
-                    l[q] = a + __shfl_xor_sync(0xffffffffu, a, 2);
-                }
-                const int src = 4 * (lane & 7), row = wrow + (lane & 15);
-                const float l0 = __shfl_sync(0xffffffffu, l[0], src), l1 = __shfl_sync(0xffffffffu, l[1], src);
-                const float r0 = __shfl_sync(0xffffffffu, R[0], src), r1 = __shfl_sync(0xffffffffu, R[1], src);
-                const float sum = lane & 8 ? l1 : l0, ref = lane & 8 ? r1 : r0, inv = sum == 0.f ? 0.f : 1.f / sum;
-                float* slot = p.ws_slots + part.slot(blockIdx.x) * Sh::kSlotFloats;
-                if (!whole && lane < 16) {
-                    __stcg(slot + row, ref);
-                    __stcg(slot + kM + row, sum);
-                }
                 const bool mine = row < rows && (Sh::kHalves == 2 || lane < 16);
                 const int col0 = lane & 16 ? 256 : 0;
+                auto load_outputs = [&](int c, float (&a)[4][32]) {        // (one wait for 128 columns)
+                    uint32_t r[4][32];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) tmem_ld32_begin(tmem + lanes + c + 32 * u, r[u]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) us::tmem_ld_frag32_end(r[u], a[u]);
+                };
                 if (whole) {
                     // Through the weights' place (the warp's 16 rows of 128 bytes, which no product
                     // reads any more), so that 64 bytes of a row are written at once: 32 columns of
                     // each half, which the row's two lanes hold.
-                    const int at = lane & 15, chunk = lane & 7, half = chunk >> 2;
+                    const int at = lane & 15;
                     uint8_t* st = p_sm + wrow * 128;
-                    uint16_t* to[4];                       // of the rows that the lane writes
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 256; c0 += 128) {
+                        float a[4][32];
+                        load_outputs(c0, a);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = wrow + 4 * k + (lane >> 3);
-                        to[k] = r < rows && half < Sh::kHalves ? out_row<kM>(p, cur.r.row0, 0, cur.rb, r, DC) + 256 * half + 8 * (chunk & 3) : nullptr;
-                    }
-#pragma unroll 2
-                    for (int c = 0; c < 256; c += 32) {
-                        float a[32];
-                        us::tmem_ld32(tmem + lanes + c, a);
+                        for (int u = 0; u < 4; ++u) {
+                            const float (&v)[32] = a[u];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            *reinterpret_cast<uint4*>(st + at * 128 + ((((lane >> 4) * 4 + j / 8) ^ (at & 7)) << 4)) =
-                                make_uint4(pack_out(a[j] * inv, a[j + 1] * inv), pack_out(a[j + 2] * inv, a[j + 3] * inv),
-                                           pack_out(a[j + 4] * inv, a[j + 5] * inv), pack_out(a[j + 6] * inv, a[j + 7] * inv));
-                        __syncwarp();
+                            for (int j = 0; j < 32; j += 8)
+                                *reinterpret_cast<uint4*>(st + at * 128 + ((((lane >> 4) * 4 + j / 8) ^ (at & 7)) << 4)) =
+                                    make_uint4(pack_out(v[j] * inv, v[j + 1] * inv), pack_out(v[j + 2] * inv, v[j + 3] * inv),
+                                               pack_out(v[j + 4] * inv, v[j + 5] * inv), pack_out(v[j + 6] * inv, v[j + 7] * inv));
+                            __syncwarp();
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int r = 4 * k + (lane >> 3);
-                            const uint4 y = *reinterpret_cast<const uint4*>(st + r * 128 + ((chunk ^ (r & 7)) << 4));
-                            if (to[k]) *reinterpret_cast<uint4*>(to[k] + c) = y;
+                            for (int k = 0; k < 4; ++k) {
+                                const int r = 4 * k + (lane >> 3);
+                                const uint4 y = *reinterpret_cast<const uint4*>(st + r * 128 + ((chunk ^ (r & 7)) << 4));
+                                if (to[k]) *reinterpret_cast<uint4*>(to[k] + c0 + 32 * u) = y;
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
                     }
                 } else {
 #pragma unroll 1
-                    for (int c = 0; c < 256; c += 64) {
-                        uint32_t r0[32], r1[32];
-                        float a[64];
-                        tmem_ld32_begin(tmem + lanes + c, r0);
-                        tmem_ld32_begin(tmem + lanes + c + 32, r1);
-                        us::tmem_ld_frag32_end(r0, *reinterpret_cast<float (*)[32]>(a));
-                        us::tmem_ld_frag32_end(r1, *reinterpret_cast<float (*)[32]>(a + 32));
+                    for (int c0 = 0; c0 < 256; c0 += 128) {
+                        float a[4][32];
+                        load_outputs(c0, a);
                         if (mine) {
 #pragma unroll
-                            for (int j = 0; j < 64; j += 4)
-                                __stcg(reinterpret_cast<float4*>(slot + 2 * kM) + (col0 + c + j) / 4 * kM + row,
-                                       make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]));
+                            for (int j = 0; j < 128; j += 4)
+                                __stcg(reinterpret_cast<float4*>(slot + 2 * kM) + (col0 + c0 + j) / 4 * kM + row,
+                                       make_float4(a[j / 32][j % 32], a[j / 32][j % 32 + 1], a[j / 32][j % 32 + 2], a[j / 32][j % 32 + 3]));
                         }
                         __syncwarp();
                     }
                 }
             }
-            if (!whole && part.first == (int)blockIdx.x && threadIdx.x == 0) p.ws_parts[blockIdx.x] = part;
             it = end;
-            cur = next;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------- copies
         // Eight lanes have 128 bytes of a row; the warp's rows are 16 k + 4 w + lane / 8, k < 4.
@@ -399,7 +398,7 @@ attn_lat_kernel(const UsAttnLatParams p) {
             const int pos = c.tile * kTile + ((first + lane) << shift);
             return pos < c.r.ctx + c.r.n ? p.c.table[(int64_t)c.b * p.c.max_pages + (pos >> p.c.page_shift)] : -1;
         };
-        int ids = count ? page_of(cur, 0) : -1;
+        int ids = count ? page_of(cur, 0) : -1, segment = 0;
         for (int it = 0; it < count;) {
             const int end = min(count, it + cur.tiles - cur.tile), last = cur.r.ctx + cur.r.n;
             Cur next = cur;
@@ -418,7 +417,8 @@ attn_lat_kernel(const UsAttnLatParams p) {
                     if (here > 0 && !good) us::set_status(p.c.status, US_ERR_CORRUPT);
                     if (here > 0 && good) ok |= ((1ull << here) - 1ull) << (16 * k);
                     has[k] = (ok >> (16 * k + row0)) & 1ull;
-                    src[k] = p.rows + (((int64_t)id << p.c.page_shift) + (pos & ((1 << p.c.page_shift) - 1))) * Sh::kW + 8 * chunk;
+                    // (a row that is not there is copied as zeros: its weight is 0, which times anything stale might be NaN)
+                    src[k] = p.rows + (has[k] ? (((int64_t)id << p.c.page_shift) + (pos & ((1 << p.c.page_shift) - 1))) * Sh::kW : 0) + 8 * chunk;
                 }
                 const uint32_t to = to0 + st * Sh::kOperand;
 #pragma unroll
@@ -429,16 +429,25 @@ attn_lat_kernel(const UsAttnLatParams p) {
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
                         for (int c = 0; c < (j ? 4 : 1); ++c)
-                            if (has[k]) cp_async16(to + (4 * part + c) * kBlock + k * 2048, src[k] + (4 * part + c) * 64);
+                            cp_async16_if(to + (4 * part + c) * kBlock + k * 2048, src[k] + (4 * part + c) * 64, has[k]);
                     cp_async_arrive(&H.full[st][part]);
                     if (j == 1 && w == 0 && lane == 0) {   // (part 0 was freed by those who read it)
                         H.valid[st] = ok;
                         us::mbar_arrive(&H.full[st][0]);
                     }
                 }
-                if (i == it && end < count) {              // the next segment's first pages, too
+                if (i > it) continue;
+                if (segment) {                             // Q when the last segment's scores are made
+                    wait(&H.q_free, segment - 1);
+                    request_q(cur, threadIdx.x - 32 * kSoftWarps);
+                }
+                ++segment;
+                if (end < count) {                         // the next segment's first pages, and its Q to L2
                     next.next_segment(p);
                     after = page_of(next, 0);
+                    if (const uint16_t* q = q_row(next, 16 * w + (lane >> 1)))
+#pragma unroll
+                        for (int c = lane & 1; c < Sh::kC; c += 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64 * c));
                 }
             }
             it = end;
@@ -452,7 +461,7 @@ attn_lat_kernel(const UsAttnLatParams p) {
             for (int it = 0; it < count && !failed; ++segment) {
                 const int end = min(count, it + cur.tiles - cur.tile);
                 wait(&H.q_full, segment);
-                us::tc_fence_after();
+                us::fence_proxy_async_smem();              // (written by plain copies, as the tiles' rows)
                 const uint64_t qd = us::umma_smem_desc_sw128(q_sm), pd = us::umma_smem_desc_sw128(p_sm);
                 int s = it, sp = 0, o = it;                // the next tile's scores (from part sp on), the next one's outputs
                 uint64_t since = 0;
@@ -482,7 +491,8 @@ attn_lat_kernel(const UsAttnLatParams p) {
                         }
                         if (++sp == Sh::kParts) {
                             us::umma_commit(&H.s_full[s & 1]);
-                            ++s, sp = 0;
+                            if (++s == end && end < count) us::umma_commit(&H.q_free);
+                            sp = 0;
                         }
                         idle = 0;
                     } else if (o < s && us::mbar_test(&H.p_full, (uint32_t)o & 1u)) {
