@@ -65,6 +65,16 @@ US_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, 
         : "memory");
 }
 
+// Of two lanes `apart`, the lower one's b and the upper one's a change places.
+US_DEV void swap_quads(uint4& a, uint4& b, int apart) {
+    const bool up = threadIdx.x & apart;
+    auto move = [&](uint32_t& x, uint32_t& y) {
+        const uint32_t z = __shfl_xor_sync(0xffffffffu, up ? x : y, apart);
+        if (up) x = z;
+        else y = z;
+    };
+    move(a.x, b.x), move(a.y, b.y), move(a.z, b.z), move(a.w, b.w);
+}
 US_DEV void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
@@ -249,47 +259,55 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                 }
                 l2 = add2(l2, add2(sums[0], sums[1]));
             }
-            // ---- the segment's end
+            // ---- the segment's end: what is to be known for it while the last product runs
+            const bool whole = tile0 == 0 && end - it == cur.tiles;
+            Part part = {};
+            if (!whole) part = wk.sharers(wk.t0 + it - tile0, wk.t0 + it - tile0 + cur.tiles, cur, rows);
+            const int srow = st * kM + row, wrow = srow & ~31;         // of the segment
+            float a, b;
+            unpair(l2, a, b);
+            const float sum = a + b, inv = sum == 0.f ? 0.f : 1.f / sum;
+            float* slot = p.ws_slots + part.slot(blockIdx.x) * Sh::kSlotFloats;
+            if (!whole && wrow < rows) {
+                __stcg(slot + srow, R);
+                __stcg(slot + kRows + srow, sum);
+            }
+            if (!whole && part.first == (int)blockIdx.x && threadIdx.x == 0) p.ws_parts[blockIdx.x] = part;
+            // (the row that the lane's quad begins with, and the lane's piece of each of the quad's rows)
+            uint16_t* out = p.O + (int64_t)(cur.r.row0 + cur.rb * kRows + (srow & ~3)) * p.ldo + (int64_t)cur.h * D + 8 * (lane & 3);
+            const int left = rows - (srow & ~3);
+            if (end < count) cur.next_segment(p);
             if (mine) wait(&H.pv_done[st], used - 1);
             us::tc_fence_after();
-            const int64_t s0 = wk.t0 + it - tile0;
-            const Part part = wk.sharers(s0, s0 + cur.tiles, cur, rows);
-            const bool whole = part.first == part.last;
-            const int srow = st * kM + row;                // of the segment
-            if (st * kM + (row & ~31) < rows) {
-                float a, b;
-                unpair(l2, a, b);
-                const float sum = a + b, inv = sum == 0.f ? 0.f : 1.f / sum;
-                float* slot = p.ws_slots + part.slot(blockIdx.x) * Sh::kSlotFloats;
-                if (!whole) {
-                    __stcg(slot + srow, R);
-                    __stcg(slot + kRows + srow, sum);
-                }
-                uint16_t* out = srow < rows ? out_row<kRows>(p, cur.r.row0, cur.h, cur.rb, srow, D) : nullptr;
+            if (wrow < rows) {
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float y[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) y[k] = 0.f;
                     if (mine) us::tmem_ld32(o_tm + c, y);
-                    if (!whole) {
+                    if (whole) {
+                        // four lanes exchange their 64 bytes each of four rows: 64 bytes of a row are written at once
+                        uint4 v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = make_uint4(pack_out(y[8 * k] * inv, y[8 * k + 1] * inv), pack_out(y[8 * k + 2] * inv, y[8 * k + 3] * inv),
+                                              pack_out(y[8 * k + 4] * inv, y[8 * k + 5] * inv), pack_out(y[8 * k + 6] * inv, y[8 * k + 7] * inv));
+                        swap_quads(v[0], v[1], 1), swap_quads(v[2], v[3], 1);
+                        swap_quads(v[0], v[2], 2), swap_quads(v[1], v[3], 2);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < left) *reinterpret_cast<uint4*>(out + k * p.ldo + c) = v[k];
+                    } else {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
                             __stcg(reinterpret_cast<float4*>(slot + 2 * kRows) + (c + k) / 4 * kRows + srow,
                                    make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]));
-                    } else if (srow < rows) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8)
-                            *reinterpret_cast<uint4*>(out + c + k) =
-                                make_uint4(pack_out(y[k] * inv, y[k + 1] * inv), pack_out(y[k + 2] * inv, y[k + 3] * inv),
-                                           pack_out(y[k + 4] * inv, y[k + 5] * inv), pack_out(y[k + 6] * inv, y[k + 7] * inv));
                     }
                     __syncwarp();
                 }
             }
-            if (!whole && part.first == (int)blockIdx.x && threadIdx.x == 0) p.ws_parts[blockIdx.x] = part;
             it = end;
-            if (it < count) cur.next_segment(p);
         }
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------- copies
@@ -305,7 +323,7 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                     for (int c = 0; c < kK; ++c)
                         tma_load_3d(q_sm + (st * kK + c) * kBlock, &maps.q, 64 * c, cur.h, cur.r.row0 + cur.rb * kRows + st * kM, &H.q_full[st]);
                 };
-                queries(0), queries(1);                                // (in the order in which they are needed)
+                queries(0);                                // (all in the order in which the MMAs need it)
                 for (int i = it; i < end; ++i) {
                     const int row = k0 + (cur.tile + i - it) * kTile, item = i % kItems;
                     // block c of the tile, when the one whose place it takes is free
@@ -322,6 +340,7 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                         if (c < kK - 1) tma_load_3d(to, &maps.k, 64 * c, cur.h, row, bar);
                         else tma_load_3d(to, &maps.r, 0, 0, row, bar);
                     }
+                    if (i == it) queries(1);
                     bar = &H.v_full[item];
 #pragma unroll 1
                     for (int c = 0; c < kV; ++c) {
@@ -341,73 +360,86 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
         // --------------------------------------------------------------- MMA
         if (us::elect_one()) {
             int segment[2] = {0, 0}, used[2] = {0, 0};     // segments and tiles of each stream so far
-            for (int it = 0; it < count && !failed;) {
-                const int end = min(count, it + cur.tiles - cur.tile), n = end - it;
-                const int mine0 = min(n, max(0, stream_tiles(cur.r, cur.rb, 0) - cur.tile));
-                const int mine1 = min(n, max(0, stream_tiles(cur.r, cur.rb, 1) - cur.tile));
-                // Scores of tile j for stream ST, which has `mine` of them; first: nothing has waited for the
-                // tile yet; last: nothing after them reads its keys.  (A wait for what is there takes some
-                // 150 cycles beside the softmax: there are no more of them than have to be.)
-                auto qk = [&](auto ST, int j, int mine, bool first, bool last) {
-                    constexpr int st = decltype(ST)::value;
-                    constexpr uint32_t id = us::umma_idesc_f16(kM, kTile);
-                    const int x = it + j, item = x % kItems;
-                    if (j == 0) wait(&H.q_full[st], segment[st]++);
-                    if (first) wait(&H.k_full[item], x / kItems);
+            // What there is to do with a tile (they are asked for one after the other): which streams
+            // read it, whether it is the first of its segment here, and a stream's last one.
+            constexpr unsigned kUse0 = 1, kUse1 = 2, kFirst = 4, kLast0 = 8, kLast1 = 16;
+            int it = 0, end = 0, mine0 = 0, mine1 = 0;
+            auto todo = [&](int x) -> unsigned {
+                if (x >= count) return 0;
+                if (x == end) {
+                    if (x) cur.next_segment(p);
+                    it = end, end = min(count, it + cur.tiles - cur.tile);
+                    mine0 = min(end - it, max(0, stream_tiles(cur.r, cur.rb, 0) - cur.tile));
+                    mine1 = min(end - it, max(0, stream_tiles(cur.r, cur.rb, 1) - cur.tile));
+                }
+                const int j = x - it;
+                return (j < mine0 ? kUse0 : 0) | (j < mine1 ? kUse1 : 0) | (j == 0 ? kFirst : 0) | (j == mine0 - 1 ? kLast0 : 0) |
+                       (j == mine1 - 1 ? kLast1 : 0);
+            };
+            // Scores of tile x for stream ST; first: nothing has waited for the tile yet; last: nothing after
+            // them reads its keys.  (A wait for what is there takes some 150 cycles beside the softmax: there
+            // are no more of them than have to be.)
+            auto qk = [&](auto ST, int x, unsigned what, bool first, bool last) {
+                constexpr int st = decltype(ST)::value;
+                constexpr uint32_t id = us::umma_idesc_f16(kM, kTile);
+                const int item = x % kItems;
+                if (what & kFirst) wait(&H.q_full[st], segment[st]++);
+                if (first) wait(&H.k_full[item], x / kItems);
+                us::tc_fence_after();
+                const uint64_t qd = us::umma_smem_desc_sw128(q_sm + st * kK * kBlock);
+#pragma unroll
+                for (int c = 0; c < kK; ++c) {
+                    const uint64_t kd = us::umma_smem_desc_sw128(ring + (x * kT + c) % kSlots * kBlock);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        us::umma_f16(tmem + st * 128, qd + (uint64_t)((c * kBlock + kk * 32) >> 4), kd + (uint64_t)(kk * 32 >> 4), id,
+                                     c > 0 || kk > 0);
+                }
+                us::umma_commit(&H.s_full[st]);
+                if (last) us::umma_commit(&H.k_free[item]);
+                if (what & (st ? kLast1 : kLast0)) us::umma_commit(&H.q_free[st]);
+            };
+            auto pv = [&](auto ST, int x, unsigned what, bool first, bool last) {
+                constexpr int st = decltype(ST)::value;
+                const int item = x % kItems;
+                if (first) wait(&H.v_full[item], x / kItems);
+                const uint32_t o = tmem + 256 + st * 128, w = tmem + st * 128;
+                const int v0 = (x * kT + kK) % kSlots;
+                const uint64_t rd = us::umma_smem_desc_mn_sw128(ring, kBlock), vd = rd + (uint64_t)(v0 * (kBlock >> 4));
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    wait(&H.p_full[st][half], used[st]);
                     us::tc_fence_after();
-                    const uint64_t qd = us::umma_smem_desc_sw128(q_sm + st * kK * kBlock);
+                    if (kV == 1 || v0 + 1 == kSlots) {     // one block of columns, or two that the ring's end parts
 #pragma unroll
-                    for (int c = 0; c < kK; ++c) {
-                        const uint64_t kd = us::umma_smem_desc_sw128(ring + (x * kT + c) % kSlots * kBlock);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            us::umma_f16(tmem + st * 128, qd + (uint64_t)((c * kBlock + kk * 32) >> 4), kd + (uint64_t)(kk * 32 >> 4), id,
-                                         c > 0 || kk > 0);
-                    }
-                    us::umma_commit(&H.s_full[st]);
-                    if (last) us::umma_commit(&H.k_free[item]);
-                    if (j == mine - 1) us::umma_commit(&H.q_free[st]);
-                };
-                auto pv = [&](auto ST, int j, bool first, bool last) {
-                    constexpr int st = decltype(ST)::value;
-                    const int x = it + j, item = x % kItems;
-                    if (first) wait(&H.v_full[item], x / kItems);
-                    const uint32_t o = tmem + 256 + st * 128, w = tmem + st * 128;
-                    const int v0 = (x * kT + kK) % kSlots;
-                    const uint64_t rd = us::umma_smem_desc_mn_sw128(ring, kBlock), vd = rd + (uint64_t)(v0 * (kBlock >> 4));
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        wait(&H.p_full[st][half], used[st]);
-                        us::tc_fence_after();
-                        if (kV == 1 || v0 + 1 == kSlots) { // one block of columns, or two that the ring's end parts
-#pragma unroll
-                            for (int c = 0; c < kV; ++c)
-#pragma unroll
-                                for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                                    us::umma_f16_ta(o + 64 * c, w + 8 * kk, (c ? rd : vd) + (uint64_t)(kk * 2048 >> 4),
-                                                    us::umma_idesc_f16(kM, 64) | us::kUmmaBMajorMN, j > 0 || kk > 0);
-                        } else {
+                        for (int c = 0; c < kV; ++c)
 #pragma unroll
                             for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                                us::umma_f16_ta(o, w + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), us::umma_idesc_f16(kM, 64 * kV) | us::kUmmaBMajorMN,
-                                                j > 0 || kk > 0);
-                        }
+                                us::umma_f16_ta(o + 64 * c, w + 8 * kk, (c ? rd : vd) + (uint64_t)(kk * 2048 >> 4),
+                                                us::umma_idesc_f16(kM, 64) | us::kUmmaBMajorMN, !(what & kFirst) || kk > 0);
+                    } else {
+#pragma unroll
+                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                            us::umma_f16_ta(o, w + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), us::umma_idesc_f16(kM, 64 * kV) | us::kUmmaBMajorMN,
+                                            !(what & kFirst) || kk > 0);
                     }
-                    ++used[st];
-                    if (last) us::umma_commit(&H.v_free[item]);
-                    us::umma_commit(&H.pv_done[st]);
-                };
-                constexpr std::integral_constant<int, 0> S0{};
-                constexpr std::integral_constant<int, 1> S1{};
-#pragma unroll 1
-                for (int j = -1; j < n && !failed; ++j) {
-                    if (j >= 0 && j < mine0) pv(S0, j, true, j >= mine1);
-                    if (j + 1 < mine0) qk(S0, j + 1, mine0, true, j + 1 >= mine1);
-                    if (j >= 0 && j < mine1) pv(S1, j, j >= mine0, true);
-                    if (j + 1 < mine1) qk(S1, j + 1, mine1, j + 1 >= mine0, true);
                 }
-                it = end;
-                if (it < count) cur.next_segment(p);
+                ++used[st];
+                if (last) us::umma_commit(&H.v_free[item]);
+                us::umma_commit(&H.pv_done[st]);
+            };
+            constexpr std::integral_constant<int, 0> S0{};
+            constexpr std::integral_constant<int, 1> S1{};
+            // A stream's outputs of a tile and its scores of the next, be that of the next segment (whose
+            // scores are there, then, when the last one's outputs have been written)
+            unsigned now = 0, next = todo(0);
+#pragma unroll 1
+            for (int x = -1; x < count && !failed; ++x) {
+                if (now & kUse0) pv(S0, x, now, true, !(now & kUse1));
+                if (next & kUse0) qk(S0, x + 1, next, true, !(next & kUse1));
+                if (now & kUse1) pv(S1, x, now, !(now & kUse0), true);
+                if (next & kUse1) qk(S1, x + 1, next, !(next & kUse0), true);
+                now = next, next = todo(x + 2);
             }
             // Arrivals that no other warp waits for: they land while the CTA still has its shared memory
             for (int i = max(0, count - kItems); i < count; ++i) wait(&H.k_free[i % kItems], i / kItems), wait(&H.v_free[i % kItems], i / kItems);
