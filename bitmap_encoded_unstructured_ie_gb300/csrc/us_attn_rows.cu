@@ -11,8 +11,8 @@
 // cores work on one while the other's weights are made.  A stream takes the tiles that
 // its last row sees.
 //   warps 0-3, 4-7: softmax of stream 0 / 1, a thread a row
-//   warp 8: one thread issues the MMAs
-//   warp 9: one thread issues the copies (TMA, 128-byte swizzle): Q, then tile after
+//   warps 8, 9: one thread issues the MMAs of stream 0 / 1
+//   warp 10: one thread issues the copies (TMA, 128-byte swizzle): Q, then tile after
 //           tile, its keys and its values as an item each, in blocks of 128 rows of 64
 //           values, into a ring of such blocks
 // Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set, and
@@ -32,14 +32,14 @@ namespace {
 using namespace us::attn;
 
 constexpr int kM = 128, kRows = 256, kTile = 128; // query rows of a stream, of a segment; positions of a tile
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kThreads = 320;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 10, kThreads = 352;
 constexpr float kTop = 11.f, kRoom = 15.9f;        // log2 of a row's largest weight when R is set, and at most
 constexpr int kBlock = 128 * 128;                 // bytes of 128 rows of 64 values
 constexpr int kItems = 4;                         // keys, and values, of tiles that have a barrier each
 
 struct Header {
     uint64_t k_full[kItems], v_full[kItems], k_free[kItems], v_free[kItems];
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], pv_done[2];    // by stream (weights: and half of the positions)
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], pv_done[2], turn[2];      // by stream (weights: and half of the positions)
     uint32_t tmem;
 };
 
@@ -103,10 +103,10 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kItems; ++i)
-            us::mbar_init(&H.k_full[i], 1), us::mbar_init(&H.v_full[i], 1), us::mbar_init(&H.k_free[i], 1), us::mbar_init(&H.v_free[i], 1);
+            us::mbar_init(&H.k_full[i], 1), us::mbar_init(&H.v_full[i], 1), us::mbar_init(&H.k_free[i], 2), us::mbar_init(&H.v_free[i], 2);
         for (int i = 0; i < 2; ++i) {
             us::mbar_init(&H.q_full[i], 1), us::mbar_init(&H.q_free[i], 1), us::mbar_init(&H.s_full[i], 1);
-            us::mbar_init(&H.p_full[i][0], 4), us::mbar_init(&H.p_full[i][1], 4), us::mbar_init(&H.pv_done[i], 1);
+            us::mbar_init(&H.p_full[i][0], 4), us::mbar_init(&H.p_full[i][1], 4), us::mbar_init(&H.pv_done[i], 1), us::mbar_init(&H.turn[i], 1);
         }
         us::fence_mbar_init();
     }
@@ -139,13 +139,12 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
         const float none = scale < 0.f ? INFINITY : -INFINITY;         // an unseen score: -inf when scaled
         const uint64_t s2 = pair(scale, scale);
         if (threadIdx.x == 0) p.ws_parts[blockIdx.x].rows = 0;     // until a shared segment begins here
-        int used = 0;                                      // tiles of this stream so far
+        int used = 0, segment = 0;                         // tiles and segments of this stream so far
         for (int it = 0; it < count;) {
             // ---- a segment, or this CTA's part of it: tiles it .. end - 1, of which the stream's `mine`
             const int end = min(count, it + cur.tiles - cur.tile), tile0 = cur.tile;
             const int rows = min(kRows, cur.r.n - cur.rb * kRows), tok = min(cur.r.n - 1, cur.rb * kRows + st * kM + row);
             const int mine = min(end - it, max(0, stream_tiles(cur.r, cur.rb, st) - tile0));
-            const int other = st ? min(end - it, max(0, stream_tiles(cur.r, cur.rb, 0) - tile0)) : 0;
             float R = -INFINITY;
             uint64_t l2 = 0;
             for (int j = 0; j < mine; ++j, ++used) {
@@ -195,8 +194,6 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                 const float ref = to == -INFINITY ? 0.f : to;
                 const uint64_t neg = pair(-ref, -ref);
                 if (j && __any_sync(0xffffffffu, moved)) { // the outputs so far first (their product is done: these scores came after)
-                    wait(&H.pv_done[st], used - 1);
-                    us::tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         float y[16];
@@ -208,10 +205,10 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                     }
                 }
                 // Values where no position is count as 0, and what some rows do not see (positions
-                // behind the segment's first one) is made finite; the first stream that reads the
-                // tile sees to it.
+                // behind the segment's first one) is made finite, by both streams that read the tile,
+                // each before its own product (they write the same).
                 const int there = cur.r.ctx + cur.r.n - pos0, all_see = cur.r.ctx + cur.rb * kRows + 1 - pos0;
-                if ((there < kTile || all_see < kTile) && j >= other) {
+                if (there < kTile || all_see < kTile) {
                     const int x = it + j;
                     wait(&H.v_full[x % kItems], x / kItems);
 #pragma unroll 1
@@ -277,7 +274,7 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
             uint16_t* out = p.O + (int64_t)(cur.r.row0 + cur.rb * kRows + (srow & ~3)) * p.ldo + (int64_t)cur.h * D + 8 * (lane & 3);
             const int left = rows - (srow & ~3);
             if (end < count) cur.next_segment(p);
-            if (mine) wait(&H.pv_done[st], used - 1);
+            if (mine) wait(&H.pv_done[st], segment++);
             us::tc_fence_after();
             if (wrow < rows) {
 #pragma unroll 1
@@ -356,35 +353,29 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
             for (int i = max(0, count - kItems); i < count; ++i) wait(&H.k_full[i % kItems], i / kItems), wait(&H.v_full[i % kItems], i / kItems);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else {
         // --------------------------------------------------------------- MMA
+        // A thread for each stream, so that one's waits, commits and arithmetic (six cycles an instruction)
+        // do not hold up the other, and they take turns (a tile's outputs and the next one's scores):
+        // left to themselves, both streams come to want the tensor cores, then the exponentials, at once.
         if (us::elect_one()) {
-            int segment[2] = {0, 0}, used[2] = {0, 0};     // segments and tiles of each stream so far
-            // What there is to do with a tile (they are asked for one after the other): which streams
-            // read it, whether it is the first of its segment here, and a stream's last one.
-            constexpr unsigned kUse0 = 1, kUse1 = 2, kFirst = 4, kLast0 = 8, kLast1 = 16;
-            int it = 0, end = 0, mine0 = 0, mine1 = 0;
+            const int st = warp - kMmaWarp;
+            int segment = 0, used = 0, it = 0, end = 0, mine = 0;          // segments and tiles of the stream so far
+            // What the stream has to do with a tile (they are asked for one after the other): whether it
+            // reads it, and whether that is the first or last one of its segment here.
+            constexpr unsigned kUse = 1, kFirst = 2, kLast = 4;
             auto todo = [&](int x) -> unsigned {
                 if (x >= count) return 0;
                 if (x == end) {
                     if (x) cur.next_segment(p);
                     it = end, end = min(count, it + cur.tiles - cur.tile);
-                    mine0 = min(end - it, max(0, stream_tiles(cur.r, cur.rb, 0) - cur.tile));
-                    mine1 = min(end - it, max(0, stream_tiles(cur.r, cur.rb, 1) - cur.tile));
+                    mine = min(end - it, max(0, stream_tiles(cur.r, cur.rb, st) - cur.tile));
                 }
-                const int j = x - it;
-                return (j < mine0 ? kUse0 : 0) | (j < mine1 ? kUse1 : 0) | (j == 0 ? kFirst : 0) | (j == mine0 - 1 ? kLast0 : 0) |
-                       (j == mine1 - 1 ? kLast1 : 0);
+                return (x - it < mine ? kUse : 0) | (x == it ? kFirst : 0) | (x - it == mine - 1 ? kLast : 0);
             };
-            // Scores of tile x for stream ST; first: nothing has waited for the tile yet; last: nothing after
-            // them reads its keys.  (A wait for what is there takes some 150 cycles beside the softmax: there
-            // are no more of them than have to be.)
-            auto qk = [&](auto ST, int x, unsigned what, bool first, bool last) {
-                constexpr int st = decltype(ST)::value;
+            auto qk = [&](int x, unsigned what) {
                 constexpr uint32_t id = us::umma_idesc_f16(kM, kTile);
-                const int item = x % kItems;
-                if (what & kFirst) wait(&H.q_full[st], segment[st]++);
-                if (first) wait(&H.k_full[item], x / kItems);
+                if (what & kFirst) wait(&H.q_full[st], segment++);
                 us::tc_fence_after();
                 const uint64_t qd = us::umma_smem_desc_sw128(q_sm + st * kK * kBlock);
 #pragma unroll
@@ -395,20 +386,18 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                         us::umma_f16(tmem + st * 128, qd + (uint64_t)((c * kBlock + kk * 32) >> 4), kd + (uint64_t)(kk * 32 >> 4), id,
                                      c > 0 || kk > 0);
                 }
+                us::mbar_arrive(&H.turn[st]);
                 us::umma_commit(&H.s_full[st]);
-                if (last) us::umma_commit(&H.k_free[item]);
-                if (what & (st ? kLast1 : kLast0)) us::umma_commit(&H.q_free[st]);
+                us::umma_commit(&H.k_free[x % kItems]);
+                if (what & kLast) us::umma_commit(&H.q_free[st]);
             };
-            auto pv = [&](auto ST, int x, unsigned what, bool first, bool last) {
-                constexpr int st = decltype(ST)::value;
-                const int item = x % kItems;
-                if (first) wait(&H.v_full[item], x / kItems);
+            auto pv = [&](int x, unsigned what) {
                 const uint32_t o = tmem + 256 + st * 128, w = tmem + st * 128;
                 const int v0 = (x * kT + kK) % kSlots;
                 const uint64_t rd = us::umma_smem_desc_mn_sw128(ring, kBlock), vd = rd + (uint64_t)(v0 * (kBlock >> 4));
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    wait(&H.p_full[st][half], used[st]);
+                    wait(&H.p_full[st][half], used);
                     us::tc_fence_after();
                     if (kV == 1 || v0 + 1 == kSlots) {     // one block of columns, or two that the ring's end parts
 #pragma unroll
@@ -424,29 +413,34 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                                             !(what & kFirst) || kk > 0);
                     }
                 }
-                ++used[st];
-                if (last) us::umma_commit(&H.v_free[item]);
-                us::umma_commit(&H.pv_done[st]);
+                ++used;
+                us::umma_commit(&H.v_free[x % kItems]);
+                if (what & kLast) us::umma_commit(&H.pv_done[st]);         // (within a segment the next scores say it)
             };
-            constexpr std::integral_constant<int, 0> S0{};
-            constexpr std::integral_constant<int, 1> S1{};
-            // A stream's outputs of a tile and its scores of the next, be that of the next segment (whose
-            // scores are there, then, when the last one's outputs have been written)
+            // The stream's outputs of a tile and its scores of the next, be that of the next segment (whose
+            // scores are there, then, when the last one's outputs have been written).  A tile that the
+            // stream does not read it gives back as it comes: every one is given back by both.
             unsigned now = 0, next = todo(0);
 #pragma unroll 1
             for (int x = -1; x < count && !failed; ++x) {
-                if (now & kUse0) pv(S0, x, now, true, !(now & kUse1));
-                if (next & kUse0) qk(S0, x + 1, next, true, !(next & kUse1));
-                if (now & kUse1) pv(S1, x, now, !(now & kUse0), true);
-                if (next & kUse1) qk(S1, x + 1, next, !(next & kUse0), true);
+                if (x >= 0) wait(&H.v_full[x % kItems], x / kItems);
+                if (st || x >= 0) wait(&H.turn[st ^ 1], x + st);
+                if (x >= 0) {
+                    if (now & kUse) pv(x, now);
+                    else us::mbar_arrive(&H.v_free[x % kItems]);
+                }
+                if (x + 1 < count) {
+                    wait(&H.k_full[(x + 1) % kItems], (x + 1) / kItems);
+                    if (next & kUse) qk(x + 1, next);
+                    else us::mbar_arrive(&H.turn[st]), us::mbar_arrive(&H.k_free[(x + 1) % kItems]);
+                } else {
+                    us::mbar_arrive(&H.turn[st]);
+                }
                 now = next, next = todo(x + 2);
             }
             // Arrivals that no other warp waits for: they land while the CTA still has its shared memory
             for (int i = max(0, count - kItems); i < count; ++i) wait(&H.k_free[i % kItems], i / kItems), wait(&H.v_free[i % kItems], i / kItems);
-            for (int st = 0; st < 2; ++st) {
-                if (used[st]) wait(&H.pv_done[st], used[st] - 1);
-                if (segment[st]) wait(&H.q_free[st], segment[st] - 1);
-            }
+            if (segment) wait(&H.pv_done[st], segment - 1), wait(&H.q_free[st], segment - 1);
         }
         __syncwarp();
     }
