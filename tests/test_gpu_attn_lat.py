@@ -120,6 +120,19 @@ def test_single_tokens(us, Dc, Hq, page, ctx):
     assert np.array_equal(got, s.run(None))                    # a chain of one is a tree of one
 
 
+@pytest.mark.parametrize("Dc,Hq,n", [(256, 64, 1), (512, 64, 1), (512, 16, 4), (256, 20, 9)])
+def test_many_segments_a_cta(us, Dc, Hq, n):
+    """Several requests' tiles on every SM, of one to ten tiles each."""
+    ctx = [int(c) for c in np.random.default_rng(21).integers(0, 600, 170)]
+    s = Setup(us, Dc, Hq, 64, ctx, [n] * len(ctx), 22)
+    words, grids = s.tree()
+    ws = us.workspace_attn_lat(s.C, Hq, n)
+    got = s.run(words, ws=ws)
+    s.check(got, grids, only=range(0, len(ctx), 7))
+    for _ in range(3):
+        assert np.array_equal(got, s.run(words, ws=ws))
+
+
 @pytest.mark.parametrize("Dc,Hq,page,ctx,n", [
     (512, 16, 64, [200, 0, 63], [64, 64, 1]),
     (256, 4, 32, [100, 7, 450, 0], [13, 25, 0, 2]),

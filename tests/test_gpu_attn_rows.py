@@ -94,6 +94,19 @@ def test_long_prompts_on_many_heads(us):
         assert np.array_equal(got, s.run(ws=ws))
 
 
+@pytest.mark.parametrize("D", [128, 64])
+def test_many_short_segments(us, D):
+    """Several segments on every SM, of which the two streams read unlike numbers of tiles."""
+    n = [20, 300, 1, 140, 256, 40] * 4
+    kv = [20, 300, 129, 260, 500, 41] * 4
+    s = Setup(us, D, 40, kv, n, 5)
+    ws = us.workspace_attn_rows(D, 64, D, 40, len(n), 300)
+    got = s.run(ws=ws)
+    s.check(got, heads=[0, 13, 39])
+    for _ in range(3):
+        assert np.array_equal(got, s.run(ws=ws))
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.05, 1e-6])
 def test_scales(us, scale):
     s = Setup(us, 128, 2, [300, 20], [200, 20], 2)
