@@ -13,16 +13,24 @@
 // a block, not 128: O's 512 columns of 128 rows would take all of TMEM.  A product of
 // 64 rows takes 16 lanes of each warp's 32 in TMEM; O's columns 256 .. 511 lie in the
 // other 16 lanes, so O takes 256 columns and two tiles' scores 128 more.
-//   warps 0-3: softmax of 16 rows each, the segment's Q and its outputs
-//   warps 4-7: find pages and copy the tiles' rows, 16 bytes a lane, each to its place of
-//           the 128-byte swizzle.  (By tensor copies a tile came at 33 bytes a cycle, 10 at a
-//           kernel's start, and the issuing thread was held up meanwhile.)
+//   warps 0-3: softmax of 16 rows each, the first segment's Q, the outputs
+//   warps 4-7: find pages and copy the tiles' rows and further Q, 16 bytes a lane, to their places of
+//           the 128-byte swizzle.  (By tensor copies, a box a page: 152 requests of 2000 positions
+//           in pages of 16 took 83 us, 65 so; pages of 64 the same, trees 3 % less.)
 //   warp 8: one thread issues the MMAs, whichever of the next tile's scores (its rows
 //           have landed) and the last one's outputs (its weights are there) can go
 // Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set, and
 // moves when a score passes R + 15.9 (fp16 holds 2^15.9 and keeps all bits of weights
 // down to 2^-25 of the largest).  R, sums and outputs of a segment shared by several CTAs
 // are joined by a second kernel.
+//
+// What bounds it.  Long caches: bytes, a tile every 1.88 us on each of 152 SMs, 5.9 TB/s (48
+// requests of 8192 positions, 343 MB: 79 us; 50.5 at a copy's rate), as both stages, 147 KB,
+// are held while their products run.  Full rows of trees: the products, 1.56 us a tile, of
+// which 2270 cycles are the tensor cores' (a product of 64 rows takes as long as one of 128;
+// 320 rows of 8 requests behind 4095 positions: 44 us).  Short ones: a launch and its join,
+// 11 us, and 6 us a further segment on an SM (its scores, weights and product one after the
+// other, outputs out of TMEM in 4000 cycles).
 #include <atomic>
 
 #include "us_attn_lat.cuh"

@@ -31,7 +31,8 @@ int num_sms();
 namespace attn {
 
 // Waits for phase `parity` of `bar`, at most kWaitLimitNs (then US_ERR_TIMEOUT is
-// recorded).  Without a pause between tries: six warps leave the issue slots to it.
+// recorded).  Without a pause between tries: these kernels' few warps leave the issue
+// slots to it.
 US_DEV bool spin(uint64_t* bar, uint32_t parity, unsigned* status) {
     if (us::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = us::globaltimer_ns();

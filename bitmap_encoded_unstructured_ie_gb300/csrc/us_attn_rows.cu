@@ -19,8 +19,16 @@
 // moves when a score passes R + 15.9 (fp16 holds 2^15.9 and keeps all bits of weights
 // down to 2^-25 of the largest).  R, sums and outputs of a segment shared by several
 // CTAs are joined by a second kernel.
+//
+// What bounds it: turns.  Of 4200 cycles for a tile of both streams the tensor cores work
+// 2620 (12 steps of 65 cycles a stream for the scores, 8 of 66 for the outputs), a stream's
+// softmax takes 2500 (the exponentials alone 1024), and between its last weights and its
+// next scores' first use pass 1600: the product of the second half, the scores, two waits,
+// and often the next keys, which find a place in the ring (224 KB are in use) only when
+// the other stream has read the values before.  512 tokens behind 8192, 32 heads: 85.6 us
+// (46.7 at the rate of a large product); prompts of 1777, 32 heads: 97.5 us (30.9; half of a
+// diagonal tile is masked, and start, segments' ends and join are 20 of it).
 #include <atomic>
-#include <type_traits>
 
 #include "us_attn_lat.cuh"
 #include "us_internal.h"

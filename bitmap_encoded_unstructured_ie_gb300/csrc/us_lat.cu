@@ -7,9 +7,9 @@
 // Commit: entries of listed tokens move to consecutive positions, all of a request's
 // reads before its writes; 128 bytes of every row a CTA.
 //
-// Bytes bound the long calls (prompts of 85 MB: 16.4 us, 5.2 TB/s, 12.5 us at a copy's
-// rate), latency the short ones (offsets and table, rows, the sum's shuffles: a token each
-// of 64 requests 3.6 us).
+// Bytes bound the long calls (three prompts of up to 8192 tokens written and read back, 85 MB:
+// 16.4 us, 5.2 TB/s; 12.5 us at a copy's rate), latency the short ones (offsets and table, rows,
+// the sum's shuffles: a token each of 24 requests written and read back 3.6 us).
 #include "us_internal.h"
 #include "us_lat.cuh"
 #include "us_launch.cuh"

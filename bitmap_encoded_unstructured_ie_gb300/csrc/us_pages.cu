@@ -14,7 +14,7 @@
 // the pages in runs of up to 128 of one request, so that one long request is spread like
 // many short ones.  A warp finds a run's request in two steps, each lane looking at
 // another sum (by bisection for each page: 512 requests that give and take 280000 pages
-// 25 us, 11 us so).  A step of 48 requests with up to eight drafts takes 2.6 us a call.
+// 25 us, 11 us so).  48 requests that grow by up to four positions take 2.6 us a call.
 #include "us_internal.h"
 #include "us_kv.cuh"
 #include "us_launch.cuh"

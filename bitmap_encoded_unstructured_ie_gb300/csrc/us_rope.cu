@@ -214,7 +214,7 @@ us_status launch_as(const Call& p, cudaStream_t st) {
 }
 
 // Four heads a chunk where that leaves work for every SM, else one: a step of 16 tokens
-// is latency, which four heads one after the other lengthen (5.2 us with the attention behind it,
+// is latency, which four heads one after the other lengthen (written and read back in 5.2 us,
 // 7.1 with four), prompts are bytes and instructions, which four heads share (52.6 us, 60.5 with one).
 template <int LANES, int ELEM>
 us_status launch_heads(const Call& p, cudaStream_t st) {
