@@ -40,7 +40,7 @@ namespace {
 using namespace us::attn;
 
 constexpr int kM = 128, kRows = 256, kTile = 128; // query rows of a stream, of a segment; positions of a tile
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 10, kThreads = 352;
+constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18, kThreads = 608;
 constexpr float kTop = 11.f, kRoom = 15.9f;        // log2 of a row's largest weight when R is set, and at most
 constexpr int kBlock = 128 * 128;                 // bytes of 128 rows of 64 values
 constexpr int kItems = 4;                         // keys, and values, of tiles that have a barrier each
@@ -48,6 +48,7 @@ constexpr int kItems = 4;                         // keys, and values, of tiles 
 struct Header {
     uint64_t k_full[kItems], v_full[kItems], k_free[kItems], v_free[kItems];
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], pv_done[2], turn[2];      // by stream (weights: and half of the positions)
+    float row[2][2][kM];                          // by stream and half of the positions: of its rows
     uint32_t tmem;
 };
 
@@ -56,7 +57,7 @@ struct Shape {
     static constexpr int kK = D / 64 + 1, kV = D / 64, kT = kK + kV;       // blocks of a tile's keys, values, both
     static constexpr int kSlots = D == 128 ? 8 : 9;                        // blocks of the ring
     static_assert((kSlots + kT - 1) / kT + 1 <= kItems, "tiles that have blocks in the ring");
-    static constexpr int kSmem = (2 * kK + kSlots) * kBlock + (int)sizeof(Header) + 1024;
+    static constexpr int kSmem = (2 * kK + kSlots) * kBlock + (int)sizeof(Header);
     static constexpr int kSlotFloats = slot_floats(kRows, D);
     static_assert(kSmem <= 232448, "shared memory");
 };
@@ -102,8 +103,11 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
     using Sh = Shape<D>;
     constexpr int kK = Sh::kK, kV = Sh::kV, kT = Sh::kT, kSlots = Sh::kSlots;
     using Cur = Cursor<kRows, kTile>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((0u - us::smem_addr(smem_raw)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];      // (there is no room to align it by hand)
+    if (us::smem_addr(smem) & 1023u) {
+        if (threadIdx.x == 0) us::set_status(p.c.status, US_ERR_CUDA);
+        return;
+    }
     uint8_t* q_sm = smem;
     uint8_t* ring = q_sm + 2 * kK * kBlock;
     Header& H = *reinterpret_cast<Header*>(ring + kSlots * kBlock);
@@ -139,14 +143,22 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
 
     if (warp < kSoftWarps) {
         // ----------------------------------------------------------- softmax
-        const int st = warp >> 2, row = (warp & 3) * 32 + lane;               // of the stream
+        const int st = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;      // of the stream
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
-        const uint32_t s_tm = tmem + lanes + st * 128, o_tm = tmem + lanes + 256 + st * 128;
+        const uint32_t s_tm = tmem + lanes + st * 128 + half * 64;
+        const uint32_t o_tm = tmem + lanes + 256 + st * 128 + half * (D / 2);      // the thread's columns of its row
         // (a scale of 0 would make NaN of masked scores; this one makes 1 of every weight, too)
         const float scale = p.scale == 0.f ? 1e-37f : p.scale * 1.4426950408889634f;
         const float none = scale < 0.f ? INFINITY : -INFINITY;         // an unseen score: -inf when scaled
         const uint64_t s2 = pair(scale, scale);
         if (threadIdx.x == 0) p.ws_parts[blockIdx.x].rows = 0;     // until a shared segment begins here
+        // What the row's other thread has; both warps of the rows take part.  (The next tile's
+        // scores, and so its maxima, come after both have arrived with their weights.)
+        auto exchange = [&](float x) {
+            H.row[st][half][row] = x;
+            us::named_bar_sync(1 + 4 * st + (warp & 3), 64);
+            return H.row[st][half ^ 1][row];
+        };
         int used = 0, segment = 0;                         // tiles and segments of this stream so far
         for (int it = 0; it < count;) {
             // ---- a segment, or this CTA's part of it: tiles it .. end - 1, of which the stream's `mine`
@@ -159,10 +171,9 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                 const int pos0 = (tile0 + j) * kTile;
                 wait(&H.s_full[st], used);
                 us::tc_fence_after();
-                // The scores are read twice, 32 at a time, the next ones on their way while these are
-                // used; the loops are kept short, so that the code of all roles stays near.
-                const int seen = cur.r.ctx + tok + 1 - pos0;       // positions that the row sees
-                const bool edge = __any_sync(0xffffffffu, seen < kTile);
+                // The thread's 64 scores of its row are read twice, 32 at a time.
+                const int seen = cur.r.ctx + tok + 1 - pos0 - 64 * half;       // positions that the row sees
+                const bool edge = __any_sync(0xffffffffu, seen < 64);
                 uint32_t r0[32], r1[32];
                 auto finish = [&](int c, uint32_t (&r)[32], float (&v)[32]) {
                     us::tmem_ld_frag32_end(r, v);
@@ -183,17 +194,17 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                     }
                     top = fmaxf(t[0], t[1]);
                 };
-                tmem_ld32_begin(s_tm, r0);
-#pragma unroll 1
-                for (int c = 0; c < kTile; c += 64) {
+                {
                     float v[32];
-                    finish(c, r0, v);
-                    tmem_ld32_begin(s_tm + c + 32, r1);
+                    tmem_ld32_begin(s_tm, r0);
+                    finish(0, r0, v);
+                    tmem_ld32_begin(s_tm + 32, r1);
                     largest(v);
-                    finish(c + 32, r1, v);
-                    tmem_ld32_begin(s_tm + (c ? 0 : 64), r0);      // (at the end: the first ones again)
+                    finish(32, r1, v);
+                    tmem_ld32_begin(s_tm, r0);
                     largest(v);
                 }
+                top = fmaxf(top, exchange(top));
                 const float to = top > R + kRoom ? top - kTop : R;
                 const float f = to == R ? 1.f : ex2(R - to);
                 const bool moved = to != R;
@@ -203,7 +214,7 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                 const uint64_t neg = pair(-ref, -ref);
                 if (j && __any_sync(0xffffffffu, moved)) { // the outputs so far first (their product is done: these scores came after)
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
+                    for (int c = 0; c < D / 2; c += 16) {
                         float y[16];
                         uint32_t o[16];
                         us::tmem_ld16(o_tm + c, y);
@@ -216,18 +227,18 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                 // behind the segment's first one) is made finite, by both streams that read the tile,
                 // each before its own product (they write the same).
                 const int there = cur.r.ctx + cur.r.n - pos0, all_see = cur.r.ctx + cur.rb * kRows + 1 - pos0;
-                if (there < kTile || all_see < kTile) {
+                if (min(there, all_see) < 64 * half + 64) {
                     const int x = it + j;
                     wait(&H.v_full[x % kItems], x / kItems);
 #pragma unroll 1
                     for (int c = 0; c < kV; ++c) {
-                        uint4* b = reinterpret_cast<uint4*>(ring + (x * kT + kK + c) % kSlots * kBlock) + (threadIdx.x & 127);
-                        uint4 y[8];
+                        uint4* b = reinterpret_cast<uint4*>(ring + (x * kT + kK + c) % kSlots * kBlock) + 512 * half + (threadIdx.x & 127);
+                        uint4 y[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = b[128 * i];
+                        for (int i = 0; i < 4; ++i) y[i] = b[128 * i];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int at = (threadIdx.x & 127) / 8 + 16 * i;           // the position
+                        for (int i = 0; i < 4; ++i) {
+                            const int at = 64 * half + (threadIdx.x & 127) / 8 + 16 * i;           // the position
                             if (at >= there) b[128 * i] = make_uint4(0, 0, 0, 0);
                             else if (at >= all_see && !all_finite(y[i])) b[128 * i] = finite(y[i]);
                         }
@@ -245,23 +256,20 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                         sums[k & 1] = add2(sums[k & 1], pair(x, y));
                         w[k] = pack_half2(x, y);
                     }
-                    tmem_st16(s_tm + c / 2, w);            // over scores that were read
+                    tmem_st16(s_tm + c / 2, w);            // over scores that this thread has read
                 };
-#pragma unroll 1
-                for (int c = 0; c < kTile; c += 64) {
+                {
                     float v[32];
-                    finish(c, r0, v);
-                    tmem_ld32_begin(s_tm + c + 32, r1);
-                    weigh(c, v);
-                    finish(c + 32, r1, v);
-                    if (c == 0) tmem_ld32_begin(s_tm + 64, r0);
-                    weigh(c + 32, v);
-                    // (the product of the first half begins while the second is made)
-                    us::tmem_wait_st();
-                    us::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) us::mbar_arrive(&H.p_full[st][c >> 6]);
+                    finish(0, r0, v);
+                    tmem_ld32_begin(s_tm + 32, r1);
+                    weigh(0, v);
+                    finish(32, r1, v);
+                    weigh(32, v);
                 }
+                us::tmem_wait_st();
+                us::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) us::mbar_arrive(&H.p_full[st][half]);
                 l2 = add2(l2, add2(sums[0], sums[1]));
             }
             // ---- the segment's end: what is to be known for it while the last product runs
@@ -269,24 +277,26 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
             Part part = {};
             if (!whole) part = wk.sharers(wk.t0 + it - tile0, wk.t0 + it - tile0 + cur.tiles, cur, rows);
             const int srow = st * kM + row, wrow = srow & ~31;         // of the segment
-            float a, b;
-            unpair(l2, a, b);
-            const float sum = a + b, inv = sum == 0.f ? 0.f : 1.f / sum;
             float* slot = p.ws_slots + part.slot(blockIdx.x) * Sh::kSlotFloats;
-            if (!whole && wrow < rows) {
-                __stcg(slot + srow, R);
-                __stcg(slot + kRows + srow, sum);
-            }
             if (!whole && part.first == (int)blockIdx.x && threadIdx.x == 0) p.ws_parts[blockIdx.x] = part;
             // (the row that the lane's quad begins with, and the lane's piece of each of the quad's rows)
-            uint16_t* out = p.O + (int64_t)(cur.r.row0 + cur.rb * kRows + (srow & ~3)) * p.ldo + (int64_t)cur.h * D + 8 * (lane & 3);
+            uint16_t* out = p.O + (int64_t)(cur.r.row0 + cur.rb * kRows + (srow & ~3)) * p.ldo + (int64_t)cur.h * D + half * (D / 2) + 8 * (lane & 3);
             const int left = rows - (srow & ~3);
             if (end < count) cur.next_segment(p);
             if (mine) wait(&H.pv_done[st], segment++);
             us::tc_fence_after();
+            float a, b;
+            unpair(l2, a, b);
+            a += b;
+            const float sum = a + exchange(a), inv = sum == 0.f ? 0.f : 1.f / sum;
+            us::named_bar_sync(1 + 4 * st + (warp & 3), 64);           // (read, before a maximum of the next segment comes there)
             if (wrow < rows) {
+                if (!whole && half == 0) {
+                    __stcg(slot + srow, R);
+                    __stcg(slot + kRows + srow, sum);
+                }
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = 0; c < D / 2; c += 32) {
                     float y[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) y[k] = 0.f;
@@ -306,7 +316,7 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
-                            __stcg(reinterpret_cast<float4*>(slot + 2 * kRows) + (c + k) / 4 * kRows + srow,
+                            __stcg(reinterpret_cast<float4*>(slot + 2 * kRows) + (half * (D / 2) + c + k) / 4 * kRows + srow,
                                    make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]));
                     }
                     __syncwarp();
@@ -412,12 +422,12 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                         for (int c = 0; c < kV; ++c)
 #pragma unroll
                             for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                                us::umma_f16_ta(o + 64 * c, w + 8 * kk, (c ? rd : vd) + (uint64_t)(kk * 2048 >> 4),
+                                us::umma_f16_ta(o + 64 * c, w + 8 * kk + 32 * half, (c ? rd : vd) + (uint64_t)(kk * 2048 >> 4),
                                                 us::umma_idesc_f16(kM, 64) | us::kUmmaBMajorMN, !(what & kFirst) || kk > 0);
                     } else {
 #pragma unroll
                         for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                            us::umma_f16_ta(o, w + 8 * kk, vd + (uint64_t)(kk * 2048 >> 4), us::umma_idesc_f16(kM, 64 * kV) | us::kUmmaBMajorMN,
+                            us::umma_f16_ta(o, w + 8 * kk + 32 * half, vd + (uint64_t)(kk * 2048 >> 4), us::umma_idesc_f16(kM, 64 * kV) | us::kUmmaBMajorMN,
                                             !(what & kFirst) || kk > 0);
                     }
                 }
