@@ -10,9 +10,9 @@
 // streams of 128 rows, each with its own scores, outputs and softmax warps: the tensor
 // cores work on one while the other's weights are made.  A stream takes the tiles that
 // its last row sees.
-//   warps 0-3, 4-7: softmax of stream 0 / 1, a thread a row
-//   warps 8, 9: one thread issues the MMAs of stream 0 / 1
-//   warp 10: one thread issues the copies (TMA, 128-byte swizzle): Q, then tile after
+//   warps 0-7, 8-15: softmax of stream 0 / 1, two threads a row, 64 positions each
+//   warps 16, 17: one thread issues the MMAs of stream 0 / 1
+//   warp 18: one thread issues the copies (TMA, 128-byte swizzle): Q, then tile after
 //           tile, its keys and its values as an item each, in blocks of 128 rows of 64
 //           values, into a ring of such blocks
 // Weights are 2^(s - R); a row's reference R is its maximum less 11 when it is set, and
@@ -20,14 +20,16 @@
 // down to 2^-25 of the largest).  R, sums and outputs of a segment shared by several
 // CTAs are joined by a second kernel.
 //
-// What bounds it: turns.  Of 4200 cycles for a tile of both streams the tensor cores work
-// 2620 (12 steps of 65 cycles a stream for the scores, 8 of 66 for the outputs), a stream's
-// softmax takes 2500 (the exponentials alone 1024), and between its last weights and its
-// next scores' first use pass 1600: the product of the second half, the scores, two waits,
-// and often the next keys, which find a place in the ring (224 KB are in use) only when
-// the other stream has read the values before.  512 tokens behind 8192, 32 heads: 85.6 us
-// (46.7 at the rate of a large product); prompts of 1777, 32 heads: 97.5 us (30.9; half of a
-// diagonal tile is masked, and start, segments' ends and join are 20 of it).
+// What bounds it: the way round.  Of 3950 cycles for a tile of both streams the tensor
+// cores work 2620 (12 steps of 65 cycles a stream for the scores, 8 of 66 for the outputs).
+// A tile's keys find their place in the ring when stream 1 is through with the values
+// before the last (Q and ring are 224 KB), take 2500 cycles to land (80 KB a tile and SM
+// come at 20 of about 33 bytes a cycle), and then stream 0's scores and stream 1's outputs
+// follow, which free the next values.  A stream's softmax, 1850 cycles, hides behind that
+// (with one thread a row it took 2500, and all 2 to 4 % longer).  512 tokens behind 8192, 32
+// heads: 83.8 us (46.7 at the rate of a large product); three prompts of up to 1777, 32
+// heads: 93.2 us (30.9; half of a diagonal tile is masked, and start, segments' ends and
+// join are 20 of it).
 #include <atomic>
 
 #include "us_attn_lat.cuh"
