@@ -262,7 +262,8 @@ us_status check_tokens(int T, const int32_t* off, const int32_t* pos, const int3
     if (T < 0 || max_n < 1 || !off || !pos || !aligned16(off) || !aligned16(pos)) return US_ERR_INVALID_ARG;
     if (depth && !aligned16(depth)) return US_ERR_INVALID_ARG;
     if (max_n >= 1 << 30) return US_ERR_TOO_LARGE;
-    a.off = off; a.pos = pos; a.T = T; a.max_n = max_n;
+    a.off = off; a.pos = pos; a.T = T;
+    a.max_n = max_n < T ? max_n : T > 0 ? T : 1;           // (no request has more; grids are made for it)
     return US_OK;
 }
 

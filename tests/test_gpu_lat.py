@@ -149,3 +149,28 @@ def test_entries_beyond_32_bit_offsets(us):
     assert us.us_get_last_device_status() == us.US_OK
     s = torch.softmax(q[0].double() @ x.double().T * 0.07, -1)
     assert (o[0].double() - s @ x[:, :512].double()).abs().max() <= 2e-3 * x.abs().max().item()
+
+
+def test_a_limit_far_beyond_the_rows(us):
+    """max_n is a promise, not a size: 2^30 - 1 of it gives what the rows' own number gives."""
+    n, most = 37, (1 << 30) - 1
+    C, table, rng = make(us, 256, 16, [n + 5], 77)
+    x, w = dev(values(rng, n, 1, 320)[:, 0]), dev((1 + 0.3 * rng.standard_normal(256)).astype(np.float16))
+    off, pos, r = dev(offsets([n])), i32([5]), rope(us, 64, 0)
+    q = dev(values(rng, n, 4, 64))
+    P = us.kv_pool(16, 8, 1, 4)
+    us.us_kv_reserve(P, i32([n + 5]))
+    C.rows.fill_(0)                                                # (what the call does not write is seen, too)
+    got = {}
+    for m in (n, most):
+        rows, o = torch.zeros(n, 320, dtype=torch.float16, device="cuda"), torch.zeros(n, 4, 256, dtype=torch.float16, device="cuda")
+        qo, slots = torch.zeros_like(q), torch.zeros(n, dtype=torch.int64, device="cuda")
+        us.us_lat_write(C, r, x, w, off, pos, None, m)
+        us.us_lat_read(C, off, pos, m, rows)
+        us.us_norm_rope(r, q, None, qo, None, None, None, off, pos, None, m)
+        us.us_kv_slots(P, off, pos, m, slots)
+        m4 = min(m, most // 4)
+        us.us_attn_lat(C, rows.unflatten(1, (1, 320)).expand(n, 4, 320).contiguous(), off, pos, None, m4, 0.05, o, us.workspace_attn_lat(C, 4, m4))
+        assert us.us_get_last_device_status() == us.US_OK
+        got[m] = [t.cpu() for t in (rows, qo, slots, o)]
+    assert got[n][0].abs().max() > 0 and all(torch.equal(a, b) for a, b in zip(got[n], got[most]))
