@@ -6,19 +6,16 @@
 
 namespace us {
 
+// args: a pointer to each of the kernel's parameters (us_api.cu)
+us_status launch_kernel(const void* kern, dim3 grid, int threads, size_t smem, cudaStream_t st, void** args);
+
 template <class... Params, class... Args>
 us_status launch_pdl(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, Params(args)...) == cudaSuccess ? US_OK : US_ERR_CUDA;
+    auto with = [&](Params... p) {
+        void* at[] = {const_cast<void*>(static_cast<const void*>(&p))...};
+        return launch_kernel(reinterpret_cast<const void*>(kern), grid, threads, smem, st, at);
+    };
+    return with(Params(args)...);
 }
 
 }  // namespace us

@@ -144,3 +144,28 @@ def test_captured_and_replayed(us):
         assert slots.cpu().tolist() == [ref.slot(b, lens[b] - 1) for b in range(3)]
         lens = lens + 7
     assert us.us_get_last_device_status() == us.US_OK
+
+
+def test_threads_that_have_not_used_the_device(us):
+    """Calls from new threads, several at once, each on a stream and a pool of its own."""
+    import threading
+    pools = [us.kv_pool(16, 200, 4, 50) for _ in range(8)]
+    refs = [lat.Pool(16, 200, 4, 50) for _ in range(8)]
+    lens = [[10 * i, 700, 0, 33 + i] for i in range(8)]
+    at, streams, errors = [i32(n) for n in lens], [torch.cuda.Stream() for _ in range(8)], []
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            us.us_kv_reserve(pools[i], at[i], streams[i])
+        except Exception as e:                                     # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and us.us_get_last_device_status() == us.US_OK
+    for P, ref, n in zip(pools, refs, lens):
+        ref.reserve(n)
+        same(P, ref)
