@@ -719,9 +719,10 @@ def lat_cache(Dc: int, Dr: int, page_size: int, num_pages: int, page_table: torc
 def _row2(X: torch.Tensor, W: int, device: int):
     """Rows, pointer and row distance of T x W fp16 rows."""
     T, w = X.shape
-    assert X.dtype in _HALVES and w == W and X.stride(1) == 1, "rows must be T x W CUDA fp16 with contiguous values"
+    ld, sd = X.stride()
+    assert X.dtype in _HALVES and w == W and sd == 1, "rows must be T x W CUDA fp16 with contiguous values"
     assert X.get_device() == device, "tensors must be on one device"
-    return T, X.data_ptr(), (X.stride(0) if T > 1 else W)
+    return T, X.data_ptr(), (ld if T > 1 else W)
 
 
 def us_lat_write(C: LatCache, rope: Rope, X: torch.Tensor, w, tok_off: torch.Tensor, pos: torch.Tensor, depth, max_n: int,
