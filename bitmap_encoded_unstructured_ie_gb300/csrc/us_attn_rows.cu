@@ -20,16 +20,16 @@
 // down to 2^-25 of the largest).  R, sums and outputs of a segment shared by several
 // CTAs are joined by a second kernel.
 //
-// What bounds it: the way round.  Of 3950 cycles for a tile of both streams the tensor
+// What bounds it: the way round.  Of 3800 cycles for a tile of both streams the tensor
 // cores work 2620 (12 steps of 65 cycles a stream for the scores, 8 of 66 for the outputs).
 // A tile's keys find their place in the ring when stream 1 is through with the values
 // before the last (Q and ring are 224 KB), take 2500 cycles to land (80 KB a tile and SM
 // come at 20 of about 33 bytes a cycle), and then stream 0's scores and stream 1's outputs
 // follow, which free the next values.  A stream's softmax, 1850 cycles, hides behind that
 // (with one thread a row it took 2500, and all 2 to 4 % longer).  512 tokens behind 8192, 32
-// heads: 83.8 us (46.7 at the rate of a large product); three prompts of up to 1777, 32
-// heads: 93.2 us (30.9; half of a diagonal tile is masked, and start, segments' ends and
-// join are 20 of it).
+// heads: 81.0 us (46.7 at the rate of a large product; 83.8 where a copy brings 128 bytes
+// to L2, not 256); three prompts of up to 1777, 32 heads: 93.2 us (30.9; half of a diagonal
+// tile is masked, and start, segments' ends and join are 20 of it).
 #include <atomic>
 
 #include "us_attn_lat.cuh"
