@@ -120,7 +120,8 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
             us::mbar_init(&H.k_full[i], 1), us::mbar_init(&H.v_full[i], 1), us::mbar_init(&H.k_free[i], 2), us::mbar_init(&H.v_free[i], 2);
         for (int i = 0; i < 2; ++i) {
             us::mbar_init(&H.q_full[i], 1), us::mbar_init(&H.q_free[i], 1), us::mbar_init(&H.s_full[i], 1);
-            us::mbar_init(&H.p_full[i][0], 4), us::mbar_init(&H.p_full[i][1], 4), us::mbar_init(&H.pv_done[i], 1), us::mbar_init(&H.turn[i], 1);
+            // (the first half's weights and all of the outputs' columns, the second half's weights)
+            us::mbar_init(&H.p_full[i][0], 8), us::mbar_init(&H.p_full[i][1], 4), us::mbar_init(&H.pv_done[i], 1), us::mbar_init(&H.turn[i], 1);
         }
         us::fence_mbar_init();
     }
@@ -224,6 +225,14 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                         for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(y[k] * f);
                         tmem_st16(o_tm + c, o);
                     }
+                    us::tmem_wait_st();
+                }
+                // The product of the first 64 positions adds to all columns of the outputs, so it waits
+                // for this half's columns too, not only for the other half's weights.
+                if (half) {
+                    us::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) us::mbar_arrive(&H.p_full[st][0]);
                 }
                 // Values where no position is count as 0, and what some rows do not see (positions
                 // behind the segment's first one) is made finite, by both streams that read the tile,
