@@ -47,8 +47,9 @@ US_DEV bool spin(uint64_t* bar, uint32_t parity, unsigned* status) {
 }
 
 // fp16 pairs with infinities and NaN as 0.  A value that a row does not see has weight
-// 0 in it, and 0 times what is not finite would be NaN; in a row that does see it, its
-// key has made NaN of the weight.
+// 0 in it, and 0 times what is not finite would be NaN.  What a row that sees it gets:
+// over latent rows its key has made NaN of the weight, over expanded rows it is added
+// at the segment's end.
 US_DEV uint32_t not_finite(uint32_t x) { return __vcmpeq2(x & 0x7C007C00u, 0x7C007C00u); }
 US_DEV bool all_finite(uint4 x) { return (not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w)) == 0; }
 US_DEV uint4 finite(uint4 x) {

@@ -51,7 +51,9 @@ struct Header {
     uint64_t k_full[kItems], v_full[kItems], k_free[kItems], v_free[kItems];
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], pv_done[2], turn[2];      // by stream (weights: and half of the positions)
     float row[2][2][kM];                          // by stream and half of the positions: of its rows
-    uint32_t tmem;
+    uint32_t tmem, cleared;                       // cleared: some value was not finite, and made 0 in the ring
+    int4 part[kSoftWarps];                        // of the warp's segment that ends (registers are short): see there
+    int request[kSoftWarps];
 };
 
 template <int D>                                  // Dn = Dv
@@ -124,6 +126,7 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
             us::mbar_init(&H.p_full[i][0], 8), us::mbar_init(&H.p_full[i][1], 4), us::mbar_init(&H.pv_done[i], 1), us::mbar_init(&H.turn[i], 1);
         }
         us::fence_mbar_init();
+        H.cleared = 0;
     }
     if (warp == kLoadWarp && lane < 4)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.q + lane)) : "memory");
@@ -234,24 +237,26 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                     __syncwarp();
                     if (lane == 0) us::mbar_arrive(&H.p_full[st][0]);
                 }
-                // Values where no position is count as 0, and what some rows do not see (positions
-                // behind the segment's first one) is made finite, by both streams that read the tile,
-                // each before its own product (they write the same).
+                // Values where no position is count as 0, and of those that some rows do not see (positions
+                // behind the segment's first one) what is not finite is cleared; the rows that see it get it
+                // at the segment's end.  Stream 0 does that for both: its product with a tile goes first.
+                // Tiles that it does not read are stream 1's.
                 const int there = cur.r.ctx + cur.r.n - pos0, all_see = cur.r.ctx + cur.rb * kRows + 1 - pos0;
-                if (min(there, all_see) < 64 * half + 64) {
+                if (min(there, all_see) < 64 * half + 64 && (st == 0 || stream_tiles(cur.r, cur.rb, 0) - tile0 <= j)) {
                     const int x = it + j;
                     wait(&H.v_full[x % kItems], x / kItems);
 #pragma unroll 1
-                    for (int c = 0; c < kV; ++c) {
-                        uint4* b = reinterpret_cast<uint4*>(ring + (x * kT + kK + c) % kSlots * kBlock) + 512 * half + (threadIdx.x & 127);
-                        uint4 y[4];
+                    for (int c = 0; c < 2 * kV; ++c) {
+                        uint4* b = reinterpret_cast<uint4*>(ring + (x * kT + kK + c / 2) % kSlots * kBlock) + 512 * half + 256 * (c & 1) + (threadIdx.x & 127);
+                        uint4 y[2];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) y[i] = b[128 * i];
+                        for (int i = 0; i < 2; ++i) y[i] = b[128 * i];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int at = 64 * half + (threadIdx.x & 127) / 8 + 16 * i;           // the position
+                        for (int i = 0; i < 2; ++i) {
+                            const int at = 64 * half + 32 * (c & 1) + (threadIdx.x & 127) / 8 + 16 * i;           // the position
                             if (at >= there) b[128 * i] = make_uint4(0, 0, 0, 0);
-                            else if (at >= all_see && !all_finite(y[i])) b[128 * i] = finite(y[i]);
+                            else if (at >= all_see && !all_finite(y[i]))
+                                b[128 * i] = finite(y[i]), *static_cast<volatile uint32_t*>(&H.cleared) = 1;
                         }
                     }
                     us::fence_proxy_async_smem();
@@ -293,9 +298,43 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
             // (the row that the lane's quad begins with, and the lane's piece of each of the quad's rows)
             uint16_t* out = p.O + (int64_t)(cur.r.row0 + cur.rb * kRows + (srow & ~3)) * p.ldo + (int64_t)cur.h * D + half * (D / 2) + 8 * (lane & 3);
             const int left = rows - (srow & ~3);
+            if (lane == 0) {                               // where values may have been cleared: positions between z and w, seen as x says
+                H.part[warp] = make_int4(cur.r.ctx + cur.rb * kRows + 1, cur.h, tile0 * kTile, min(cur.r.ctx + cur.r.n, (tile0 + end - it) * kTile));
+                H.request[warp] = cur.b;
+            }
             if (end < count) cur.next_segment(p);
             if (mine) wait(&H.pv_done[st], segment++);
             us::tc_fence_after();
+            if (mine && *static_cast<volatile uint32_t*>(&H.cleared)) {        // (once set, for good: such inputs are rare)
+                __syncwarp();
+                const int4 of = H.part[warp];
+                const int v0 = max(of.x, of.z), v1 = min(of.x + srow, of.w);
+                const uint16_t* v = p.k.V + (int64_t)(p.kv_off[H.request[warp]] + v0) * p.k.ldv + of.y * p.k.hsv + half * (D / 2);
+#pragma unroll 1
+                for (int c = 0; c < D / 2; c += 16) {
+                    float y[16];
+                    uint32_t o[16];
+                    us::tmem_ld16(o_tm + c, y);
+                    // (a weight is positive: what is not finite is the sum)
+#pragma unroll 1
+                    for (int at = 0; at < v1 - v0; ++at)
+#pragma unroll
+                        for (int k = 0; k < 16; k += 8) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(v + at * p.k.ldv + c + k);
+                            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float z = us::half_bits_to_float((uint16_t)(u[e >> 1] >> (16 * (e & 1))));
+                                y[k + e] += z - z == 0.f ? 0.f : z;
+                            }
+                        }
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(y[k]);
+                    tmem_st16(o_tm + c, o);
+                }
+                us::tmem_wait_st();
+            }
             float a, b;
             unpair(l2, a, b);
             a += b;

@@ -531,7 +531,8 @@ us_status us_attn_lat_workspace_bytes(const us_lat_cache* C, int Hq, int max_n, 
  *   w_p = exp(scale * (Q[t][h][:Dn] . K[p][h] + Q[t][h][Dn:] . KR[p]))
  * at most 65504 in magnitude; accumulation and weights as in us_attn_lat.
  * Key rows that a query does not see have no part in its output, whatever they hold;
- * rows outside kv_off[b] .. are not looked at.
+ * rows outside kv_off[b] .. are not looked at.  Of those that it sees, a value that is
+ * not finite makes its column of the output +-65504 or NaN, as the sum is.
  * Q: T rows of H heads of Dn + Dr values side by side, O: of Dv; K: S rows of Dn
  * values a head, ldk elements apart, a head hsk behind the last; V the same, of Dv;
  * KR: S rows of Dr.  Distances are multiples of 8.  (Dn, Dr, Dv): (128, 64, 128) or

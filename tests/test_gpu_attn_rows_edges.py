@@ -30,3 +30,31 @@ def test_outputs_that_are_rescaled_with_every_tile(us, D, H, kv, n):
     s.check(got, heads=[0, H // 2, H - 1])
     for _ in range(5):
         assert np.array_equal(got, s.run(ws=ws))
+
+
+@pytest.mark.parametrize("what", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("D,H,ctx,n,at", [
+    (128, 2, 0, 150, 5), (128, 2, 0, 300, 5), (64, 2, 0, 512, 200), (128, 3, 100, 300, 0), (128, 2, 100, 512, 130),
+    (64, 3, 0, 300, 260), (64, 160, 0, 300, 20), (128, 100, 30, 280, 257), (64, 4, 0, 1, 0),
+])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them(us, what, D, H, ctx, n, at):
+    """Two values of token `at` and one head, its key finite: their columns of that token and those behind it are what
+    the sum is; all else is as if they were 0, on both sides of a block of 256 queries."""
+    s = Setup(us, D, H, [ctx + n, 40], [n, 40], 32)
+    h, cols = H - 1, [3, D - 2]
+    s.V[ctx + at, h, cols] = 0
+    want = s.run()
+    s.check(want, heads=[0, h])
+    want[at:n, h, cols] = what if np.isnan(what) else np.sign(what) * 65504
+    s.V[ctx + at, h, cols] = what
+    assert np.array_equal(s.run(), want, equal_nan=True)
+
+
+def test_values_of_both_signs_that_are_not_finite(us):
+    """Infinity less infinity, and each alone for the rows that see one of them."""
+    s = Setup(us, 128, 2, [200], [200], 33)
+    s.V[[50, 90], 0, 7] = 0
+    want = s.run()
+    s.V[50, 0, 7], s.V[90, 0, 7] = np.inf, -np.inf
+    want[50:90, 0, 7], want[90:, 0, 7] = 65504, np.nan
+    assert np.array_equal(s.run(), want, equal_nan=True)
