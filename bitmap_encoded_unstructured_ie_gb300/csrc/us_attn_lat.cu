@@ -283,7 +283,7 @@ attn_lat_kernel(const UsAttnLatParams p) {
                 if (wrow >= rows && i > it) wait(&H.pv_done, i - 1);
                 // What some rows do not see is made finite (drafts, or in a chain what is behind the
                 // segment's first token); what is not there was copied as zeros.
-                const int behind = cur.r.n - base, all_see = max(0, (p.mask ? (cur.r.n > 1 ? 0 : 1) : cur.rb * kM / G + 1) - base);
+                const int behind = cur.r.n - base, all_see = max(0, (p.mask ? 0 : cur.rb * kM / G + 1) - base);
                 if (all_see < min(kTile, behind)) {
                     // eight threads have 128 bytes of a row, each row's blocks at once
                     uint8_t* x = x_sm + st * Sh::kOperand + (threadIdx.x & 7) * 16;
