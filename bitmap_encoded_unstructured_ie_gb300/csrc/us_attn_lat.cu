@@ -168,6 +168,7 @@ attn_lat_kernel(const UsAttnLatParams p) {
         const int g = lane >> 2, c2 = 2 * (lane & 3), wrow = 16 * warp;
         const uint32_t lanes = (uint32_t)warp * 32u << 16;
         const float scale = p.scale * 1.4426950408889634f;
+        const uint64_t s2 = pair(scale, scale);
         if (threadIdx.x == 0) p.ws_parts[blockIdx.x].rows = 0;     // until a shared segment begins here
         // what the lane's rows see of the call's own positions: their masks, or in a chain how many
         auto seen_of = [&](const Cur& at, uint64_t (&seen)[2]) {
@@ -211,8 +212,13 @@ attn_lat_kernel(const UsAttnLatParams p) {
                 if (wrow < rows) {
                     float v[32];
                     tmem_ld_frag64(tmem + lanes + 256 + 64 * (i & 1), v);
+                    // s + 0 s: an infinite score becomes NaN, so that an entry which is not finite makes NaN of the
+                    // rows that see it whichever sign it has there (a weight of 0 would lose it)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= scale;
+                    for (int j = 0; j < 32; j += 2) {
+                        const uint64_t x = mul2(pair(v[j], v[j + 1]), s2);
+                        unpair(fma2(x, 0ull, x), v[j], v[j + 1]);
+                    }
                     if (base + 64 > 0 || ok != ~0ull) {
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {

@@ -512,8 +512,8 @@ us_status us_lat_commit(const us_lat_cache* C, int T, const int32_t* acc_off, co
  * magnitude, 0 for a row that sees no position.  Scores, sums and outputs are
  * accumulated in fp32; a weight enters its product as fp16, rounded once.  Entries of
  * the call's tokens that a row does not see, and what lies behind a request's last
- * position, may hold anything; those that every row sees (us_lat_write stores finite
- * ones) make NaN of the rows if they are not finite.
+ * position, may hold anything; an entry that is not finite (us_lat_write stores finite
+ * ones) makes NaN of the rows that see it.
  * Q: T rows of Hq heads of Dc + Dr values, O: of Dc.  mask, max_n, errors and the
  * workspace (zeroed once) as in us_attn_kv; Hq <= 1024.  Repeated calls give the same
  * bits. */

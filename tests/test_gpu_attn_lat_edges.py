@@ -32,3 +32,23 @@ def test_single_tokens_that_do_not_see_themselves(us, what, Dc, Hq):
     got = s.run(words)
     s.check(got, grids)
     assert (got[0] == 0).all() and (got[1] != 0).any()
+
+
+@pytest.mark.parametrize("what", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("Dc,Hq,ctx,n,at,col", [
+    (512, 4, 20, 6, 22, 100), (256, 64, 90, 9, 91, 3), (512, 16, 0, 64, 30, 511), (512, 4, 20, 6, 5, 100), (256, 8, 300, 3, 10, 260),
+    (512, 2, 30, 5, 32, 575),
+])
+def test_entries_that_are_not_finite_make_nan_of_the_rows_that_see_them(us, what, Dc, Hq, ctx, n, at, col):
+    """One value of one entry, of the context or of the call's tokens, latent or of the key, and queries of both signs there."""
+    for tree in (False, True):
+        s = Setup(us, Dc, Hq, 16, [ctx], [n], 42)
+        words, grids = s.tree() if tree else s.chain()
+        s.Q[..., col] = np.where(np.arange(Hq) % 2, 1, -1)
+        want = s.run(words)
+        s.check(want, grids)
+        put(s, 0, at, what, col)
+        s.load()
+        sees = np.ones(n, bool) if at < ctx else np.array(grids[0], bool)[:, at - ctx]
+        got = s.run(words)
+        assert np.isnan(got[sees]).all() and np.array_equal(got[~sees], want[~sees]) and sees.any()
