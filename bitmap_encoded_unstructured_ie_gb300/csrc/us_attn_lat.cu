@@ -44,7 +44,6 @@ using namespace us::attn;
 
 constexpr int kM = 64, kTile = 64;                // query rows of a segment, positions of a tile
 constexpr int kSoftWarps = 4, kLoadWarps = 4, kMmaWarp = kSoftWarps + kLoadWarps, kThreads = 32 * (kMmaWarp + 1);
-constexpr float kTop = 11.f, kRoom = 15.9f;        // log2 of a row's largest weight when R is set, and at most
 constexpr int kBlock = 64 * 128;                  // bytes of 64 rows of 64 values
 constexpr int kMaxStages = 4;
 
@@ -240,7 +239,7 @@ attn_lat_kernel(const UsAttnLatParams p) {
                         for (int k = 0; k < 8; ++k) top = max3(top, v[4 * k + 2 * q], v[4 * k + 2 * q + 1]);
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        const float to = top > R[q] + kRoom ? top - kTop : R[q];
+                        const float to = reference(R[q], top);
                         f[q] = to == R[q] ? 1.f : ex2(R[q] - to);
                         moved |= to != R[q];
                         R[q] = to;

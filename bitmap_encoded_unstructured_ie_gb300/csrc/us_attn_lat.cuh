@@ -46,6 +46,15 @@ US_DEV bool spin(uint64_t* bar, uint32_t parity, unsigned* status) {
     return false;
 }
 
+// A row's reference for scores up to `top`: R, or a new one less than the largest by
+// kTop, log2 of its weight, once that is beyond kRoom.  Scores from 2^20 on lie 2^-3 and
+// more apart: R + kRoom, or top - kTop, would be rounded to where a weight is beyond
+// fp16 (2^16).  There the largest score itself is the reference.
+US_DEV float reference(float R, float top) {
+    constexpr float kTop = 11.f, kRoom = 15.9f, kFine = 0x1p20f;
+    return top > R + (fabsf(R) < kFine ? kRoom : 0.f) ? top - (fabsf(top) < kFine ? kTop : 0.f) : R;
+}
+
 // fp16 pairs with infinities and NaN as 0.  A value that a row does not see has weight
 // 0 in it, and 0 times what is not finite would be NaN.  What a row that sees it gets:
 // over latent rows its key has made NaN of the weight, over expanded rows it is added

@@ -52,3 +52,43 @@ def test_entries_that_are_not_finite_make_nan_of_the_rows_that_see_them(us, what
         sees = np.ones(n, bool) if at < ctx else np.array(grids[0], bool)[:, at - ctx]
         got = s.run(words)
         assert np.isnan(got[sees]).all() and np.array_equal(got[~sees], want[~sees]) and sees.any()
+
+
+@pytest.mark.parametrize("Dc,Hq,ctx", [(512, 16, 0), (256, 64, 0), (512, 4, 700)])
+@pytest.mark.parametrize("size", [40, 120, 250, 1000, 2000, 4000, 20000, 60000])
+def test_large_scores(us, Dc, Hq, ctx, size):
+    """Entries of one direction and steadily different lengths, which queries of both signs rank: each row's output is the
+    first or the last entry.  Scores are a tenth of themselves apart at the ends, and from 2^9 to beyond 2^30."""
+    s = Setup(us, Dc, Hq, 16, [ctx], [1], 43)
+    along = np.sign(s.rng.standard_normal(s.W))
+    for order in (1, -1):
+        length = np.full(ctx + 1, 1.0)
+        length[0] = 0.8 if order > 0 else 1.0
+        length[1:] = np.linspace(0.85, 0.95, ctx) if ctx else 0
+        length[ctx] = 1.0 if order > 0 or not ctx else 0.8
+        for p in range(ctx + 1):
+            put(s, 0, p, (size * length[p] * along).astype(np.float16))
+        s.load()
+        s.Q[:] = (size * along * np.where(np.arange(Hq) % 2, -1, 1)[:, None]).astype(np.float16)
+        got, rows = s.run(None)[0], s.rows(0).astype(np.float64)[:, :Dc]
+        # the next best score lies 0.05 size^2 W scale away: a weight of e^-60 and less from size 40 on
+        best = np.abs(rows[:, 0])
+        for h in range(Hq):
+            want = rows[best.argmax() if h % 2 == 0 else best.argmin()]
+            assert (np.abs(got[h] - want) <= 2.0 ** -10 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("Hq", [2, 64])
+@pytest.mark.parametrize("base", [512, 1024, 2048, 4096])
+def test_large_scores_close_to_one_another(us, Hq, base):
+    """Scores of 2^20 to 2^23 (base 1024) that rise by a little from tile to tile: outputs are weighted means."""
+    for step in (3.3, 3.4, 3.5, 3.6, 7.0, 11.0):
+        s = Setup(us, 256, Hq, 64, [191], [1], 44)
+        for p in range(192):
+            put(s, 0, p, 0, slice(256, 320))
+            put(s, 0, p, [base, step * (p // 64)], slice(256, 258))
+        s.load()
+        s.Q[:] = 0
+        s.Q[..., 256], s.Q[..., 257], s.scale = 1024, 1, 1.0
+        got, most = s.run(None), np.abs(s.rows(0)[:, :256].astype(np.float64)).max()
+        assert (np.abs(got) <= most * (1 + 2.0 ** -9)).all()
