@@ -43,7 +43,6 @@ using namespace us::attn;
 
 constexpr int kM = 128, kRows = 256, kTile = 128; // query rows of a stream, of a segment; positions of a tile
 constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18, kThreads = 608;
-constexpr float kTop = 11.f, kRoom = 15.9f;        // log2 of a row's largest weight when R is set, and at most
 constexpr int kBlock = 128 * 128;                 // bytes of 128 rows of 64 values
 constexpr int kItems = 4;                         // keys, and values, of tiles that have a barrier each
 
@@ -211,13 +210,16 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                     largest(v);
                 }
                 top = fmaxf(top, exchange(top));
-                const float to = top > R + kRoom ? top - kTop : R;
+                const float to = reference(R, top);
                 const float f = to == R ? 1.f : ex2(R - to);
                 const bool moved = to != R;
                 R = to;
                 l2 = mul2(l2, pair(f, f));
                 const float ref = to == -INFINITY ? 0.f : to;
                 const uint64_t neg = pair(-ref, -ref);
+                // Large scores are rounded before the reference, which is one of them, is taken off: unrounded,
+                // the largest would lie up to half a step, which may be thousands, beside it.
+                const bool coarse = __any_sync(0xffffffffu, fabsf(ref) >= kFine);
                 if (j && __any_sync(0xffffffffu, moved)) { // the outputs so far first (their product is done: these scores came after)
 #pragma unroll 1
                     for (int c = 0; c < D / 2; c += 16) {
@@ -277,10 +279,25 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
                 {
                     float v[32];
                     finish(0, r0, v);
-                    tmem_ld32_begin(s_tm + 32, r1);
-                    weigh(0, v);
-                    finish(32, r1, v);
-                    weigh(32, v);
+                    if (!coarse) {
+                        tmem_ld32_begin(s_tm + 32, r1);
+                        weigh(0, v);
+                        finish(32, r1, v);
+                        weigh(32, v);
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 32) {
+                            uint32_t w[16];
+                            if (c) tmem_ld32_begin(s_tm + 32, r1), finish(32, r1, v);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float x = ex2(__fadd_rn(__fmul_rn(v[2 * k], scale), -ref)), y = ex2(__fadd_rn(__fmul_rn(v[2 * k + 1], scale), -ref));
+                                sums[k & 1] = add2(sums[k & 1], pair(x, y));
+                                w[k] = pack_half2(x, y);
+                            }
+                            tmem_st16(s_tm + c / 2, w);
+                        }
+                    }
                 }
                 us::tmem_wait_st();
                 us::tc_fence_before();

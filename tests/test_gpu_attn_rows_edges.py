@@ -58,3 +58,38 @@ def test_values_of_both_signs_that_are_not_finite(us):
     s.V[50, 0, 7], s.V[90, 0, 7] = np.inf, -np.inf
     want[50:90, 0, 7], want[90:, 0, 7] = 65504, np.nan
     assert np.array_equal(s.run(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("D,H,ctx,n", [(128, 2, 0, 1), (64, 2, 0, 1), (128, 3, 400, 1), (64, 40, 700, 3)])
+@pytest.mark.parametrize("size", [60, 250, 1000, 2000, 4000, 7000, 20000, 60000])
+def test_large_scores(us, D, H, ctx, n, size):
+    """Keys of one direction and steadily different lengths, which queries of both signs rank: each row's output is the value
+    of the first position or of its own.  Scores from 2^10 to beyond 2^30."""
+    s = Setup(us, D, H, [ctx + n], [n], 34)
+    L, along = ctx + n, np.sign(s.rng.standard_normal(D + 64))
+    for order in (1, -1):
+        length = np.linspace(0.85, 0.9, L)
+        length[0], length[ctx:] = (0.8, 0.95 + 0.05 * np.arange(n) / 3) if order > 0 else (1.0, 0.8 - 0.05 * np.arange(n) / 3)
+        key = (size * length[:, None] * along).astype(np.float16)
+        s.K[:], s.R[:] = key[:, None, :D], key[:, D:]
+        s.Q[:] = (size * along * np.where(np.arange(H) % 2, -1, 1)[:, None]).astype(np.float16)
+        got = s.run()
+        # the next best score lies 0.016 size^2 (D + 64) scale away: a weight of e^-600 and less from size 60 on
+        for i in range(n):
+            for h in range(H):
+                want = s.V[ctx + i if (h % 2 == 0) == (order > 0) else 0, h].astype(np.float64)
+                assert (np.abs(got[i, h] - want) <= 2.0 ** -10 * np.abs(want) + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("H", [1, 64])
+@pytest.mark.parametrize("base", [512, 1024, 2048, 4096])
+def test_large_scores_close_to_one_another(us, H, base):
+    """Scores of 2^20 to 2^23 (base 1024) that rise by a little from tile to tile: outputs are weighted means."""
+    for step in (3.3, 3.4, 3.5, 3.6, 7.0, 11.0):
+        s = Setup(us, 64, H, [384], [200], 35)
+        s.R[:] = 0
+        s.R[:, 0], s.R[:, 1] = base, step * (np.arange(384) // 128)
+        s.Q[:] = 0
+        s.Q[..., 64], s.Q[..., 65], s.scale = 1024, 1, 1.0
+        got, most = s.run(), np.abs(s.V.astype(np.float64)).max()
+        assert (np.abs(got) <= most * (1 + 2.0 ** -9)).all()
