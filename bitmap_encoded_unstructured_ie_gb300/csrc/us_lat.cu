@@ -88,7 +88,8 @@ lat_write_kernel(const UsLatCache L, const UsKvCall a, const us_rope rope, const
             for (int v = 0; v < kV; ++v)
                 reinterpret_cast<uint4*>(row)[32 * v + lane] = make_uint4(pack(y[v][0], y[v][1]), pack(y[v][2], y[v][3]),
                                                                           pack(y[v][4], y[v][5]), pack(y[v][6], y[v][7]));
-            const uint32_t k2 = pack(ka * c - kb * s, kb * c + ka * s);
+            // (without a rotation a value does not meet its neighbour, which may not be finite)
+            const uint32_t k2 = rope.R ? pack(ka * c - kb * s, kb * c + ka * s) : pack(ka, kb);
             if (pairs) {
                 reinterpret_cast<uint32_t*>(row + DC)[lane] = k2;
             } else {
