@@ -988,7 +988,8 @@ us_status us_attn_rows(const us_attn_kv_rows* A, const uint16_t* Q, int64_t ldq,
     p.k = *A;
     p.c.Hkv = A->H; p.c.B = B; p.c.page_shift = 10; p.c.max_pages = 1 << 20;       // 2^30 positions
     p.c.status = status_ptr();
-    p.a.off = tok_off; p.a.T = T; p.a.max_n = max_n;
+    p.a.off = tok_off; p.a.T = T;
+    p.a.max_n = max_n < T ? max_n : T;                     // (as in check_tokens: the join is chosen by it)
     p.Q = Q; p.O = O; p.ldq = ldq; p.ldo = ldo; p.Hq = A->H; p.G = 1; p.scale = scale;
     p.kv_off = kv_off;
     const size_t need = us::attn_rows_ws(p);

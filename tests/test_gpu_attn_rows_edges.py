@@ -93,3 +93,13 @@ def test_large_scores_close_to_one_another(us, H, base):
         s.Q[..., 64], s.Q[..., 65], s.scale = 1024, 1, 1.0
         got, most = s.run(), np.abs(s.V.astype(np.float64)).max()
         assert (np.abs(got) <= most * (1 + 2.0 ** -9)).all()
+
+
+@pytest.mark.parametrize("D,H,kv,n", [(128, 1, [4000], [3]), (64, 2, [3000, 500], [20, 1])])
+def test_a_limit_far_beyond_the_rows(us, D, H, kv, n):
+    """max_n is a promise: beyond the rows of the call it has no part in how states are joined."""
+    s = Setup(us, D, H, kv, n, 36)
+    got = s.run(max_n=sum(n))
+    s.check(got)
+    for max_n in (sum(n) + 1, 5000, 1 << 28):
+        assert np.array_equal(got, s.run(max_n=max_n))
