@@ -136,6 +136,8 @@ US_DEV Request make_request(const P& p, int o0, int o1, int ctx, unsigned* statu
     if (r.n > 0) {
         r.ctx = us::kv_context(p.c, ctx, r.n, status);
         if (r.ctx >= 0) r.nrb = (int)((unsigned)(r.n * p.G + ROWS - 1) / ROWS);
+    } else if (P::kOffsets && ctx < 0) {
+        us::set_status(status, US_ERR_INVALID_ARG);        // (positions of no token are not looked at, offsets are)
     }
     return r;
 }

@@ -17,7 +17,8 @@ struct UsAttnRowsParams : UsAttnParams {
     us_attn_kv_rows k;
     const int32_t* kv_off;           // request b's key rows; its tokens are the last of them
 
-    // (a template's call finds this one by the parameters' own type)  -1: offsets that are not usable
+    // (a template's call finds these by the parameters' own type)
+    static constexpr bool kOffsets = true;
     US_DEV int context(int b, int o0, int o1) const {
         const int k0 = kv_off[b], k1 = kv_off[b + 1];
         return k0 >= 0 && k1 >= k0 && k1 <= k.S && o1 >= o0 && k1 - k0 >= o1 - o0 ? (k1 - k0) - (o1 - o0) : -1;

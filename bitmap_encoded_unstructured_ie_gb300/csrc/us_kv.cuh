@@ -46,7 +46,8 @@ struct UsAttnParams {
     float* ws_slots;                 // partial states
     us::attn::Part* ws_parts;        // shared segments
 
-    // positions before the tokens of request b, rows o0 .. o1 - 1
+    // positions before the tokens of request b, rows o0 .. o1 - 1; kOffsets: from offsets, -1 where these are not usable
+    static constexpr bool kOffsets = false;
     US_DEV int context(int b, int, int) const { return a.pos[b]; }
 };
 

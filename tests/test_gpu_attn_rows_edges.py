@@ -2,8 +2,11 @@
 and what stands between the threads that share a row."""
 import numpy as np
 import pytest
+import torch
 
 from tests.test_gpu_attn_rows import Setup
+from tests.test_gpu_kv_cache import dev
+from tests.test_gpu_rope import i32
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +106,24 @@ def test_a_limit_far_beyond_the_rows(us, D, H, kv, n):
     s.check(got)
     for max_n in (sum(n) + 1, 5000, 1 << 28):
         assert np.array_equal(got, s.run(max_n=max_n))
+
+
+def test_key_offsets_of_requests_without_queries_are_checked(us):
+    """Offsets that do not ascend or leave 0..S are recorded whichever request they are of; the others are served."""
+    s = Setup(us, 64, 2, [40, 30, 60], [20, 0, 30], 37)
+    good = s.run()
+    o = torch.zeros(50, 2, 64, dtype=torch.float16, device="cuda")
+    ws = us.workspace_attn_rows(64, 64, 64, 2, 3, 30)
+    for off, kv_off, code, kept in (
+            ([0, 20, 20, 50], [0, 40, 70, 130], us.US_OK, [(0, 50)]),
+            ([0, 20, 20, 50], [0, 40, 40, 130], us.US_OK, [(0, 20)]),               # no key rows either: the last one has 90
+            ([0, 20, 20, 50], [0, 80, 70, 130], us.US_ERR_INVALID_ARG, [(20, 50)]),  # (the first one has 80)
+            ([0, 20, 50, 50], [0, 40, 100, 131], us.US_ERR_INVALID_ARG, [(0, 20)]),
+            ([0, 0, 0, 0], [0, -1, 70, 130], us.US_ERR_INVALID_ARG, []),
+            ([0, 0, 0, 0], [0, 40, 70, 130], us.US_OK, [])):
+        o.fill_(7.0)
+        us.us_attn_rows(dev(s.Q), dev(s.K), dev(s.R), dev(s.V), i32(off), i32(kv_off), 30, s.scale, o, ws)
+        assert us.us_get_last_device_status() == code, (off, kv_off)
+        for a, b in kept:
+            assert np.array_equal(o[a:b].cpu().numpy(), good[a:b])
+        assert (o[off[3]:] == 7).all()
