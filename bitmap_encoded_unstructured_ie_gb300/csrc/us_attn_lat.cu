@@ -48,7 +48,7 @@ constexpr int kBlock = 64 * 128;                  // bytes of 64 rows of 64 valu
 constexpr int kMaxStages = 4;
 
 struct Header {
-    uint64_t full[kMaxStages][3], free[kMaxStages][3], s_full[2], p_full, pv_done, q_full, q_free;
+    uint64_t full[kMaxStages][3], free[kMaxStages][3], s_full[2], p_full, pv_done, q_full, q_free, over;
     uint64_t valid[kMaxStages];                   // which of the tile's positions exist
     uint32_t tmem;
 };
@@ -123,7 +123,7 @@ attn_lat_kernel(const UsAttnLatParams p) {
             for (int j = 0; j < Sh::kParts; ++j)               // (part 0: `valid`, too)
                 us::mbar_init(&H.full[i][j], 32 * kLoadWarps + (j == 0)), us::mbar_init(&H.free[i][j], 1);
         for (int i = 0; i < 2; ++i) us::mbar_init(&H.s_full[i], 1);
-        us::mbar_init(&H.p_full, kSoftWarps), us::mbar_init(&H.pv_done, 1), us::mbar_init(&H.q_full, 32 * kLoadWarps), us::mbar_init(&H.q_free, 1);
+        us::mbar_init(&H.p_full, kSoftWarps), us::mbar_init(&H.pv_done, 1), us::mbar_init(&H.q_full, 32 * kLoadWarps), us::mbar_init(&H.q_free, 1), us::mbar_init(&H.over, 1);
         us::fence_mbar_init();
     }
     if (warp == kMmaWarp) us::tmem_alloc(&H.tmem, 512);
@@ -537,6 +537,10 @@ attn_lat_kernel(const UsAttnLatParams p) {
                 for (int i = max(0, count - kStages); i < count; ++i)
                     for (int j = 0; j < Sh::kParts; ++j) wait(&H.free[i % kStages][j], i / kStages);
                 wait(&H.pv_done, count - 1);
+            }
+            if (failed) {                                  // (after a wait that ran out: its products, before TMEM is given back)
+                us::umma_commit(&H.over);
+                spin(&H.over, 0, p.c.status);
             }
         }
         __syncwarp();

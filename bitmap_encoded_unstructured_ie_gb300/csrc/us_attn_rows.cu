@@ -48,7 +48,7 @@ constexpr int kItems = 4;                         // keys, and values, of tiles 
 
 struct Header {
     uint64_t k_full[kItems], v_full[kItems], k_free[kItems], v_free[kItems];
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], pv_done[2], turn[2];      // by stream (weights: and half of the positions)
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], pv_done[2], turn[2], over[2];      // by stream (weights: and half of the positions)
     float row[2][2][kM];                          // by stream and half of the positions: of its rows
     uint32_t tmem, cleared;                       // cleared: some value was not finite, and made 0 in the ring
     int4 part[kSoftWarps];                        // of the warp's segment that ends (registers are short): see there
@@ -122,7 +122,7 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
         for (int i = 0; i < 2; ++i) {
             us::mbar_init(&H.q_full[i], 1), us::mbar_init(&H.q_free[i], 1), us::mbar_init(&H.s_full[i], 1);
             // (the first half's weights and all of the outputs' columns, the second half's weights)
-            us::mbar_init(&H.p_full[i][0], 8), us::mbar_init(&H.p_full[i][1], 4), us::mbar_init(&H.pv_done[i], 1), us::mbar_init(&H.turn[i], 1);
+            us::mbar_init(&H.p_full[i][0], 8), us::mbar_init(&H.p_full[i][1], 4), us::mbar_init(&H.pv_done[i], 1), us::mbar_init(&H.turn[i], 1), us::mbar_init(&H.over[i], 1);
         }
         us::fence_mbar_init();
         H.cleared = 0;
@@ -394,19 +394,20 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------- copies
         if (us::elect_one()) {
-            int segment[2] = {0, 0};                       // segments of each stream so far
-            for (int it = 0; it < count;) {
+            int segment[2] = {0, 0}, keys = 0, values = 0; // segments of each stream, and tiles, that copies have been begun for
+            for (int it = 0; it < count && !failed;) {
                 const int end = min(count, it + cur.tiles - cur.tile), k0 = p.kv_off[cur.b];
                 auto queries = [&](int st) {
                     if (stream_tiles(cur.r, cur.rb, st) <= cur.tile) return;
                     if (segment[st]) wait(&H.q_free[st], segment[st] - 1);
+                    if (failed) return;
                     ++segment[st];
                     us::mbar_arrive_expect_tx(&H.q_full[st], kK * kBlock);
                     for (int c = 0; c < kK; ++c)
                         tma_load_3d(q_sm + (st * kK + c) * kBlock, &maps.q, 64 * c, cur.h, cur.r.row0 + cur.rb * kRows + st * kM, &H.q_full[st]);
                 };
                 queries(0);                                // (all in the order in which the MMAs need it)
-                for (int i = it; i < end; ++i) {
+                for (int i = it; i < end && !failed; ++i) {
                     const int row = k0 + (cur.tile + i - it) * kTile, item = i % kItems;
                     // block c of the tile, when the one whose place it takes is free
                     auto place = [&](int c) {
@@ -418,24 +419,30 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
 #pragma unroll 1
                     for (int c = 0; c < kK; ++c) {
                         uint8_t* to = place(c);
-                        if (c == 0) us::mbar_arrive_expect_tx(bar, kK * kBlock);
+                        if (failed) break;
+                        if (c == 0) us::mbar_arrive_expect_tx(bar, kK * kBlock), keys = i + 1;
                         if (c < kK - 1) tma_load_3d(to, &maps.k, 64 * c, cur.h, row, bar);
                         else tma_load_3d(to, &maps.r, 0, 0, row, bar);
                     }
-                    if (i == it) queries(1);
+                    if (i == it && !failed) queries(1);
                     bar = &H.v_full[item];
 #pragma unroll 1
                     for (int c = 0; c < kV; ++c) {
                         uint8_t* to = place(kK + c);
-                        if (c == 0) us::mbar_arrive_expect_tx(bar, kV * kBlock);
+                        if (failed) break;
+                        if (c == 0) us::mbar_arrive_expect_tx(bar, kV * kBlock), values = i + 1;
                         tma_load_3d(to, &maps.v, 64 * c, cur.h, row, bar);
                     }
                 }
                 it = end;
                 if (it < count) cur.next_segment(p);
             }
-            // nothing of its own is left in flight when the CTA ends
-            for (int i = max(0, count - kItems); i < count; ++i) wait(&H.k_full[i % kItems], i / kItems), wait(&H.v_full[i % kItems], i / kItems);
+            // nothing of its own is left in flight when the CTA ends, after a wait that ran out neither
+            auto landed = [&](uint64_t* bar, int use) { spin(bar, (uint32_t)use & 1u, p.c.status); };
+            for (int i = max(0, keys - kItems); i < keys; ++i) landed(&H.k_full[i % kItems], i / kItems);
+            for (int i = max(0, values - kItems); i < values; ++i) landed(&H.v_full[i % kItems], i / kItems);
+            for (int st = 0; st < 2; ++st)
+                if (segment[st]) landed(&H.q_full[st], segment[st] - 1);
         }
         __syncwarp();
     } else {
@@ -526,6 +533,10 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
             // Arrivals that no other warp waits for: they land while the CTA still has its shared memory
             for (int i = max(0, count - kItems); i < count; ++i) wait(&H.k_free[i % kItems], i / kItems), wait(&H.v_free[i % kItems], i / kItems);
             if (segment) wait(&H.pv_done[st], segment - 1), wait(&H.q_free[st], segment - 1);
+            if (failed) {                                  // (after a wait that ran out: its products, before TMEM is given back)
+                us::umma_commit(&H.over[st]);
+                spin(&H.over[st], 0, p.c.status);
+            }
         }
         __syncwarp();
     }
