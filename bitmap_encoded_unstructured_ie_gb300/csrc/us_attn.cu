@@ -290,6 +290,7 @@ attn_mma_kernel(const UsAttnParams p) {
     // 2^(s - m); a row's m is 11 less than its largest s + log2(V's scale), so that an
     // entry which a row does not see, or hardly weighs, takes no bits from its weights.
     float m[NT][2], l[NT][2], o[kMT][NT][4];
+    float room = kMost;                                    // 0 from where an m is large on
     uint32_t qf[Sh::kKS][NT][2];
     const float sc = p.scale * 1.4426950408889634f;        // weights as powers of two
     int parts = 0;
@@ -297,6 +298,7 @@ attn_mma_kernel(const UsAttnParams p) {
 
     auto begin_segment = [&]() {
         const int rows = cur.r.n * G;
+        room = kMost;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
@@ -412,7 +414,7 @@ attn_mma_kernel(const UsAttnParams p) {
                 for (int e = 0; e < 2; ++e) {
                     mx[nt][e] = fmaxf(sx[0][nt][e] + lv[0][0], sx[0][nt][e + 2] + lv[0][1]);
                     if constexpr (kSub == 2) mx[nt][e] = max3(mx[nt][e], sx[1][nt][e] + lv[1][0], sx[1][nt][e + 2] + lv[1][1]);
-                    grow |= mx[nt][e] > m[nt][e] + kMost;
+                    grow |= mx[nt][e] > m[nt][e] + room;
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -422,7 +424,8 @@ attn_mma_kernel(const UsAttnParams p) {
                         float x = mx[nt][e];
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        x = fmaxf(x - kTop, m[nt][e]);
+                        x = fmaxf(x - (fabsf(x) < kFine ? kTop : 0.f), m[nt][e]);
+                        if (x != -INFINITY && fabsf(x) >= kFine) room = 0.f;
                         const float f = x == -INFINITY ? 1.f : ex2(m[nt][e] - x);
                         m[nt][e] = x;
                         l[nt][e] *= f;

@@ -38,6 +38,11 @@ US_DEV void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Scores from here on lie 2^-4 and more apart.  A reference that is less than the largest
+// score by a few powers of two would be rounded to where a weight is beyond fp16 (2^16),
+// so there the largest score itself is the reference.
+constexpr float kFine = 0x1p19f;
+
 US_DEV float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

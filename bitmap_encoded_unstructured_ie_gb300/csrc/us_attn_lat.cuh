@@ -48,10 +48,7 @@ US_DEV bool spin(uint64_t* bar, uint32_t parity, unsigned* status) {
 }
 
 // A row's reference for scores up to `top`: R, or a new one less than the largest by
-// kTop, log2 of its weight, once that is beyond kRoom.  Scores from kFine on lie 2^-4 and
-// more apart: R + kRoom, or top - kTop, would be rounded to where a weight is beyond
-// fp16 (2^16).  There the largest score itself is the reference.
-constexpr float kFine = 0x1p19f;
+// kTop, log2 of its weight, once that is beyond kRoom (scores from kFine on: by nothing).
 US_DEV float reference(float R, float top) {
     constexpr float kTop = 11.f, kRoom = 15.9f;
     return top > R + (fabsf(R) < kFine ? kRoom : 0.f) ? top - (fabsf(top) < kFine ? kTop : 0.f) : R;

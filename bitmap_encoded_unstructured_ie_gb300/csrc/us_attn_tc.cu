@@ -257,6 +257,7 @@ attn_tc_kernel(const UsAttnParams p) {
             // references and sums (two partial ones each) of the lane's rows wrow + 8 q + g
             float R[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             uint64_t l2[4] = {};
+            bool coarse = false;                           // some of the warp's references are large
             constexpr int kStep = NQ == 2 ? 1 : 2;         // a stream's tiles: every one, or every other
             const int i0 = NQ == 2 ? it : it + ((it ^ st) & 1);
             for (int i = i0; i < end; i += kStep) {
@@ -278,8 +279,8 @@ attn_tc_kernel(const UsAttnParams p) {
                         uint64_t sum[4], neg[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) neg[q] = pair(-R[q], -R[q]);
-                        // (a segment's first tile has no reference yet)
-                        for (bool fit = edge || (i == i0 && a == 0);; fit = true) {
+                        // (a segment's first tile has no reference yet; large scores, unrounded, may lie far beside theirs)
+                        for (bool fit = edge || (i == i0 && a == 0) || coarse;; fit = true) {
                             if (fit) {
                                 // scaled and masked scores, back in their place, and what they move
                                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -324,7 +325,7 @@ attn_tc_kernel(const UsAttnParams p) {
                                     float x = top[q];
                                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                                    const float to = x > R[q] + kTop ? x - kTop : R[q];
+                                    const float to = x > R[q] + (fabsf(R[q]) < kFine ? kTop : 0.f) ? x - (fabsf(x) < kFine ? kTop : 0.f) : R[q];
                                     f[q] = to == R[q] ? 1.f : ex2(R[q] - to);
                                     moved |= to != R[q];
                                     R[q] = to;
@@ -332,6 +333,10 @@ attn_tc_kernel(const UsAttnParams p) {
                                     const float ref = to == -INFINITY ? 0.f : to;
                                     neg[q] = pair(-ref, -ref);
                                 }
+                                coarse = false;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) coarse |= R[q] != -INFINITY && fabsf(R[q]) >= kFine;
+                                coarse = __any_sync(0xffffffffu, coarse);
                                 if ((i != i0 || a) && __any_sync(0xffffffffu, moved)) {
                                     wait(&H.pv_done[st][a ^ 1], i / kStep + a - 1);    // the stream's outputs so far first
                                     us::tc_fence_after();
