@@ -4,9 +4,10 @@
 // A row x of D values becomes y = x rsqrt(mean(x^2) + eps) w, and its first R values
 // are turned in pairs by A = 2 pi (p turns[j] mod 2^64) / 2^64: the product of a
 // position and a frequency held as a 64-bit fraction of a turn wraps where the angle
-// does, so the angle is off by 2^-33 turns at any position, where p * freq in fp32
-// would be off by p * 2^-24 radians.  cos and sin are made once a token and CTA, in
-// shared memory, and serve all of its heads.
+// does.  Its upper 32 bits, as a signed fraction of a turn, are rounded to fp32: the angle
+// is off by at most 2^-26 + 2^-32 turns (1e-7 radians, and sincospi's 2 ulp) at any
+// position, where p * freq in fp32 would be off by p * 2^-24 radians.  cos and sin are made
+// once a token and CTA, in shared memory, and serve all of its heads.
 //
 // D / 16 lanes (of 4, 8 or 16) hold a row, each two pieces of eight values: of the first
 // R those whose values are turned with one another, (8 l .., R/2 + 8 l ..) or 16 values

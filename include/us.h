@@ -435,7 +435,8 @@ us_status us_kv_slots(const us_kv_pool* P, int T, const int32_t* tok_off, const 
  *   (y_a, y_b) -> (y_a cos A_j - y_b sin A_j, y_b cos A_j + y_a sin A_j)
  * all in fp32, rounded to fp16 once at the end.  A_j = 2 pi p turns[j] / 2^64, with
  * turns[j] uint64, a frequency in turns a position: p turns[j] modulo 2^64 is the
- * angle's fraction of a turn, exact at any position.  R: a multiple of 16, at most D
+ * angle's fraction of a turn, exact at any position, and enters cos and sin rounded to
+ * fp32 (off by at most 2^-26 + 2^-32 turns).  R: a multiple of 16, at most D
  * (0: no rotation, turns may be NULL).
  * Token i of request b stands at position pos[b] + i, or pos[b] + depth[t] where
  * `depth` (int32 [T]) is given: a tree's drafts stand at their depth.
