@@ -24,13 +24,16 @@
 // down to 2^-25 of the largest).  R, sums and outputs of a segment shared by several CTAs
 // are joined by a second kernel.
 //
-// What bounds it.  Long caches: bytes, a tile every 1.88 us on each of 152 SMs, 5.9 TB/s (48
-// requests of 8192 positions, 343 MB: 79 us; 50.5 at a copy's rate), as both stages, 147 KB,
-// are held while their products run.  Full rows of trees: the products, 1.56 us a tile, of
-// which 2270 cycles are the tensor cores' (a product of 64 rows takes as long as one of 128;
-// 320 rows of 8 requests behind 4095 positions: 44 us).  Short ones: a launch and its join,
-// 11 us, and 6 us a further segment on an SM (its scores, weights and product one after the
-// other, outputs out of TMEM in 4000 cycles).
+// What bounds it (clock stamps of the slowest SM, in us).  Long caches: bytes, a tile every
+// 1.9 on each of 152 SMs, 5.9 TB/s, as both stages, 147 KB, are held while their products
+// run.  48 requests of up to 8192 positions, 343 MB, take 79 (50.5 at a copy's rate): 59 are
+// its 31 tiles, 3 pass until its share is found, 5 until first scores, 5 are the ends of two
+// segments' parts, 4.5 the join.  Trees: 320 rows of each of 8 requests behind up to 4095
+// positions take 44: 20 are 13 tiles (1.55 each, of which 2270 cycles are the tensor cores', as a
+// product of 64 rows takes as long as one of 128), 7 the ends of two parts, 3 the first
+// scores, 2 the share, 9 the join: 40 segments are shared out as 180 parts.  Short ones: a
+// launch and its join, 11, and 6 a further segment on an SM (its scores, weights and product one
+// after the other, outputs out of TMEM in 4000 cycles).
 #include <atomic>
 
 #include "us_attn_lat.cuh"

@@ -27,9 +27,13 @@
 // come at 20 of about 33 bytes a cycle), and then stream 0's scores and stream 1's outputs
 // follow, which free the next values.  A stream's softmax, 1850 cycles, hides behind that
 // (with one thread a row it took 2500, and all 2 to 4 % longer).  512 tokens behind 8192, 32
-// heads: 81.0 us (46.7 at the rate of a large product; 83.8 where a copy brings 128 bytes
-// to L2, not 256); three prompts of up to 1777, 32 heads: 93.2 us (30.9; half of a diagonal
-// tile is masked, and start, segments' ends and join are 20 of it).
+// heads: 82 us (46.7 at the rate of a large product; 3 % more where a copy brings 128 bytes
+// to L2, not 256), of which, by clock stamps, 60 are the slowest SM's 29 tiles, 5 pass until
+// first scores, 5 are segments' ends, 2.6 its share, 6 the join.  Three prompts of up to 1777,
+// 32 heads: 94 us (30.9): half of a diagonal tile is masked, and an even share of tiles, 24 or
+// 25, has 2 to 7 segments in it: the slowest SM's 25 tiles are 58, the ends of six segments 15,
+// their first scores 9, its share 3.5; the quickest is through after three quarters of that.
+// 64-wide heads: 71 and 78 us.
 #include <atomic>
 
 #include "us_attn_lat.cuh"

@@ -206,7 +206,8 @@ template <int LANES, int HEADS, int ELEM>
 us_status launch_as(const Call& p, cudaStream_t st) {
     constexpr int kGroups = kThreads / LANES;
     const int nq = (p.q.H + HEADS - 1) / HEADS, nk = (p.k.H + HEADS - 1) / HEADS, per = nq + nk + (ELEM == kNone ? 0 : nk);
-    // four rounds a CTA, or one where that leaves SMs without work
+    // four rounds a CTA, or one where that leaves SMs without work (16384 tokens of 40 heads of 128, four heads a
+    // chunk: 65.5 / 68.1 us, quantised into the cache 98.6 / 112.8; 16 tokens, one head a chunk: 4.1 / 2.25)
     const int64_t all = (int64_t)p.a.max_n * per;
     int chunks = all * p.c.B >= (int64_t)8 * kGroups * us::num_sms() ? 4 * kGroups : kGroups;
     if (chunks > (kTokens - 1) * per) chunks = (kTokens - 1) * per;
@@ -217,6 +218,9 @@ us_status launch_as(const Call& p, cudaStream_t st) {
 // Four heads a chunk where that leaves work for every SM, else one: a step of 16 tokens
 // is latency, which four heads one after the other lengthen (written and read back in 5.2 us,
 // 7.1 with four), prompts are bytes and instructions, which four heads share (52.6 us, 60.5 with one).
+// Near the border, 40 heads of 128: 256 tokens 3.1 with one, 3.5 with four (one round a CTA, as
+// above); 768 5.8 / 4.6; 1024 6.7 / 6.5; 2048 11.1 / 10.0, where four rounds take 11.2; 8192 40.8 /
+// 36.2, 38.0.  Heads that four does not divide are worse off: 8192 tokens of 5 and 5 heads 13.7, one 12.1.
 template <int LANES, int ELEM>
 us_status launch_heads(const Call& p, cudaStream_t st) {
     const int64_t rows = (int64_t)p.a.max_n * p.c.B * (p.q.H + p.k.H + (ELEM == kNone ? 0 : p.c.Hkv));

@@ -1,7 +1,8 @@
 """One latent attention block of a decoder, served:  python examples/latent_decode.py
 
 Every token leaves one latent row and one rotated key, which all heads share, in a paged
-cache.  Its projections are unstructured-sparse matrices (us_spmm_f16).  Three requests
+cache.  Its projections are unstructured-sparse matrices (us_spmm_f16); a token's queries and
+outputs pass through the head's part of one of them, dense, by einsum.  Three requests
 prefill their prompts in chunks, then decode single tokens:
   1. pages for the new tokens                           us_kv_reserve
   2. queries, latent rows; their rotation, the cache    us_spmm_f16, us_norm_rope, us_lat_write

@@ -321,6 +321,9 @@ us_status us_quantize_x(const uint16_t* X, int N, int K, uint8_t* Xq, uint16_t* 
  * request, the others those positions).  A page number outside
  * 0..num_pages-1 records US_ERR_CORRUPT and its positions are skipped (not
  * attended to).
+ * Grids, but those of the attentions, are made for max_n rows of every request: a call whose requests are of very
+ * different lengths is better made as two (a prompt of 2048 tokens and 256 single ones
+ * in us_lat_write: 67 us as one call, 2.6 and 2.1 as two; us_norm_rope 88, 11.2 and 3.3).
  * fp16 rows hold whole heads side by side; ld* is the distance of two rows in
  * elements (a multiple of 8, so that slices of a fused projection serve).
  * ------------------------------------------------------------------------- */
@@ -536,7 +539,8 @@ us_status us_attn_lat_workspace_bytes(const us_lat_cache* C, int Hq, int max_n, 
  * not finite makes its column of the output +-65504 or NaN, as the sum is.
  * Q: T rows of H heads of Dn + Dr values side by side, O: of Dv; K: S rows of Dn
  * values a head, ldk elements apart, a head hsk behind the last; V the same, of Dv;
- * KR: S rows of Dr.  Distances are multiples of 8.  (Dn, Dr, Dv): (128, 64, 128) or
+ * KR: S rows of Dr.  Distances are multiples of 8; a row's heads lie within its ldk (ldv)
+ * elements.  (Dn, Dr, Dv): (128, 64, 128) or
  * (64, 64, 64) (US_ERR_UNSUPPORTED otherwise); B and H at most 1024; S at most 2^30.
  * Offsets that do not ascend, leave 0..T or 0..S, give a request more than max_n
  * queries or more queries than key rows record US_ERR_INVALID_ARG and the request is
