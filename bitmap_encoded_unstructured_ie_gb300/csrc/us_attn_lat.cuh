@@ -88,12 +88,12 @@ static_assert(sizeof(Part) <= 32, "parts");
 // columns of a row, kAtOnce states at once; its group of threads takes every
 // GROUPS-th state of the segment, and the groups' sums are added in shared memory.
 // Few segments have many sharers each and are given 8 groups; many have about two, and
-// one group does: up to an eighth as many segments as CTAs (19), and there both take about as
-// long (one token of B requests of 60000 / B positions, 8 groups against 1: B = 1 30.8 / 138 us, 8
-// 27.1 / 43.4, 19 29.7 / 33.4, 32 33.4 / 30.3, 76 48.9 / 30.9; 16 expanded rows behind 8000: 1 head
-// 13.5 / 25.6, 19 heads 29.1 / 29.7, 64 heads 63.7 / 60.7).    blockIdx.x: a shared segment and 16 of its rows (of `blocks` such),
-// blockIdx.y: which columns; segments by the CTA that shares one first, or, where they
-// are few, counted.
+// one group does: up to an eighth as many segments as CTAs (19), and there both take about
+// as long (one token of B requests of 60000 / B positions, 8 groups / 1: B = 1 30.8 / 138 us,
+// 8 27.1 / 43.4, 19 29.7 / 33.4, 32 33.4 / 30.3, 76 48.9 / 30.9; 16 expanded rows behind 8000:
+// 1 head 13.5 / 25.6, 19 heads 29.1 / 29.7, 64 heads 63.7 / 60.7).
+// blockIdx.x: a shared segment and 16 of its rows (of `blocks` such), blockIdx.y: which
+// columns; segments by the CTA that shares one first, or, where they are few, counted.
 template <int ROWS, int D, int GROUPS, class P>
 __global__ void __launch_bounds__(kJoinThreads)
 join_kernel(const P p, int blocks, int ctas) {
