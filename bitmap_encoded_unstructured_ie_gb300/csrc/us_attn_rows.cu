@@ -326,8 +326,8 @@ attn_rows_kernel(const UsAttnRowsParams p, const __grid_constant__ Maps maps) {
             if (end < count) cur.next_segment(p);
             if (mine) wait(&H.pv_done[st], segment++);
             us::tc_fence_after();
-            if (mine && *static_cast<volatile uint32_t*>(&H.cleared)) {        // (once set, for good: such inputs are rare)
-                __syncwarp();
+            // (once set, for good: such inputs are rare; a vote, as the other stream may set it between two lanes' reads)
+            if (mine && __any_sync(0xffffffffu, *static_cast<volatile uint32_t*>(&H.cleared) != 0)) {
                 const int4 of = H.part[warp];
                 const int v0 = max(of.x, of.z), v1 = min(of.x + srow, of.w);
                 const uint16_t* v = p.k.V + (int64_t)(p.kv_off[H.request[warp]] + v0) * p.k.ldv + of.y * p.k.hsv + half * (D / 2);
