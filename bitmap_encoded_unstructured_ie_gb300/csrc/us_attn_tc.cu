@@ -43,7 +43,7 @@
 // memory for its 32 cycles of work), issue slots for 56 %, the exponentials' unit for
 // 35 %.  Softmax, MMAs and conversion wait for each other in turn; what would shorten
 // the turn (more stages, scores of a whole tile) has no shared memory or TMEM left.
-// 512 tokens of 64 query heads on 8, behind 8192 positions, int8: 178 us, 800 TFLOP/s;
+// 512 tokens of 64 query heads on 8, behind 8192 positions, int8: 180 us, 787 TFLOP/s;
 // four trees of 64 tokens of 32 heads on 8, behind 4095, int4: 40 us, of which 13 are
 // tiles, 5 pass until the first scores, 4 are a CTA's partial state, and the rest is
 // the join and two launches.
